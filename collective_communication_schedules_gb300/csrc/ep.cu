@@ -1094,6 +1094,91 @@ __global__ void ep_combine_fused_kernel(const __grid_constant__ EpRoute R) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Gradient of the combine: for every valid pair (t, j) of source s, with row r
+// of buffer d,   drow[d][r] = bf16(w * dy[s][t]),   dw[s][t, j] = <row[d][r], dy[s][t]>
+// (binary32 products and sums; 0 for a pair without a row).  Bound by its
+// bytes: every row read, every row's gradient written, dy read once per token.
+struct EpGrad {
+  EpRoute R;                // x: dy of each source; buf: the rows; w: gate weights
+  char* drow[kMaxRanks];
+  float* dw[kMaxRanks];
+};
+
+// A warp takes `group` consecutive pairs of one token (all of them, or one
+// where that leaves SMs without work) and a row in chunks of kGradVecs 16-byte
+// vectors per lane; the loads of a chunk are issued before its arithmetic.
+constexpr int kGradVecs = 8;
+template <bool VEC>
+__global__ void __launch_bounds__(256) ep_combine_grad_kernel(const __grid_constant__ EpGrad G, int group) {
+  pdl_enter();
+  const EpRoute& R = G.R;
+  __shared__ long long base[kMaxRanks * kMaxRanks];
+  route_bases(R, base);
+  const int lane = threadIdx.x & 31;
+  const int groups = (R.topk + group - 1) / group;
+  const long long items = (long long)R.k * R.tokens * groups;
+  const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
+  const int hv = R.hidden / 8;
+  for (long long it = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += warps) {
+    const long long tok = it / groups;
+    const int j0 = int(it - tok * groups) * group, j1 = min(R.topk, j0 + group);
+    const int s = int(tok / R.tokens), t = int(tok - (long long)s * R.tokens);
+    const char* dy = R.x[s] + size_t(t) * R.hidden * 2;
+    for (int j = j0; j < j1; ++j) {
+      const size_t pr = size_t(t) * R.topk + j;
+      const int p = R.pos_of[s][pr];
+      int d = 0;
+      long long row = -1;
+      if (p >= 0) row = route_row(R, base, s, pair_expert(R, s, pr), p, 2, &d);
+      float dot = 0.f;
+      if (row >= 0) {
+        const float w = R.w[s][pr];
+        const size_t at = size_t(row) * R.hidden * 2;
+        if (VEC) {
+          const uint4* a = reinterpret_cast<const uint4*>(dy);
+          const uint4* b = reinterpret_cast<const uint4*>(R.buf[d] + at);
+          uint4* o = reinterpret_cast<uint4*>(G.drow[d] + at);
+          for (int v0 = lane; v0 < hv; v0 += 32 * kGradVecs) {
+            uint4 x[kGradVecs], y[kGradVecs];
+#pragma unroll
+            for (int q = 0; q < kGradVecs; ++q) {
+              const bool in = v0 + 32 * q < hv;
+              y[q] = in ? __ldcs(b + v0 + 32 * q) : make_uint4(0, 0, 0, 0);
+              x[q] = in ? __ldg(a + v0 + 32 * q) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int q = 0; q < kGradVecs; ++q) {
+              const uint32_t xs[4] = {x[q].x, x[q].y, x[q].z, x[q].w}, ys[4] = {y[q].x, y[q].y, y[q].z, y[q].w};
+              uint32_t os[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float lo = __uint_as_float(xs[e] << 16), hi = __uint_as_float(xs[e] & 0xFFFF0000u);
+                dot = fmaf(lo, __uint_as_float(ys[e] << 16), dot);
+                dot = fmaf(hi, __uint_as_float(ys[e] & 0xFFFF0000u), dot);
+                os[e] = uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(w * lo))) |
+                        (uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(w * hi))) << 16);
+              }
+              if (v0 + 32 * q < hv) __stcs(o + v0 + 32 * q, make_uint4(os[0], os[1], os[2], os[3]));
+            }
+          }
+        } else {
+          const uint16_t* a = reinterpret_cast<const uint16_t*>(dy);
+          const uint16_t* b = reinterpret_cast<const uint16_t*>(R.buf[d] + at);
+          uint16_t* o = reinterpret_cast<uint16_t*>(G.drow[d] + at);
+          for (int h = lane; h < R.hidden; h += 32) {
+            const float v = __uint_as_float(uint32_t(a[h]) << 16);
+            dot = fmaf(v, __uint_as_float(uint32_t(b[h]) << 16), dot);
+            o[h] = __bfloat16_as_ushort(__float2bfloat16_rn(w * v));
+          }
+        }
+      }
+      for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+      if (lane == 0) G.dw[s][pr] = dot;
+    }
+  }
+}
+
 int tiles_of(int n) { return (n + kTileItems - 1) / kTileItems; }
 
 // Launch with programmatic stream serialization (see pdl_enter).
@@ -1227,6 +1312,8 @@ cudaError_t ep_preload() {
                        reinterpret_cast<const void*>(&ep_dispatch_bulk_kernel),
                        reinterpret_cast<const void*>(&ep_combine_bulk_kernel),
                        reinterpret_cast<const void*>(&ep_combine_fused_kernel),
+                       reinterpret_cast<const void*>(&ep_combine_grad_kernel<true>),
+                       reinterpret_cast<const void*>(&ep_combine_grad_kernel<false>),
                        reinterpret_cast<const void*>(kCombineFused[0]), reinterpret_cast<const void*>(kCombineFused[1]),
                        reinterpret_cast<const void*>(kCombineFused[2]), reinterpret_cast<const void*>(kCombineFused[3]),
                        reinterpret_cast<const void*>(kCombineFused[4]), reinterpret_cast<const void*>(kCombineFused[5]),
@@ -1501,6 +1588,70 @@ hocResult_t combine_ranks(const char* who, int packed, int nranks, const void* c
   return HOC_SUCCESS;
 }
 
+// Gradient of the combine of every source, rows and their gradients in the
+// expert ranks' buffers (packed = 0) or in each source's own (packed = 1).
+hocResult_t combine_grad_ranks(const char* who, int packed, int nranks, const void* const* dy,
+                               const void* const* rows, const size_t* rows_capacity,
+                               const int32_t* const* expert_ids, const int32_t* const* pos_of,
+                               const uint64_t* counts, const float* const* weights, int tokens, int topk, int hidden,
+                               int experts, void* const* drows, float* const* dweights, int32_t* status,
+                               cudaStream_t s) {
+  char msg[160];
+  if (nranks < 1 || nranks > kMaxRanks || tokens < 0 || topk < 1 || hidden < 1 || experts < 1 ||
+      experts % nranks != 0) {
+    snprintf(msg, sizeof msg, "%s: bad rank count, shape or expert count", who);
+    set_error_detail(msg);
+    return HOC_ERR_INVALID_ARG;
+  }
+  if (tokens == 0) return HOC_SUCCESS;
+  if (!dy || !rows || !rows_capacity || (!packed && (!expert_ids || !counts)) || !pos_of || !weights || !drows ||
+      !dweights || !status || size_t(tokens) * topk > size_t(INT32_MAX)) {
+    snprintf(msg, sizeof msg, "%s: NULL array, or more than 2^31 pairs", who);
+    set_error_detail(msg);
+    return HOC_ERR_INVALID_ARG;
+  }
+  EpGrad G{};
+  EpRoute& R = G.R;
+  bool vec = hidden % 8 == 0;
+  for (int r = 0; r < nranks; ++r) {
+    const bool room = rows_capacity[r] >= size_t(hidden);  // a rank that got no rows may have no buffers
+    if (!dy[r] || (room && (!rows[r] || !drows[r])) || (!packed && !expert_ids[r]) || !pos_of[r] || !weights[r] ||
+        !dweights[r]) {
+      snprintf(msg, sizeof msg, "%s: NULL per-rank pointer", who);
+      set_error_detail(msg);
+      return HOC_ERR_INVALID_ARG;
+    }
+    R.x[r] = static_cast<const char*>(dy[r]);
+    R.buf[r] = static_cast<char*>(const_cast<void*>(rows[r]));
+    R.cap_rows[r] = rows_capacity[r] / size_t(hidden);
+    R.ids[r] = packed ? nullptr : expert_ids[r];
+    R.pos_of[r] = pos_of[r];
+    R.w[r] = weights[r];
+    G.drow[r] = static_cast<char*>(drows[r]);
+    G.dw[r] = dweights[r];
+    vec = vec && ((reinterpret_cast<uintptr_t>(dy[r]) | reinterpret_cast<uintptr_t>(rows[r]) |
+                   reinterpret_cast<uintptr_t>(drows[r])) & 15u) == 0;
+  }
+  R.counts = packed ? nullptr : reinterpret_cast<const unsigned long long*>(counts);
+  R.status = status;
+  R.k = nranks;
+  R.tokens = tokens;
+  R.topk = topk;
+  R.hidden = hidden;
+  R.per_rank = experts / nranks;
+  R.packed = packed;
+  // A warp per token, or per pair where a warp per token would leave SMs idle.
+  const long long tokens_all = (long long)nranks * tokens;
+  const int group = tokens_all < 152 * 16 ? 1 : topk;
+  const long long warps = tokens_all * ((topk + group - 1) / group);
+  const cudaError_t e = vec ? launch_pdl(ep_combine_grad_kernel<true>, dim3(scatter_grid(warps)), 256, 0, s, G, group)
+                            : launch_pdl(ep_combine_grad_kernel<false>, dim3(scatter_grid(warps)), 256, 0, s, G, group);
+  if (e == cudaSuccess) return HOC_SUCCESS;
+  snprintf(msg, sizeof msg, "%s: launch failed", who);
+  set_error_detail(msg);
+  return HOC_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace hoc
 
@@ -1535,4 +1686,24 @@ extern "C" hocResult_t hoc_ep_combine_all(int nranks, const void* const* rows, c
                                           int topk, int hidden, void* const* y, int32_t* status, void* stream) {
   return hoc::combine_ranks("hoc_ep_combine_all", 1, nranks, rows, rows_capacity, nullptr, pos_of, nullptr, weights,
                             tokens, topk, hidden, nranks, y, status, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" hocResult_t hoc_ep_combine_grad(int nranks, const void* const* dy, const void* const* rows,
+                                           const size_t* rows_capacity, const int32_t* const* expert_ids,
+                                           const int32_t* const* pos_of, const uint64_t* counts,
+                                           const float* const* weights, int tokens, int topk, int hidden, int experts,
+                                           void* const* drows, float* const* dweights, int32_t* status, void* stream) {
+  return hoc::combine_grad_ranks("hoc_ep_combine_grad", 0, nranks, dy, rows, rows_capacity, expert_ids, pos_of, counts,
+                                 weights, tokens, topk, hidden, experts, drows, dweights, status,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+extern "C" hocResult_t hoc_ep_combine_grad_all(int nranks, const void* const* dy, const void* const* rows,
+                                               const size_t* rows_capacity, const int32_t* const* pos_of,
+                                               const float* const* weights, int tokens, int topk, int hidden,
+                                               void* const* drows, float* const* dweights, int32_t* status,
+                                               void* stream) {
+  return hoc::combine_grad_ranks("hoc_ep_combine_grad_all", 1, nranks, dy, rows, rows_capacity, nullptr, pos_of,
+                                 nullptr, weights, tokens, topk, hidden, nranks, drows, dweights, status,
+                                 static_cast<cudaStream_t>(stream));
 }

@@ -57,6 +57,8 @@ cudaError_t reduce_preload();
 cudaError_t tma_preload();       // TMA copy kernel and TMA-fed reduce kernel
 cudaError_t ep_preload();        // expert-parallel pack and combine kernels
 cudaError_t workload_preload();  // probe and stand-in compute kernels
+cudaError_t mm_preload();        // expert and linear products and the kernels beside them
+cudaError_t grad_preload();      // gradient norm and clipping
 
 // TMA-fed variant (reduce_tma.cu): same fold, bulk copies through shared memory.
 uint64_t reduce_tma_seg_tiles(int dtype, const ReduceSeg& s, int k);

@@ -1,0 +1,498 @@
+// Entry points of hoc_layer.h: argument checks, the choice of a product
+// kernel, and the small kernels around the products (row ranges of a dispatch,
+// activation gradient, bias gradient).
+#include <cstdio>
+#include <cstring>
+
+#include "mm.h"
+
+namespace hoc {
+namespace {
+
+// ------------------------------------------------------------ row ranges
+struct SegIds {
+  const int32_t* ids[kMaxRanks];
+};
+
+constexpr int kSegThreads = 256;
+constexpr int kSegItems = 2048;     // pairs of one CTA
+constexpr int kSegShared = 8192;    // experts whose counters fit in shared memory
+
+// seg[d][1 + s * per + g] += pairs of source s (blockIdx.y) for expert g of
+// rank d.  Integer atomics: the sums do not depend on their order.
+__global__ void seg_count_kernel(const __grid_constant__ SegIds P, int n, int experts, int per, int nranks,
+                                 unsigned long long* seg) {
+  extern __shared__ int hist[];
+  const int s = blockIdx.y;
+  const bool shared = experts <= kSegShared;
+  const size_t stride = size_t(nranks) * per + 1;
+  for (int e = threadIdx.x; shared && e < experts; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  const int64_t lo = int64_t(blockIdx.x) * kSegItems;
+  for (int64_t i = lo + threadIdx.x; i < lo + kSegItems && i < n; i += blockDim.x) {
+    const int e = P.ids[s][i];
+    if (e < 0 || e >= experts) continue;
+    if (shared) atomicAdd(&hist[e], 1);
+    else atomicAdd(seg + (e / per) * stride + 1 + size_t(s) * per + e % per, 1ull);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; shared && e < experts; e += blockDim.x)
+    if (hist[e]) atomicAdd(seg + (e / per) * stride + 1 + size_t(s) * per + e % per, (unsigned long long)hist[e]);
+}
+
+// Counts to offsets: an inclusive scan of seg[d][1 ..] in place, one CTA per rank.
+__global__ void seg_scan_kernel(int m, int64_t* seg) {
+  int64_t* v = seg + size_t(blockIdx.x) * (size_t(m) + 1) + 1;
+  __shared__ int64_t part[kSegThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t base = 0;
+  for (int at = 0; at < m; at += kSegThreads) {
+    const int i = at + int(threadIdx.x);
+    int64_t x = i < m ? v[i] : 0;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int64_t before = base, all = 0;
+    for (int w = 0; w < kSegThreads / 32; ++w) {
+      if (w < warp) before += part[w];
+      all += part[w];
+    }
+    if (i < m) v[i] = before + x;
+    base += all;
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------ activation gradient
+// dz = dy * act'(pre), 8 values of a row per thread where rows are whole
+// 16-byte vectors, else one.  Bound by its bytes: dy and pre read, dz written.
+template <int V>
+__global__ void act_grad_kernel(const __nv_bfloat16* dy, const __nv_bfloat16* pre, __nv_bfloat16* dz, int64_t rows,
+                                int width, int act) {
+  struct alignas(2 * V) Vec {
+    __nv_bfloat16 v[V];
+  };
+  const int per = width / V;
+  const int64_t n = rows * per;
+  const bool gated = act == HOC_ACT_SWIGLU;
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t row = i / per;
+    const int64_t f = (i - row * per) * V;
+    const int64_t at = gated ? row * 2 * width + f : row * width + f;
+    const Vec d = *reinterpret_cast<const Vec*>(dy + row * width + f);
+    const Vec z = *reinterpret_cast<const Vec*>(pre + at);
+    Vec o, o2;
+    if (gated) {
+      const Vec u = *reinterpret_cast<const Vec*>(pre + at + width);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float g = __bfloat162float(z.v[e]), dd = __bfloat162float(d.v[e]);
+        o.v[e] = __float2bfloat16_rn(dd * __bfloat162float(u.v[e]) * mm_act_slope(HOC_ACT_SILU, g));
+        o2.v[e] = __float2bfloat16_rn(dd * mm_act(HOC_ACT_SILU, g));
+      }
+      *reinterpret_cast<Vec*>(dz + at + width) = o2;
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        o.v[e] = __float2bfloat16_rn(__bfloat162float(d.v[e]) * mm_act_slope(act, __bfloat162float(z.v[e])));
+    }
+    *reinterpret_cast<Vec*>(dz + at) = o;
+  }
+}
+
+// ------------------------------------------------------------ bias gradient
+// db[e][n] (+)= sum over the expert's rows of dy[r][n].  A CTA sums 64 columns
+// of one expert: warp w takes rows w, w + 32, ... of each range, lane l columns
+// 2 l and 2 l + 1; the 32 warps' binary32 sums are added in warp order.
+constexpr int kBiasWarps = 32;
+__global__ void __launch_bounds__(32 * kBiasWarps) bias_grad_kernel(const __grid_constant__ MmParams P) {
+  __shared__ float sums[kBiasWarps][64];
+  const int i = blockIdx.y, p = P.part0 + i / P.groups, g = P.group0 + i % P.groups;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = int(blockIdx.x) * 64 + lane * 2;
+  const __nv_bfloat16* dy = P.dy[p];
+  const bool pair = c + 1 < P.out && P.ld_dy % 2 == 0 && (reinterpret_cast<uintptr_t>(dy) & 3u) == 0;
+  float a = 0.f, b = 0.f;
+  const int ns = P.seg ? P.sources : 1;
+  for (int s = 0; s < ns; ++s) {
+    int64_t lo, n;
+    mm_range(P, p, g, s, lo, n);
+#pragma unroll 4
+    for (int64_t r = warp; r < n; r += kBiasWarps) {
+      const __nv_bfloat16* q = dy + (lo + r) * P.ld_dy + c;
+      if (pair) {
+        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(q);
+        a += __low2float(v);
+        b += __high2float(v);
+      } else {
+        if (c < P.out) a += bf16_of(q);
+        if (c + 1 < P.out) b += bf16_of(q + 1);
+      }
+    }
+  }
+  sums[warp][lane * 2] = a;
+  sums[warp][lane * 2 + 1] = b;
+  __syncthreads();
+  const int col = int(blockIdx.x) * 64 + int(threadIdx.x);
+  if (threadIdx.x >= 64 || col >= P.out) return;
+  float v = 0.f;
+  for (int w = 0; w < kBiasWarps; ++w) v += sums[w][threadIdx.x];
+  const int64_t at = int64_t(g) * P.out + col;
+  if (P.out_f32) {
+    float* o = static_cast<float*>(P.pre_out[p]) + at;
+    *o = P.accumulate ? *o + v : v;
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(P.pre_out[p]) + at;
+    *o = __float2bfloat16_rn(P.accumulate ? bf16_of(o) + v : v);
+  }
+}
+
+// ------------------------------------------------------------ host
+constexpr int kMaxWidth = 1 << 20;
+constexpr size_t kMaxRows = size_t(1) << 30;
+
+hocResult_t refuse(const char* who, const char* what) {
+  char msg[160];
+  snprintf(msg, sizeof msg, "%s: %s", who, what);
+  set_error_detail(msg);
+  return HOC_ERR_INVALID_ARG;
+}
+
+int sm_count() {
+  int dev = 0, sms = 1;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+bool widths_ok(int in, int out) { return in >= 1 && out >= 1 && in <= kMaxWidth && out <= kMaxWidth; }
+
+bool act_ok(int act) { return act >= HOC_ACT_NONE && act <= HOC_ACT_SWIGLU; }
+
+// Checks the groups and fills the layout part of P.
+hocResult_t take_groups(const char* who, const hocRowGroups_t* G, MmParams& P) {
+  if (!G || !G->seg || !G->capacity) return refuse(who, "groups, its seg and its capacity must be given");
+  if (G->nranks < 1 || G->nranks > kMaxRanks || G->experts < 1 || G->experts > kMaxWidth || G->sources < 1 ||
+      G->sources > 4096)
+    return refuse(who, "rank, expert or source count out of range");
+  for (int p = 0; p < G->nranks; ++p) {
+    if (G->capacity[p] > kMaxRows) return refuse(who, "a buffer of more than 2^30 rows");
+    P.cap[p] = int64_t(G->capacity[p]);
+  }
+  P.seg = G->seg;
+  P.experts = G->experts;
+  P.sources = G->sources;
+  P.parts = G->nranks;
+  P.groups = G->experts;
+  return HOC_SUCCESS;
+}
+
+template <class T>
+hocResult_t take(const char* who, const char* name, const void* const* from, const MmParams& P, bool rows, T** to) {
+  char msg[96];
+  snprintf(msg, sizeof msg, "%s holds a NULL pointer", name);
+  if (!from) return refuse(who, msg);
+  for (int p = 0; p < P.parts; ++p) {
+    if (!from[p] && !(rows && P.cap[p] == 0)) return refuse(who, msg);
+    to[p] = static_cast<T*>(const_cast<void*>(from[p]));
+    if (reinterpret_cast<uintptr_t>(from[p]) & 1u) return refuse(who, "a pointer that is not aligned to its elements");
+  }
+  return HOC_SUCCESS;
+}
+
+// Runs one product, in as many launches as kMmMaxGroups asks for.
+hocResult_t run_product(const char* who, MmParams& P, int mode, cudaStream_t s) {
+  const int sms = sm_count();
+  const int nranks = P.parts, experts = P.groups;
+  const int by_group = experts < kMmMaxGroups ? experts : kMmMaxGroups;
+  const int by_part = kMmMaxGroups / by_group < nranks ? kMmMaxGroups / by_group : nranks;
+  for (int p = 0; p < nranks; p += by_part)
+    for (int g = 0; g < experts; g += by_group) {
+      P.part0 = p;
+      P.parts = nranks - p < by_part ? nranks - p : by_part;
+      P.group0 = g;
+      P.groups = experts - g < by_group ? experts - g : by_group;
+      int64_t rows = 0;
+      for (int q = p; q < p + P.parts; ++q) rows += P.cap[q];
+      if (rows == 0 && mode != kWgrad) continue;
+      const cudaError_t e = launch_mm_any(P, mode, sms, s);
+      if (e != cudaSuccess) {
+        char msg[160];
+        snprintf(msg, sizeof msg, "%s: launch failed: %s", who, cudaGetErrorString(e));
+        set_error_detail(msg);
+        return HOC_ERR_CUDA;
+      }
+    }
+  P.part0 = P.group0 = 0;
+  P.parts = nranks;
+  P.groups = experts;
+  return HOC_SUCCESS;
+}
+
+// 64-wide tiles bound every kernel's tile count; it has to fit the tile index.
+bool tiles_ok(const MmParams& P, int mode, int width) {
+  int64_t c = 0;
+  for (int p = 0; p < P.parts; ++p)
+    c += mode == kWgrad ? int64_t(P.groups) * ((P.out + 63) / 64)
+                        : P.cap[p] / 64 + int64_t(P.groups) * (1 + P.sources / 8);
+  return c * ((int64_t(width) + 63) / 64) < (int64_t(1) << 31);
+}
+
+hocResult_t run_wgrad(const char* who, MmParams& P, void* const* db, cudaStream_t s) {
+  if (!tiles_ok(P, kWgrad, P.in)) return refuse(who, "more than 2^31 tiles");
+  hocResult_t r = run_product(who, P, kWgrad, s);
+  if (r != HOC_SUCCESS || !db) return r;
+  for (int p = 0; p < P.parts; ++p) P.pre_out[p] = db[p];
+  const int pairs = P.parts * P.groups;
+  MmParams Q = P;
+  for (int at = 0; at < pairs;) {  // the grid's y extent ends at 65535
+    const int p = at / P.groups, g = at % P.groups;
+    Q.part0 = p;
+    Q.group0 = g;
+    Q.parts = 1;
+    Q.groups = P.groups - g < 65535 ? P.groups - g : 65535;
+    if (g == 0 && P.groups * int64_t(P.parts - p) <= 65535) {
+      Q.parts = P.parts - p;
+      Q.groups = P.groups;
+    }
+    bias_grad_kernel<<<dim3((P.out + 63) / 64, Q.parts * Q.groups), 32 * kBiasWarps, 0, s>>>(Q);
+    at += Q.parts * Q.groups;
+  }
+  if (cudaGetLastError() != cudaSuccess) {
+    set_error_detail("bias gradient: launch failed");
+    return HOC_ERR_CUDA;
+  }
+  return HOC_SUCCESS;
+}
+
+template <class V>
+hocResult_t take_one(const char* who, const char* name, const void* v, V** to) {
+  char msg[96];
+  snprintf(msg, sizeof msg, "%s must be given", name);
+  if (!v) return refuse(who, msg);
+  if (reinterpret_cast<uintptr_t>(v) & 1u) return refuse(who, "a pointer that is not aligned to its elements");
+  to[0] = static_cast<V*>(const_cast<void*>(v));
+  return HOC_SUCCESS;
+}
+
+hocResult_t dense(const char* who, int rows, int in, int out, int32_t* status, MmParams& P) {
+  if (rows < 0 || size_t(rows) > kMaxRows || !widths_ok(in, out)) return refuse(who, "row count or width out of range");
+  if (!status) return refuse(who, "status must be given");
+  P.parts = P.groups = P.experts = P.sources = 1;
+  P.cap[0] = rows;
+  P.in = in;
+  P.out = out;
+  P.status = status;
+  return HOC_SUCCESS;
+}
+
+#define HOC_TRY(x)                                 \
+  do {                                             \
+    const hocResult_t try_r = (x);                 \
+    if (try_r != HOC_SUCCESS) return try_r;        \
+  } while (0)
+
+}  // namespace
+
+cudaError_t mm_preload() {
+  const void* fns[] = {reinterpret_cast<const void*>(&seg_count_kernel), reinterpret_cast<const void*>(&seg_scan_kernel),
+                       reinterpret_cast<const void*>(&act_grad_kernel<8>), reinterpret_cast<const void*>(&act_grad_kernel<1>),
+                       reinterpret_cast<const void*>(&bias_grad_kernel)};
+  for (const void* f : fns) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, f);
+    if (e != cudaSuccess) return e;
+  }
+  return mm_any_preload();
+}
+
+}  // namespace hoc
+
+using namespace hoc;
+
+extern "C" hocResult_t hoc_ep_segments(int nranks, const int32_t* const* expert_ids, int tokens, int topk, int experts,
+                                       int64_t* seg, void* stream) {
+  const char* who = "hoc_ep_segments";
+  if (nranks < 1 || nranks > kMaxRanks || tokens < 0 || topk < 1 || experts < 1 || experts > kMaxWidth ||
+      experts % nranks != 0)
+    return refuse(who, "bad rank count, shape or expert count");
+  if (!seg || size_t(tokens) * topk > size_t(INT32_MAX)) return refuse(who, "seg must be given, tokens * topk fit 31 bits");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  SegIds P{};
+  for (int r = 0; tokens > 0 && r < nranks; ++r) {
+    if (!expert_ids || !expert_ids[r]) return refuse(who, "expert_ids holds a NULL pointer");
+    P.ids[r] = expert_ids[r];
+  }
+  const size_t per_rank = size_t(experts) + 1;  // nranks * (experts / nranks) + 1
+  cudaError_t e = cudaMemsetAsync(seg, 0, sizeof(int64_t) * per_rank * nranks, s);
+  if (e == cudaSuccess && tokens > 0) {
+    const int n = tokens * topk;
+    seg_count_kernel<<<dim3((n + kSegItems - 1) / kSegItems, nranks), kSegThreads,
+                       experts <= kSegShared ? sizeof(int) * size_t(experts) : 0, s>>>(
+        P, n, experts, experts / nranks, nranks, reinterpret_cast<unsigned long long*>(seg));
+    seg_scan_kernel<<<nranks, kSegThreads, 0, s>>>(experts, seg);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) return HOC_SUCCESS;
+  set_error_detail("hoc_ep_segments: launch failed");
+  return HOC_ERR_CUDA;
+}
+
+extern "C" hocResult_t hoc_expert_mm(const hocRowGroups_t* groups, const void* const* x, const void* const* weight,
+                                     const void* const* bias, int in, int out, int act, void* const* y,
+                                     void* const* pre, int32_t* status, void* stream) {
+  const char* who = "hoc_expert_mm";
+  MmParams P{};
+  HOC_TRY(take_groups(who, groups, P));
+  if (!widths_ok(in, out) || !act_ok(act) || !status) return refuse(who, "bad width or activation, or no status");
+  P.in = P.ld_rows = in;
+  P.out = P.ld_y = out;
+  P.act = act;
+  P.status = status;
+  HOC_TRY(take(who, "x", x, P, true, P.rows));
+  HOC_TRY(take(who, "weight", weight, P, false, P.w));
+  if (bias) HOC_TRY(take(who, "bias", bias, P, false, P.bias));
+  HOC_TRY(take(who, "y", y, P, true, P.y));
+  if (pre) HOC_TRY(take(who, "pre", pre, P, true, P.pre_out));
+  if (!tiles_ok(P, kForward, 2 * out)) return refuse(who, "more than 2^31 tiles");
+  return run_product(who, P, kForward, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" hocResult_t hoc_expert_mm_dgrad(const hocRowGroups_t* groups, const void* const* dy,
+                                           const void* const* weight, int in, int out, int act,
+                                           const void* const* pre, void* const* dx, int32_t* status, void* stream) {
+  const char* who = "hoc_expert_mm_dgrad";
+  MmParams P{};
+  HOC_TRY(take_groups(who, groups, P));
+  if (!widths_ok(in, out) || !act_ok(act) || !status) return refuse(who, "bad width or activation, or no status");
+  P.in = in;
+  P.out = P.ld_rows = out;
+  P.ld_y = act == HOC_ACT_SWIGLU ? 2 * int64_t(in) : in;
+  P.act = act;
+  P.status = status;
+  HOC_TRY(take(who, "dy", dy, P, true, P.rows));
+  HOC_TRY(take(who, "weight", weight, P, false, P.w));
+  if (act != HOC_ACT_NONE) HOC_TRY(take(who, "pre", pre, P, true, P.pre));
+  HOC_TRY(take(who, "dx", dx, P, true, P.y));
+  if (!tiles_ok(P, kDgrad, in)) return refuse(who, "more than 2^31 tiles");
+  return run_product(who, P, kDgrad, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" hocResult_t hoc_expert_mm_wgrad(const hocRowGroups_t* groups, const void* const* dy, const void* const* x,
+                                           int in, int out, hocDataType_t dtype, int accumulate, void* const* dw,
+                                           void* const* db, int32_t* status, void* stream) {
+  const char* who = "hoc_expert_mm_wgrad";
+  MmParams P{};
+  HOC_TRY(take_groups(who, groups, P));
+  if (!widths_ok(in, out) || !status) return refuse(who, "bad width, or no status");
+  if (dtype != HOC_BFLOAT16 && dtype != HOC_FLOAT32) return refuse(who, "dtype must be HOC_BFLOAT16 or HOC_FLOAT32");
+  P.in = P.ld_rows = in;
+  P.out = P.ld_dy = out;
+  P.out_f32 = dtype == HOC_FLOAT32;
+  P.accumulate = accumulate != 0;
+  P.ld_y = in;
+  P.status = status;
+  HOC_TRY(take(who, "dy", dy, P, true, P.dy));
+  HOC_TRY(take(who, "x", x, P, true, P.rows));
+  HOC_TRY(take(who, "dw", dw, P, false, P.y));
+  if (db) HOC_TRY(take(who, "db", db, P, false, P.pre_out));
+  for (int p = 0; P.out_f32 && p < P.parts; ++p)
+    if ((reinterpret_cast<uintptr_t>(P.y[p]) | reinterpret_cast<uintptr_t>(P.pre_out[p])) & 3u)
+      return refuse(who, "a pointer that is not aligned to its elements");
+  return run_wgrad(who, P, db, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" hocResult_t hoc_linear(int rows, const void* x, size_t ldx, const void* weight, const void* bias,
+                                  const void* residual, size_t ldr, int in, int out, int act, void* y, size_t ldy,
+                                  void* pre, int32_t* status, void* stream) {
+  const char* who = "hoc_linear";
+  MmParams P{};
+  HOC_TRY(dense(who, rows, in, out, status, P));
+  if (!act_ok(act)) return refuse(who, "bad activation");
+  if (rows == 0) return HOC_SUCCESS;
+  if (ldx < size_t(in) || ldy < size_t(out) || (residual && ldr < size_t(out)) || ldx > (size_t(1) << 32) ||
+      ldy > (size_t(1) << 32) || ldr > (size_t(1) << 32))
+    return refuse(who, "a row stride shorter than its row, or past 2^32");
+  P.act = act;
+  P.ld_rows = int64_t(ldx);
+  P.ld_y = int64_t(ldy);
+  P.ld_res = int64_t(ldr);
+  HOC_TRY(take_one(who, "x", x, P.rows));
+  HOC_TRY(take_one(who, "weight", weight, P.w));
+  HOC_TRY(take_one(who, "y", y, P.y));
+  if (bias) HOC_TRY(take_one(who, "bias", bias, P.bias));
+  if (residual) HOC_TRY(take_one(who, "residual", residual, P.res));
+  if (pre) HOC_TRY(take_one(who, "pre", pre, P.pre_out));
+  if (!tiles_ok(P, kForward, 2 * out)) return refuse(who, "more than 2^31 tiles");
+  return run_product(who, P, kForward, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" hocResult_t hoc_linear_dgrad(int rows, const void* dy, size_t lddy, const void* weight, int in, int out,
+                                        int act, const void* pre, void* dx, int32_t* status, void* stream) {
+  const char* who = "hoc_linear_dgrad";
+  MmParams P{};
+  HOC_TRY(dense(who, rows, in, out, status, P));
+  if (!act_ok(act)) return refuse(who, "bad activation");
+  if (rows == 0) return HOC_SUCCESS;
+  if (lddy < size_t(out) || lddy > (size_t(1) << 32)) return refuse(who, "a row stride shorter than its row, or past 2^32");
+  P.act = act;
+  P.ld_rows = int64_t(lddy);
+  P.ld_y = act == HOC_ACT_SWIGLU ? 2 * int64_t(in) : in;
+  HOC_TRY(take_one(who, "dy", dy, P.rows));
+  HOC_TRY(take_one(who, "weight", weight, P.w));
+  HOC_TRY(take_one(who, "dx", dx, P.y));
+  if (act != HOC_ACT_NONE) HOC_TRY(take_one(who, "pre", pre, P.pre));
+  if (!tiles_ok(P, kDgrad, in)) return refuse(who, "more than 2^31 tiles");
+  return run_product(who, P, kDgrad, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" hocResult_t hoc_linear_wgrad(int rows, const void* dy, size_t lddy, const void* x, size_t ldx, int in,
+                                        int out, hocDataType_t dtype, int accumulate, void* dw, void* db,
+                                        int32_t* status, void* stream) {
+  const char* who = "hoc_linear_wgrad";
+  MmParams P{};
+  HOC_TRY(dense(who, rows, in, out, status, P));
+  if (dtype != HOC_BFLOAT16 && dtype != HOC_FLOAT32) return refuse(who, "dtype must be HOC_BFLOAT16 or HOC_FLOAT32");
+  if (lddy < size_t(out) || ldx < size_t(in) || lddy > (size_t(1) << 32) || ldx > (size_t(1) << 32))
+    return refuse(who, "a row stride shorter than its row, or past 2^32");
+  P.out_f32 = dtype == HOC_FLOAT32;
+  P.accumulate = accumulate != 0;
+  P.ld_rows = int64_t(ldx);
+  P.ld_dy = int64_t(lddy);
+  P.ld_y = in;
+  if (rows > 0) {
+    HOC_TRY(take_one(who, "dy", dy, P.dy));
+    HOC_TRY(take_one(who, "x", x, P.rows));
+  }
+  HOC_TRY(take_one(who, "dw", dw, P.y));
+  if (db) HOC_TRY(take_one(who, "db", db, P.pre_out));
+  if (P.out_f32 && ((reinterpret_cast<uintptr_t>(dw) | reinterpret_cast<uintptr_t>(db)) & 3u))
+    return refuse(who, "a pointer that is not aligned to its elements");
+  return run_wgrad(who, P, db ? P.pre_out : nullptr, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" hocResult_t hoc_act_grad(int rows, int width, int act, const void* dy, const void* pre, void* dz,
+                                    void* stream) {
+  const char* who = "hoc_act_grad";
+  if (rows < 0 || size_t(rows) > kMaxRows || !widths_ok(width, width) || act <= HOC_ACT_NONE || !act_ok(act))
+    return refuse(who, "row count, width or activation out of range");
+  if (rows == 0) return HOC_SUCCESS;
+  const __nv_bfloat16 *d[1], *z[1];
+  __nv_bfloat16* o[1];
+  HOC_TRY(take_one(who, "dy", dy, d));
+  HOC_TRY(take_one(who, "pre", pre, z));
+  HOC_TRY(take_one(who, "dz", dz, o));
+  const bool vec = width % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(pre) |
+                                       reinterpret_cast<uintptr_t>(dz)) & 15u) == 0;
+  const int64_t n = int64_t(rows) * (vec ? width / 8 : width);
+  const int64_t want = (n + 255) / 256, cap = int64_t(sm_count()) * 8;
+  const int grid = int(want < cap ? want : cap);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (vec) act_grad_kernel<8><<<grid, 256, 0, s>>>(d[0], z[0], o[0], rows, width, act);
+  else act_grad_kernel<1><<<grid, 256, 0, s>>>(d[0], z[0], o[0], rows, width, act);
+  if (cudaGetLastError() == cudaSuccess) return HOC_SUCCESS;
+  set_error_detail("hoc_act_grad: launch failed");
+  return HOC_ERR_CUDA;
+}

@@ -1,0 +1,151 @@
+// Matrix products on rows grouped by expert: what the host entry points
+// (layer.cu) pass to the kernels (mm_any.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "hoc_internal.h"
+#include "hoc_layer.h"
+
+namespace hoc {
+
+// The three products of a layer.  Each computes out[c][f] with f contiguous:
+//   kForward  out[row][out feature] = sum over in  of W[f][k] x[row][k]
+//   kDgrad    out[row][in feature]  = sum over out of W[k][f] dy[row][k]
+//   kWgrad    out[out feature][in feature] = sum over an expert's rows of dy[row][c] x[row][f]
+enum MmMode { kForward = 0, kDgrad = 1, kWgrad = 2 };
+
+// Experts (over the rank buffers of one launch) whose tile counts a CTA keeps
+// in shared memory; layer.cu splits calls with more into several launches.
+constexpr int kMmMaxGroups = 1024;
+
+struct MmParams {
+  const int64_t* seg;  // [nranks][sources * experts + 1] row offsets; null: one range, all rows
+  int experts;         // experts of one rank (the seg layout)
+  int sources;
+  int part0, parts;    // rank buffers of this launch
+  int group0, groups;  // experts of each of them in this launch
+  int64_t cap[kMaxRanks];  // rows of each rank buffer
+  int in, out;             // weight: [experts][out (x 2 when gated)][in]
+  int act;                 // hocAct_t: forward, of the output; dgrad, of the layer below
+  int out_f32, accumulate; // wgrad
+  const __nv_bfloat16* rows[kMaxRanks];  // forward: x; dgrad: dy; wgrad: x
+  const __nv_bfloat16* dy[kMaxRanks];    // wgrad
+  const __nv_bfloat16* w[kMaxRanks];
+  const __nv_bfloat16* bias[kMaxRanks];
+  const __nv_bfloat16* res[kMaxRanks];
+  const __nv_bfloat16* pre[kMaxRanks];  // dgrad: pre-activation of the layer below
+  void* y[kMaxRanks];
+  void* pre_out[kMaxRanks];  // forward: pre-activation to keep
+  int64_t ld_rows, ld_dy, ld_res, ld_y;
+  int32_t* status;
+};
+
+// Device helpers ------------------------------------------------------------
+// The row range of (rank buffer p, expert g, source s), cut to the buffer.
+__device__ __forceinline__ void mm_range(const MmParams& P, int p, int g, int s, int64_t& lo, int64_t& n) {
+  const int64_t cap = P.cap[p];
+  if (P.seg == nullptr) {
+    lo = 0;
+    n = cap;
+    return;
+  }
+  const int64_t* at = P.seg + int64_t(p) * (int64_t(P.sources) * P.experts + 1) + int64_t(s) * P.experts + g;
+  const int64_t a = at[0], b = at[1];
+  lo = a < 0 ? 0 : (a < cap ? a : cap);
+  const int64_t hi = b < lo ? lo : (b < cap ? b : cap);
+  n = hi - lo;
+}
+
+// Fills, for every (rank buffer, expert) pair i of the launch, vrows[i]: its
+// rows, each source's count rounded up to `pad`, and tile0[i]: the tiles of the
+// pairs before it, tiles(vrows) tiles each; tile0[n] is the total.  The whole
+// CTA calls it (blockDim.x a multiple of 32).
+template <class Tiles>
+__device__ __forceinline__ void mm_count(const MmParams& P, int pad, int* vrows, unsigned* tile0, Tiles tiles) {
+  const int n = P.parts * P.groups;
+  const int ns = P.seg ? P.sources : 1;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int p = P.part0 + i / P.groups;
+    int64_t sum = 0;
+#pragma unroll 4
+    for (int s = 0; s < ns; ++s) {
+      int64_t lo, c;
+      mm_range(P, p, P.group0 + i % P.groups, s, lo, c);
+      sum += (c + pad - 1) / pad * pad;
+    }
+    const int64_t most = P.cap[p] + int64_t(ns) * (pad - 1);  // more only if ranges overlap
+    vrows[i] = int(sum < most ? sum : most);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    unsigned base = 0;
+    for (int at = 0; at < n; at += 32) {
+      const int i = at + int(threadIdx.x);
+      const unsigned mine = i < n ? tiles(vrows[i]) : 0;
+      unsigned incl = mine;
+      for (int off = 1; off < 32; off <<= 1) {
+        const unsigned v = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+        if (int(threadIdx.x) >= off) incl += v;
+      }
+      if (i < n) tile0[i] = base + incl - mine;
+      base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    if (threadIdx.x == 0) tile0[n] = base;
+  }
+  __syncthreads();
+}
+
+// The pair that tile t belongs to: the last i with tile0[i] <= t (t below the total).
+__device__ __forceinline__ int mm_find(const unsigned* tile0, int n, unsigned t) {
+  int lo = 0, hi = n;  // tile0[lo] <= t < tile0[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile0[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float bf16_of(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// 1 / (1 + exp(-z)) for every finite z: exp overflows to inf and the quotient to 0.
+__device__ __forceinline__ float mm_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// sqrt(2 / pi) and the cubic coefficient of the tanh form of GELU, of which
+// 0.5 (1 + tanh v) = sigmoid(2 v).
+constexpr float kGeluScale = 0.7978845608028654f;
+constexpr float kGeluCubic = 0.044715f;
+
+__device__ __forceinline__ float mm_act(int act, float z) {
+  switch (act) {
+    case HOC_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);
+    case HOC_ACT_GELU: return z * mm_sigmoid(2.f * kGeluScale * (z + kGeluCubic * z * z * z));
+    case HOC_ACT_SILU: return z * mm_sigmoid(z);
+    default: return z;
+  }
+}
+
+// d act(z) / dz; the products of a vanishing s (1 - s) with a huge z are cut at |z| = 30, where they are 0.
+__device__ __forceinline__ float mm_act_slope(int act, float z) {
+  switch (act) {
+    case HOC_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case HOC_ACT_GELU: {
+      const float s = mm_sigmoid(2.f * kGeluScale * (z + kGeluCubic * z * z * z));
+      const float c = fminf(fmaxf(z, -30.f), 30.f);
+      return s + c * s * (1.f - s) * 2.f * kGeluScale * (1.f + 3.f * kGeluCubic * c * c);
+    }
+    case HOC_ACT_SILU: {
+      const float s = mm_sigmoid(z);
+      const float c = fminf(fmaxf(z, -120.f), 120.f);
+      return s * (1.f + c * (1.f - s));
+    }
+    default: return 1.f;
+  }
+}
+
+// Host side -----------------------------------------------------------------
+cudaError_t launch_mm_any(const MmParams& P, int mode, int sms, cudaStream_t s);
+cudaError_t mm_any_preload();
+
+}  // namespace hoc

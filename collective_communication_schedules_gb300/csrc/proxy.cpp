@@ -382,6 +382,8 @@ hocResult_t preload_kernels(int device) {
   if (e == cudaSuccess) e = tma_preload();
   if (e == cudaSuccess) e = ep_preload();
   if (e == cudaSuccess) e = workload_preload();
+  if (e == cudaSuccess) e = mm_preload();
+  if (e == cudaSuccess) e = grad_preload();
   if (e != cudaSuccess) {
     set_error_detail("loading the library's kernels before starting the proxy failed");
     return HOC_ERR_CUDA;

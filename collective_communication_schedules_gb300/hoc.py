@@ -114,6 +114,47 @@ _SIGS["hoc_ep_pack_all"] = _SIGS["hoc_ep_dispatch_fused"]
 _SIGS["hoc_ep_combine_all"] = (C.c_int, [C.c_int, C.POINTER(C.c_void_p), C.POINTER(C.c_size_t), C.POINTER(C.c_void_p),
                                          C.POINTER(C.c_void_p), C.c_int, C.c_int, C.c_int, C.POINTER(C.c_void_p),
                                          C.c_void_p, C.c_void_p])
+_SIGS["hoc_ep_combine_grad"] = (C.c_int, [C.c_int, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.POINTER(C.c_size_t),
+                                          C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.c_void_p,
+                                          C.POINTER(C.c_void_p), C.c_int, C.c_int, C.c_int, C.c_int,
+                                          C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.c_void_p, C.c_void_p])
+_SIGS["hoc_ep_combine_grad_all"] = (C.c_int, [C.c_int, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
+                                              C.POINTER(C.c_size_t), C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
+                                              C.c_int, C.c_int, C.c_int, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
+                                              C.c_void_p, C.c_void_p])
+
+
+class _RowGroups(C.Structure):
+    _fields_ = [("nranks", C.c_int), ("experts", C.c_int), ("sources", C.c_int), ("seg", C.c_void_p),
+                ("capacity", C.POINTER(C.c_size_t))]
+
+
+_SIGS["hoc_ep_segments"] = (C.c_int, [C.c_int, C.POINTER(C.c_void_p), C.c_int, C.c_int, C.c_int, C.c_void_p,
+                                      C.c_void_p])
+_SIGS["hoc_expert_mm"] = (C.c_int, [C.POINTER(_RowGroups), C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
+                                    C.POINTER(C.c_void_p), C.c_int, C.c_int, C.c_int, C.POINTER(C.c_void_p),
+                                    C.POINTER(C.c_void_p), C.c_void_p, C.c_void_p])
+_SIGS["hoc_expert_mm_dgrad"] = (C.c_int, [C.POINTER(_RowGroups), C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
+                                          C.c_int, C.c_int, C.c_int, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
+                                          C.c_void_p, C.c_void_p])
+_SIGS["hoc_expert_mm_wgrad"] = (C.c_int, [C.POINTER(_RowGroups), C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
+                                          C.c_int, C.c_int, C.c_int, C.c_int, C.POINTER(C.c_void_p),
+                                          C.POINTER(C.c_void_p), C.c_void_p, C.c_void_p])
+_SIGS["hoc_linear"] = (C.c_int, [C.c_int, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                                 C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p,
+                                 C.c_void_p])
+_SIGS["hoc_linear_dgrad"] = (C.c_int, [C.c_int, C.c_void_p, C.c_size_t, C.c_void_p, C.c_int, C.c_int, C.c_int,
+                                       C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p])
+_SIGS["hoc_linear_wgrad"] = (C.c_int, [C.c_int, C.c_void_p, C.c_size_t, C.c_void_p, C.c_size_t, C.c_int, C.c_int,
+                                       C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p])
+_SIGS["hoc_act_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p])
+_SIGS["hoc_tensor_list_create"] = (C.c_int, [C.POINTER(C.c_void_p), C.c_int, C.POINTER(C.c_void_p),
+                                             C.POINTER(C.c_size_t), C.c_int])
+_SIGS["hoc_tensor_list_destroy"] = (C.c_int, [C.c_void_p])
+_SIGS["hoc_grad_workspace"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)])
+_SIGS["hoc_grad_norm"] = (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["hoc_grad_clip"] = (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_size_t,
+                                    C.c_void_p])
 _SIGS["hoc_allreduce_host"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.c_size_t,
                                          C.c_int, C.c_int, C.c_void_p])
 _SIGS["hoc_proxy_status"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64), C.POINTER(C.c_uint64),
@@ -579,6 +620,283 @@ def ep_combine_fused(rows, rows_capacity, expert_ids, pos_of, counts, weights, t
                                       int(tokens), int(topk), int(hidden), int(experts),
                                       _ptr_array(y, 2 * int(tokens) * int(hidden), "y"), _ptr(status, 4, "status"),
                                       _stream(stream)), "hoc_ep_combine_fused")
+
+
+def _combine_grad_args(dy, rows, rows_capacity, pos_of, weights, tokens, topk, hidden, drows, dweights):
+    k = len(rows)
+    n = int(tokens) * int(topk)
+    caps = [int(v) for v in rows_capacity]
+    if any(len(v) != k for v in (dy, caps, pos_of, weights, drows, dweights)):
+        raise ValueError(f"expected {k} per-rank tensors and capacities")
+    span = [2 * c for c in caps]
+    return (k, n, (C.c_size_t * k)(*caps), _ptr_array(dy, 2 * int(tokens) * int(hidden), "dy"),
+            _ptr_array(rows, span, "rows"), _ptr_array(pos_of, 4 * n, "pos_of"), _ptr_array(weights, 4 * n, "weights"),
+            _ptr_array(drows, span, "drows"), _ptr_array(dweights, 4 * n, "dweights"))
+
+
+def ep_combine_grad(dy, rows, rows_capacity, expert_ids, pos_of, counts, weights, tokens: int, topk: int, hidden: int,
+                    experts: int, drows, dweights, status, stream=None):
+    """Gradient of ep_combine_fused for the rows and the gate weights (see include/hoc_ep.h)."""
+    k, n, cap, dyp, rp, pp, wp, dp, dwp = _combine_grad_args(dy, rows, rows_capacity, pos_of, weights, tokens, topk,
+                                                             hidden, drows, dweights)
+    if len(expert_ids) != k:
+        raise ValueError(f"expected {k} per-rank tensors and capacities")
+    _check(lib().hoc_ep_combine_grad(k, dyp, rp, cap, _ptr_array(expert_ids, 4 * n, "expert_ids"), pp,
+                                     _ptr(counts, 8 * k * k, "counts"), wp, int(tokens), int(topk), int(hidden),
+                                     int(experts), dp, dwp, _ptr(status, 4, "status"), _stream(stream)),
+           "hoc_ep_combine_grad")
+
+
+def ep_combine_grad_all(dy, rows, rows_capacity, pos_of, weights, tokens: int, topk: int, hidden: int, drows, dweights,
+                        status, stream=None):
+    """Gradient of ep_combine_all: rows and their gradients in each source's packed order."""
+    k, _, cap, dyp, rp, pp, wp, dp, dwp = _combine_grad_args(dy, rows, rows_capacity, pos_of, weights, tokens, topk,
+                                                             hidden, drows, dweights)
+    _check(lib().hoc_ep_combine_grad_all(k, dyp, rp, cap, pp, wp, int(tokens), int(topk), int(hidden), dp, dwp,
+                                         _ptr(status, 4, "status"), _stream(stream)), "hoc_ep_combine_grad_all")
+
+
+# ------------------------------------------------------- expert and linear layers
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
+
+
+def _act(act) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act is one of {', '.join(ACTS)}, not {act!r}")
+    return ACTS[act]
+
+
+def _typed(x, dtypes, what: str):
+    """`x` checked to be a tensor of one of `dtypes` (names)."""
+    import torch
+    if isinstance(x, int) or x.dtype not in [getattr(torch, d) for d in dtypes]:
+        raise TypeError(f"{what}: expected a tensor of {' or '.join(dtypes)}")
+    return x
+
+
+def _shaped(x, shape, what: str, dtypes=("bfloat16",)) -> int:
+    """Address of the contiguous device tensor `x`, which has to have `shape`."""
+    if tuple(_typed(x, dtypes, what).shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
+    return _ptr(x, 0, what)
+
+
+def _strided(x, shape, what: str):
+    """Address and row stride of the bf16 matrix `x`, whose rows' elements are contiguous."""
+    if tuple(_typed(x, ("bfloat16",), what).shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError(f"{what}: must be a CUDA tensor")
+    rows, width = shape
+    if width > 1 and x.stride(1) != 1:
+        raise ValueError(f"{what}: a row's elements must be contiguous")
+    if rows > 1 and x.stride(0) < width:
+        raise ValueError(f"{what}: rows must not overlap")
+    return x.data_ptr(), max(x.stride(0) if rows > 1 else width, width)
+
+
+def _per_rank(xs, shapes, what: str, dtypes=("bfloat16",)) -> C.Array:
+    if len(xs) != len(shapes):
+        raise ValueError(f"{what}: expected {len(shapes)} per-rank tensors, got {len(xs)}")
+    return (C.c_void_p * len(xs))(*[_shaped(x, s, f"{what}[{r}]", dtypes) for r, (x, s) in enumerate(zip(xs, shapes))])
+
+
+def _groups(rows, experts: int, seg):
+    """The hocRowGroups_t of buffers with `rows[d]` rows each, and what it points to."""
+    k = len(rows)
+    _typed(seg, ("int64",), "seg")
+    if seg.dim() != 2 or seg.shape[0] != k or seg.shape[1] < experts + 1 or (seg.shape[1] - 1) % experts:
+        raise ValueError(f"seg: expected shape [{k}, sources * {experts} + 1], got {tuple(seg.shape)}")
+    cap = (C.c_size_t * max(1, k))(*rows)
+    return _RowGroups(k, experts, (seg.shape[1] - 1) // experts, _ptr(seg, 0, "seg"), cap), cap
+
+
+def ep_segments(expert_ids, experts: int, topk: int, seg, stream=None):
+    """Row ranges of every expert in the receive layout of a dispatch (see include/hoc_layer.h): expert_ids are the k
+    sources' [tokens * topk] int32 ids, experts counts all ranks'; seg: [k, experts + 1] int64."""
+    k = len(expert_ids)
+    n = expert_ids[0].numel() if k else 0
+    if topk < 1 or n % topk:
+        raise ValueError("expert_ids must hold topk ids per token")
+    for r, v in enumerate(expert_ids):
+        _typed(v, ("int32",), f"expert_ids[{r}]")
+    _check(lib().hoc_ep_segments(k, _ptr_array(expert_ids, 4 * n, "expert_ids"), n // topk, int(topk), int(experts),
+                                 _shaped(seg, (k, int(experts) + 1), "seg", ("int64",)), _stream(stream)),
+           "hoc_ep_segments")
+
+
+def expert_mm(x, weight, seg, y, *, status, bias=None, act: str = "none", pre=None, stream=None):
+    """y[d][r] = act(W[d][e] x[d][r] + bias[d][e]) for the rows r that seg gives to expert e of rank d (see
+    include/hoc_layer.h).  Lists of k device tensors: x [capacity, in], weight [experts, out, in] ([experts, 2 * out,
+    in] for swiglu), y [capacity, out]; pre keeps the pre-activations for the gradients."""
+    a, k = _act(act), len(x)
+    if not k or weight[0].dim() != 3 or x[0].dim() != 2:
+        raise ValueError("x: a list of matrices, weight: a list of [experts, out, in] tensors")
+    mul = 2 if act == "swiglu" else 1
+    experts, wide, inp = weight[0].shape
+    if wide % mul:
+        raise ValueError("weight: swiglu needs an even number of rows, gates first")
+    out, rows = wide // mul, [t.shape[0] for t in x]
+    g, _keep = _groups(rows, experts, seg)
+    _check(lib().hoc_expert_mm(C.byref(g), _per_rank(x, [(n, inp) for n in rows], "x"),
+                               _per_rank(weight, [(experts, wide, inp)] * k, "weight"),
+                               None if bias is None else _per_rank(bias, [(experts, wide)] * k, "bias"), inp, out, a,
+                               _per_rank(y, [(n, out) for n in rows], "y"),
+                               None if pre is None else _per_rank(pre, [(n, wide) for n in rows], "pre"),
+                               _ptr(status, 4, "status"), _stream(stream)), "hoc_expert_mm")
+
+
+def expert_mm_dgrad(dy, weight, seg, dx, *, status, act: str = "none", pre=None, stream=None):
+    """dx[d][r] = W[d][e]^T dy[d][r]; with act the layer's input came out of that activation and dx is the gradient
+    for what went into it, pre (see include/hoc_layer.h)."""
+    a, k = _act(act), len(dy)
+    if not k or weight[0].dim() != 3 or dy[0].dim() != 2:
+        raise ValueError("dy: a list of matrices, weight: a list of [experts, out, in] tensors")
+    if (act != "none") != (pre is not None):
+        raise ValueError("pre is given exactly when there is an activation")
+    experts, out, inp = weight[0].shape
+    wide, rows = inp * (2 if act == "swiglu" else 1), [t.shape[0] for t in dy]
+    g, _keep = _groups(rows, experts, seg)
+    _check(lib().hoc_expert_mm_dgrad(C.byref(g), _per_rank(dy, [(n, out) for n in rows], "dy"),
+                                     _per_rank(weight, [(experts, out, inp)] * k, "weight"), inp, out, a,
+                                     None if pre is None else _per_rank(pre, [(n, wide) for n in rows], "pre"),
+                                     _per_rank(dx, [(n, wide) for n in rows], "dx"), _ptr(status, 4, "status"),
+                                     _stream(stream)), "hoc_expert_mm_dgrad")
+
+
+def expert_mm_wgrad(dy, x, seg, dw, *, status, db=None, accumulate: bool = False, stream=None):
+    """dw[d][e] (+)= sum of dy[r]^T x[r] over the rows of expert e of rank d, db[d][e] (+)= sum of dy[r]; dw [experts,
+    out, in] and db [experts, out] in bf16 or float32 (see include/hoc_layer.h)."""
+    k = len(x)
+    if not k or dw[0].dim() != 3:
+        raise ValueError("x: a list of matrices, dw: a list of [experts, out, in] tensors")
+    experts, out, inp = dw[0].shape
+    rows, dt = [t.shape[0] for t in x], ("float32",) if dw[0].dtype.is_floating_point and dw[0].element_size() == 4 else ("bfloat16",)
+    g, _keep = _groups(rows, experts, seg)
+    _check(lib().hoc_expert_mm_wgrad(C.byref(g), _per_rank(dy, [(n, out) for n in rows], "dy"),
+                                     _per_rank(x, [(n, inp) for n in rows], "x"), inp, out, _dtype_code(dw[0]),
+                                     int(bool(accumulate)), _per_rank(dw, [(experts, out, inp)] * k, "dw", dt),
+                                     None if db is None else _per_rank(db, [(experts, out)] * k, "db", dt),
+                                     _ptr(status, 4, "status"), _stream(stream)), "hoc_expert_mm_wgrad")
+
+
+def linear(x, weight, y, *, status, bias=None, act: str = "none", pre=None, residual=None, stream=None):
+    """y = act(x W^T + bias) + residual; x, y and residual may be rows of wider buffers (see include/hoc_layer.h)."""
+    a = _act(act)
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x and weight must be matrices")
+    (rows, inp), wide = x.shape, weight.shape[0]
+    mul = 2 if act == "swiglu" else 1
+    if wide % mul:
+        raise ValueError("weight: swiglu needs an even number of rows, gates first")
+    out = wide // mul
+    xp, ldx = _strided(x, (rows, inp), "x")
+    yp, ldy = _strided(y, (rows, out), "y")
+    rp, ldr = _strided(residual, (rows, out), "residual") if residual is not None else (None, 0)
+    _check(lib().hoc_linear(rows, xp, ldx, _shaped(weight, (wide, inp), "weight"),
+                            None if bias is None else _shaped(bias, (wide,), "bias"), rp, ldr, inp, out, a, yp, ldy,
+                            None if pre is None else _shaped(pre, (rows, wide), "pre"), _ptr(status, 4, "status"),
+                            _stream(stream)), "hoc_linear")
+
+
+def linear_dgrad(dy, weight, dx, *, status, act: str = "none", pre=None, stream=None):
+    """dx = dy W, through the activation below the layer as in expert_mm_dgrad (see include/hoc_layer.h)."""
+    a = _act(act)
+    if dy.dim() != 2 or weight.dim() != 2:
+        raise ValueError("dy and weight must be matrices")
+    if (act != "none") != (pre is not None):
+        raise ValueError("pre is given exactly when there is an activation")
+    out, inp = weight.shape
+    rows, wide = dy.shape[0], inp * (2 if act == "swiglu" else 1)
+    dp, ldd = _strided(dy, (rows, out), "dy")
+    _check(lib().hoc_linear_dgrad(rows, dp, ldd, _shaped(weight, (out, inp), "weight"), inp, out, a,
+                                  None if pre is None else _shaped(pre, (rows, wide), "pre"),
+                                  _shaped(dx, (rows, wide), "dx"), _ptr(status, 4, "status"), _stream(stream)),
+           "hoc_linear_dgrad")
+
+
+def linear_wgrad(dy, x, dw, *, status, db=None, accumulate: bool = False, stream=None):
+    """dw (+)= dy^T x and db (+)= column sums of dy, in bf16 or float32 (see include/hoc_layer.h)."""
+    if dw.dim() != 2 or x.dim() != 2:
+        raise ValueError("x and dw must be matrices")
+    (out, inp), rows = dw.shape, x.shape[0]
+    dt = ("float32",) if dw.dtype.is_floating_point and dw.element_size() == 4 else ("bfloat16",)
+    dp, ldd = _strided(dy, (rows, out), "dy")
+    xp, ldx = _strided(x, (rows, inp), "x")
+    _check(lib().hoc_linear_wgrad(rows, dp, ldd, xp, ldx, inp, out, _dtype_code(dw), int(bool(accumulate)),
+                                  _shaped(dw, (out, inp), "dw", dt),
+                                  None if db is None else _shaped(db, (out,), "db", dt), _ptr(status, 4, "status"),
+                                  _stream(stream)), "hoc_linear_wgrad")
+
+
+def act_grad(dy, pre, dz, act: str, stream=None):
+    """dz = dy * act'(pre); dz may be pre, or dy where the activation is not gated (see include/hoc_layer.h)."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix")
+    rows, width = dy.shape
+    wide = width * (2 if act == "swiglu" else 1)
+    _check(lib().hoc_act_grad(rows, width, _act(act), _shaped(dy, (rows, width), "dy"),
+                              _shaped(pre, (rows, wide), "pre"), _shaped(dz, (rows, wide), "dz"), _stream(stream)),
+           "hoc_act_grad")
+
+
+# ------------------------------------------------------------- gradient clipping
+class TensorList:
+    """Device tensors of one dtype (float32 or bfloat16), as a table the gradient kernels read.
+
+    Holds references to the tensors; free it with close() or as a context manager."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        dts = {t.dtype for t in self.tensors}
+        if len(dts) > 1:
+            raise TypeError("the tensors of a list must have one dtype")
+        dtype = _dtype_code(self.tensors[0]) if self.tensors else FLOAT32
+        n = len(self.tensors)
+        counts = (C.c_size_t * max(1, n))(*[t.numel() for t in self.tensors])
+        h = C.c_void_p()
+        _check(lib().hoc_tensor_list_create(C.byref(h), n, _ptr_array(self.tensors, 0, "tensors"), counts, dtype),
+               "hoc_tensor_list_create")
+        self._h = h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _check(lib().hoc_tensor_list_destroy(self._h), "hoc_tensor_list_destroy")
+            self._h = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *a):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def grad_workspace(tensors: TensorList) -> int:
+    """int32 entries of scratch that grad_norm and grad_clip need for this list."""
+    n = C.c_size_t()
+    _check(lib().hoc_grad_workspace(tensors._h, C.byref(n)), "hoc_grad_workspace")
+    return n.value
+
+
+def grad_norm(tensors: TensorList, norm, workspace, stream=None):
+    """norm[0] = the global 2-norm of the list (see include/hoc_grad.h); norm: float32, workspace: int32 tensors."""
+    _check(lib().hoc_grad_norm(tensors._h, _ptr(_typed(norm, ("float32",), "norm"), 4, "norm"),
+                               _ptr(_typed(workspace, ("int32",), "workspace"), 0, "workspace"),
+                               int(workspace.numel()), _stream(stream)), "hoc_grad_norm")
+
+
+def grad_clip(src: TensorList, dst: TensorList, max_norm: float, norm, workspace, stream=None):
+    """dst = min(1, max_norm / (norm + 1e-6)) * src with the global norm of src, which is left in norm[0]; dst may be
+    src (see include/hoc_grad.h)."""
+    _check(lib().hoc_grad_clip(src._h, dst._h, C.byref(C.c_float(max_norm)), _ptr(_typed(norm, ("float32",), "norm"), 4, "norm"),
+                               _ptr(_typed(workspace, ("int32",), "workspace"), 0, "workspace"),
+                               int(workspace.numel()), _stream(stream)), "hoc_grad_clip")
 
 
 def sm_count(device: int = 0) -> int:

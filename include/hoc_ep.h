@@ -138,6 +138,35 @@ hocResult_t hoc_ep_combine_all(int nranks, const void* const* rows, const size_t
                                const int32_t* const* pos_of, const float* const* weights, int tokens, int topk,
                                int hidden, void* const* y, int32_t* status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Gradient of the combine, for training through the experts.
+ * ------------------------------------------------------------------------- */
+
+/* Gradient of hoc_ep_combine_fused: dy[s] is the gradient for y[s], [tokens,
+ * hidden] bf16; rows, rows_capacity, expert_ids, pos_of, counts and weights are
+ * those of the combine.  For every valid pair (t, j) of source s with its row r
+ * in rank d's buffer
+ *   drows[d][r] = bf16(fp32(weights[s][t, j] * dy[s][t])),
+ *   dweights[s][t, j] = sum over hidden of row[d][r] * dy[s][t]   (fp32 sums),
+ * drows[d] having the layout and capacity of rows[d] (not the same buffer);
+ * rows that no pair names are not written.  dweights is 0 for a dropped pair
+ * and for one whose row lies outside its buffer (bit 1 of *status, not cleared
+ * here).  The gradient for the tokens is hoc_ep_combine_fused of the experts'
+ * input gradients with all weights 1.  A rank whose capacity is 0 may have NULL
+ * buffers. */
+hocResult_t hoc_ep_combine_grad(int nranks, const void* const* dy, const void* const* rows,
+                                const size_t* rows_capacity, const int32_t* const* expert_ids,
+                                const int32_t* const* pos_of, const uint64_t* counts, const float* const* weights,
+                                int tokens, int topk, int hidden, int experts, void* const* drows,
+                                float* const* dweights, int32_t* status, void* stream);
+
+/* The same for hoc_ep_combine_all: rows[s] and drows[s] hold source s's rows in
+ * packed order. */
+hocResult_t hoc_ep_combine_grad_all(int nranks, const void* const* dy, const void* const* rows,
+                                    const size_t* rows_capacity, const int32_t* const* pos_of,
+                                    const float* const* weights, int tokens, int topk, int hidden, void* const* drows,
+                                    float* const* dweights, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,409 @@
+"""Expert products grouped by ragged row ranges, the linear layer, and their gradients, against 64-bit plain forms
+(tests/layer_ref.py derives the bounds)."""
+import pytest
+import torch
+
+from collective_communication_schedules_gb300 import hoc
+from tests import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def normal(*shape, seed=0, sigma=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device=DEV) * sigma).to(BF)
+
+
+def status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+# counts [rank][source][expert], in, out: ranges that end inside every tile size, empty experts and sources, one row,
+# a rank without rows, all rows at one expert, widths that are and are not whole 16-byte rows
+LAYOUTS = {
+    "one row": ([[[1]]], 64, 32),
+    "aligned": ([[[64, 128]]], 128, 64),
+    "ragged": (ref.random_counts(2, 3, 4, 40, 1), 200, 136),
+    "many sources": (ref.random_counts(3, 16, 2, 9, 2), 72, 48),
+    "tile edges": ([[[255, 256, 257]], [[7, 8, 9]]], 264, 272),
+    "empty rank": ([[[0, 0], [0, 0]], [[5, 0], [0, 11]]], 64, 64),
+    "one expert": ([[[0, 700, 0, 0], [0, 333, 0, 0]]], 512, 304),
+    "odd widths": (ref.random_counts(2, 2, 3, 50, 3), 61, 45),
+    "odd in": (ref.random_counts(1, 2, 3, 70, 4), 131, 64),
+    "odd out": (ref.random_counts(1, 2, 3, 70, 5), 64, 131),
+    "wide": ([[[33, 90]], [[200, 1]]], 1032, 520),
+    "many experts": (ref.random_counts(1, 1, 1500, 3, 6), 40, 24),
+}
+
+
+def expert_inputs(name, mul=1, sigma_x=1.0):
+    counts, inp, out = LAYOUTS[name]
+    L = ref.Routed(counts)
+    x = [normal(n, inp, seed=10 + d, sigma=sigma_x) for d, n in enumerate(L.cap)]
+    for d in range(L.k):
+        x[d][L.of[d] < 0] = float("nan")  # nobody's rows must reach no result
+    w = [normal(L.experts, mul * out, inp, seed=20 + d, sigma=inp ** -0.5) for d in range(L.k)]
+    b = [normal(L.experts, mul * out, seed=30 + d, sigma=0.5) for d in range(L.k)]
+    return L, x, w, b, inp, out
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("name", list(LAYOUTS))
+def test_expert_forward(name, act):
+    mul = 2 if act == "swiglu" else 1
+    L, x, w, b, inp, out = expert_inputs(name, mul)
+    with_bias = act != "relu"
+    y = [torch.full((n, out), 7.0, dtype=BF, device=DEV) for n in L.cap]
+    pre = [torch.full((n, mul * out), 7.0, dtype=BF, device=DEV) for n in L.cap]
+    st = status()
+    hoc.expert_mm(x, w, L.seg, y, status=st, bias=b if with_bias else None, act=act, pre=pre)
+    y2 = [torch.empty_like(v) for v in y]
+    hoc.expert_mm(x, w, L.seg, y2, status=st, bias=b if with_bias else None, act=act)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for d in range(L.k):
+        nobody = L.of[d] < 0
+        assert bool((y[d][nobody] == 7).all()) and bool((pre[d][nobody] == 7).all()), "a row of no range was written"
+        assert torch.equal(y[d][~nobody], y2[d][~nobody])
+        for e in range(L.experts):
+            r = L.rows(d, e)
+            if len(r) == 0:
+                continue
+            z, ez, want, ey = ref.forward(x[d][r], w[d][e], b[d][e] if with_bias else None, act)
+            ref.close(pre[d][r], z, ez, f"pre {d} {e}")
+            ref.close(y[d][r], want, ey, f"y {d} {e}")
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("name", list(LAYOUTS))
+def test_expert_dgrad(name, act):
+    mul = 2 if act == "swiglu" else 1
+    counts, inp, out = LAYOUTS[name]
+    L = ref.Routed(counts)
+    dy = [normal(n, out, seed=40 + d) for d, n in enumerate(L.cap)]
+    pre = [normal(n, mul * inp, seed=50 + d, sigma=2.0) for d, n in enumerate(L.cap)]
+    for d in range(L.k):
+        dy[d][L.of[d] < 0] = float("nan")
+    w = [normal(L.experts, out, inp, seed=20 + d, sigma=inp ** -0.5) for d in range(L.k)]
+    dx = [torch.full((n, mul * inp), 7.0, dtype=BF, device=DEV) for n in L.cap]
+    st = status()
+    hoc.expert_mm_dgrad(dy, w, L.seg, dx, status=st, act=act, pre=pre if act != "none" else None)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for d in range(L.k):
+        assert bool((dx[d][L.of[d] < 0] == 7).all()), "a row of no range was written"
+        for e in range(L.experts):
+            r = L.rows(d, e)
+            if len(r):
+                want, err = ref.dgrad(dy[d][r], w[d][e], act, pre[d][r])
+                ref.close(dx[d][r], want, err, f"dx {d} {e}")
+
+
+@pytest.mark.parametrize("dtype,accumulate", [(BF, False), (torch.float32, True), (torch.float32, False), (BF, True)])
+@pytest.mark.parametrize("name", list(LAYOUTS))
+def test_expert_wgrad(name, dtype, accumulate):
+    L, x, _, _, inp, out = expert_inputs(name)
+    dy = [normal(n, out, seed=40 + d) for d, n in enumerate(L.cap)]
+    for d in range(L.k):
+        dy[d][L.of[d] < 0] = float("nan")
+    dw = [normal(L.experts, out, inp, seed=60 + d).to(dtype) for d in range(L.k)]
+    db = [normal(L.experts, out, seed=70 + d).to(dtype) for d in range(L.k)]
+    was = [v.double() for v in dw], [v.double() for v in db]
+    st = status()
+    hoc.expert_mm_wgrad(dy, x, L.seg, dw, status=st, db=db, accumulate=accumulate)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    half = ref.BF16 if dtype == BF else ref.F32
+    for d in range(L.k):
+        for e in range(L.experts):
+            r = L.rows(d, e)
+            a, v = dy[d][r].double(), x[d][r].double()
+            n = max(1, len(r))
+            ew, eb = (a.abs().t() @ v.abs()) * n * ref.F32, a.abs().sum(0) * n * ref.F32
+            want_w, want_b = a.t() @ v, a.sum(0)
+            if accumulate:
+                want_w, want_b = want_w + was[0][d][e], want_b + was[1][d][e]
+            ref.close(dw[d][e], want_w, ew + want_w.abs() * ref.F32, f"dw {d} {e}", half)
+            ref.close(db[d][e], want_b, eb + want_b.abs() * ref.F32, f"db {d} {e}", half)
+
+
+def test_rows_of_one_expert_stay_out_of_the_others():
+    """NaN and inf rows of one expert reach no other expert's results, in any direction."""
+    L = ref.Routed([[[37, 21, 5], [3, 0, 44]]])
+    inp, out = 128, 96
+    x, dy = normal(L.cap[0], inp, seed=1), normal(L.cap[0], out, seed=2)
+    bad = L.rows(0, 1)
+    x[bad], dy[bad] = float("nan"), float("inf")
+    w = [normal(3, out, inp, seed=3, sigma=inp ** -0.5)]
+    y, dx = torch.zeros(L.cap[0], out, dtype=BF, device=DEV), torch.zeros(L.cap[0], inp, dtype=BF, device=DEV)
+    dw = [torch.zeros(3, out, inp, dtype=BF, device=DEV)]
+    db = [torch.zeros(3, out, dtype=BF, device=DEV)]
+    st = status()
+    hoc.expert_mm([x], w, L.seg, [y], status=st)
+    hoc.expert_mm_dgrad([dy], w, L.seg, [dx], status=st)
+    hoc.expert_mm_wgrad([dy], [x], L.seg, dw, status=st, db=db)
+    torch.cuda.synchronize()
+    for e in (0, 2):
+        r = L.rows(0, e)
+        assert bool(torch.isfinite(y[r]).all()) and bool(torch.isfinite(dx[r]).all())
+        assert bool(torch.isfinite(dw[0][e]).all()) and bool(torch.isfinite(db[0][e]).all())
+    assert bool(y[bad].isnan().all()) and bool(dw[0][1].isnan().all())
+
+
+def test_ranges_are_cut_to_the_buffer():
+    """Ranges past the buffer's capacity, as after a dispatch that ran out of room, are cut; nothing past it is touched."""
+    inp, out, cap = 64, 64, 50
+    big = torch.full((cap + 30, inp), float("nan"), dtype=BF, device=DEV)
+    x = big[:cap]
+    x.copy_(normal(cap, inp, seed=1))
+    seg = torch.tensor([[0, 30, 80, 75]], device=DEV)  # the second ends past the buffer, the third before it starts
+    w = [normal(3, out, inp, seed=2, sigma=inp ** -0.5)]
+    ybig = torch.full((cap + 30, out), 7.0, dtype=BF, device=DEV)
+    dw = [torch.zeros(3, out, inp, dtype=BF, device=DEV)]
+    st = status()
+    dy = normal(cap, out, seed=3)
+    hoc.expert_mm([x], w, seg, [ybig[:cap]], status=st)
+    hoc.expert_mm_wgrad([dy], [x], seg, dw, status=st)
+    torch.cuda.synchronize()
+    assert bool((ybig[cap:] == 7).all())
+    for e, (lo, hi) in enumerate([(0, 30), (30, 50)]):
+        _, _, want, err = ref.forward(x[lo:hi], w[0][e], None, "none")
+        ref.close(ybig[lo:hi], want, err, f"y {e}")
+        a, v = dy[lo:hi].double(), x[lo:hi].double()
+        ref.close(dw[0][e], a.t() @ v, (a.abs().t() @ v.abs()) * (hi - lo) * ref.F32, f"dw {e}")
+    assert bool((dw[0][2] == 0).all())
+
+
+LINEARS = [  # rows, in, out
+    (1, 64, 64), (1, 4096, 520), (3, 1032, 264), (8, 512, 4096), (9, 128, 72), (16, 2048, 96), (17, 256, 640),
+    (31, 520, 136), (64, 1024, 1024), (100, 136, 2056), (256, 512, 512), (257, 264, 776), (1000, 96, 40),
+    (2, 33, 17), (5, 1, 1), (130, 77, 99), (40, 64, 33), (40, 35, 64),
+]
+
+
+@pytest.mark.parametrize("act,residual,pad", [("none", False, 0), ("gelu", True, 8), ("silu", True, 0), ("relu", False, 1),
+                                              ("swiglu", False, 0), ("swiglu", True, 16)])
+@pytest.mark.parametrize("rows,inp,out", LINEARS)
+def test_linear(rows, inp, out, act, residual, pad):
+    mul = 2 if act == "swiglu" else 1
+    x = normal(rows, inp + pad, seed=1)[:, :inp]
+    w, b = normal(mul * out, inp, seed=2, sigma=inp ** -0.5), normal(mul * out, seed=3)
+    r = normal(rows, out + pad, seed=4)[:, :out] if residual else None
+    ybig = torch.full((rows, out + pad), 7.0, dtype=BF, device=DEV)
+    y, pre = ybig[:, :out], torch.empty(rows, mul * out, dtype=BF, device=DEV)
+    st = status()
+    hoc.linear(x, w, y, status=st, bias=b, act=act, pre=pre, residual=r)
+    y2 = r.clone() if residual else torch.empty(rows, out, dtype=BF, device=DEV)
+    hoc.linear(x, w, y2, status=st, bias=b, act=act, residual=y2 if residual else None)  # in place on the residual
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert bool((ybig[:, out:] == 7).all()), "written past a row's end"
+    z, ez, want, ey = ref.forward(x, w, b, act)
+    ref.close(pre, z, ez, "pre")
+    if residual:
+        want = want + r.double()
+        ey = ey + want.abs() * ref.F32
+    ref.close(y, want, ey, "y")
+    assert torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("rows,inp,out", LINEARS)
+def test_linear_gradients(rows, inp, out, act):
+    mul = 2 if act == "swiglu" else 1
+    x, dy = normal(rows, inp + 8, seed=1)[:, :inp], normal(rows, out + 8, seed=2)[:, :out]
+    w, pre = normal(out, inp, seed=3, sigma=inp ** -0.5), normal(rows, mul * inp, seed=4)
+    dx = torch.empty(rows, mul * inp, dtype=BF, device=DEV)
+    dw, db = torch.empty(out, inp, device=DEV), torch.empty(out, device=DEV)
+    st = status()
+    hoc.linear_dgrad(dy, w, dx, status=st, act=act, pre=pre if act != "none" else None)
+    hoc.linear_wgrad(dy, x, dw, status=st, db=db)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    want, err = ref.dgrad(dy, w, act, pre)
+    ref.close(dx, want, err, "dx")
+    a, v = dy.double(), x.double()
+    ref.close(dw, a.t() @ v, (a.abs().t() @ v.abs()) * rows * ref.F32, "dw", ref.F32)
+    ref.close(db, a.sum(0), a.abs().sum(0) * rows * ref.F32, "db", ref.F32)
+
+
+def test_linear_without_rows():
+    w, st = normal(32, 64, seed=1), status()
+    x, y = torch.empty(0, 64, dtype=BF, device=DEV), torch.empty(0, 32, dtype=BF, device=DEV)
+    hoc.linear(x, w, y, status=st)
+    hoc.linear_dgrad(y, w, x, status=st)
+    dw, db = torch.full((32, 64), 5.0, device=DEV), torch.full((32,), 5.0, device=DEV)
+    hoc.linear_wgrad(y, x, dw, status=st, db=db, accumulate=True)
+    assert bool((dw == 5).all()) and bool((db == 5).all())
+    hoc.linear_wgrad(y, x, dw, status=st, db=db)
+    assert bool((dw == 0).all()) and bool((db == 0).all())
+
+
+def test_a_few_bytes_off():
+    """Operands that start 2 bytes past a 16-byte boundary."""
+    n, inp, out = 70, 64, 48
+    off = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)  # noqa: E731
+    x, w, b = off(normal(n, inp, seed=1)), off(normal(out, inp, seed=2, sigma=0.1)), off(normal(out, seed=3))
+    y, st = off(torch.zeros(n, out, dtype=BF, device=DEV)), status()
+    hoc.linear(x, w, y, status=st, bias=b, act="gelu")
+    _, _, want, err = ref.forward(x, w, b, "gelu")
+    ref.close(y, want, err, "y")
+
+
+def test_on_another_stream_and_in_a_graph():
+    n, inp, out = 300, 256, 128
+    x, w, st = normal(n, inp, seed=1), normal(out, inp, seed=2, sigma=inp ** -0.5), status()
+    y = torch.zeros(n, out, dtype=BF, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    hoc.linear(x, w, y, status=st, stream=s)
+    s.synchronize()
+    first = y.clone()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        hoc.linear(x, w, y, status=st, stream=s)
+    x.copy_(normal(n, inp, seed=9))
+    g.replay()
+    torch.cuda.synchronize()
+    _, _, want, err = ref.forward(x, w, None, "none")
+    ref.close(y, want, err, "replayed")
+    assert not torch.equal(first, y)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("rows,width", [(1, 1), (5, 64), (33, 40), (7, 13)])
+def test_act_grad(rows, width, act):
+    mul = 2 if act == "swiglu" else 1
+    dy, pre = normal(rows, width, seed=1), normal(rows, mul * width, seed=2, sigma=3.0)
+    dz = torch.empty_like(pre)
+    hoc.act_grad(dy, pre, dz, act)
+    want, err = ref.dgrad(dy, torch.eye(width, device=DEV), act, pre)
+    ref.close(dz, want, err, "dz")
+    again = pre.clone()
+    hoc.act_grad(dy, again, again, act)
+    assert torch.equal(again, dz)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "swiglu", "relu"])
+def test_activations_at_the_ends_of_the_range(act):
+    """Values whose exponentials over- or underflow, and infinite ones; against the limits."""
+    v = torch.tensor([0.0, -0.0, 30.0, -30.0, 100.0, -100.0, 3e38, -3e38, 1e-38], device=DEV).to(BF)
+    n = len(v)
+    eye = torch.ones(1, 1, dtype=BF, device=DEV)
+    x = v.view(n, 1).contiguous()
+    w = torch.cat([eye, eye]) if act == "swiglu" else eye
+    b = torch.tensor([0.0, 1.0], device=DEV).to(BF) if act == "swiglu" else None
+    y, st = torch.empty(n, 1, dtype=BF, device=DEV), status()
+    hoc.linear(x, w, y, status=st, act=act, bias=b)
+    z = v.double()
+    want = z.clamp(min=0) if act == "relu" else z * torch.sigmoid(z) if act != "gelu" else ref.act("gelu", z)
+    if act == "swiglu":
+        want = want * (z + 1)
+    over = want.abs() > 3.4e38
+    assert bool(torch.isfinite(y[~over]).all())
+    ref.close(y[~over, 0], want[~over], want[~over].abs() * ref.MATH + 1e-30, "y")
+    dz = torch.empty(n, 2 if act == "swiglu" else 1, dtype=BF, device=DEV)
+    pre = torch.cat([x, torch.ones_like(x)], 1) if act == "swiglu" else x
+    hoc.act_grad(torch.ones(n, 1, dtype=BF, device=DEV), pre.contiguous(), dz, act)
+    assert bool(torch.isfinite(dz).all())
+    assert dz[2, 0] == 1 and dz[4, 0] == 1 and dz[6, 0] == 1 and abs(float(dz[5, 0])) < 1e-30 and dz[7, 0] == 0
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "swiglu"])
+def test_gradients_against_differences(act):
+    """The gradients of sum(act(x W^T) * c) for x and W against central differences of the 64-bit definition."""
+    rows, inp, out, mul = 4, 8, 8, 2 if act == "swiglu" else 1
+    x, w = normal(rows, inp, seed=1), normal(mul * out, inp, seed=2, sigma=0.5)
+    c = normal(rows, out, seed=3)
+    y, pre, st = torch.empty(rows, out, dtype=BF, device=DEV), torch.empty(rows, mul * out, dtype=BF, device=DEV), status()
+    hoc.linear(x, w, y, status=st, act=act, pre=pre)
+    dz, dx, dw = torch.empty_like(pre), torch.empty_like(x), torch.empty(mul * out, inp, device=DEV)
+    hoc.act_grad(c, pre, dz, act)
+    hoc.linear_dgrad(dz, w, dx, status=st)
+    hoc.linear_wgrad(dz, x, dw, status=st)
+
+    def loss(xx, ww):
+        return float((ref.forward(xx, ww, None, act)[2] * c.double()).sum())
+
+    h = 1e-5
+    for t, got, which in ((x.double(), dx, 0), (w.double(), dw, 1)):
+        for i in range(t.shape[0]):
+            for j in range(t.shape[1]):
+                up, dn = t.clone(), t.clone()
+                up[i, j] += h
+                dn[i, j] -= h
+                args = [(up, w.double()), (dn, w.double())] if which == 0 else [(x.double(), up), (x.double(), dn)]
+                want = (loss(*args[0]) - loss(*args[1])) / (2 * h)
+                # pre, dz and dx are each rounded to bf16: three roundings of terms of the size of the products
+                scale = float((dz.double().abs()[i] @ w.double().abs()[:, j]) if which == 0
+                              else (dz.double().abs()[:, i] @ x.double().abs()[:, j]))
+                assert abs(float(got[i, j]) - want) <= 6 * ref.BF16 * (scale + abs(want)) + 1e-6, (which, i, j)
+
+
+def test_segments_follow_the_dispatch():
+    """ep_segments gives the ranges in which a fused dispatch leaves each expert's rows; dropped pairs count nowhere."""
+    k, tokens, topk, experts, hidden = 4, 77, 3, 8, 16
+    g = torch.Generator(device=DEV).manual_seed(3)
+    ids = [torch.rand(tokens, experts, generator=g, device=DEV).topk(topk, 1).indices.to(torch.int32).flatten() for _ in range(k)]
+    ids[1][5] = -1
+    ids[2][9] = experts
+    x = [torch.arange(tokens, device=DEV).view(-1, 1).expand(tokens, hidden).to(BF).contiguous() for _ in range(k)]
+    cap = [k * tokens * topk] * k
+    recv = [torch.full((c, hidden), -1.0, dtype=BF, device=DEV) for c in cap]
+    pos = [torch.empty(tokens * topk, dtype=torch.int32, device=DEV) for _ in range(k)]
+    counts = torch.empty(k, k, dtype=torch.int64, device=DEV)
+    ws = torch.empty(k * hoc.ep_pack_workspace(tokens, topk, experts), dtype=torch.int32, device=DEV)
+    hoc.ep_dispatch_fused(ids, x, experts, [t.view(-1) for t in recv], [c * hidden for c in cap], pos, counts, ws, status())
+    seg = torch.full((k, experts + 1), -5, dtype=torch.int64, device=DEV)
+    hoc.ep_segments(ids, experts, topk, seg)
+    per = experts // k
+    for d in range(k):
+        at = 0
+        for s in range(k):
+            for e in range(per):
+                want = torch.nonzero(ids[s] == d * per + e).flatten() // topk
+                lo, hi = seg[d, s * per + e].item(), seg[d, s * per + e + 1].item()
+                assert lo == at and hi == at + len(want)
+                assert torch.equal(recv[d][lo:hi, 0].long(), want)
+                at = hi
+    many = [torch.randint(0, 9000, (500,), generator=g, device=DEV, dtype=torch.int32)]
+    seg = torch.empty(1, 9001, dtype=torch.int64, device=DEV)
+    hoc.ep_segments(many, 9000, 1, seg)
+    assert torch.equal(seg[0, 1:], torch.bincount(many[0].long(), minlength=9000).cumsum(0)) and seg[0, 0] == 0
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_random_expert_layers(seed):
+    """Random layouts and widths through all three products."""
+    g = torch.Generator().manual_seed(100 + seed)
+    pick = lambda *v: v[int(torch.randint(len(v), (1,), generator=g))]  # noqa: E731
+    k, sources, experts = pick(1, 2, 5), pick(1, 2, 8), pick(1, 3, 8)
+    inp, out, act = pick(8, 96, 192, 328, 50), pick(16, 64, 144, 400, 21), pick("none", "gelu", "swiglu")
+    mul = 2 if act == "swiglu" else 1
+    L = ref.Routed(ref.random_counts(k, sources, experts, pick(3, 60, 300), seed))
+    x = [normal(n, inp, seed=seed + d) for d, n in enumerate(L.cap)]
+    w = [normal(experts, mul * out, inp, seed=20 + d, sigma=inp ** -0.5) for d in range(k)]
+    y = [torch.empty(n, out, dtype=BF, device=DEV) for n in L.cap]
+    pre = [torch.empty(n, mul * out, dtype=BF, device=DEV) for n in L.cap]
+    dx = [torch.empty(n, inp, dtype=BF, device=DEV) for n in L.cap]
+    dw = [torch.empty(experts, mul * out, inp, dtype=BF, device=DEV) for _ in range(k)]
+    st = status()
+    hoc.expert_mm(x, w, L.seg, y, status=st, act=act, pre=pre)
+    hoc.expert_mm_dgrad(pre, w, L.seg, dx, status=st)
+    hoc.expert_mm_wgrad(pre, x, L.seg, dw, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for d in range(k):
+        for e in range(experts):
+            r = L.rows(d, e)
+            a, v = pre[d][r].double(), x[d][r].double()
+            ref.close(dw[d][e], a.t() @ v, (a.abs().t() @ v.abs()) * max(1, len(r)) * ref.F32, f"dw {d} {e}")
+            if len(r):
+                z, ez, want, ey = ref.forward(x[d][r], w[d][e], None, act)
+                ref.close(y[d][r], want, ey, f"y {d} {e}")
+                want, err = ref.dgrad(pre[d][r], w[d][e], "none", None)
+                ref.close(dx[d][r], want, err, f"dx {d} {e}")
