@@ -1,5 +1,5 @@
 // Matrix products on rows grouped by expert: what the host entry points
-// (layer.cu) pass to the kernels (mm_any.cu).
+// (layer.cu) pass to the kernels (mm_any.cu, mm_tc.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -147,5 +147,9 @@ __device__ __forceinline__ float mm_act_slope(int act, float z) {
 // Host side -----------------------------------------------------------------
 cudaError_t launch_mm_any(const MmParams& P, int mode, int sms, cudaStream_t s);
 cudaError_t mm_any_preload();
+// Whether the tensor-core kernel takes these operands (alignment and widths).
+bool mm_tc_takes(const MmParams& P, int mode);
+cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s);
+cudaError_t mm_tc_preload();
 
 }  // namespace hoc

@@ -407,3 +407,26 @@ def test_random_expert_layers(seed):
                 ref.close(y[d][r], want, ey, f"y {d} {e}")
                 want, err = ref.dgrad(pre[d][r], w[d][e], "none", None)
                 ref.close(dx[d][r], want, err, f"dx {d} {e}")
+
+
+@pytest.mark.parametrize("product", ["forward", "dgrad", "wgrad"])
+def test_a_wait_that_runs_out_sets_the_status(product, monkeypatch):
+    """HOC_FAULT=mm_stall makes every copy barrier expect 16 bytes that no copy brings: the kernel's waits run out
+    (0.1 s), it sets bit 2 and returns, and the next call is right again."""
+    n, inp, out = 300, 256, 512
+    x, dy, w = normal(n, inp, seed=1), normal(n, out, seed=2), normal(out, inp, seed=3, sigma=inp ** -0.5)
+    y, dx, dw, st = torch.empty_like(dy), torch.empty_like(x), torch.empty_like(w), status()
+    call = {"forward": lambda: hoc.linear(x, w, y, status=st), "dgrad": lambda: hoc.linear_dgrad(dy, w, dx, status=st),
+            "wgrad": lambda: hoc.linear_wgrad(dy, x, dw, status=st)}[product]
+    monkeypatch.setenv("HOC_FAULT", "mm_stall")
+    call()
+    torch.cuda.synchronize()
+    assert st.item() == 4
+    monkeypatch.delenv("HOC_FAULT")
+    st.zero_()
+    call()
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    got, want = {"forward": (y, x.double() @ w.double().t()), "dgrad": (dx, dy.double() @ w.double()),
+                 "wgrad": (dw, dy.double().t() @ x.double())}[product]
+    assert float((got.double() - want).norm() / want.norm()) < 2 * ref.BF16
