@@ -24,7 +24,7 @@
 // are overwritten with zeros in shared memory before the MMA reads them.
 //
 // Warps of a CTA: 0 tensor copies, 1 MMA (of the pair's first CTA), 2 tensor
-// memory and the zeroing, 4-7 epilogue.  Every wait is bounded: a wait that runs
+// memory and the zeroing, 4-11 epilogue.  Every wait is bounded: a wait that runs
 // out sets bit 2 of the status, and all roles leave.
 #include <atomic>
 #include <cstdlib>
@@ -38,7 +38,9 @@
 namespace hoc {
 namespace {
 
-constexpr int kTcThreads = 256;
+constexpr int kTcThreads = 384;
+constexpr int kTcEpilogue = 8;                  // warps: two to each 32 lanes of tensor memory
+constexpr int kTcColumns = 16;                  // accumulator columns of an epilogue step
 constexpr int kTcStages = 6;
 constexpr int kTcDepth = 64;                    // contraction elements of a stage: one 128-byte swizzled row
 constexpr uint32_t kTcOperand = 128 * 128;      // bytes of one operand of a stage in one CTA
@@ -59,11 +61,11 @@ struct TcParams {
 };
 
 struct TcShared {
-  uint64_t full[kTcStages];   // forward, dgrad: the pair's loads, on the first CTA; wgrad: this CTA's loads
-  uint64_t ready[kTcStages];  // wgrad: both CTAs' stages are loaded and their padding rows zero (first CTA)
+  uint64_t full[kTcStages];   // on the first CTA: both CTAs' loads of a stage
+  uint64_t part[kTcStages];   // wgrad: this CTA's loads of a stage that holds padding rows
   uint64_t empty[kTcStages];
   uint64_t acc_full[2];
-  uint64_t acc_empty[2];      // on the first CTA: 4 epilogue warps of both CTAs
+  uint64_t acc_empty[2];      // on the first CTA: the epilogue warps of both CTAs
   uint32_t tmem;
   volatile int dead;
   int vrows[kMmMaxGroups];
@@ -89,23 +91,22 @@ __device__ __forceinline__ uint32_t on_first(const uint64_t* bar) {
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(ptx::smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// Announces `tx` bytes of copies.  Relaxed: nothing this thread wrote is handed
+// over, and a release to the cluster made every stage wait for about 1000 cycles.
+__device__ __forceinline__ void arrive_expect_cluster(uint32_t addr, uint32_t tx) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(tx)
+               : "memory");
+}
+// The same where only tensor memory, ordered by the tcgen05 fences, is handed over.
+__device__ __forceinline__ void arrive_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // Waits for the phase with `parity`; false when the limit passed here or in
 // another role, after which the caller leaves its loop.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const TcParams& T, TcShared* S) {
-  if (try_wait_cluster(bar, parity)) return true;
+  if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t deadline = ptx::global_ns() + T.wait_ns;
-  while (!try_wait_cluster(bar, parity)) {
+  while (!ptx::mbar_try_wait(bar, parity)) {
     if (S->dead) return false;
     if (ptx::global_ns() > deadline) {
       atomicOr(T.P.status, 4);
@@ -161,15 +162,12 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       "h"(uint16_t(3))
       : "memory");
 }
-__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[kTcColumns], uint32_t addr) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -214,16 +212,16 @@ __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, int g, i
   return R;
 }
 // Each lane's group of 8 virtual rows at `v` (a multiple of 8): its first row in
-// the buffer and how many of the 8 are the expert's (0: past the end).  The
-// whole warp calls it; R holds the first 32 sources' ranges.
-__device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges R, int v, int& row, int& valid) {
+// the buffer and how many rows its range has from there on (0: past the end).
+// The whole warp calls it; R holds the first 32 sources' ranges.
+__device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges R, int v, int& row, int& left) {
   const int ns = P.seg ? P.sources : 1;
   int64_t at = v;
   bool found = false;
   row = int(P.cap[p]);
-  valid = 0;
+  left = 0;
   for (int base = 0; base < ns; base += 32) {
-    if (base) R = load_ranges(P, p, g, base);
+    if (ns > 32) R = load_ranges(P, p, g, base);
     const int m = min(32, ns - base);
     for (int j = 0; j < m; ++j) {
       const int64_t lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
@@ -231,11 +229,22 @@ __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges
       if (!found && at < padded) {
         found = true;
         row = int(lo + at);
-        valid = int(n - at < 8 ? n - at : 8);
+        left = int(n - at);
       }
       at -= padded;
     }
   }
+}
+
+// wgrad: the 64 virtual rows of stage s, a group of 8 per lane modulo 8.
+// Returns (to all lanes) how many stages from s on are 64 rows each of the range
+// that stage s begins in, without padding; 0 when stage s is not.
+__device__ __forceinline__ int stage_rows(const MmParams& P, const Tile& A, const Ranges& R, int s, int& row,
+                                          int& valid) {
+  int left;
+  group_at(P, A.p, A.g, R, s * kTcDepth + int(threadIdx.x & 7) * 8, row, left);
+  valid = min(left, 8);
+  return __shfl_sync(0xFFFFFFFFu, left, 0) / kTcDepth;
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -255,113 +264,150 @@ __device__ __forceinline__ void with_act(int act, F f) {
   }
 }
 
-// 32 columns of the accumulator: v[j] is feature `f` (of this lane) and column
-// col + j; row and valid name the groups of 8 columns of the tile, one per lane.
+// What the epilogue reads beside the accumulator for a step's columns: the residual,
+// the pre-activation of the layer below, or the weights to add to.  Loaded one
+// step ahead, so that its latency passes under other work.
+struct Beside {
+  uint32_t a[kTcColumns], b[kTcColumns];  // bf16 bits, or (wgrad, binary32 weights) floats
+};
+
+__device__ __forceinline__ uint32_t bits_of(const __nv_bfloat16* p) {
+  return *reinterpret_cast<const uint16_t*>(p);
+}
+__device__ __forceinline__ float float_of(uint32_t bf16_bits) { return __uint_as_float(bf16_bits << 16); }
+
+// Loads are unconditional, at places clamped to the tensors (values of rows or
+// features that do not exist are never used): predicated ones made the compiler
+// wait for each before it issued the next.
 template <int MODE, int ACT>
-__device__ __forceinline__ void store_columns(const MmParams& P, const Tile& A, const uint32_t (&v)[32], int col, int f,
-                                              int row, int valid, float bias) {
-  const int lane = threadIdx.x & 31;
-  constexpr bool gated = MODE == kForward && ACT == HOC_ACT_SWIGLU;
-  const int width = MODE == kForward ? P.out : P.in;
-  const bool mine = f < width;
-  const int64_t wide = int64_t(P.out) * (gated ? 2 : 1);
-  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.y[A.p]);
-  __nv_bfloat16* keep = static_cast<__nv_bfloat16*>(P.pre_out[A.p]);
-  const __nv_bfloat16* res = P.res[A.p];
-  const __nv_bfloat16* pre = P.pre[A.p];
-  if constexpr (gated) {
-    // Lanes 0-15 hold the gates of 16 features, lanes 16-31 their values.  They
-    // swap halves: each then has both for 16 of the 32 columns.
-    const bool upper = lane >= 16;
+__device__ __forceinline__ void load_beside(const MmParams& P, const Tile& A, int col, int f, int row, int valid,
+                                            Beside& B) {
+  if (col >= A.n) return;
+  const bool upper = (threadIdx.x & 31) >= 16;
+  const int fc = min(f, (MODE == kForward ? P.out : P.in) - 1);
+  if constexpr (MODE == kWgrad) {
+    if (!P.accumulate) return;
+    const int64_t first = int64_t(A.g) * P.out * P.in + fc;
+    if (P.out_f32) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+      for (int j = 0; j < kTcColumns; ++j)
+        B.a[j] = __float_as_uint(
+            static_cast<const float*>(P.y[A.p])[first + int64_t(min(A.c0 + col + j, P.out - 1)) * P.in]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kTcColumns; ++j)
+        B.a[j] = bits_of(static_cast<const __nv_bfloat16*>(P.y[A.p]) + first +
+                         int64_t(min(A.c0 + col + j, P.out - 1)) * P.in);
+    }
+  } else if constexpr (MODE == kForward) {
+    if (!P.res[A.p]) return;
+#pragma unroll
+    for (int q = 0; q < (ACT == HOC_ACT_SWIGLU ? 1 : 2); ++q) {
+      const int gi = (col >> 3) + q + (ACT == HOC_ACT_SWIGLU && upper ? 1 : 0);
+      const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
+      const __nv_bfloat16* at = P.res[A.p] + int64_t(nv ? r0 : 0) * P.ld_res + fc;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) B.a[q * 8 + j] = bits_of(at + (j < nv ? j * P.ld_res : 0));
+    }
+  } else if constexpr (ACT != HOC_ACT_NONE) {
+    const int64_t ld = int64_t(P.in) * (ACT == HOC_ACT_SWIGLU ? 2 : 1);
+#pragma unroll
+    for (int q = 0; q < kTcColumns / 8; ++q) {
       const int gi = (col >> 3) + q;
       const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
-      if (col + q * 8 < A.n && keep && mine)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < nv)
-            keep[int64_t(r0 + j) * wide + (upper ? P.out : 0) + f] =
-                __float2bfloat16_rn(__uint_as_float(v[q * 8 + j]) + bias);
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[16 + j]) + bias, 16);
-      const float own = __uint_as_float(upper ? v[16 + j] : v[j]) + bias;
-      const int gl = (col >> 3) + (j >> 3), gi = gl + (upper ? 2 : 0);
-      const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
-      if (gi * 8 < A.n && (j & 7) < nv && mine) {
-        const float g = upper ? other : own, u = upper ? own : other;
-        const int64_t r = r0 + (j & 7);
-        float o = mm_act(HOC_ACT_SILU, g) * u;
-        if (res) o += bf16_of(res + r * P.ld_res + f);
-        y[r * P.ld_y + f] = __float2bfloat16_rn(o);
-      }
-    }
-  } else {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int gi = (col >> 3) + q;
-    const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
-    if (col + q * 8 >= A.n || !mine) continue;
-    float a[8], b[8];
-    if (MODE == kDgrad && ACT != HOC_ACT_NONE) {
-      const int64_t ldp = int64_t(P.in) * (ACT == HOC_ACT_SWIGLU ? 2 : 1);
+      const __nv_bfloat16* at = P.pre[A.p] + int64_t(nv ? r0 : 0) * ld + fc;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        a[j] = j < nv ? bf16_of(pre + int64_t(r0 + j) * ldp + f) : 0.f;
-        if (ACT == HOC_ACT_SWIGLU) b[j] = j < nv ? bf16_of(pre + int64_t(r0 + j) * ldp + P.in + f) : 0.f;
+        const int64_t off = j < nv ? j * ld : 0;
+        B.a[q * 8 + j] = bits_of(at + off);
+        if (ACT == HOC_ACT_SWIGLU) B.b[q * 8 + j] = bits_of(at + off + P.in);
       }
     }
-    if (MODE == kForward && res) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = j < nv ? bf16_of(res + int64_t(r0 + j) * P.ld_res + f) : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j >= nv) continue;
-      const int64_t r = r0 + j;
-      float x = __uint_as_float(v[q * 8 + j]);
-      __nv_bfloat16* o = y + r * P.ld_y + f;
-      if (MODE == kForward) {
-        x += bias;
-        if (keep) keep[r * wide + f] = __float2bfloat16_rn(x);
-        x = mm_act(ACT, x);
-        if (res) x += a[j];
-        *o = __float2bfloat16_rn(x);
-      } else if (ACT == HOC_ACT_SWIGLU) {
-        o[0] = __float2bfloat16_rn(x * b[j] * mm_act_slope(HOC_ACT_SILU, a[j]));
-        o[P.in] = __float2bfloat16_rn(x * mm_act(HOC_ACT_SILU, a[j]));
-      } else {
-        *o = __float2bfloat16_rn(ACT == HOC_ACT_NONE ? x : x * mm_act_slope(ACT, a[j]));
-      }
-    }
-  }
   }
 }
 
-// wgrad: columns are out features, lanes in features.
-__device__ __forceinline__ void store_weights(const MmParams& P, const Tile& A, const uint32_t (&v)[32], int col,
-                                              int f) {
-  if (f >= P.in) return;
-  const int64_t first = (int64_t(A.g) * P.out + A.c0 + col) * P.in + f;
-  const int m = min(32, P.out - (A.c0 + col));
-  if (P.out_f32) {
-    float* o = static_cast<float*>(P.y[A.p]) + first;
+// A step's columns of the accumulator: v[j] is feature `f` (of this lane) and column
+// col + j; row and valid name the groups of 8 columns of the tile, one per lane.
+template <int MODE, int ACT>
+__device__ __forceinline__ void store_columns(const MmParams& P, const Tile& A, const uint32_t (&v)[kTcColumns], int col, int f,
+                                              int row, int valid, float bias, const Beside& B) {
+  constexpr bool gated = MODE == kForward && ACT == HOC_ACT_SWIGLU;
+  if constexpr (MODE == kWgrad) {  // columns are out features
+    if (f >= P.in) return;
+    const int64_t first = (int64_t(A.g) * P.out + A.c0 + col) * P.in + f;
+    const int m = min(kTcColumns, P.out - (A.c0 + col));
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
+    for (int j = 0; j < kTcColumns; ++j)
       if (j < m) {
-        const float x = __uint_as_float(v[j]);
-        o[int64_t(j) * P.in] = P.accumulate ? o[int64_t(j) * P.in] + x : x;
+        float x = __uint_as_float(v[j]);
+        if (P.out_f32) {
+          if (P.accumulate) x += __uint_as_float(B.a[j]);
+          static_cast<float*>(P.y[A.p])[first + int64_t(j) * P.in] = x;
+        } else {
+          if (P.accumulate) x += float_of(B.a[j]);
+          static_cast<__nv_bfloat16*>(P.y[A.p])[first + int64_t(j) * P.in] = __float2bfloat16_rn(x);
+        }
       }
   } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(P.y[A.p]) + first;
+    const int width = MODE == kForward ? P.out : P.in;
+    const bool mine = f < width;
+    const int64_t wide = int64_t(P.out) * (gated ? 2 : 1);
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.y[A.p]);
+    __nv_bfloat16* keep = static_cast<__nv_bfloat16*>(P.pre_out[A.p]);
+    const bool res = MODE == kForward && P.res[A.p] != nullptr;
+    if constexpr (gated) {
+      // Lanes 0-15 hold the gates of 16 features, lanes 16-31 their values.  They
+      // swap halves: each then has both for 8 of the 16 columns.
+      const bool upper = (threadIdx.x & 31) >= 16;
+      if (keep)
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < m) {
-        const float x = __uint_as_float(v[j]);
-        o[int64_t(j) * P.in] = __float2bfloat16_rn(P.accumulate ? bf16_of(o + int64_t(j) * P.in) + x : x);
+        for (int q = 0; q < kTcColumns / 8; ++q) {
+          const int gi = (col >> 3) + q;
+          const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
+          __nv_bfloat16* at = keep + int64_t(r0) * wide + (upper ? P.out : 0) + f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < nv && mine) at[j * wide] = __float2bfloat16_rn(__uint_as_float(v[q * 8 + j]) + bias);
+        }
+      const int gi = (col >> 3) + (upper ? 1 : 0);
+      const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
+      __nv_bfloat16* at = y + int64_t(r0) * P.ld_y + f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[8 + j]) + bias, 16);
+        const float own = __uint_as_float(upper ? v[8 + j] : v[j]) + bias;
+        float o = mm_act(HOC_ACT_SILU, upper ? other : own) * (upper ? own : other);
+        if (res) o += float_of(B.a[j]);
+        if (j < nv && mine) at[j * P.ld_y] = __float2bfloat16_rn(o);
       }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kTcColumns / 8; ++q) {
+        const int gi = (col >> 3) + q;
+        const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
+        __nv_bfloat16* at = y + int64_t(r0) * P.ld_y + f;
+        __nv_bfloat16* ak = keep + int64_t(r0) * wide + f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j >= nv || !mine) continue;
+          float x = __uint_as_float(v[q * 8 + j]);
+          if (MODE == kForward) {
+            x += bias;
+            if (keep) ak[j * wide] = __float2bfloat16_rn(x);
+            x = mm_act(ACT, x);
+            if (res) x += float_of(B.a[q * 8 + j]);
+            at[j * P.ld_y] = __float2bfloat16_rn(x);
+          } else if (ACT == HOC_ACT_SWIGLU) {
+            const float g = float_of(B.a[q * 8 + j]);
+            at[j * P.ld_y] = __float2bfloat16_rn(x * float_of(B.b[q * 8 + j]) * mm_act_slope(HOC_ACT_SILU, g));
+            at[j * P.ld_y + P.in] = __float2bfloat16_rn(x * mm_act(HOC_ACT_SILU, g));
+          } else {
+            at[j * P.ld_y] =
+                __float2bfloat16_rn(ACT == HOC_ACT_NONE ? x : x * mm_act_slope(ACT, float_of(B.a[q * 8 + j])));
+          }
+        }
+      }
+    }
   }
 }
 
@@ -380,13 +426,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTcStages; ++s) {
-      ptx::mbar_init(&S->full[s], 1);
-      ptx::mbar_init(&S->ready[s], 2);
+      ptx::mbar_init(&S->full[s], 2);
+      ptx::mbar_init(&S->part[s], 1);
       ptx::mbar_init(&S->empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&S->acc_full[a], 1);
-      ptx::mbar_init(&S->acc_empty[a], 8);
+      ptx::mbar_init(&S->acc_empty[a], 2 * kTcEpilogue);
     }
     S->dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -415,74 +461,122 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const unsigned first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
   if (warp == 0) {
-    // ---- tensor copies
+    // ---- tensor copies.  The loop over a tile's stages runs on one lane
+    // wherever the rows of a stage are contiguous (a warp whose lanes issue copies
+    // in turn took 830 cycles a stage, more than the 512 of its MMAs).
+    const uint32_t full0 = on_first(&S->full[0]);
     uint32_t k = 0;  // stages filled
     bool ok = true;
     for (unsigned t = first; ok && t < tiles; t += stride) {
       const Tile A = tile_at<MODE>(T, S, t);
       const Ranges R = load_ranges(P, A.p, A.g, 0);
-      const int half = A.n / 2;  // rows of B in this CTA
-      int row = 0, valid = 0;
-      bool whole = false;
-      if (MODE != kWgrad) {
-        group_at(P, A.p, A.g, R, A.c0 + rank * half + lane * 8, row, valid);
-        const int start = __shfl_sync(0xFFFFFFFFu, row, lane & ~7);
-        const unsigned same = __ballot_sync(0xFFFFFFFFu, valid > 0 && row == start + (lane & 7) * 8);
-        whole = ((same >> (lane & ~7)) & 0xFFu) == 0xFFu && (lane | 7) * 8 < half;
-      }
-      const int blocks = (half + 63) / 64;  // wgrad: 64-feature blocks of dy
+      const int half = A.n / 2;  // rows of B in this CTA (wgrad: features)
+      const int blocks = (half + 63) / 64;
       const int fa = A.f0 + rank * (gated ? 64 : 128);
-      for (int s = 0; s < A.steps; ++s, ++k) {
-        const uint32_t st = k % kTcStages, round = k / kTcStages;
-        if (round && !warp_wait(&S->empty[st], (round - 1) & 1, T, S)) {
-          ok = false;
-          break;
-        }
-        const uint32_t a = base + st * kTcStage, b = a + kTcOperand;
-        uint32_t bar;
-        if (MODE == kWgrad) {
-          group_at(P, A.p, A.g, R, s * kTcDepth + (lane & 7) * 8, row, valid);
-          const int start = __shfl_sync(0xFFFFFFFFu, row, 0);
-          whole = __all_sync(0xFFFFFFFFu, valid > 0 && row == start + (lane & 7) * 8);
-          if (whole) row = start;  // lane i then fetches block i, of all 64 rows
-          bar = ptx::smem_addr(&S->full[st]);
-          if (lane == 0) ptx::mbar_arrive_expect_tx(&S->full[st], kTcOperand + uint32_t(blocks) * 8192u + T.tx_pad);
+      auto weights = [&](uint32_t a, int x, uint32_t bar) {
+        if (MODE == kDgrad) {
+          copy3(a, &T.w[A.p], fa, x, A.g, bar);
+          copy3(a + 8192u, &T.w[A.p], fa + 64, x, A.g, bar);
+        } else if (gated) {
+          copy5(a, &T.w[A.p], x, 0, 0, fa / 16, A.g, bar);
         } else {
-          bar = on_first(&S->full[st]);
-          if (rank == 0 && lane == 0)
-            ptx::mbar_arrive_expect_tx(&S->full[st], 2 * (kTcOperand + uint32_t(half) * 128u) + T.tx_pad);
+          copy3(a, &T.w[A.p], x, fa, A.g, bar);
         }
-        __syncwarp();
-        if (MODE == kWgrad) {
-          // operand blocks of 64 features: 0, 1 x; 2, 3 dy
-          const int which = whole ? lane : lane >> 3;
-          const int x = which < 2 ? A.f0 + rank * 128 + which * 64 : A.c0 + rank * half + (which - 2) * 64;
-          const uint32_t to = a + uint32_t(which) * 8192u;
-          if (which < 2 + blocks) {
-            if (whole)
-              copy2(to, which < 2 ? &T.row64[A.p] : &T.dy64[A.p], x, row, bar);
-            else
-              copy2(to + uint32_t(lane & 7) * 1024u, which < 2 ? &T.row8[A.p] : &T.dy8[A.p], x, row, bar);
-          }
-        } else {
-          const int x = s * kTcDepth;
-          if (whole) {
-            if ((lane & 7) == 0) copy2(b + uint32_t(lane) * 1024u, &T.row64[A.p], x, row, bar);
-          } else if (lane * 8 < half) {
-            copy2(b + uint32_t(lane) * 1024u, &T.row8[A.p], x, row, bar);
-          }
-          if (lane == 31) {
-            if (MODE == kDgrad) {
-              copy3(a, &T.w[A.p], fa, x, A.g, bar);
-              copy3(a + 8192u, &T.w[A.p], fa + 64, x, A.g, bar);
-            } else if (gated) {
-              copy5(a, &T.w[A.p], x, 0, 0, fa / 16, A.g, bar);
-            } else {
-              copy3(a, &T.w[A.p], x, fa, A.g, bar);
+      };
+      if (MODE != kWgrad) {
+        int row, left;
+        group_at(P, A.p, A.g, R, A.c0 + rank * half + lane * 8, row, left);
+        const int start = __shfl_sync(0xFFFFFFFFu, row, lane & ~7);
+        // 64-row blocks whose groups, as far as they hold rows, follow one another in the buffer
+        const unsigned broken = __ballot_sync(0xFFFFFFFFu, lane * 8 < half && left > 0 && row != start + (lane & 7) * 8);
+        const int row1 = __shfl_sync(0xFFFFFFFFu, row, 8);
+        if (!broken) {
+          if (lane == 0) {
+            const uint32_t bytes = kTcOperand + uint32_t(blocks) * 8192u + T.tx_pad;
+            for (int s = 0; s < A.steps; ++s, ++k) {
+              const uint32_t st = k % kTcStages, round = k / kTcStages;
+              if (round && !wait_bounded(&S->empty[st], (round - 1) & 1, T, S)) {
+                ok = false;
+                break;
+              }
+              const uint32_t a = base + st * kTcStage, bar = full0 + st * 8u;
+              arrive_expect_cluster(bar, bytes);
+              weights(a, s * kTcDepth, bar);
+              copy2(a + kTcOperand, &T.row64[A.p], s * kTcDepth, row, bar);
+              if (blocks > 1) copy2(a + kTcOperand + 8192u, &T.row64[A.p], s * kTcDepth, row1, bar);
             }
           }
+        } else {
+          for (int s = 0; s < A.steps; ++s, ++k) {
+            const uint32_t st = k % kTcStages, round = k / kTcStages;
+            if (round && !warp_wait(&S->empty[st], (round - 1) & 1, T, S)) {
+              ok = false;
+              break;
+            }
+            const uint32_t a = base + st * kTcStage, bar = full0 + st * 8u;
+            if (lane == 0) {
+              arrive_expect_cluster(bar, kTcOperand + uint32_t(half) * 128u + T.tx_pad);
+              weights(a, s * kTcDepth, bar);
+            }
+            __syncwarp();
+            if (lane * 8 < half)
+              copy2(a + kTcOperand + uint32_t(lane) * 1024u, &T.row8[A.p], s * kTcDepth, row, bar);
+            __syncwarp();
+          }
         }
-        __syncwarp();
+        k = __shfl_sync(0xFFFFFFFFu, k, 0);
+        ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
+      } else {
+        const uint32_t bytes = kTcOperand + uint32_t(blocks) * 8192u + T.tx_pad;
+        for (int s = 0; ok && s < A.steps;) {
+          int row, valid;
+          const int run = stage_rows(P, A, R, s, row, valid);
+          if (run > 0) {
+            if (lane == 0)
+              for (int i = 0; i < run; ++i, ++k) {
+                const uint32_t st = k % kTcStages, round = k / kTcStages;
+                if (round && !wait_bounded(&S->empty[st], (round - 1) & 1, T, S)) {
+                  ok = false;
+                  break;
+                }
+                const uint32_t a = base + st * kTcStage, bar = full0 + st * 8u;
+                const int r = row + i * kTcDepth;
+                arrive_expect_cluster(bar, bytes);
+                copy2(a, &T.row64[A.p], A.f0 + rank * 128, r, bar);
+                copy2(a + 8192u, &T.row64[A.p], A.f0 + rank * 128 + 64, r, bar);
+                copy2(a + kTcOperand, &T.dy64[A.p], A.c0 + rank * half, r, bar);
+                if (blocks > 1) copy2(a + kTcOperand + 8192u, &T.dy64[A.p], A.c0 + rank * half + 64, r, bar);
+              }
+            k = __shfl_sync(0xFFFFFFFFu, k, 0);
+            ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
+            s += run;
+            continue;
+          }
+          const uint32_t st = k % kTcStages, round = k / kTcStages;
+          if (round && !warp_wait(&S->empty[st], (round - 1) & 1, T, S)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a = base + st * kTcStage, bar = ptx::smem_addr(&S->part[st]);
+          // rows that follow one another (padding at the end): one copy per 64 features
+          const int start = __shfl_sync(0xFFFFFFFFu, row, 0);
+          const bool in_line = __all_sync(0xFFFFFFFFu, valid == 0 || row == start + (lane & 7) * 8);
+          if (lane == 0) arrive_expect_cluster(bar, bytes);
+          __syncwarp();
+          // lanes: block of 64 features (0, 1 of x, then those of dy) x group of 8 rows
+          const int which = lane >> 3;
+          const int x = which < 2 ? A.f0 + rank * 128 + which * 64 : A.c0 + rank * half + (which - 2) * 64;
+          if (which < 2 + blocks) {
+            const uint32_t to = a + uint32_t(which) * 8192u;
+            if (!in_line)
+              copy2(to + uint32_t(lane & 7) * 1024u, which < 2 ? &T.row8[A.p] : &T.dy8[A.p], x, row, bar);
+            else if ((lane & 7) == 0)
+              copy2(to, which < 2 ? &T.row64[A.p] : &T.dy64[A.p], x, row, bar);
+          }
+          __syncwarp();
+          ++s;
+          ++k;
+        }
       }
     }
     // The MMAs' last releases of the stages have to land before this CTA may leave.
@@ -504,7 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int s = 0; s < A.steps; ++s, ++k) {
           const uint32_t st = k % kTcStages;
-          if (!wait_bounded(MODE == kWgrad ? &S->ready[st] : &S->full[st], (k / kTcStages) & 1, T, S)) {
+          if (!wait_bounded(&S->full[st], (k / kTcStages) & 1, T, S)) {
             ok = false;
             break;
           }
@@ -523,37 +617,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
     __syncwarp();
   } else if (MODE == kWgrad && warp == 2) {
-    // ---- zero the padding rows of each stage, then hand it to the MMA
-    uint32_t k = 0;
+    // ---- zero the padding rows of the stages that hold any, then hand them to the MMA
+    const uint32_t full0 = on_first(&S->full[0]);
+    uint32_t k = 0, phases = 0;  // bit st: parity of part[st]
     bool ok = true;
     for (unsigned t = first; ok && t < tiles; t += stride) {
       const Tile A = tile_at<MODE>(T, S, t);
       const Ranges R = load_ranges(P, A.p, A.g, 0);
-      for (int s = 0; s < A.steps; ++s, ++k) {
-        const uint32_t st = k % kTcStages;
+      for (int s = 0; s < A.steps;) {
         int row, valid;
-        group_at(P, A.p, A.g, R, s * kTcDepth + (lane & 7) * 8, row, valid);
-        unsigned part = __ballot_sync(0xFFFFFFFFu, valid > 0 && valid < 8) & 0xFFu;
-        if (!warp_wait(&S->full[st], (k / kTcStages) & 1, T, S)) {
+        const int run = stage_rows(P, A, R, s, row, valid);
+        s += run > 0 ? run : 1;
+        k += run;
+        if (run > 0) continue;
+        const uint32_t st = k % kTcStages;
+        ++k;
+        if (!warp_wait(&S->part[st], (phases >> st) & 1, T, S)) {
           ok = false;
           break;
         }
-        while (part) {
-          const int gi = __ffs(part) - 1;
-          part &= part - 1;
-          // lanes: 4 blocks of 64 features (2 of x, 2 of dy) x 8 vectors of a 128-byte row
-          unsigned char* at = stages + size_t(st) * kTcStage + (lane >> 3) * 8192 + gi * 1024 + (lane & 7) * 16;
+        phases ^= 1u << st;
+        // lanes: 4 blocks of 64 features (2 of x, 2 of dy) x 8 vectors of a 128-byte row
+        unsigned char* at = stages + size_t(st) * kTcStage + (lane >> 3) * 8192 + (lane & 7) * 16;
+        for (int gi = 0; gi < 8; ++gi)
           for (int r = __shfl_sync(0xFFFFFFFFu, valid, gi); r < 8; ++r)
-            *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0, 0, 0, 0);
-        }
+            *reinterpret_cast<uint4*>(at + (gi * 8 + r) * 128) = make_uint4(0, 0, 0, 0);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_cluster(on_first(&S->ready[st]));
+        if (lane == 0) arrive_cluster(full0 + st * 8u);
       }
     }
   } else if (warp >= 4) {
-    // ---- epilogue: warp q of 4 has the 32 tensor-memory lanes 32 q ..
-    const int q = warp & 3;
+    // ---- epilogue: warps q and q + 4 have the tensor-memory lanes 32 q .. and take turns along the columns
+    const int q = warp & 3, col0 = (warp - 4) / 4 * kTcColumns;
     uint32_t it = 0;
     for (unsigned t = first; t < tiles; t += stride) {
       const Tile A = tile_at<MODE>(T, S, t);
@@ -562,35 +658,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       float bias = 0.f;
       if (MODE != kWgrad) {
         group_at(P, A.p, A.g, load_ranges(P, A.p, A.g, 0), A.c0 + lane * 8, row, valid);
-        if (lane * 8 >= T.tile_rows) valid = 0;  // the next tile's rows
+        valid = lane * 8 < T.tile_rows ? min(valid, 8) : 0;  // past them: the next tile's rows
         if (MODE == kForward && P.bias[A.p] && f < P.out)
           bias = bf16_of(P.bias[A.p] + int64_t(A.g) * (gated ? 2 : 1) * P.out + (gated && lane >= 16 ? P.out : 0) + f);
       }
       if (A.steps == 0) {  // wgrad of an expert without rows
-        uint32_t v[32];
+        uint32_t v[kTcColumns];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0;
+        for (int j = 0; j < kTcColumns; ++j) v[j] = 0;
+        Beside none;
         if (!P.accumulate)
-          for (int col = 0; col < A.n; col += 32) store_weights(P, A, v, col, f);
+          for (int col = col0; col < A.n; col += 2 * kTcColumns)
+            store_columns<MODE, HOC_ACT_NONE>(P, A, v, col, f, row, valid, bias, none);
         continue;
       }
       const uint32_t acc = it & 1;
-      if (!warp_wait(&S->acc_full[acc], (it >> 1) & 1, T, S)) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t at = tmem + acc * 256u + (uint32_t(q * 32) << 16);
+      bool ok = true;
       auto columns = [&](auto tag) {
-        for (int col = 0; col < A.n; col += 32) {
-          uint32_t v[32];
-          tmem_load32(v, at + uint32_t(col));
-          if constexpr (MODE == kWgrad) store_weights(P, A, v, col, f);
-          else store_columns<MODE, decltype(tag)::act>(P, A, v, col, f, row, valid, bias);
+        constexpr int act = decltype(tag)::act;
+        Beside B, next;
+        load_beside<MODE, act>(P, A, col0, f, row, valid, B);
+        ok = warp_wait(&S->acc_full[acc], (it >> 1) & 1, T, S);
+        if (!ok) return;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int col = col0; col < A.n; col += 2 * kTcColumns) {
+          load_beside<MODE, act>(P, A, col + 2 * kTcColumns, f, row, valid, next);
+          uint32_t v[kTcColumns];
+          tmem_load(v, at + uint32_t(col));
+          store_columns<MODE, act>(P, A, v, col, f, row, valid, bias, B);
+          B = next;
         }
       };
       if (MODE == kWgrad) columns(ActTag<HOC_ACT_NONE>{});
       else with_act(P.act, columns);
+      if (!ok) break;
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive_cluster(on_first(&S->acc_empty[acc]));
+      if (lane == 0) arrive_relaxed(on_first(&S->acc_empty[acc]));
       ++it;
     }
   }
