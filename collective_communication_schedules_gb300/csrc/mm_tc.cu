@@ -23,8 +23,9 @@
 // that are not stored; in the weight gradient, where rows are summed over, they
 // are overwritten with zeros in shared memory before the MMA reads them.
 //
-// Warps of a CTA: 0 tensor copies, 1 MMA (of the pair's first CTA), 2 tensor
-// memory and the zeroing, 4-11 epilogue.  Every wait is bounded: a wait that runs
+// Warps of a CTA: 0 and 2 tensor copies of the rows, 64 each; 3 those of the
+// weights; 1 MMA (of the pair's first CTA); 4-11 epilogue.  In the weight gradient
+// warp 0 issues all copies and warp 2 zeroes padding rows.  Every wait is bounded: a wait that runs
 // out sets bit 2 of the status, and all roles leave.
 #include <atomic>
 #include <cstdlib>
@@ -41,7 +42,6 @@ namespace {
 constexpr int kTcThreads = 384;
 constexpr int kTcEpilogue = 8;                  // warps: two to each 32 lanes of tensor memory
 constexpr int kTcColumns = 16;                  // accumulator columns of an epilogue step
-constexpr int kTcStages = 6;
 constexpr int kTcDepth = 64;                    // contraction elements of a stage: one 128-byte swizzled row
 constexpr uint32_t kTcOperand = 128 * 128;      // bytes of one operand of a stage in one CTA
 constexpr uint32_t kTcStage = 2 * kTcOperand;
@@ -60,10 +60,16 @@ struct TcParams {
   CUtensorMap dy64[kMaxRanks], dy8[kMaxRanks];   // wgrad
 };
 
+// Stages: what the epilogue's planes leave of 227 KB (a sixth stage is worth 1 to 2
+// % of the rate on long contractions).
+template <int MODE>
+constexpr int kStages = MODE == kWgrad ? 6 : 5;
+constexpr int kTcMostStages = 6;
+
 struct TcShared {
-  uint64_t full[kTcStages];   // on the first CTA: both CTAs' loads of a stage
-  uint64_t part[kTcStages];   // wgrad: this CTA's loads of a stage that holds padding rows
-  uint64_t empty[kTcStages];
+  uint64_t full[kTcMostStages];   // on the first CTA: both CTAs' loads of a stage
+  uint64_t part[kTcMostStages];   // wgrad: this CTA's loads of a stage that holds padding rows
+  uint64_t empty[kTcMostStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];      // on the first CTA: the epilogue warps of both CTAs
   uint32_t tmem;
@@ -71,7 +77,6 @@ struct TcShared {
   int vrows[kMmMaxGroups];
   unsigned tile0[kMmMaxGroups + 1];
 };
-constexpr size_t kTcSmem = 1024 + size_t(kTcStages) * kTcStage + sizeof(TcShared);
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -200,15 +205,27 @@ __device__ __forceinline__ Tile tile_at(const TcParams& T, const TcShared* S, un
   return A;
 }
 
-// The ranges of one expert, one source per lane (reloaded 32 at a time where there are more).
+// The ranges of one expert, one source per lane: first row, rows, and the
+// virtual row it starts at (of the 32 sources at hand; `all`: past the last).
 struct Ranges {
-  int64_t lo;
-  int64_t n;
+  int lo, n, start, all;
 };
 __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, int g, int base) {
-  const int s = base + int(threadIdx.x & 31);
-  Ranges R{0, 0};
-  if (s < (P.seg ? P.sources : 1)) mm_range(P, p, g, s, R.lo, R.n);
+  const int lane = threadIdx.x & 31, s = base + lane;
+  int64_t lo = 0, n = 0;
+  if (s < (P.seg ? P.sources : 1)) mm_range(P, p, g, s, lo, n);
+  Ranges R;
+  R.lo = int(lo);
+  R.n = int(n);
+  const int padded = (R.n + 7) & ~7;
+  int incl = padded;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  R.start = incl - padded;
+  R.all = __shfl_sync(0xFFFFFFFFu, incl, 31);
   return R;
 }
 // Each lane's group of 8 virtual rows at `v` (a multiple of 8): its first row in
@@ -216,23 +233,23 @@ __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, int g, i
 // The whole warp calls it; R holds the first 32 sources' ranges.
 __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges R, int v, int& row, int& left) {
   const int ns = P.seg ? P.sources : 1;
-  int64_t at = v;
-  bool found = false;
   row = int(P.cap[p]);
   left = 0;
   for (int base = 0; base < ns; base += 32) {
     if (ns > 32) R = load_ranges(P, p, g, base);
-    const int m = min(32, ns - base);
-    for (int j = 0; j < m; ++j) {
-      const int64_t lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
-      const int64_t padded = (n + 7) & ~int64_t(7);
-      if (!found && at < padded) {
-        found = true;
-        row = int(lo + at);
-        left = int(n - at);
-      }
-      at -= padded;
+    int j = 0;  // the last source that starts at or before v
+#pragma unroll
+    for (int step = 16; step; step >>= 1) {
+      const int at = __shfl_sync(0xFFFFFFFFu, R.start, j + step);
+      if (at <= v) j += step;
     }
+    const int lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
+    const int off = v - __shfl_sync(0xFFFFFFFFu, R.start, j);
+    if (v >= 0 && off < n) {
+      row = lo + off;
+      left = n - off;
+    }
+    v -= R.all;  // negative once it was found
   }
 }
 
@@ -264,161 +281,271 @@ __device__ __forceinline__ void with_act(int act, F f) {
   }
 }
 
-// What the epilogue reads beside the accumulator for a step's columns: the residual,
-// the pre-activation of the layer below, or the weights to add to.  Loaded one
-// step ahead, so that its latency passes under other work.
-struct Beside {
-  uint32_t a[kTcColumns], b[kTcColumns];  // bf16 bits, or (wgrad, binary32 weights) floats
+// Rows move between global and shared memory as 16-byte vectors: the lanes of a
+// warp hold 32 features, 64 bytes of a row, and stores of single values from
+// there (2048 of them for a tile) were what bounded the kernel at the expert
+// layer's widths.  Four warps together stage kTcColumns rows of 128 features, so
+// that a row goes out as 256 contiguous bytes.  What the epilogue reads beside
+// the accumulator (the residual, the pre-activation of the layer below) comes
+// the same way, a step ahead.
+
+// Where the features of a staged row are in global memory: `chunks` vectors of 8
+// features, of which the last may lie past the row's end.
+struct Strip {
+  char* at;        // feature f0 of row 0
+  int64_t pitch;   // bytes of a row
+  int left;        // features from f0 to the end of a row
 };
 
-__device__ __forceinline__ uint32_t bits_of(const __nv_bfloat16* p) {
-  return *reinterpret_cast<const uint16_t*>(p);
-}
-__device__ __forceinline__ float float_of(uint32_t bf16_bits) { return __uint_as_float(bf16_bits << 16); }
+constexpr uint32_t kTcRowBytes = 256;
+constexpr uint32_t kTcPlane = kTcColumns * kTcRowBytes;  // one staged array
 
-// Loads are unconditional, at places clamped to the tensors (values of rows or
-// features that do not exist are never used): predicated ones made the compiler
-// wait for each before it issued the next.
-template <int MODE, int ACT>
-__device__ __forceinline__ void load_beside(const MmParams& P, const Tile& A, int col, int f, int row, int valid,
-                                            Beside& B) {
-  if (col >= A.n) return;
-  const bool upper = (threadIdx.x & 31) >= 16;
-  const int fc = min(f, (MODE == kForward ? P.out : P.in) - 1);
-  if constexpr (MODE == kWgrad) {
-    if (!P.accumulate) return;
-    const int64_t first = int64_t(A.g) * P.out * P.in + fc;
-    if (P.out_f32) {
+__device__ __forceinline__ void group_barrier(int eg) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + eg), "n"(128) : "memory");
+}
+// Whether `ok` holds in all four warps.
+__device__ __forceinline__ bool group_all(int eg, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(int(ok)), "r"(1 + eg), "n"(128)
+      : "memory");
+  return r != 0;
+}
+// The row that column `c` of the step at `col` stands for, -1 if none.  Whole warps call it.
+__device__ __forceinline__ int64_t row_of(int col, int c, int row, int valid) {
+  const int gi = ((col + c) >> 3) & 31;
+  const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi), nv = __shfl_sync(0xFFFFFFFFu, valid, gi);
+  return (c & 7) < nv ? int64_t(r0) + (c & 7) : -1;
+}
+
+// kTcColumns rows of CHUNKS vectors between shared memory (row pitch 16 * CHUNKS
+// bytes) and a strip, by 128 threads.  `at` names the row of a column or -1.
+template <int CHUNKS, class At>
+__device__ __forceinline__ void fetch_rows(uint32_t smem, const Strip& G, At at) {
+  const int i = int(threadIdx.x) & 127;
 #pragma unroll
-      for (int j = 0; j < kTcColumns; ++j)
-        B.a[j] = __float_as_uint(
-            static_cast<const float*>(P.y[A.p])[first + int64_t(min(A.c0 + col + j, P.out - 1)) * P.in]);
-    } else {
+  for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h) {
+    const int c = (i + 128 * h) / CHUNKS, v = (i + 128 * h) % CHUNKS;
+    const int64_t r = at(c);
+    if (r >= 0 && v * 8 < G.left)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem + uint32_t(c * CHUNKS + v) * 16u),
+                   "l"(G.at + r * G.pitch + v * 16)
+                   : "memory");
+  }
+}
+template <int CHUNKS, class At>
+__device__ __forceinline__ void put_rows(const unsigned char* smem, const Strip& G, At at, int turn = 0) {
+  const int i = int(threadIdx.x) & 127;
 #pragma unroll
-      for (int j = 0; j < kTcColumns; ++j)
-        B.a[j] = bits_of(static_cast<const __nv_bfloat16*>(P.y[A.p]) + first +
-                         int64_t(min(A.c0 + col + j, P.out - 1)) * P.in);
-    }
-  } else if constexpr (MODE == kForward) {
-    if (!P.res[A.p]) return;
-#pragma unroll
-    for (int q = 0; q < (ACT == HOC_ACT_SWIGLU ? 1 : 2); ++q) {
-      const int gi = (col >> 3) + q + (ACT == HOC_ACT_SWIGLU && upper ? 1 : 0);
-      const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
-      const __nv_bfloat16* at = P.res[A.p] + int64_t(nv ? r0 : 0) * P.ld_res + fc;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) B.a[q * 8 + j] = bits_of(at + (j < nv ? j * P.ld_res : 0));
-    }
-  } else if constexpr (ACT != HOC_ACT_NONE) {
-    const int64_t ld = int64_t(P.in) * (ACT == HOC_ACT_SWIGLU ? 2 : 1);
-#pragma unroll
-    for (int q = 0; q < kTcColumns / 8; ++q) {
-      const int gi = (col >> 3) + q;
-      const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
-      const __nv_bfloat16* at = P.pre[A.p] + int64_t(nv ? r0 : 0) * ld + fc;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t off = j < nv ? j * ld : 0;
-        B.a[q * 8 + j] = bits_of(at + off);
-        if (ACT == HOC_ACT_SWIGLU) B.b[q * 8 + j] = bits_of(at + off + P.in);
-      }
-    }
+  for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h) {
+    const int c = (i + 128 * h) / CHUNKS, v = (i + 128 * h) % CHUNKS;
+    const int64_t r = at(c);
+    if (r >= 0 && v * 8 < G.left)
+      *reinterpret_cast<uint4*>(G.at + r * G.pitch + v * 16) =
+          *reinterpret_cast<const uint4*>(smem + (c * CHUNKS + (v ^ turn)) * 16);
   }
 }
 
-// A step's columns of the accumulator: v[j] is feature `f` (of this lane) and column
-// col + j; row and valid name the groups of 8 columns of the tile, one per lane.
+__device__ __forceinline__ float bf16_at(const unsigned char* p) {
+  return __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(p)) << 16);
+}
+__device__ __forceinline__ void put_bf16(unsigned char* p, float v) {
+  *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(v);
+}
+
+// The epilogue of one tile by group `eg` of four warps (warp q of it has tensor
+// memory lanes 32 q ..): the steps of kTcColumns columns whose number is eg modulo
+// 2.  in: the group's two input planes (two arrays each); out: its two output
+// planes, which the arrays that are stored take in turn, with one barrier each.
+// False when the accumulator did not come.
 template <int MODE, int ACT>
-__device__ __forceinline__ void store_columns(const MmParams& P, const Tile& A, const uint32_t (&v)[kTcColumns], int col, int f,
-                                              int row, int valid, float bias, const Beside& B) {
+__device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, const Tile& A, unsigned char* in,
+                                             unsigned char* out, uint32_t& turn, uint32_t acc_at, uint64_t* acc_full,
+                                             uint32_t parity, int eg, int q, int rank, int row, int valid, float bias) {
   constexpr bool gated = MODE == kForward && ACT == HOC_ACT_SWIGLU;
-  if constexpr (MODE == kWgrad) {  // columns are out features
-    if (f >= P.in) return;
-    const int64_t first = (int64_t(A.g) * P.out + A.c0 + col) * P.in + f;
-    const int m = min(kTcColumns, P.out - (A.c0 + col));
+  constexpr bool twice = MODE == kDgrad && ACT == HOC_ACT_SWIGLU;  // two inputs, two outputs
+  const MmParams& P = T.P;
+  const int lane = threadIdx.x & 31;
+  const int f0 = A.f0 + rank * (gated ? 64 : 128);
+  const int width = MODE == kForward ? P.out : P.in;
+  const int64_t wide = int64_t(width) * (ACT == HOC_ACT_SWIGLU ? 2 : 1);  // of pre
+  const uint32_t in_addr = ptx::smem_addr(in);
+  const bool res = MODE == kForward && P.res[A.p] != nullptr;
+  const bool keep = MODE == kForward && P.pre_out[A.p] != nullptr;
+  const bool reads = res || (MODE == kDgrad && ACT != HOC_ACT_NONE);
+  // clamped so that no pointer is formed past the tensors
+  const int left = width - f0, fs = left > 0 ? f0 : 0;
+  const Strip y{static_cast<char*>(P.y[A.p]) + 2 * int64_t(fs), 2 * P.ld_y, left};
+  Strip beside{};
+  if (res) beside = {reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.res[A.p])) + 2 * int64_t(fs), 2 * P.ld_res, left};
+  if (MODE == kDgrad && ACT != HOC_ACT_NONE)
+    beside = {reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.pre[A.p])) + 2 * int64_t(fs), 2 * wide, left};
+  const Strip kept{static_cast<char*>(P.pre_out[A.p]) + 2 * int64_t(fs), 2 * wide, left};
+  auto second = [&](Strip s) {
+    s.at += 2 * int64_t(width);
+    return s;
+  };
+  auto fetch = [&](int col) {
+    if (reads && col < A.n) {
+      const uint32_t to = in_addr + (uint32_t(col / kTcColumns) / 2 & 1) * 2 * kTcPlane;
+      auto at = [&](int c) { return row_of(col, c, row, valid); };
+      fetch_rows<gated ? 8 : 16>(to, beside, at);
+      if (twice) fetch_rows<16>(to + kTcPlane, second(beside), at);
+    }
+    if (reads) asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int first = eg * kTcColumns;
+  fetch(first);
+  bool ok = true;
+  if (A.steps > 0) {
+    ok = warp_wait(acc_full, parity, T, S);
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  }
+  if (!group_all(eg, ok)) {
+    if (reads) asm volatile("cp.async.wait_all;" ::: "memory");
+    return false;
+  }
+  for (int col = first; col < A.n; col += 2 * kTcColumns) {
+    fetch(col + 2 * kTcColumns);
+    uint32_t v[kTcColumns];
+    if (MODE != kWgrad || A.steps > 0) {
+      tmem_load(v, acc_at + uint32_t(col));
+    } else {
 #pragma unroll
-    for (int j = 0; j < kTcColumns; ++j)
-      if (j < m) {
-        float x = __uint_as_float(v[j]);
-        if (P.out_f32) {
-          if (P.accumulate) x += __uint_as_float(B.a[j]);
-          static_cast<float*>(P.y[A.p])[first + int64_t(j) * P.in] = x;
-        } else {
-          if (P.accumulate) x += float_of(B.a[j]);
-          static_cast<__nv_bfloat16*>(P.y[A.p])[first + int64_t(j) * P.in] = __float2bfloat16_rn(x);
+      for (int j = 0; j < kTcColumns; ++j) v[j] = 0;
+    }
+    auto at = [&](int c) { return row_of(col, c, row, valid); };
+    const unsigned char* x = in + (uint32_t(col / kTcColumns) / 2 & 1) * 2 * kTcPlane;
+    if (reads) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      group_barrier(eg);
+    }
+    if constexpr (MODE == kWgrad) {  // columns are out features
+      const int c0 = A.c0 + col, f = f0 + q * 32 + lane;
+      const int64_t first_at = (int64_t(A.g) * P.out + c0) * P.in;
+      if (P.out_f32) {
+        float* o = static_cast<float*>(P.y[A.p]) + first_at + f;
+        float add[kTcColumns];
+#pragma unroll
+        for (int j = 0; j < kTcColumns; ++j)
+          add[j] = P.accumulate && f < P.in && c0 + j < P.out ? o[int64_t(j) * P.in] : 0.f;
+#pragma unroll
+        for (int j = 0; j < kTcColumns; ++j)
+          if (f < P.in && c0 + j < P.out) o[int64_t(j) * P.in] = add[j] + __uint_as_float(v[j]);
+      } else {
+        unsigned char* o = out + (turn++ & 1) * kTcPlane;
+        if (P.accumulate) {
+          const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(P.y[A.p]) + first_at + f;
+          float add[kTcColumns];
+#pragma unroll
+          for (int j = 0; j < kTcColumns; ++j)
+            add[j] = f < P.in && c0 + j < P.out ? bf16_of(w + int64_t(j) * P.in) : 0.f;
+#pragma unroll
+          for (int j = 0; j < kTcColumns; ++j) v[j] = __float_as_uint(add[j] + __uint_as_float(v[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < kTcColumns; ++j) put_bf16(o + j * kTcRowBytes + (q * 32 + lane) * 2, __uint_as_float(v[j]));
+        group_barrier(eg);
+        const Strip w{static_cast<char*>(P.y[A.p]) + 2 * (int64_t(A.g) * P.out * P.in + fs), 2 * int64_t(P.in), left};
+        put_rows<16>(o, w, [&](int c) { return c0 + c < P.out ? int64_t(c0 + c) : int64_t(-1); });
+      }
+    } else if constexpr (gated) {
+      // Lanes 0-15 hold the gates of 16 features, lanes 16-31 their values.
+      const bool upper = lane >= 16;
+      const int mine = (q * 16 + (lane & 15)) * 2;  // byte of this lane's feature in a row of 64
+      if (keep) {
+        // gates in the first half of a staged row, values in the second with 32-byte
+        // units exchanged, so that both halves of the warp write to different banks
+        unsigned char* o = out + (turn++ & 1) * kTcPlane;
+#pragma unroll
+        for (int j = 0; j < kTcColumns; ++j)
+          put_bf16(o + j * kTcRowBytes + (upper ? 128 + (mine ^ 32) : mine), __uint_as_float(v[j]) + bias);
+        group_barrier(eg);
+        const int i = int(threadIdx.x) & 127;
+#pragma unroll
+        for (int h = 0; h < kTcColumns * 16 / 128; ++h) {
+          const int c = (i + 128 * h) / 16, u = (i + 128 * h) % 8;
+          const bool value = (i + 128 * h) % 16 >= 8;
+          const int64_t r = at(c);
+          if (r >= 0 && u * 8 < left)
+            *reinterpret_cast<uint4*>(kept.at + r * kept.pitch + (value ? 2 * int64_t(width) : 0) + u * 16) =
+                *reinterpret_cast<const uint4*>(o + c * kTcRowBytes + (value ? 128 + ((u * 16) ^ 32) : u * 16));
         }
       }
-  } else {
-    const int width = MODE == kForward ? P.out : P.in;
-    const bool mine = f < width;
-    const int64_t wide = int64_t(P.out) * (gated ? 2 : 1);
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.y[A.p]);
-    __nv_bfloat16* keep = static_cast<__nv_bfloat16*>(P.pre_out[A.p]);
-    const bool res = MODE == kForward && P.res[A.p] != nullptr;
-    if constexpr (gated) {
-      // Lanes 0-15 hold the gates of 16 features, lanes 16-31 their values.  They
-      // swap halves: each then has both for 8 of the 16 columns.
-      const bool upper = (threadIdx.x & 31) >= 16;
-      if (keep)
-#pragma unroll
-        for (int q = 0; q < kTcColumns / 8; ++q) {
-          const int gi = (col >> 3) + q;
-          const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
-          __nv_bfloat16* at = keep + int64_t(r0) * wide + (upper ? P.out : 0) + f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < nv && mine) at[j * wide] = __float2bfloat16_rn(__uint_as_float(v[q * 8 + j]) + bias);
-        }
-      const int gi = (col >> 3) + (upper ? 1 : 0);
-      const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
-      __nv_bfloat16* at = y + int64_t(r0) * P.ld_y + f;
+      // The halves of a warp swap: each lane then has gate and value of 8 of the 16 columns.
+      unsigned char* o = out + (turn++ & 1) * kTcPlane;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[8 + j]) + bias, 16);
         const float own = __uint_as_float(upper ? v[8 + j] : v[j]) + bias;
-        float o = mm_act(HOC_ACT_SILU, upper ? other : own) * (upper ? own : other);
-        if (res) o += float_of(B.a[j]);
-        if (j < nv && mine) at[j * P.ld_y] = __float2bfloat16_rn(o);
+        const int at_byte = (upper ? 8 + j : j) * 128 + mine;
+        float z = mm_act(HOC_ACT_SILU, upper ? other : own) * (upper ? own : other);
+        if (res) z += bf16_at(x + at_byte);
+        put_bf16(o + at_byte, z);
       }
+      group_barrier(eg);
+      put_rows<8>(o, y, at);
     } else {
+      const int mine = (q * 32 + lane) * 2;
+      if (keep) {
+        unsigned char* o = out + (turn++ & 1) * kTcPlane;
 #pragma unroll
-      for (int q = 0; q < kTcColumns / 8; ++q) {
-        const int gi = (col >> 3) + q;
-        const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi & 31), nv = __shfl_sync(0xFFFFFFFFu, valid, gi & 31);
-        __nv_bfloat16* at = y + int64_t(r0) * P.ld_y + f;
-        __nv_bfloat16* ak = keep + int64_t(r0) * wide + f;
+        for (int j = 0; j < kTcColumns; ++j) put_bf16(o + j * kTcRowBytes + mine, __uint_as_float(v[j]) + bias);
+        group_barrier(eg);
+        put_rows<16>(o, kept, at);
+      }
+      unsigned char* o = out + (turn++ & 1) * kTcPlane;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j >= nv || !mine) continue;
-          float x = __uint_as_float(v[q * 8 + j]);
-          if (MODE == kForward) {
-            x += bias;
-            if (keep) ak[j * wide] = __float2bfloat16_rn(x);
-            x = mm_act(ACT, x);
-            if (res) x += float_of(B.a[q * 8 + j]);
-            at[j * P.ld_y] = __float2bfloat16_rn(x);
-          } else if (ACT == HOC_ACT_SWIGLU) {
-            const float g = float_of(B.a[q * 8 + j]);
-            at[j * P.ld_y] = __float2bfloat16_rn(x * float_of(B.b[q * 8 + j]) * mm_act_slope(HOC_ACT_SILU, g));
-            at[j * P.ld_y + P.in] = __float2bfloat16_rn(x * mm_act(HOC_ACT_SILU, g));
-          } else {
-            at[j * P.ld_y] =
-                __float2bfloat16_rn(ACT == HOC_ACT_NONE ? x : x * mm_act_slope(ACT, float_of(B.a[q * 8 + j])));
-          }
+      for (int j = 0; j < kTcColumns; ++j) {
+        const unsigned char* z = x + j * kTcRowBytes + mine;
+        float d = __uint_as_float(v[j]);
+        if (MODE == kForward) {
+          d = mm_act(ACT, d + bias);
+          if (res) d += bf16_at(z);
+        } else if (twice) {
+          const float g = bf16_at(z);
+          v[j] = __float_as_uint(d * mm_act(HOC_ACT_SILU, g));
+          d *= bf16_at(z + kTcPlane) * mm_act_slope(HOC_ACT_SILU, g);
+        } else if (ACT != HOC_ACT_NONE) {
+          d *= mm_act_slope(ACT, bf16_at(z));
         }
+        put_bf16(o + j * kTcRowBytes + mine, d);
+      }
+      group_barrier(eg);
+      put_rows<16>(o, y, at);
+      if (twice) {
+        unsigned char* o2 = out + (turn++ & 1) * kTcPlane;
+#pragma unroll
+        for (int j = 0; j < kTcColumns; ++j) put_bf16(o2 + j * kTcRowBytes + mine, __uint_as_float(v[j]));
+        group_barrier(eg);
+        put_rows<16>(o2, second(y), at);
       }
     }
   }
+  if (reads) asm volatile("cp.async.wait_all;" ::: "memory");
+  return true;
 }
 
 // ------------------------------------------------------------------ kernel
+// Stages, then for each of the two epilogue groups four input planes (not in
+// wgrad) and two output planes, then the barriers and tile counts.
+template <int MODE>
+constexpr size_t kTcPlanes = 2 * (MODE == kWgrad ? 2 : 6);
+template <int MODE>
+constexpr size_t kTcSmem = 1024 + size_t(kStages<MODE>) * kTcStage + kTcPlanes<MODE> * kTcPlane + sizeof(TcShared);
+static_assert(kTcSmem<kForward> <= 232448 && kTcSmem<kWgrad> <= 232448, "227 KB of shared memory");
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     mm_tc_kernel(const __grid_constant__ TcParams T) {
   extern __shared__ unsigned char raw[];
   const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
   unsigned char* stages = raw + (base - ptx::smem_addr(raw));
-  TcShared* S = reinterpret_cast<TcShared*>(stages + size_t(kTcStages) * kTcStage);
+  constexpr int kTcStages = kStages<MODE>;
+  unsigned char* planes = stages + size_t(kTcStages) * kTcStage;
+  TcShared* S = reinterpret_cast<TcShared*>(planes + kTcPlanes<MODE> * kTcPlane);
   const MmParams& P = T.P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(cta_rank());
@@ -426,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTcStages; ++s) {
-      ptx::mbar_init(&S->full[s], 2);
+      ptx::mbar_init(&S->full[s], MODE == kWgrad ? 2 : 6);  // both CTAs' producer warps
       ptx::mbar_init(&S->part[s], 1);
       ptx::mbar_init(&S->empty[s], 1);
     }
@@ -460,11 +587,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const unsigned tiles = S->tile0[P.parts * P.groups];
   const unsigned first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
-  if (warp == 0) {
-    // ---- tensor copies.  The loop over a tile's stages runs on one lane
+  if (warp == 0 || (MODE != kWgrad && warp == 2)) {
+    // ---- tensor copies of the rows.  The loop over a tile's stages runs on one lane
     // wherever the rows of a stage are contiguous (a warp whose lanes issue copies
     // in turn took 830 cycles a stage, more than the 512 of its MMAs).
     const uint32_t full0 = on_first(&S->full[0]);
+    const int block = warp == 2;  // forward, dgrad: the 64 rows of this CTA's half that the warp fetches
     uint32_t k = 0;  // stages filled
     bool ok = true;
     for (unsigned t = first; ok && t < tiles; t += stride) {
@@ -472,40 +600,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       const Ranges R = load_ranges(P, A.p, A.g, 0);
       const int half = A.n / 2;  // rows of B in this CTA (wgrad: features)
       const int blocks = (half + 63) / 64;
-      const int fa = A.f0 + rank * (gated ? 64 : 128);
-      auto weights = [&](uint32_t a, int x, uint32_t bar) {
-        if (MODE == kDgrad) {
-          copy3(a, &T.w[A.p], fa, x, A.g, bar);
-          copy3(a + 8192u, &T.w[A.p], fa + 64, x, A.g, bar);
-        } else if (gated) {
-          copy5(a, &T.w[A.p], x, 0, 0, fa / 16, A.g, bar);
-        } else {
-          copy3(a, &T.w[A.p], x, fa, A.g, bar);
-        }
-      };
       if (MODE != kWgrad) {
+        // This warp's 64 rows of B, a group of 8 per lane modulo 8
+        const int mine = min(half - block * 64, 64);
         int row, left;
-        group_at(P, A.p, A.g, R, A.c0 + rank * half + lane * 8, row, left);
-        const int start = __shfl_sync(0xFFFFFFFFu, row, lane & ~7);
-        // 64-row blocks whose groups, as far as they hold rows, follow one another in the buffer
-        const unsigned broken = __ballot_sync(0xFFFFFFFFu, lane * 8 < half && left > 0 && row != start + (lane & 7) * 8);
-        const int row1 = __shfl_sync(0xFFFFFFFFu, row, 8);
-        if (!broken) {
-          if (lane == 0) {
-            const uint32_t bytes = kTcOperand + uint32_t(blocks) * 8192u + T.tx_pad;
+        group_at(P, A.p, A.g, R, A.c0 + rank * half + block * 64 + (lane & 7) * 8, row, left);
+        const int start = __shfl_sync(0xFFFFFFFFu, row, 0);
+        const bool used = (lane & 7) * 8 < mine;
+        // groups that hold rows follow one another in the buffer: one copy of 64 rows
+        const bool in_line = __all_sync(0xFFFFFFFFu, !used || left == 0 || row == start + (lane & 7) * 8);
+        const uint32_t bytes = mine <= 0 ? 0u : in_line ? 8192u : uint32_t(mine) * 128u;
+        if (in_line || mine <= 0) {
+          if (lane == 0)
             for (int s = 0; s < A.steps; ++s, ++k) {
               const uint32_t st = k % kTcStages, round = k / kTcStages;
               if (round && !wait_bounded(&S->empty[st], (round - 1) & 1, T, S)) {
                 ok = false;
                 break;
               }
-              const uint32_t a = base + st * kTcStage, bar = full0 + st * 8u;
-              arrive_expect_cluster(bar, bytes);
-              weights(a, s * kTcDepth, bar);
-              copy2(a + kTcOperand, &T.row64[A.p], s * kTcDepth, row, bar);
-              if (blocks > 1) copy2(a + kTcOperand + 8192u, &T.row64[A.p], s * kTcDepth, row1, bar);
+              const uint32_t b = base + st * kTcStage + kTcOperand + block * 8192u, bar = full0 + st * 8u;
+              arrive_expect_cluster(bar, bytes + T.tx_pad);
+              if (mine > 0) copy2(b, &T.row64[A.p], s * kTcDepth, start, bar);
             }
-          }
         } else {
           for (int s = 0; s < A.steps; ++s, ++k) {
             const uint32_t st = k % kTcStages, round = k / kTcStages;
@@ -513,14 +629,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
               ok = false;
               break;
             }
-            const uint32_t a = base + st * kTcStage, bar = full0 + st * 8u;
-            if (lane == 0) {
-              arrive_expect_cluster(bar, kTcOperand + uint32_t(half) * 128u + T.tx_pad);
-              weights(a, s * kTcDepth, bar);
-            }
+            const uint32_t b = base + st * kTcStage + kTcOperand + block * 8192u, bar = full0 + st * 8u;
+            if (lane == 0) arrive_expect_cluster(bar, bytes + T.tx_pad);
             __syncwarp();
-            if (lane * 8 < half)
-              copy2(a + kTcOperand + uint32_t(lane) * 1024u, &T.row8[A.p], s * kTcDepth, row, bar);
+            if (used && lane < 8) copy2(b + uint32_t(lane) * 1024u, &T.row8[A.p], s * kTcDepth, row, bar);
             __syncwarp();
           }
         }
@@ -558,9 +670,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             break;
           }
           const uint32_t a = base + st * kTcStage, bar = ptx::smem_addr(&S->part[st]);
-          // rows that follow one another (padding at the end): one copy per 64 features
+          // 64 rows that follow one another: one copy per 64 features
           const int start = __shfl_sync(0xFFFFFFFFu, row, 0);
-          const bool in_line = __all_sync(0xFFFFFFFFu, valid == 0 || row == start + (lane & 7) * 8);
+          const bool in_line = __all_sync(0xFFFFFFFFu, valid > 0 && row == start + (lane & 7) * 8);
           if (lane == 0) arrive_expect_cluster(bar, bytes);
           __syncwarp();
           // lanes: block of 64 features (0, 1 of x, then those of dy) x group of 8 rows
@@ -582,6 +694,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     // The MMAs' last releases of the stages have to land before this CTA may leave.
     for (uint32_t j = k > uint32_t(kTcStages) ? k - kTcStages : 0; ok && j < k; ++j)
       ok = warp_wait(&S->empty[j % kTcStages], (j / kTcStages) & 1, T, S);
+  } else if (MODE != kWgrad && warp == 3) {
+    // ---- tensor copies of the weights
+    if (lane == 0) {
+      const uint32_t full0 = on_first(&S->full[0]);
+      uint32_t k = 0;
+      bool ok = true;
+      for (unsigned t = first; ok && t < tiles; t += stride) {
+        const Tile A = tile_at<MODE>(T, S, t);
+        const int fa = A.f0 + rank * (gated ? 64 : 128);
+        for (int s = 0; s < A.steps; ++s, ++k) {
+          const uint32_t st = k % kTcStages, round = k / kTcStages;
+          if (round && !wait_bounded(&S->empty[st], (round - 1) & 1, T, S)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a = base + st * kTcStage, bar = full0 + st * 8u;
+          const int x = s * kTcDepth;
+          arrive_expect_cluster(bar, kTcOperand);
+          if (MODE == kDgrad) {
+            copy3(a, &T.w[A.p], fa, x, A.g, bar);
+            copy3(a + 8192u, &T.w[A.p], fa + 64, x, A.g, bar);
+          } else if (gated) {
+            copy5(a, &T.w[A.p], x, 0, 0, fa / 16, A.g, bar);
+          } else {
+            copy3(a, &T.w[A.p], x, fa, A.g, bar);
+          }
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ---- MMA
     if (lane == 0) {
@@ -639,60 +781,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         phases ^= 1u << st;
         // lanes: 4 blocks of 64 features (2 of x, 2 of dy) x 8 vectors of a 128-byte row
         unsigned char* at = stages + size_t(st) * kTcStage + (lane >> 3) * 8192 + (lane & 7) * 16;
-        for (int gi = 0; gi < 8; ++gi)
-          for (int r = __shfl_sync(0xFFFFFFFFu, valid, gi); r < 8; ++r)
-            *reinterpret_cast<uint4*>(at + (gi * 8 + r) * 128) = make_uint4(0, 0, 0, 0);
+        // (a group past the expert's end was fetched from past the buffer's: zeros already)
+        unsigned partial = __ballot_sync(0xFFFFFFFFu, valid > 0 && valid < 8) & 0xFFu;
+        while (partial) {
+          const int gi = __ffs(partial) - 1;
+          partial &= partial - 1;
+          const int nv = __shfl_sync(0xFFFFFFFFu, valid, gi);
+#pragma unroll
+          for (int r = 1; r < 8; ++r)
+            if (r >= nv) *reinterpret_cast<uint4*>(at + (gi * 8 + r) * 128) = make_uint4(0, 0, 0, 0);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) arrive_cluster(full0 + st * 8u);
       }
     }
   } else if (warp >= 4) {
-    // ---- epilogue: warps q and q + 4 have the tensor-memory lanes 32 q .. and take turns along the columns
-    const int q = warp & 3, col0 = (warp - 4) / 4 * kTcColumns;
-    uint32_t it = 0;
+    // ---- epilogue: two groups of four warps take turns along the columns
+    const int q = warp & 3, eg = (warp - 4) / 4;
+    unsigned char* in = planes + eg * (MODE == kWgrad ? 2 : 6) * kTcPlane;
+    unsigned char* out = MODE == kWgrad ? in : in + 4 * kTcPlane;
+    uint32_t it = 0, turn = 0;
     for (unsigned t = first; t < tiles; t += stride) {
       const Tile A = tile_at<MODE>(T, S, t);
-      const int f = gated ? A.f0 + rank * 64 + q * 16 + (lane & 15) : A.f0 + rank * 128 + q * 32 + lane;
       int row = 0, valid = 0;
       float bias = 0.f;
       if (MODE != kWgrad) {
         group_at(P, A.p, A.g, load_ranges(P, A.p, A.g, 0), A.c0 + lane * 8, row, valid);
         valid = lane * 8 < T.tile_rows ? min(valid, 8) : 0;  // past them: the next tile's rows
+        const int f = gated ? A.f0 + rank * 64 + q * 16 + (lane & 15) : A.f0 + rank * 128 + q * 32 + lane;
         if (MODE == kForward && P.bias[A.p] && f < P.out)
           bias = bf16_of(P.bias[A.p] + int64_t(A.g) * (gated ? 2 : 1) * P.out + (gated && lane >= 16 ? P.out : 0) + f);
-      }
-      if (A.steps == 0) {  // wgrad of an expert without rows
-        uint32_t v[kTcColumns];
-#pragma unroll
-        for (int j = 0; j < kTcColumns; ++j) v[j] = 0;
-        Beside none;
-        if (!P.accumulate)
-          for (int col = col0; col < A.n; col += 2 * kTcColumns)
-            store_columns<MODE, HOC_ACT_NONE>(P, A, v, col, f, row, valid, bias, none);
-        continue;
+      } else if (A.steps == 0 && P.accumulate) {
+        continue;  // an expert without rows adds nothing
       }
       const uint32_t acc = it & 1;
       const uint32_t at = tmem + acc * 256u + (uint32_t(q * 32) << 16);
       bool ok = true;
-      auto columns = [&](auto tag) {
-        constexpr int act = decltype(tag)::act;
-        Beside B, next;
-        load_beside<MODE, act>(P, A, col0, f, row, valid, B);
-        ok = warp_wait(&S->acc_full[acc], (it >> 1) & 1, T, S);
-        if (!ok) return;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int col = col0; col < A.n; col += 2 * kTcColumns) {
-          load_beside<MODE, act>(P, A, col + 2 * kTcColumns, f, row, valid, next);
-          uint32_t v[kTcColumns];
-          tmem_load(v, at + uint32_t(col));
-          store_columns<MODE, act>(P, A, v, col, f, row, valid, bias, B);
-          B = next;
-        }
+      auto tile = [&](auto tag) {
+        ok = run_epilogue<MODE, decltype(tag)::act>(T, S, A, in, out, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q,
+                                                    rank, row, valid, bias);
       };
-      if (MODE == kWgrad) columns(ActTag<HOC_ACT_NONE>{});
-      else with_act(P.act, columns);
+      if constexpr (MODE == kWgrad) tile(ActTag<HOC_ACT_NONE>{});
+      else with_act(P.act, tile);
       if (!ok) break;
+      if (A.steps == 0) continue;  // no accumulator was used
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive_relaxed(on_first(&S->acc_empty[acc]));
@@ -768,10 +901,15 @@ bool encode_weight(CUtensorMap* m, const MmParams& P, int mode, const void* at) 
 
 bool mm_tc_takes(const MmParams& P, int mode) {
   const bool gated = mode == kForward && P.act == HOC_ACT_SWIGLU;
-  if (P.in % 8 || P.out % (gated ? 16 : 8) || P.ld_rows % 8 || (mode == kWgrad && P.ld_dy % 8)) return false;
+  if (P.in % 8 || P.out % (gated ? 16 : 8) || P.ld_rows % 8 || P.ld_y % 8 || (mode == kWgrad && P.ld_dy % 8)) return false;
   uintptr_t at = 0;
-  for (int p = 0; p < P.parts; ++p)
-    at |= reinterpret_cast<uintptr_t>(P.rows[p]) | reinterpret_cast<uintptr_t>(P.dy[p]) | reinterpret_cast<uintptr_t>(P.w[p]);
+  for (int p = 0; p < P.parts; ++p) {
+    at |= reinterpret_cast<uintptr_t>(P.rows[p]) | reinterpret_cast<uintptr_t>(P.dy[p]) |
+          reinterpret_cast<uintptr_t>(P.w[p]) | reinterpret_cast<uintptr_t>(P.y[p]) | reinterpret_cast<uintptr_t>(P.pre[p]) |
+          reinterpret_cast<uintptr_t>(P.res[p]);
+    if (mode == kForward) at |= reinterpret_cast<uintptr_t>(P.pre_out[p]);
+    if (P.res[p] && P.ld_res % 8) return false;
+  }
   return (at & 15u) == 0 && encoder() != nullptr;
 }
 
@@ -801,7 +939,8 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
     if (!ok) return cudaErrorInvalidValue;
   }
   const void* fn = reinterpret_cast<const void*>(kTc[mode]);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmem));
+  const size_t smem = mode == kForward ? kTcSmem<kForward> : mode == kDgrad ? kTcSmem<kDgrad> : kTcSmem<kWgrad>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -811,7 +950,7 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = kTcSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
