@@ -104,50 +104,86 @@ __global__ void act_grad_kernel(const __nv_bfloat16* dy, const __nv_bfloat16* pr
 }
 
 // ------------------------------------------------------------ bias gradient
-// db[e][n] (+)= sum over the expert's rows of dy[r][n].  A CTA sums 64 columns
-// of one expert: warp w takes rows w, w + 32, ... of each range, lane l columns
-// 2 l and 2 l + 1; the 32 warps' binary32 sums are added in warp order.
-constexpr int kBiasWarps = 32;
-__global__ void __launch_bounds__(32 * kBiasWarps) bias_grad_kernel(const __grid_constant__ MmParams P) {
+// db[e][n] (+)= sum over the expert's rows of dy[r][n]: bound by reading dy once
+// more (after the weight gradient has read it, from L2 where it fits).  A cluster
+// of 8 CTAs sums 64 columns of one expert, each warp taking 4 rows at a time of 8
+// lanes x 8 columns (or, where rows are not whole 16-byte vectors, one row of 32
+// lanes x 2 columns).  Binary32 sums; lanes, warps and CTAs are added in a fixed
+// order.  With one CTA for the 64 columns the 4096 x 4096 gradient took 31 us.
+constexpr int kBiasWarps = 16;
+constexpr int kBiasCtas = 8;
+template <bool VEC>
+__global__ void __cluster_dims__(1, 1, kBiasCtas) __launch_bounds__(32 * kBiasWarps)
+    bias_grad_kernel(const __grid_constant__ MmParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float sums[kBiasWarps][64];
+  __shared__ float mine[64];
   const int i = blockIdx.y, p = P.part0 + i / P.groups, g = P.group0 + i % P.groups;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = int(blockIdx.x) * 64 + lane * 2;
+  const int part = int(blockIdx.z) * kBiasWarps + warp;
+  const int c0 = int(blockIdx.x) * 64;
   const __nv_bfloat16* dy = P.dy[p];
-  const bool pair = c + 1 < P.out && P.ld_dy % 2 == 0 && (reinterpret_cast<uintptr_t>(dy) & 3u) == 0;
-  float a = 0.f, b = 0.f;
+  constexpr int N = VEC ? 8 : 2;
+  constexpr int kRows = VEC ? 4 : 1;  // rows of a warp at a time
+  const int c = c0 + (VEC ? (lane & 7) * 8 : lane * 2), sub = VEC ? lane >> 3 : 0;
+  float acc[N] = {};
   const int ns = P.seg ? P.sources : 1;
-  for (int s = 0; s < ns; ++s) {
+  for (int s = 0; s < ns && c < P.out; ++s) {
     int64_t lo, n;
     mm_range(P, p, g, s, lo, n);
 #pragma unroll 4
-    for (int64_t r = warp; r < n; r += kBiasWarps) {
+    for (int64_t r = int64_t(part) * kRows + sub; r < n; r += kBiasWarps * kBiasCtas * kRows) {
       const __nv_bfloat16* q = dy + (lo + r) * P.ld_dy + c;
-      if (pair) {
-        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(q);
-        a += __low2float(v);
-        b += __high2float(v);
+      if constexpr (VEC) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[2 * e] += __uint_as_float(w[e] << 16);
+          acc[2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
+        }
       } else {
-        if (c < P.out) a += bf16_of(q);
-        if (c + 1 < P.out) b += bf16_of(q + 1);
+        acc[0] += bf16_of(q);
+        if (c + 1 < P.out) acc[1] += bf16_of(q + 1);
       }
     }
   }
-  sums[warp][lane * 2] = a;
-  sums[warp][lane * 2 + 1] = b;
-  __syncthreads();
-  const int col = int(blockIdx.x) * 64 + int(threadIdx.x);
-  if (threadIdx.x >= 64 || col >= P.out) return;
-  float v = 0.f;
-  for (int w = 0; w < kBiasWarps; ++w) v += sums[w][threadIdx.x];
-  const int64_t at = int64_t(g) * P.out + col;
-  if (P.out_f32) {
-    float* o = static_cast<float*>(P.pre_out[p]) + at;
-    *o = P.accumulate ? *o + v : v;
-  } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(P.pre_out[p]) + at;
-    *o = __float2bfloat16_rn(P.accumulate ? bf16_of(o) + v : v);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (VEC) {
+      acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], 8);
+      acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], 16);
+    }
+    if (!VEC || lane < 8) sums[warp][lane * N + e] = acc[e];
   }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    float v = 0.f;
+    for (int w = 0; w < kBiasWarps; ++w) v += sums[w][threadIdx.x];
+    mine[threadIdx.x] = v;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int col = c0 + int(threadIdx.x);
+  if (blockIdx.z == 0 && threadIdx.x < 64 && col < P.out) {
+    float v = 0.f;
+    const uint32_t here = uint32_t(__cvta_generic_to_shared(&mine[threadIdx.x]));
+    for (int w = 0; w < kBiasCtas; ++w) {
+      uint32_t there;
+      float x;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(w));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(there) : "memory");
+      v += x;
+    }
+    const int64_t at = int64_t(g) * P.out + col;
+    if (P.out_f32) {
+      float* o = static_cast<float*>(P.pre_out[p]) + at;
+      *o = P.accumulate ? *o + v : v;
+    } else {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(P.pre_out[p]) + at;
+      *o = __float2bfloat16_rn(P.accumulate ? bf16_of(o) + v : v);
+    }
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ------------------------------------------------------------ host
@@ -247,6 +283,8 @@ hocResult_t run_wgrad(const char* who, MmParams& P, void* const* db, cudaStream_
   if (r != HOC_SUCCESS || !db) return r;
   for (int p = 0; p < P.parts; ++p) P.pre_out[p] = db[p];
   const int pairs = P.parts * P.groups;
+  bool vec = P.out % 8 == 0 && P.ld_dy % 8 == 0;
+  for (int p = 0; p < P.parts; ++p) vec = vec && (reinterpret_cast<uintptr_t>(P.dy[p]) & 15u) == 0;
   MmParams Q = P;
   for (int at = 0; at < pairs;) {  // the grid's y extent ends at 65535
     const int p = at / P.groups, g = at % P.groups;
@@ -258,7 +296,9 @@ hocResult_t run_wgrad(const char* who, MmParams& P, void* const* db, cudaStream_
       Q.parts = P.parts - p;
       Q.groups = P.groups;
     }
-    bias_grad_kernel<<<dim3((P.out + 63) / 64, Q.parts * Q.groups), 32 * kBiasWarps, 0, s>>>(Q);
+    const dim3 grid((P.out + 63) / 64, Q.parts * Q.groups, kBiasCtas);
+    if (vec) bias_grad_kernel<true><<<grid, 32 * kBiasWarps, 0, s>>>(Q);
+    else bias_grad_kernel<false><<<grid, 32 * kBiasWarps, 0, s>>>(Q);
     at += Q.parts * Q.groups;
   }
   if (cudaGetLastError() != cudaSuccess) {
@@ -300,7 +340,8 @@ hocResult_t dense(const char* who, int rows, int in, int out, int32_t* status, M
 cudaError_t mm_preload() {
   const void* fns[] = {reinterpret_cast<const void*>(&seg_count_kernel), reinterpret_cast<const void*>(&seg_scan_kernel),
                        reinterpret_cast<const void*>(&act_grad_kernel<8>), reinterpret_cast<const void*>(&act_grad_kernel<1>),
-                       reinterpret_cast<const void*>(&bias_grad_kernel)};
+                       reinterpret_cast<const void*>(&bias_grad_kernel<true>),
+                       reinterpret_cast<const void*>(&bias_grad_kernel<false>)};
   for (const void* f : fns) {
     cudaFuncAttributes a;
     const cudaError_t e = cudaFuncGetAttributes(&a, f);

@@ -58,7 +58,8 @@ __device__ __forceinline__ void mm_range(const MmParams& P, int p, int g, int s,
 }
 
 // Fills, for every (rank buffer, expert) pair i of the launch, vrows[i]: its
-// rows, each source's count rounded up to `pad`, and tile0[i]: the tiles of the
+// rows, each source's count rounded up to `pad` (64: to 8, and the sum of every 32
+// sources to 64), and tile0[i]: the tiles of the
 // pairs before it, tiles(vrows) tiles each; tile0[n] is the total.  The whole
 // CTA calls it (blockDim.x a multiple of 32).
 template <class Tiles>
@@ -72,9 +73,11 @@ __device__ __forceinline__ void mm_count(const MmParams& P, int pad, int* vrows,
     for (int s = 0; s < ns; ++s) {
       int64_t lo, c;
       mm_range(P, p, P.group0 + i % P.groups, s, lo, c);
-      sum += (c + pad - 1) / pad * pad;
+      const int to = pad < 8 ? pad : 8;
+      sum += (c + to - 1) / to * to;
+      if ((s & 31) == 31 || s == ns - 1) sum = (sum + pad - 1) / pad * pad;
     }
-    const int64_t most = P.cap[p] + int64_t(ns) * (pad - 1);  // more only if ranges overlap
+    const int64_t most = P.cap[p] + int64_t(ns) * (pad - 1) + pad;  // more only if ranges overlap
     vrows[i] = int(sum < most ? sum : most);
   }
   __syncthreads();

@@ -17,15 +17,17 @@
 //
 // An expert's rows lie in one range per source.  They are taken as one virtual
 // row space in which every range is padded to a multiple of 8, the height of a
-// swizzle atom; 8 aligned rows in a row of groups that are contiguous in memory
-// are fetched by one 64-row copy, others by 8-row copies.  Padding rows hold a
-// neighbour's data: in the forward product and the data gradient they are columns
-// that are not stored; in the weight gradient, where rows are summed over, they
-// are overwritten with zeros in shared memory before the MMA reads them.
+// swizzle atom; 64 virtual rows that are contiguous in memory are fetched by one
+// copy, others by copies of 8.  Padding rows hold a neighbour's data: in the
+// forward product and the data gradient they are columns that are not stored; in
+// the weight gradient, where rows are summed over, they are overwritten with zeros
+// in shared memory before the MMA reads them.  There, the whole multiples of 64
+// rows of the ranges come first, each stage one copy per 64 features, and what
+// remains of the ranges is packed into the last stages.
 //
 // Warps of a CTA: 0 and 2 tensor copies of the rows, 64 each; 3 those of the
 // weights; 1 MMA (of the pair's first CTA); 4-11 epilogue.  In the weight gradient
-// warp 0 issues all copies and warp 2 zeroes padding rows.  Every wait is bounded: a wait that runs
+// warp 0 issues all copies and warps 2 and 3 zero padding rows.  Every wait is bounded: a wait that runs
 // out sets bit 2 of the status, and all roles leave.
 #include <atomic>
 #include <cstdlib>
@@ -52,7 +54,7 @@ constexpr uint64_t kTcWaitNs = 2000000000ull;
 
 struct TcParams {
   MmParams P;
-  int tile_rows;     // forward, dgrad: rows of a tile, a multiple of 32
+  int tile_rows;     // most rows c of a tile, a multiple of 32
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
   uint64_t wait_ns;
   CUtensorMap w[kMaxRanks];                      // forward, dgrad
@@ -125,6 +127,23 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, con
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const TcParams& T, TcShared* S) {
   return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, T, S));
 }
+// One lane of a warp, for the instructions that one thread issues.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// The stage that is next in turn, and the parity of its current round.
+template <int STAGES>
+struct Turn {
+  uint32_t st = 0, round = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == STAGES) {
+      st = 0;
+      ++round;
+    }
+  }
+};
 // Tensor copies; the barrier may be the pair's other CTA's.
 __device__ __forceinline__ void copy2(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
   asm volatile(
@@ -195,7 +214,7 @@ __device__ __forceinline__ Tile tile_at(const TcParams& T, const TcShared* S, un
   A.g = P.group0 + i % P.groups;
   const unsigned lt = t - S->tile0[i];
   const int rows = S->vrows[i];
-  const int per = MODE == kWgrad ? kTcRows : T.tile_rows, extent = MODE == kWgrad ? P.out : rows;
+  const int per = T.tile_rows, extent = MODE == kWgrad ? P.out : rows;
   const unsigned ctiles = (extent + per - 1) / per;
   const bool gated = MODE == kForward && P.act == HOC_ACT_SWIGLU;
   A.f0 = int(lt / ctiles) * (gated ? kTcFeatures / 2 : kTcFeatures);
@@ -206,10 +225,14 @@ __device__ __forceinline__ Tile tile_at(const TcParams& T, const TcShared* S, un
 }
 
 // The ranges of one expert, one source per lane: first row, rows, and the
-// virtual row it starts at (of the 32 sources at hand; `all`: past the last).
+// virtual row they start at (of the 32 sources at hand; `all`: past the last).
+// PAD 8: sources one after another, each padded to 8.  PAD 64: first the whole
+// multiples of 64 rows of every range, then what remains of them (`rest`), each
+// padded to 8, and the end padded to 64 (mm_count counts the same).
 struct Ranges {
-  int lo, n, start, all;
+  int lo, n, start, rest, all;
 };
+template <int PAD>
 __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, int g, int base) {
   const int lane = threadIdx.x & 31, s = base + lane;
   int64_t lo = 0, n = 0;
@@ -217,49 +240,71 @@ __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, int g, i
   Ranges R;
   R.lo = int(lo);
   R.n = int(n);
-  const int padded = (R.n + 7) & ~7;
-  int incl = padded;
+  const int whole = PAD == 8 ? 0 : R.n / PAD * PAD, rest = (R.n - whole + 7) & ~7;
+  int a = whole, b = rest;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int x = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-    if (lane >= off) incl += x;
+    const int x = __shfl_up_sync(0xFFFFFFFFu, a, off), y = __shfl_up_sync(0xFFFFFFFFu, b, off);
+    if (lane >= off) {
+      a += x;
+      b += y;
+    }
   }
-  R.start = incl - padded;
-  R.all = __shfl_sync(0xFFFFFFFFu, incl, 31);
+  const int wholes = __shfl_sync(0xFFFFFFFFu, a, 31);
+  R.rest = wholes + b - rest;
+  R.start = PAD == 8 ? R.rest : a - whole;
+  R.all = (wholes + __shfl_sync(0xFFFFFFFFu, b, 31) + PAD - 1) / PAD * PAD;
   return R;
 }
 // Each lane's group of 8 virtual rows at `v` (a multiple of 8): its first row in
 // the buffer and how many rows its range has from there on (0: past the end).
 // The whole warp calls it; R holds the first 32 sources' ranges.
+template <int PAD>
 __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges R, int v, int& row, int& left) {
   const int ns = P.seg ? P.sources : 1;
   row = int(P.cap[p]);
   left = 0;
   for (int base = 0; base < ns; base += 32) {
-    if (ns > 32) R = load_ranges(P, p, g, base);
-    int j = 0;  // the last source that starts at or before v
+    if (ns > 32) R = load_ranges<PAD>(P, p, g, base);
+    const int m = min(32, ns - base);
+    if (PAD == 8) {
+      int j = 0;  // the last source that starts at or before v
 #pragma unroll
-    for (int step = 16; step; step >>= 1) {
-      const int at = __shfl_sync(0xFFFFFFFFu, R.start, j + step);
-      if (at <= v) j += step;
-    }
-    const int lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
-    const int off = v - __shfl_sync(0xFFFFFFFFu, R.start, j);
-    if (v >= 0 && off < n) {
-      row = lo + off;
-      left = n - off;
+      for (int step = 16; step; step >>= 1) {
+        const int at = __shfl_sync(0xFFFFFFFFu, R.start, j + step);
+        if (at <= v) j += step;
+      }
+      const int lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
+      const int off = v - __shfl_sync(0xFFFFFFFFu, R.start, j);
+      if (v >= 0 && off < n) {
+        row = lo + off;
+        left = n - off;
+      }
+    } else {
+      for (int j = 0; j < m; ++j) {
+        const int lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
+        const int a = v - __shfl_sync(0xFFFFFFFFu, R.start, j), b = v - __shfl_sync(0xFFFFFFFFu, R.rest, j);
+        const int whole = n / PAD * PAD;
+        if (v >= 0 && a >= 0 && a < whole) {
+          row = lo + a;
+          left = whole - a;
+        } else if (v >= 0 && b >= 0 && b < n - whole) {
+          row = lo + whole + b;
+          left = n - whole - b;
+        }
+      }
     }
     v -= R.all;  // negative once it was found
   }
 }
 
-// wgrad: the 64 virtual rows of stage s, a group of 8 per lane modulo 8.
-// Returns (to all lanes) how many stages from s on are 64 rows each of the range
-// that stage s begins in, without padding; 0 when stage s is not.
+// wgrad: the 64 virtual rows of stage s, a group of 8 per lane modulo 8 (row, and
+// valid rows of the 8).  Returns (to all lanes) how many stages from s on are 64
+// rows each of one range; 0 when stage s is not.
 __device__ __forceinline__ int stage_rows(const MmParams& P, const Tile& A, const Ranges& R, int s, int& row,
                                           int& valid) {
   int left;
-  group_at(P, A.p, A.g, R, s * kTcDepth + int(threadIdx.x & 7) * 8, row, left);
+  group_at<kTcDepth>(P, A.p, A.g, R, s * kTcDepth + int(threadIdx.x & 7) * 8, row, left);
   valid = min(left, 8);
   return __shfl_sync(0xFFFFFFFFu, left, 0) / kTcDepth;
 }
@@ -576,9 +621,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const int fcount = MODE == kForward ? P.out : P.in;
   const int ftile = gated ? kTcFeatures / 2 : kTcFeatures;
   const unsigned ftiles = (fcount + ftile - 1) / ftile;
-  mm_count(P, 8, S->vrows, S->tile0, [&](int rows) {
-    const int per = MODE == kWgrad ? kTcRows : T.tile_rows, extent = MODE == kWgrad ? P.out : rows;
-    return unsigned((extent + per - 1) / per) * ftiles;
+  mm_count(P, MODE == kWgrad ? kTcDepth : 8, S->vrows, S->tile0, [&](int rows) {
+    const int extent = MODE == kWgrad ? P.out : rows;
+    return unsigned((extent + T.tile_rows - 1) / T.tile_rows) * ftiles;
   });
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   cluster_sync();
@@ -588,129 +633,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const unsigned first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
   if (warp == 0 || (MODE != kWgrad && warp == 2)) {
-    // ---- tensor copies of the rows.  The loop over a tile's stages runs on one lane
-    // wherever the rows of a stage are contiguous (a warp whose lanes issue copies
-    // in turn took 830 cycles a stage, more than the 512 of its MMAs).
+    // ---- tensor copies of the rows.  The whole warp walks the stages, so that
+    // addresses stay in uniform registers, and one lane issues what it can.
+    const bool one = elect_one();
     const uint32_t full0 = on_first(&S->full[0]);
     const int block = warp == 2;  // forward, dgrad: the 64 rows of this CTA's half that the warp fetches
-    uint32_t k = 0;  // stages filled
+    Turn<kTcStages> k;
     bool ok = true;
+    // Waits until the MMAs have released the stage's last filling.
+    auto free = [&]() { return k.round == 0 || warp_wait(&S->empty[k.st], (k.round - 1) & 1, T, S); };
     for (unsigned t = first; ok && t < tiles; t += stride) {
       const Tile A = tile_at<MODE>(T, S, t);
-      const Ranges R = load_ranges(P, A.p, A.g, 0);
+      const Ranges R = load_ranges<MODE == kWgrad ? kTcDepth : 8>(P, A.p, A.g, 0);
       const int half = A.n / 2;  // rows of B in this CTA (wgrad: features)
-      const int blocks = (half + 63) / 64;
       if (MODE != kWgrad) {
         // This warp's 64 rows of B, a group of 8 per lane modulo 8
         const int mine = min(half - block * 64, 64);
         int row, left;
-        group_at(P, A.p, A.g, R, A.c0 + rank * half + block * 64 + (lane & 7) * 8, row, left);
+        group_at<8>(P, A.p, A.g, R, A.c0 + rank * half + block * 64 + (lane & 7) * 8, row, left);
         const int start = __shfl_sync(0xFFFFFFFFu, row, 0);
         const bool used = (lane & 7) * 8 < mine;
         // groups that hold rows follow one another in the buffer: one copy of 64 rows
         const bool in_line = __all_sync(0xFFFFFFFFu, !used || left == 0 || row == start + (lane & 7) * 8);
-        const uint32_t bytes = mine <= 0 ? 0u : in_line ? 8192u : uint32_t(mine) * 128u;
-        if (in_line || mine <= 0) {
-          if (lane == 0)
-            for (int s = 0; s < A.steps; ++s, ++k) {
-              const uint32_t st = k % kTcStages, round = k / kTcStages;
-              if (round && !wait_bounded(&S->empty[st], (round - 1) & 1, T, S)) {
-                ok = false;
-                break;
-              }
-              const uint32_t b = base + st * kTcStage + kTcOperand + block * 8192u, bar = full0 + st * 8u;
-              arrive_expect_cluster(bar, bytes + T.tx_pad);
-              if (mine > 0) copy2(b, &T.row64[A.p], s * kTcDepth, start, bar);
-            }
-        } else {
-          for (int s = 0; s < A.steps; ++s, ++k) {
-            const uint32_t st = k % kTcStages, round = k / kTcStages;
-            if (round && !warp_wait(&S->empty[st], (round - 1) & 1, T, S)) {
-              ok = false;
-              break;
-            }
-            const uint32_t b = base + st * kTcStage + kTcOperand + block * 8192u, bar = full0 + st * 8u;
-            if (lane == 0) arrive_expect_cluster(bar, bytes + T.tx_pad);
-            __syncwarp();
-            if (used && lane < 8) copy2(b + uint32_t(lane) * 1024u, &T.row8[A.p], s * kTcDepth, row, bar);
-            __syncwarp();
-          }
-        }
-        k = __shfl_sync(0xFFFFFFFFu, k, 0);
-        ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
-      } else {
-        const uint32_t bytes = kTcOperand + uint32_t(blocks) * 8192u + T.tx_pad;
-        for (int s = 0; ok && s < A.steps;) {
-          int row, valid;
-          const int run = stage_rows(P, A, R, s, row, valid);
-          if (run > 0) {
-            if (lane == 0)
-              for (int i = 0; i < run; ++i, ++k) {
-                const uint32_t st = k % kTcStages, round = k / kTcStages;
-                if (round && !wait_bounded(&S->empty[st], (round - 1) & 1, T, S)) {
-                  ok = false;
-                  break;
-                }
-                const uint32_t a = base + st * kTcStage, bar = full0 + st * 8u;
-                const int r = row + i * kTcDepth;
-                arrive_expect_cluster(bar, bytes);
-                copy2(a, &T.row64[A.p], A.f0 + rank * 128, r, bar);
-                copy2(a + 8192u, &T.row64[A.p], A.f0 + rank * 128 + 64, r, bar);
-                copy2(a + kTcOperand, &T.dy64[A.p], A.c0 + rank * half, r, bar);
-                if (blocks > 1) copy2(a + kTcOperand + 8192u, &T.dy64[A.p], A.c0 + rank * half + 64, r, bar);
-              }
-            k = __shfl_sync(0xFFFFFFFFu, k, 0);
-            ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
-            s += run;
-            continue;
-          }
-          const uint32_t st = k % kTcStages, round = k / kTcStages;
-          if (round && !warp_wait(&S->empty[st], (round - 1) & 1, T, S)) {
+        const uint32_t bytes = (mine <= 0 ? 0u : in_line ? 8192u : uint32_t(mine) * 128u) + T.tx_pad;
+        for (int s = 0; s < A.steps; ++s, k.next()) {
+          if (!free()) {
             ok = false;
             break;
           }
-          const uint32_t a = base + st * kTcStage, bar = ptx::smem_addr(&S->part[st]);
-          // 64 rows that follow one another: one copy per 64 features
-          const int start = __shfl_sync(0xFFFFFFFFu, row, 0);
-          const bool in_line = __all_sync(0xFFFFFFFFu, valid > 0 && row == start + (lane & 7) * 8);
-          if (lane == 0) arrive_expect_cluster(bar, bytes);
-          __syncwarp();
-          // lanes: block of 64 features (0, 1 of x, then those of dy) x group of 8 rows
-          const int which = lane >> 3;
-          const int x = which < 2 ? A.f0 + rank * 128 + which * 64 : A.c0 + rank * half + (which - 2) * 64;
-          if (which < 2 + blocks) {
-            const uint32_t to = a + uint32_t(which) * 8192u;
-            if (!in_line)
-              copy2(to + uint32_t(lane & 7) * 1024u, which < 2 ? &T.row8[A.p] : &T.dy8[A.p], x, row, bar);
-            else if ((lane & 7) == 0)
-              copy2(to, which < 2 ? &T.row64[A.p] : &T.dy64[A.p], x, row, bar);
+          const uint32_t b = base + k.st * kTcStage + kTcOperand + block * 8192u, bar = full0 + k.st * 8u;
+          if (one) {
+            arrive_expect_cluster(bar, bytes);
+            if (mine > 0 && in_line) copy2(b, &T.row64[A.p], s * kTcDepth, start, bar);
+          }
+          if (!in_line) {
+            __syncwarp();
+            if (used && lane < 8) copy2(b + uint32_t(lane) * 1024u, &T.row8[A.p], s * kTcDepth, row, bar);
           }
           __syncwarp();
+        }
+      } else {
+        const int blocks = (half + 63) / 64;
+        const uint32_t bytes = kTcOperand + uint32_t(blocks) * 8192u + T.tx_pad;
+        const int fx = A.f0 + rank * 128, fd = A.c0 + rank * half;
+        for (int s = 0; ok && s < A.steps;) {
+          int row, valid;
+          const int run = stage_rows(P, A, R, s, row, valid);
+          int r = __shfl_sync(0xFFFFFFFFu, row, 0);
+          for (int i = 0; i < run; ++i, r += kTcDepth, k.next()) {
+            if (!free()) {
+              ok = false;
+              break;
+            }
+            const uint32_t a = base + k.st * kTcStage, bar = full0 + k.st * 8u;
+            if (one) {
+              arrive_expect_cluster(bar, bytes);
+              copy2(a, &T.row64[A.p], fx, r, bar);
+              copy2(a + 8192u, &T.row64[A.p], fx + 64, r, bar);
+              copy2(a + kTcOperand, &T.dy64[A.p], fd, r, bar);
+              if (blocks > 1) copy2(a + kTcOperand + 8192u, &T.dy64[A.p], fd + 64, r, bar);
+            }
+            __syncwarp();
+          }
+          s += run;
+          if (run > 0) continue;
+          if (!free()) {
+            ok = false;
+            break;
+          }
+          // groups of several ranges: lanes are blocks of 64 features (0, 1 of x, then those of dy) x groups
+          const uint32_t a = base + k.st * kTcStage, bar = ptx::smem_addr(&S->part[k.st]);
+          if (one) arrive_expect_cluster(bar, bytes);
+          __syncwarp();
+          const int which = lane >> 3;
+          if (which < 2 + blocks)
+            copy2(a + uint32_t(which) * 8192u + uint32_t(lane & 7) * 1024u, which < 2 ? &T.row8[A.p] : &T.dy8[A.p],
+                  which < 2 ? fx + which * 64 : fd + (which - 2) * 64, row, bar);
+          __syncwarp();
           ++s;
-          ++k;
+          k.next();
         }
       }
     }
     // The MMAs' last releases of the stages have to land before this CTA may leave.
-    for (uint32_t j = k > uint32_t(kTcStages) ? k - kTcStages : 0; ok && j < k; ++j)
-      ok = warp_wait(&S->empty[j % kTcStages], (j / kTcStages) & 1, T, S);
+    for (int j = 0; ok && j < kTcStages; ++j, k.next()) ok = free();
   } else if (MODE != kWgrad && warp == 3) {
     // ---- tensor copies of the weights
-    if (lane == 0) {
-      const uint32_t full0 = on_first(&S->full[0]);
-      uint32_t k = 0;
-      bool ok = true;
-      for (unsigned t = first; ok && t < tiles; t += stride) {
-        const Tile A = tile_at<MODE>(T, S, t);
-        const int fa = A.f0 + rank * (gated ? 64 : 128);
-        for (int s = 0; s < A.steps; ++s, ++k) {
-          const uint32_t st = k % kTcStages, round = k / kTcStages;
-          if (round && !wait_bounded(&S->empty[st], (round - 1) & 1, T, S)) {
-            ok = false;
-            break;
-          }
-          const uint32_t a = base + st * kTcStage, bar = full0 + st * 8u;
-          const int x = s * kTcDepth;
+    const bool one = elect_one();
+    const uint32_t full0 = on_first(&S->full[0]);
+    Turn<kTcStages> k;
+    bool ok = true;
+    for (unsigned t = first; ok && t < tiles; t += stride) {
+      const Tile A = tile_at<MODE>(T, S, t);
+      const int fa = A.f0 + rank * (gated ? 64 : 128);
+      for (int s = 0; s < A.steps; ++s, k.next()) {
+        if (k.round && !warp_wait(&S->empty[k.st], (k.round - 1) & 1, T, S)) {
+          ok = false;
+          break;
+        }
+        const uint32_t a = base + k.st * kTcStage, bar = full0 + k.st * 8u;
+        const int x = s * kTcDepth;
+        if (one) {
           arrive_expect_cluster(bar, kTcOperand);
           if (MODE == kDgrad) {
             copy3(a, &T.w[A.p], fa, x, A.g, bar);
@@ -721,67 +744,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             copy3(a, &T.w[A.p], x, fa, A.g, bar);
           }
         }
+        __syncwarp();
       }
     }
-    __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ---- MMA
-    if (lane == 0) {
-      uint32_t k = 0, it = 0;
-      bool ok = true;
-      const uint32_t kind = (1u << 4) | (1u << 7) | (1u << 10) | (MODE != kForward ? 1u << 15 : 0u) |
-                            (MODE == kWgrad ? 1u << 16 : 0u) | (uint32_t(kTcFeatures / 16) << 24);
-      for (unsigned t = first; ok && t < tiles; t += stride) {
-        const Tile A = tile_at<MODE>(T, S, t);
-        if (A.steps == 0) continue;  // an expert without rows: the epilogue writes zeros
-        const uint32_t idesc = kind | (uint32_t(A.n / 8) << 17);
-        const uint32_t acc = it & 1, d = tmem + acc * 256u;
-        if (it >= 2 && !wait_bounded(&S->acc_empty[acc], ((it >> 1) - 1) & 1, T, S)) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int s = 0; s < A.steps; ++s, ++k) {
-          const uint32_t st = k % kTcStages;
-          if (!wait_bounded(&S->full[st], (k / kTcStages) & 1, T, S)) {
-            ok = false;
-            break;
-          }
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t a = base + st * kTcStage, b = a + kTcOperand;
-          const uint64_t da = MODE == kForward ? smem_desc(a, 16, 1024) : smem_desc(a, 8192, 1024);
-          const uint64_t db = MODE == kWgrad ? smem_desc(b, 8192, 1024) : smem_desc(b, 16, 1024);
-#pragma unroll
-          for (int q = 0; q < kTcDepth / 16; ++q)  // 16 deep: 32 bytes along a K-major row, 16 rows of an M/N-major block
-            mma_pair(d, da + q * (MODE == kForward ? 2 : 128), db + q * (MODE == kWgrad ? 128 : 2), idesc, s | q);
-          commit_pair(&S->empty[st]);
-        }
-        if (ok) commit_pair(&S->acc_full[acc]);
-        ++it;
-      }
-    }
-    __syncwarp();
-  } else if (MODE == kWgrad && warp == 2) {
-    // ---- zero the padding rows of the stages that hold any, then hand them to the MMA
-    const uint32_t full0 = on_first(&S->full[0]);
-    uint32_t k = 0, phases = 0;  // bit st: parity of part[st]
+    const bool one = elect_one();
+    Turn<kTcStages> k;
+    uint32_t it = 0;
     bool ok = true;
+    const uint32_t kind = (1u << 4) | (1u << 7) | (1u << 10) | (MODE != kForward ? 1u << 15 : 0u) |
+                          (MODE == kWgrad ? 1u << 16 : 0u) | (uint32_t(kTcFeatures / 16) << 24);
+    const uint64_t a0 = MODE == kForward ? smem_desc(base, 16, 1024) : smem_desc(base, 8192, 1024);
+    const uint64_t b0 = MODE == kWgrad ? smem_desc(base + kTcOperand, 8192, 1024) : smem_desc(base + kTcOperand, 16, 1024);
     for (unsigned t = first; ok && t < tiles; t += stride) {
       const Tile A = tile_at<MODE>(T, S, t);
-      const Ranges R = load_ranges(P, A.p, A.g, 0);
-      for (int s = 0; s < A.steps;) {
-        int row, valid;
-        const int run = stage_rows(P, A, R, s, row, valid);
-        s += run > 0 ? run : 1;
-        k += run;
-        if (run > 0) continue;
-        const uint32_t st = k % kTcStages;
-        ++k;
-        if (!warp_wait(&S->part[st], (phases >> st) & 1, T, S)) {
+      if (A.steps == 0) continue;  // an expert without rows: the epilogue writes zeros
+      const uint32_t idesc = kind | (uint32_t(A.n / 8) << 17);
+      const uint32_t acc = it & 1, d = tmem + acc * 256u;
+      if (it >= 2 && !warp_wait(&S->acc_empty[acc], ((it >> 1) - 1) & 1, T, S)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      for (int s = 0; s < A.steps; ++s, k.next()) {
+        if (!warp_wait(&S->full[k.st], k.round & 1, T, S)) {
           ok = false;
           break;
         }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t da = a0 + k.st * (kTcStage >> 4), db = b0 + k.st * (kTcStage >> 4);
+        if (one) {
+#pragma unroll
+          for (int q = 0; q < kTcDepth / 16; ++q)  // 16 deep: 32 bytes along a K-major row, 16 rows of an M/N-major block
+            mma_pair(d, da + q * (MODE == kForward ? 2 : 128), db + q * (MODE == kWgrad ? 128 : 2), idesc, s | q);
+          commit_pair(&S->empty[k.st]);
+        }
+        __syncwarp();
+      }
+      if (ok && one) commit_pair(&S->acc_full[acc]);
+      __syncwarp();
+      ++it;
+    }
+  } else if (MODE == kWgrad && (warp == 2 || warp == 3)) {
+    // ---- zero the padding rows of the stages that hold any, then hand them to the
+    // MMA.  Two warps share them, since a release to the cluster takes longer than
+    // the MMAs of a stage: one the even stages, one the odd ones, so that a warp
+    // waits on every phase of the barriers that it waits on.
+    const uint32_t full0 = on_first(&S->full[0]);
+    Turn<kTcStages> k;
+    uint32_t phases = 0;  // bit st: parity of part[st]
+    bool ok = true;
+    for (unsigned t = first; ok && t < tiles; t += stride) {
+      const Tile A = tile_at<MODE>(T, S, t);
+      const Ranges R = load_ranges<kTcDepth>(P, A.p, A.g, 0);
+      for (int s = 0; s < A.steps;) {
+        int row, valid;
+        const int run = stage_rows(P, A, R, s, row, valid);
+        for (int i = 0; i < run; ++i) k.next();
+        s += run;
+        if (run > 0) continue;
+        const uint32_t st = k.st, parity = (phases >> st) & 1;
+        k.next();
+        ++s;
+        if ((st & 1) != uint32_t(warp - 2)) continue;
         phases ^= 1u << st;
+        if (!warp_wait(&S->part[st], parity, T, S)) {
+          ok = false;
+          break;
+        }
         // lanes: 4 blocks of 64 features (2 of x, 2 of dy) x 8 vectors of a 128-byte row
+        // (a group without rows came from past the buffer's end: zeros already)
         unsigned char* at = stages + size_t(st) * kTcStage + (lane >> 3) * 8192 + (lane & 7) * 16;
-        // (a group past the expert's end was fetched from past the buffer's: zeros already)
         unsigned partial = __ballot_sync(0xFFFFFFFFu, valid > 0 && valid < 8) & 0xFFu;
         while (partial) {
           const int gi = __ffs(partial) - 1;
@@ -807,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       int row = 0, valid = 0;
       float bias = 0.f;
       if (MODE != kWgrad) {
-        group_at(P, A.p, A.g, load_ranges(P, A.p, A.g, 0), A.c0 + lane * 8, row, valid);
+        group_at<8>(P, A.p, A.g, load_ranges<8>(P, A.p, A.g, 0), A.c0 + lane * 8, row, valid);
         valid = lane * 8 < T.tile_rows ? min(valid, 8) : 0;  // past them: the next tile's rows
         const int f = gated ? A.f0 + rank * 64 + q * 16 + (lane & 15) : A.f0 + rank * 128 + q * 32 + lane;
         if (MODE == kForward && P.bias[A.p] && f < P.out)
@@ -913,6 +944,55 @@ bool mm_tc_takes(const MmParams& P, int mode) {
   return (at & 15u) == 0 && encoder() != nullptr;
 }
 
+// The launch but for its grid and stream, and the CTA pairs that fit the device at
+// once (asked once for each kernel and device).
+cudaError_t configure(const void* fn, int mode, size_t smem, cudaLaunchAttribute (&attr)[2], cudaLaunchConfig_t& cfg,
+                      int& pairs) {
+  static std::atomic<int> known[3][64];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  pairs = dev < 64 ? known[mode][dev].load() : 0;
+  if (pairs > 0) return cudaSuccess;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2);
+  e = cudaOccupancyMaxActiveClusters(&pairs, fn, &cfg);
+  cfg.numAttrs = 2;
+  if (e == cudaSuccess && pairs < 1) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess && dev < 64) known[mode][dev].store(pairs);
+  return e;
+}
+
+// Rows of a tile.  Where the number of rows is known (one range, or the features
+// of the weight gradient) the height whose tiles fill the CTA pairs best: a wave
+// costs about 256 + T for tiles of T rows (its features' operand comes with every
+// tile), e.g. 4096 rows x 16 feature tiles on 76 pairs: 4 waves of 224 rows instead
+// of 4 of 256 (101 -> 95 us at 4096 deep).  Ragged rows take the largest: a tile's
+// MMAs are only as wide as the rows that it has.
+int choose_rows(int64_t rows, int64_t others, int pairs) {
+  int best = kTcRows;
+  int64_t least = INT64_MAX;
+  for (int r = kTcRows; r >= 64; r -= 32) {
+    const int64_t tiles = (rows + r - 1) / r * others, cost = (tiles + pairs - 1) / pairs * (256 + r);
+    if (cost < least) {
+      least = cost;
+      best = r;
+    }
+  }
+  return best;
+}
+
 cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   TcParams T;
   T.P = P;
@@ -921,11 +1001,21 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   const bool stall = fault && !strcmp(fault, "mm_stall");
   T.tx_pad = stall ? 16u : 0u;
   T.wait_ns = stall ? 100000000ull : kTcWaitNs;
+  const void* fn = reinterpret_cast<const void*>(kTc[mode]);
+  const size_t smem = mode == kForward ? kTcSmem<kForward> : mode == kDgrad ? kTcSmem<kDgrad> : kTcSmem<kWgrad>;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  int pairs = 0;
+  cudaError_t e = configure(fn, mode, smem, attr, cfg, pairs);
+  if (e != cudaSuccess) return e;
+  cfg.stream = s;
   int64_t tiles = 0;
   const int ftile = mode == kForward && P.act == HOC_ACT_SWIGLU ? kTcFeatures / 2 : kTcFeatures;
   const int64_t ftiles = ((mode == kForward ? P.out : P.in) + ftile - 1) / ftile;
+  if (mode == kWgrad) T.tile_rows = choose_rows(P.out, ftiles * P.groups * P.parts, pairs);
+  else if (P.seg == nullptr) T.tile_rows = choose_rows(P.cap[0], ftiles, pairs);
   for (int p = P.part0; p < P.part0 + P.parts; ++p) {
-    tiles += ftiles * (mode == kWgrad ? int64_t(P.groups) * ((P.out + kTcRows - 1) / kTcRows)
+    tiles += ftiles * (mode == kWgrad ? int64_t(P.groups) * ((P.out + T.tile_rows - 1) / T.tile_rows)
                                       : P.cap[p] / T.tile_rows + int64_t(P.groups) * (1 + P.sources * 8 / T.tile_rows));
     bool ok = mode == kWgrad || encode_weight(&T.w[p], P, mode, P.w[p]);
     if (P.cap[p] > 0) {  // a buffer without rows has no tile that reads it
@@ -938,36 +1028,7 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
     }
     if (!ok) return cudaErrorInvalidValue;
   }
-  const void* fn = reinterpret_cast<const void*>(kTc[mode]);
-  const size_t smem = mode == kForward ? kTcSmem<kForward> : mode == kDgrad ? kTcSmem<kDgrad> : kTcSmem<kWgrad>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(2);
-  // CTA pairs that fit the device at once: asked once for each kernel and device
-  static std::atomic<int> known[3][64];
-  int dev = 0;
-  e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  int pairs = dev < 64 ? known[mode][dev].load() : 0;
-  if (pairs == 0) {
-    e = cudaOccupancyMaxActiveClusters(&pairs, fn, &cfg);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) known[mode][dev].store(pairs);
-  }
-  cfg.numAttrs = 2;
-  cfg.gridDim = dim3(2 * unsigned(tiles < 1 ? 1 : tiles < pairs ? tiles : pairs > 0 ? pairs : 1));
+  cfg.gridDim = dim3(2 * unsigned(tiles < 1 ? 1 : tiles < pairs ? tiles : pairs));
   return cudaLaunchKernelEx(&cfg, kTc[mode], T);
 }
 
