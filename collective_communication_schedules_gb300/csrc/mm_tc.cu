@@ -18,7 +18,7 @@
 // An expert's rows lie in one range per source.  They are taken as one virtual
 // row space in which every range is padded to a multiple of 8, the height of a
 // swizzle atom; 64 virtual rows that are contiguous in memory are fetched by one
-// copy, others by copies of 8.  Padding rows hold a neighbour's data: in the
+// copy, others by copies of 32, 16 and 8.  Padding rows hold a neighbour's data: in the
 // forward product and the data gradient they are columns that are not stored; in
 // the weight gradient, where rows are summed over, they are overwritten with zeros
 // in shared memory before the MMA reads them.  There, the whole multiples of 64
@@ -58,8 +58,8 @@ struct TcParams {
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
   uint64_t wait_ns;
   CUtensorMap w[kMaxRanks];                      // forward, dgrad
-  CUtensorMap row64[kMaxRanks], row8[kMaxRanks]; // P.rows in boxes of 64 and 8 rows
-  CUtensorMap dy64[kMaxRanks], dy8[kMaxRanks];   // wgrad
+  CUtensorMap row[kMaxRanks][4];                 // P.rows in boxes of 8 << i rows
+  CUtensorMap dy[kMaxRanks][4];                  // wgrad
 };
 
 // Stages: what the epilogue's planes leave of 227 KB (a sixth stage is worth 1 to 2
@@ -296,6 +296,23 @@ __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges
     }
     v -= R.all;  // negative once it was found
   }
+}
+
+// How 64 virtual rows, a group of 8 per lane modulo 8, are fetched: a run of groups
+// that follow one another in the buffer by copies of 64, 32, 16 and 8 rows, as the
+// binary digits of its length say (groups without rows make runs too).  Returns
+// log2 of the groups of the copy that starts at this lane's group, or -1.
+__device__ __forceinline__ int box_at(int row, int left) {
+  const int j = threadIdx.x & 7;
+  const int r = __shfl_up_sync(0xFFFFFFFFu, row, 1), l = __shfl_up_sync(0xFFFFFFFFu, left, 1);
+  const bool goes_on = j > 0 && (left > 0 ? l > 0 && row == r + 8 : l <= 0);
+  const unsigned starts = (__ballot_sync(0xFFFFFFFFu, !goes_on) & 0xFFu) | 0x100u;
+  const int from = 31 - __clz(starts & ((2u << j) - 1u));
+  const int len = __ffs(starts >> (j + 1)) + j - from, at = j - from;
+  if (len == 8) return at == 0 ? 3 : -1;
+  if ((len & 4) && at == 0) return 2;
+  if ((len & 2) && at == (len & 4)) return 1;
+  return (len & 1) && at == (len & 6) ? 0 : -1;
 }
 
 // wgrad: the 64 virtual rows of stage s, a group of 8 per lane modulo 8 (row, and
@@ -651,25 +668,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const int mine = min(half - block * 64, 64);
         int row, left;
         group_at<8>(P, A.p, A.g, R, A.c0 + rank * half + block * 64 + (lane & 7) * 8, row, left);
-        const int start = __shfl_sync(0xFFFFFFFFu, row, 0);
-        const bool used = (lane & 7) * 8 < mine;
-        // groups that hold rows follow one another in the buffer: one copy of 64 rows
-        const bool in_line = __all_sync(0xFFFFFFFFu, !used || left == 0 || row == start + (lane & 7) * 8);
-        const uint32_t bytes = (mine <= 0 ? 0u : in_line ? 8192u : uint32_t(mine) * 128u) + T.tx_pad;
+        if ((lane & 7) * 8 >= mine) left = 0;
+        // Columns of groups without rows are not stored: they are not fetched.
+        const int box = left > 0 ? box_at(row, left) : (box_at(row, left), -1);
+        const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xFFFFFFFFu, left > 0) & 0xFFu)) * 1024u + T.tx_pad;
+        const CUtensorMap* map = &T.row[A.p][box < 0 ? 0 : box];
         for (int s = 0; s < A.steps; ++s, k.next()) {
           if (!free()) {
             ok = false;
             break;
           }
           const uint32_t b = base + k.st * kTcStage + kTcOperand + block * 8192u, bar = full0 + k.st * 8u;
-          if (one) {
-            arrive_expect_cluster(bar, bytes);
-            if (mine > 0 && in_line) copy2(b, &T.row64[A.p], s * kTcDepth, start, bar);
-          }
-          if (!in_line) {
-            __syncwarp();
-            if (used && lane < 8) copy2(b + uint32_t(lane) * 1024u, &T.row8[A.p], s * kTcDepth, row, bar);
-          }
+          if (one) arrive_expect_cluster(bar, bytes);
+          __syncwarp();
+          if (lane < 8 && box >= 0) copy2(b + uint32_t(lane) * 1024u, map, s * kTcDepth, row, bar);
           __syncwarp();
         }
       } else {
@@ -688,10 +700,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             const uint32_t a = base + k.st * kTcStage, bar = full0 + k.st * 8u;
             if (one) {
               arrive_expect_cluster(bar, bytes);
-              copy2(a, &T.row64[A.p], fx, r, bar);
-              copy2(a + 8192u, &T.row64[A.p], fx + 64, r, bar);
-              copy2(a + kTcOperand, &T.dy64[A.p], fd, r, bar);
-              if (blocks > 1) copy2(a + kTcOperand + 8192u, &T.dy64[A.p], fd + 64, r, bar);
+              copy2(a, &T.row[A.p][3], fx, r, bar);
+              copy2(a + 8192u, &T.row[A.p][3], fx + 64, r, bar);
+              copy2(a + kTcOperand, &T.dy[A.p][3], fd, r, bar);
+              if (blocks > 1) copy2(a + kTcOperand + 8192u, &T.dy[A.p][3], fd + 64, r, bar);
             }
             __syncwarp();
           }
@@ -701,13 +713,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             ok = false;
             break;
           }
-          // groups of several ranges: lanes are blocks of 64 features (0, 1 of x, then those of dy) x groups
+          // runs of several ranges: lanes are blocks of 64 features (0, 1 of x, then those of dy) x groups
           const uint32_t a = base + k.st * kTcStage, bar = ptx::smem_addr(&S->part[k.st]);
+          const int box = box_at(row, valid), which = lane >> 3;
           if (one) arrive_expect_cluster(bar, bytes);
           __syncwarp();
-          const int which = lane >> 3;
-          if (which < 2 + blocks)
-            copy2(a + uint32_t(which) * 8192u + uint32_t(lane & 7) * 1024u, which < 2 ? &T.row8[A.p] : &T.dy8[A.p],
+          if (which < 2 + blocks && box >= 0)
+            copy2(a + uint32_t(which) * 8192u + uint32_t(lane & 7) * 1024u,
+                  which < 2 ? &T.row[A.p][box] : &T.dy[A.p][box],
                   which < 2 ? fx + which * 64 : fd + (which - 2) * 64, row, bar);
           __syncwarp();
           ++s;
@@ -1020,11 +1033,10 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
     bool ok = mode == kWgrad || encode_weight(&T.w[p], P, mode, P.w[p]);
     if (P.cap[p] > 0) {  // a buffer without rows has no tile that reads it
       const int64_t width = mode == kDgrad ? P.out : P.in;
-      ok = ok && encode_rows(&T.row64[p], P.rows[p], width, P.cap[p], P.ld_rows, 64) &&
-           encode_rows(&T.row8[p], P.rows[p], width, P.cap[p], P.ld_rows, 8);
-      if (mode == kWgrad)
-        ok = ok && encode_rows(&T.dy64[p], P.dy[p], P.out, P.cap[p], P.ld_dy, 64) &&
-             encode_rows(&T.dy8[p], P.dy[p], P.out, P.cap[p], P.ld_dy, 8);
+      for (int i = 0; i < 4; ++i) {
+        ok = ok && encode_rows(&T.row[p][i], P.rows[p], width, P.cap[p], P.ld_rows, 8 << i);
+        if (mode == kWgrad) ok = ok && encode_rows(&T.dy[p][i], P.dy[p], P.out, P.cap[p], P.ld_dy, 8 << i);
+      }
     }
     if (!ok) return cudaErrorInvalidValue;
   }
