@@ -66,19 +66,26 @@ template <class Tiles>
 __device__ __forceinline__ void mm_count(const MmParams& P, int pad, int* vrows, unsigned* tile0, Tiles tiles) {
   const int n = P.parts * P.groups;
   const int ns = P.seg ? P.sources : 1;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int p = P.part0 + i / P.groups;
+  // The lanes of a warp take the sources of as many pairs as fit, then add up in segments of `w` lanes.
+  int w = 1;
+  while (w < ns && w < 32) w *= 2;
+  const int lane = threadIdx.x & 31, sub = lane & (w - 1);
+  const int per = int(blockDim.x) / w;  // pairs at a time
+  for (int at = 0; at < n; at += per) {
+    const int i = at + int(threadIdx.x) / w;
     int64_t sum = 0;
-#pragma unroll 4
-    for (int s = 0; s < ns; ++s) {
-      int64_t lo, c;
-      mm_range(P, p, P.group0 + i % P.groups, s, lo, c);
+    for (int base = 0; base < ns; base += 32) {
+      int64_t lo, c = 0;
+      if (i < n && base + sub < ns) mm_range(P, P.part0 + i / P.groups, P.group0 + i % P.groups, base + sub, lo, c);
       const int to = pad < 8 ? pad : 8;
-      sum += (c + to - 1) / to * to;
-      if ((s & 31) == 31 || s == ns - 1) sum = (sum + pad - 1) / pad * pad;
+      c = (c + to - 1) / to * to;
+      for (int off = w / 2; off; off >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, off);
+      sum += (c + pad - 1) / pad * pad;
     }
-    const int64_t most = P.cap[p] + int64_t(ns) * (pad - 1) + pad;  // more only if ranges overlap
-    vrows[i] = int(sum < most ? sum : most);
+    if (i < n && sub == 0) {
+      const int64_t most = P.cap[P.part0 + i / P.groups] + int64_t(ns) * (pad - 1) + pad;  // more only if ranges overlap
+      vrows[i] = int(sum < most ? sum : most);
+    }
   }
   __syncthreads();
   if (threadIdx.x < 32) {

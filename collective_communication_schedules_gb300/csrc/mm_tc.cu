@@ -230,7 +230,7 @@ __device__ __forceinline__ Tile tile_at(const TcParams& T, const TcShared* S, un
 // multiples of 64 rows of every range, then what remains of them (`rest`), each
 // padded to 8, and the end padded to 64 (mm_count counts the same).
 struct Ranges {
-  int lo, n, start, rest, all;
+  int lo, n, start, rest, wholes, all;
 };
 template <int PAD>
 __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, int g, int base) {
@@ -251,6 +251,7 @@ __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, int g, i
     }
   }
   const int wholes = __shfl_sync(0xFFFFFFFFu, a, 31);
+  R.wholes = wholes;
   R.rest = wholes + b - rest;
   R.start = PAD == 8 ? R.rest : a - whole;
   R.all = (wholes + __shfl_sync(0xFFFFFFFFu, b, 31) + PAD - 1) / PAD * PAD;
@@ -266,33 +267,20 @@ __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges
   left = 0;
   for (int base = 0; base < ns; base += 32) {
     if (ns > 32) R = load_ranges<PAD>(P, p, g, base);
-    const int m = min(32, ns - base);
-    if (PAD == 8) {
-      int j = 0;  // the last source that starts at or before v
+    // whole multiples of PAD, or what remains (for PAD 64 all lanes alike: their v share a multiple of 64)
+    const bool whole = PAD > 8 && v < R.wholes;
+    const int key = whole ? R.start : R.rest;
+    int j = 0;  // the last source that starts at or before v
 #pragma unroll
-      for (int step = 16; step; step >>= 1) {
-        const int at = __shfl_sync(0xFFFFFFFFu, R.start, j + step);
-        if (at <= v) j += step;
-      }
-      const int lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
-      const int off = v - __shfl_sync(0xFFFFFFFFu, R.start, j);
-      if (v >= 0 && off < n) {
-        row = lo + off;
-        left = n - off;
-      }
-    } else {
-      for (int j = 0; j < m; ++j) {
-        const int lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
-        const int a = v - __shfl_sync(0xFFFFFFFFu, R.start, j), b = v - __shfl_sync(0xFFFFFFFFu, R.rest, j);
-        const int whole = n / PAD * PAD;
-        if (v >= 0 && a >= 0 && a < whole) {
-          row = lo + a;
-          left = whole - a;
-        } else if (v >= 0 && b >= 0 && b < n - whole) {
-          row = lo + whole + b;
-          left = n - whole - b;
-        }
-      }
+    for (int step = 16; step; step >>= 1) {
+      const int at = __shfl_sync(0xFFFFFFFFu, key, j + step);
+      if (at <= v) j += step;
+    }
+    const int lo = __shfl_sync(0xFFFFFFFFu, R.lo, j), n = __shfl_sync(0xFFFFFFFFu, R.n, j);
+    const int off = v - __shfl_sync(0xFFFFFFFFu, key, j), cut = PAD > 8 ? n / PAD * PAD : 0;
+    if (v >= 0 && off < (whole ? cut : n - cut)) {
+      row = lo + (whole ? 0 : cut) + off;
+      left = (whole ? cut : n - cut) - off;
     }
     v -= R.all;  // negative once it was found
   }
@@ -349,7 +337,8 @@ __device__ __forceinline__ void with_act(int act, F f) {
 // layer's widths.  Four warps together stage kTcColumns rows of 128 features, so
 // that a row goes out as 256 contiguous bytes.  What the epilogue reads beside
 // the accumulator (the residual, the pre-activation of the layer below) comes
-// the same way, a step ahead.
+// the same way, two steps ahead (one step was shorter than the latency of HBM), and
+// results take the place of what was read.
 
 // Where the features of a staged row are in global memory: `chunks` vectors of 8
 // features, of which the last may lie past the row's end.
@@ -382,32 +371,38 @@ __device__ __forceinline__ int64_t row_of(int col, int c, int row, int valid) {
   return (c & 7) < nv ? int64_t(r0) + (c & 7) : -1;
 }
 
-// kTcColumns rows of CHUNKS vectors between shared memory (row pitch 16 * CHUNKS
-// bytes) and a strip, by 128 threads.  `at` names the row of a column or -1.
-template <int CHUNKS, class At>
-__device__ __forceinline__ void fetch_rows(uint32_t smem, const Strip& G, At at) {
-  const int i = int(threadIdx.x) & 127;
+// The rows that this thread moves in a step at `col`: vector (i + 128 h) % CHUNKS
+// of column (i + 128 h) / CHUNKS, i its number in the group.  at(c): the row of
+// column c of the step, or -1.
+template <int CHUNKS>
+struct Rows {
+  int64_t r[kTcColumns * CHUNKS / 128];
+  template <class At>
+  __device__ __forceinline__ explicit Rows(At at) {
 #pragma unroll
-  for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h) {
-    const int c = (i + 128 * h) / CHUNKS, v = (i + 128 * h) % CHUNKS;
-    const int64_t r = at(c);
-    if (r >= 0 && v * 8 < G.left)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem + uint32_t(c * CHUNKS + v) * 16u),
-                   "l"(G.at + r * G.pitch + v * 16)
+    for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h) r[h] = at((int(threadIdx.x & 127) + 128 * h) / CHUNKS);
+  }
+};
+// kTcColumns rows of CHUNKS vectors from a strip into shared memory (rows of
+// 16 * CHUNKS bytes) and back, by 128 threads.
+template <int CHUNKS>
+__device__ __forceinline__ void fetch_rows(uint32_t smem, const Strip& G, const Rows<CHUNKS>& R) {
+  const int i = int(threadIdx.x) & 127, v = i % CHUNKS;
+#pragma unroll
+  for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h)
+    if (R.r[h] >= 0 && v * 8 < G.left)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem + uint32_t(i + 128 * h) * 16u),
+                   "l"(G.at + R.r[h] * G.pitch + v * 16)
                    : "memory");
-  }
 }
-template <int CHUNKS, class At>
-__device__ __forceinline__ void put_rows(const unsigned char* smem, const Strip& G, At at, int turn = 0) {
-  const int i = int(threadIdx.x) & 127;
+template <int CHUNKS>
+__device__ __forceinline__ void put_rows(const unsigned char* smem, const Strip& G, const Rows<CHUNKS>& R) {
+  const int i = int(threadIdx.x) & 127, v = i % CHUNKS;
 #pragma unroll
-  for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h) {
-    const int c = (i + 128 * h) / CHUNKS, v = (i + 128 * h) % CHUNKS;
-    const int64_t r = at(c);
-    if (r >= 0 && v * 8 < G.left)
-      *reinterpret_cast<uint4*>(G.at + r * G.pitch + v * 16) =
-          *reinterpret_cast<const uint4*>(smem + (c * CHUNKS + (v ^ turn)) * 16);
-  }
+  for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h)
+    if (R.r[h] >= 0 && v * 8 < G.left)
+      *reinterpret_cast<uint4*>(G.at + R.r[h] * G.pitch + v * 16) =
+          *reinterpret_cast<const uint4*>(smem + (i + 128 * h) * 16);
 }
 
 __device__ __forceinline__ float bf16_at(const unsigned char* p) {
@@ -419,12 +414,12 @@ __device__ __forceinline__ void put_bf16(unsigned char* p, float v) {
 
 // The epilogue of one tile by group `eg` of four warps (warp q of it has tensor
 // memory lanes 32 q ..): the steps of kTcColumns columns whose number is eg modulo
-// 2.  in: the group's two input planes (two arrays each); out: its two output
-// planes, which the arrays that are stored take in turn, with one barrier each.
-// False when the accumulator did not come.
+// 2.  in: the group's three input buffers (dgrad: of two planes each); out: its two
+// output planes, which the arrays that are stored take in turn; turn and buffer go on
+// from tile to tile.  False when the accumulator did not come.
 template <int MODE, int ACT>
 __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, const Tile& A, unsigned char* in,
-                                             unsigned char* out, uint32_t& turn, uint32_t acc_at, uint64_t* acc_full,
+                                             unsigned char* out, uint32_t& turn, uint32_t& buffer, uint32_t acc_at, uint64_t* acc_full,
                                              uint32_t parity, int eg, int q, int rank, int row, int valid, float bias) {
   constexpr bool gated = MODE == kForward && ACT == HOC_ACT_SWIGLU;
   constexpr bool twice = MODE == kDgrad && ACT == HOC_ACT_SWIGLU;  // two inputs, two outputs
@@ -449,17 +444,20 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
     s.at += 2 * int64_t(width);
     return s;
   };
-  auto fetch = [&](int col) {
-    if (reads && col < A.n) {
-      const uint32_t to = in_addr + (uint32_t(col / kTcColumns) / 2 & 1) * 2 * kTcPlane;
-      auto at = [&](int c) { return row_of(col, c, row, valid); };
-      fetch_rows<gated ? 8 : 16>(to, beside, at);
-      if (twice) fetch_rows<16>(to + kTcPlane, second(beside), at);
+  constexpr uint32_t kBuffer = (MODE == kDgrad ? 2 : 1) * kTcPlane;
+  auto fetch = [&](int col, uint32_t buffer) {
+    if (col < A.n) {
+      const Rows<gated ? 8 : 16> r([&](int c) { return row_of(col, c, row, valid); });
+      fetch_rows(in_addr + buffer * kBuffer, beside, r);
+      if constexpr (twice) fetch_rows(in_addr + buffer * kBuffer + kTcPlane, second(beside), r);
     }
-    if (reads) asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   const int first = eg * kTcColumns;
-  fetch(first);
+  if (reads) {  // the buffer of the last tile's last step may still be read: the two others
+    fetch(first, buffer);
+    fetch(first + 2 * kTcColumns, buffer == 2 ? 0 : buffer + 1);
+  }
   bool ok = true;
   if (A.steps > 0) {
     ok = warp_wait(acc_full, parity, T, S);
@@ -470,7 +468,6 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
     return false;
   }
   for (int col = first; col < A.n; col += 2 * kTcColumns) {
-    fetch(col + 2 * kTcColumns);
     uint32_t v[kTcColumns];
     if (MODE != kWgrad || A.steps > 0) {
       tmem_load(v, acc_at + uint32_t(col));
@@ -479,11 +476,15 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
       for (int j = 0; j < kTcColumns; ++j) v[j] = 0;
     }
     auto at = [&](int c) { return row_of(col, c, row, valid); };
-    const unsigned char* x = in + (uint32_t(col / kTcColumns) / 2 & 1) * 2 * kTcPlane;
+    unsigned char* x = in + buffer * kBuffer;
     if (reads) {
       asm volatile("cp.async.wait_group 1;" ::: "memory");
-      group_barrier(eg);
+      group_barrier(eg);  // this step's input is there, and the buffer of the step before is free
+      fetch(col + 4 * kTcColumns, buffer == 0 ? 2 : buffer - 1);
+      buffer = buffer == 2 ? 0 : buffer + 1;
     }
+    // Where the arrays to be stored are staged: in the place of what was read, or in the next output plane.
+    auto plane = [&]() { return reads ? x : out + (turn++ & 1) * kTcPlane; };
     if constexpr (MODE == kWgrad) {  // columns are out features
       const int c0 = A.c0 + col, f = f0 + q * 32 + lane;
       const int64_t first_at = (int64_t(A.g) * P.out + c0) * P.in;
@@ -511,7 +512,7 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
         for (int j = 0; j < kTcColumns; ++j) put_bf16(o + j * kTcRowBytes + (q * 32 + lane) * 2, __uint_as_float(v[j]));
         group_barrier(eg);
         const Strip w{static_cast<char*>(P.y[A.p]) + 2 * (int64_t(A.g) * P.out * P.in + fs), 2 * int64_t(P.in), left};
-        put_rows<16>(o, w, [&](int c) { return c0 + c < P.out ? int64_t(c0 + c) : int64_t(-1); });
+        put_rows(o, w, Rows<16>([&](int c) { return c0 + c < P.out ? int64_t(c0 + c) : int64_t(-1); }));
       }
     } else if constexpr (gated) {
       // Lanes 0-15 hold the gates of 16 features, lanes 16-31 their values.
@@ -537,7 +538,7 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
         }
       }
       // The halves of a warp swap: each lane then has gate and value of 8 of the 16 columns.
-      unsigned char* o = out + (turn++ & 1) * kTcPlane;
+      unsigned char* o = plane();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[8 + j]) + bias, 16);
@@ -548,17 +549,18 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
         put_bf16(o + at_byte, z);
       }
       group_barrier(eg);
-      put_rows<8>(o, y, at);
+      put_rows(o, y, Rows<8>(at));
     } else {
       const int mine = (q * 32 + lane) * 2;
+      const Rows<16> r(at);
       if (keep) {
         unsigned char* o = out + (turn++ & 1) * kTcPlane;
 #pragma unroll
         for (int j = 0; j < kTcColumns; ++j) put_bf16(o + j * kTcRowBytes + mine, __uint_as_float(v[j]) + bias);
         group_barrier(eg);
-        put_rows<16>(o, kept, at);
+        put_rows(o, kept, r);
       }
-      unsigned char* o = out + (turn++ & 1) * kTcPlane;
+      unsigned char* o = plane();
 #pragma unroll
       for (int j = 0; j < kTcColumns; ++j) {
         const unsigned char* z = x + j * kTcRowBytes + mine;
@@ -567,23 +569,17 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
           d = mm_act(ACT, d + bias);
           if (res) d += bf16_at(z);
         } else if (twice) {
-          const float g = bf16_at(z);
-          v[j] = __float_as_uint(d * mm_act(HOC_ACT_SILU, g));
-          d *= bf16_at(z + kTcPlane) * mm_act_slope(HOC_ACT_SILU, g);
+          const float g = bf16_at(z), u = bf16_at(z + kTcPlane);
+          put_bf16(o + kTcPlane + j * kTcRowBytes + mine, d * mm_act(HOC_ACT_SILU, g));
+          d *= u * mm_act_slope(HOC_ACT_SILU, g);
         } else if (ACT != HOC_ACT_NONE) {
           d *= mm_act_slope(ACT, bf16_at(z));
         }
         put_bf16(o + j * kTcRowBytes + mine, d);
       }
       group_barrier(eg);
-      put_rows<16>(o, y, at);
-      if (twice) {
-        unsigned char* o2 = out + (turn++ & 1) * kTcPlane;
-#pragma unroll
-        for (int j = 0; j < kTcColumns; ++j) put_bf16(o2 + j * kTcRowBytes + mine, __uint_as_float(v[j]));
-        group_barrier(eg);
-        put_rows<16>(o2, second(y), at);
-      }
+      put_rows(o, y, r);
+      if constexpr (twice) put_rows(o + kTcPlane, second(y), r);
     }
   }
   if (reads) asm volatile("cp.async.wait_all;" ::: "memory");
@@ -591,13 +587,17 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
 }
 
 // ------------------------------------------------------------------ kernel
-// Stages, then for each of the two epilogue groups four input planes (not in
-// wgrad) and two output planes, then the barriers and tile counts.
+// Stages, then the planes of the two epilogue groups (three input buffers, in dgrad
+// of two planes and otherwise followed by two output planes; dgrad without an
+// activation takes its output planes from its buffers; wgrad has output planes
+// only), then the barriers and tile counts.
 template <int MODE>
-constexpr size_t kTcPlanes = 2 * (MODE == kWgrad ? 2 : 6);
+constexpr size_t kGroupPlanes = MODE == kForward ? 5 : MODE == kDgrad ? 6 : 2;
+template <int MODE>
+constexpr size_t kTcPlanes = 2 * kGroupPlanes<MODE>;
 template <int MODE>
 constexpr size_t kTcSmem = 1024 + size_t(kStages<MODE>) * kTcStage + kTcPlanes<MODE> * kTcPlane + sizeof(TcShared);
-static_assert(kTcSmem<kForward> <= 232448 && kTcSmem<kWgrad> <= 232448, "227 KB of shared memory");
+static_assert(kTcSmem<kForward> <= 232448 && kTcSmem<kDgrad> <= 232448 && kTcSmem<kWgrad> <= 232448, "227 KB of shared memory");
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
@@ -632,6 +632,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                  "r"(kTcTmemColumns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (warp == 3 && lane < P.parts) {
+    auto prefetch = [](const CUtensorMap* m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); };
+    if (MODE != kWgrad) prefetch(&T.w[P.part0 + lane]);
+    if (P.cap[P.part0 + lane] > 0) prefetch(&T.row[P.part0 + lane][3]);
+    if (MODE == kWgrad && P.cap[P.part0 + lane] > 0) prefetch(&T.dy[P.part0 + lane][3]);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -843,9 +849,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   } else if (warp >= 4) {
     // ---- epilogue: two groups of four warps take turns along the columns
     const int q = warp & 3, eg = (warp - 4) / 4;
-    unsigned char* in = planes + eg * (MODE == kWgrad ? 2 : 6) * kTcPlane;
-    unsigned char* out = MODE == kWgrad ? in : in + 4 * kTcPlane;
-    uint32_t it = 0, turn = 0;
+    unsigned char* in = planes + eg * kGroupPlanes<MODE> * kTcPlane;
+    unsigned char* out = MODE == kForward ? in + 3 * kTcPlane : in;
+    uint32_t it = 0, turn = 0, buffer = 0;
     for (unsigned t = first; t < tiles; t += stride) {
       const Tile A = tile_at<MODE>(T, S, t);
       int row = 0, valid = 0;
@@ -863,7 +869,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       const uint32_t at = tmem + acc * 256u + (uint32_t(q * 32) << 16);
       bool ok = true;
       auto tile = [&](auto tag) {
-        ok = run_epilogue<MODE, decltype(tag)::act>(T, S, A, in, out, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q,
+        ok = run_epilogue<MODE, decltype(tag)::act>(T, S, A, in, out, turn, buffer, at, &S->acc_full[acc], (it >> 1) & 1, eg, q,
                                                     rank, row, valid, bias);
       };
       if constexpr (MODE == kWgrad) tile(ActTag<HOC_ACT_NONE>{});
