@@ -242,7 +242,7 @@ hocResult_t take(const char* who, const char* name, const void* const* from, con
 hocResult_t run_product(const char* who, MmParams& P, int mode, cudaStream_t s) {
   const int sms = sm_count();
   const int nranks = P.parts, experts = P.groups;
-  const bool tc = mm_tc_takes(P, mode);
+  const bool few = mm_few_takes(P, mode), tc = !few && mm_tc_takes(P, mode);
   const int by_group = experts < kMmMaxGroups ? experts : kMmMaxGroups;
   const int by_part = kMmMaxGroups / by_group < nranks ? kMmMaxGroups / by_group : nranks;
   for (int p = 0; p < nranks; p += by_part)
@@ -254,7 +254,9 @@ hocResult_t run_product(const char* who, MmParams& P, int mode, cudaStream_t s) 
       int64_t rows = 0;
       for (int q = p; q < p + P.parts; ++q) rows += P.cap[q];
       if (rows == 0 && mode != kWgrad) continue;
-      const cudaError_t e = tc ? launch_mm_tc(P, mode, s) : launch_mm_any(P, mode, sms, s);
+      const cudaError_t e = few  ? launch_mm_few(P, s)
+                            : tc ? launch_mm_tc(P, mode, s)
+                                 : launch_mm_any(P, mode, sms, s);
       if (e != cudaSuccess) {
         char msg[160];
         snprintf(msg, sizeof msg, "%s: launch failed: %s", who, cudaGetErrorString(e));
@@ -347,7 +349,8 @@ cudaError_t mm_preload() {
     const cudaError_t e = cudaFuncGetAttributes(&a, f);
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = mm_any_preload();
+  cudaError_t e = mm_any_preload();
+  if (e == cudaSuccess) e = mm_few_preload();
   return e == cudaSuccess ? mm_tc_preload() : e;
 }
 

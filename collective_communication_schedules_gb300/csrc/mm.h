@@ -1,5 +1,5 @@
 // Matrix products on rows grouped by expert: what the host entry points
-// (layer.cu) pass to the kernels (mm_any.cu, mm_tc.cu).
+// (layer.cu) pass to the kernels (mm_any.cu, mm_few.cu, mm_tc.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -161,5 +161,9 @@ cudaError_t mm_any_preload();
 bool mm_tc_takes(const MmParams& P, int mode);
 cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s);
 cudaError_t mm_tc_preload();
+// Whether the kernel for a few rows takes this product (one range, at most 32 rows).
+bool mm_few_takes(const MmParams& P, int mode);
+cudaError_t launch_mm_few(const MmParams& P, cudaStream_t s);
+cudaError_t mm_few_preload();
 
 }  // namespace hoc

@@ -55,6 +55,8 @@ constexpr uint64_t kTcWaitNs = 2000000000ull;
 struct TcParams {
   MmParams P;
   int tile_rows;     // most rows c of a tile, a multiple of 32
+  uint32_t stage;    // bytes of a stage: 128 x 64 of A, half of tile_rows x 64 of B
+  uint32_t stages;
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
   uint64_t wait_ns;
   CUtensorMap w[kMaxRanks];                      // forward, dgrad
@@ -62,11 +64,11 @@ struct TcParams {
   CUtensorMap dy[kMaxRanks][4];                  // wgrad
 };
 
-// Stages: what the epilogue's planes leave of 227 KB (a sixth stage is worth 1 to 2
-// % of the rate on long contractions).
+// Shared memory for the stages: what the epilogue's planes leave of 227 KB.  That
+// is 5 stages (wgrad 6) of a tile of 256 rows, and up to 8 of a lower one.
 template <int MODE>
-constexpr int kStages = MODE == kWgrad ? 6 : 5;
-constexpr int kTcMostStages = 6;
+constexpr uint32_t kStageBytes = (MODE == kWgrad ? 6 : 5) * kTcStage;
+constexpr int kTcMostStages = 8;
 
 struct TcShared {
   uint64_t full[kTcMostStages];   // on the first CTA: both CTAs' loads of a stage
@@ -134,11 +136,11 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 // The stage that is next in turn, and the parity of its current round.
-template <int STAGES>
 struct Turn {
-  uint32_t st = 0, round = 0;
+  uint32_t stages, st = 0, round = 0;
+  __device__ __forceinline__ explicit Turn(uint32_t n) : stages(n) {}
   __device__ __forceinline__ void next() {
-    if (++st == STAGES) {
+    if (++st == stages) {
       st = 0;
       ++round;
     }
@@ -596,7 +598,7 @@ constexpr size_t kGroupPlanes = MODE == kForward ? 5 : MODE == kDgrad ? 6 : 2;
 template <int MODE>
 constexpr size_t kTcPlanes = 2 * kGroupPlanes<MODE>;
 template <int MODE>
-constexpr size_t kTcSmem = 1024 + size_t(kStages<MODE>) * kTcStage + kTcPlanes<MODE> * kTcPlane + sizeof(TcShared);
+constexpr size_t kTcSmem = 1024 + kStageBytes<MODE> + kTcPlanes<MODE> * kTcPlane + sizeof(TcShared);
 static_assert(kTcSmem<kForward> <= 232448 && kTcSmem<kDgrad> <= 232448 && kTcSmem<kWgrad> <= 232448, "227 KB of shared memory");
 
 template <int MODE>
@@ -605,8 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   extern __shared__ unsigned char raw[];
   const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
   unsigned char* stages = raw + (base - ptx::smem_addr(raw));
-  constexpr int kTcStages = kStages<MODE>;
-  unsigned char* planes = stages + size_t(kTcStages) * kTcStage;
+  unsigned char* planes = stages + kStageBytes<MODE>;
   TcShared* S = reinterpret_cast<TcShared*>(planes + kTcPlanes<MODE> * kTcPlane);
   const MmParams& P = T.P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -614,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const bool gated = MODE == kForward && P.act == HOC_ACT_SWIGLU;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kTcStages; ++s) {
+    for (int s = 0; s < kTcMostStages; ++s) {
       ptx::mbar_init(&S->full[s], MODE == kWgrad ? 2 : 6);  // both CTAs' producer warps
       ptx::mbar_init(&S->part[s], 1);
       ptx::mbar_init(&S->empty[s], 1);
@@ -661,7 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     const bool one = elect_one();
     const uint32_t full0 = on_first(&S->full[0]);
     const int block = warp == 2;  // forward, dgrad: the 64 rows of this CTA's half that the warp fetches
-    Turn<kTcStages> k;
+    Turn k(T.stages);
     bool ok = true;
     // Waits until the MMAs have released the stage's last filling.
     auto free = [&]() { return k.round == 0 || warp_wait(&S->empty[k.st], (k.round - 1) & 1, T, S); };
@@ -684,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t b = base + k.st * kTcStage + kTcOperand + block * 8192u, bar = full0 + k.st * 8u;
+          const uint32_t b = base + k.st * T.stage + kTcOperand + block * 8192u, bar = full0 + k.st * 8u;
           if (one) arrive_expect_cluster(bar, bytes);
           __syncwarp();
           if (lane < 8 && box >= 0) copy2(b + uint32_t(lane) * 1024u, map, s * kTcDepth, row, bar);
@@ -703,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
               ok = false;
               break;
             }
-            const uint32_t a = base + k.st * kTcStage, bar = full0 + k.st * 8u;
+            const uint32_t a = base + k.st * T.stage, bar = full0 + k.st * 8u;
             if (one) {
               arrive_expect_cluster(bar, bytes);
               copy2(a, &T.row[A.p][3], fx, r, bar);
@@ -720,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             break;
           }
           // runs of several ranges: lanes are blocks of 64 features (0, 1 of x, then those of dy) x groups
-          const uint32_t a = base + k.st * kTcStage, bar = ptx::smem_addr(&S->part[k.st]);
+          const uint32_t a = base + k.st * T.stage, bar = ptx::smem_addr(&S->part[k.st]);
           const int box = box_at(row, valid), which = lane >> 3;
           if (one) arrive_expect_cluster(bar, bytes);
           __syncwarp();
@@ -735,12 +736,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       }
     }
     // The MMAs' last releases of the stages have to land before this CTA may leave.
-    for (int j = 0; ok && j < kTcStages; ++j, k.next()) ok = free();
+    for (uint32_t j = 0; ok && j < T.stages; ++j, k.next()) ok = free();
   } else if (MODE != kWgrad && warp == 3) {
     // ---- tensor copies of the weights
     const bool one = elect_one();
     const uint32_t full0 = on_first(&S->full[0]);
-    Turn<kTcStages> k;
+    Turn k(T.stages);
     bool ok = true;
     for (unsigned t = first; ok && t < tiles; t += stride) {
       const Tile A = tile_at<MODE>(T, S, t);
@@ -750,7 +751,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t a = base + k.st * kTcStage, bar = full0 + k.st * 8u;
+        const uint32_t a = base + k.st * T.stage, bar = full0 + k.st * 8u;
         const int x = s * kTcDepth;
         if (one) {
           arrive_expect_cluster(bar, kTcOperand);
@@ -769,7 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   } else if (warp == 1 && rank == 0) {
     // ---- MMA
     const bool one = elect_one();
-    Turn<kTcStages> k;
+    Turn k(T.stages);
     uint32_t it = 0;
     bool ok = true;
     const uint32_t kind = (1u << 4) | (1u << 7) | (1u << 10) | (MODE != kForward ? 1u << 15 : 0u) |
@@ -789,7 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t da = a0 + k.st * (kTcStage >> 4), db = b0 + k.st * (kTcStage >> 4);
+        const uint64_t da = a0 + k.st * (T.stage >> 4), db = b0 + k.st * (T.stage >> 4);
         if (one) {
 #pragma unroll
           for (int q = 0; q < kTcDepth / 16; ++q)  // 16 deep: 32 bytes along a K-major row, 16 rows of an M/N-major block
@@ -808,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     // the MMAs of a stage: one the even stages, one the odd ones, so that a warp
     // waits on every phase of the barriers that it waits on.
     const uint32_t full0 = on_first(&S->full[0]);
-    Turn<kTcStages> k;
+    Turn k(T.stages);
     uint32_t phases = 0;  // bit st: parity of part[st]
     bool ok = true;
     for (unsigned t = first; ok && t < tiles; t += stride) {
@@ -831,7 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         }
         // lanes: 4 blocks of 64 features (2 of x, 2 of dy) x 8 vectors of a 128-byte row
         // (a group without rows came from past the buffer's end: zeros already)
-        unsigned char* at = stages + size_t(st) * kTcStage + (lane >> 3) * 8192 + (lane & 7) * 16;
+        unsigned char* at = stages + size_t(st) * T.stage + (lane >> 3) * 8192 + (lane & 7) * 16;
         unsigned partial = __ballot_sync(0xFFFFFFFFu, valid > 0 && valid < 8) & 0xFFu;
         while (partial) {
           const int gi = __ffs(partial) - 1;
@@ -947,6 +948,17 @@ bool encode_weight(CUtensorMap* m, const MmParams& P, int mode, const void* at) 
   return encode(m, at, 3, dims, strides, box);
 }
 
+// Ragged rows: 256, since a tile's MMAs are only as wide as the rows that it has,
+// unless the buffers' room says that an expert has few rows on average; lower tiles
+// then leave shared memory for more stages, and the weights that a decoding step
+// streams need many bytes in flight.
+int choose_rows_ragged(const MmParams& P) {
+  int64_t rows = 0;
+  for (int p = P.part0; p < P.part0 + P.parts; ++p) rows += P.cap[p];
+  const int64_t each = rows / P.parts / P.experts;
+  return each <= 32 ? 64 : each <= 64 ? 128 : kTcRows;
+}
+
 }  // namespace
 
 bool mm_tc_takes(const MmParams& P, int mode) {
@@ -997,8 +1009,7 @@ cudaError_t configure(const void* fn, int mode, size_t smem, cudaLaunchAttribute
 // of the weight gradient) the height whose tiles fill the CTA pairs best: a wave
 // costs about 256 + T for tiles of T rows (its features' operand comes with every
 // tile), e.g. 4096 rows x 16 feature tiles on 76 pairs: 4 waves of 224 rows instead
-// of 4 of 256 (101 -> 95 us at 4096 deep).  Ragged rows take the largest: a tile's
-// MMAs are only as wide as the rows that it has.
+// of 4 of 256 (101 -> 95 us at 4096 deep).
 int choose_rows(int64_t rows, int64_t others, int pairs) {
   int best = kTcRows;
   int64_t least = INT64_MAX;
@@ -1033,6 +1044,10 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   const int64_t ftiles = ((mode == kForward ? P.out : P.in) + ftile - 1) / ftile;
   if (mode == kWgrad) T.tile_rows = choose_rows(P.out, ftiles * P.groups * P.parts, pairs);
   else if (P.seg == nullptr) T.tile_rows = choose_rows(P.cap[0], ftiles, pairs);
+  else T.tile_rows = choose_rows_ragged(P);
+  T.stage = mode == kWgrad ? kTcStage : kTcOperand + uint32_t(T.tile_rows) * (kTcDepth * 2 / 2);
+  T.stages = (mode == kWgrad ? kStageBytes<kWgrad> : kStageBytes<kForward>) / T.stage;
+  if (T.stages > uint32_t(kTcMostStages)) T.stages = kTcMostStages;
   for (int p = P.part0; p < P.part0 + P.parts; ++p) {
     tiles += ftiles * (mode == kWgrad ? int64_t(P.groups) * ((P.out + T.tile_rows - 1) / T.tile_rows)
                                       : P.cap[p] / T.tile_rows + int64_t(P.groups) * (1 + P.sources * 8 / T.tile_rows));
