@@ -1125,15 +1125,25 @@ __global__ void __launch_bounds__(256) ep_combine_grad_kernel(const __grid_const
     const int j0 = int(it - tok * groups) * group, j1 = min(R.topk, j0 + group);
     const int s = int(tok / R.tokens), t = int(tok - (long long)s * R.tokens);
     const char* dy = R.x[s] + size_t(t) * R.hidden * 2;
+    // the lanes resolve 32 pairs at a time: each its row (or none) and weight
+    int d_of = 0;
+    long long row_of = -1;
+    float w_of = 0.f;
     for (int j = j0; j < j1; ++j) {
       const size_t pr = size_t(t) * R.topk + j;
-      const int p = R.pos_of[s][pr];
-      int d = 0;
-      long long row = -1;
-      if (p >= 0) row = route_row(R, base, s, pair_expert(R, s, pr), p, 2, &d);
+      if ((j - j0) % 32 == 0) {
+        row_of = -1;
+        if (j + lane < j1) {
+          const int p = R.pos_of[s][pr + lane], e = pair_expert(R, s, pr + lane);
+          w_of = R.w[s][pr + lane];
+          if (p >= 0) row_of = route_row(R, base, s, e, p, 2, &d_of);
+        }
+      }
+      const int d = __shfl_sync(0xFFFFFFFFu, d_of, (j - j0) % 32);
+      const long long row = __shfl_sync(0xFFFFFFFFu, row_of, (j - j0) % 32);
+      const float w = __shfl_sync(0xFFFFFFFFu, w_of, (j - j0) % 32);
       float dot = 0.f;
       if (row >= 0) {
-        const float w = R.w[s][pr];
         const size_t at = size_t(row) * R.hidden * 2;
         if (VEC) {
           const uint4* a = reinterpret_cast<const uint4*>(dy);

@@ -35,12 +35,11 @@ namespace {
 
 using Tile = hocTensorList::Tile;
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;
 constexpr int kGradUnroll = 4;          // 16-byte loads a thread has in flight
-constexpr size_t kTileMost = 32768;     // elements
+constexpr size_t kTileMost = 16384;     // elements: with 32768, 12800 tiles on 608 CTAs left 4 % of them idle in the last round
 constexpr size_t kTileLeast = 2048;
-constexpr int kGradCtas = 152 * 8;      // at most: partial sums in the workspace
-static_assert(kGradCtas % 2 == 0, "the workspace is binary64");
+constexpr int kGradCtas = 152 * 4;      // at most: partial sums in the workspace
 
 template <class T>
 __device__ __forceinline__ float widen(T v);
@@ -68,17 +67,6 @@ __device__ __forceinline__ uint64_t head_of(const char* p, uint64_t n) {
   return h < n ? h : n;
 }
 
-// Sum over the CTA, the same for every thread, in a fixed order.
-__device__ __forceinline__ double cta_sum(double v, double* sh) {
-  for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double all = 0;
-  for (int w = 0; w < kGradThreads / 32; ++w) all += sh[w];
-  return all;
-}
-
 template <class T>
 __global__ void __launch_bounds__(kGradThreads) grad_square_kernel(const Tile* __restrict__ tiles, uint64_t ntiles,
                                                                    double* __restrict__ partial) {
@@ -86,9 +74,11 @@ __global__ void __launch_bounds__(kGradThreads) grad_square_kernel(const Tile* _
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int V = 16 / sizeof(T);
   __shared__ double sh[kGradThreads / 32];
-  double mine = 0;
+  double mine = 0;  // lane 0: the warp's sum.  This GPU adds few binary64 values a cycle, so that is once a tile.
+  Tile next = blockIdx.x < ntiles ? tiles[blockIdx.x] : Tile{};
   for (uint64_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
-    const Tile tile = tiles[t];
+    const Tile tile = next;
+    if (t + gridDim.x < ntiles) next = tiles[t + gridDim.x];
     const T* p = reinterpret_cast<const T*>(tile.ptr);
     const uint64_t head = head_of<T>(tile.ptr, tile.n), nvec = (tile.n - head) / V;
     const uint64_t tail0 = head + nvec * V;
@@ -112,23 +102,36 @@ __global__ void __launch_bounds__(kGradThreads) grad_square_kernel(const Tile* _
           s[u] = fmaf(f, f, s[u]);
         }
     }
-    mine += double((s[0] + s[1]) + (s[2] + s[3]));
+    float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+    if ((threadIdx.x & 31) == 0) mine += double(sum);
   }
-  const double all = cta_sum(mine, sh);
-  if (threadIdx.x == 0) partial[blockIdx.x] = all;
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double all = 0;
+    for (int w = 0; w < kGradThreads / 32; ++w) all += sh[w];
+    partial[blockIdx.x] = all;
+  }
 }
 
-__device__ __forceinline__ float norm_of(const double* partial, int n, double* sh) {
-  double v = 0;
-  for (int i = threadIdx.x; i < n; i += kGradThreads) v += partial[i];
-  return float(sqrt(cta_sum(v, sh)));
+// sqrt of the partial sums' total, added up by one warp in a fixed order.
+__device__ __forceinline__ float norm_of(const double* partial, int n, float* sh) {
+  if (threadIdx.x < 32) {
+    double v = 0;
+    for (int i = threadIdx.x; i < n; i += 32) v += partial[i];
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    if (threadIdx.x == 0) *sh = float(sqrt(v));
+  }
+  __syncthreads();
+  return *sh;
 }
 
 __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const double* __restrict__ partial, int n,
                                                                  float* norm) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ double sh[kGradThreads / 32];
-  const float v = norm_of(partial, n, sh);
+  __shared__ float sh;
+  const float v = norm_of(partial, n, &sh);
   if (threadIdx.x == 0) *norm = v;
 }
 
@@ -139,17 +142,21 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const Tile* sr
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int V = 16 / sizeof(T);
-  __shared__ double sh[kGradThreads / 32];
-  const float nv = norm_of(partial, n, sh);
+  __shared__ float sh;
+  const float nv = norm_of(partial, n, &sh);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
   float c = max_norm / (nv + 1e-6f);
   if (c > 1.f) c = 1.f;  // NaN stays
-  if (in_place && c == 1.f) return;
+  if ((in_place && c == 1.f) || blockIdx.x >= ntiles) return;
+  Tile next = src[ntiles - 1 - blockIdx.x], next_dst = dst[ntiles - 1 - blockIdx.x];
   for (uint64_t k = blockIdx.x; k < ntiles; k += gridDim.x) {
-    const uint64_t t = ntiles - 1 - k;
-    const Tile a = src[t];
+    const Tile a = next, b = next_dst;
+    if (k + gridDim.x < ntiles) {
+      next = src[ntiles - 1 - (k + gridDim.x)];
+      next_dst = dst[ntiles - 1 - (k + gridDim.x)];
+    }
     const T* p = reinterpret_cast<const T*>(a.ptr);
-    T* q = reinterpret_cast<T*>(dst[t].ptr);
+    T* q = reinterpret_cast<T*>(b.ptr);
     if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) != 0) {
       for (uint64_t i = threadIdx.x; i < a.n; i += kGradThreads) q[i] = narrow<T>(c * widen(p[i]));
       continue;

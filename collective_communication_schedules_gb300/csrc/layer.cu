@@ -1,8 +1,8 @@
 // Entry points of hoc_layer.h: argument checks, the choice of a product
 // kernel, and the small kernels around the products (row ranges of a dispatch,
 // activation gradient, bias gradient).
+#include <atomic>
 #include <cstdio>
-#include <cstring>
 
 #include "mm.h"
 
@@ -198,8 +198,12 @@ hocResult_t refuse(const char* who, const char* what) {
 }
 
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, sms = 1;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev < 64 && known[dev].load() > 0) return known[dev].load();
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev < 64) known[dev].store(sms);
   return sms;
 }
 

@@ -231,13 +231,21 @@ def _ptr_array(xs: Sequence, nbytes=0, what: str = "buffer", device: bool = True
     spans = list(nbytes) if isinstance(nbytes, (list, tuple)) else [nbytes] * len(xs)
     if len(spans) != len(xs):
         raise ValueError(f"{what}: expected {len(spans)} rank buffers, got {len(xs)}")
-    return (C.c_void_p * len(xs))(*[_ptr(x, n, f"{what}[{r}]", device) for r, (x, n) in enumerate(zip(xs, spans))])
+    out = (C.c_void_p * len(xs))()
+    for r, (x, n) in enumerate(zip(xs, spans)):
+        # the checks of _ptr, which names the buffer if one fails
+        if isinstance(x, int) or not x.is_contiguous() or x.numel() * x.element_size() < n or x.is_cuda != device:
+            out[r] = _ptr(x, n, f"{what}[{r}]", device)
+        else:
+            out[r] = x.data_ptr()
+    return out
 
 
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without building a Stream object
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -666,45 +674,59 @@ def _act(act) -> int:
     return ACTS[act]
 
 
-def _typed(x, dtypes, what: str):
-    """`x` checked to be a tensor of one of `dtypes` (names)."""
-    import torch
-    if isinstance(x, int) or x.dtype not in [getattr(torch, d) for d in dtypes]:
-        raise TypeError(f"{what}: expected a tensor of {' or '.join(dtypes)}")
+_TORCH = {}  # torch dtypes by name, once torch is imported
+
+
+def _dt(name: str):
+    if not _TORCH:
+        import torch
+        _TORCH.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "int64")})
+    return _TORCH[name]
+
+
+def _typed(x, dtype: str, what: str):
+    """`x` checked to be a tensor of `dtype`."""
+    if isinstance(x, int) or x.dtype is not _dt(dtype):
+        raise TypeError(f"{what}: expected a {dtype} tensor")
     return x
 
 
-def _shaped(x, shape, what: str, dtypes=("bfloat16",)) -> int:
+def _shaped(x, shape: tuple, what: str, dtype: str = "bfloat16", rank: int = -1) -> int:
     """Address of the contiguous device tensor `x`, which has to have `shape`."""
-    if tuple(_typed(x, dtypes, what).shape) != tuple(shape):
-        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
-    return _ptr(x, 0, what)
+    if isinstance(x, int) or x.dtype is not _dt(dtype) or x.shape != shape or not x.is_cuda or not x.is_contiguous():
+        name = what if rank < 0 else f"{what}[{rank}]"
+        _typed(x, dtype, name)
+        if x.shape != shape:
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(x.shape)}")
+        return _ptr(x, 0, name)
+    return x.data_ptr()
 
 
-def _strided(x, shape, what: str):
+def _strided(x, shape: tuple, what: str):
     """Address and row stride of the bf16 matrix `x`, whose rows' elements are contiguous."""
-    if tuple(_typed(x, ("bfloat16",), what).shape) != tuple(shape):
-        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
+    if _typed(x, "bfloat16", what).shape != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(x.shape)}")
     if not x.is_cuda:
         raise ValueError(f"{what}: must be a CUDA tensor")
     rows, width = shape
-    if width > 1 and x.stride(1) != 1:
+    if width > 1 and rows and x.stride(1) != 1:
         raise ValueError(f"{what}: a row's elements must be contiguous")
     if rows > 1 and x.stride(0) < width:
         raise ValueError(f"{what}: rows must not overlap")
     return x.data_ptr(), max(x.stride(0) if rows > 1 else width, width)
 
 
-def _per_rank(xs, shapes, what: str, dtypes=("bfloat16",)) -> C.Array:
-    if len(xs) != len(shapes):
-        raise ValueError(f"{what}: expected {len(shapes)} per-rank tensors, got {len(xs)}")
-    return (C.c_void_p * len(xs))(*[_shaped(x, s, f"{what}[{r}]", dtypes) for r, (x, s) in enumerate(zip(xs, shapes))])
+def _per_rank(xs, shapes, what: str, dtype: str = "bfloat16") -> C.Array:
+    n = len(shapes)
+    if len(xs) != n:
+        raise ValueError(f"{what}: expected {n} per-rank tensors, got {len(xs)}")
+    return (C.c_void_p * n)(*[_shaped(xs[r], shapes[r], what, dtype, r) for r in range(n)])
 
 
 def _groups(rows, experts: int, seg):
     """The hocRowGroups_t of buffers with `rows[d]` rows each, and what it points to."""
     k = len(rows)
-    _typed(seg, ("int64",), "seg")
+    _typed(seg, "int64", "seg")
     if seg.dim() != 2 or seg.shape[0] != k or seg.shape[1] < experts + 1 or (seg.shape[1] - 1) % experts:
         raise ValueError(f"seg: expected shape [{k}, sources * {experts} + 1], got {tuple(seg.shape)}")
     cap = (C.c_size_t * max(1, k))(*rows)
@@ -719,9 +741,9 @@ def ep_segments(expert_ids, experts: int, topk: int, seg, stream=None):
     if topk < 1 or n % topk:
         raise ValueError("expert_ids must hold topk ids per token")
     for r, v in enumerate(expert_ids):
-        _typed(v, ("int32",), f"expert_ids[{r}]")
+        _typed(v, "int32", f"expert_ids[{r}]")
     _check(lib().hoc_ep_segments(k, _ptr_array(expert_ids, 4 * n, "expert_ids"), n // topk, int(topk), int(experts),
-                                 _shaped(seg, (k, int(experts) + 1), "seg", ("int64",)), _stream(stream)),
+                                 _shaped(seg, (k, int(experts) + 1), "seg", "int64"), _stream(stream)),
            "hoc_ep_segments")
 
 
@@ -771,7 +793,7 @@ def expert_mm_wgrad(dy, x, seg, dw, *, status, db=None, accumulate: bool = False
     if not k or dw[0].dim() != 3:
         raise ValueError("x: a list of matrices, dw: a list of [experts, out, in] tensors")
     experts, out, inp = dw[0].shape
-    rows, dt = [t.shape[0] for t in x], ("float32",) if dw[0].dtype.is_floating_point and dw[0].element_size() == 4 else ("bfloat16",)
+    rows, dt = [t.shape[0] for t in x], "float32" if dw[0].dtype is _dt("float32") else "bfloat16"
     g, _keep = _groups(rows, experts, seg)
     _check(lib().hoc_expert_mm_wgrad(C.byref(g), _per_rank(dy, [(n, out) for n in rows], "dy"),
                                      _per_rank(x, [(n, inp) for n in rows], "x"), inp, out, _dtype_code(dw[0]),
@@ -820,7 +842,7 @@ def linear_wgrad(dy, x, dw, *, status, db=None, accumulate: bool = False, stream
     if dw.dim() != 2 or x.dim() != 2:
         raise ValueError("x and dw must be matrices")
     (out, inp), rows = dw.shape, x.shape[0]
-    dt = ("float32",) if dw.dtype.is_floating_point and dw.element_size() == 4 else ("bfloat16",)
+    dt = "float32" if dw.dtype is _dt("float32") else "bfloat16"
     dp, ldd = _strided(dy, (rows, out), "dy")
     xp, ldx = _strided(x, (rows, inp), "x")
     _check(lib().hoc_linear_wgrad(rows, dp, ldd, xp, ldx, inp, out, _dtype_code(dw), int(bool(accumulate)),
@@ -886,16 +908,16 @@ def grad_workspace(tensors: TensorList) -> int:
 
 def grad_norm(tensors: TensorList, norm, workspace, stream=None):
     """norm[0] = the global 2-norm of the list (see include/hoc_grad.h); norm: float32, workspace: int32 tensors."""
-    _check(lib().hoc_grad_norm(tensors._h, _ptr(_typed(norm, ("float32",), "norm"), 4, "norm"),
-                               _ptr(_typed(workspace, ("int32",), "workspace"), 0, "workspace"),
+    _check(lib().hoc_grad_norm(tensors._h, _ptr(_typed(norm, "float32", "norm"), 4, "norm"),
+                               _ptr(_typed(workspace, "int32", "workspace"), 0, "workspace"),
                                int(workspace.numel()), _stream(stream)), "hoc_grad_norm")
 
 
 def grad_clip(src: TensorList, dst: TensorList, max_norm: float, norm, workspace, stream=None):
     """dst = min(1, max_norm / (norm + 1e-6)) * src with the global norm of src, which is left in norm[0]; dst may be
     src (see include/hoc_grad.h)."""
-    _check(lib().hoc_grad_clip(src._h, dst._h, C.byref(C.c_float(max_norm)), _ptr(_typed(norm, ("float32",), "norm"), 4, "norm"),
-                               _ptr(_typed(workspace, ("int32",), "workspace"), 0, "workspace"),
+    _check(lib().hoc_grad_clip(src._h, dst._h, C.byref(C.c_float(max_norm)), _ptr(_typed(norm, "float32", "norm"), 4, "norm"),
+                               _ptr(_typed(workspace, "int32", "workspace"), 0, "workspace"),
                                int(workspace.numel()), _stream(stream)), "hoc_grad_clip")
 
 
