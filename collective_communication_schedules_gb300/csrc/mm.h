@@ -42,6 +42,12 @@ struct MmParams {
 };
 
 // Device helpers ------------------------------------------------------------
+// The rows [a, b) cut to a buffer of `cap` rows.
+__device__ __forceinline__ void mm_cut(int64_t cap, int64_t a, int64_t b, int64_t& lo, int64_t& n) {
+  lo = a < 0 ? 0 : (a < cap ? a : cap);
+  const int64_t hi = b < lo ? lo : (b < cap ? b : cap);
+  n = hi - lo;
+}
 // The row range of (rank buffer p, expert g, source s), cut to the buffer.
 __device__ __forceinline__ void mm_range(const MmParams& P, int p, int g, int s, int64_t& lo, int64_t& n) {
   const int64_t cap = P.cap[p];
@@ -51,10 +57,7 @@ __device__ __forceinline__ void mm_range(const MmParams& P, int p, int g, int s,
     return;
   }
   const int64_t* at = P.seg + int64_t(p) * (int64_t(P.sources) * P.experts + 1) + int64_t(s) * P.experts + g;
-  const int64_t a = at[0], b = at[1];
-  lo = a < 0 ? 0 : (a < cap ? a : cap);
-  const int64_t hi = b < lo ? lo : (b < cap ? b : cap);
-  n = hi - lo;
+  mm_cut(cap, at[0], at[1], lo, n);
 }
 
 // Fills, for every (rank buffer, expert) pair i of the launch, vrows[i]: its

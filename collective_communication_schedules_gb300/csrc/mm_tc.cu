@@ -49,6 +49,7 @@ constexpr uint32_t kTcOperand = 128 * 128;      // bytes of one operand of a sta
 constexpr uint32_t kTcStage = 2 * kTcOperand;
 constexpr int kTcFeatures = 256;                // of a pair's tile
 constexpr int kTcRows = 256;                    // at most, of a tile
+constexpr unsigned kTcPanel = 8;
 constexpr uint32_t kTcTmemColumns = 512;        // two accumulators of 256 columns
 constexpr uint64_t kTcWaitNs = 2000000000ull;
 
@@ -79,7 +80,10 @@ struct TcShared {
   uint32_t tmem;
   volatile int dead;
   int vrows[kMmMaxGroups];
-  unsigned tile0[kMmMaxGroups + 1];
+  unsigned tile0[kMmMaxGroups + 1];    // forward, dgrad: whole tiles of the pairs before
+  unsigned short order[kMmMaxGroups];  // forward, dgrad: pairs with a lower tile at their end; wgrad: all; most rows first
+  int key[256];                        // what the order goes by, while it is made
+  int lower;                           // forward, dgrad: how many of those
 };
 
 // ------------------------------------------------------------------ PTX
@@ -207,21 +211,82 @@ struct Tile {
   int steps;    // stages of the contraction
 };
 
+// The order of the tiles: whole ones first, pair by pair, then the lower tile that
+// ends a pair's rows, the one with the most rows first (wgrad: the tiles of the
+// pair with the most rows first).  Tiles of falling cost, dealt to the CTA pairs in
+// turn and every second time backwards, come out within 1 to 7 % of an even share
+// at the expert layer's Zipf(1.1) loads (in the given order and always forwards 2
+// to 25 %).
+__device__ __forceinline__ unsigned dealt(unsigned i, unsigned who, unsigned of) {
+  return i * of + (i & 1 ? of - 1 - who : who);
+}
+
+// Fills S->order and S->lower from S->vrows.  The whole CTA calls it.
+template <int MODE>
+__device__ __forceinline__ void order_pairs(const TcParams& T, TcShared* S) {
+  const int n = T.P.parts * T.P.groups;
+  auto key = [&](int i) { return MODE == kWgrad ? S->vrows[i] : S->vrows[i] % T.tile_rows; };
+  if (threadIdx.x == 0) S->lower = 0;
+  if (n <= 256)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) S->key[i] = key(i);
+  __syncthreads();
+  if (n <= 256) {  // rank of each pair by counting; beyond that the sort would cost more than it gains
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int mine = S->key[i];
+      int before = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) before += S->key[j] > mine || (S->key[j] == mine && j < i);
+      S->order[before] = static_cast<unsigned short>(i);
+      if (mine > 0) atomicAdd(&S->lower, 1);
+    }
+  } else if (threadIdx.x < 32) {
+    int at = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + int(threadIdx.x);
+      const bool take = i < n && (MODE == kWgrad || key(i) > 0);
+      const unsigned some = __ballot_sync(0xFFFFFFFFu, take);
+      if (take) S->order[at + __popc(some & ((1u << threadIdx.x) - 1u))] = static_cast<unsigned short>(i);
+      at += __popc(some);
+    }
+    if (threadIdx.x == 0) S->lower = at;
+  }
+  __syncthreads();
+}
+
 template <int MODE>
 __device__ __forceinline__ Tile tile_at(const TcParams& T, const TcShared* S, unsigned t) {
   const MmParams& P = T.P;
-  const int i = mm_find(S->tile0, P.parts * P.groups, t);
+  const int n = P.parts * P.groups;
+  const bool gated = MODE == kForward && P.act == HOC_ACT_SWIGLU;
+  const int ftile = gated ? kTcFeatures / 2 : kTcFeatures;
+  const unsigned ftiles = ((MODE == kForward ? P.out : P.in) + ftile - 1) / ftile;
+  unsigned i, ct, ft;
+  if (MODE == kWgrad) {
+    const unsigned ctiles = (P.out + T.tile_rows - 1) / T.tile_rows, each = ctiles * ftiles;
+    i = S->order[t / each];
+    ct = t % each % ctiles;
+    ft = t % each / ctiles;
+  } else if (t < S->tile0[n]) {
+    i = mm_find(S->tile0, n, t);
+    // panels of 8 row tiles, so that the tiles in flight share rows and features about evenly
+    const unsigned lt = t - S->tile0[i], whole = (S->tile0[i + 1] - S->tile0[i]) / ftiles;
+    const unsigned panel = lt / (kTcPanel * ftiles), in_panel = lt - panel * kTcPanel * ftiles;
+    const unsigned high = min(kTcPanel, whole - panel * kTcPanel);
+    ct = panel * kTcPanel + in_panel % high;
+    ft = in_panel / high;
+  } else {
+    const unsigned u = t - S->tile0[n];
+    i = S->order[u / ftiles];
+    ct = (S->tile0[i + 1] - S->tile0[i]) / ftiles;
+    ft = u % ftiles;
+  }
   Tile A;
   A.p = P.part0 + i / P.groups;
   A.g = P.group0 + i % P.groups;
-  const unsigned lt = t - S->tile0[i];
+  A.f0 = int(ft) * ftile;
+  A.c0 = int(ct) * T.tile_rows;
   const int rows = S->vrows[i];
-  const int per = T.tile_rows, extent = MODE == kWgrad ? P.out : rows;
-  const unsigned ctiles = (extent + per - 1) / per;
-  const bool gated = MODE == kForward && P.act == HOC_ACT_SWIGLU;
-  A.f0 = int(lt / ctiles) * (gated ? kTcFeatures / 2 : kTcFeatures);
-  A.c0 = int(lt % ctiles) * per;
-  A.n = (min(per, extent - A.c0) + 31) / 32 * 32;
+  A.n = (min(T.tile_rows, (MODE == kWgrad ? P.out : rows) - A.c0) + 31) / 32 * 32;
   A.steps = ((MODE == kForward ? P.in : MODE == kDgrad ? P.out : rows) + kTcDepth - 1) / kTcDepth;
   return A;
 }
@@ -234,11 +299,24 @@ __device__ __forceinline__ Tile tile_at(const TcParams& T, const TcShared* S, un
 struct Ranges {
   int lo, n, start, rest, wholes, all;
 };
+// What a lane reads for it: issued a tile ahead, so that nothing waits for it.
+struct Ends {
+  int64_t from, to;
+};
+__device__ __forceinline__ Ends load_ends(const MmParams& P, int p, int g, int base) {
+  const int s = base + int(threadIdx.x & 31);
+  Ends E{0, P.seg == nullptr && s == 0 ? P.cap[p] : 0};
+  if (P.seg != nullptr && s < P.sources) {
+    const int64_t* at = P.seg + int64_t(p) * (int64_t(P.sources) * P.experts + 1) + int64_t(s) * P.experts + g;
+    E = {at[0], at[1]};
+  }
+  return E;
+}
 template <int PAD>
-__device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, int g, int base) {
-  const int lane = threadIdx.x & 31, s = base + lane;
-  int64_t lo = 0, n = 0;
-  if (s < (P.seg ? P.sources : 1)) mm_range(P, p, g, s, lo, n);
+__device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, Ends E) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo, n;
+  mm_cut(P.cap[p], E.from, E.to, lo, n);
   Ranges R;
   R.lo = int(lo);
   R.n = int(n);
@@ -268,7 +346,7 @@ __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges
   row = int(P.cap[p]);
   left = 0;
   for (int base = 0; base < ns; base += 32) {
-    if (ns > 32) R = load_ranges<PAD>(P, p, g, base);
+    if (ns > 32) R = load_ranges<PAD>(P, p, load_ends(P, p, g, base));
     // whole multiples of PAD, or what remains (for PAD 64 all lanes alike: their v share a multiple of 64)
     const bool whole = PAD > 8 && v < R.wholes;
     const int key = whole ? R.start : R.rest;
@@ -287,6 +365,50 @@ __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges
     v -= R.all;  // negative once it was found
   }
 }
+
+// The tiles of one CTA pair, as each warp walks them.  The lanes work out 32 tiles
+// at a time, one each (a tile takes several divisions, which between two tiles
+// would cost as much as a stage's products), and what a warp reads to find a tile's
+// rows is read a tile ahead.
+struct Work {
+  const TcParams& T;
+  const TcShared* S;
+  unsigned who, of, tiles, i = 0;
+  bool more = false, ahead_more = false;
+  Tile now, ahead, mine;
+  Ends ends, ahead_ends;
+  __device__ __forceinline__ Work(const TcParams& t, const TcShared* s, unsigned w, unsigned o, unsigned n)
+      : T(t), S(s), who(w), of(o), tiles(n) {}
+  template <int MODE>
+  __device__ __forceinline__ void look_ahead(bool rows = true) {
+    const unsigned at = i & 31;
+    if (at == 0) {
+      const unsigned t = dealt(i + (threadIdx.x & 31), who, of);
+      mine.n = 0;
+      if (t < tiles) mine = tile_at<MODE>(T, S, t);
+      __syncwarp();
+    }
+    ++i;
+    ahead.n = __shfl_sync(0xFFFFFFFFu, mine.n, at);
+    ahead.p = __shfl_sync(0xFFFFFFFFu, mine.p, at);
+    ahead.g = __shfl_sync(0xFFFFFFFFu, mine.g, at);
+    ahead.f0 = __shfl_sync(0xFFFFFFFFu, mine.f0, at);
+    ahead.c0 = __shfl_sync(0xFFFFFFFFu, mine.c0, at);
+    ahead.steps = __shfl_sync(0xFFFFFFFFu, mine.steps, at);
+    ahead_more = ahead.n > 0;  // only the last round may be short
+    if (ahead_more && rows) ahead_ends = load_ends(T.P, ahead.p, ahead.g, 0);
+  }
+  __device__ __forceinline__ void next() {
+    more = ahead_more;
+    now = ahead;
+    ends = ahead_ends;
+  }
+  template <int MODE>
+  __device__ __forceinline__ void first() {
+    look_ahead<MODE>();
+    next();
+  }
+};
 
 // How 64 virtual rows, a group of 8 per lane modulo 8, are fetched: a run of groups
 // that follow one another in the buffer by copies of 64, 32, 16 and 8 rows, as the
@@ -642,19 +764,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int fcount = MODE == kForward ? P.out : P.in;
   const int ftile = gated ? kTcFeatures / 2 : kTcFeatures;
-  const unsigned ftiles = (fcount + ftile - 1) / ftile;
-  mm_count(P, MODE == kWgrad ? kTcDepth : 8, S->vrows, S->tile0, [&](int rows) {
-    const int extent = MODE == kWgrad ? P.out : rows;
-    return unsigned((extent + T.tile_rows - 1) / T.tile_rows) * ftiles;
-  });
+  const unsigned ftiles = ((MODE == kForward ? P.out : P.in) + ftile - 1) / ftile;
+  mm_count(P, MODE == kWgrad ? kTcDepth : 8, S->vrows, S->tile0,
+           [&](int rows) { return MODE == kWgrad ? 0u : unsigned(rows / T.tile_rows) * ftiles; });
+  order_pairs<MODE>(T, S);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = S->tmem;
-  const unsigned tiles = S->tile0[P.parts * P.groups];
-  const unsigned first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  const unsigned tiles = MODE == kWgrad ? unsigned(P.parts * P.groups) * ftiles * ((P.out + T.tile_rows - 1) / T.tile_rows)
+                                        : S->tile0[P.parts * P.groups] + unsigned(S->lower) * ftiles;
+  const unsigned who = blockIdx.x >> 1, of = gridDim.x >> 1;
 
   if (warp == 0 || (MODE != kWgrad && warp == 2)) {
     // ---- tensor copies of the rows.  The whole warp walks the stages, so that
@@ -666,9 +787,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     // Waits until the MMAs have released the stage's last filling.
     auto free = [&]() { return k.round == 0 || warp_wait(&S->empty[k.st], (k.round - 1) & 1, T, S); };
-    for (unsigned t = first; ok && t < tiles; t += stride) {
-      const Tile A = tile_at<MODE>(T, S, t);
-      const Ranges R = load_ranges<MODE == kWgrad ? kTcDepth : 8>(P, A.p, A.g, 0);
+    Work W(T, S, who, of, tiles);
+    for (W.first<MODE>(); ok && W.more; W.next()) {
+      const Tile& A = W.now;
+      const Ranges R = load_ranges<MODE == kWgrad ? kTcDepth : 8>(P, A.p, W.ends);
+      W.look_ahead<MODE>();
       const int half = A.n / 2;  // rows of B in this CTA (wgrad: features)
       if (MODE != kWgrad) {
         // This warp's 64 rows of B, a group of 8 per lane modulo 8
@@ -743,8 +866,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     const uint32_t full0 = on_first(&S->full[0]);
     Turn k(T.stages);
     bool ok = true;
-    for (unsigned t = first; ok && t < tiles; t += stride) {
-      const Tile A = tile_at<MODE>(T, S, t);
+    Work W(T, S, who, of, tiles);
+    for (W.first<MODE>(); ok && W.more; W.next()) {
+      const Tile& A = W.now;
+      W.look_ahead<MODE>(false);
       const int fa = A.f0 + rank * (gated ? 64 : 128);
       for (int s = 0; s < A.steps; ++s, k.next()) {
         if (k.round && !warp_wait(&S->empty[k.st], (k.round - 1) & 1, T, S)) {
@@ -777,8 +902,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                           (MODE == kWgrad ? 1u << 16 : 0u) | (uint32_t(kTcFeatures / 16) << 24);
     const uint64_t a0 = MODE == kForward ? smem_desc(base, 16, 1024) : smem_desc(base, 8192, 1024);
     const uint64_t b0 = MODE == kWgrad ? smem_desc(base + kTcOperand, 8192, 1024) : smem_desc(base + kTcOperand, 16, 1024);
-    for (unsigned t = first; ok && t < tiles; t += stride) {
-      const Tile A = tile_at<MODE>(T, S, t);
+    Work W(T, S, who, of, tiles);
+    for (W.first<MODE>(); ok && W.more; W.next()) {
+      const Tile& A = W.now;
+      if (A.steps == 0) W.look_ahead<MODE>(false);
       if (A.steps == 0) continue;  // an expert without rows: the epilogue writes zeros
       const uint32_t idesc = kind | (uint32_t(A.n / 8) << 17);
       const uint32_t acc = it & 1, d = tmem + acc * 256u;
@@ -798,6 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           commit_pair(&S->empty[k.st]);
         }
         __syncwarp();
+        if (s == 0) W.look_ahead<MODE>(false);  // under the first stage's products
       }
       if (ok && one) commit_pair(&S->acc_full[acc]);
       __syncwarp();
@@ -812,9 +940,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     Turn k(T.stages);
     uint32_t phases = 0;  // bit st: parity of part[st]
     bool ok = true;
-    for (unsigned t = first; ok && t < tiles; t += stride) {
-      const Tile A = tile_at<MODE>(T, S, t);
-      const Ranges R = load_ranges<kTcDepth>(P, A.p, A.g, 0);
+    Work W(T, S, who, of, tiles);
+    for (W.first<MODE>(); ok && W.more; W.next()) {
+      const Tile& A = W.now;
+      const Ranges R = load_ranges<kTcDepth>(P, A.p, W.ends);
+      W.look_ahead<MODE>();
       for (int s = 0; s < A.steps;) {
         int row, valid;
         const int run = stage_rows(P, A, R, s, row, valid);
@@ -853,19 +983,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     unsigned char* in = planes + eg * kGroupPlanes<MODE> * kTcPlane;
     unsigned char* out = MODE == kForward ? in + 3 * kTcPlane : in;
     uint32_t it = 0, turn = 0, buffer = 0;
-    for (unsigned t = first; t < tiles; t += stride) {
-      const Tile A = tile_at<MODE>(T, S, t);
+    Work W(T, S, who, of, tiles);
+    for (W.first<MODE>(); W.more; W.next()) {
+      const Tile& A = W.now;
       int row = 0, valid = 0;
       float bias = 0.f;
       if (MODE != kWgrad) {
-        group_at<8>(P, A.p, A.g, load_ranges<8>(P, A.p, A.g, 0), A.c0 + lane * 8, row, valid);
+        group_at<8>(P, A.p, A.g, load_ranges<8>(P, A.p, W.ends), A.c0 + lane * 8, row, valid);
         valid = lane * 8 < T.tile_rows ? min(valid, 8) : 0;  // past them: the next tile's rows
         const int f = gated ? A.f0 + rank * 64 + q * 16 + (lane & 15) : A.f0 + rank * 128 + q * 32 + lane;
         if (MODE == kForward && P.bias[A.p] && f < P.out)
           bias = bf16_of(P.bias[A.p] + int64_t(A.g) * (gated ? 2 : 1) * P.out + (gated && lane >= 16 ? P.out : 0) + f);
-      } else if (A.steps == 0 && P.accumulate) {
-        continue;  // an expert without rows adds nothing
       }
+      W.look_ahead<MODE>(MODE != kWgrad);
+      if (MODE == kWgrad && A.steps == 0 && P.accumulate) continue;  // an expert without rows adds nothing
       const uint32_t acc = it & 1;
       const uint32_t at = tmem + acc * 256u + (uint32_t(q * 32) << 16);
       bool ok = true;
