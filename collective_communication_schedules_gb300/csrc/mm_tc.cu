@@ -92,9 +92,8 @@ __device__ __forceinline__ uint32_t cta_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address, in the cluster's shared memory, of the first CTA's copy of a local barrier.
 __device__ __forceinline__ uint32_t on_first(const uint64_t* bar) {
   uint32_t a;
@@ -226,6 +225,14 @@ template <int MODE>
 __device__ __forceinline__ void order_pairs(const TcParams& T, TcShared* S) {
   const int n = T.P.parts * T.P.groups;
   auto key = [&](int i) { return MODE == kWgrad ? S->vrows[i] : S->vrows[i] % T.tile_rows; };
+  if (n == 1) {
+    if (threadIdx.x == 0) {
+      S->order[0] = 0;
+      S->lower = key(0) > 0;
+    }
+    __syncthreads();
+    return;
+  }
   if (threadIdx.x == 0) S->lower = 0;
   if (n <= 256)
     for (int i = threadIdx.x; i < n; i += blockDim.x) S->key[i] = key(i);
@@ -762,6 +769,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     if (P.cap[P.part0 + lane] > 0) prefetch(&T.row[P.part0 + lane][3]);
     if (MODE == kWgrad && P.cap[P.part0 + lane] > 0) prefetch(&T.dy[P.part0 + lane][3]);
   }
+  // The other CTA's barriers are first used after the wait below.
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncwarp();
+  cluster_arrive();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int ftile = gated ? kTcFeatures / 2 : kTcFeatures;
@@ -769,8 +780,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   mm_count(P, MODE == kWgrad ? kTcDepth : 8, S->vrows, S->tile0,
            [&](int rows) { return MODE == kWgrad ? 0u : unsigned(rows / T.tile_rows) * ftiles; });
   order_pairs<MODE>(T, S);
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  cluster_sync();
+  __syncwarp();
+  cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = S->tmem;
   const unsigned tiles = MODE == kWgrad ? unsigned(P.parts * P.groups) * ftiles * ((P.out + T.tile_rows - 1) / T.tile_rows)
@@ -1022,7 +1033,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  cluster_sync();
+  cluster_arrive();
+  cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == 2)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcTmemColumns));
