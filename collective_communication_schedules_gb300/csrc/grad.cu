@@ -4,10 +4,12 @@
 // passes are bound by their bytes: the first reads every element, the second
 // reads it again and writes it (the coefficient needs every element, so the
 // second read can only be saved where L2 still holds the data; the second pass
-// therefore walks the tiles backwards, starting with those read last).  Two
-// launches: the first leaves one binary64 partial sum per CTA, and every CTA of
-// the second adds them all up itself, in the same order, instead of a launch
-// or a grid barrier in between.
+// therefore walks the tiles backwards, starting with those read last).  The first
+// pass leaves one binary64 partial sum per CTA.  Few tiles: every CTA of the second
+// pass adds the partial sums up itself, in the same order, which saves a launch.
+// Many tiles: one CTA adds them up in a launch between the passes, and the second
+// pass has one CTA per tile, handed out as SMs become free (32 tensors of 13.1 M
+// bf16: 378 us, against 405 us with a fixed share of the tiles per CTA).
 #include <cstdio>
 #include <new>
 #include <vector>
@@ -35,11 +37,11 @@ namespace {
 
 using Tile = hocTensorList::Tile;
 
-constexpr int kGradThreads = 512;
+constexpr int kGradThreads = 256;
 constexpr int kGradUnroll = 4;          // 16-byte loads a thread has in flight
-constexpr size_t kTileMost = 16384;     // elements: with 32768, 12800 tiles on 608 CTAs left 4 % of them idle in the last round
+constexpr size_t kTileMost = 8192;      // elements: one set of a thread's bf16 loads
 constexpr size_t kTileLeast = 2048;
-constexpr int kGradCtas = 152 * 4;      // at most: partial sums in the workspace
+constexpr int kGradCtas = 152 * 8;      // at most: partial sums in the workspace
 
 template <class T>
 __device__ __forceinline__ float widen(T v);
@@ -135,6 +137,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const double* _
   if (threadIdx.x == 0) *norm = v;
 }
 
+// partial: the first pass's n partial sums, of which this kernel makes the norm; or
+// null where norm holds it already.
 template <class T>
 __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const Tile* src, const Tile* dst, uint64_t ntiles,
                                                                   const double* __restrict__ partial, int n,
@@ -143,8 +147,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const Tile* sr
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int V = 16 / sizeof(T);
   __shared__ float sh;
-  const float nv = norm_of(partial, n, &sh);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
+  const float nv = partial ? norm_of(partial, n, &sh) : *norm;
+  if (partial && blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
   float c = max_norm / (nv + 1e-6f);
   if (c > 1.f) c = 1.f;  // NaN stays
   if ((in_place && c == 1.f) || blockIdx.x >= ntiles) return;
@@ -340,10 +344,14 @@ extern "C" hocResult_t hoc_grad_clip(const hocTensorList_t* src, const hocTensor
   const Tile *a = src->tiles, *b = dst->tiles;
   const uint64_t n = src->ntiles;
   const double* partial = reinterpret_cast<const double*>(workspace);
-  const int g = grid_of(src), same = src == dst;
-  const cudaError_t e = src->dtype == HOC_FLOAT32
-                            ? launch(grad_scale_kernel<float>, g, s, a, b, n, partial, g, *max_norm, norm, same)
-                            : launch(grad_scale_kernel<__nv_bfloat16>, g, s, a, b, n, partial, g, *max_norm, norm, same);
+  const int sums = grid_of(src), same = src == dst;
+  const bool few = n <= uint64_t(kGradCtas);
+  cudaError_t e = few ? cudaSuccess : launch(grad_norm_kernel, 1, s, partial, sums, norm);
+  if (!few) partial = nullptr;
+  const int g = few ? sums : int(n < (1u << 30) ? n : (1u << 30));
+  if (e == cudaSuccess)
+    e = src->dtype == HOC_FLOAT32 ? launch(grad_scale_kernel<float>, g, s, a, b, n, partial, sums, *max_norm, norm, same)
+                                  : launch(grad_scale_kernel<__nv_bfloat16>, g, s, a, b, n, partial, sums, *max_norm, norm, same);
   if (e == cudaSuccess) return HOC_SUCCESS;
   set_error_detail("hoc_grad_clip: launch failed");
   return HOC_ERR_CUDA;

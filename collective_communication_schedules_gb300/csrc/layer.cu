@@ -110,12 +110,15 @@ __global__ void act_grad_kernel(const __nv_bfloat16* dy, const __nv_bfloat16* pr
 // lanes x 8 columns (or, where rows are not whole 16-byte vectors, one row of 32
 // lanes x 2 columns).  Binary32 sums; lanes, warps and CTAs are added in a fixed
 // order.  With one CTA for the 64 columns the 4096 x 4096 gradient took 31 us.
-constexpr int kBiasWarps = 16;
+// Launched right behind the product (programmatic dependent launch), it runs beside
+// it: it needs nothing of it, and what both need was complete when the product's
+// CTAs, which let it start, had passed their own wait.  Every kernel that is
+// launched before it therefore waits before it lets dependents start.
+constexpr int kBiasWarps = 8;
 constexpr int kBiasCtas = 8;
 template <bool VEC>
 __global__ void __cluster_dims__(1, 1, kBiasCtas) __launch_bounds__(32 * kBiasWarps)
     bias_grad_kernel(const __grid_constant__ MmParams P) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float sums[kBiasWarps][64];
   __shared__ float mine[64];
   const int i = blockIdx.y, p = P.part0 + i / P.groups, g = P.group0 + i % P.groups;
@@ -184,6 +187,8 @@ __global__ void __cluster_dims__(1, 1, kBiasCtas) __launch_bounds__(32 * kBiasWa
     }
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // Whatever follows on the stream waits for this grid; so this grid waits for the product's.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------ host
@@ -302,9 +307,16 @@ hocResult_t run_wgrad(const char* who, MmParams& P, void* const* db, cudaStream_
       Q.parts = P.parts - p;
       Q.groups = P.groups;
     }
-    const dim3 grid((P.out + 63) / 64, Q.parts * Q.groups, kBiasCtas);
-    if (vec) bias_grad_kernel<true><<<grid, 32 * kBiasWarps, 0, s>>>(Q);
-    else bias_grad_kernel<false><<<grid, 32 * kBiasWarps, 0, s>>>(Q);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((P.out + 63) / 64, Q.parts * Q.groups, kBiasCtas);
+    cfg.blockDim = dim3(32 * kBiasWarps);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, vec ? bias_grad_kernel<true> : bias_grad_kernel<false>, Q) != cudaSuccess) break;
     at += Q.parts * Q.groups;
   }
   if (cudaGetLastError() != cudaSuccess) {
