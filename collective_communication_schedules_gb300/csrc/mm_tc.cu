@@ -58,6 +58,7 @@ struct TcParams {
   int tile_rows;     // most rows c of a tile, a multiple of 32
   uint32_t stage;    // bytes of a stage: 128 x 64 of A, half of tile_rows x 64 of B
   uint32_t stages;
+  int loose;         // what the epilogue moves is not whole 16-byte vectors
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
   uint64_t wait_ns;
   CUtensorMap w[kMaxRanks];                      // forward, dgrad
@@ -477,7 +478,13 @@ struct Strip {
   char* at;        // feature f0 of row 0
   int64_t pitch;   // bytes of a row
   int left;        // features from f0 to the end of a row
+  bool loose;      // rows are not whole 16-byte vectors: moved value by value
 };
+// The first `left` of 8 values, one by one.
+__device__ __forceinline__ void put_loose(char* to, const unsigned char* from, int left) {
+  for (int e = 0; e < 8; ++e)
+    if (e < left) *reinterpret_cast<uint16_t*>(to + e * 2) = *reinterpret_cast<const uint16_t*>(from + e * 2);
+}
 
 constexpr uint32_t kTcRowBytes = 256;
 constexpr uint32_t kTcPlane = kTcColumns * kTcRowBytes;  // one staged array
@@ -519,6 +526,16 @@ struct Rows {
 template <int CHUNKS>
 __device__ __forceinline__ void fetch_rows(uint32_t smem, const Strip& G, const Rows<CHUNKS>& R) {
   const int i = int(threadIdx.x) & 127, v = i % CHUNKS;
+  if (G.loose) {
+#pragma unroll
+    for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h)
+      for (int e = 0; e < 8; ++e)
+        if (R.r[h] >= 0 && v * 8 + e < G.left) {
+          const uint16_t x = *reinterpret_cast<const uint16_t*>(G.at + R.r[h] * G.pitch + (v * 8 + e) * 2);
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(smem + uint32_t(i + 128 * h) * 16u + e * 2), "h"(x) : "memory");
+        }
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h)
     if (R.r[h] >= 0 && v * 8 < G.left)
@@ -529,6 +546,12 @@ __device__ __forceinline__ void fetch_rows(uint32_t smem, const Strip& G, const 
 template <int CHUNKS>
 __device__ __forceinline__ void put_rows(const unsigned char* smem, const Strip& G, const Rows<CHUNKS>& R) {
   const int i = int(threadIdx.x) & 127, v = i % CHUNKS;
+  if (G.loose) {
+#pragma unroll
+    for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h)
+      put_loose(G.at + R.r[h] * G.pitch + v * 16, smem + (i + 128 * h) * 16, R.r[h] >= 0 ? G.left - v * 8 : 0);
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < kTcColumns * CHUNKS / 128; ++h)
     if (R.r[h] >= 0 && v * 8 < G.left)
@@ -565,12 +588,12 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
   const bool reads = res || (MODE == kDgrad && ACT != HOC_ACT_NONE);
   // clamped so that no pointer is formed past the tensors
   const int left = width - f0, fs = left > 0 ? f0 : 0;
-  const Strip y{static_cast<char*>(P.y[A.p]) + 2 * int64_t(fs), 2 * P.ld_y, left};
+  const Strip y{static_cast<char*>(P.y[A.p]) + 2 * int64_t(fs), 2 * P.ld_y, left, T.loose != 0};
   Strip beside{};
-  if (res) beside = {reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.res[A.p])) + 2 * int64_t(fs), 2 * P.ld_res, left};
+  if (res) beside = {reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.res[A.p])) + 2 * int64_t(fs), 2 * P.ld_res, left, T.loose != 0};
   if (MODE == kDgrad && ACT != HOC_ACT_NONE)
-    beside = {reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.pre[A.p])) + 2 * int64_t(fs), 2 * wide, left};
-  const Strip kept{static_cast<char*>(P.pre_out[A.p]) + 2 * int64_t(fs), 2 * wide, left};
+    beside = {reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.pre[A.p])) + 2 * int64_t(fs), 2 * wide, left, T.loose != 0};
+  const Strip kept{static_cast<char*>(P.pre_out[A.p]) + 2 * int64_t(fs), 2 * wide, left, T.loose != 0};
   auto second = [&](Strip s) {
     s.at += 2 * int64_t(width);
     return s;
@@ -642,7 +665,7 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
 #pragma unroll
         for (int j = 0; j < kTcColumns; ++j) put_bf16(o + j * kTcRowBytes + (q * 32 + lane) * 2, __uint_as_float(v[j]));
         group_barrier(eg);
-        const Strip w{static_cast<char*>(P.y[A.p]) + 2 * (int64_t(A.g) * P.out * P.in + fs), 2 * int64_t(P.in), left};
+        const Strip w{static_cast<char*>(P.y[A.p]) + 2 * (int64_t(A.g) * P.out * P.in + fs), 2 * int64_t(P.in), left, T.loose != 0};
         put_rows(o, w, Rows<16>([&](int c) { return c0 + c < P.out ? int64_t(c0 + c) : int64_t(-1); }));
       }
     } else if constexpr (gated) {
@@ -663,9 +686,10 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
           const int c = (i + 128 * h) / 16, u = (i + 128 * h) % 8;
           const bool value = (i + 128 * h) % 16 >= 8;
           const int64_t r = at(c);
-          if (r >= 0 && u * 8 < left)
-            *reinterpret_cast<uint4*>(kept.at + r * kept.pitch + (value ? 2 * int64_t(width) : 0) + u * 16) =
-                *reinterpret_cast<const uint4*>(o + c * kTcRowBytes + (value ? 128 + ((u * 16) ^ 32) : u * 16));
+          char* to = kept.at + r * kept.pitch + (value ? 2 * int64_t(width) : 0) + u * 16;
+          const unsigned char* from = o + c * kTcRowBytes + (value ? 128 + ((u * 16) ^ 32) : u * 16);
+          if (T.loose) put_loose(to, from, r >= 0 ? left - u * 8 : 0);
+          else if (r >= 0 && u * 8 < left) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
         }
       }
       // The halves of a warp swap: each lane then has gate and value of 8 of the 16 columns.
@@ -1079,14 +1103,14 @@ bool encode_rows(CUtensorMap* m, const void* at, int64_t width, int64_t rows, in
 }
 
 bool encode_weight(CUtensorMap* m, const MmParams& P, int mode, const void* at) {
-  const cuuint64_t in = P.in, out = P.out, ne = P.experts;
+  const cuuint64_t in = P.in, out = P.out, ld = P.ld_w, rows = P.out_w, ne = P.experts;
   if (mode == kForward && P.act == HOC_ACT_SWIGLU) {
     // [expert][gate, value][out / 16][16][in], fetched so that 16 gates and their 16 values alternate
-    const cuuint64_t dims[5] = {in, 16, 2, out / 16, ne}, strides[4] = {in, out * in, 16 * in, 2 * out * in};
+    const cuuint64_t dims[5] = {in, 16, 2, rows / 16, ne}, strides[4] = {ld, rows * ld, 16 * ld, 2 * rows * ld};
     const cuuint32_t box[5] = {kTcDepth, 16, 2, 4, 1};
     return encode(m, at, 5, dims, strides, box);
   }
-  const cuuint64_t dims[3] = {in, out, ne}, strides[2] = {in, out * in};
+  const cuuint64_t dims[3] = {in, out, ne}, strides[2] = {ld, rows * ld};
   const cuuint32_t box[3] = {kTcDepth, mode == kForward ? 128u : 64u, 1};
   return encode(m, at, 3, dims, strides, box);
 }
@@ -1100,22 +1124,6 @@ int choose_rows_ragged(const MmParams& P) {
   for (int p = P.part0; p < P.part0 + P.parts; ++p) rows += P.cap[p];
   const int64_t each = rows / P.parts / P.experts;
   return each <= 32 ? 64 : each <= 64 ? 128 : kTcRows;
-}
-
-}  // namespace
-
-bool mm_tc_takes(const MmParams& P, int mode) {
-  const bool gated = mode == kForward && P.act == HOC_ACT_SWIGLU;
-  if (P.in % 8 || P.out % (gated ? 16 : 8) || P.ld_rows % 8 || P.ld_y % 8 || (mode == kWgrad && P.ld_dy % 8)) return false;
-  uintptr_t at = 0;
-  for (int p = 0; p < P.parts; ++p) {
-    at |= reinterpret_cast<uintptr_t>(P.rows[p]) | reinterpret_cast<uintptr_t>(P.dy[p]) |
-          reinterpret_cast<uintptr_t>(P.w[p]) | reinterpret_cast<uintptr_t>(P.y[p]) | reinterpret_cast<uintptr_t>(P.pre[p]) |
-          reinterpret_cast<uintptr_t>(P.res[p]);
-    if (mode == kForward) at |= reinterpret_cast<uintptr_t>(P.pre_out[p]);
-    if (P.res[p] && P.ld_res % 8) return false;
-  }
-  return (at & 15u) == 0 && encoder() != nullptr;
 }
 
 // The launch but for its grid and stream, and the CTA pairs that fit the device at
@@ -1166,10 +1174,35 @@ int choose_rows(int64_t rows, int64_t others, int pairs) {
   return best;
 }
 
+}  // namespace
+
+bool mm_tc_takes(const MmParams& P, int mode) {
+  const bool gated = mode == kForward && P.act == HOC_ACT_SWIGLU;
+  if (P.ld_rows % 8 || (mode == kWgrad ? P.ld_dy % 8 : P.ld_w % 8) || (gated && P.out_w % 16)) return false;
+  uintptr_t at = 0;
+  for (int p = 0; p < P.parts; ++p)
+    at |= reinterpret_cast<uintptr_t>(P.rows[p]) | reinterpret_cast<uintptr_t>(P.dy[p]) | reinterpret_cast<uintptr_t>(P.w[p]);
+  return (at & 15u) == 0 && encoder() != nullptr;
+}
+
+// Whether a row that the epilogue reads or writes is not whole 16-byte vectors.
+static bool is_loose(const MmParams& P, int mode) {
+  const int width = mode == kForward ? P.out : P.in;
+  if (width % 8 || P.ld_y % 8) return true;
+  uintptr_t at = 0;
+  for (int p = 0; p < P.parts; ++p) {
+    at |= reinterpret_cast<uintptr_t>(P.y[p]) | reinterpret_cast<uintptr_t>(P.pre[p]) | reinterpret_cast<uintptr_t>(P.res[p]);
+    if (mode == kForward) at |= reinterpret_cast<uintptr_t>(P.pre_out[p]);
+    if (P.res[p] && P.ld_res % 8) return true;
+  }
+  return (at & 15u) != 0;
+}
+
 cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   TcParams T;
   T.P = P;
   T.tile_rows = kTcRows;
+  T.loose = is_loose(P, mode);
   const char* fault = getenv("HOC_FAULT");
   const bool stall = fault && !strcmp(fault, "mm_stall");
   T.tx_pad = stall ? 16u : 0u;

@@ -14,8 +14,14 @@
  *     linear values after them: [experts, 2 * out, in].
  *   - `status` is a device int32; bit 2 (value 4) is set, never cleared, if a
  *     bounded wait inside a kernel gave up (the results are then undefined).
- *   - Everything is stream-ordered, allocates nothing, never waits on the host
- *     and may be captured into a CUDA graph after one call of the same kind.
+ *   - Everything is stream-ordered, never waits on the host and may be captured
+ *     into a CUDA graph after one call of the same kind.
+ *   - Rows of x, dy and the weights that start on 16-byte boundaries (widths and
+ *     strides that are multiples of 8, aligned pointers) run as they lie, with
+ *     no memory beside the arguments'.  For other rows, products above a small
+ *     size copy the operands into scratch that the call allocates and frees in
+ *     stream order from a memory pool of this library's own, which keeps what it
+ *     was given; where no scratch is to be had a slower kernel runs.
  *   - Inputs must not overlap outputs, except as stated.
  */
 #ifndef HOC_LAYER_H

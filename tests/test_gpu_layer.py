@@ -430,3 +430,92 @@ def test_a_wait_that_runs_out_sets_the_status(product, monkeypatch):
     got, want = {"forward": (y, x.double() @ w.double().t()), "dgrad": (dx, dy.double() @ w.double()),
                  "wgrad": (dw, dy.double().t() @ x.double())}[product]
     assert float((got.double() - want).norm() / want.norm()) < 2 * ref.BF16
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("rows,inp,out", [(600, 333, 129), (300, 328, 131), (257, 515, 264), (9, 2049, 1031), (20, 1030, 2051),
+                                          (130, 514, 250)])
+def test_rows_that_are_not_whole_vectors(rows, inp, out, act):
+    """Products large enough to run on realigned copies of their operands, with epilogue rows of any alignment."""
+    mul = 2 if act == "swiglu" else 1
+    x, dy = normal(rows, inp + 3, seed=1)[:, 1: 1 + inp], normal(rows, out + 1, seed=2)[:, :out]
+    w, b, r = normal(mul * out, inp, seed=3, sigma=inp ** -0.5), normal(mul * out, seed=4), normal(rows, out + 5, seed=5)[:, 2: 2 + out]
+    ybig = torch.full((rows, out + 3), 7.0, dtype=BF, device=DEV)
+    y, pre, st = ybig[:, 1: 1 + out], torch.empty(rows, mul * out, dtype=BF, device=DEV), status()
+    hoc.linear(x, w, y, status=st, bias=b, act=act, pre=pre, residual=r)
+    wd, prd = normal(out, inp, seed=6, sigma=inp ** -0.5), normal(rows, mul * inp, seed=7)
+    dx = torch.empty(rows, mul * inp, dtype=BF, device=DEV)
+    hoc.linear_dgrad(dy, wd, dx, status=st, act=act, pre=prd if act != "none" else None)
+    old = normal(out, inp, seed=8)
+    dw, dwf, db = old.clone(), torch.empty(out, inp, device=DEV), torch.zeros(out, dtype=BF, device=DEV)
+    hoc.linear_wgrad(dy, x, dw, status=st, db=db, accumulate=True)
+    hoc.linear_wgrad(dy, x, dwf, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert bool((ybig[:, 0] == 7).all()) and bool((ybig[:, 1 + out:] == 7).all()), "written outside the rows"
+    z, ez, want, ey = ref.forward(x, w, b, act)
+    ref.close(pre, z, ez, "pre")
+    want = want + r.double()
+    ref.close(y, want, ey + want.abs() * ref.F32, "y")
+    want, err = ref.dgrad(dy, wd, act, prd)
+    ref.close(dx, want, err, "dx")
+    a, v = dy.double(), x.double()
+    ew = (a.abs().t() @ v.abs()) * rows * ref.F32
+    ref.close(dwf, a.t() @ v, ew, "dw", ref.F32)
+    want = a.t() @ v + old.double()
+    ref.close(dw, want, ew + want.abs() * ref.F32, "dw added")
+    ref.close(db, a.sum(0), a.abs().sum(0) * rows * ref.F32, "db")
+
+
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+def test_expert_rows_that_are_not_whole_vectors(act):
+    """The same for expert products: two ranks, two sources, an expert without rows, NaN rows that belong to nobody."""
+    mul = 2 if act == "swiglu" else 1
+    inp, out = 307, 205
+    L = ref.Routed([[[70, 0, 33], [5, 0, 100]], [[1, 64, 9], [200, 8, 0]]])
+    x = [normal(n, inp, seed=1 + d) for d, n in enumerate(L.cap)]
+    dy = [normal(n, out, seed=3 + d) for d, n in enumerate(L.cap)]
+    for d in range(2):
+        x[d][L.of[d] < 0] = dy[d][L.of[d] < 0] = float("nan")
+    w = [normal(3, mul * out, inp, seed=5 + d, sigma=inp ** -0.5) for d in range(2)]
+    wd = [normal(3, out, inp, seed=7 + d, sigma=inp ** -0.5) for d in range(2)]
+    prd = [normal(n, mul * inp, seed=9 + d) for d, n in enumerate(L.cap)]
+    y = [torch.full((n, out), 7.0, dtype=BF, device=DEV) for n in L.cap]
+    dx = [torch.full((n, mul * inp), 7.0, dtype=BF, device=DEV) for n in L.cap]
+    dw = [torch.full((3, out, inp), 7.0, dtype=BF, device=DEV) for _ in range(2)]
+    st = status()
+    hoc.expert_mm(x, w, L.seg, y, status=st, act=act)
+    hoc.expert_mm_dgrad(dy, wd, L.seg, dx, status=st, act=act, pre=prd)
+    hoc.expert_mm_wgrad(dy, x, L.seg, dw, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for d in range(2):
+        assert bool((y[d][L.of[d] < 0] == 7).all()) and bool((dx[d][L.of[d] < 0] == 7).all())
+        for e in range(3):
+            r = L.rows(d, e)
+            a, v = dy[d][r].double(), x[d][r].double()
+            ref.close(dw[d][e], a.t() @ v, (a.abs().t() @ v.abs()) * max(1, len(r)) * ref.F32, f"dw {d} {e}")
+            if len(r):
+                _, _, want, ey = ref.forward(x[d][r], w[d][e], None, act)
+                ref.close(y[d][r], want, ey, f"y {d} {e}")
+                want, err = ref.dgrad(dy[d][r], wd[d][e], act, prd[d][r])
+                ref.close(dx[d][r], want, err, f"dx {d} {e}")
+
+
+def test_realigned_copies_in_a_graph():
+    n, inp, out = 300, 333, 129
+    x, w, st = normal(n, inp, seed=1), normal(out, inp, seed=2, sigma=inp ** -0.5), status()
+    y = torch.zeros(n, out, dtype=BF, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    hoc.linear(x, w, y, status=st, stream=s)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        hoc.linear(x, w, y, status=st, stream=s)
+    for seed in (9, 10):
+        x.copy_(normal(n, inp, seed=seed))
+        g.replay()
+        torch.cuda.synchronize()
+        _, _, want, err = ref.forward(x, w, None, "none")
+        ref.close(y, want, err, "replayed")
