@@ -27,7 +27,8 @@
 //
 // Warps of a CTA: 0 and 2 tensor copies of the rows, 64 each; 3 those of the
 // weights; 1 MMA (of the pair's first CTA); 4-11 epilogue.  In the weight gradient
-// warp 0 issues all copies and warps 2 and 3 zero padding rows.  Every wait is bounded: a wait that runs
+// warps 0 and 12 issue all copies of every second stage, and warps 2, 3 and 13-15
+// zero padding rows.  Every wait is bounded: a wait that runs
 // out sets bit 2 of the status, and all roles leave.
 #include <atomic>
 #include <cstdlib>
@@ -41,7 +42,8 @@
 namespace hoc {
 namespace {
 
-constexpr int kTcThreads = 384;
+template <int MODE>
+constexpr int kTcThreads = MODE == kWgrad ? 512 : 384;
 constexpr int kTcEpilogue = 8;                  // warps: two to each 32 lanes of tensor memory
 constexpr int kTcColumns = 16;                  // accumulator columns of an epilogue step
 constexpr int kTcDepth = 64;                    // contraction elements of a stage: one 128-byte swizzled row
@@ -201,7 +203,6 @@ __device__ __forceinline__ void tmem_load(uint32_t (&r)[kTcColumns], uint32_t ad
       : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-
 // ------------------------------------------------------------------ tiles
 // A tile of the launch, as every role derives it for itself.
 struct Tile {
@@ -612,23 +613,15 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
     fetch(first, buffer);
     fetch(first + 2 * kTcColumns, buffer == 2 ? 0 : buffer + 1);
   }
-  bool ok = true;
-  if (A.steps > 0) {
-    ok = warp_wait(acc_full, parity, T, S);
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  }
+  const bool ok = warp_wait(acc_full, parity, T, S);
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (!group_all(eg, ok)) {
     if (reads) asm volatile("cp.async.wait_all;" ::: "memory");
     return false;
   }
   for (int col = first; col < A.n; col += 2 * kTcColumns) {
     uint32_t v[kTcColumns];
-    if (MODE != kWgrad || A.steps > 0) {
-      tmem_load(v, acc_at + uint32_t(col));
-    } else {
-#pragma unroll
-      for (int j = 0; j < kTcColumns; ++j) v[j] = 0;
-    }
+    tmem_load(v, acc_at + uint32_t(col));
     auto at = [&](int c) { return row_of(col, c, row, valid); };
     unsigned char* x = in + buffer * kBuffer;
     if (reads) {
@@ -639,36 +632,7 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
     }
     // Where the arrays to be stored are staged: in the place of what was read, or in the next output plane.
     auto plane = [&]() { return reads ? x : out + (turn++ & 1) * kTcPlane; };
-    if constexpr (MODE == kWgrad) {  // columns are out features
-      const int c0 = A.c0 + col, f = f0 + q * 32 + lane;
-      const int64_t first_at = (int64_t(A.g) * P.out + c0) * P.in;
-      if (P.out_f32) {
-        float* o = static_cast<float*>(P.y[A.p]) + first_at + f;
-        float add[kTcColumns];
-#pragma unroll
-        for (int j = 0; j < kTcColumns; ++j)
-          add[j] = P.accumulate && f < P.in && c0 + j < P.out ? o[int64_t(j) * P.in] : 0.f;
-#pragma unroll
-        for (int j = 0; j < kTcColumns; ++j)
-          if (f < P.in && c0 + j < P.out) o[int64_t(j) * P.in] = add[j] + __uint_as_float(v[j]);
-      } else {
-        unsigned char* o = out + (turn++ & 1) * kTcPlane;
-        if (P.accumulate) {
-          const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(P.y[A.p]) + first_at + f;
-          float add[kTcColumns];
-#pragma unroll
-          for (int j = 0; j < kTcColumns; ++j)
-            add[j] = f < P.in && c0 + j < P.out ? bf16_of(w + int64_t(j) * P.in) : 0.f;
-#pragma unroll
-          for (int j = 0; j < kTcColumns; ++j) v[j] = __float_as_uint(add[j] + __uint_as_float(v[j]));
-        }
-#pragma unroll
-        for (int j = 0; j < kTcColumns; ++j) put_bf16(o + j * kTcRowBytes + (q * 32 + lane) * 2, __uint_as_float(v[j]));
-        group_barrier(eg);
-        const Strip w{static_cast<char*>(P.y[A.p]) + 2 * (int64_t(A.g) * P.out * P.in + fs), 2 * int64_t(P.in), left, T.loose != 0};
-        put_rows(o, w, Rows<16>([&](int c) { return c0 + c < P.out ? int64_t(c0 + c) : int64_t(-1); }));
-      }
-    } else if constexpr (gated) {
+    if constexpr (gated) {
       // Lanes 0-15 hold the gates of 16 features, lanes 16-31 their values.
       const bool upper = lane >= 16;
       const int mine = (q * 16 + (lane & 15)) * 2;  // byte of this lane's feature in a row of 64
@@ -741,13 +705,79 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
   return true;
 }
 
+// The same for the weight gradient: columns are out features, rows of the weight;
+// nothing is read but the weights that are added to.
+constexpr int kWgColumns = 16;
+__device__ __forceinline__ bool run_wgrad_epilogue(const TcParams& T, TcShared* S, const Tile& A, unsigned char* out,
+                                                   uint32_t& turn, uint32_t acc_at, uint64_t* acc_full,
+                                                   uint32_t parity, int eg, int q, int rank) {
+  const MmParams& P = T.P;
+  const int lane = threadIdx.x & 31, i = int(threadIdx.x) & 127;
+  const int f0 = A.f0 + rank * 128, f = f0 + q * 32 + lane, left = P.in - f0;
+  bool ok = true;
+  if (A.steps > 0) {
+    ok = warp_wait(acc_full, parity, T, S);
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  }
+  if (!group_all(eg, ok)) return false;
+  for (int col = eg * kWgColumns; col < A.n; col += 2 * kWgColumns) {
+    uint32_t v[kWgColumns];
+    if (A.steps > 0) {
+      tmem_load(v, acc_at + uint32_t(col));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kWgColumns; ++j) v[j] = 0;
+    }
+    const int c0 = A.c0 + col;
+    const int64_t at = (int64_t(A.g) * P.out + c0) * P.in;  // weight [c0][0]
+    if (P.out_f32) {
+      float* o = static_cast<float*>(P.y[A.p]) + at + f;
+      if (P.accumulate) {
+        float add[kWgColumns];
+#pragma unroll
+        for (int j = 0; j < kWgColumns; ++j) add[j] = f < P.in && c0 + j < P.out ? o[int64_t(j) * P.in] : 0.f;
+#pragma unroll
+        for (int j = 0; j < kWgColumns; ++j) v[j] = __float_as_uint(add[j] + __uint_as_float(v[j]));
+      }
+#pragma unroll
+      for (int j = 0; j < kWgColumns; ++j)
+        if (f < P.in && c0 + j < P.out) o[int64_t(j) * P.in] = __uint_as_float(v[j]);
+      continue;
+    }
+    if (P.accumulate) {
+      const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(P.y[A.p]) + at + f;
+      float add[kWgColumns];
+#pragma unroll
+      for (int j = 0; j < kWgColumns; ++j) add[j] = f < P.in && c0 + j < P.out ? bf16_of(w + int64_t(j) * P.in) : 0.f;
+#pragma unroll
+      for (int j = 0; j < kWgColumns; ++j) v[j] = __float_as_uint(add[j] + __uint_as_float(v[j]));
+    }
+    unsigned char* o = out + (turn++ & 1) * (kWgColumns * kTcRowBytes);
+#pragma unroll
+    for (int j = 0; j < kWgColumns; ++j) put_bf16(o + j * kTcRowBytes + (q * 32 + lane) * 2, __uint_as_float(v[j]));
+    group_barrier(eg);
+    // 128 threads: 8 rows of 16 vectors at a time
+    const int c = i / 16, u = i % 16;
+    char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(P.y[A.p]) + at) + (int64_t(c) * P.in + (left > 0 ? f0 : 0)) * 2 + u * 16;
+#pragma unroll
+    for (int h = 0; h < kWgColumns / 8; ++h) {
+      const unsigned char* from = o + (i + 128 * h) * 16;
+      char* row = to + int64_t(h) * 16 * P.in;
+      const bool there = c0 + c + 8 * h < P.out && u * 8 < left;
+      if (T.loose) put_loose(row, from, there ? left - u * 8 : 0);
+      else if (there) *reinterpret_cast<uint4*>(row) = *reinterpret_cast<const uint4*>(from);
+    }
+  }
+  return true;
+}
+
 // ------------------------------------------------------------------ kernel
 // Stages, then the planes of the two epilogue groups (three input buffers, in dgrad
 // of two planes and otherwise followed by two output planes; dgrad without an
 // activation takes its output planes from its buffers; wgrad has output planes
 // only), then the barriers and tile counts.
 template <int MODE>
-constexpr size_t kGroupPlanes = MODE == kForward ? 5 : MODE == kDgrad ? 6 : 2;
+constexpr size_t kGroupPlanes = MODE == kForward ? 5 : MODE == kDgrad ? 6 : 2 * kWgColumns / kTcColumns;
 template <int MODE>
 constexpr size_t kTcPlanes = 2 * kGroupPlanes<MODE>;
 template <int MODE>
@@ -755,7 +785,7 @@ constexpr size_t kTcSmem = 1024 + kStageBytes<MODE> + kTcPlanes<MODE> * kTcPlane
 static_assert(kTcSmem<kForward> <= 232448 && kTcSmem<kDgrad> <= 232448 && kTcSmem<kWgrad> <= 232448, "227 KB of shared memory");
 
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
     mm_tc_kernel(const __grid_constant__ TcParams T) {
   extern __shared__ unsigned char raw[];
   const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
@@ -812,12 +842,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                                         : S->tile0[P.parts * P.groups] + unsigned(S->lower) * ftiles;
   const unsigned who = blockIdx.x >> 1, of = gridDim.x >> 1;
 
-  if (warp == 0 || (MODE != kWgrad && warp == 2)) {
+  if (warp == 0 || warp == (MODE == kWgrad ? 12 : 2)) {
     // ---- tensor copies of the rows.  The whole warp walks the stages, so that
     // addresses stay in uniform registers, and one lane issues what it can.
     const bool one = elect_one();
     const uint32_t full0 = on_first(&S->full[0]);
-    const int block = warp == 2;  // forward, dgrad: the 64 rows of this CTA's half that the warp fetches
+    const int block = warp != 0;  // forward, dgrad: the 64 rows of this CTA's half that the warp fetches
+    auto own = [&](uint32_t st) { return MODE != kWgrad || int(st & 1) == block; };  // wgrad: its stages
     Turn k(T.stages);
     bool ok = true;
     // Waits until the MMAs have released the stage's last filling.
@@ -835,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         group_at<8>(P, A.p, A.g, R, A.c0 + rank * half + block * 64 + (lane & 7) * 8, row, left);
         if ((lane & 7) * 8 >= mine) left = 0;
         // Columns of groups without rows are not stored: they are not fetched.
-        const int box = left > 0 ? box_at(row, left) : (box_at(row, left), -1);
+        const int any = box_at(row, left), box = left > 0 ? any : -1;
         const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xFFFFFFFFu, left > 0) & 0xFFu)) * 1024u + T.tx_pad;
         const CUtensorMap* map = &T.row[A.p][box < 0 ? 0 : box];
         for (int s = 0; s < A.steps; ++s, k.next()) {
@@ -854,10 +885,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const uint32_t bytes = kTcOperand + uint32_t(blocks) * 8192u + T.tx_pad;
         const int fx = A.f0 + rank * 128, fd = A.c0 + rank * half;
         for (int s = 0; ok && s < A.steps;) {
+          if (P.sources <= 32 && s >= R.wholes / kTcDepth && !own(k.st)) {  // remainders, the other warp's
+            ++s;
+            k.next();
+            continue;
+          }
           int row, valid;
           const int run = stage_rows(P, A, R, s, row, valid);
           int r = __shfl_sync(0xFFFFFFFFu, row, 0);
           for (int i = 0; i < run; ++i, r += kTcDepth, k.next()) {
+            if (!own(k.st)) continue;
             if (!free()) {
               ok = false;
               break;
@@ -874,6 +911,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           }
           s += run;
           if (run > 0) continue;
+          if (!own(k.st)) {
+            ++s;
+            k.next();
+            continue;
+          }
           if (!free()) {
             ok = false;
             break;
@@ -894,7 +936,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       }
     }
     // The MMAs' last releases of the stages have to land before this CTA may leave.
-    for (uint32_t j = 0; ok && j < T.stages; ++j, k.next()) ok = free();
+    for (uint32_t j = 0; ok && j < T.stages; ++j, k.next()) ok = !own(k.st) || free();
   } else if (MODE != kWgrad && warp == 3) {
     // ---- tensor copies of the weights
     const bool one = elect_one();
@@ -966,11 +1008,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       __syncwarp();
       ++it;
     }
-  } else if (MODE == kWgrad && (warp == 2 || warp == 3)) {
+  } else if (MODE == kWgrad && (warp == 2 || warp == 3 || warp > 12)) {
     // ---- zero the padding rows of the stages that hold any, then hand them to the
-    // MMA.  Two warps share them, since a release to the cluster takes longer than
-    // the MMAs of a stage: one the even stages, one the odd ones, so that a warp
-    // waits on every phase of the barriers that it waits on.
+    // MMA.  A release to the cluster takes about 1400 cycles, the MMAs of a stage 512:
+    // five warps, each with stages of its own, so that a warp waits on every phase of
+    // the barriers that it waits on.
+    const uint32_t own = warp < 4 ? warp - 2 : warp - 11;
     const uint32_t full0 = on_first(&S->full[0]);
     Turn k(T.stages);
     uint32_t phases = 0;  // bit st: parity of part[st]
@@ -986,15 +1029,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < run; ++i) k.next();
         s += run;
         if (run > 0) continue;
-        const uint32_t st = k.st, parity = (phases >> st) & 1;
+        const uint32_t st = k.st;
         k.next();
         ++s;
-        if ((st & 1) != uint32_t(warp - 2)) continue;
-        phases ^= 1u << st;
-        if (!warp_wait(&S->part[st], parity, T, S)) {
+        if (st % 5 != own) continue;
+        if (!warp_wait(&S->part[st], (phases >> st) & 1, T, S)) {
           ok = false;
           break;
         }
+        phases ^= 1u << st;
         // lanes: 4 blocks of 64 features (2 of x, 2 of dy) x 8 vectors of a 128-byte row
         // (a group without rows came from past the buffer's end: zeros already)
         unsigned char* at = stages + size_t(st) * T.stage + (lane >> 3) * 8192 + (lane & 7) * 16;
@@ -1012,7 +1055,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         if (lane == 0) arrive_cluster(full0 + st * 8u);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 4 + kTcEpilogue) {
     // ---- epilogue: two groups of four warps take turns along the columns
     const int q = warp & 3, eg = (warp - 4) / 4;
     unsigned char* in = planes + eg * kGroupPlanes<MODE> * kTcPlane;
@@ -1035,12 +1078,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       const uint32_t acc = it & 1;
       const uint32_t at = tmem + acc * 256u + (uint32_t(q * 32) << 16);
       bool ok = true;
-      auto tile = [&](auto tag) {
-        ok = run_epilogue<MODE, decltype(tag)::act>(T, S, A, in, out, turn, buffer, at, &S->acc_full[acc], (it >> 1) & 1, eg, q,
-                                                    rank, row, valid, bias);
-      };
-      if constexpr (MODE == kWgrad) tile(ActTag<HOC_ACT_NONE>{});
-      else with_act(P.act, tile);
+      if constexpr (MODE == kWgrad) {
+        ok = run_wgrad_epilogue(T, S, A, out, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q, rank);
+      } else {
+        with_act(P.act, [&](auto tag) {
+          ok = run_epilogue<MODE, decltype(tag)::act>(T, S, A, in, out, turn, buffer, at, &S->acc_full[acc],
+                                                      (it >> 1) & 1, eg, q, rank, row, valid, bias);
+        });
+      }
       if (!ok) break;
       if (A.steps == 0) continue;  // no accumulator was used
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1136,7 +1181,7 @@ cudaError_t configure(const void* fn, int mode, size_t smem, cudaLaunchAttribute
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kTcThreads);
+  cfg.blockDim = dim3(mode == kWgrad ? kTcThreads<kWgrad> : kTcThreads<kForward>);
   cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
