@@ -59,7 +59,8 @@ struct TcParams {
   MmParams P;
   int tile_rows;     // most rows c of a tile, a multiple of 32
   uint32_t stage;    // bytes of a stage: 128 x 64 of A, half of tile_rows x 64 of B
-  uint32_t stages;
+  uint32_t stages;   // as many as the epilogue's planes leave room for: 5 or 6 of a tile of 256 rows
+  uint32_t planes;   // staged arrays of each of the two epilogue groups
   int loose;         // what the epilogue moves is not whole 16-byte vectors
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
   uint64_t wait_ns;
@@ -68,10 +69,6 @@ struct TcParams {
   CUtensorMap dy[kMaxRanks][4];                  // wgrad
 };
 
-// Shared memory for the stages: what the epilogue's planes leave of 227 KB.  That
-// is 5 stages (wgrad 6) of a tile of 256 rows, and up to 8 of a lower one.
-template <int MODE>
-constexpr uint32_t kStageBytes = (MODE == kWgrad ? 6 : 5) * kTcStage;
 constexpr int kTcMostStages = 8;
 
 struct TcShared {
@@ -772,17 +769,17 @@ __device__ __forceinline__ bool run_wgrad_epilogue(const TcParams& T, TcShared* 
 }
 
 // ------------------------------------------------------------------ kernel
-// Stages, then the planes of the two epilogue groups (three input buffers, in dgrad
-// of two planes and otherwise followed by two output planes; dgrad without an
-// activation takes its output planes from its buffers; wgrad has output planes
-// only), then the barriers and tile counts.
-template <int MODE>
-constexpr size_t kGroupPlanes = MODE == kForward ? 5 : MODE == kDgrad ? 6 : 2 * kWgColumns / kTcColumns;
-template <int MODE>
-constexpr size_t kTcPlanes = 2 * kGroupPlanes<MODE>;
-template <int MODE>
-constexpr size_t kTcSmem = 1024 + kStageBytes<MODE> + kTcPlanes<MODE> * kTcPlane + sizeof(TcShared);
-static_assert(kTcSmem<kForward> <= 232448 && kTcSmem<kDgrad> <= 232448 && kTcSmem<kWgrad> <= 232448, "227 KB of shared memory");
+// Shared memory: the stages, the planes of the two epilogue groups (two output
+// planes; where the epilogue reads rows, three input buffers, which in dgrad have two
+// planes each and hold the results too), the barriers and tile counts.
+constexpr uint32_t kTcSmem = 232448;  // 227 KB
+constexpr uint32_t planes_of(int mode, bool reads) { return !reads ? 2 : mode == kForward ? 5 : 6; }
+constexpr uint32_t stages_in(uint32_t planes, uint32_t stage) {
+  const uint32_t n = (kTcSmem - 1024 - uint32_t(sizeof(TcShared)) - 2 * planes * kTcPlane) / stage;
+  return n < uint32_t(kTcMostStages) ? n : uint32_t(kTcMostStages);
+}
+static_assert(kWgColumns == kTcColumns, "the planes are of one size");
+static_assert(stages_in(2, kTcStage) == 6 && stages_in(6, kTcStage) == 5, "stages of a tile of 256 rows");
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
@@ -790,8 +787,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
   extern __shared__ unsigned char raw[];
   const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
   unsigned char* stages = raw + (base - ptx::smem_addr(raw));
-  unsigned char* planes = stages + kStageBytes<MODE>;
-  TcShared* S = reinterpret_cast<TcShared*>(planes + kTcPlanes<MODE> * kTcPlane);
+  unsigned char* planes = stages + T.stages * T.stage;
+  TcShared* S = reinterpret_cast<TcShared*>(planes + 2 * T.planes * kTcPlane);
   const MmParams& P = T.P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(cta_rank());
@@ -1058,8 +1055,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
   } else if (warp >= 4 && warp < 4 + kTcEpilogue) {
     // ---- epilogue: two groups of four warps take turns along the columns
     const int q = warp & 3, eg = (warp - 4) / 4;
-    unsigned char* in = planes + eg * kGroupPlanes<MODE> * kTcPlane;
-    unsigned char* out = MODE == kForward ? in + 3 * kTcPlane : in;
+    unsigned char* in = planes + eg * T.planes * kTcPlane;
+    unsigned char* out = MODE == kForward && T.planes > 2 ? in + 3 * kTcPlane : in;
     uint32_t it = 0, turn = 0, buffer = 0;
     Work W(T, S, who, of, tiles);
     for (W.first<MODE>(); W.more; W.next()) {
@@ -1253,11 +1250,10 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   T.tx_pad = stall ? 16u : 0u;
   T.wait_ns = stall ? 100000000ull : kTcWaitNs;
   const void* fn = reinterpret_cast<const void*>(kTc[mode]);
-  const size_t smem = mode == kForward ? kTcSmem<kForward> : mode == kDgrad ? kTcSmem<kDgrad> : kTcSmem<kWgrad>;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   int pairs = 0;
-  cudaError_t e = configure(fn, mode, smem, attr, cfg, pairs);
+  cudaError_t e = configure(fn, mode, kTcSmem, attr, cfg, pairs);
   if (e != cudaSuccess) return e;
   cfg.stream = s;
   int64_t tiles = 0;
@@ -1267,8 +1263,10 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   else if (P.seg == nullptr) T.tile_rows = choose_rows(P.cap[0], ftiles, pairs);
   else T.tile_rows = choose_rows_ragged(P);
   T.stage = mode == kWgrad ? kTcStage : kTcOperand + uint32_t(T.tile_rows) * (kTcDepth * 2 / 2);
-  T.stages = (mode == kWgrad ? kStageBytes<kWgrad> : kStageBytes<kForward>) / T.stage;
-  if (T.stages > uint32_t(kTcMostStages)) T.stages = kTcMostStages;
+  bool reads = mode == kDgrad && P.act != HOC_ACT_NONE;
+  for (int p = 0; mode == kForward && p < P.part0 + P.parts; ++p) reads = reads || P.res[p] != nullptr;
+  T.planes = planes_of(mode, reads);
+  T.stages = stages_in(T.planes, T.stage);
   for (int p = P.part0; p < P.part0 + P.parts; ++p) {
     tiles += ftiles * (mode == kWgrad ? int64_t(P.groups) * ((P.out + T.tile_rows - 1) / T.tile_rows)
                                       : P.cap[p] / T.tile_rows + int64_t(P.groups) * (1 + P.sources * 8 / T.tile_rows));

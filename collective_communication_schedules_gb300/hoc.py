@@ -228,17 +228,18 @@ def _ptr(x, nbytes: int = 0, what: str = "buffer", device: bool = True) -> int:
 
 def _ptr_array(xs: Sequence, nbytes=0, what: str = "buffer", device: bool = True) -> C.Array:
     """Addresses of the rank buffers; `nbytes` is one span for all ranks or a list, one per rank."""
-    spans = list(nbytes) if isinstance(nbytes, (list, tuple)) else [nbytes] * len(xs)
-    if len(spans) != len(xs):
-        raise ValueError(f"{what}: expected {len(spans)} rank buffers, got {len(xs)}")
-    out = (C.c_void_p * len(xs))()
-    for r, (x, n) in enumerate(zip(xs, spans)):
+    one = not isinstance(nbytes, (list, tuple))
+    if not one and len(nbytes) != len(xs):
+        raise ValueError(f"{what}: expected {len(nbytes)} rank buffers, got {len(xs)}")
+    out = []
+    for r, x in enumerate(xs):
+        n = nbytes if one else nbytes[r]
         # the checks of _ptr, which names the buffer if one fails
-        if isinstance(x, int) or not x.is_contiguous() or x.numel() * x.element_size() < n or x.is_cuda != device:
-            out[r] = _ptr(x, n, f"{what}[{r}]", device)
+        if isinstance(x, int) or x.numel() * x.element_size() < n or x.is_cuda != device or not x.is_contiguous():
+            out.append(_ptr(x, n, f"{what}[{r}]", device))
         else:
-            out[r] = x.data_ptr()
-    return out
+            out.append(x.data_ptr())
+    return (C.c_void_p * len(out))(*out)
 
 
 def _stream(stream) -> int:

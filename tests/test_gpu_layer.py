@@ -519,3 +519,52 @@ def test_realigned_copies_in_a_graph():
         torch.cuda.synchronize()
         _, _, want, err = ref.forward(x, w, None, "none")
         ref.close(y, want, err, "replayed")
+
+
+@pytest.mark.parametrize("most", [5, 90])
+def test_more_sources_than_a_warp_has_lanes(most):
+    """40 and 70 row ranges to an expert: the ranges are walked 32 at a time."""
+    inp, out = 136, 72
+    for sources in (40, 70):
+        L = ref.Routed(ref.random_counts(1, sources, 2, most, sources + most))
+        n = L.cap[0]
+        x, dy = normal(n, inp, seed=1), normal(n, out, seed=2)
+        x[L.of[0] < 0] = dy[L.of[0] < 0] = float("nan")
+        w = [normal(2, out, inp, seed=3, sigma=inp ** -0.5)]
+        y, dx = torch.full((n, out), 7.0, dtype=BF, device=DEV), torch.full((n, inp), 7.0, dtype=BF, device=DEV)
+        dw, db = [torch.empty(2, out, inp, device=DEV)], [torch.empty(2, out, device=DEV)]
+        st = status()
+        hoc.expert_mm([x], w, L.seg, [y], status=st)
+        hoc.expert_mm_dgrad([dy], w, L.seg, [dx], status=st)
+        hoc.expert_mm_wgrad([dy], [x], L.seg, dw, status=st, db=db)
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        assert bool((y[L.of[0] < 0] == 7).all())
+        for e in range(2):
+            r = L.rows(0, e)
+            _, _, want, err = ref.forward(x[r], w[0][e], None, "none")
+            ref.close(y[r], want, err, f"y {e}")
+            want, err = ref.dgrad(dy[r], w[0][e], "none", None)
+            ref.close(dx[r], want, err, f"dx {e}")
+            a, v = dy[r].double(), x[r].double()
+            ref.close(dw[0][e], a.t() @ v, (a.abs().t() @ v.abs()) * len(r) * ref.F32, f"dw {e}", ref.F32)
+            ref.close(db[0][e], a.sum(0), a.abs().sum(0) * len(r) * ref.F32, f"db {e}", ref.F32)
+
+
+def test_every_expert_tile_order():
+    """More experts than are sorted (256), with whole and lower tiles among them, and the two-launch split (more than
+    1024): every row is computed once, by its own expert."""
+    for experts, most in ((300, 520), (1100, 5)):
+        counts = ref.random_counts(1, 1, experts, most, experts, empty=0.5)
+        L = ref.Routed(counts)
+        n, inp, out = L.cap[0], 16, 8
+        x = normal(n, inp, seed=1)
+        w = [normal(experts, out, inp, seed=2)]
+        y, st = torch.full((n, out), 7.0, dtype=BF, device=DEV), status()
+        hoc.expert_mm([x], w, L.seg, [y], status=st)
+        own = L.of[0].clamp(min=0)
+        want = torch.einsum("rk,rok->ro", x.double(), w[0].double()[own])
+        err = torch.einsum("rk,rok->ro", x.double().abs(), w[0].double().abs()[own]) * inp * ref.F32
+        has = L.of[0] >= 0
+        ref.close(y[has], want[has], err[has], "y")
+        assert bool((y[~has] == 7).all()) and st.item() == 0
