@@ -71,25 +71,37 @@ template <class Tiles>
 __device__ __forceinline__ void mm_count(const MmParams& P, int pad, int* vrows, unsigned* tile0, Tiles tiles) {
   const int n = P.parts * P.groups;
   const int ns = P.seg ? P.sources : 1;
-  // The lanes of a warp take the sources of as many pairs as fit, then add up in segments of `w` lanes.
+  // The lanes of a warp take the sources of as many pairs as fit, then add up in
+  // segments of `w` lanes.  32-bit sums: valid ranges of a buffer add up to less than
+  // 2^31 rows, and whatever others wrap to is cut to the most there can be.
   int w = 1;
   while (w < ns && w < 32) w *= 2;
-  const int lane = threadIdx.x & 31, sub = lane & (w - 1);
-  const int per = int(blockDim.x) / w;  // pairs at a time
-  for (int at = 0; at < n; at += per) {
-    const int i = at + int(threadIdx.x) / w;
-    int64_t sum = 0;
+  const int sub = threadIdx.x & (w - 1), per = int(blockDim.x) / w;  // pairs at a time
+  constexpr int kAhead = 2;  // loads of a thread in flight
+  for (int at = 0; at < n; at += per * kAhead) {
+    int sum[kAhead] = {};
     for (int base = 0; base < ns; base += 32) {
-      int64_t lo, c = 0;
-      if (i < n && base + sub < ns) mm_range(P, P.part0 + i / P.groups, P.group0 + i % P.groups, base + sub, lo, c);
-      const int to = pad < 8 ? pad : 8;
-      c = (c + to - 1) / to * to;
-      for (int off = w / 2; off; off >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, off);
-      sum += (c + pad - 1) / pad * pad;
+      int64_t lo, c[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = at + u * per + int(threadIdx.x) / w, part = i / P.groups;
+        c[u] = 0;
+        if (i < n && base + sub < ns) mm_range(P, P.part0 + part, P.group0 + i - part * P.groups, base + sub, lo, c[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int to = pad < 8 ? pad : 8;
+        int rows = int((c[u] + to - 1) / to * to);
+        for (int off = w / 2; off; off >>= 1) rows += __shfl_xor_sync(0xFFFFFFFFu, rows, off);
+        sum[u] += (rows + pad - 1) / pad * pad;
+      }
     }
-    if (i < n && sub == 0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = at + u * per + int(threadIdx.x) / w;
+      if (i >= n || sub != 0) continue;
       const int64_t most = P.cap[P.part0 + i / P.groups] + int64_t(ns) * (pad - 1) + pad;  // more only if ranges overlap
-      vrows[i] = int(sum < most ? sum : most);
+      vrows[i] = int(sum[u] < 0 ? 0 : sum[u] < most ? sum[u] : most);
     }
   }
   __syncthreads();

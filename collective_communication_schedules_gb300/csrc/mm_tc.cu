@@ -6,8 +6,8 @@
 // 256 rows c in its columns, so
 //   - the ragged side (an expert's rows) is the N extent of the MMA, which may
 //     be any multiple of 32: a short range costs what it has, not a whole tile;
-//   - a thread of the epilogue owns one feature, so bias and store addresses
-//     are uniform along its registers and a warp stores 64 contiguous bytes.
+//   - a thread of the epilogue owns one feature, whose bias is one register, and
+//     what it stores lies beside what its neighbours store.
 // A pair of CTAs (a cluster of two SMs) computes one tile with cta_group::2:
 // each holds 128 features of A and half of the rows of B, 64 deep per stage, so
 // a stage moves 32 KB into each SM for 128 x 256 x 64 products.  Operands come
@@ -18,19 +18,22 @@
 // An expert's rows lie in one range per source.  They are taken as one virtual
 // row space in which every range is padded to a multiple of 8, the height of a
 // swizzle atom; 64 virtual rows that are contiguous in memory are fetched by one
-// copy, others by copies of 32, 16 and 8.  Padding rows hold a neighbour's data: in the
-// forward product and the data gradient they are columns that are not stored; in
-// the weight gradient, where rows are summed over, they are overwritten with zeros
-// in shared memory before the MMA reads them.  There, the whole multiples of 64
-// rows of the ranges come first, each stage one copy per 64 features, and what
+// copy, others by copies of 32, 16 and 8.  Padding rows hold a neighbour's data: in
+// the forward product and the data gradient they are columns that are not stored;
+// in the weight gradient, where rows are summed over, they are overwritten with
+// zeros in shared memory before the MMA reads them.  There, the whole multiples of
+// 64 rows of the ranges come first, each stage one copy per 64 features, and what
 // remains of the ranges is packed into the last stages.
 //
 // Warps of a CTA: 0 and 2 tensor copies of the rows, 64 each; 3 those of the
 // weights; 1 MMA (of the pair's first CTA); 4-11 epilogue.  In the weight gradient
 // warps 0 and 12 issue all copies of every second stage, and warps 2, 3 and 13-15
-// zero padding rows.  Every wait is bounded: a wait that runs
-// out sets bit 2 of the status, and all roles leave.
+// zero padding rows.  Every wait is bounded: a wait that runs out sets bit 2 of the
+// status, and all roles leave.
+//
+// TC_FIGURES
 #include <atomic>
+#include <climits>
 #include <cstdlib>
 #include <cstring>
 
@@ -51,12 +54,29 @@ constexpr uint32_t kTcOperand = 128 * 128;      // bytes of one operand of a sta
 constexpr uint32_t kTcStage = 2 * kTcOperand;
 constexpr int kTcFeatures = 256;                // of a pair's tile
 constexpr int kTcRows = 256;                    // at most, of a tile
-constexpr unsigned kTcPanel = 8;
+constexpr unsigned kTcPanel = 8;                // row tiles of a panel (see tile_at)
 constexpr uint32_t kTcTmemColumns = 512;        // two accumulators of 256 columns
 constexpr uint64_t kTcWaitNs = 2000000000ull;
 
+// Division of numbers below 2^31 by a number that the host knows: a multiplication
+// and a shift.  (The compiler's division takes over 100 cycles; a warp that looks up
+// its first tile did it seven times before its first copy.)
+struct Divisor {
+  uint32_t d, m, s;
+  __device__ __forceinline__ unsigned of(unsigned n) const { return unsigned((uint64_t(n) * m) >> s); }
+};
+Divisor divisor(uint32_t d) {
+  uint32_t log = 0;
+  while ((uint64_t(1) << log) < d) ++log;
+  return {d, uint32_t((uint64_t(1) << (31 + log)) / d + 1), 31 + log};
+}
+
 struct TcParams {
   MmParams P;
+  Divisor ftiles;    // feature tiles
+  Divisor ctiles, each;  // wgrad: tiles of out features, and all tiles of an expert
+  Divisor groups;    // P.groups
+  Divisor rows;      // tile_rows
   int tile_rows;     // most rows c of a tile, a multiple of 32
   uint32_t stage;    // bytes of a stage: 128 x 64 of A, half of tile_rows x 64 of B
   uint32_t stages;   // as many as the epilogue's planes leave room for: 5 or 6 of a tile of 256 rows
@@ -82,7 +102,7 @@ struct TcShared {
   int vrows[kMmMaxGroups];
   unsigned tile0[kMmMaxGroups + 1];    // forward, dgrad: whole tiles of the pairs before
   unsigned short order[kMmMaxGroups];  // forward, dgrad: pairs with a lower tile at their end; wgrad: all; most rows first
-  int key[256];                        // what the order goes by, while it is made
+  int key[256], rank[256];             // what the order goes by, while it is made
   int lower;                           // forward, dgrad: how many of those
 };
 
@@ -223,7 +243,10 @@ __device__ __forceinline__ unsigned dealt(unsigned i, unsigned who, unsigned of)
 template <int MODE>
 __device__ __forceinline__ void order_pairs(const TcParams& T, TcShared* S) {
   const int n = T.P.parts * T.P.groups;
-  auto key = [&](int i) { return MODE == kWgrad ? S->vrows[i] : S->vrows[i] % T.tile_rows; };
+  auto key = [&](int i) {
+    const int rows = S->vrows[i];
+    return MODE == kWgrad ? rows : rows - int(T.rows.of(rows)) * T.tile_rows;
+  };
   if (n == 1) {
     if (threadIdx.x == 0) {
       S->order[0] = 0;
@@ -233,28 +256,41 @@ __device__ __forceinline__ void order_pairs(const TcParams& T, TcShared* S) {
     return;
   }
   if (threadIdx.x == 0) S->lower = 0;
-  if (n <= 256)
-    for (int i = threadIdx.x; i < n; i += blockDim.x) S->key[i] = key(i);
-  __syncthreads();
   if (n <= 256) {  // rank of each pair by counting; beyond that the sort would cost more than it gains
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int mine = S->key[i];
+      S->key[i] = key(i);
+      S->rank[i] = 0;
+    }
+    __syncthreads();
+    // a warp per 32 pairs and share of the others
+    const int blocks = (n + 31) / 32, warps = int(blockDim.x) / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int shares = warps / blocks > 0 ? warps / blocks : 1;
+    for (int w = warp; w < blocks * shares; w += warps) {
+      const int i = w % blocks * 32 + lane, share = w / blocks;
+      const int mine = i < n ? S->key[i] : 0;
       int before = 0;
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) before += S->key[j] > mine || (S->key[j] == mine && j < i);
-      S->order[before] = static_cast<unsigned short>(i);
-      if (mine > 0) atomicAdd(&S->lower, 1);
+#pragma unroll 4
+      for (int j = share; j < n; j += shares) before += S->key[j] > mine || (S->key[j] == mine && j < i);
+      if (i < n) atomicAdd(&S->rank[i], before);
     }
-  } else if (threadIdx.x < 32) {
-    int at = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + int(threadIdx.x);
-      const bool take = i < n && (MODE == kWgrad || key(i) > 0);
-      const unsigned some = __ballot_sync(0xFFFFFFFFu, take);
-      if (take) S->order[at + __popc(some & ((1u << threadIdx.x) - 1u))] = static_cast<unsigned short>(i);
-      at += __popc(some);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      S->order[S->rank[i]] = static_cast<unsigned short>(i);
+      if (S->key[i] > 0) atomicAdd(&S->lower, 1);
     }
-    if (threadIdx.x == 0) S->lower = at;
+  } else {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int at = 0;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + int(threadIdx.x);
+        const bool take = i < n && (MODE == kWgrad || key(i) > 0);
+        const unsigned some = __ballot_sync(0xFFFFFFFFu, take);
+        if (take) S->order[at + __popc(some & ((1u << threadIdx.x) - 1u))] = static_cast<unsigned short>(i);
+        at += __popc(some);
+      }
+      if (threadIdx.x == 0) S->lower = at;
+    }
   }
   __syncthreads();
 }
@@ -263,32 +299,31 @@ template <int MODE>
 __device__ __forceinline__ Tile tile_at(const TcParams& T, const TcShared* S, unsigned t) {
   const MmParams& P = T.P;
   const int n = P.parts * P.groups;
-  const bool gated = MODE == kForward && P.act == HOC_ACT_SWIGLU;
-  const int ftile = gated ? kTcFeatures / 2 : kTcFeatures;
-  const unsigned ftiles = ((MODE == kForward ? P.out : P.in) + ftile - 1) / ftile;
+  const int ftile = MODE == kForward && P.act == HOC_ACT_SWIGLU ? kTcFeatures / 2 : kTcFeatures;
   unsigned i, ct, ft;
   if (MODE == kWgrad) {
-    const unsigned ctiles = (P.out + T.tile_rows - 1) / T.tile_rows, each = ctiles * ftiles;
-    i = S->order[t / each];
-    ct = t % each % ctiles;
-    ft = t % each / ctiles;
+    const unsigned at = T.each.of(t), u = t - at * T.each.d;
+    i = S->order[at];
+    ft = T.ctiles.of(u);
+    ct = u - ft * T.ctiles.d;
   } else if (t < S->tile0[n]) {
     i = mm_find(S->tile0, n, t);
     // panels of 8 row tiles, so that the tiles in flight share rows and features about evenly
-    const unsigned lt = t - S->tile0[i], whole = (S->tile0[i + 1] - S->tile0[i]) / ftiles;
-    const unsigned panel = lt / (kTcPanel * ftiles), in_panel = lt - panel * kTcPanel * ftiles;
+    const unsigned lt = t - S->tile0[i], whole = T.ftiles.of(S->tile0[i + 1] - S->tile0[i]);
+    const unsigned panel = T.ftiles.of(lt) / kTcPanel, u = lt - panel * kTcPanel * T.ftiles.d;
     const unsigned high = min(kTcPanel, whole - panel * kTcPanel);
-    ct = panel * kTcPanel + in_panel % high;
-    ft = in_panel / high;
+    ft = high == kTcPanel ? u / kTcPanel : u / high;
+    ct = panel * kTcPanel + u - ft * high;
   } else {
-    const unsigned u = t - S->tile0[n];
-    i = S->order[u / ftiles];
-    ct = (S->tile0[i + 1] - S->tile0[i]) / ftiles;
-    ft = u % ftiles;
+    const unsigned u = t - S->tile0[n], at = T.ftiles.of(u);
+    i = S->order[at];
+    ct = T.ftiles.of(S->tile0[i + 1] - S->tile0[i]);
+    ft = u - at * T.ftiles.d;
   }
+  const unsigned part = T.groups.of(i);
   Tile A;
-  A.p = P.part0 + i / P.groups;
-  A.g = P.group0 + i % P.groups;
+  A.p = P.part0 + part;
+  A.g = P.group0 + i - part * T.groups.d;
   A.f0 = int(ft) * ftile;
   A.c0 = int(ct) * T.tile_rows;
   const int rows = S->vrows[i];
@@ -328,19 +363,21 @@ __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, Ends E) 
   R.n = int(n);
   const int whole = PAD == 8 ? 0 : R.n / PAD * PAD, rest = (R.n - whole + 7) & ~7;
   int a = whole, b = rest;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
+  const int ns = P.seg ? P.sources : 1;
+  for (int off = 1; off < 32 && off < ns; off <<= 1) {
     const int x = __shfl_up_sync(0xFFFFFFFFu, a, off), y = __shfl_up_sync(0xFFFFFFFFu, b, off);
     if (lane >= off) {
       a += x;
       b += y;
     }
   }
-  const int wholes = __shfl_sync(0xFFFFFFFFu, a, 31);
+  const int last = min(ns, 32) - 1;  // lanes past the sources add nothing
+  const int wholes = __shfl_sync(0xFFFFFFFFu, a, last);
   R.wholes = wholes;
   R.rest = wholes + b - rest;
   R.start = PAD == 8 ? R.rest : a - whole;
-  R.all = (wholes + __shfl_sync(0xFFFFFFFFu, b, 31) + PAD - 1) / PAD * PAD;
+  if (lane >= ns) R.start = R.rest = INT_MAX;  // no source: starts past everything
+  R.all = (wholes + __shfl_sync(0xFFFFFFFFu, b, last) + PAD - 1) / PAD * PAD;
   return R;
 }
 // Each lane's group of 8 virtual rows at `v` (a multiple of 8): its first row in
@@ -357,8 +394,7 @@ __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges
     const bool whole = PAD > 8 && v < R.wholes;
     const int key = whole ? R.start : R.rest;
     int j = 0;  // the last source that starts at or before v
-#pragma unroll
-    for (int step = 16; step; step >>= 1) {
+    for (int step = ns > 8 ? 16 : ns > 1 ? 4 : 0; step; step >>= 1) {
       const int at = __shfl_sync(0xFFFFFFFFu, key, j + step);
       if (at <= v) j += step;
     }
@@ -826,17 +862,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
   cluster_arrive();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int ftile = gated ? kTcFeatures / 2 : kTcFeatures;
-  const unsigned ftiles = ((MODE == kForward ? P.out : P.in) + ftile - 1) / ftile;
   mm_count(P, MODE == kWgrad ? kTcDepth : 8, S->vrows, S->tile0,
-           [&](int rows) { return MODE == kWgrad ? 0u : unsigned(rows / T.tile_rows) * ftiles; });
+           [&](int rows) { return MODE == kWgrad ? 0u : T.rows.of(rows) * T.ftiles.d; });
   order_pairs<MODE>(T, S);
   __syncwarp();
   cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = S->tmem;
-  const unsigned tiles = MODE == kWgrad ? unsigned(P.parts * P.groups) * ftiles * ((P.out + T.tile_rows - 1) / T.tile_rows)
-                                        : S->tile0[P.parts * P.groups] + unsigned(S->lower) * ftiles;
+  const unsigned tiles = MODE == kWgrad ? unsigned(P.parts * P.groups) * T.each.d
+                                        : S->tile0[P.parts * P.groups] + unsigned(S->lower) * T.ftiles.d;
   const unsigned who = blockIdx.x >> 1, of = gridDim.x >> 1;
 
   if (warp == 0 || warp == (MODE == kWgrad ? 12 : 2)) {
@@ -1266,6 +1300,11 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   bool reads = mode == kDgrad && P.act != HOC_ACT_NONE;
   for (int p = 0; mode == kForward && p < P.part0 + P.parts; ++p) reads = reads || P.res[p] != nullptr;
   T.planes = planes_of(mode, reads);
+  T.ftiles = divisor(uint32_t(ftiles));
+  T.ctiles = divisor(uint32_t((P.out + T.tile_rows - 1) / T.tile_rows));
+  T.each = divisor(T.ctiles.d * T.ftiles.d);
+  T.groups = divisor(uint32_t(P.groups));
+  T.rows = divisor(uint32_t(T.tile_rows));
   T.stages = stages_in(T.planes, T.stage);
   for (int p = P.part0; p < P.part0 + P.parts; ++p) {
     tiles += ftiles * (mode == kWgrad ? int64_t(P.groups) * ((P.out + T.tile_rows - 1) / T.tile_rows)
