@@ -20,15 +20,20 @@ enum MmMode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 constexpr int kMmMaxGroups = 1024;
 
 struct MmParams {
+  // read by every warp before its first tile: together, in as few constant-cache lines as can be
   const int64_t* seg;  // [nranks][sources * experts + 1] row offsets; null: one range, all rows
   int experts;         // experts of one rank (the seg layout)
   int sources;
   int part0, parts;    // rank buffers of this launch
   int group0, groups;  // experts of each of them in this launch
-  int64_t cap[kMaxRanks];  // rows of each rank buffer
   int in, out;             // weight: [experts][out (x 2 when gated)][in]
   int act;                 // hocAct_t: forward, of the output; dgrad, of the layer below
   int out_f32, accumulate; // wgrad
+  int32_t* status;
+  int64_t ld_rows, ld_dy, ld_res, ld_y;
+  int64_t ld_w;     // elements from one row of a weight to the next (in, but for a realigned copy)
+  int64_t out_w;    // rows of an expert's weight, of its gates when gated (out, likewise)
+  int64_t cap[kMaxRanks];  // rows of each rank buffer
   const __nv_bfloat16* rows[kMaxRanks];  // forward: x; dgrad: dy; wgrad: x
   const __nv_bfloat16* dy[kMaxRanks];    // wgrad
   const __nv_bfloat16* w[kMaxRanks];
@@ -37,10 +42,6 @@ struct MmParams {
   const __nv_bfloat16* pre[kMaxRanks];  // dgrad: pre-activation of the layer below
   void* y[kMaxRanks];
   void* pre_out[kMaxRanks];  // forward: pre-activation to keep
-  int64_t ld_rows, ld_dy, ld_res, ld_y;
-  int64_t ld_w;     // elements from one row of a weight to the next (in, but for a realigned copy)
-  int64_t out_w;    // rows of an expert's weight, of its gates when gated (out, likewise)
-  int32_t* status;
 };
 
 // Device helpers ------------------------------------------------------------

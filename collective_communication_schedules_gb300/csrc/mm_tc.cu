@@ -72,7 +72,6 @@ Divisor divisor(uint32_t d) {
 }
 
 struct TcParams {
-  MmParams P;
   Divisor ftiles;    // feature tiles
   Divisor ctiles, each;  // wgrad: tiles of out features, and all tiles of an expert
   Divisor groups;    // P.groups
@@ -84,6 +83,7 @@ struct TcParams {
   int loose;         // what the epilogue moves is not whole 16-byte vectors
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
   uint64_t wait_ns;
+  MmParams P;
   CUtensorMap w[kMaxRanks];                      // forward, dgrad
   CUtensorMap row[kMaxRanks][4];                 // P.rows in boxes of 8 << i rows
   CUtensorMap dy[kMaxRanks][4];                  // wgrad
@@ -151,6 +151,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, con
 // The same by a whole warp, with one answer for all lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const TcParams& T, TcShared* S) {
   return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, T, S));
+}
+// Programmatic dependent launch: waits for the kernel before this one on the
+// stream, then lets the next one start.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 // One lane of a warp, for the instructions that one thread issues.
 __device__ __forceinline__ bool elect_one() {
@@ -247,14 +253,6 @@ __device__ __forceinline__ void order_pairs(const TcParams& T, TcShared* S) {
     const int rows = S->vrows[i];
     return MODE == kWgrad ? rows : rows - int(T.rows.of(rows)) * T.tile_rows;
   };
-  if (n == 1) {
-    if (threadIdx.x == 0) {
-      S->order[0] = 0;
-      S->lower = key(0) > 0;
-    }
-    __syncthreads();
-    return;
-  }
   if (threadIdx.x == 0) S->lower = 0;
   if (n <= 256) {  // rank of each pair by counting; beyond that the sort would cost more than it gains
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -295,8 +293,9 @@ __device__ __forceinline__ void order_pairs(const TcParams& T, TcShared* S) {
   __syncthreads();
 }
 
+// (Not inlined: every role calls it, once for 32 tiles, and shares its instructions.)
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(const TcParams& T, const TcShared* S, unsigned t) {
+__device__ __noinline__ Tile tile_at(const TcParams& T, const TcShared* S, unsigned t) {
   const MmParams& P = T.P;
   const int n = P.parts * P.groups;
   const int ftile = MODE == kForward && P.act == HOC_ACT_SWIGLU ? kTcFeatures / 2 : kTcFeatures;
@@ -445,12 +444,19 @@ struct Work {
     now = ahead;
     ends = ahead_ends;
   }
-  template <int MODE>
-  __device__ __forceinline__ void first() {
-    look_ahead<MODE>();
-    next();
-  }
 };
+// f() for each tile, W.now being the tile and the next one looked up already; until
+// it returns false.
+template <int MODE, class F>
+__device__ __forceinline__ void each_tile(Work& W, bool rows, F f) {
+  for (;;) {  // once without a tile, so that the look-up stands in one place
+    W.look_ahead<MODE>(rows);
+    if (!W.more && W.T.P.seg == nullptr) after_previous();
+    if (W.more && !f()) return;
+    if (!W.ahead_more) return;
+    W.next();
+  }
+}
 
 // How 64 virtual rows, a group of 8 per lane modulo 8, are fetched: a run of groups
 // that follow one another in the buffer by copies of 64, 32, 16 and 8 rows, as the
@@ -860,11 +866,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();
   cluster_arrive();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  mm_count(P, MODE == kWgrad ? kTcDepth : 8, S->vrows, S->tile0,
-           [&](int rows) { return MODE == kWgrad ? 0u : T.rows.of(rows) * T.ftiles.d; });
-  order_pairs<MODE>(T, S);
+  if (P.seg != nullptr) {
+    after_previous();
+    mm_count(P, MODE == kWgrad ? kTcDepth : 8, S->vrows, S->tile0,
+             [&](int rows) { return MODE == kWgrad ? 0u : T.rows.of(rows) * T.ftiles.d; });
+    order_pairs<MODE>(T, S);
+  } else {  // one range: nothing is read before the operands, which each role waits for itself
+    if (threadIdx.x == 0) {
+      const int pad = MODE == kWgrad ? kTcDepth : 8, rows = int((P.cap[0] + pad - 1) / pad * pad);
+      const unsigned whole = T.rows.of(rows);
+      S->vrows[0] = rows;
+      S->tile0[0] = 0;
+      S->tile0[1] = whole * T.ftiles.d;
+      S->order[0] = 0;
+      S->lower = rows > int(whole) * T.tile_rows;
+    }
+    __syncthreads();
+  }
   __syncwarp();
   cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -885,10 +903,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
     // Waits until the MMAs have released the stage's last filling.
     auto free = [&]() { return k.round == 0 || warp_wait(&S->empty[k.st], (k.round - 1) & 1, T, S); };
     Work W(T, S, who, of, tiles);
-    for (W.first<MODE>(); ok && W.more; W.next()) {
+    each_tile<MODE>(W, true, [&]() {
       const Tile& A = W.now;
       const Ranges R = load_ranges<MODE == kWgrad ? kTcDepth : 8>(P, A.p, W.ends);
-      W.look_ahead<MODE>();
       const int half = A.n / 2;  // rows of B in this CTA (wgrad: features)
       if (MODE != kWgrad) {
         // This warp's 64 rows of B, a group of 8 per lane modulo 8
@@ -965,7 +982,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
           k.next();
         }
       }
-    }
+      return ok;
+    });
     // The MMAs' last releases of the stages have to land before this CTA may leave.
     for (uint32_t j = 0; ok && j < T.stages; ++j, k.next()) ok = !own(k.st) || free();
   } else if (MODE != kWgrad && warp == 3) {
@@ -975,9 +993,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
     Turn k(T.stages);
     bool ok = true;
     Work W(T, S, who, of, tiles);
-    for (W.first<MODE>(); ok && W.more; W.next()) {
+    each_tile<MODE>(W, false, [&]() {
       const Tile& A = W.now;
-      W.look_ahead<MODE>(false);
       const int fa = A.f0 + rank * (gated ? 64 : 128);
       for (int s = 0; s < A.steps; ++s, k.next()) {
         if (k.round && !warp_wait(&S->empty[k.st], (k.round - 1) & 1, T, S)) {
@@ -999,7 +1016,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
         }
         __syncwarp();
       }
-    }
+      return ok;
+    });
   } else if (warp == 1 && rank == 0) {
     // ---- MMA
     const bool one = elect_one();
@@ -1011,33 +1029,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
     const uint64_t a0 = MODE == kForward ? smem_desc(base, 16, 1024) : smem_desc(base, 8192, 1024);
     const uint64_t b0 = MODE == kWgrad ? smem_desc(base + kTcOperand, 8192, 1024) : smem_desc(base + kTcOperand, 16, 1024);
     Work W(T, S, who, of, tiles);
-    for (W.first<MODE>(); ok && W.more; W.next()) {
+    for (;;) {  // once without a tile: the next one is looked up under a tile's first products
       const Tile& A = W.now;
-      if (A.steps == 0) W.look_ahead<MODE>(false);
-      if (A.steps == 0) continue;  // an expert without rows: the epilogue writes zeros
+      const bool run = W.more && A.steps > 0;  // an expert without rows: the epilogue writes zeros
       const uint32_t idesc = kind | (uint32_t(A.n / 8) << 17);
       const uint32_t acc = it & 1, d = tmem + acc * 256u;
-      if (it >= 2 && !warp_wait(&S->acc_empty[acc], ((it >> 1) - 1) & 1, T, S)) break;
+      if (run && it >= 2 && !warp_wait(&S->acc_empty[acc], ((it >> 1) - 1) & 1, T, S)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (int s = 0; s < A.steps; ++s, k.next()) {
-        if (!warp_wait(&S->full[k.st], k.round & 1, T, S)) {
-          ok = false;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t da = a0 + k.st * (T.stage >> 4), db = b0 + k.st * (T.stage >> 4);
-        if (one) {
+      const int steps = run ? A.steps : 1;
+      for (int s = 0; s < steps; ++s) {
+        if (run) {
+          if (!warp_wait(&S->full[k.st], k.round & 1, T, S)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t da = a0 + k.st * (T.stage >> 4), db = b0 + k.st * (T.stage >> 4);
+          if (one) {
 #pragma unroll
-          for (int q = 0; q < kTcDepth / 16; ++q)  // 16 deep: 32 bytes along a K-major row, 16 rows of an M/N-major block
-            mma_pair(d, da + q * (MODE == kForward ? 2 : 128), db + q * (MODE == kWgrad ? 128 : 2), idesc, s | q);
-          commit_pair(&S->empty[k.st]);
+            for (int q = 0; q < kTcDepth / 16; ++q)  // 16 deep: 32 bytes along a K-major row, 16 rows of an M/N-major block
+              mma_pair(d, da + q * (MODE == kForward ? 2 : 128), db + q * (MODE == kWgrad ? 128 : 2), idesc, s | q);
+            commit_pair(&S->empty[k.st]);
+          }
+          __syncwarp();
+          k.next();
         }
-        __syncwarp();
-        if (s == 0) W.look_ahead<MODE>(false);  // under the first stage's products
+        if (s == 0) W.look_ahead<MODE>(false);
       }
-      if (ok && one) commit_pair(&S->acc_full[acc]);
-      __syncwarp();
-      ++it;
+      if (!ok) break;
+      if (run) {
+        if (one) commit_pair(&S->acc_full[acc]);
+        __syncwarp();
+        ++it;
+      }
+      if (!W.ahead_more) break;
+      W.next();
     }
   } else if (MODE == kWgrad && (warp == 2 || warp == 3 || warp > 12)) {
     // ---- zero the padding rows of the stages that hold any, then hand them to the
@@ -1050,10 +1076,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
     uint32_t phases = 0;  // bit st: parity of part[st]
     bool ok = true;
     Work W(T, S, who, of, tiles);
-    for (W.first<MODE>(); ok && W.more; W.next()) {
+    each_tile<MODE>(W, true, [&]() {
       const Tile& A = W.now;
       const Ranges R = load_ranges<kTcDepth>(P, A.p, W.ends);
-      W.look_ahead<MODE>();
       for (int s = 0; s < A.steps;) {
         int row, valid;
         const int run = stage_rows(P, A, R, s, row, valid);
@@ -1085,7 +1110,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
         __syncwarp();
         if (lane == 0) arrive_cluster(full0 + st * 8u);
       }
-    }
+      return ok;
+    });
   } else if (warp >= 4 && warp < 4 + kTcEpilogue) {
     // ---- epilogue: two groups of four warps take turns along the columns
     const int q = warp & 3, eg = (warp - 4) / 4;
@@ -1093,7 +1119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
     unsigned char* out = MODE == kForward && T.planes > 2 ? in + 3 * kTcPlane : in;
     uint32_t it = 0, turn = 0, buffer = 0;
     Work W(T, S, who, of, tiles);
-    for (W.first<MODE>(); W.more; W.next()) {
+    each_tile<MODE>(W, MODE != kWgrad, [&]() {
       const Tile& A = W.now;
       int row = 0, valid = 0;
       float bias = 0.f;
@@ -1104,8 +1130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
         if (MODE == kForward && P.bias[A.p] && f < P.out)
           bias = bf16_of(P.bias[A.p] + int64_t(A.g) * (gated ? 2 : 1) * P.out + (gated && lane >= 16 ? P.out : 0) + f);
       }
-      W.look_ahead<MODE>(MODE != kWgrad);
-      if (MODE == kWgrad && A.steps == 0 && P.accumulate) continue;  // an expert without rows adds nothing
+      if (MODE == kWgrad && A.steps == 0 && P.accumulate) return true;  // an expert without rows adds nothing
       const uint32_t acc = it & 1;
       const uint32_t at = tmem + acc * 256u + (uint32_t(q * 32) << 16);
       bool ok = true;
@@ -1117,13 +1142,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
                                                       (it >> 1) & 1, eg, q, rank, row, valid, bias);
         });
       }
-      if (!ok) break;
-      if (A.steps == 0) continue;  // no accumulator was used
+      if (!ok) return false;
+      if (A.steps == 0) return true;  // no accumulator was used
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive_relaxed(on_first(&S->acc_empty[acc]));
       ++it;
-    }
+      return true;
+    });
   }
   __syncwarp();
   if (S->dead) {
