@@ -13,7 +13,8 @@
 // a stage moves 32 KB into each SM for 128 x 256 x 64 products.  Operands come
 // by tensor copies into 128-byte-swizzled stages; accumulators are double
 // buffered in tensor memory, so the epilogue of a tile runs under the products of
-// the next one.
+// the next one.  Where one range of rows makes few tiles, two or four pairs of a
+// cluster share the contraction of a tile.
 //
 // An expert's rows lie in one range per source.  They are taken as one virtual
 // row space in which every range is padded to a multiple of 8, the height of a
@@ -55,6 +56,7 @@ constexpr uint32_t kTcStage = 2 * kTcOperand;
 constexpr int kTcFeatures = 256;                // of a pair's tile
 constexpr int kTcRows = 256;                    // at most, of a tile
 constexpr unsigned kTcPanel = 8;                // row tiles of a panel (see tile_at)
+constexpr int kTcMostShares = 2;                // log2: clusters of 8 CTAs
 constexpr uint32_t kTcTmemColumns = 512;        // two accumulators of 256 columns
 constexpr uint64_t kTcWaitNs = 2000000000ull;
 
@@ -81,6 +83,8 @@ struct TcParams {
   uint32_t stages;   // as many as the epilogue's planes leave room for: 5 or 6 of a tile of 256 rows
   uint32_t planes;   // staged arrays of each of the two epilogue groups
   int loose;         // what the epilogue moves is not whole 16-byte vectors
+  int log_shares;    // CTA pairs that share the contraction of a tile: 1, 2 or 4, all of one cluster
+  int per;           // stages of each of them (the last may have fewer); INT_MAX where there is one
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
   uint64_t wait_ns;
   MmParams P;
@@ -97,6 +101,7 @@ struct TcShared {
   uint64_t empty[kTcMostStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];      // on the first CTA: the epilogue warps of both CTAs
+  uint64_t go, came;          // shares: the others' stages may be written to; their sums for this one's columns are here
   uint32_t tmem;
   volatile int dead;
   int vrows[kMmMaxGroups];
@@ -114,12 +119,14 @@ __device__ __forceinline__ uint32_t cta_rank() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// The address, in the cluster's shared memory, of the first CTA's copy of a local barrier.
-__device__ __forceinline__ uint32_t on_first(const uint64_t* bar) {
+// The address, in the cluster's shared memory, of another CTA's copy of what is at a
+// local address; of the pair's first CTA's copy of a barrier.
+__device__ __forceinline__ uint32_t on_cta(uint32_t addr, uint32_t cta) {
   uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_addr(bar)));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
   return a;
 }
+__device__ __forceinline__ uint32_t on_first(const uint64_t* bar) { return on_cta(ptx::smem_addr(bar), cta_rank() & ~1u); }
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -133,12 +140,25 @@ __device__ __forceinline__ void arrive_expect_cluster(uint32_t addr, uint32_t tx
 __device__ __forceinline__ void arrive_relaxed(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(ptx::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Waits for the phase with `parity`; false when the limit passed here or in
-// another role, after which the caller leaves its loop.
+// another role, after which the caller leaves its loop.  CLUSTER: what other CTAs'
+// threads wrote before they arrived is to be read.
+template <bool CLUSTER>
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const TcParams& T, TcShared* S) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+  auto came = [&]() { return CLUSTER ? try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+  if (came()) return true;
   const uint64_t deadline = ptx::global_ns() + T.wait_ns;
-  while (!ptx::mbar_try_wait(bar, parity)) {
+  while (!came()) {
     if (S->dead) return false;
     if (ptx::global_ns() > deadline) {
       atomicOr(T.P.status, 4);
@@ -149,8 +169,9 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, con
   return true;
 }
 // The same by a whole warp, with one answer for all lanes.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const TcParams& T, TcShared* S) {
-  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, T, S));
+  return __all_sync(0xFFFFFFFFu, wait_bounded<CLUSTER>(bar, parity, T, S));
 }
 // Programmatic dependent launch: waits for the kernel before this one on the
 // stream, then lets the next one start.
@@ -214,7 +235,7 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           ptx::smem_addr(bar)),
-      "h"(uint16_t(3))
+      "h"(uint16_t(3u << (cta_rank() & ~1u)))
       : "memory");
 }
 __device__ __forceinline__ void tmem_load(uint32_t (&r)[kTcColumns], uint32_t addr) {
@@ -232,7 +253,7 @@ struct Tile {
   int p, g;     // rank buffer, expert
   int f0;       // first feature
   int c0, n;    // first row (virtual row; wgrad: out feature) and the MMA's N
-  int steps;    // stages of the contraction
+  int steps;    // stages of the contraction, this share's
 };
 
 // The order of the tiles: whole ones first, pair by pair, then the lower tile that
@@ -328,6 +349,7 @@ __device__ __noinline__ Tile tile_at(const TcParams& T, const TcShared* S, unsig
   const int rows = S->vrows[i];
   A.n = (min(T.tile_rows, (MODE == kWgrad ? P.out : rows) - A.c0) + 31) / 32 * 32;
   A.steps = ((MODE == kForward ? P.in : MODE == kDgrad ? P.out : rows) + kTcDepth - 1) / kTcDepth;
+  A.steps = min(A.steps - int(cta_rank() >> 1) * T.per, T.per);
   return A;
 }
 
@@ -445,13 +467,21 @@ struct Work {
     ends = ahead_ends;
   }
 };
+// Before a warp uses what the cluster's CTAs set up, and reads or writes what the kernel
+// before this one may: each does it once, when it has looked up its first tile.
+__device__ __forceinline__ void begin(const TcParams& T) {
+  __syncwarp();
+  cluster_wait();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (T.P.seg == nullptr) after_previous();  // with ranges, it was needed before they were read
+}
 // f() for each tile, W.now being the tile and the next one looked up already; until
 // it returns false.
 template <int MODE, class F>
 __device__ __forceinline__ void each_tile(Work& W, bool rows, F f) {
   for (;;) {  // once without a tile, so that the look-up stands in one place
     W.look_ahead<MODE>(rows);
-    if (!W.more && W.T.P.seg == nullptr) after_previous();
+    if (!W.more) begin(W.T);
     if (W.more && !f()) return;
     if (!W.ahead_more) return;
     W.next();
@@ -606,13 +636,79 @@ __device__ __forceinline__ void put_bf16(unsigned char* p, float v) {
   *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(v);
 }
 
+// Shares of a contraction.  Where a product has few tiles, the CTA pairs of a cluster
+// compute one together, each from a part of the contraction: one pair would stream
+// its operands through two SMs while the others idle.  Each then has sums of the
+// whole tile; the columns are dealt out in blocks of two epilogue steps, and a CTA
+// sends the sums of the others' columns into their stages, which are free once all
+// products of those CTAs are done.  The sums are added in the order of the shares,
+// whoever adds them.  64 rows of 7168 -> 512 columns take 20 us with four shares, 26
+// with two and 36 with one; 64 x 4096 x 4096 22 us with two and 26 with one; the weight
+// gradient of 8192 rows of 512 x 512 22, 26 and 38 us.
+constexpr uint32_t kTcSums = kTcColumns * 128 * 4;  // bytes of a step: [4 columns][lane][4]
+
+// Where the sums of share `from` for the step at `col` lie in the stages of the step's owner `to`.
+__device__ __forceinline__ uint32_t sums_at(const TcParams& T, int col, int from, int to) {
+  const int j = col / kTcColumns, others = (1 << T.log_shares) - 1;
+  return uint32_t(((j >> (1 + T.log_shares)) * 2 + (j & 1)) * others + (from < to ? from : from - 1)) * kTcSums +
+         (threadIdx.x & 127) * 16u;
+}
+// Sends the sums of the other shares' columns (of the steps whose number is eg modulo
+// 2) and waits for those of this one's.  Whole warps call it, after their accumulator came.
+__device__ __forceinline__ bool exchange_sums(const TcParams& T, TcShared* S, int n, uint32_t stages, uint32_t acc_at,
+                                              int eg) {
+  const int cta = int(cta_rank()), mine = cta >> 1, rank = cta & 1, shares = 1 << T.log_shares, lane = threadIdx.x & 31;
+  if ((threadIdx.x & ~31u) == 128 && lane < shares && lane != mine)  // this CTA's products are done
+    arrive_cluster(on_cta(ptx::smem_addr(&S->go), 2 * lane + rank));
+  __syncwarp();
+  if (!warp_wait<true>(&S->go, 0, T, S)) return false;
+  for (int col = eg * kTcColumns; col < n; col += 2 * kTcColumns) {
+    const int to = (col / (2 * kTcColumns)) & (shares - 1);
+    if (to == mine) continue;
+    uint32_t v[kTcColumns];
+    tmem_load(v, acc_at + uint32_t(col));
+    const uint32_t at = on_cta(stages + sums_at(T, col, mine, to), 2 * to + rank);
+#pragma unroll
+    for (int j = 0; j < kTcColumns; j += 4)
+      asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + j * 512u), "r"(v[j]), "r"(v[j + 1]),
+                   "r"(v[j + 2]), "r"(v[j + 3])
+                   : "memory");
+  }
+  __syncwarp();
+  if (lane < shares && lane != mine) arrive_cluster(on_cta(ptx::smem_addr(&S->came), 2 * lane + rank));
+  __syncwarp();
+  return warp_wait<true>(&S->came, 0, T, S);
+}
+// Adds the other shares' sums to this one's, v, of the step at `col`.
+__device__ __forceinline__ void add_sums(const TcParams& T, uint32_t (&v)[kTcColumns], uint32_t stages, int col) {
+  const int mine = int(cta_rank()) >> 1, shares = 1 << T.log_shares;
+  float sum[kTcColumns];
+#pragma unroll
+  for (int j = 0; j < kTcColumns; ++j) sum[j] = 0.f;
+  for (int s = 0; s < shares; ++s) {
+    const uint32_t at = stages + sums_at(T, col, s, mine);
+#pragma unroll
+    for (int j = 0; j < kTcColumns; j += 4) {
+      uint32_t x[4] = {v[j], v[j + 1], v[j + 2], v[j + 3]};
+      if (s != mine)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(at + j * 512u));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[j + i] += __uint_as_float(x[i]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kTcColumns; ++j) v[j] = __float_as_uint(sum[j]);
+}
+
 // The epilogue of one tile by group `eg` of four warps (warp q of it has tensor
 // memory lanes 32 q ..): the steps of kTcColumns columns whose number is eg modulo
 // 2.  in: the group's three input buffers (dgrad: of two planes each); out: its two
 // output planes, which the arrays that are stored take in turn; turn and buffer go on
 // from tile to tile.  False when the accumulator did not come.
 template <int MODE, int ACT>
-__device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, const Tile& A, unsigned char* in,
+__device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, const Tile& A, uint32_t stages, unsigned char* in,
                                              unsigned char* out, uint32_t& turn, uint32_t& buffer, uint32_t acc_at, uint64_t* acc_full,
                                              uint32_t parity, int eg, int q, int rank, int row, int valid, float bias) {
   constexpr bool gated = MODE == kForward && ACT == HOC_ACT_SWIGLU;
@@ -647,26 +743,29 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  const int first = eg * kTcColumns;
+  const int mine = int(cta_rank()) >> 1, stride = (2 * kTcColumns) << T.log_shares;
+  const int first = eg * kTcColumns + mine * 2 * kTcColumns;
   if (reads) {  // the buffer of the last tile's last step may still be read: the two others
     fetch(first, buffer);
-    fetch(first + 2 * kTcColumns, buffer == 2 ? 0 : buffer + 1);
+    fetch(first + stride, buffer == 2 ? 0 : buffer + 1);
   }
-  const bool ok = warp_wait(acc_full, parity, T, S);
+  bool ok = warp_wait(acc_full, parity, T, S);
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (ok && T.log_shares) ok = exchange_sums(T, S, A.n, stages, acc_at, eg);
   if (!group_all(eg, ok)) {
     if (reads) asm volatile("cp.async.wait_all;" ::: "memory");
     return false;
   }
-  for (int col = first; col < A.n; col += 2 * kTcColumns) {
+  for (int col = first; col < A.n; col += stride) {
     uint32_t v[kTcColumns];
     tmem_load(v, acc_at + uint32_t(col));
+    if (T.log_shares) add_sums(T, v, stages, col);
     auto at = [&](int c) { return row_of(col, c, row, valid); };
     unsigned char* x = in + buffer * kBuffer;
     if (reads) {
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       group_barrier(eg);  // this step's input is there, and the buffer of the step before is free
-      fetch(col + 4 * kTcColumns, buffer == 0 ? 2 : buffer - 1);
+      fetch(col + 2 * stride, buffer == 0 ? 2 : buffer - 1);
       buffer = buffer == 2 ? 0 : buffer + 1;
     }
     // Where the arrays to be stored are staged: in the place of what was read, or in the next output plane.
@@ -747,8 +846,8 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
 // The same for the weight gradient: columns are out features, rows of the weight;
 // nothing is read but the weights that are added to.
 constexpr int kWgColumns = 16;
-__device__ __forceinline__ bool run_wgrad_epilogue(const TcParams& T, TcShared* S, const Tile& A, unsigned char* out,
-                                                   uint32_t& turn, uint32_t acc_at, uint64_t* acc_full,
+__device__ __forceinline__ bool run_wgrad_epilogue(const TcParams& T, TcShared* S, const Tile& A, uint32_t stages,
+                                                   unsigned char* out, uint32_t& turn, uint32_t acc_at, uint64_t* acc_full,
                                                    uint32_t parity, int eg, int q, int rank) {
   const MmParams& P = T.P;
   const int lane = threadIdx.x & 31, i = int(threadIdx.x) & 127;
@@ -757,12 +856,15 @@ __device__ __forceinline__ bool run_wgrad_epilogue(const TcParams& T, TcShared* 
   if (A.steps > 0) {
     ok = warp_wait(acc_full, parity, T, S);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (ok && T.log_shares) ok = exchange_sums(T, S, A.n, stages, acc_at, eg);
   }
   if (!group_all(eg, ok)) return false;
-  for (int col = eg * kWgColumns; col < A.n; col += 2 * kWgColumns) {
+  const int mine = int(cta_rank()) >> 1;
+  for (int col = (eg + 2 * mine) * kWgColumns; col < A.n; col += (2 * kWgColumns) << T.log_shares) {
     uint32_t v[kWgColumns];
     if (A.steps > 0) {
       tmem_load(v, acc_at + uint32_t(col));
+      if (T.log_shares) add_sums(T, v, stages, col);
     } else {
 #pragma unroll
       for (int j = 0; j < kWgColumns; ++j) v[j] = 0;
@@ -824,7 +926,7 @@ static_assert(kWgColumns == kTcColumns, "the planes are of one size");
 static_assert(stages_in(2, kTcStage) == 6 && stages_in(6, kTcStage) == 5, "stages of a tile of 256 rows");
 
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
+__global__ void __launch_bounds__(kTcThreads<MODE>, 1)
     mm_tc_kernel(const __grid_constant__ TcParams T) {
   extern __shared__ unsigned char raw[];
   const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
@@ -833,7 +935,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
   TcShared* S = reinterpret_cast<TcShared*>(planes + 2 * T.planes * kTcPlane);
   const MmParams& P = T.P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = int(cta_rank());
+  const int rank = int(cta_rank()) & 1;  // in the pair
+  const int from = int(cta_rank() >> 1) * T.per;  // this share's first stage
   const bool gated = MODE == kForward && P.act == HOC_ACT_SWIGLU;
 
   if (threadIdx.x == 0) {
@@ -846,6 +949,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
       ptx::mbar_init(&S->acc_full[a], 1);
       ptx::mbar_init(&S->acc_empty[a], 2 * kTcEpilogue);
     }
+    ptx::mbar_init(&S->go, (1 << T.log_shares) - 1 + (T.log_shares == 0));
+    ptx::mbar_init(&S->came, ((1 << T.log_shares) - 1) * kTcEpilogue + (T.log_shares == 0));
     S->dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -883,13 +988,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
     }
     __syncthreads();
   }
-  __syncwarp();
-  cluster_wait();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = S->tmem;
   const unsigned tiles = MODE == kWgrad ? unsigned(P.parts * P.groups) * T.each.d
                                         : S->tile0[P.parts * P.groups] + unsigned(S->lower) * T.ftiles.d;
-  const unsigned who = blockIdx.x >> 1, of = gridDim.x >> 1;
+  const unsigned who = blockIdx.x >> (1 + T.log_shares), of = gridDim.x >> (1 + T.log_shares);
 
   if (warp == 0 || warp == (MODE == kWgrad ? 12 : 2)) {
     // ---- tensor copies of the rows.  The whole warp walks the stages, so that
@@ -925,7 +1027,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
           const uint32_t b = base + k.st * T.stage + kTcOperand + block * 8192u, bar = full0 + k.st * 8u;
           if (one) arrive_expect_cluster(bar, bytes);
           __syncwarp();
-          if (lane < 8 && box >= 0) copy2(b + uint32_t(lane) * 1024u, map, s * kTcDepth, row, bar);
+          if (lane < 8 && box >= 0) copy2(b + uint32_t(lane) * 1024u, map, (from + s) * kTcDepth, row, bar);
           __syncwarp();
         }
       } else {
@@ -933,13 +1035,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
         const uint32_t bytes = kTcOperand + uint32_t(blocks) * 8192u + T.tx_pad;
         const int fx = A.f0 + rank * 128, fd = A.c0 + rank * half;
         for (int s = 0; ok && s < A.steps;) {
-          if (P.sources <= 32 && s >= R.wholes / kTcDepth && !own(k.st)) {  // remainders, the other warp's
+          if (P.sources <= 32 && from + s >= R.wholes / kTcDepth && !own(k.st)) {  // remainders, the other warp's
             ++s;
             k.next();
             continue;
           }
           int row, valid;
-          const int run = stage_rows(P, A, R, s, row, valid);
+          const int run = min(stage_rows(P, A, R, from + s, row, valid), A.steps - s);
           int r = __shfl_sync(0xFFFFFFFFu, row, 0);
           for (int i = 0; i < run; ++i, r += kTcDepth, k.next()) {
             if (!own(k.st)) continue;
@@ -1002,7 +1104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
           break;
         }
         const uint32_t a = base + k.st * T.stage, bar = full0 + k.st * 8u;
-        const int x = s * kTcDepth;
+        const int x = (from + s) * kTcDepth;
         if (one) {
           arrive_expect_cluster(bar, kTcOperand);
           if (MODE == kDgrad) {
@@ -1056,6 +1158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
         }
         if (s == 0) W.look_ahead<MODE>(false);
       }
+      if (!W.more) begin(T);
       if (!ok) break;
       if (run) {
         if (one) commit_pair(&S->acc_full[acc]);
@@ -1081,7 +1184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
       const Ranges R = load_ranges<kTcDepth>(P, A.p, W.ends);
       for (int s = 0; s < A.steps;) {
         int row, valid;
-        const int run = stage_rows(P, A, R, s, row, valid);
+        const int run = min(stage_rows(P, A, R, from + s, row, valid), A.steps - s);
         for (int i = 0; i < run; ++i) k.next();
         s += run;
         if (run > 0) continue;
@@ -1135,10 +1238,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
       const uint32_t at = tmem + acc * 256u + (uint32_t(q * 32) << 16);
       bool ok = true;
       if constexpr (MODE == kWgrad) {
-        ok = run_wgrad_epilogue(T, S, A, out, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q, rank);
+        ok = run_wgrad_epilogue(T, S, A, base, out, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q, rank);
       } else {
         with_act(P.act, [&](auto tag) {
-          ok = run_epilogue<MODE, decltype(tag)::act>(T, S, A, in, out, turn, buffer, at, &S->acc_full[acc],
+          ok = run_epilogue<MODE, decltype(tag)::act>(T, S, A, base, in, out, turn, buffer, at, &S->acc_full[acc],
                                                       (it >> 1) & 1, eg, q, rank, row, valid, bias);
         });
       }
@@ -1150,6 +1253,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads<MODE>, 1)
       ++it;
       return true;
     });
+  } else {
+    begin(T);
   }
   __syncwarp();
   if (S->dead) {
@@ -1228,51 +1333,61 @@ int choose_rows_ragged(const MmParams& P) {
   return each <= 32 ? 64 : each <= 64 ? 128 : kTcRows;
 }
 
-// The launch but for its grid and stream, and the CTA pairs that fit the device at
-// once (asked once for each kernel and device).
-cudaError_t configure(const void* fn, int mode, size_t smem, cudaLaunchAttribute (&attr)[2], cudaLaunchConfig_t& cfg,
-                      int& pairs) {
-  static std::atomic<int> known[3][64];
+// The launch but for its grid and stream, and the clusters that fit the device at
+// once (asked once for each kernel, cluster size and device).
+cudaError_t configure(const void* fn, int mode, int log_shares, cudaLaunchAttribute (&attr)[2], cudaLaunchConfig_t& cfg,
+                      int& clusters) {
+  static std::atomic<int> known[3][kTcMostShares + 1][64];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2u << log_shares;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(mode == kWgrad ? kTcThreads<kWgrad> : kTcThreads<kForward>);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kTcSmem;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmem));
   if (e != cudaSuccess) return e;
   int dev = 0;
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  pairs = dev < 64 ? known[mode][dev].load() : 0;
-  if (pairs > 0) return cudaSuccess;
+  clusters = dev < 64 ? known[mode][log_shares][dev].load() : 0;
+  if (clusters > 0) return cudaSuccess;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(2);
-  e = cudaOccupancyMaxActiveClusters(&pairs, fn, &cfg);
+  cfg.gridDim = dim3(2u << log_shares);
+  e = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg);
   cfg.numAttrs = 2;
-  if (e == cudaSuccess && pairs < 1) e = cudaErrorInvalidConfiguration;
-  if (e == cudaSuccess && dev < 64) known[mode][dev].store(pairs);
+  if (e == cudaSuccess && clusters < 1) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess && dev < 64) known[mode][log_shares][dev].store(clusters);
   return e;
 }
 
-// Rows of a tile.  Where the number of rows is known (one range, or the features
-// of the weight gradient) the height whose tiles fill the CTA pairs best: a wave
-// costs about 256 + T for tiles of T rows (its features' operand comes with every
-// tile), e.g. 4096 rows x 16 feature tiles on 76 pairs: 4 waves of 224 rows instead
-// of 4 of 256 (101 -> 95 us at 4096 deep).
-int choose_rows(int64_t rows, int64_t others, int pairs) {
-  int best = kTcRows;
+// Rows of a tile, and shares of its contraction, where the number of rows is known (one
+// range, or the features of the weight gradient): those that take the fewest cycles.
+// With several waves of tiles a stage of r rows costs about 256 + r (its features'
+// operand comes with every tile), e.g. 4096 rows x 16 feature tiles on 76 pairs: 4 waves
+// of 224 rows instead of 4 of 256 (101 -> 95 us at 4096 deep); a single wave waits for
+// memory, about 640 a stage whatever its height.  Sharing costs two hand-overs across
+// the cluster and the sums' way.
+struct Cut {
+  int rows, log_shares;
+};
+Cut choose_cut(int64_t rows, int64_t others, int64_t steps, const int* clusters, int most_shares) {
+  Cut best{kTcRows, 0};
   int64_t least = INT64_MAX;
-  for (int r = kTcRows; r >= 64; r -= 32) {
-    const int64_t tiles = (rows + r - 1) / r * others, cost = (tiles + pairs - 1) / pairs * (256 + r);
-    if (cost < least) {
-      least = cost;
-      best = r;
+  for (int r = kTcRows; r >= 64; r -= 32)
+    for (int log = 0; log <= most_shares; ++log) {
+      const int64_t tiles = (rows + r - 1) / r * others, waves = (tiles + clusters[log] - 1) / clusters[log];
+      const int64_t per = (steps + (1 << log) - 1) >> log;
+      if (log && (waves > 1 || per * ((1 << log) - 1) >= steps)) continue;
+      const int64_t stage = waves == 1 ? 640 : waves * (r < 144 ? 400 : 256 + r);
+      const int64_t cost = stage * per + (16 * r >> log) + (log == 0 ? 0 : log == 1 ? 3000 + 32 * r : 4000 + 48 * r);
+      if (cost < least) {
+        least = cost;
+        best = {r, log};
+      }
     }
-  }
   return best;
 }
 
@@ -1303,7 +1418,6 @@ static bool is_loose(const MmParams& P, int mode) {
 cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   TcParams T;
   T.P = P;
-  T.tile_rows = kTcRows;
   T.loose = is_loose(P, mode);
   const char* fault = getenv("HOC_FAULT");
   const bool stall = fault && !strcmp(fault, "mm_stall");
@@ -1312,16 +1426,26 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kTc[mode]);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
-  int pairs = 0;
-  cudaError_t e = configure(fn, mode, kTcSmem, attr, cfg, pairs);
-  if (e != cudaSuccess) return e;
-  cfg.stream = s;
+  cudaError_t e = cudaSuccess;
   int64_t tiles = 0;
   const int ftile = mode == kForward && P.act == HOC_ACT_SWIGLU ? kTcFeatures / 2 : kTcFeatures;
   const int64_t ftiles = ((mode == kForward ? P.out : P.in) + ftile - 1) / ftile;
-  if (mode == kWgrad) T.tile_rows = choose_rows(P.out, ftiles * P.groups * P.parts, pairs);
-  else if (P.seg == nullptr) T.tile_rows = choose_rows(P.cap[0], ftiles, pairs);
-  else T.tile_rows = choose_rows_ragged(P);
+  const int64_t depth = mode == kForward ? P.in : mode == kDgrad ? P.out : P.cap[P.part0];
+  const int64_t steps = (depth + kTcDepth - 1) / kTcDepth;
+  Cut cut{0, 0};
+  int clusters[kTcMostShares + 1] = {};
+  const int most = P.seg == nullptr ? kTcMostShares : 0;
+  for (int log = most; log >= 0 && e == cudaSuccess; --log) e = configure(fn, mode, log, attr, cfg, clusters[log]);
+  if (e != cudaSuccess) return e;
+  if (mode == kWgrad) cut = choose_cut(P.out, ftiles * P.groups * P.parts, steps, clusters, most);
+  else if (P.seg == nullptr) cut = choose_cut(P.cap[0], ftiles, steps, clusters, most);
+  else cut.rows = choose_rows_ragged(P);
+  T.tile_rows = cut.rows;
+  T.log_shares = cut.log_shares;
+  T.per = T.log_shares ? int((steps + (1 << T.log_shares) - 1) >> T.log_shares) : INT_MAX;
+  if (T.log_shares) e = configure(fn, mode, T.log_shares, attr, cfg, clusters[T.log_shares]);
+  if (e != cudaSuccess) return e;
+  cfg.stream = s;
   T.stage = mode == kWgrad ? kTcStage : kTcOperand + uint32_t(T.tile_rows) * (kTcDepth * 2 / 2);
   bool reads = mode == kDgrad && P.act != HOC_ACT_NONE;
   for (int p = 0; mode == kForward && p < P.part0 + P.parts; ++p) reads = reads || P.res[p] != nullptr;
@@ -1345,7 +1469,8 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
     }
     if (!ok) return cudaErrorInvalidValue;
   }
-  cfg.gridDim = dim3(2 * unsigned(tiles < 1 ? 1 : tiles < pairs ? tiles : pairs));
+  const int at_once = clusters[T.log_shares];
+  cfg.gridDim = dim3(unsigned(tiles < 1 ? 1 : tiles < at_once ? tiles : at_once) << (1 + T.log_shares));
   return cudaLaunchKernelEx(&cfg, kTc[mode], T);
 }
 

@@ -568,3 +568,40 @@ def test_every_expert_tile_order():
         has = L.of[0] >= 0
         ref.close(y[has], want[has], err[has], "y")
         assert bool((y[~has] == 7).all()) and st.item() == 0
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("rows,inp,out", [(33, 8192, 512), (70, 4104, 296), (257, 1000, 256), (40, 328, 8), (130, 520, 2056),
+                                          (2100, 40, 24), (1025, 264, 520), (5000, 72, 128)])
+def test_a_contraction_shared_by_several_ctas(rows, inp, out, act):
+    """Few tiles and a long contraction, of x's or dy's width or of the rows."""
+    mul = 2 if act == "swiglu" else 1
+    x, w, b = normal(rows, inp, seed=1), normal(mul * out, inp, seed=2, sigma=inp ** -0.5), normal(mul * out, seed=3)
+    r, dy = normal(rows, out, seed=4), normal(rows, out, seed=5)
+    wd, below = w[:out], normal(rows, mul * inp, seed=6)
+    st = status()
+    got = []
+    for _ in range(3):
+        y, pre = torch.empty(rows, out, dtype=BF, device=DEV), torch.empty(rows, mul * out, dtype=BF, device=DEV)
+        dx = torch.empty(rows, mul * inp, dtype=BF, device=DEV)
+        dw, db = torch.empty(out, inp, device=DEV), torch.empty(out, device=DEV)
+        dwb = torch.ones(out, inp, dtype=BF, device=DEV)
+        hoc.linear(x, w, y, status=st, bias=b, act=act, pre=pre, residual=r)
+        hoc.linear_dgrad(dy, wd, dx, status=st, act=act, pre=below if act != "none" else None)
+        hoc.linear_wgrad(dy, x, dw, status=st, db=db)
+        hoc.linear_wgrad(dy, x, dwb, status=st, accumulate=True)
+        got.append((y, pre, dx, dw, db, dwb))
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert all(torch.equal(a, c) for other in got[1:] for a, c in zip(got[0], other)), "the order of the sums changed"
+    z, ez, want, ey = ref.forward(x, w, b, act)
+    ref.close(pre, z, ez, "pre")
+    want = want + r.double()
+    ref.close(y, want, ey + want.abs() * ref.F32, "y")
+    want, err = ref.dgrad(dy, wd, act, below)
+    ref.close(dx, want, err, "dx")
+    a, v = dy.double(), x.double()
+    err = (a.abs().t() @ v.abs()) * rows * ref.F32
+    ref.close(dw, a.t() @ v, err, "dw", ref.F32)
+    ref.close(db, a.sum(0), a.abs().sum(0) * rows * ref.F32, "db", ref.F32)
+    ref.close(dwb, a.t() @ v + 1, err + ref.F32, "dw added to")
