@@ -73,7 +73,7 @@ Divisor divisor(uint32_t d) {
   return {d, uint32_t((uint64_t(1) << (31 + log)) / d + 1), 31 + log};
 }
 
-struct TcParams {
+struct TcParams {  // but for the tensor maps
   Divisor ftiles;    // feature tiles
   Divisor ctiles, each;  // wgrad: tiles of out features, and all tiles of an expert
   Divisor groups;    // P.groups
@@ -88,9 +88,19 @@ struct TcParams {
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
   uint64_t wait_ns;
   MmParams P;
-  CUtensorMap w[kMaxRanks];                      // forward, dgrad
-  CUtensorMap row[kMaxRanks][4];                 // P.rows in boxes of 8 << i rows
-  CUtensorMap dy[kMaxRanks][4];                  // wgrad
+};
+// RAGGED: ranges of rows of experts, on any ranks; else all rows of one buffer.  That
+// is a kernel of its own because what a cold start costs is code and parameters that
+// come from memory.  Without the look-up of ranges and the 15 other ranks' maps (18 KB)
+// a product of 64 x 64 x 256 takes 10.2 us from a flushed cache instead of 12.3, and 3.9
+// instead of 4.6 among others; 4096 x 2048 x 2048 33 instead of 36.
+template <bool RAGGED>
+struct TcLaunch {
+  static constexpr int kRanks = RAGGED ? kMaxRanks : 1;
+  TcParams T;
+  CUtensorMap w[kRanks];       // forward, dgrad
+  CUtensorMap row[kRanks][4];  // P.rows in boxes of 8 << i rows
+  CUtensorMap dy[kRanks][4];   // wgrad
 };
 
 constexpr int kTcMostStages = 8;
@@ -314,42 +324,54 @@ __device__ __forceinline__ void order_pairs(const TcParams& T, TcShared* S) {
   __syncthreads();
 }
 
+// Tiles of the launch.
+template <int MODE, bool RAGGED>
+__device__ __forceinline__ unsigned tile_count(const TcParams& T, const TcShared* S) {
+  const MmParams& P = T.P;
+  if (MODE == kWgrad) return unsigned(P.parts * P.groups) * T.each.d;
+  if (RAGGED) return S->tile0[P.parts * P.groups] + unsigned(S->lower) * T.ftiles.d;
+  return T.rows.of(unsigned(P.cap[0]) + T.tile_rows - 1) * T.ftiles.d;
+}
 // (Not inlined: every role calls it, once for 32 tiles, and shares its instructions.)
-template <int MODE>
+template <int MODE, bool RAGGED>
 __device__ __noinline__ Tile tile_at(const TcParams& T, const TcShared* S, unsigned t) {
   const MmParams& P = T.P;
   const int n = P.parts * P.groups;
   const int ftile = MODE == kForward && P.act == HOC_ACT_SWIGLU ? kTcFeatures / 2 : kTcFeatures;
-  unsigned i, ct, ft;
+  unsigned i = 0, ct, ft;
   if (MODE == kWgrad) {
-    const unsigned at = T.each.of(t), u = t - at * T.each.d;
-    i = S->order[at];
+    const unsigned at = RAGGED ? T.each.of(t) : 0, u = t - at * T.each.d;
+    if (RAGGED) i = S->order[at];
     ft = T.ctiles.of(u);
     ct = u - ft * T.ctiles.d;
-  } else if (t < S->tile0[n]) {
-    i = mm_find(S->tile0, n, t);
-    // panels of 8 row tiles, so that the tiles in flight share rows and features about evenly
-    const unsigned lt = t - S->tile0[i], whole = T.ftiles.of(S->tile0[i + 1] - S->tile0[i]);
-    const unsigned panel = T.ftiles.of(lt) / kTcPanel, u = lt - panel * kTcPanel * T.ftiles.d;
-    const unsigned high = min(kTcPanel, whole - panel * kTcPanel);
-    ft = high == kTcPanel ? u / kTcPanel : u / high;
-    ct = panel * kTcPanel + u - ft * high;
   } else {
-    const unsigned u = t - S->tile0[n], at = T.ftiles.of(u);
-    i = S->order[at];
-    ct = T.ftiles.of(S->tile0[i + 1] - S->tile0[i]);
-    ft = u - at * T.ftiles.d;
+    const unsigned all = RAGGED ? S->tile0[n] : T.rows.of(unsigned(P.cap[0])) * T.ftiles.d;  // whole tiles
+    if (t < all) {
+      if (RAGGED) i = mm_find(S->tile0, n, t);
+      // panels of 8 row tiles, so that the tiles in flight share rows and features about evenly
+      const unsigned t0 = RAGGED ? S->tile0[i] : 0, lt = t - t0;
+      const unsigned whole = T.ftiles.of((RAGGED ? S->tile0[i + 1] : all) - t0);
+      const unsigned panel = T.ftiles.of(lt) / kTcPanel, u = lt - panel * kTcPanel * T.ftiles.d;
+      const unsigned high = min(kTcPanel, whole - panel * kTcPanel);
+      ft = high == kTcPanel ? u / kTcPanel : u / high;
+      ct = panel * kTcPanel + u - ft * high;
+    } else {
+      const unsigned u = t - all, at = RAGGED ? T.ftiles.of(u) : 0;
+      if (RAGGED) i = S->order[at];
+      ct = T.ftiles.of(RAGGED ? S->tile0[i + 1] - S->tile0[i] : all);
+      ft = u - at * T.ftiles.d;
+    }
   }
-  const unsigned part = T.groups.of(i);
+  const unsigned part = RAGGED ? T.groups.of(i) : 0;
   Tile A;
-  A.p = P.part0 + part;
-  A.g = P.group0 + i - part * T.groups.d;
+  A.p = RAGGED ? P.part0 + part : 0;
+  A.g = RAGGED ? P.group0 + i - part * T.groups.d : 0;
   A.f0 = int(ft) * ftile;
   A.c0 = int(ct) * T.tile_rows;
-  const int rows = S->vrows[i];
+  const int rows = RAGGED ? S->vrows[i] : int(P.cap[0]);
   A.n = (min(T.tile_rows, (MODE == kWgrad ? P.out : rows) - A.c0) + 31) / 32 * 32;
   A.steps = ((MODE == kForward ? P.in : MODE == kDgrad ? P.out : rows) + kTcDepth - 1) / kTcDepth;
-  A.steps = min(A.steps - int(cta_rank() >> 1) * T.per, T.per);
+  if (!RAGGED) A.steps = min(A.steps - int(cta_rank() >> 1) * T.per, T.per);
   return A;
 }
 
@@ -365,26 +387,32 @@ struct Ranges {
 struct Ends {
   int64_t from, to;
 };
+template <bool RAGGED>
 __device__ __forceinline__ Ends load_ends(const MmParams& P, int p, int g, int base) {
   const int s = base + int(threadIdx.x & 31);
-  Ends E{0, P.seg == nullptr && s == 0 ? P.cap[p] : 0};
-  if (P.seg != nullptr && s < P.sources) {
+  Ends E{0, 0};
+  if (RAGGED && s < P.sources) {
     const int64_t* at = P.seg + int64_t(p) * (int64_t(P.sources) * P.experts + 1) + int64_t(s) * P.experts + g;
     E = {at[0], at[1]};
   }
   return E;
 }
-template <int PAD>
+template <int PAD, bool RAGGED>
 __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, Ends E) {
+  Ranges R{};
+  if (!RAGGED) {  // virtual rows are the buffer's rows
+    R.n = int(P.cap[0]);
+    R.wholes = R.n / PAD * PAD;
+    return R;
+  }
   const int lane = threadIdx.x & 31;
   int64_t lo, n;
   mm_cut(P.cap[p], E.from, E.to, lo, n);
-  Ranges R;
   R.lo = int(lo);
   R.n = int(n);
   const int whole = PAD == 8 ? 0 : R.n / PAD * PAD, rest = (R.n - whole + 7) & ~7;
   int a = whole, b = rest;
-  const int ns = P.seg ? P.sources : 1;
+  const int ns = P.sources;
   for (int off = 1; off < 32 && off < ns; off <<= 1) {
     const int x = __shfl_up_sync(0xFFFFFFFFu, a, off), y = __shfl_up_sync(0xFFFFFFFFu, b, off);
     if (lane >= off) {
@@ -404,13 +432,18 @@ __device__ __forceinline__ Ranges load_ranges(const MmParams& P, int p, Ends E) 
 // Each lane's group of 8 virtual rows at `v` (a multiple of 8): its first row in
 // the buffer and how many rows its range has from there on (0: past the end).
 // The whole warp calls it; R holds the first 32 sources' ranges.
-template <int PAD>
+template <int PAD, bool RAGGED>
 __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges R, int v, int& row, int& left) {
-  const int ns = P.seg ? P.sources : 1;
+  if (!RAGGED) {
+    row = min(v, R.n);
+    left = R.n - row;
+    return;
+  }
+  const int ns = P.sources;
   row = int(P.cap[p]);
   left = 0;
   for (int base = 0; base < ns; base += 32) {
-    if (ns > 32) R = load_ranges<PAD>(P, p, load_ends(P, p, g, base));
+    if (ns > 32) R = load_ranges<PAD, true>(P, p, load_ends<true>(P, p, g, base));
     // whole multiples of PAD, or what remains (for PAD 64 all lanes alike: their v share a multiple of 64)
     const bool whole = PAD > 8 && v < R.wholes;
     const int key = whole ? R.start : R.rest;
@@ -433,6 +466,7 @@ __device__ __forceinline__ void group_at(const MmParams& P, int p, int g, Ranges
 // at a time, one each (a tile takes several divisions, which between two tiles
 // would cost as much as a stage's products), and what a warp reads to find a tile's
 // rows is read a tile ahead.
+template <bool RAGGED>
 struct Work {
   const TcParams& T;
   const TcShared* S;
@@ -448,7 +482,7 @@ struct Work {
     if (at == 0) {
       const unsigned t = dealt(i + (threadIdx.x & 31), who, of);
       mine.n = 0;
-      if (t < tiles) mine = tile_at<MODE>(T, S, t);
+      if (t < tiles) mine = tile_at<MODE, RAGGED>(T, S, t);
       __syncwarp();
     }
     ++i;
@@ -459,7 +493,7 @@ struct Work {
     ahead.c0 = __shfl_sync(0xFFFFFFFFu, mine.c0, at);
     ahead.steps = __shfl_sync(0xFFFFFFFFu, mine.steps, at);
     ahead_more = ahead.n > 0;  // only the last round may be short
-    if (ahead_more && rows) ahead_ends = load_ends(T.P, ahead.p, ahead.g, 0);
+    if (ahead_more && rows) ahead_ends = load_ends<RAGGED>(T.P, ahead.p, ahead.g, 0);
   }
   __device__ __forceinline__ void next() {
     more = ahead_more;
@@ -469,19 +503,20 @@ struct Work {
 };
 // Before a warp uses what the cluster's CTAs set up, and reads or writes what the kernel
 // before this one may: each does it once, when it has looked up its first tile.
-__device__ __forceinline__ void begin(const TcParams& T) {
+template <bool RAGGED>
+__device__ __forceinline__ void begin() {
   __syncwarp();
   cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  if (T.P.seg == nullptr) after_previous();  // with ranges, it was needed before they were read
+  if (!RAGGED) after_previous();  // with ranges, it was needed before they were read
 }
 // f() for each tile, W.now being the tile and the next one looked up already; until
 // it returns false.
-template <int MODE, class F>
-__device__ __forceinline__ void each_tile(Work& W, bool rows, F f) {
+template <int MODE, bool RAGGED, class F>
+__device__ __forceinline__ void each_tile(Work<RAGGED>& W, bool rows, F f) {
   for (;;) {  // once without a tile, so that the look-up stands in one place
-    W.look_ahead<MODE>(rows);
-    if (!W.more) begin(W.T);
+    W.template look_ahead<MODE>(rows);
+    if (!W.more) begin<RAGGED>();
     if (W.more && !f()) return;
     if (!W.ahead_more) return;
     W.next();
@@ -508,10 +543,11 @@ __device__ __forceinline__ int box_at(int row, int left) {
 // wgrad: the 64 virtual rows of stage s, a group of 8 per lane modulo 8 (row, and
 // valid rows of the 8).  Returns (to all lanes) how many stages from s on are 64
 // rows each of one range; 0 when stage s is not.
+template <bool RAGGED>
 __device__ __forceinline__ int stage_rows(const MmParams& P, const Tile& A, const Ranges& R, int s, int& row,
                                           int& valid) {
   int left;
-  group_at<kTcDepth>(P, A.p, A.g, R, s * kTcDepth + int(threadIdx.x & 7) * 8, row, left);
+  group_at<kTcDepth, RAGGED>(P, A.p, A.g, R, s * kTcDepth + int(threadIdx.x & 7) * 8, row, left);
   valid = min(left, 8);
   return __shfl_sync(0xFFFFFFFFu, left, 0) / kTcDepth;
 }
@@ -707,7 +743,7 @@ __device__ __forceinline__ void add_sums(const TcParams& T, uint32_t (&v)[kTcCol
 // 2.  in: the group's three input buffers (dgrad: of two planes each); out: its two
 // output planes, which the arrays that are stored take in turn; turn and buffer go on
 // from tile to tile.  False when the accumulator did not come.
-template <int MODE, int ACT>
+template <int MODE, int ACT, bool RAGGED>
 __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, const Tile& A, uint32_t stages, unsigned char* in,
                                              unsigned char* out, uint32_t& turn, uint32_t& buffer, uint32_t acc_at, uint64_t* acc_full,
                                              uint32_t parity, int eg, int q, int rank, int row, int valid, float bias) {
@@ -743,15 +779,15 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  const int mine = int(cta_rank()) >> 1, stride = (2 * kTcColumns) << T.log_shares;
-  const int first = eg * kTcColumns + mine * 2 * kTcColumns;
+  const int share = RAGGED ? 0 : int(cta_rank()) >> 1, stride = RAGGED ? 2 * kTcColumns : (2 * kTcColumns) << T.log_shares;
+  const int first = (eg + 2 * share) * kTcColumns;
   if (reads) {  // the buffer of the last tile's last step may still be read: the two others
     fetch(first, buffer);
     fetch(first + stride, buffer == 2 ? 0 : buffer + 1);
   }
   bool ok = warp_wait(acc_full, parity, T, S);
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  if (ok && T.log_shares) ok = exchange_sums(T, S, A.n, stages, acc_at, eg);
+  if (!RAGGED && ok && T.log_shares) ok = exchange_sums(T, S, A.n, stages, acc_at, eg);
   if (!group_all(eg, ok)) {
     if (reads) asm volatile("cp.async.wait_all;" ::: "memory");
     return false;
@@ -759,7 +795,7 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
   for (int col = first; col < A.n; col += stride) {
     uint32_t v[kTcColumns];
     tmem_load(v, acc_at + uint32_t(col));
-    if (T.log_shares) add_sums(T, v, stages, col);
+    if (!RAGGED && T.log_shares) add_sums(T, v, stages, col);
     auto at = [&](int c) { return row_of(col, c, row, valid); };
     unsigned char* x = in + buffer * kBuffer;
     if (reads) {
@@ -846,6 +882,7 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
 // The same for the weight gradient: columns are out features, rows of the weight;
 // nothing is read but the weights that are added to.
 constexpr int kWgColumns = 16;
+template <bool RAGGED>
 __device__ __forceinline__ bool run_wgrad_epilogue(const TcParams& T, TcShared* S, const Tile& A, uint32_t stages,
                                                    unsigned char* out, uint32_t& turn, uint32_t acc_at, uint64_t* acc_full,
                                                    uint32_t parity, int eg, int q, int rank) {
@@ -856,15 +893,15 @@ __device__ __forceinline__ bool run_wgrad_epilogue(const TcParams& T, TcShared* 
   if (A.steps > 0) {
     ok = warp_wait(acc_full, parity, T, S);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (ok && T.log_shares) ok = exchange_sums(T, S, A.n, stages, acc_at, eg);
+    if (!RAGGED && ok && T.log_shares) ok = exchange_sums(T, S, A.n, stages, acc_at, eg);
   }
   if (!group_all(eg, ok)) return false;
-  const int mine = int(cta_rank()) >> 1;
-  for (int col = (eg + 2 * mine) * kWgColumns; col < A.n; col += (2 * kWgColumns) << T.log_shares) {
+  const int share = RAGGED ? 0 : int(cta_rank()) >> 1, stride = RAGGED ? 2 * kWgColumns : (2 * kWgColumns) << T.log_shares;
+  for (int col = (eg + 2 * share) * kWgColumns; col < A.n; col += stride) {
     uint32_t v[kWgColumns];
     if (A.steps > 0) {
       tmem_load(v, acc_at + uint32_t(col));
-      if (T.log_shares) add_sums(T, v, stages, col);
+      if (!RAGGED && T.log_shares) add_sums(T, v, stages, col);
     } else {
 #pragma unroll
       for (int j = 0; j < kWgColumns; ++j) v[j] = 0;
@@ -925,9 +962,10 @@ constexpr uint32_t stages_in(uint32_t planes, uint32_t stage) {
 static_assert(kWgColumns == kTcColumns, "the planes are of one size");
 static_assert(stages_in(2, kTcStage) == 6 && stages_in(6, kTcStage) == 5, "stages of a tile of 256 rows");
 
-template <int MODE>
+template <int MODE, bool RAGGED>
 __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
-    mm_tc_kernel(const __grid_constant__ TcParams T) {
+    mm_tc_kernel(const __grid_constant__ TcLaunch<RAGGED> L) {
+  const TcParams& T = L.T;
   extern __shared__ unsigned char raw[];
   const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
   unsigned char* stages = raw + (base - ptx::smem_addr(raw));
@@ -936,7 +974,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
   const MmParams& P = T.P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(cta_rank()) & 1;  // in the pair
-  const int from = int(cta_rank() >> 1) * T.per;  // this share's first stage
+  const int from = RAGGED ? 0 : int(cta_rank() >> 1) * T.per;  // this share's first stage
   const bool gated = MODE == kForward && P.act == HOC_ACT_SWIGLU;
 
   if (threadIdx.x == 0) {
@@ -963,35 +1001,23 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
   }
   if (warp == 3 && lane < P.parts) {
     auto prefetch = [](const CUtensorMap* m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); };
-    if (MODE != kWgrad) prefetch(&T.w[P.part0 + lane]);
-    if (P.cap[P.part0 + lane] > 0) prefetch(&T.row[P.part0 + lane][3]);
-    if (MODE == kWgrad && P.cap[P.part0 + lane] > 0) prefetch(&T.dy[P.part0 + lane][3]);
+    if (MODE != kWgrad) prefetch(&L.w[P.part0 + lane]);
+    if (P.cap[P.part0 + lane] > 0) prefetch(&L.row[P.part0 + lane][3]);
+    if (MODE == kWgrad && P.cap[P.part0 + lane] > 0) prefetch(&L.dy[P.part0 + lane][3]);
   }
   // The other CTA's barriers are first used after the wait below.
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();
   cluster_arrive();
-  if (P.seg != nullptr) {
+  if (RAGGED) {
     after_previous();
     mm_count(P, MODE == kWgrad ? kTcDepth : 8, S->vrows, S->tile0,
              [&](int rows) { return MODE == kWgrad ? 0u : T.rows.of(rows) * T.ftiles.d; });
     order_pairs<MODE>(T, S);
-  } else {  // one range: nothing is read before the operands, which each role waits for itself
-    if (threadIdx.x == 0) {
-      const int pad = MODE == kWgrad ? kTcDepth : 8, rows = int((P.cap[0] + pad - 1) / pad * pad);
-      const unsigned whole = T.rows.of(rows);
-      S->vrows[0] = rows;
-      S->tile0[0] = 0;
-      S->tile0[1] = whole * T.ftiles.d;
-      S->order[0] = 0;
-      S->lower = rows > int(whole) * T.tile_rows;
-    }
-    __syncthreads();
   }
-  const uint32_t tmem = S->tmem;
-  const unsigned tiles = MODE == kWgrad ? unsigned(P.parts * P.groups) * T.each.d
-                                        : S->tile0[P.parts * P.groups] + unsigned(S->lower) * T.ftiles.d;
-  const unsigned who = blockIdx.x >> (1 + T.log_shares), of = gridDim.x >> (1 + T.log_shares);
+  const unsigned tiles = tile_count<MODE, RAGGED>(T, S);
+  const int log = RAGGED ? 1 : 1 + T.log_shares;  // of the cluster's CTAs
+  const unsigned who = blockIdx.x >> log, of = gridDim.x >> log;
 
   if (warp == 0 || warp == (MODE == kWgrad ? 12 : 2)) {
     // ---- tensor copies of the rows.  The whole warp walks the stages, so that
@@ -1004,21 +1030,21 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
     bool ok = true;
     // Waits until the MMAs have released the stage's last filling.
     auto free = [&]() { return k.round == 0 || warp_wait(&S->empty[k.st], (k.round - 1) & 1, T, S); };
-    Work W(T, S, who, of, tiles);
-    each_tile<MODE>(W, true, [&]() {
+    Work<RAGGED> W(T, S, who, of, tiles);
+    each_tile<MODE, RAGGED>(W, true, [&]() {
       const Tile& A = W.now;
-      const Ranges R = load_ranges<MODE == kWgrad ? kTcDepth : 8>(P, A.p, W.ends);
+      const Ranges R = load_ranges<MODE == kWgrad ? kTcDepth : 8, RAGGED>(P, A.p, W.ends);
       const int half = A.n / 2;  // rows of B in this CTA (wgrad: features)
       if (MODE != kWgrad) {
         // This warp's 64 rows of B, a group of 8 per lane modulo 8
         const int mine = min(half - block * 64, 64);
         int row, left;
-        group_at<8>(P, A.p, A.g, R, A.c0 + rank * half + block * 64 + (lane & 7) * 8, row, left);
+        group_at<8, RAGGED>(P, A.p, A.g, R, A.c0 + rank * half + block * 64 + (lane & 7) * 8, row, left);
         if ((lane & 7) * 8 >= mine) left = 0;
         // Columns of groups without rows are not stored: they are not fetched.
         const int any = box_at(row, left), box = left > 0 ? any : -1;
         const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xFFFFFFFFu, left > 0) & 0xFFu)) * 1024u + T.tx_pad;
-        const CUtensorMap* map = &T.row[A.p][box < 0 ? 0 : box];
+        const CUtensorMap* map = &L.row[A.p][box < 0 ? 0 : box];
         for (int s = 0; s < A.steps; ++s, k.next()) {
           if (!free()) {
             ok = false;
@@ -1041,7 +1067,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
             continue;
           }
           int row, valid;
-          const int run = min(stage_rows(P, A, R, from + s, row, valid), A.steps - s);
+          const int run = min(stage_rows<RAGGED>(P, A, R, from + s, row, valid), A.steps - s);
           int r = __shfl_sync(0xFFFFFFFFu, row, 0);
           for (int i = 0; i < run; ++i, r += kTcDepth, k.next()) {
             if (!own(k.st)) continue;
@@ -1052,10 +1078,10 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
             const uint32_t a = base + k.st * T.stage, bar = full0 + k.st * 8u;
             if (one) {
               arrive_expect_cluster(bar, bytes);
-              copy2(a, &T.row[A.p][3], fx, r, bar);
-              copy2(a + 8192u, &T.row[A.p][3], fx + 64, r, bar);
-              copy2(a + kTcOperand, &T.dy[A.p][3], fd, r, bar);
-              if (blocks > 1) copy2(a + kTcOperand + 8192u, &T.dy[A.p][3], fd + 64, r, bar);
+              copy2(a, &L.row[A.p][3], fx, r, bar);
+              copy2(a + 8192u, &L.row[A.p][3], fx + 64, r, bar);
+              copy2(a + kTcOperand, &L.dy[A.p][3], fd, r, bar);
+              if (blocks > 1) copy2(a + kTcOperand + 8192u, &L.dy[A.p][3], fd + 64, r, bar);
             }
             __syncwarp();
           }
@@ -1077,7 +1103,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
           __syncwarp();
           if (which < 2 + blocks && box >= 0)
             copy2(a + uint32_t(which) * 8192u + uint32_t(lane & 7) * 1024u,
-                  which < 2 ? &T.row[A.p][box] : &T.dy[A.p][box],
+                  which < 2 ? &L.row[A.p][box] : &L.dy[A.p][box],
                   which < 2 ? fx + which * 64 : fd + (which - 2) * 64, row, bar);
           __syncwarp();
           ++s;
@@ -1094,8 +1120,8 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
     const uint32_t full0 = on_first(&S->full[0]);
     Turn k(T.stages);
     bool ok = true;
-    Work W(T, S, who, of, tiles);
-    each_tile<MODE>(W, false, [&]() {
+    Work<RAGGED> W(T, S, who, of, tiles);
+    each_tile<MODE, RAGGED>(W, false, [&]() {
       const Tile& A = W.now;
       const int fa = A.f0 + rank * (gated ? 64 : 128);
       for (int s = 0; s < A.steps; ++s, k.next()) {
@@ -1108,12 +1134,12 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
         if (one) {
           arrive_expect_cluster(bar, kTcOperand);
           if (MODE == kDgrad) {
-            copy3(a, &T.w[A.p], fa, x, A.g, bar);
-            copy3(a + 8192u, &T.w[A.p], fa + 64, x, A.g, bar);
+            copy3(a, &L.w[A.p], fa, x, A.g, bar);
+            copy3(a + 8192u, &L.w[A.p], fa + 64, x, A.g, bar);
           } else if (gated) {
-            copy5(a, &T.w[A.p], x, 0, 0, fa / 16, A.g, bar);
+            copy5(a, &L.w[A.p], x, 0, 0, fa / 16, A.g, bar);
           } else {
-            copy3(a, &T.w[A.p], x, fa, A.g, bar);
+            copy3(a, &L.w[A.p], x, fa, A.g, bar);
           }
         }
         __syncwarp();
@@ -1130,12 +1156,12 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
                           (MODE == kWgrad ? 1u << 16 : 0u) | (uint32_t(kTcFeatures / 16) << 24);
     const uint64_t a0 = MODE == kForward ? smem_desc(base, 16, 1024) : smem_desc(base, 8192, 1024);
     const uint64_t b0 = MODE == kWgrad ? smem_desc(base + kTcOperand, 8192, 1024) : smem_desc(base + kTcOperand, 16, 1024);
-    Work W(T, S, who, of, tiles);
+    Work<RAGGED> W(T, S, who, of, tiles);
     for (;;) {  // once without a tile: the next one is looked up under a tile's first products
       const Tile& A = W.now;
       const bool run = W.more && A.steps > 0;  // an expert without rows: the epilogue writes zeros
       const uint32_t idesc = kind | (uint32_t(A.n / 8) << 17);
-      const uint32_t acc = it & 1, d = tmem + acc * 256u;
+      const uint32_t acc = it & 1, d = S->tmem + acc * 256u;
       if (run && it >= 2 && !warp_wait(&S->acc_empty[acc], ((it >> 1) - 1) & 1, T, S)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int steps = run ? A.steps : 1;
@@ -1156,9 +1182,9 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
           __syncwarp();
           k.next();
         }
-        if (s == 0) W.look_ahead<MODE>(false);
+        if (s == 0) W.template look_ahead<MODE>(false);
       }
-      if (!W.more) begin(T);
+      if (!W.more) begin<RAGGED>();
       if (!ok) break;
       if (run) {
         if (one) commit_pair(&S->acc_full[acc]);
@@ -1178,13 +1204,13 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
     Turn k(T.stages);
     uint32_t phases = 0;  // bit st: parity of part[st]
     bool ok = true;
-    Work W(T, S, who, of, tiles);
-    each_tile<MODE>(W, true, [&]() {
+    Work<RAGGED> W(T, S, who, of, tiles);
+    each_tile<MODE, RAGGED>(W, true, [&]() {
       const Tile& A = W.now;
-      const Ranges R = load_ranges<kTcDepth>(P, A.p, W.ends);
+      const Ranges R = load_ranges<kTcDepth, RAGGED>(P, A.p, W.ends);
       for (int s = 0; s < A.steps;) {
         int row, valid;
-        const int run = min(stage_rows(P, A, R, from + s, row, valid), A.steps - s);
+        const int run = min(stage_rows<RAGGED>(P, A, R, from + s, row, valid), A.steps - s);
         for (int i = 0; i < run; ++i) k.next();
         s += run;
         if (run > 0) continue;
@@ -1221,13 +1247,13 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
     unsigned char* in = planes + eg * T.planes * kTcPlane;
     unsigned char* out = MODE == kForward && T.planes > 2 ? in + 3 * kTcPlane : in;
     uint32_t it = 0, turn = 0, buffer = 0;
-    Work W(T, S, who, of, tiles);
-    each_tile<MODE>(W, MODE != kWgrad, [&]() {
+    Work<RAGGED> W(T, S, who, of, tiles);
+    each_tile<MODE, RAGGED>(W, MODE != kWgrad, [&]() {
       const Tile& A = W.now;
       int row = 0, valid = 0;
       float bias = 0.f;
       if (MODE != kWgrad) {
-        group_at<8>(P, A.p, A.g, load_ranges<8>(P, A.p, W.ends), A.c0 + lane * 8, row, valid);
+        group_at<8, RAGGED>(P, A.p, A.g, load_ranges<8, RAGGED>(P, A.p, W.ends), A.c0 + lane * 8, row, valid);
         valid = lane * 8 < T.tile_rows ? min(valid, 8) : 0;  // past them: the next tile's rows
         const int f = gated ? A.f0 + rank * 64 + q * 16 + (lane & 15) : A.f0 + rank * 128 + q * 32 + lane;
         if (MODE == kForward && P.bias[A.p] && f < P.out)
@@ -1235,13 +1261,13 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
       }
       if (MODE == kWgrad && A.steps == 0 && P.accumulate) return true;  // an expert without rows adds nothing
       const uint32_t acc = it & 1;
-      const uint32_t at = tmem + acc * 256u + (uint32_t(q * 32) << 16);
+      const uint32_t at = S->tmem + acc * 256u + (uint32_t(q * 32) << 16);
       bool ok = true;
       if constexpr (MODE == kWgrad) {
-        ok = run_wgrad_epilogue(T, S, A, base, out, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q, rank);
+        ok = run_wgrad_epilogue<RAGGED>(T, S, A, base, out, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q, rank);
       } else {
         with_act(P.act, [&](auto tag) {
-          ok = run_epilogue<MODE, decltype(tag)::act>(T, S, A, base, in, out, turn, buffer, at, &S->acc_full[acc],
+          ok = run_epilogue<MODE, decltype(tag)::act, RAGGED>(T, S, A, base, in, out, turn, buffer, at, &S->acc_full[acc],
                                                       (it >> 1) & 1, eg, q, rank, row, valid, bias);
         });
       }
@@ -1254,7 +1280,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
       return true;
     });
   } else {
-    begin(T);
+    begin<RAGGED>();
   }
   __syncwarp();
   if (S->dead) {
@@ -1268,11 +1294,13 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
   cluster_wait();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == 2)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcTmemColumns));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(S->tmem), "r"(kTcTmemColumns));
 }
 
-using TcFn = void (*)(TcParams);
-const TcFn kTc[3] = {mm_tc_kernel<kForward>, mm_tc_kernel<kDgrad>, mm_tc_kernel<kWgrad>};
+template <bool RAGGED>
+using TcFn = void (*)(TcLaunch<RAGGED>);
+template <bool RAGGED>
+constexpr TcFn<RAGGED> kTc[3] = {mm_tc_kernel<kForward, RAGGED>, mm_tc_kernel<kDgrad, RAGGED>, mm_tc_kernel<kWgrad, RAGGED>};
 
 // ------------------------------------------------------------------ host
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1335,9 +1363,10 @@ int choose_rows_ragged(const MmParams& P) {
 
 // The launch but for its grid and stream, and the clusters that fit the device at
 // once (asked once for each kernel, cluster size and device).
-cudaError_t configure(const void* fn, int mode, int log_shares, cudaLaunchAttribute (&attr)[2], cudaLaunchConfig_t& cfg,
+cudaError_t configure(const void* fn, int mode, bool ragged, int log_shares, cudaLaunchAttribute (&attr)[2], cudaLaunchConfig_t& cfg,
                       int& clusters) {
-  static std::atomic<int> known[3][kTcMostShares + 1][64];
+  static std::atomic<int> known[3][kTcMostShares + 2][64];  // ragged ones last
+  const int kind = ragged ? kTcMostShares + 1 : log_shares;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2u << log_shares;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -1352,14 +1381,14 @@ cudaError_t configure(const void* fn, int mode, int log_shares, cudaLaunchAttrib
   int dev = 0;
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  clusters = dev < 64 ? known[mode][log_shares][dev].load() : 0;
+  clusters = dev < 64 ? known[mode][kind][dev].load() : 0;
   if (clusters > 0) return cudaSuccess;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2u << log_shares);
   e = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg);
   cfg.numAttrs = 2;
   if (e == cudaSuccess && clusters < 1) e = cudaErrorInvalidConfiguration;
-  if (e == cudaSuccess && dev < 64) known[mode][log_shares][dev].store(clusters);
+  if (e == cudaSuccess && dev < 64) known[mode][kind][dev].store(clusters);
   return e;
 }
 
@@ -1415,15 +1444,17 @@ static bool is_loose(const MmParams& P, int mode) {
   return (at & 15u) != 0;
 }
 
-cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
-  TcParams T;
+template <bool RAGGED>
+static cudaError_t launch(const MmParams& P, int mode, cudaStream_t s) {
+  TcLaunch<RAGGED> L;
+  TcParams& T = L.T;
   T.P = P;
   T.loose = is_loose(P, mode);
   const char* fault = getenv("HOC_FAULT");
   const bool stall = fault && !strcmp(fault, "mm_stall");
   T.tx_pad = stall ? 16u : 0u;
   T.wait_ns = stall ? 100000000ull : kTcWaitNs;
-  const void* fn = reinterpret_cast<const void*>(kTc[mode]);
+  const void* fn = reinterpret_cast<const void*>(kTc<RAGGED>[mode]);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   cudaError_t e = cudaSuccess;
@@ -1434,16 +1465,16 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   const int64_t steps = (depth + kTcDepth - 1) / kTcDepth;
   Cut cut{0, 0};
   int clusters[kTcMostShares + 1] = {};
-  const int most = P.seg == nullptr ? kTcMostShares : 0;
-  for (int log = most; log >= 0 && e == cudaSuccess; --log) e = configure(fn, mode, log, attr, cfg, clusters[log]);
+  const int most = RAGGED ? 0 : kTcMostShares;
+  for (int log = most; log >= 0 && e == cudaSuccess; --log) e = configure(fn, mode, RAGGED, log, attr, cfg, clusters[log]);
   if (e != cudaSuccess) return e;
   if (mode == kWgrad) cut = choose_cut(P.out, ftiles * P.groups * P.parts, steps, clusters, most);
-  else if (P.seg == nullptr) cut = choose_cut(P.cap[0], ftiles, steps, clusters, most);
+  else if (!RAGGED) cut = choose_cut(P.cap[0], ftiles, steps, clusters, most);
   else cut.rows = choose_rows_ragged(P);
   T.tile_rows = cut.rows;
   T.log_shares = cut.log_shares;
   T.per = T.log_shares ? int((steps + (1 << T.log_shares) - 1) >> T.log_shares) : INT_MAX;
-  if (T.log_shares) e = configure(fn, mode, T.log_shares, attr, cfg, clusters[T.log_shares]);
+  if (T.log_shares) e = configure(fn, mode, RAGGED, T.log_shares, attr, cfg, clusters[T.log_shares]);
   if (e != cudaSuccess) return e;
   cfg.stream = s;
   T.stage = mode == kWgrad ? kTcStage : kTcOperand + uint32_t(T.tile_rows) * (kTcDepth * 2 / 2);
@@ -1459,28 +1490,34 @@ cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
   for (int p = P.part0; p < P.part0 + P.parts; ++p) {
     tiles += ftiles * (mode == kWgrad ? int64_t(P.groups) * ((P.out + T.tile_rows - 1) / T.tile_rows)
                                       : P.cap[p] / T.tile_rows + int64_t(P.groups) * (1 + P.sources * 8 / T.tile_rows));
-    bool ok = mode == kWgrad || encode_weight(&T.w[p], P, mode, P.w[p]);
+    bool ok = mode == kWgrad || encode_weight(&L.w[p], P, mode, P.w[p]);
     if (P.cap[p] > 0) {  // a buffer without rows has no tile that reads it
       const int64_t width = mode == kDgrad ? P.out : P.in;
       for (int i = 0; i < 4; ++i) {
-        ok = ok && encode_rows(&T.row[p][i], P.rows[p], width, P.cap[p], P.ld_rows, 8 << i);
-        if (mode == kWgrad) ok = ok && encode_rows(&T.dy[p][i], P.dy[p], P.out, P.cap[p], P.ld_dy, 8 << i);
+        ok = ok && encode_rows(&L.row[p][i], P.rows[p], width, P.cap[p], P.ld_rows, 8 << i);
+        if (mode == kWgrad) ok = ok && encode_rows(&L.dy[p][i], P.dy[p], P.out, P.cap[p], P.ld_dy, 8 << i);
       }
     }
     if (!ok) return cudaErrorInvalidValue;
   }
   const int at_once = clusters[T.log_shares];
   cfg.gridDim = dim3(unsigned(tiles < 1 ? 1 : tiles < at_once ? tiles : at_once) << (1 + T.log_shares));
-  return cudaLaunchKernelEx(&cfg, kTc[mode], T);
+  return cudaLaunchKernelEx(&cfg, kTc<RAGGED>[mode], L);
+}
+
+cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s) {
+  return P.seg == nullptr ? launch<false>(P, mode, s) : launch<true>(P, mode, s);
 }
 
 cudaError_t mm_tc_preload() {
-  for (TcFn f : kTc) {
+  cudaError_t e = cudaSuccess;
+  auto load = [&](auto fn) {
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(f));
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(fn));
+  };
+  for (auto fn : kTc<false>) load(fn);
+  for (auto fn : kTc<true>) load(fn);
+  return e;
 }
 
 }  // namespace hoc
