@@ -9,6 +9,10 @@
 // the contraction's elements within a fragment is free as long as both operands
 // share it, so lane t of a row takes 8 consecutive elements.  The warps' binary32
 // sums are added in warp order in shared memory.
+//
+// 4096 x 4096 weights from a flushed cache take 12.3 us at 1 row (2.7 TB/s; 8.8 us in a
+// graph of calls, 3.8 TB/s), 14.3 at 16, 16.4 at 32; 2048 x 1408 at 1 row 8.2 us.  What
+// bounds it at such sizes is latency: a warp makes four rounds of loads.
 #include "mm.h"
 
 namespace hoc {
@@ -136,10 +140,16 @@ const FewFn kFew[3][2] = {{mm_few_kernel<1, 1>, mm_few_kernel<1, 2>},
 
 }  // namespace
 
+// Up to 32 rows.  Above 16 every load of weights meets four blocks of rows, and for
+// large weights the tcgen05 kernel is faster (24 rows, us here and there): 4096 x 4096
+// 16.4 and 18.5, with gates 30.7 and 24.6; 7168 x 7168 36.9 and 32.8, with gates 67.6
+// and 53.2; 7168 x 512 with gates 24.6 and 18.4; 2048 x 1408 with gates 12.3 and 14.3.
 bool mm_few_takes(const MmParams& P, int mode) {
+  const bool large = P.cap[0] > 16 && int64_t(P.in) * P.out * (P.act == HOC_ACT_SWIGLU ? 5 : 1) > 1 << 24;
   return mode == kForward && P.seg == nullptr && P.cap[0] <= 32 && P.ld_rows % 8 == 0 && P.ld_w % 8 == 0 &&
          (P.in % 8 == 0 || P.ld_w != P.in) &&
-         ((reinterpret_cast<uintptr_t>(P.rows[0]) | reinterpret_cast<uintptr_t>(P.w[0])) & 15u) == 0;
+         ((reinterpret_cast<uintptr_t>(P.rows[0]) | reinterpret_cast<uintptr_t>(P.w[0])) & 15u) == 0 &&
+         !(large && mm_tc_takes(P, mode));
 }
 
 cudaError_t launch_mm_few(const MmParams& P, cudaStream_t s) {

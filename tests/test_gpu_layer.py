@@ -605,3 +605,15 @@ def test_a_contraction_shared_by_several_ctas(rows, inp, out, act):
     ref.close(dw, a.t() @ v, err, "dw", ref.F32)
     ref.close(db, a.sum(0), a.abs().sum(0) * rows * ref.F32, "db", ref.F32)
     ref.close(dwb, a.t() @ v + 1, err + ref.F32, "dw added to")
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("rows", [16, 17, 32])
+def test_few_rows_of_large_weights(rows, act):
+    inp, out = 4160, 4104
+    x, w = normal(rows, inp, seed=1), normal((2 if act == "swiglu" else 1) * out, inp, seed=2, sigma=inp ** -0.5)
+    y, st = torch.empty(rows, out, dtype=BF, device=DEV), status()
+    hoc.linear(x, w, y, status=st, act=act)
+    assert st.item() == 0
+    _, _, want, err = ref.forward(x, w, None, act)
+    ref.close(y, want, err, "y")
