@@ -42,6 +42,8 @@ __global__ void seg_count_kernel(const __grid_constant__ SegIds P, int n, int ex
 }
 
 // Counts to offsets: an inclusive scan of seg[d][1 ..] in place, one CTA per rank.
+// Both and the zeroing before them are bound by their launches: 15 us for 8 x 4096
+// tokens, top-6 of 64 experts.
 __global__ void seg_scan_kernel(int m, int64_t* seg) {
   int64_t* v = seg + size_t(blockIdx.x) * (size_t(m) + 1) + 1;
   __shared__ int64_t part[kSegThreads / 32];
@@ -68,41 +70,65 @@ __global__ void seg_scan_kernel(int m, int64_t* seg) {
 }
 
 // ------------------------------------------------------------ activation gradient
-// dz = dy * act'(pre), 8 values of a row per thread where rows are whole
-// 16-byte vectors, else one.  Bound by its bytes: dy and pre read, dz written.
-template <int V>
-__global__ void act_grad_kernel(const __nv_bfloat16* dy, const __nv_bfloat16* pre, __nv_bfloat16* dz, int64_t rows,
-                                int width, int act) {
+// dz = dy * act'(pre), in vectors of 8 values where rows are whole 16-byte vectors,
+// else of one.  Bound by its bytes: dy and pre read, dz written.  A thread loads
+// all its vectors before its arithmetic.  65,536 rows of 1280: GELU 93 us with two
+// vectors (5.4 TB/s; 98 with one, 104 with four), the gated form, which loads three
+// rows, 142 us with one (5.9 TB/s; 152 with two, 187 with four).
+constexpr int kActThreads = 256;
+constexpr int kGatedVecs = 1, kPlainVecs = 2;
+template <int V, int ACT>
+__global__ void __launch_bounds__(kActThreads)
+    act_grad_kernel(const __nv_bfloat16* dy, const __nv_bfloat16* pre, __nv_bfloat16* dz, int64_t rows, int width) {
   struct alignas(2 * V) Vec {
     __nv_bfloat16 v[V];
   };
-  const int per = width / V;
+  const unsigned per = unsigned(width / V);
   const int64_t n = rows * per;
-  const bool gated = act == HOC_ACT_SWIGLU;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t row = i / per;
-    const int64_t f = (i - row * per) * V;
-    const int64_t at = gated ? row * 2 * width + f : row * width + f;
-    const Vec d = *reinterpret_cast<const Vec*>(dy + row * width + f);
-    const Vec z = *reinterpret_cast<const Vec*>(pre + at);
-    Vec o, o2;
-    if (gated) {
-      const Vec u = *reinterpret_cast<const Vec*>(pre + at + width);
+  constexpr bool gated = ACT == HOC_ACT_SWIGLU;
+  constexpr int kVecs = gated ? kGatedVecs : kPlainVecs;
+  for (int64_t base = int64_t(blockIdx.x) * kActThreads * kVecs; base < n; base += int64_t(gridDim.x) * kActThreads * kVecs) {
+    Vec d[kVecs], z[kVecs], u[kVecs];
+    int64_t at[kVecs];  // of pre and dz; -1 past the end
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int64_t i = base + j * kActThreads + int(threadIdx.x);
+      at[j] = -1;
+      if (i >= n) continue;
+      // a gated row is twice as wide
+      const int64_t row = !gated ? 0 : i < (int64_t(1) << 32) ? int64_t(unsigned(i) / per) : i / per;
+      at[j] = i * V + row * width;
+      d[j] = *reinterpret_cast<const Vec*>(dy + i * V);
+      z[j] = *reinterpret_cast<const Vec*>(pre + at[j]);
+      if (gated) u[j] = *reinterpret_cast<const Vec*>(pre + at[j] + width);
+    }
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      if (at[j] < 0) continue;
+      Vec o, o2;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float g = __bfloat162float(z.v[e]), dd = __bfloat162float(d.v[e]);
-        o.v[e] = __float2bfloat16_rn(dd * __bfloat162float(u.v[e]) * mm_act_slope(HOC_ACT_SILU, g));
-        o2.v[e] = __float2bfloat16_rn(dd * mm_act(HOC_ACT_SILU, g));
+        const float g = __bfloat162float(z[j].v[e]), dd = __bfloat162float(d[j].v[e]);
+        if (gated) {
+          o.v[e] = __float2bfloat16_rn(dd * __bfloat162float(u[j].v[e]) * mm_act_slope(HOC_ACT_SILU, g));
+          o2.v[e] = __float2bfloat16_rn(dd * mm_act(HOC_ACT_SILU, g));
+        } else {
+          o.v[e] = __float2bfloat16_rn(dd * mm_act_slope(ACT, g));
+        }
       }
-      *reinterpret_cast<Vec*>(dz + at + width) = o2;
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        o.v[e] = __float2bfloat16_rn(__bfloat162float(d.v[e]) * mm_act_slope(act, __bfloat162float(z.v[e])));
+      *reinterpret_cast<Vec*>(dz + at[j]) = o;
+      if (gated) *reinterpret_cast<Vec*>(dz + at[j] + width) = o2;
     }
-    *reinterpret_cast<Vec*>(dz + at) = o;
   }
 }
+
+using ActFn = void (*)(const __nv_bfloat16*, const __nv_bfloat16*, __nv_bfloat16*, int64_t, int);
+// By whether rows are whole 16-byte vectors, and the activation.
+const ActFn kActGrad[2][4] = {{act_grad_kernel<1, HOC_ACT_RELU>, act_grad_kernel<1, HOC_ACT_GELU>,
+                               act_grad_kernel<1, HOC_ACT_SILU>, act_grad_kernel<1, HOC_ACT_SWIGLU>},
+                              {act_grad_kernel<8, HOC_ACT_RELU>, act_grad_kernel<8, HOC_ACT_GELU>,
+                               act_grad_kernel<8, HOC_ACT_SILU>, act_grad_kernel<8, HOC_ACT_SWIGLU>}};
+static_assert(HOC_ACT_RELU == 1 && HOC_ACT_GELU == 2 && HOC_ACT_SILU == 3 && HOC_ACT_SWIGLU == 4, "the order above");
 
 // ------------------------------------------------------------ bias gradient
 // db[e][n] (+)= sum over the expert's rows of dy[r][n]: bound by reading dy once
@@ -110,7 +136,8 @@ __global__ void act_grad_kernel(const __nv_bfloat16* dy, const __nv_bfloat16* pr
 // of 8 CTAs sums 64 columns of one expert, each warp taking 4 rows at a time of 8
 // lanes x 8 columns (or, where rows are not whole 16-byte vectors, one row of 32
 // lanes x 2 columns).  Binary32 sums; lanes, warps and CTAs are added in a fixed
-// order.  With one CTA for the 64 columns the 4096 x 4096 gradient took 31 us.
+// order.  With one CTA for the 64 columns the 4096 x 4096 gradient took 31 us; with
+// eight, beside the product, it adds 8 us to the 78 us of 4096 rows of 4096 x 4096.
 // Launched right behind the product (programmatic dependent launch), it runs beside
 // it: it needs nothing of it, and what both need was complete when the product's
 // CTAs, which let it start, had passed their own wait.  Every kernel that is
@@ -196,7 +223,7 @@ __global__ void __cluster_dims__(1, 1, kBiasCtas) __launch_bounds__(32 * kBiasWa
 // Rows of `width` values from anywhere to rows of `to_ld` values on 16-byte
 // boundaries, the rest of each row zero: a thread makes one 16-byte vector, from
 // aligned words (and, where the source starts between two words, its first and last
-// value).  Bound by its bytes.
+// value).  Bound by its bytes; the widths where it pays are at kRealignLeast.
 struct Realign {
   const uint16_t* from[kMaxRanks];
   uint4* to[kMaxRanks];
@@ -540,7 +567,6 @@ hocResult_t dense(const char* who, int rows, int in, int out, int32_t* status, M
 
 cudaError_t mm_preload() {
   const void* fns[] = {reinterpret_cast<const void*>(&seg_count_kernel), reinterpret_cast<const void*>(&seg_scan_kernel),
-                       reinterpret_cast<const void*>(&act_grad_kernel<8>), reinterpret_cast<const void*>(&act_grad_kernel<1>),
                        reinterpret_cast<const void*>(&realign_kernel),
                        reinterpret_cast<const void*>(&bias_grad_kernel<true>),
                        reinterpret_cast<const void*>(&bias_grad_kernel<false>)};
@@ -549,6 +575,12 @@ cudaError_t mm_preload() {
     const cudaError_t e = cudaFuncGetAttributes(&a, f);
     if (e != cudaSuccess) return e;
   }
+  for (const auto& row : kActGrad)
+    for (ActFn f : row) {
+      cudaFuncAttributes a;
+      const cudaError_t e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(f));
+      if (e != cudaSuccess) return e;
+    }
   cudaError_t e = mm_any_preload();
   if (e == cudaSuccess) e = mm_few_preload();
   return e == cudaSuccess ? mm_tc_preload() : e;
@@ -733,11 +765,10 @@ extern "C" hocResult_t hoc_act_grad(int rows, int width, int act, const void* dy
   const bool vec = width % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(pre) |
                                        reinterpret_cast<uintptr_t>(dz)) & 15u) == 0;
   const int64_t n = int64_t(rows) * (vec ? width / 8 : width);
-  const int64_t want = (n + 255) / 256, cap = int64_t(sm_count()) * 8;
-  const int grid = int(want < cap ? want : cap);
+  const int64_t each = kActThreads * (act == HOC_ACT_SWIGLU ? kGatedVecs : kPlainVecs), want = (n + each - 1) / each;
+  const int grid = int(want < 1 << 20 ? want : 1 << 20);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (vec) act_grad_kernel<8><<<grid, 256, 0, s>>>(d[0], z[0], o[0], rows, width, act);
-  else act_grad_kernel<1><<<grid, 256, 0, s>>>(d[0], z[0], o[0], rows, width, act);
+  kActGrad[vec][act - HOC_ACT_RELU]<<<grid, kActThreads, 0, s>>>(d[0], z[0], o[0], rows, width);
   if (cudaGetLastError() == cudaSuccess) return HOC_SUCCESS;
   set_error_detail("hoc_act_grad: launch failed");
   return HOC_ERR_CUDA;
