@@ -137,9 +137,10 @@ static_assert(HOC_ACT_RELU == 1 && HOC_ACT_GELU == 2 && HOC_ACT_SILU == 3 && HOC
 // lanes x 8 columns (or, where rows are not whole 16-byte vectors, one row of 32
 // lanes x 2 columns).  Binary32 sums; lanes, warps and CTAs are added in a fixed
 // order.  With one CTA for the 64 columns the 4096 x 4096 gradient took 31 us; with
-// eight, beside the product, it adds 8 us to the 78 us of 4096 rows of 4096 x 4096.
+// eight it adds 8 us to the 78 us of 4096 rows of 4096 x 4096.
+// For one range of rows the product's spare warps mostly do the same (mm_tc.cu).
 // Launched right behind the product (programmatic dependent launch), it runs beside
-// it: it needs nothing of it, and what both need was complete when the product's
+// it where SMs have room: it needs nothing of it, and what both need was complete when the product's
 // CTAs, which let it start, had passed their own wait.  Every kernel that is
 // launched before it therefore waits before it lets dependents start.
 constexpr int kBiasWarps = 8;
@@ -447,7 +448,7 @@ void realign(MmParams& P, int mode, cudaStream_t s, void** used) {
 }
 
 // Launches one product, in as many launches as kMmMaxGroups asks for.
-hocResult_t launch_product(const char* who, MmParams P, int mode, cudaStream_t s) {
+hocResult_t launch_product(const char* who, MmParams P, int mode, cudaStream_t s, bool* summed) {
   const int sms = sm_count();
   const int nranks = P.parts, experts = P.groups;
   const bool few = mm_few_takes(P, mode), tc = !few && mm_tc_takes(P, mode);
@@ -463,7 +464,7 @@ hocResult_t launch_product(const char* who, MmParams P, int mode, cudaStream_t s
       for (int q = p; q < p + P.parts; ++q) rows += P.cap[q];
       if (rows == 0 && mode != kWgrad) continue;
       const cudaError_t e = few  ? launch_mm_few(P, s)
-                            : tc ? launch_mm_tc(P, mode, s)
+                            : tc ? launch_mm_tc(P, mode, s, summed)
                                  : launch_mm_any(P, mode, sms, s);
       if (e != cudaSuccess) {
         char msg[160];
@@ -475,13 +476,13 @@ hocResult_t launch_product(const char* who, MmParams P, int mode, cudaStream_t s
   return HOC_SUCCESS;
 }
 
-hocResult_t run_product(const char* who, const MmParams& given, int mode, cudaStream_t s) {
+hocResult_t run_product(const char* who, const MmParams& given, int mode, cudaStream_t s, bool* summed = nullptr) {
   MmParams P = given;
   P.ld_w = P.in;
   P.out_w = P.out;
   void* held = nullptr;
   if (!mm_few_takes(P, mode) && !mm_tc_takes(P, mode)) realign(P, mode, s, &held);
-  const hocResult_t r = launch_product(who, P, mode, s);
+  const hocResult_t r = launch_product(who, P, mode, s, summed);
   if (held && cudaFreeAsync(held, s) != cudaSuccess && r == HOC_SUCCESS) {
     set_error_detail("freeing scratch failed");
     return HOC_ERR_CUDA;
@@ -500,9 +501,10 @@ bool tiles_ok(const MmParams& P, int mode, int width) {
 
 hocResult_t run_wgrad(const char* who, MmParams& P, void* const* db, cudaStream_t s) {
   if (!tiles_ok(P, kWgrad, P.in)) return refuse(who, "more than 2^31 tiles");
-  hocResult_t r = run_product(who, P, kWgrad, s);
-  if (r != HOC_SUCCESS || !db) return r;
-  for (int p = 0; p < P.parts; ++p) P.pre_out[p] = db[p];
+  for (int p = 0; p < P.parts; ++p) P.pre_out[p] = db ? db[p] : nullptr;
+  bool summed = false;
+  hocResult_t r = run_product(who, P, kWgrad, s, &summed);
+  if (r != HOC_SUCCESS || !db || summed) return r;
   const int pairs = P.parts * P.groups;
   bool vec = P.out % 8 == 0 && P.ld_dy % 8 == 0;
   for (int p = 0; p < P.parts; ++p) vec = vec && (reinterpret_cast<uintptr_t>(P.dy[p]) & 15u) == 0;

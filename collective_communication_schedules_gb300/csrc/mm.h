@@ -178,7 +178,8 @@ cudaError_t mm_any_preload();
 // Whether the tensor-core kernel takes these operands (alignment and widths of
 // what tensor copies fetch; the epilogue's rows may lie anywhere).
 bool mm_tc_takes(const MmParams& P, int mode);
-cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s);
+// summed (weight gradient): whether the launch sums the columns of dy too, to P.pre_out[0].
+cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s, bool* summed);
 cudaError_t mm_tc_preload();
 // Whether the kernel for a few rows takes this product (one range, at most 32 rows).
 bool mm_few_takes(const MmParams& P, int mode);

@@ -617,3 +617,21 @@ def test_few_rows_of_large_weights(rows, act):
     assert st.item() == 0
     _, _, want, err = ref.forward(x, w, None, act)
     ref.close(y, want, err, "y")
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("rows,inp,out", [(1, 512, 512), (70, 1024, 1048), (515, 2048, 1400), (2047, 512, 520)])
+def test_bias_gradient_beside_the_weight_gradient(rows, inp, out, accumulate):
+    """Column sums by the product's own warps, their order fixed; rows that lie apart."""
+    x, dy = normal(rows, inp, seed=1), normal(rows, out + 8, seed=2)[:, :out]
+    w0, b0, st = normal(out, inp, seed=3), normal(out, seed=4), status()
+    got = []
+    for _ in range(2):
+        dw, db = w0.clone(), b0.clone()
+        hoc.linear_wgrad(dy, x, dw, status=st, db=db, accumulate=accumulate)
+        got.append((dw, db))
+    assert st.item() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    a, v, keep = dy.double(), x.double(), float(accumulate)
+    ref.close(got[0][0], a.t() @ v + keep * w0.double(), (a.abs().t() @ v.abs()) * rows * ref.F32 + w0.double().abs() * ref.F32, "dw")
+    ref.close(got[0][1], a.sum(0) + keep * b0.double(), a.abs().sum(0) * rows * ref.F32 + b0.double().abs() * ref.F32, "db")
