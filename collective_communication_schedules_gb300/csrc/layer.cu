@@ -381,7 +381,7 @@ void realign(MmParams& P, int mode, cudaStream_t s, void** used) {
     Operand& o = op[i];
     const bool weights = i == 1 && mode != kWgrad;
     o.block = weights ? P.out : 1;
-    o.to_block = weights && gated ? up_to(P.out, 16) : o.block;
+    o.to_block = weights && gated ? up_to(P.out, 8) : o.block;
     // (a width that is not whole vectors: the kernel for a few rows relies on the zeros behind both operands' rows)
     o.copy = o.from_ld % 8 != 0 || o.width % 8 != 0 || o.to_block != o.block;
     for (int p = 0; p < P.parts; ++p) {

@@ -819,12 +819,12 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
     // Where the arrays to be stored are staged: in the place of what was read, or in the next output plane.
     auto plane = [&]() { return reads ? x : out + (turn++ & 1) * kTcPlane; };
     if constexpr (gated) {
-      // Lanes 0-15 hold the gates of 16 features, lanes 16-31 their values.
-      const bool upper = lane >= 16;
-      const int mine = (q * 16 + (lane & 15)) * 2;  // byte of this lane's feature in a row of 64
+      // Lanes 0-7 and 16-23 hold the gates of 16 features, the lanes 8 above them their values.
+      const bool upper = lane & 8;
+      const int mine = (q * 16 + lane / 16 * 8 + (lane & 7)) * 2;  // byte of this lane's feature in a row of 64
       if (keep) {
         // gates in the first half of a staged row, values in the second with 32-byte
-        // units exchanged, so that both halves of the warp write to different banks
+        // units exchanged, so that gates and values go to different banks
         unsigned char* o = out + (turn++ & 1) * kTcPlane;
 #pragma unroll
         for (int j = 0; j < kTcColumns; ++j)
@@ -842,11 +842,11 @@ __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, con
           else if (r >= 0 && u * 8 < left) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
         }
       }
-      // The halves of a warp swap: each lane then has gate and value of 8 of the 16 columns.
+      // They swap: each lane then has gate and value of 8 of the 16 columns.
       unsigned char* o = plane();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[8 + j]) + bias, 16);
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[8 + j]) + bias, 8);
         const float own = __uint_as_float(upper ? v[8 + j] : v[j]) + bias;
         const int at_byte = (upper ? 8 + j : j) * 128 + mine;
         float z = mm_act(HOC_ACT_SILU, upper ? other : own) * (upper ? own : other);
@@ -1200,7 +1200,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
             copy3(a, &L.w[A.p], fa, x, A.g, bar);
             copy3(a + 8192u, &L.w[A.p], fa + 64, x, A.g, bar);
           } else if (gated) {
-            copy5(a, &L.w[A.p], x, 0, 0, fa / 16, A.g, bar);
+            copy5(a, &L.w[A.p], x, 0, 0, fa / 8, A.g, bar);
           } else {
             copy3(a, &L.w[A.p], x, fa, A.g, bar);
           }
@@ -1321,9 +1321,9 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
       if (MODE != kWgrad) {
         group_at<8, RAGGED>(P, A.p, A.g, load_ranges<8, RAGGED>(P, A.p, W.ends), A.c0 + lane * 8, row, valid);
         valid = lane * 8 < T.tile_rows ? min(valid, 8) : 0;  // past them: the next tile's rows
-        const int f = gated ? A.f0 + rank * 64 + q * 16 + (lane & 15) : A.f0 + rank * 128 + q * 32 + lane;
+        const int f = gated ? A.f0 + rank * 64 + q * 16 + lane / 16 * 8 + (lane & 7) : A.f0 + rank * 128 + q * 32 + lane;
         if (MODE == kForward && P.bias[A.p] && f < P.out)
-          bias = bf16_of(P.bias[A.p] + int64_t(A.g) * (gated ? 2 : 1) * P.out + (gated && lane >= 16 ? P.out : 0) + f);
+          bias = bf16_of(P.bias[A.p] + int64_t(A.g) * (gated ? 2 : 1) * P.out + (gated && (lane & 8) ? P.out : 0) + f);
       }
       if (MODE == kWgrad && A.steps == 0 && P.accumulate) return true;  // an expert without rows adds nothing
       const uint32_t acc = it & 1;
@@ -1406,9 +1406,10 @@ bool encode_rows(CUtensorMap* m, const void* at, int64_t width, int64_t rows, in
 bool encode_weight(CUtensorMap* m, const MmParams& P, int mode, const void* at) {
   const cuuint64_t in = P.in, out = P.out, ld = P.ld_w, rows = P.out_w, ne = P.experts;
   if (mode == kForward && P.act == HOC_ACT_SWIGLU) {
-    // [expert][gate, value][out / 16][16][in], fetched so that 16 gates and their 16 values alternate
-    const cuuint64_t dims[5] = {in, 16, 2, rows / 16, ne}, strides[4] = {ld, rows * ld, 16 * ld, 2 * rows * ld};
-    const cuuint32_t box[5] = {kTcDepth, 16, 2, 4, 1};
+    // [expert][gate, value][out / 8][8][in], fetched so that 8 gates and their 8 values alternate
+    // (16 and 16 would need copies of the weights where out is no multiple of 16)
+    const cuuint64_t dims[5] = {in, 8, 2, rows / 8, ne}, strides[4] = {ld, rows * ld, 8 * ld, 2 * rows * ld};
+    const cuuint32_t box[5] = {kTcDepth, 8, 2, 8, 1};
     return encode(m, at, 5, dims, strides, box);
   }
   const cuuint64_t dims[3] = {in, out, ne}, strides[2] = {ld, rows * ld};
@@ -1490,7 +1491,7 @@ Cut choose_cut(int64_t rows, int64_t others, int64_t steps, const int* clusters,
 
 bool mm_tc_takes(const MmParams& P, int mode) {
   const bool gated = mode == kForward && P.act == HOC_ACT_SWIGLU;
-  if (P.ld_rows % 8 || (mode == kWgrad ? P.ld_dy % 8 : P.ld_w % 8) || (gated && P.out_w % 16)) return false;
+  if (P.ld_rows % 8 || (mode == kWgrad ? P.ld_dy % 8 : P.ld_w % 8) || (gated && P.out_w % 8)) return false;
   uintptr_t at = 0;
   for (int p = 0; p < P.parts; ++p)
     at |= reinterpret_cast<uintptr_t>(P.rows[p]) | reinterpret_cast<uintptr_t>(P.dy[p]) | reinterpret_cast<uintptr_t>(P.w[p]);

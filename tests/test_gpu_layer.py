@@ -635,3 +635,16 @@ def test_bias_gradient_beside_the_weight_gradient(rows, inp, out, accumulate):
     a, v, keep = dy.double(), x.double(), float(accumulate)
     ref.close(got[0][0], a.t() @ v + keep * w0.double(), (a.abs().t() @ v.abs()) * rows * ref.F32 + w0.double().abs() * ref.F32, "dw")
     ref.close(got[0][1], a.sum(0) + keep * b0.double(), a.abs().sum(0) * rows * ref.F32 + b0.double().abs() * ref.F32, "db")
+
+
+@pytest.mark.parametrize("out", [8, 24, 72, 136, 264])
+def test_gates_of_any_multiple_of_eight(out):
+    """Gates and values lie `out` rows apart; the last tile holds fewer than its 128."""
+    rows, inp = 150, 200
+    x, w, b = normal(rows, inp, seed=1), normal(2 * out, inp, seed=2, sigma=inp ** -0.5), normal(2 * out, seed=3)
+    y, pre, st = torch.empty(rows, out, dtype=BF, device=DEV), torch.empty(rows, 2 * out, dtype=BF, device=DEV), status()
+    hoc.linear(x, w, y, status=st, bias=b, act="swiglu", pre=pre)
+    assert st.item() == 0
+    z, ez, want, err = ref.forward(x, w, b, "swiglu")
+    ref.close(pre, z, ez, "pre")
+    ref.close(y, want, err, "y")
