@@ -37,8 +37,8 @@
 // TFLOP/s), gradients 80 us (1718); 8192 rows of 4096 -> 8192 forward and data
 // gradient 295 us (1864), weight gradient 308 us (1785); bound by the tensor cores and,
 // in the first, by the waves' ends.  8 ranks x 4096 tokens, top-6 of 64 experts, Zipf
-// (196,608 rows in 512 ranges): 2048 -> 1280 gated with its pre-activation 1290 us (1600
-// TFLOP/s), weight gradient of 2048 x 2560 1400 us (1470; the packed remainders of
+// (196,608 rows in 512 ranges): 2048 -> 1280 gated with its pre-activation 1205 to 1240 us
+// (1660 to 1710 TFLOP/s), weight gradient of 2048 x 2560 1400 us (1470; the packed remainders of
 // ranges and stores of 671 MB), and at half the tokens the data gradient 1280 <- 2048
 // through the gate 415 us (1240 TFLOP/s and 4.2 TB/s: 313 of them without the rows that
 // the epilogue reads and writes).  16 tokens instead of 4096: 128 us, 107 in a row (6.1
@@ -91,7 +91,7 @@ struct TcParams {  // but for the tensor maps
   int tile_rows;     // most rows c of a tile, a multiple of 32
   uint32_t stage;    // bytes of a stage: 128 x 64 of A, half of tile_rows x 64 of B
   uint32_t stages;   // as many as the epilogue's planes leave room for: 5 or 6 of a tile of 256 rows
-  uint32_t planes;   // staged arrays of each of the two epilogue groups
+  uint32_t planes;   // of kTcPlane bytes for each of the two epilogue groups
   int sums;          // wgrad of one range: spare warps sum the columns of dy, to P.pre_out[0]
   int loose;         // what the epilogue moves is not whole 16-byte vectors
   int log_shares;    // CTA pairs that share the contraction of a tile: 1, 2 or 4, all of one cluster
@@ -581,23 +581,61 @@ __device__ __forceinline__ void with_act(int act, F f) {
   }
 }
 
-// Rows move between global and shared memory as 16-byte vectors: the lanes of a
-// warp hold 32 features, 64 bytes of a row, and stores of single values from
-// there (2048 of them for a tile) were what bounded the kernel at the expert
-// layer's widths.  Four warps together stage kTcColumns rows of 128 features, so
-// that a row goes out as 256 contiguous bytes.  What the epilogue reads beside
-// the accumulator (the residual, the pre-activation of the layer below) comes
-// the same way, two steps ahead (one step was shorter than the latency of HBM), and
-// results take the place of what was read.
+// A lane of tensor memory holds one feature, a row in global memory is contiguous in
+// features: the sums cross over through shared memory.  Four warps put
+// kTcColumns columns of 128 features there as binary32 and take them out as 8
+// features of one row per thread, so that what is stored, and a residual, moves as
+// 16-byte vectors straight between registers and global memory.  (Stores of single
+// values were what bounded the kernel at the expert layer's widths; staging the rounded
+// values took 1263 us for the gated product of 2048 -> 1280 with its pre-activation,
+// this takes 1205.)
 
-// Where the features of a staged row are in global memory: `chunks` vectors of 8
-// features, of which the last may lie past the row's end.
+// The rows of a tensor from a feature on.
 struct Strip {
-  char* at;        // feature f0 of row 0
+  char* at;        // that feature in row 0
   int64_t pitch;   // bytes of a row
-  int left;        // features from f0 to the end of a row
+  int left;        // features from there to the end of a row; none of them when it is not positive
   bool loose;      // rows are not whole 16-byte vectors: moved value by value
 };
+__device__ __forceinline__ uint4 get8(const Strip& G, int row) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (row < 0 || G.left <= 0) return v;
+  const char* at = G.at + row * G.pitch;
+  if (!G.loose) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    return v;
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < G.left) w[e / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(at)[e]) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void put8(const Strip& G, int row, const float (&z)[8]) {
+  if (row < 0 || G.left <= 0) return;
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 pair = __floats2bfloat162_rn(z[2 * e], z[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&pair);
+  }
+  char* at = G.at + row * G.pitch;
+  if (!G.loose) {
+    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < G.left) reinterpret_cast<uint16_t*>(at)[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
+}
+__device__ __forceinline__ void unpack8(const uint4& v, float (&z)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    z[2 * e] = __uint_as_float(w[e] << 16);
+    z[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
 // The first `left` of 8 values, one by one.
 __device__ __forceinline__ void put_loose(char* to, const unsigned char* from, int left) {
   for (int e = 0; e < 8; ++e)
@@ -621,18 +659,17 @@ __device__ __forceinline__ bool group_all(int eg, bool ok) {
   return r != 0;
 }
 // The row that column `c` of the step at `col` stands for, -1 if none.  Whole warps call it.
-__device__ __forceinline__ int64_t row_of(int col, int c, int row, int valid) {
+__device__ __forceinline__ int row_of(int col, int c, int row, int valid) {
   const int gi = ((col + c) >> 3) & 31;
   const int r0 = __shfl_sync(0xFFFFFFFFu, row, gi), nv = __shfl_sync(0xFFFFFFFFu, valid, gi);
-  return (c & 7) < nv ? int64_t(r0) + (c & 7) : -1;
+  return (c & 7) < nv ? r0 + (c & 7) : -1;
 }
-
 // The rows that this thread moves in a step at `col`: vector (i + 128 h) % CHUNKS
 // of column (i + 128 h) / CHUNKS, i its number in the group.  at(c): the row of
 // column c of the step, or -1.
 template <int CHUNKS>
 struct Rows {
-  int64_t r[kTcColumns * CHUNKS / 128];
+  int r[kTcColumns * CHUNKS / 128];
   template <class At>
   __device__ __forceinline__ explicit Rows(At at) {
 #pragma unroll
@@ -752,142 +789,187 @@ __device__ __forceinline__ void add_sums(const TcParams& T, uint32_t (&v)[kTcCol
 
 // The epilogue of one tile by group `eg` of four warps (warp q of it has tensor
 // memory lanes 32 q ..): the steps of kTcColumns columns whose number is eg modulo
-// 2.  in: the group's three input buffers (dgrad: of two planes each); out: its two
-// output planes, which the arrays that are stored take in turn; turn and buffer go on
-// from tile to tile.  False when the accumulator did not come.
+// 2 (of this share's).  (MODE kDgrad: with no activation.)  plane: the group's staging, [column][128 features] binary32, in
+// which the 16-byte quads of a warp's 32 features are exchanged by q, so that both
+// sides reach all banks.  False when the accumulator did not come.
 template <int MODE, int ACT, bool RAGGED>
-__device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, const Tile& A, uint32_t stages, unsigned char* in,
-                                             unsigned char* out, uint32_t& turn, uint32_t& buffer, uint32_t acc_at, uint64_t* acc_full,
-                                             uint32_t parity, int eg, int q, int rank, int row, int valid, float bias) {
+__device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, const Tile& A, uint32_t stages, uint32_t plane,
+                                             uint32_t acc_at, uint64_t* acc_full, uint32_t parity, int eg, int q, int rank,
+                                             int row, int valid, float bias) {
   constexpr bool gated = MODE == kForward && ACT == HOC_ACT_SWIGLU;
-  constexpr bool twice = MODE == kDgrad && ACT == HOC_ACT_SWIGLU;  // two inputs, two outputs
+  constexpr int kVectors = gated ? 8 : 16;                         // of 8 features, in a row
+  constexpr int kPer = kTcColumns * kVectors / 128;                // of a thread, in a step
   const MmParams& P = T.P;
-  const int lane = threadIdx.x & 31;
-  const int f0 = A.f0 + rank * (gated ? 64 : 128);
+  const int lane = threadIdx.x & 31, i = threadIdx.x & 127;
+  const int u = i % kVectors, c0 = i / kVectors;  // this thread's vector, and its first column
   const int width = MODE == kForward ? P.out : P.in;
   const int64_t wide = int64_t(width) * (ACT == HOC_ACT_SWIGLU ? 2 : 1);  // of pre
-  const uint32_t in_addr = ptx::smem_addr(in);
   const bool res = MODE == kForward && P.res[A.p] != nullptr;
   const bool keep = MODE == kForward && P.pre_out[A.p] != nullptr;
-  const bool reads = res || (MODE == kDgrad && ACT != HOC_ACT_NONE);
   // clamped so that no pointer is formed past the tensors
-  const int left = width - f0, fs = left > 0 ? f0 : 0;
-  const Strip y{static_cast<char*>(P.y[A.p]) + 2 * int64_t(fs), 2 * P.ld_y, left, T.loose != 0};
-  Strip beside{};
-  if (res) beside = {reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.res[A.p])) + 2 * int64_t(fs), 2 * P.ld_res, left, T.loose != 0};
-  if (MODE == kDgrad && ACT != HOC_ACT_NONE)
-    beside = {reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.pre[A.p])) + 2 * int64_t(fs), 2 * wide, left, T.loose != 0};
-  const Strip kept{static_cast<char*>(P.pre_out[A.p]) + 2 * int64_t(fs), 2 * wide, left, T.loose != 0};
+  const int f0 = A.f0 + rank * (gated ? 64 : 128) + u * 8, left = width - f0, fs = left > 0 ? f0 : 0;
+  auto strip = [&](const void* at, int64_t ld) {
+    return Strip{static_cast<char*>(const_cast<void*>(at)) + 2 * int64_t(fs), 2 * ld, left, T.loose != 0};
+  };
   auto second = [&](Strip s) {
     s.at += 2 * int64_t(width);
     return s;
   };
-  constexpr uint32_t kBuffer = (MODE == kDgrad ? 2 : 1) * kTcPlane;
+  const Strip y = strip(P.y[A.p], P.ld_y), kept = strip(P.pre_out[A.p], wide);
+  const Strip beside = strip(P.res[A.p], P.ld_res);
+  int r[kPer];      // this thread's rows of a step
+  uint4 add[kPer];  // and the residual there, loaded a step ahead
+  auto load = [&](int col) {
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) {
+      r[h] = row_of(col, c0 + h * (kTcColumns / kPer), row, valid);
+      if (res && col < A.n) add[h] = get8(beside, r[h]);
+    }
+  };
+  const int share = RAGGED ? 0 : int(cta_rank()) >> 1, stride = RAGGED ? 2 * kTcColumns : (2 * kTcColumns) << T.log_shares;
+  const int first = (eg + 2 * share) * kTcColumns;
+  if (res) {
+    // The tile's residual into L2, a row of 128 features per lane and warp: a step is shorter than the latency of
+    // HBM (8192 rows of 512 -> 4096 with a residual 64 us, 78 without this).
+    const int from = A.f0 + rank * (gated ? 64 : 128), w = eg * 4 + q;
+    if (w < valid)
+      for (int f = from; f < from + (gated ? 64 : 128) && f < width; f += 64)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(P.res[A.p] + (row + w) * P.ld_res + f));
+  }
+  load(first);
+  bool ok = warp_wait(acc_full, parity, T, S);
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (!RAGGED && ok && T.log_shares) ok = exchange_sums(T, S, A.n, stages, acc_at, eg);
+  if (!group_all(eg, ok)) return false;
+  const uint32_t put_at = plane + uint32_t(((q * 8 + (lane >> 2)) ^ q) * 16 + (lane & 3) * 4);
+  for (int col = first; col < A.n; col += stride) {
+    uint32_t v[kTcColumns];
+    tmem_load(v, acc_at + uint32_t(col));
+    if (!RAGGED && T.log_shares) add_sums(T, v, stages, col);
+#pragma unroll
+    for (int j = 0; j < kTcColumns; ++j)
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(put_at + j * 512u), "f"(__uint_as_float(v[j]) + bias) : "memory");
+    group_barrier(eg);
+    float z[kPer][gated ? 16 : 8];
+#pragma unroll
+    for (int h = 0; h < kPer; ++h)
+#pragma unroll
+      for (int k = 0; k < (gated ? 4 : 2); ++k) {
+        const int quad = gated ? (4 * u + k) ^ (u >> 1) : (2 * u + k) ^ (u >> 2);
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(z[h][4 * k]), "=f"(z[h][4 * k + 1]), "=f"(z[h][4 * k + 2]), "=f"(z[h][4 * k + 3])
+                     : "r"(plane + (c0 + h * (kTcColumns / kPer)) * 512u + uint32_t(quad) * 16u)
+                     : "memory");
+      }
+    group_barrier(eg);  // the plane is free again
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) {
+      float o[8], x[8];
+      if (res) unpack8(add[h], x);
+      if constexpr (gated) {
+        float g[8], l[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          g[e] = z[h][e];
+          l[e] = z[h][8 + e];
+          o[e] = mm_act(HOC_ACT_SILU, g[e]) * l[e];
+          if (res) o[e] += x[e];
+        }
+        if (keep) {
+          put8(kept, r[h], g);
+          put8(second(kept), r[h], l);
+        }
+      } else if constexpr (MODE == kForward) {
+        if (keep) put8(kept, r[h], z[h]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          o[e] = mm_act(ACT, z[h][e]);
+          if (res) o[e] += x[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = z[h][e];
+      }
+      put8(y, r[h], o);
+    }
+    load(col + stride);
+  }
+  return true;
+}
+
+// The data gradient through an activation reads a row, or with gates two, for each
+// that it writes.  Loads into registers cannot be kept in flight long enough there (444
+// us through the gate for the data gradient of 1280 <- 2048, where this takes 411, and 179
+// against 126 through SiLU for 36,432 rows of 1984 <- 392): rows come into shared memory by asynchronous copies two
+// steps ahead, and results, staged as bf16, take the place of what was read.  plane: the
+// group's three buffers, with gates of two planes each.
+template <int ACT, bool RAGGED>
+__device__ __forceinline__ bool run_slope_epilogue(const TcParams& T, TcShared* S, const Tile& A, uint32_t stages,
+                                                   unsigned char* planes, uint32_t& buffer, uint32_t acc_at, uint64_t* acc_full,
+                                                   uint32_t parity, int eg, int q, int rank, int row, int valid) {
+  constexpr bool twice = ACT == HOC_ACT_SWIGLU;  // two inputs, two outputs
+  const MmParams& P = T.P;
+  const int lane = threadIdx.x & 31, width = P.in, f0 = A.f0 + rank * 128;
+  const int64_t wide = int64_t(width) * (twice ? 2 : 1);  // of pre
+  const uint32_t planes_addr = ptx::smem_addr(planes);
+  // clamped so that no pointer is formed past the tensors
+  const int left = width - f0, fs = left > 0 ? f0 : 0;
+  const Strip y{static_cast<char*>(P.y[A.p]) + 2 * int64_t(fs), 2 * P.ld_y, left, T.loose != 0};
+  const Strip beside{reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.pre[A.p])) + 2 * int64_t(fs), 2 * wide, left, T.loose != 0};
+  auto second = [&](Strip s) {
+    s.at += 2 * int64_t(width);
+    return s;
+  };
+  constexpr uint32_t kBuffer = 2 * kTcPlane;
   auto fetch = [&](int col, uint32_t buffer) {
     if (col < A.n) {
-      const Rows<gated ? 8 : 16> r([&](int c) { return row_of(col, c, row, valid); });
-      fetch_rows(in_addr + buffer * kBuffer, beside, r);
-      if constexpr (twice) fetch_rows(in_addr + buffer * kBuffer + kTcPlane, second(beside), r);
+      const Rows<16> r([&](int c) { return row_of(col, c, row, valid); });
+      fetch_rows(planes_addr + buffer * kBuffer, beside, r);
+      if constexpr (twice) fetch_rows(planes_addr + buffer * kBuffer + kTcPlane, second(beside), r);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   const int share = RAGGED ? 0 : int(cta_rank()) >> 1, stride = RAGGED ? 2 * kTcColumns : (2 * kTcColumns) << T.log_shares;
   const int first = (eg + 2 * share) * kTcColumns;
-  if (reads) {  // the buffer of the last tile's last step may still be read: the two others
-    fetch(first, buffer);
-    fetch(first + stride, buffer == 2 ? 0 : buffer + 1);
-  }
+  // the buffer of the last tile's last step may still be read: the two others
+  fetch(first, buffer);
+  fetch(first + stride, buffer == 2 ? 0 : buffer + 1);
   bool ok = warp_wait(acc_full, parity, T, S);
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (!RAGGED && ok && T.log_shares) ok = exchange_sums(T, S, A.n, stages, acc_at, eg);
   if (!group_all(eg, ok)) {
-    if (reads) asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return false;
   }
   for (int col = first; col < A.n; col += stride) {
     uint32_t v[kTcColumns];
     tmem_load(v, acc_at + uint32_t(col));
     if (!RAGGED && T.log_shares) add_sums(T, v, stages, col);
-    auto at = [&](int c) { return row_of(col, c, row, valid); };
-    unsigned char* x = in + buffer * kBuffer;
-    if (reads) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      group_barrier(eg);  // this step's input is there, and the buffer of the step before is free
-      fetch(col + 2 * stride, buffer == 0 ? 2 : buffer - 1);
-      buffer = buffer == 2 ? 0 : buffer + 1;
+    unsigned char* x = planes + buffer * kBuffer;
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    group_barrier(eg);  // this step's input is there, and the buffer of the step before is free
+    fetch(col + 2 * stride, buffer == 0 ? 2 : buffer - 1);
+    buffer = buffer == 2 ? 0 : buffer + 1;
+    const Rows<16> r([&](int c) { return row_of(col, c, row, valid); });
+#pragma unroll
+    for (int j = 0; j < kTcColumns; ++j) {
+      unsigned char* z = x + j * kTcRowBytes + (q * 32 + lane) * 2;
+      float d = __uint_as_float(v[j]);
+      const float g = bf16_at(z);
+      if constexpr (twice) {
+        const float u = bf16_at(z + kTcPlane);
+        put_bf16(z + kTcPlane, d * mm_act(HOC_ACT_SILU, g));
+        d *= u * mm_act_slope(HOC_ACT_SILU, g);
+      } else {
+        d *= mm_act_slope(ACT, g);
+      }
+      put_bf16(z, d);
     }
-    // Where the arrays to be stored are staged: in the place of what was read, or in the next output plane.
-    auto plane = [&]() { return reads ? x : out + (turn++ & 1) * kTcPlane; };
-    if constexpr (gated) {
-      // Lanes 0-7 and 16-23 hold the gates of 16 features, the lanes 8 above them their values.
-      const bool upper = lane & 8;
-      const int mine = (q * 16 + lane / 16 * 8 + (lane & 7)) * 2;  // byte of this lane's feature in a row of 64
-      if (keep) {
-        // gates in the first half of a staged row, values in the second with 32-byte
-        // units exchanged, so that gates and values go to different banks
-        unsigned char* o = out + (turn++ & 1) * kTcPlane;
-#pragma unroll
-        for (int j = 0; j < kTcColumns; ++j)
-          put_bf16(o + j * kTcRowBytes + (upper ? 128 + (mine ^ 32) : mine), __uint_as_float(v[j]) + bias);
-        group_barrier(eg);
-        const int i = int(threadIdx.x) & 127;
-#pragma unroll
-        for (int h = 0; h < kTcColumns * 16 / 128; ++h) {
-          const int c = (i + 128 * h) / 16, u = (i + 128 * h) % 8;
-          const bool value = (i + 128 * h) % 16 >= 8;
-          const int64_t r = at(c);
-          char* to = kept.at + r * kept.pitch + (value ? 2 * int64_t(width) : 0) + u * 16;
-          const unsigned char* from = o + c * kTcRowBytes + (value ? 128 + ((u * 16) ^ 32) : u * 16);
-          if (T.loose) put_loose(to, from, r >= 0 ? left - u * 8 : 0);
-          else if (r >= 0 && u * 8 < left) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
-        }
-      }
-      // They swap: each lane then has gate and value of 8 of the 16 columns.
-      unsigned char* o = plane();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(upper ? v[j] : v[8 + j]) + bias, 8);
-        const float own = __uint_as_float(upper ? v[8 + j] : v[j]) + bias;
-        const int at_byte = (upper ? 8 + j : j) * 128 + mine;
-        float z = mm_act(HOC_ACT_SILU, upper ? other : own) * (upper ? own : other);
-        if (res) z += bf16_at(x + at_byte);
-        put_bf16(o + at_byte, z);
-      }
-      group_barrier(eg);
-      put_rows(o, y, Rows<8>(at));
-    } else {
-      const int mine = (q * 32 + lane) * 2;
-      const Rows<16> r(at);
-      if (keep) {
-        unsigned char* o = out + (turn++ & 1) * kTcPlane;
-#pragma unroll
-        for (int j = 0; j < kTcColumns; ++j) put_bf16(o + j * kTcRowBytes + mine, __uint_as_float(v[j]) + bias);
-        group_barrier(eg);
-        put_rows(o, kept, r);
-      }
-      unsigned char* o = plane();
-#pragma unroll
-      for (int j = 0; j < kTcColumns; ++j) {
-        const unsigned char* z = x + j * kTcRowBytes + mine;
-        float d = __uint_as_float(v[j]);
-        if (MODE == kForward) {
-          d = mm_act(ACT, d + bias);
-          if (res) d += bf16_at(z);
-        } else if (twice) {
-          const float g = bf16_at(z), u = bf16_at(z + kTcPlane);
-          put_bf16(o + kTcPlane + j * kTcRowBytes + mine, d * mm_act(HOC_ACT_SILU, g));
-          d *= u * mm_act_slope(HOC_ACT_SILU, g);
-        } else if (ACT != HOC_ACT_NONE) {
-          d *= mm_act_slope(ACT, bf16_at(z));
-        }
-        put_bf16(o + j * kTcRowBytes + mine, d);
-      }
-      group_barrier(eg);
-      put_rows(o, y, r);
-      if constexpr (twice) put_rows(o + kTcPlane, second(y), r);
-    }
+    group_barrier(eg);
+    put_rows(x, y, r);
+    if constexpr (twice) put_rows(x + kTcPlane, second(y), r);
   }
-  if (reads) asm volatile("cp.async.wait_all;" ::: "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
   return true;
 }
 
@@ -1013,11 +1095,10 @@ __device__ __forceinline__ void sum_columns(const MmParams& P, TcShared* S, int 
 }
 
 // ------------------------------------------------------------------ kernel
-// Shared memory: the stages, the planes of the two epilogue groups (two output
-// planes; where the epilogue reads rows, three input buffers, which in dgrad have two
-// planes each and hold the results too), the barriers and tile counts.
+// Shared memory: the stages, the planes of the two epilogue groups (two, or the six of
+// three input buffers), the barriers and tile counts.
 constexpr uint32_t kTcSmem = 232448;  // 227 KB
-constexpr uint32_t planes_of(int mode, bool reads) { return !reads ? 2 : mode == kForward ? 5 : 6; }
+constexpr uint32_t planes_of(int mode, int act) { return mode == kDgrad && act != HOC_ACT_NONE ? 6 : 2; }
 constexpr uint32_t stages_in(uint32_t planes, uint32_t stage) {
   const uint32_t n = (kTcSmem - 1024 - uint32_t(sizeof(TcShared)) - 2 * planes * kTcPlane) / stage;
   return n < uint32_t(kTcMostStages) ? n : uint32_t(kTcMostStages);
@@ -1310,8 +1391,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
   } else if (warp >= 4 && warp < 4 + kTcEpilogue) {
     // ---- epilogue: two groups of four warps take turns along the columns
     const int q = warp & 3, eg = (warp - 4) / 4;
-    unsigned char* in = planes + eg * T.planes * kTcPlane;
-    unsigned char* out = MODE == kForward && T.planes > 2 ? in + 3 * kTcPlane : in;
+    unsigned char* mine = planes + eg * T.planes * kTcPlane;
     uint32_t it = 0, turn = 0, buffer = 0;
     Work<RAGGED> W(T, S, who, of, tiles);
     each_tile<MODE, RAGGED>(W, MODE != kWgrad, [&]() {
@@ -1330,11 +1410,16 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
       const uint32_t at = S->tmem + acc * 256u + (uint32_t(q * 32) << 16);
       bool ok = true;
       if constexpr (MODE == kWgrad) {
-        ok = run_wgrad_epilogue<RAGGED>(T, S, A, base, out, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q, rank);
+        ok = run_wgrad_epilogue<RAGGED>(T, S, A, base, mine, turn, at, &S->acc_full[acc], (it >> 1) & 1, eg, q, rank);
       } else {
         with_act(P.act, [&](auto tag) {
-          ok = run_epilogue<MODE, decltype(tag)::act, RAGGED>(T, S, A, base, in, out, turn, buffer, at, &S->acc_full[acc],
-                                                      (it >> 1) & 1, eg, q, rank, row, valid, bias);
+          constexpr int act = decltype(tag)::act;
+          if constexpr (MODE == kDgrad && act != HOC_ACT_NONE)
+            ok = run_slope_epilogue<act, RAGGED>(T, S, A, base, mine, buffer, at, &S->acc_full[acc], (it >> 1) & 1, eg, q,
+                                                 rank, row, valid);
+          else
+            ok = run_epilogue<MODE, act, RAGGED>(T, S, A, base, ptx::smem_addr(mine), at, &S->acc_full[acc], (it >> 1) & 1,
+                                                 eg, q, rank, row, valid, bias);
         });
       }
       if (!ok) return false;
@@ -1545,9 +1630,7 @@ static cudaError_t launch(const MmParams& P, int mode, cudaStream_t s, bool* sum
   if (e != cudaSuccess) return e;
   cfg.stream = s;
   T.stage = mode == kWgrad ? kTcStage : kTcOperand + uint32_t(T.tile_rows) * (kTcDepth * 2 / 2);
-  bool reads = mode == kDgrad && P.act != HOC_ACT_NONE;
-  for (int p = 0; mode == kForward && p < P.part0 + P.parts; ++p) reads = reads || P.res[p] != nullptr;
-  T.planes = planes_of(mode, reads);
+  T.planes = planes_of(mode, P.act);
   T.ftiles = divisor(uint32_t(ftiles));
   T.ctiles = divisor(uint32_t((P.out + T.tile_rows - 1) / T.tile_rows));
   T.each = divisor(T.ctiles.d * T.ftiles.d);
