@@ -1528,13 +1528,13 @@ cudaError_t configure(const void* fn, int mode, bool ragged, int log_shares, cud
   cfg.dynamicSmemBytes = kTcSmem;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmem));
-  if (e != cudaSuccess) return e;
   int dev = 0;
-  e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   clusters = dev < 64 ? known[mode][kind][dev].load() : 0;
   if (clusters > 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmem));
+  if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2u << log_shares);
   e = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg);
