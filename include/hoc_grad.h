@@ -32,7 +32,7 @@ hocResult_t hoc_tensor_list_destroy(hocTensorList_t* list);
 hocResult_t hoc_grad_workspace(const hocTensorList_t* list, size_t* ints);
 
 /* norm[0] (device binary32) = sqrt of the sum of squares over all tensors.
- * Squares are binary32, summed in binary32 within a tile of at most 32768
+ * Squares are binary32, summed in binary32 within a tile of at most 8192
  * elements and in binary64 across tiles, in an order that depends only on the
  * list: the same list and values give the same bits.  A square above
  * the binary32 range makes the norm inf, a NaN makes it NaN; 0 for no elements. */
