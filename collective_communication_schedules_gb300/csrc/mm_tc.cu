@@ -29,7 +29,7 @@
 // Warps of a CTA: 0 and 2 tensor copies of the rows, 64 each; 3 those of the
 // weights; 1 MMA (of the pair's first CTA); 4-11 epilogue.  In the weight gradient
 // warps 0 and 12 issue all copies of every second stage, and warps 2, 3 and 13-15
-// zero padding rows.  Every wait is bounded: a wait that runs out sets bit 2 of the
+// zero padding rows (one range: warp 2, and the others sum the bias gradient).  Every wait is bounded: a wait that runs out sets bit 2 of the
 // status, and all roles leave.
 //
 // Measured, single calls from a flushed cache; the peaks measured on this GPU are 1951
