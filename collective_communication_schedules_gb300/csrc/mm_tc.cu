@@ -1311,7 +1311,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
       const int steps = run ? A.steps : 1;
       for (int s = 0; s < steps; ++s) {
         if (run) {
-          if (!warp_wait(&S->full[k.st], k.round & 1, T, S)) {
+          if (!warp_wait<MODE == kWgrad>(&S->full[k.st], k.round & 1, T, S)) {  // wgrad: the other CTA's zeros too
             ok = false;
             break;
           }
