@@ -178,6 +178,9 @@ cudaError_t mm_any_preload();
 // Whether the tensor-core kernel takes these operands (alignment and widths of
 // what tensor copies fetch; the epilogue's rows may lie anywhere).
 bool mm_tc_takes(const MmParams& P, int mode);
+// Whether a row that the epilogue of this launch (rank buffers part0 .. part0 + parts)
+// reads or writes is not whole 16-byte vectors.
+bool mm_tc_loose(const MmParams& P, int mode);
 // summed (weight gradient): whether the launch sums the columns of dy too, to P.pre_out[0].
 cudaError_t launch_mm_tc(const MmParams& P, int mode, cudaStream_t s, bool* summed);
 cudaError_t mm_tc_preload();

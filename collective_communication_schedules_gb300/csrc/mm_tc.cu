@@ -1583,12 +1583,11 @@ bool mm_tc_takes(const MmParams& P, int mode) {
   return (at & 15u) == 0 && encoder() != nullptr;
 }
 
-// Whether a row that the epilogue reads or writes is not whole 16-byte vectors.
-static bool is_loose(const MmParams& P, int mode) {
+bool mm_tc_loose(const MmParams& P, int mode) {
   const int width = mode == kForward ? P.out : P.in;
   if (width % 8 || P.ld_y % 8) return true;
   uintptr_t at = 0;
-  for (int p = 0; p < P.parts; ++p) {
+  for (int p = P.part0; p < P.part0 + P.parts; ++p) {
     at |= reinterpret_cast<uintptr_t>(P.y[p]) | reinterpret_cast<uintptr_t>(P.pre[p]) | reinterpret_cast<uintptr_t>(P.res[p]);
     if (mode == kForward) at |= reinterpret_cast<uintptr_t>(P.pre_out[p]);
     if (P.res[p] && P.ld_res % 8) return true;
@@ -1601,7 +1600,7 @@ static cudaError_t launch(const MmParams& P, int mode, cudaStream_t s, bool* sum
   TcLaunch<RAGGED> L;
   TcParams& T = L.T;
   T.P = P;
-  T.loose = is_loose(P, mode);
+  T.loose = mm_tc_loose(P, mode);
   const char* fault = getenv("HOC_FAULT");
   const bool stall = fault && !strcmp(fault, "mm_stall");
   T.tx_pad = stall ? 16u : 0u;
