@@ -300,6 +300,9 @@ extern "C" hocResult_t hoc_tensor_list_create(hocTensorList_t** list, int n, con
     if (e == cudaSuccess) e = cudaMalloc(&l->tiles, bytes);
     if (e == cudaSuccess && !tiles.empty())
       e = cudaMemcpy(l->tiles, tiles.data(), sizeof(Tile) * tiles.size(), cudaMemcpyHostToDevice);
+    // A copy from pageable memory may return before the data is on the device, ordered with nothing
+    // but the default stream; the kernels read the table on any stream, ahead of what they wait for.
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
     if (e != cudaSuccess) {
       set_error_detail("hoc_tensor_list_create: allocating or filling the table failed");
       if (l->tiles) cudaFree(l->tiles);
