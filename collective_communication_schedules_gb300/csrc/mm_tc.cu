@@ -97,7 +97,7 @@ struct TcParams {  // but for the tensor maps
   int log_shares;    // CTA pairs that share the contraction of a tile: 1, 2 or 4, all of one cluster
   int per;           // stages of each of them (the last may have fewer); INT_MAX where there is one
   uint32_t tx_pad;   // bytes that the copies' barriers expect beyond their loads (0; 16 under HOC_FAULT=mm_stall)
-  uint64_t wait_ns;
+  uint64_t wait_ns;  // 2 s; 0.1 s under HOC_FAULT=mm_stall, 1 ms under mm_hurry
   MmParams P;
 };
 // RAGGED: ranges of rows of experts, on any ranks; else all rows of one buffer.  That
@@ -126,6 +126,7 @@ struct TcShared {
   float sum[2][4][16];         // wgrad of one range: column sums of dy by each spare warp
   uint32_t tmem;
   volatile int dead;
+  volatile unsigned moved;             // wgrad: changes whenever the copies go on to another stage
   int vrows[kMmMaxGroups];
   unsigned tile0[kMmMaxGroups + 1];    // forward, dgrad: whole tiles of the pairs before
   unsigned short order[kMmMaxGroups];  // forward, dgrad: pairs with a lower tile at their end; wgrad: all; most rows first
@@ -173,16 +174,24 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
   return ok != 0;
 }
 // Waits for the phase with `parity`; false when the limit passed here or in
-// another role, after which the caller leaves its loop.  CLUSTER: what other CTAs'
-// threads wrote before they arrived is to be read.
+// another role, after which the caller leaves its loop.  The limit is on standing
+// still: in the weight gradient, whose epilogue may wait through any number of stages
+// for the end of a contraction, it starts anew whenever the CTA's copies have moved
+// on (they are finite, and a stage's copies wait for the products before them).  CLUSTER:
+// what other CTAs' threads wrote before they arrived is to be read.
 template <bool CLUSTER>
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const TcParams& T, TcShared* S) {
   auto came = [&]() { return CLUSTER ? try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
   if (came()) return true;
-  const uint64_t deadline = ptx::global_ns() + T.wait_ns;
+  uint64_t deadline = ptx::global_ns() + T.wait_ns;
+  unsigned moved = S->moved;
   while (!came()) {
     if (S->dead) return false;
-    if (ptx::global_ns() > deadline) {
+    const uint64_t now = ptx::global_ns();
+    if (const unsigned m = S->moved; m != moved) {
+      moved = m;
+      deadline = now + T.wait_ns;
+    } else if (now > deadline) {
       atomicOr(T.P.status, 4);
       S->dead = 1;
       return false;
@@ -1134,6 +1143,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
     ptx::mbar_init(&S->go, (1 << T.log_shares) - 1 + (T.log_shares == 0));
     ptx::mbar_init(&S->came, ((1 << T.log_shares) - 1) * kTcEpilogue + (T.log_shares == 0));
     S->dead = 0;
+    S->moved = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -1221,6 +1231,7 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
             }
             const uint32_t a = base + k.st * T.stage, bar = full0 + k.st * 8u;
             if (one) {
+              S->moved = k.round * kTcMostStages + k.st + 1;
               arrive_expect_cluster(bar, bytes);
               copy2(a, &L.row[A.p][3], fx, r, bar);
               copy2(a + 8192u, &L.row[A.p][3], fx + 64, r, bar);
@@ -1243,7 +1254,10 @@ __global__ void __launch_bounds__(kTcThreads<MODE>, 1)
           // runs of several ranges: lanes are blocks of 64 features (0, 1 of x, then those of dy) x groups
           const uint32_t a = base + k.st * T.stage, bar = ptx::smem_addr(&S->part[k.st]);
           const int box = box_at(row, valid), which = lane >> 3;
-          if (one) arrive_expect_cluster(bar, bytes);
+          if (one) {
+            S->moved = k.round * kTcMostStages + k.st + 1;
+            arrive_expect_cluster(bar, bytes);
+          }
           __syncwarp();
           if (which < 2 + blocks && box >= 0)
             copy2(a + uint32_t(which) * 8192u + uint32_t(lane & 7) * 1024u,
@@ -1604,7 +1618,7 @@ static cudaError_t launch(const MmParams& P, int mode, cudaStream_t s, bool* sum
   const char* fault = getenv("HOC_FAULT");
   const bool stall = fault && !strcmp(fault, "mm_stall");
   T.tx_pad = stall ? 16u : 0u;
-  T.wait_ns = stall ? 100000000ull : kTcWaitNs;
+  T.wait_ns = stall ? 100000000ull : fault && !strcmp(fault, "mm_hurry") ? 1000000ull : kTcWaitNs;
   const void* fn = reinterpret_cast<const void*>(kTc<RAGGED>[mode]);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};

@@ -648,3 +648,31 @@ def test_gates_of_any_multiple_of_eight(out):
     z, ez, want, err = ref.forward(x, w, b, "swiglu")
     ref.close(pre, z, ez, "pre")
     ref.close(y, want, err, "y")
+
+
+@pytest.mark.parametrize("sources", [0, 1, 3])
+def test_a_long_contraction_is_not_a_stall(sources, monkeypatch):
+    """HOC_FAULT=mm_hurry lets waits run out after a millisecond.  The weight gradient over some 4 million rows of one
+    expert, in which the epilogue (and the warps that zero padding rows) wait for longer, is still complete: the limit
+    is on standing still.  Values are small whole numbers, so that binary32 sums are exact.  sources 0: a linear layer,
+    whose contraction four pairs of CTAs share."""
+    rows, inp, out = (1 << 22) + 37, 200, 136
+    g = torch.Generator(device=DEV).manual_seed(sources)
+    x, dy = (torch.randint(-1, 2, (rows, w), generator=g, device=DEV, dtype=torch.int8).to(BF) for w in (inp, out))
+    dw, db, st = torch.zeros(1, out, inp, device=DEV), torch.zeros(1, out, device=DEV), status()
+    monkeypatch.setenv("HOC_FAULT", "mm_hurry")
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    for _ in range(2):
+        start.record()
+        if sources:
+            cuts = [0, rows] if sources == 1 else [0, 1_000_003, 3_000_000, rows]
+            hoc.expert_mm_wgrad([dy], [x], torch.tensor([cuts], device=DEV), [dw], status=st, db=[db])
+        else:
+            hoc.linear_wgrad(dy, x, dw[0], status=st, db=db[0])
+        end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) > 3, "too short to tell a long wait from a stall"
+    assert st.item() == 0
+    want = sum(dy[i: i + (1 << 19)].double().t() @ x[i: i + (1 << 19)].double() for i in range(0, rows, 1 << 19))
+    assert torch.equal(dw[0].double(), want)
+    assert torch.equal(db[0].double(), dy.sum(0, dtype=torch.float64))
