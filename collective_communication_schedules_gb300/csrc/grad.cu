@@ -217,10 +217,17 @@ int grid_of(const hocTensorList* l) {
   return int(l->ntiles < 1 ? 1 : l->ntiles < size_t(kGradCtas) ? l->ntiles : size_t(kGradCtas));
 }
 
+// Whether the list was made on the current device: its table is there, and a launch would run here.
+bool is_here(const hocTensorList* l) {
+  int device = -1;
+  return cudaGetDevice(&device) == cudaSuccess && device == l->device;
+}
+
 // Sum of squares of every tile into the workspace's partial sums.
 hocResult_t squares(const char* who, const hocTensorList_t* src, const float* norm, const int32_t* workspace,
                     size_t workspace_ints, cudaStream_t s) {
   if (!src || !norm || !workspace) return refuse(who, "list, norm and workspace must be given");
+  if (!is_here(src)) return refuse(who, "the list belongs to another device than the current one");
   size_t need = 0;
   hoc_grad_workspace(src, &need);
   if (workspace_ints < need) return refuse(who, "workspace smaller than hoc_grad_workspace() asks for");
@@ -347,6 +354,7 @@ extern "C" hocResult_t hoc_grad_clip(const hocTensorList_t* src, const hocTensor
   if (!src || !dst) return refuse(who, "both lists must be given");
   if (!max_norm || !(*max_norm >= 0.f)) return refuse(who, "max_norm must be at least 0");
   if (src->dtype != dst->dtype || src->count != dst->count) return refuse(who, "the lists differ in counts or dtype");
+  if (src->device != dst->device) return refuse(who, "the lists belong to different devices");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const hocResult_t r = squares(who, src, norm, workspace, workspace_ints, s);
   if (r != HOC_SUCCESS) return r;

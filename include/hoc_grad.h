@@ -20,7 +20,8 @@ extern "C" {
  * pointers again.  ptr[i] and count[i] (elements, 0 allowed) are host arrays
  * read during the call.  Any element alignment; tensors of one list must not
  * overlap.  Creation allocates device memory on the current device and waits
- * for the upload; the tensors stay the caller's. */
+ * for the upload; the tensors stay the caller's.  A list is used with the device
+ * current on which it was made (HOC_ERR_INVALID_ARG otherwise). */
 typedef struct hocTensorList hocTensorList_t;
 hocResult_t hoc_tensor_list_create(hocTensorList_t** list, int n, const void* const* ptr, const size_t* count,
                                    hocDataType_t dtype);
