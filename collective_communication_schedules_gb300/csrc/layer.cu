@@ -280,6 +280,33 @@ hocResult_t refuse(const char* who, const char* what) {
   return HOC_ERR_INVALID_ARG;
 }
 
+// What a launch returned, and nothing else: the runtime's last error may be an earlier call's, which
+// is the caller's to read.  Only a failed launch's own error is cleared.
+hocResult_t launched(const char* who, cudaError_t e) {
+  if (e == cudaSuccess) return HOC_SUCCESS;
+  cudaGetLastError();
+  char msg[160];
+  snprintf(msg, sizeof msg, "%s: launch failed: %s", who, cudaGetErrorString(e));
+  set_error_detail(msg);
+  return HOC_ERR_CUDA;
+}
+
+// early: the kernel may start before the one before it on the stream has ended, and waits for that itself.
+template <class... KArgs, class... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, bool early, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = early;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 int sm_count() {
   static std::atomic<int> known[64];
   int dev = 0, sms = 1;
@@ -392,7 +419,8 @@ void realign(MmParams& P, int mode, cudaStream_t s, void** used) {
     for (int p = 0; o.copy && p < P.parts; ++p) bytes += o.bytes(p);
   }
   void* at = nullptr;
-  if (bytes == 0 || scratch(&at, bytes, s) != cudaSuccess) {
+  if (bytes == 0) return;
+  if (scratch(&at, bytes, s) != cudaSuccess) {
     cudaGetLastError();
     return;
   }
@@ -427,16 +455,7 @@ void realign(MmParams& P, int mode, cudaStream_t s, void** used) {
       Q.out_w = o.to_block;
     }
     const int64_t want = (most * (R.to_ld / 8) + 255) / 256, cap = int64_t(sm_count()) * 16;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(want < cap ? want : cap), P.parts);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, realign_kernel, R);
+    e = launch(realign_kernel, dim3(unsigned(want < cap ? want : cap), P.parts), 256, 0, true, s, R);
   }
   if (e == cudaSuccess) {
     P = Q;
@@ -466,12 +485,7 @@ hocResult_t launch_product(const char* who, MmParams P, int mode, cudaStream_t s
       const cudaError_t e = few  ? launch_mm_few(P, s)
                             : tc ? launch_mm_tc(P, mode, s, summed)
                                  : launch_mm_any(P, mode, sms, s);
-      if (e != cudaSuccess) {
-        char msg[160];
-        snprintf(msg, sizeof msg, "%s: launch failed: %s", who, cudaGetErrorString(e));
-        set_error_detail(msg);
-        return HOC_ERR_CUDA;
-      }
+      if (e != cudaSuccess) return launched(who, e);
     }
   return HOC_SUCCESS;
 }
@@ -519,21 +533,10 @@ hocResult_t run_wgrad(const char* who, MmParams& P, void* const* db, cudaStream_
       Q.parts = P.parts - p;
       Q.groups = P.groups;
     }
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((P.out + 63) / 64, Q.parts * Q.groups, kBiasCtas);
-    cfg.blockDim = dim3(32 * kBiasWarps);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, vec ? bias_grad_kernel<true> : bias_grad_kernel<false>, Q) != cudaSuccess) break;
+    const cudaError_t e = launch(vec ? bias_grad_kernel<true> : bias_grad_kernel<false>,
+                                 dim3((P.out + 63) / 64, Q.parts * Q.groups, kBiasCtas), 32 * kBiasWarps, 0, true, s, Q);
+    if (e != cudaSuccess) return launched(who, e);
     at += Q.parts * Q.groups;
-  }
-  if (cudaGetLastError() != cudaSuccess) {
-    set_error_detail("bias gradient: launch failed");
-    return HOC_ERR_CUDA;
   }
   return HOC_SUCCESS;
 }
@@ -609,15 +612,12 @@ extern "C" hocResult_t hoc_ep_segments(int nranks, const int32_t* const* expert_
   cudaError_t e = cudaMemsetAsync(seg, 0, sizeof(int64_t) * per_rank * nranks, s);
   if (e == cudaSuccess && tokens > 0) {
     const int n = tokens * topk;
-    seg_count_kernel<<<dim3((n + kSegItems - 1) / kSegItems, nranks), kSegThreads,
-                       experts <= kSegShared ? sizeof(int) * size_t(experts) : 0, s>>>(
-        P, n, experts, experts / nranks, nranks, reinterpret_cast<unsigned long long*>(seg));
-    seg_scan_kernel<<<nranks, kSegThreads, 0, s>>>(experts, seg);
-    e = cudaGetLastError();
+    e = launch(seg_count_kernel, dim3((n + kSegItems - 1) / kSegItems, nranks), kSegThreads,
+               experts <= kSegShared ? sizeof(int) * size_t(experts) : 0, false, s, P, n, experts, experts / nranks, nranks,
+               reinterpret_cast<unsigned long long*>(seg));
+    if (e == cudaSuccess) e = launch(seg_scan_kernel, dim3(nranks), kSegThreads, 0, false, s, experts, seg);
   }
-  if (e == cudaSuccess) return HOC_SUCCESS;
-  set_error_detail("hoc_ep_segments: launch failed");
-  return HOC_ERR_CUDA;
+  return launched(who, e);
 }
 
 extern "C" hocResult_t hoc_expert_mm(const hocRowGroups_t* groups, const void* const* x, const void* const* weight,
@@ -770,8 +770,6 @@ extern "C" hocResult_t hoc_act_grad(int rows, int width, int act, const void* dy
   const int64_t each = kActThreads * (act == HOC_ACT_SWIGLU ? kGatedVecs : kPlainVecs), want = (n + each - 1) / each;
   const int grid = int(want < 1 << 20 ? want : 1 << 20);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  kActGrad[vec][act - HOC_ACT_RELU]<<<grid, kActThreads, 0, s>>>(d[0], z[0], o[0], rows, width);
-  if (cudaGetLastError() == cudaSuccess) return HOC_SUCCESS;
-  set_error_detail("hoc_act_grad: launch failed");
-  return HOC_ERR_CUDA;
+  return launched(who, launch(kActGrad[vec][act - HOC_ACT_RELU], dim3(grid), kActThreads, 0, false, s, d[0], z[0], o[0],
+                              int64_t(rows), width));
 }

@@ -238,8 +238,12 @@ cudaError_t launch_mm_any(const MmParams& P, int mode, int sms, cudaStream_t s) 
     for (int p = P.part0; p < P.part0 + P.parts; ++p) c += P.cap[p] / kAnyTile + P.groups;
   const int64_t tiles = c * ((f + kAnyTile - 1) / kAnyTile), cap = int64_t(sms) * 4;
   const int grid = int(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
-  kAny[mode]<<<grid, kAnyThreads, sizeof(int) * (2 * size_t(n) + 1), s>>>(P);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kAnyThreads);
+  cfg.dynamicSmemBytes = sizeof(int) * (2 * size_t(n) + 1);
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, kAny[mode], P);
 }
 
 cudaError_t mm_any_preload() {

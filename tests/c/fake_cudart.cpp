@@ -1,17 +1,21 @@
 // A CUDA runtime of two devices without a GPU, for host code that is linked against it instead of the real one: it
 // keeps what the runtime's documentation leaves open open.  A copy from pageable host memory reaches the "device" (the
-// heap) only when its stream is waited for; the launches are counted.
+// heap) only when its stream is waited for; the launches are counted, and may be made to fail; an error stays the last
+// one until it is read.
 #include "fake_cudart.h"
 
 #include <cstdlib>
 #include <cstring>
 #include <vector>
 
+#include <cuda.h>
 #include <cuda_runtime_api.h>
 
 namespace fake {
-int device = 0, launches = 0;
-static cudaError_t last = cudaSuccess;
+int device = 0, launches = 0, last = 0;
+bool refuse = false;
+static cudaError_t now(cudaError_t e) { return e == cudaSuccess ? e : cudaError_t(last = e); }
+static cudaError_t launch() { return refuse ? now(cudaErrorInvalidConfiguration) : (++launches, cudaSuccess); }
 struct Copy {
   void* to;
   std::vector<char> bytes;
@@ -29,7 +33,7 @@ extern "C" {
 cudaError_t cudaGetDeviceCount(int* n) { return *n = 2, cudaSuccess; }
 cudaError_t cudaGetDevice(int* d) { return *d = fake::device, cudaSuccess; }
 cudaError_t cudaGetLastError() {
-  const cudaError_t e = fake::last;
+  const cudaError_t e = cudaError_t(fake::last);
   fake::last = cudaSuccess;
   return e;
 }
@@ -45,8 +49,26 @@ cudaError_t cudaMemcpy(void* to, const void* from, size_t n, cudaMemcpyKind) {
   return cudaSuccess;
 }
 cudaError_t cudaStreamSynchronize(cudaStream_t) { return fake::arrive(); }
-cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t*, const void*, void**) { return ++fake::launches, cudaSuccess; }
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t*, const void*, void**) { return fake::launch(); }
 cudaError_t cudaFuncGetAttributes(cudaFuncAttributes*, const void*) { return cudaSuccess; }
+cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { return cudaSuccess; }
+cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunchConfig_t*) { return *n = 8, cudaSuccess; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) { return *v = 16, cudaSuccess; }
+const char* cudaGetErrorString(cudaError_t) { return "an error"; }
+cudaError_t cudaMemsetAsync(void* p, int v, size_t n, cudaStream_t) { return memset(p, v, n), cudaSuccess; }
+cudaError_t cudaMemPoolCreate(cudaMemPool_t* pool, const cudaMemPoolProps*) {
+  static int one;
+  return *pool = reinterpret_cast<cudaMemPool_t>(&one), cudaSuccess;
+}
+cudaError_t cudaMemPoolSetAttribute(cudaMemPool_t, cudaMemPoolAttr, void*) { return cudaSuccess; }
+cudaError_t cudaMallocFromPoolAsync(void** p, size_t n, cudaMemPool_t, cudaStream_t) { return cudaMalloc(p, n); }
+cudaError_t cudaFreeAsync(void* p, cudaStream_t) { return free(p), cudaSuccess; }
+static CUresult encode(...) { return CUDA_SUCCESS; }
+cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** fn, unsigned, unsigned long long,
+                                             cudaDriverEntryPointQueryResult* r) {
+  *fn = reinterpret_cast<void*>(&encode);
+  return *r = cudaDriverEntryPointSuccess, cudaSuccess;
+}
 
 // What the compiler's host code for kernels refers to.
 static void* nothing[8];
@@ -55,6 +77,7 @@ void __cudaRegisterFatBinaryEnd(void**) {}
 void __cudaUnregisterFatBinary(void**) {}
 void __cudaRegisterFunction(void**, const char*, char*, const char*, int, uint3*, uint3*, dim3*, dim3*, int*) {}
 cudaError_t __cudaGetKernel(cudaKernel_t*, const void*) { return cudaSuccess; }
-cudaError_t __cudaLaunchKernel(cudaKernel_t, dim3, dim3, void**, size_t, cudaStream_t) { return ++fake::launches, cudaSuccess; }
+cudaError_t __cudaLaunchKernel(cudaKernel_t, dim3, dim3, void**, size_t, cudaStream_t) { return fake::launch(); }
+unsigned __cudaPushCallConfiguration(dim3, dim3, size_t, CUstream_st*) { return 0; }
 cudaError_t __cudaPopCallConfiguration(dim3*, dim3*, size_t*, void*) { return cudaSuccess; }
 }

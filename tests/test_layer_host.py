@@ -109,3 +109,24 @@ def test_the_binding_names_what_is_wrong():
         hoc.expert_mm_dgrad([y], [w.view(1, 32, 64)], seg[:, :2], [x], status=st, act="gelu")
     with pytest.raises(TypeError, match="one dtype"):
         hoc.TensorList([x, x.float()])
+
+
+def test_only_errors_of_the_call_itself_are_reported(tmp_path):
+    """The library's own objects over a fake CUDA runtime (tests/c/fake_cudart.cpp): an error that an earlier call left
+    is neither reported nor cleared, a failed launch is reported and leaves none."""
+    import os
+    import subprocess
+
+    from collective_communication_schedules_gb300 import build
+
+    objs = [os.path.join(build.BUILD, n + ".o") for n in ("layer", "mm_any", "mm_few", "mm_tc")]
+    if not all(os.path.exists(o) for o in objs):
+        pytest.skip("the library was not built here")
+    here = os.path.join(os.path.dirname(os.path.abspath(__file__)), "c")
+    out = str(tmp_path / "launches")
+    cmd = [build.nvcc()] + build.ARCH + ["-O1", "-std=c++17", "-cudart", "none", "-I", build.INCLUDE, "-I", here,
+                                         os.path.join(here, "launches.cpp"), os.path.join(here, "fake_cudart.cpp")]
+    r = subprocess.run(cmd + objs + ["-o", out], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([out], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "LAUNCHES OK" in r.stdout, r.stdout + r.stderr
