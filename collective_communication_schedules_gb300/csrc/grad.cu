@@ -213,6 +213,16 @@ cudaError_t launch(void (*kernel)(KArgs...), int grid, cudaStream_t s, Args... a
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// What a launch returned; a failed launch's error is not left for the next call to read.
+hocResult_t launched(const char* who, cudaError_t e) {
+  if (e == cudaSuccess) return HOC_SUCCESS;
+  cudaGetLastError();
+  char msg[160];
+  snprintf(msg, sizeof msg, "%s: launch failed: %s", who, cudaGetErrorString(e));
+  set_error_detail(msg);
+  return HOC_ERR_CUDA;
+}
+
 int grid_of(const hocTensorList* l) {
   return int(l->ntiles < 1 ? 1 : l->ntiles < size_t(kGradCtas) ? l->ntiles : size_t(kGradCtas));
 }
@@ -235,11 +245,8 @@ hocResult_t squares(const char* who, const hocTensorList_t* src, const float* no
   double* partial = reinterpret_cast<double*>(const_cast<int32_t*>(workspace));
   const Tile* tiles = src->tiles;
   const uint64_t n = src->ntiles;
-  const cudaError_t e = src->dtype == HOC_FLOAT32 ? launch(grad_square_kernel<float>, grid_of(src), s, tiles, n, partial)
-                                                  : launch(grad_square_kernel<__nv_bfloat16>, grid_of(src), s, tiles, n, partial);
-  if (e == cudaSuccess) return HOC_SUCCESS;
-  set_error_detail("gradient norm: launch failed");
-  return HOC_ERR_CUDA;
+  const auto kernel = src->dtype == HOC_FLOAT32 ? grad_square_kernel<float> : grad_square_kernel<__nv_bfloat16>;
+  return launched(who, launch(kernel, grid_of(src), s, tiles, n, partial));
 }
 
 }  // namespace
@@ -342,10 +349,8 @@ extern "C" hocResult_t hoc_grad_norm(const hocTensorList_t* src, float* norm, in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const hocResult_t r = squares("hoc_grad_norm", src, norm, workspace, workspace_ints, s);
   if (r != HOC_SUCCESS) return r;
-  if (launch(grad_norm_kernel, 1, s, reinterpret_cast<const double*>(workspace), grid_of(src), norm) == cudaSuccess)
-    return HOC_SUCCESS;
-  set_error_detail("hoc_grad_norm: launch failed");
-  return HOC_ERR_CUDA;
+  return launched("hoc_grad_norm",
+                  launch(grad_norm_kernel, 1, s, reinterpret_cast<const double*>(workspace), grid_of(src), norm));
 }
 
 extern "C" hocResult_t hoc_grad_clip(const hocTensorList_t* src, const hocTensorList_t* dst, const float* max_norm,
@@ -366,10 +371,7 @@ extern "C" hocResult_t hoc_grad_clip(const hocTensorList_t* src, const hocTensor
   cudaError_t e = few ? cudaSuccess : launch(grad_norm_kernel, 1, s, partial, sums, norm);
   if (!few) partial = nullptr;
   const int g = few ? sums : int(n < (1u << 30) ? n : (1u << 30));
-  if (e == cudaSuccess)
-    e = src->dtype == HOC_FLOAT32 ? launch(grad_scale_kernel<float>, g, s, a, b, n, partial, sums, *max_norm, norm, same)
-                                  : launch(grad_scale_kernel<__nv_bfloat16>, g, s, a, b, n, partial, sums, *max_norm, norm, same);
-  if (e == cudaSuccess) return HOC_SUCCESS;
-  set_error_detail("hoc_grad_clip: launch failed");
-  return HOC_ERR_CUDA;
+  const auto kernel = src->dtype == HOC_FLOAT32 ? grad_scale_kernel<float> : grad_scale_kernel<__nv_bfloat16>;
+  if (e == cudaSuccess) e = launch(kernel, g, s, a, b, n, partial, sums, *max_norm, norm, same);
+  return launched(who, e);
 }

@@ -49,6 +49,10 @@ int main() {
     fake::device = 1;
     CHECK(hoc_grad_norm(there, &norm, workspace, 8, nullptr) == HOC_SUCCESS);
     fake::device = 0;
+    fake::refuse = true;  // a failed launch is reported, and leaves no error for the next call
+    CHECK(hoc_grad_norm(here, &norm, workspace, 8, nullptr) == HOC_ERR_CUDA && fake::last == 0);
+    CHECK(hoc_grad_clip(here, here, &one, &norm, workspace, 8, nullptr) == HOC_ERR_CUDA && fake::last == 0);
+    fake::refuse = false;
     CHECK(hoc_tensor_list_destroy(there) == HOC_SUCCESS && hoc_tensor_list_destroy(here) == HOC_SUCCESS);
   }
   printf("LISTS OK\n");
