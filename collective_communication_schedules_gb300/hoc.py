@@ -148,6 +148,7 @@ _SIGS["hoc_linear_dgrad"] = (C.c_int, [C.c_int, C.c_void_p, C.c_size_t, C.c_void
 _SIGS["hoc_linear_wgrad"] = (C.c_int, [C.c_int, C.c_void_p, C.c_size_t, C.c_void_p, C.c_size_t, C.c_int, C.c_int,
                                        C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p])
 _SIGS["hoc_act_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p])
+_SIGS["hoc_layer_trim"] = (C.c_int, [C.c_size_t])
 _SIGS["hoc_tensor_list_create"] = (C.c_int, [C.POINTER(C.c_void_p), C.c_int, C.POINTER(C.c_void_p),
                                              C.POINTER(C.c_size_t), C.c_int])
 _SIGS["hoc_tensor_list_destroy"] = (C.c_int, [C.c_void_p])
@@ -861,6 +862,14 @@ def act_grad(dy, pre, dz, act: str, stream=None):
     _check(lib().hoc_act_grad(rows, width, _act(act), _shaped(dy, (rows, width), "dy"),
                               _shaped(pre, (rows, wide), "pre"), _shaped(dz, (rows, wide), "dz"), _stream(stream)),
            "hoc_act_grad")
+
+
+def layer_trim(keep: int = 0):
+    """Gives scratch that products on rows of odd widths left behind back to the device, all but `keep` bytes (see
+    include/hoc_layer.h); wait for their streams first."""
+    if keep < 0:
+        raise ValueError("keep must not be negative")
+    _check(lib().hoc_layer_trim(int(keep)), "hoc_layer_trim")
 
 
 # ------------------------------------------------------------- gradient clipping

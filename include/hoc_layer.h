@@ -21,7 +21,8 @@
  *     no memory beside the arguments'.  For other rows, products above a small
  *     size copy the operands into scratch that the call allocates and frees in
  *     stream order from a memory pool of this library's own, which keeps what it
- *     was given; where no scratch is to be had a slower kernel runs.
+ *     was given until hoc_layer_trim; where no scratch is to be had a slower
+ *     kernel runs.
  *   - Inputs must not overlap outputs, except as stated.
  */
 #ifndef HOC_LAYER_H
@@ -121,6 +122,11 @@ hocResult_t hoc_linear_wgrad(int rows, const void* dy, size_t lddy, const void* 
  * pre and dz [rows, width or 2 width].  dz may be pre itself, or dy itself
  * (not with SWIGLU). */
 hocResult_t hoc_act_grad(int rows, int width, int act, const void* dy, const void* pre, void* dz, void* stream);
+
+/* Gives scratch of the current device that no call uses any more back to the
+ * device, all but `keep` bytes of it.  Calls still under way on a stream keep
+ * theirs: wait for the stream first.  Nothing is given back without this call. */
+hocResult_t hoc_layer_trim(size_t keep);
 
 #ifdef __cplusplus
 }

@@ -676,3 +676,29 @@ def test_a_long_contraction_is_not_a_stall(sources, monkeypatch):
     want = sum(dy[i: i + (1 << 19)].double().t() @ x[i: i + (1 << 19)].double() for i in range(0, rows, 1 << 19))
     assert torch.equal(dw[0].double(), want)
     assert torch.equal(db[0].double(), dy.sum(0, dtype=torch.float64))
+
+
+def test_scratch_is_given_back():
+    """What realigned copies took stays with the library until it is asked for, and later calls are right again."""
+    rows, inp, out = 200_000, 1023, 255
+    x, w, st = normal(rows, inp, seed=1), normal(out, inp, seed=2, sigma=inp ** -0.5), status()
+    y, again = torch.empty(rows, out, dtype=BF, device=DEV), torch.empty(rows, out, dtype=BF, device=DEV)
+    mib = 1 << 20
+
+    def taken(since):
+        torch.cuda.synchronize()
+        return since - torch.cuda.mem_get_info()[0]
+
+    hoc.layer_trim()  # other tests' scratch
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    hoc.linear(x, w, y, status=st)
+    assert taken(before) > rows * 1024 * 2 - 64 * mib  # the copy of x is 391 MiB, taken in units of some MiB
+    hoc.layer_trim(128 * mib)
+    assert taken(before) < 192 * mib
+    hoc.linear(x, w, again, status=st)
+    hoc.layer_trim()
+    torch.cuda.synchronize()
+    hoc.layer_trim()
+    assert taken(before) < 64 * mib
+    assert torch.equal(y, again) and st.item() == 0

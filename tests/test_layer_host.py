@@ -130,3 +130,10 @@ def test_only_errors_of_the_call_itself_are_reported(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([out], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and "LAUNCHES OK" in r.stdout, r.stdout + r.stderr
+
+
+def test_trimming_without_scratch():
+    with pytest.raises(ValueError, match="keep"):
+        hoc.layer_trim(-1)
+    if not torch.cuda.is_available():
+        assert hoc.lib().hoc_layer_trim(0) == hoc.ERR_NO_DEVICE
