@@ -267,10 +267,14 @@ __global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ Re
 // ------------------------------------------------------------ host
 constexpr int kMaxWidth = 1 << 20;
 constexpr size_t kMaxRows = size_t(1) << 30;
-// Multiplications from which realigned copies pay: a forward product of 1 x 257 x
-// 255 takes 12 us with them and 16 us without, 256 x 257 x 255 22 and 23 us, 4 x 501
-// x 499 14 and 25 us; the weight gradient 18 and 12 us at 64 x 257 x 255, 20 and 25
-// us at 256 x 257 x 255 (4096 x 2047 x 2047: 70 and 520 us, 65 and 950 us).
+// When realigned copies pay: where the contraction is long, which the general kernel's few
+// CTAs walk alone (us here, with copies and without, from a flushed cache: forward 1 x 129 x
+// 127 13 and 13, 1 x 257 x 255 13 and 17; data gradient 15 and 15, 15 and 21; weight gradient
+// over 64 rows of 257 x 255 18 and 13, over 192 rows 19 and 21, over 2000 rows of 65 x 67 19
+// and 142, over 16,000 of 33 x 31 36 and 1070); and in large products whatever its length
+// (multiplications; forward 4 x 501 x 499 14 and 25, 4096 x 2047 x 2047 70 and 520; weight
+// gradient of the latter 65 and 950).  Small ones gain nothing (1 x 65 x 63 13 and 11).
+constexpr int64_t kRealignLong = 160;
 constexpr double kRealignLeast[3] = {1 << 16, 1 << 16, 1 << 24};
 
 hocResult_t refuse(const char* who, const char* what) {
@@ -390,9 +394,13 @@ cudaError_t scratch(void** at, size_t bytes, cudaStream_t s) {
 // and the general kernel takes it.
 void realign(MmParams& P, int mode, cudaStream_t s, void** used) {
   const bool gated = mode == kForward && P.act == HOC_ACT_SWIGLU;
-  int64_t rows = 0;
-  for (int p = 0; p < P.parts; ++p) rows += P.cap[p];
-  if (double(rows) * P.in * P.out * (gated ? 2 : 1) < kRealignLeast[mode]) return;
+  int64_t rows = 0, length = mode == kForward ? P.in : mode == kDgrad ? P.out : 0;
+  for (int p = 0; p < P.parts; ++p) {
+    rows += P.cap[p];
+    // rows of an expert, on average: the ranges are not known here
+    if (mode == kWgrad && P.cap[p] / P.experts > length) length = P.cap[p] / P.experts;
+  }
+  if (rows == 0 || (length < kRealignLong && double(rows) * P.in * P.out * (gated ? 2 : 1) < kRealignLeast[mode])) return;
   struct Operand {  // the rows, then dy (wgrad) or the weights
     const __nv_bfloat16* from[kMaxRanks];
     int64_t rows[kMaxRanks];

@@ -137,3 +137,23 @@ def test_trimming_without_scratch():
         hoc.layer_trim(-1)
     if not torch.cuda.is_available():
         assert hoc.lib().hoc_layer_trim(0) == hoc.ERR_NO_DEVICE
+
+
+def test_the_products_that_run_on_realigned_copies(tmp_path):
+    """The rule's two sides (sizes in tests/c/realign.cpp), by the launches of a call over the fake CUDA runtime."""
+    import os
+    import subprocess
+
+    from collective_communication_schedules_gb300 import build
+
+    objs = [os.path.join(build.BUILD, n + ".o") for n in ("layer", "mm_any", "mm_few", "mm_tc")]
+    if not all(os.path.exists(o) for o in objs):
+        pytest.skip("the library was not built here")
+    here = os.path.join(os.path.dirname(os.path.abspath(__file__)), "c")
+    out = str(tmp_path / "realign")
+    cmd = [build.nvcc()] + build.ARCH + ["-O1", "-std=c++17", "-cudart", "none", "-I", build.INCLUDE, "-I", here,
+                                         os.path.join(here, "realign.cpp"), os.path.join(here, "fake_cudart.cpp")]
+    r = subprocess.run(cmd + objs + ["-o", out], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([out], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "REALIGN OK" in r.stdout, r.stdout + r.stderr
