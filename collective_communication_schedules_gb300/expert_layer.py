@@ -24,8 +24,9 @@ from . import hoc
 class ExpertLayer:
     """Buffers of k ranks x `tokens` tokens of `hidden`, top-`topk` of `experts` experts of width `ffn`.
 
-    capacity: rows of each rank's receive buffer (default: every pair could go to any rank).  A pair whose row does
-    not fit is dropped, and status bit 0 says so."""
+    capacity: rows of each rank's receive buffer.  The default, k * tokens * topk, has room for every pair at any
+    rank; k * tokens * min(topk, experts / k) is enough where a token's experts are distinct.  A pair whose row does not fit is
+    dropped, and status bit 0 says so."""
 
     def __init__(self, k: int, tokens: int, topk: int, hidden: int, ffn: int, experts: int, capacity: int | None = None,
                  device: int = 0):
@@ -33,7 +34,7 @@ class ExpertLayer:
             raise ValueError("experts must be a multiple of the rank count")
         self.k, self.tokens, self.topk, self.hidden, self.ffn, self.experts = k, tokens, topk, hidden, ffn, experts
         self.per_rank = experts // k
-        self.rows = k * tokens * min(topk, self.per_rank) if capacity is None else int(capacity)
+        self.rows = k * tokens * topk if capacity is None else int(capacity)
         dev = torch.device("cuda", device)
 
         def ranks(*shape, dtype=torch.bfloat16):

@@ -130,3 +130,26 @@ def test_a_receive_buffer_that_is_too_small():
     assert layer.status.item() & 4 == 0
     for t in y + dx + dgate + dup + ddown:
         assert bool(torch.isfinite(t).all())
+
+
+@pytest.mark.parametrize("k,tokens,topk,experts,names", [(2, 40, 2, 2, "one"), (4, 30, 3, 4, "any"), (2, 25, 4, 4, "one")])
+def test_tokens_that_name_an_expert_twice(k, tokens, topk, experts, names):
+    """Nothing forbids it: every pair is a row of its own, and by default there is room for all of them at any rank."""
+    hidden, ffn = 64, 32
+    p = problem(k, tokens, topk, hidden, ffn, experts, 5)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    p["ids"] = [torch.ones(tokens * topk, dtype=torch.int32, device=DEV) if names == "one" else
+                torch.randint(0, experts, (tokens * topk,), generator=g, device=DEV, dtype=torch.int32) for _ in range(k)]
+    layer = ExpertLayer(k, tokens, topk, hidden, ffn, experts)
+    y, dx, dgate = ([torch.empty_like(t) for t in p[n]] for n in ("x", "x", "gate"))
+    dup, ddown = ([torch.empty_like(t) for t in p[n]] for n in ("w_up", "w_down"))
+    layer.forward(p["x"], p["ids"], p["gate"], p["w_up"], p["w_down"], y)
+    layer.backward(p["dy"], p["ids"], p["gate"], p["w_up"], p["w_down"], dx, dgate, dup, ddown)
+    torch.cuda.synchronize()
+    assert layer.status.item() == 0
+    ys, x, gate, up, down = in_64_bits(p, experts)
+    near(y, ys, 4, "y")
+    near(dx, [t.grad for t in x], 6, "dx")
+    near(dgate, [t.grad for t in gate], 4, "dgate")
+    near(dup, [t.grad for t in up], 7, "dw_up")  # (weight gradients are rounded to bf16 here: one more than above)
+    near(ddown, [t.grad for t in down], 6, "dw_down")
