@@ -153,3 +153,43 @@ def test_tokens_that_name_an_expert_twice(k, tokens, topk, experts, names):
     near(dgate, [t.grad for t in gate], 4, "dgate")
     near(dup, [t.grad for t in up], 7, "dw_up")  # (weight gradients are rounded to bf16 here: one more than above)
     near(ddown, [t.grad for t in down], 6, "dw_down")
+
+
+def each_near(got, want, bound, what):
+    """Every row of `got` (every expert's matrix) is near `want`'s, by that row's own norm; rows of zeros are exact."""
+    for s, (a, b) in enumerate(zip(got, want)):
+        a, b = a.double().flatten(1), b.detach().double().flatten(1)
+        off, size = (a - b).norm(dim=1), b.norm(dim=1)
+        bad = off > bound * size
+        assert not bool(bad.any()), f"{what}: row {int(bad.nonzero()[0])} of rank {s} is off by {float((off / size)[bad].max()):.3g}"
+
+
+@pytest.mark.parametrize("k,tokens,topk,hidden,ffn,experts", [
+    (1, 5, 1, 64, 32, 2), (2, 100, 2, 128, 64, 8), (4, 77, 3, 264, 176, 16), (8, 33, 6, 72, 48, 64), (2, 40, 2, 50, 30, 4),
+])
+def test_every_token_and_every_expert(k, tokens, topk, hidden, ffn, experts):
+    """The bounds of the whole arrays hold row by row too, twice as wide where a row is one token (50 to 264 values; an
+    expert's matrix has thousands), so that one missing pair or one row from a neighbour's range is seen: a pair is at
+    least 1 / sqrt(topk) of its token on average.  dgate is <o, dy>: o is off by at most 9 u of its norm (three roundings)
+    in a direction that has nothing to do with dy, which leaves 9 u |o| |dy| / sqrt(hidden) on average; 6 times that."""
+    p = problem(k, tokens, topk, hidden, ffn, experts, seed=20 + k)
+    layer = ExpertLayer(k, tokens, topk, hidden, ffn, experts)
+    y, dx, dgate = ([torch.empty_like(t) for t in p[n]] for n in ("x", "x", "gate"))
+    dup, ddown = ([torch.empty_like(t, dtype=torch.float32) for t in p[n]] for n in ("w_up", "w_down"))
+    layer.forward(p["x"], p["ids"], p["gate"], p["w_up"], p["w_down"], y)
+    layer.backward(p["dy"], p["ids"], p["gate"], p["w_up"], p["w_down"], dx, dgate, dup, ddown)
+    torch.cuda.synchronize()
+    assert layer.status.item() == 0
+    ys, x, gate, up, down = in_64_bits(p, experts)
+    each_near(y, ys, 2 * 3 * 4 * U, "y")
+    each_near(dx, [t.grad for t in x], 2 * 3 * 6 * U, "dx")
+    each_near(dup, [t.grad for t in up], 3 * 6 * U, "dw_up")
+    each_near(ddown, [t.grad for t in down], 3 * 5 * U, "dw_down")
+    w_up, w_down = torch.cat(p["w_up"]).double(), torch.cat(p["w_down"]).double()
+    for s in range(k):
+        e, t = p["ids"][s].long(), torch.arange(tokens * topk, device=DEV) // topk
+        a, b = torch.einsum("nfh,nh->nf", w_up[e], p["x"][s].double()[t]).chunk(2, 1)
+        o = torch.einsum("nhf,nf->nh", w_down[e], a * torch.sigmoid(a) * b)
+        scale = o.norm(dim=1) * p["dy"][s].double()[t].norm(dim=1) / hidden ** 0.5
+        bad = (dgate[s].double() - gate[s].grad).abs() > 6 * 9 * U * scale
+        assert not bool(bad.any()), f"dgate of pair {int(bad.nonzero()[0])} of source {s}"
