@@ -623,7 +623,7 @@ extern "C" hocResult_t hoc_ep_segments(int nranks, const int32_t* const* expert_
   cudaError_t e = cudaMemsetAsync(seg, 0, sizeof(int64_t) * per_rank * nranks, s);
   if (e == cudaSuccess && tokens > 0) {
     const int n = tokens * topk;
-    e = launch(seg_count_kernel, dim3((n + kSegItems - 1) / kSegItems, nranks), kSegThreads,
+    e = launch(seg_count_kernel, dim3(unsigned((int64_t(n) + kSegItems - 1) / kSegItems), nranks), kSegThreads,
                experts <= kSegShared ? sizeof(int) * size_t(experts) : 0, false, s, P, n, experts, experts / nranks, nranks,
                reinterpret_cast<unsigned long long*>(seg));
     if (e == cudaSuccess) e = launch(seg_scan_kernel, dim3(nranks), kSegThreads, 0, false, s, experts, seg);

@@ -13,6 +13,7 @@
 
 namespace fake {
 int device = 0, launches = 0, last = 0;
+unsigned widest = 0;
 bool refuse = false;
 static cudaError_t now(cudaError_t e) { return e == cudaSuccess ? e : cudaError_t(last = e); }
 static cudaError_t launch() { return refuse ? now(cudaErrorInvalidConfiguration) : (++launches, cudaSuccess); }
@@ -49,7 +50,10 @@ cudaError_t cudaMemcpy(void* to, const void* from, size_t n, cudaMemcpyKind) {
   return cudaSuccess;
 }
 cudaError_t cudaStreamSynchronize(cudaStream_t) { return fake::arrive(); }
-cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t*, const void*, void**) { return fake::launch(); }
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* cfg, const void*, void**) {
+  if (cfg->gridDim.x > fake::widest) fake::widest = cfg->gridDim.x;
+  return fake::launch();
+}
 cudaError_t cudaFuncGetAttributes(cudaFuncAttributes*, const void*) { return cudaSuccess; }
 cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { return cudaSuccess; }
 cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunchConfig_t*) { return *n = 8, cudaSuccess; }

@@ -54,6 +54,11 @@ int main() {
     check(c.second() == HOC_ERR_CUDA, c, "a failed launch is not reported");
     check(fake::last == 0, c, "left its own error to be read by the next call");
   }
+  // the most pairs that ep_segments takes, 2048 to a CTA
+  fake::refuse = false;
+  fake::widest = 0;
+  const Call most = {"ep_segments", [&] { return hoc_ep_segments(1, ids, 0x7FFFFFFF, 1, 8, seg, nullptr); }};
+  check(most.second() == HOC_SUCCESS && fake::widest == 1u << 20, most, "a grid that does not fit the pairs");
   printf(bad ? "%d WRONG\n" : "LAUNCHES OK\n", bad);
   return bad != 0;
 }
