@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kActThreads)
           o.v[e] = __float2bfloat16_rn(dd * __bfloat162float(u[j].v[e]) * mm_act_slope(HOC_ACT_SILU, g));
           o2.v[e] = __float2bfloat16_rn(dd * mm_act(HOC_ACT_SILU, g));
         } else {
-          o.v[e] = __float2bfloat16_rn(dd * mm_act_slope(ACT, g));
+          o.v[e] = __float2bfloat16_rn(mm_act_back(ACT, g, dd));
         }
       }
       *reinterpret_cast<Vec*>(dz + at[j]) = o;

@@ -154,10 +154,9 @@ __device__ __forceinline__ float mm_act(int act, float z) {
   }
 }
 
-// d act(z) / dz; the products of a vanishing s (1 - s) with a huge z are cut at |z| = 30, where they are 0.
+// d act(z) / dz (not for ReLU, see mm_act_back); the products of a vanishing s (1 - s) with a huge z are cut at |z| = 30, where they are 0.
 __device__ __forceinline__ float mm_act_slope(int act, float z) {
   switch (act) {
-    case HOC_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case HOC_ACT_GELU: {
       const float s = mm_sigmoid(2.f * kGeluScale * (z + kGeluCubic * z * z * z));
       const float c = fminf(fmaxf(z, -30.f), 30.f);
@@ -170,6 +169,12 @@ __device__ __forceinline__ float mm_act_slope(int act, float z) {
     }
     default: return 1.f;
   }
+}
+
+// The gradient for z where d is that for act(z).  A closed ReLU is a choice and not a product: infinities
+// and NaN do not come through it.
+__device__ __forceinline__ float mm_act_back(int act, float z, float d) {
+  return act == HOC_ACT_RELU ? (z > 0.f ? d : 0.f) : d * mm_act_slope(act, z);
 }
 
 // Host side -----------------------------------------------------------------

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kAnyThreads) mm_any_kernel(const __grid_consta
                 y[f] = __float2bfloat16_rn(v * zu * mm_act_slope(HOC_ACT_SILU, zg));
                 y[P.in + f] = __float2bfloat16_rn(v * mm_act(HOC_ACT_SILU, zg));
               } else {
-                if (P.act != HOC_ACT_NONE) v *= mm_act_slope(P.act, bf16_of(P.pre[p] + row * P.in + f));
+                if (P.act != HOC_ACT_NONE) v = mm_act_back(P.act, bf16_of(P.pre[p] + row * P.in + f), v);
                 y[f] = __float2bfloat16_rn(v);
               }
             }

@@ -970,7 +970,7 @@ __device__ __forceinline__ bool run_slope_epilogue(const TcParams& T, TcShared* 
         put_bf16(z + kTcPlane, d * mm_act(HOC_ACT_SILU, g));
         d *= u * mm_act_slope(HOC_ACT_SILU, g);
       } else {
-        d *= mm_act_slope(ACT, g);
+        d = mm_act_back(ACT, g, d);
       }
       put_bf16(z, d);
     }

@@ -38,7 +38,8 @@ extern "C" {
 #endif
 
 /* Activations.  GELU is the tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)));
- * SILU z / (1 + exp(-z)); SWIGLU silu(gate) * value. */
+ * SILU z / (1 + exp(-z)); SWIGLU silu(gate) * value.  A gradient through RELU is
+ * 0 where its input is not above 0, also where dy is infinite or NaN. */
 typedef enum {
   HOC_ACT_NONE = 0,
   HOC_ACT_RELU = 1,

@@ -702,3 +702,32 @@ def test_scratch_is_given_back():
     hoc.layer_trim()
     assert taken(before) < 64 * mib
     assert torch.equal(y, again) and st.item() == 0
+
+
+def test_a_closed_relu_lets_nothing_through():
+    """Where ReLU's input is not above 0 the gradient is 0 whatever comes from above, infinities and NaN among them;
+    where it is, what comes is passed on."""
+    inf, nan = float("inf"), float("nan")
+    above = torch.tensor([1.0, inf, -inf, nan], device=DEV).to(BF)
+    below = torch.tensor([-1.0, 0.0, -0.0, -inf, 2.0, inf], device=DEV).to(BF)
+    n = len(above)
+    dy = above.view(n, 1).expand(n, len(below)).contiguous()  # row i: above[i]
+    pre = below.view(1, -1).expand(n, len(below)).contiguous()
+    want = torch.where(pre > 0, dy, torch.zeros_like(dy))
+    for width in (len(below), 8 * len(below)):  # value by value, and as vectors
+        d, z = (t.repeat(1, width // len(below)) for t in (dy, pre))
+        dz = torch.full_like(d, 7.0)
+        hoc.act_grad(d, z, dz, "relu")
+        assert torch.equal(dz.nan_to_num(5.0), want.repeat(1, width // len(below)).nan_to_num(5.0))
+    # through a product: every input of the layer below gets above[i]
+    for rows, inp in ((n, 6), (n, 48), (64, 48)):
+        out = 16 if inp > 6 else 5
+        d = torch.zeros(rows, out, device=DEV).to(BF)
+        d[:n, 0] = above
+        w = torch.zeros(out, inp, device=DEV).to(BF)
+        w[0] = 1.0
+        z = below.repeat(inp // len(below)).expand(rows, inp).contiguous()
+        dx, st = torch.full((rows, inp), 7.0, device=DEV).to(BF), status()
+        hoc.linear_dgrad(d, w, dx, status=st, act="relu", pre=z)
+        want = torch.where(z > 0, d[:, :1].expand(rows, inp), torch.zeros_like(z))
+        assert torch.equal(dx.nan_to_num(5.0), want.nan_to_num(5.0)), (rows, inp)
