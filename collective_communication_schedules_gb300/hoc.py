@@ -729,6 +729,8 @@ def _groups(rows, experts: int, seg):
     """The hocRowGroups_t of buffers with `rows[d]` rows each, and what it points to."""
     k = len(rows)
     _typed(seg, "int64", "seg")
+    if not experts:
+        raise ValueError("weights of at least one expert must be given")
     if seg.dim() != 2 or seg.shape[0] != k or seg.shape[1] < experts + 1 or (seg.shape[1] - 1) % experts:
         raise ValueError(f"seg: expected shape [{k}, sources * {experts} + 1], got {tuple(seg.shape)}")
     cap = (C.c_size_t * max(1, k))(*rows)
@@ -754,7 +756,7 @@ def expert_mm(x, weight, seg, y, *, status, bias=None, act: str = "none", pre=No
     include/hoc_layer.h).  Lists of k device tensors: x [capacity, in], weight [experts, out, in] ([experts, 2 * out,
     in] for swiglu), y [capacity, out]; pre keeps the pre-activations for the gradients."""
     a, k = _act(act), len(x)
-    if not k or weight[0].dim() != 3 or x[0].dim() != 2:
+    if not k or not weight or weight[0].dim() != 3 or x[0].dim() != 2:
         raise ValueError("x: a list of matrices, weight: a list of [experts, out, in] tensors")
     mul = 2 if act == "swiglu" else 1
     experts, wide, inp = weight[0].shape
@@ -774,7 +776,7 @@ def expert_mm_dgrad(dy, weight, seg, dx, *, status, act: str = "none", pre=None,
     """dx[d][r] = W[d][e]^T dy[d][r]; with act the layer's input came out of that activation and dx is the gradient
     for what went into it, pre (see include/hoc_layer.h)."""
     a, k = _act(act), len(dy)
-    if not k or weight[0].dim() != 3 or dy[0].dim() != 2:
+    if not k or not weight or weight[0].dim() != 3 or dy[0].dim() != 2:
         raise ValueError("dy: a list of matrices, weight: a list of [experts, out, in] tensors")
     if (act != "none") != (pre is not None):
         raise ValueError("pre is given exactly when there is an activation")
@@ -792,7 +794,7 @@ def expert_mm_wgrad(dy, x, seg, dw, *, status, db=None, accumulate: bool = False
     """dw[d][e] (+)= sum of dy[r]^T x[r] over the rows of expert e of rank d, db[d][e] (+)= sum of dy[r]; dw [experts,
     out, in] and db [experts, out] in bf16 or float32 (see include/hoc_layer.h)."""
     k = len(x)
-    if not k or dw[0].dim() != 3:
+    if not k or not dw or dw[0].dim() != 3:
         raise ValueError("x: a list of matrices, dw: a list of [experts, out, in] tensors")
     experts, out, inp = dw[0].shape
     rows, dt = [t.shape[0] for t in x], "float32" if dw[0].dtype is _dt("float32") else "bfloat16"

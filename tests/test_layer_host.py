@@ -157,3 +157,17 @@ def test_the_products_that_run_on_realigned_copies(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([out], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and "REALIGN OK" in r.stdout, r.stdout + r.stderr
+
+
+def test_lists_and_experts_that_are_missing():
+    """An empty list of weights, and weights of no expert, are refused by name."""
+    x, y = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 32, dtype=torch.bfloat16)
+    st, seg = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 3, dtype=torch.int64)
+    none = torch.zeros(0, 32, 64, dtype=torch.bfloat16)
+    for w, what in (([], "weight|dw"), ([none], "expert")):
+        with pytest.raises(ValueError, match=what):
+            hoc.expert_mm([x], w, seg, [y], status=st)
+        with pytest.raises(ValueError, match=what):
+            hoc.expert_mm_dgrad([y], w, seg, [x], status=st)
+        with pytest.raises(ValueError, match=what):
+            hoc.expert_mm_wgrad([y], [x], seg, w, status=st)
