@@ -50,6 +50,7 @@ class ExpertLayer:
         self.ones = [torch.ones(tokens * topk, device=dev)] * k
         self.ws = torch.empty(max(1, k * hoc.ep_pack_workspace(tokens, topk, experts)), dtype=torch.int32, device=dev)
         self.caps = [self.rows * hidden] * k
+        torch.cuda.current_stream(dev).synchronize()  # status and ones are there for calls on any stream
 
     def forward(self, x, ids, gate, w_up, w_down, y, stream=None):
         """y[s] [tokens, hidden] of every source s; x[s] [tokens, hidden] bf16, ids[s] [tokens * topk] int32,

@@ -193,3 +193,31 @@ def test_every_token_and_every_expert(k, tokens, topk, hidden, ffn, experts):
         scale = o.norm(dim=1) * p["dy"][s].double()[t].norm(dim=1) / hidden ** 0.5
         bad = (dgate[s].double() - gate[s].grad).abs() > 6 * 9 * U * scale
         assert not bool(bad.any()), f"dgate of pair {int(bad.nonzero()[0])} of source {s}"
+
+
+def test_a_layer_is_used_at_once_on_a_stream_of_its_own():
+    """What the constructor fills is there when it returns, whatever the stream that it was made on is doing."""
+    k, tokens, topk, hidden, ffn, experts = 2, 64, 2, 128, 64, 8
+    p = problem(k, tokens, topk, hidden, ffn, experts, 6)
+    new = lambda n: [torch.empty_like(t) for t in p[n]]  # noqa: E731
+    y, dx, dgate, dup, ddown = (new(n) for n in ("x", "x", "gate", "w_up", "w_down"))
+    side = torch.cuda.Stream()
+    before = ExpertLayer(k, tokens, topk, hidden, ffn, experts)  # memory for the second, with something in it
+    before.forward(p["x"], p["ids"], p["gate"], p["w_up"], p["w_down"], y)  # (a kernel's first launch may wait)
+    before.backward(p["dy"], p["ids"], p["gate"], p["w_up"], p["w_down"], dx, dgate, dup, ddown)
+    before.status.fill_(7)
+    before.ones[0].fill_(7.0)
+    del before
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # cycles: about a tenth of a second
+    layer = ExpertLayer(k, tokens, topk, hidden, ffn, experts)
+    layer.forward(p["x"], p["ids"], p["gate"], p["w_up"], p["w_down"], y, stream=side)
+    layer.backward(p["dy"], p["ids"], p["gate"], p["w_up"], p["w_down"], dx, dgate, dup, ddown, stream=side)
+    side.synchronize()
+    got = [t.clone() for t in y + dx + dgate + dup + ddown]
+    torch.cuda.synchronize()
+    assert layer.status.item() == 0
+    layer.forward(p["x"], p["ids"], p["gate"], p["w_up"], p["w_down"], y)
+    layer.backward(p["dy"], p["ids"], p["gate"], p["w_up"], p["w_down"], dx, dgate, dup, ddown)
+    for a, b in zip(got, y + dx + dgate + dup + ddown):
+        assert torch.equal(a, b)
