@@ -41,7 +41,7 @@ struct MmParams {
   const __nv_bfloat16* res[kMaxRanks];
   const __nv_bfloat16* pre[kMaxRanks];  // dgrad: pre-activation of the layer below
   void* y[kMaxRanks];
-  void* pre_out[kMaxRanks];  // forward: pre-activation to keep
+  void* pre_out[kMaxRanks];  // forward: pre-activation to keep; wgrad: the bias gradient
 };
 
 // Device helpers ------------------------------------------------------------
@@ -154,7 +154,8 @@ __device__ __forceinline__ float mm_act(int act, float z) {
   }
 }
 
-// d act(z) / dz (not for ReLU, see mm_act_back); the products of a vanishing s (1 - s) with a huge z are cut at |z| = 30, where they are 0.
+// d act(z) / dz (ReLU's is in mm_act_back); the products of a vanishing s (1 - s) with a
+// huge z are cut where they are 0, at |z| = 30 and 120.
 __device__ __forceinline__ float mm_act_slope(int act, float z) {
   switch (act) {
     case HOC_ACT_GELU: {

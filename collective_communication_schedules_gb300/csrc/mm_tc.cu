@@ -29,19 +29,20 @@
 // Warps of a CTA: 0 and 2 tensor copies of the rows, 64 each; 3 those of the
 // weights; 1 MMA (of the pair's first CTA); 4-11 epilogue.  In the weight gradient
 // warps 0 and 12 issue all copies of every second stage, and warps 2, 3 and 13-15
-// zero padding rows (one range: warp 2, and the others sum the bias gradient).  Every wait is bounded: a wait that runs out sets bit 2 of the
-// status, and all roles leave.
+// zero padding rows (one range: warp 2, and the others sum the bias gradient).  Every
+// wait is bounded: one that runs out sets bit 2 of the status, and all roles leave.
 //
 // Measured, single calls from a flushed cache; the peaks measured on this GPU are 1951
-// TFLOP/s and 6.69 TB/s.  One range of rows: 4096 x 4096 x 4096 forward 83 us (1656
-// TFLOP/s), gradients 80 us (1718); 8192 rows of 4096 -> 8192 forward and data
-// gradient 295 us (1864), weight gradient 308 us (1785); bound by the tensor cores and,
-// in the first, by the waves' ends.  8 ranks x 4096 tokens, top-6 of 64 experts, Zipf
-// (196,608 rows in 512 ranges): 2048 -> 1280 gated with its pre-activation 1205 to 1240 us
-// (1660 to 1710 TFLOP/s), weight gradient of 2048 x 2560 1400 us (1470; the packed remainders of
+// TFLOP/s and 6.69 TB/s.  One range of rows: 4096 x 4096 x 4096 forward 81 us (1706
+// TFLOP/s), gradients 79 us (1750); 8192 rows of 4096 -> 8192 forward and data
+// gradient 287 and 289 us (1913, 1900), weight gradient 318 us (1728); bound by the tensor
+// cores and, in the first, by the waves' ends.  8 ranks x 4096 tokens, top-6 of 64 experts,
+// Zipf (196,608 rows in 512 ranges): 2048 -> 1280 gated with its pre-activation 1208 us (1710
+// TFLOP/s), weight gradient of 2048 x 2560 1426 us (1450; the packed remainders of
 // ranges and stores of 671 MB), and at half the tokens the data gradient 1280 <- 2048
-// through the gate 415 us (1240 TFLOP/s and 4.2 TB/s: 313 of them without the rows that
-// the epilogue reads and writes).  16 tokens instead of 4096: 128 us, 107 in a row (6.1
+// through the gate 411 us (1250 TFLOP/s and 4.2 TB/s: 313 of them without the rows that
+// the epilogue reads and writes).  16 tokens instead of 4096: 129 us.  Calls in a row, in
+// which the large ones run into the power limit: 1390, 1520, 465 and 108 us (the last 6.0
 // TB/s: bound by reading the experts' weights).
 #include <atomic>
 #include <climits>
@@ -611,7 +612,9 @@ __device__ __forceinline__ uint4 get8(const Strip& G, int row) {
   if (row < 0 || G.left <= 0) return v;
   const char* at = G.at + row * G.pitch;
   if (!G.loose) {
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(at));
     return v;
   }
   uint32_t w[4] = {0, 0, 0, 0};
@@ -798,9 +801,9 @@ __device__ __forceinline__ void add_sums(const TcParams& T, uint32_t (&v)[kTcCol
 
 // The epilogue of one tile by group `eg` of four warps (warp q of it has tensor
 // memory lanes 32 q ..): the steps of kTcColumns columns whose number is eg modulo
-// 2 (of this share's).  (MODE kDgrad: with no activation.)  plane: the group's staging, [column][128 features] binary32, in
-// which the 16-byte quads of a warp's 32 features are exchanged by q, so that both
-// sides reach all banks.  False when the accumulator did not come.
+// 2 (of this share's).  (MODE kDgrad: with no activation.)  plane: the group's staging,
+// [column][128 features] binary32, in which the 16-byte quads of a warp's 32 features are
+// exchanged by q, so that both sides reach all banks.  False when the accumulator did not come.
 template <int MODE, int ACT, bool RAGGED>
 __device__ __forceinline__ bool run_epilogue(const TcParams& T, TcShared* S, const Tile& A, uint32_t stages, uint32_t plane,
                                              uint32_t acc_at, uint64_t* acc_full, uint32_t parity, int eg, int q, int rank,
@@ -924,7 +927,8 @@ __device__ __forceinline__ bool run_slope_epilogue(const TcParams& T, TcShared* 
   // clamped so that no pointer is formed past the tensors
   const int left = width - f0, fs = left > 0 ? f0 : 0;
   const Strip y{static_cast<char*>(P.y[A.p]) + 2 * int64_t(fs), 2 * P.ld_y, left, T.loose != 0};
-  const Strip beside{reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.pre[A.p])) + 2 * int64_t(fs), 2 * wide, left, T.loose != 0};
+  const Strip beside{reinterpret_cast<char*>(const_cast<__nv_bfloat16*>(P.pre[A.p])) + 2 * int64_t(fs), 2 * wide, left,
+                     T.loose != 0};
   auto second = [&](Strip s) {
     s.at += 2 * int64_t(width);
     return s;
@@ -1039,7 +1043,8 @@ __device__ __forceinline__ bool run_wgrad_epilogue(const TcParams& T, TcShared* 
     group_barrier(eg);
     // 128 threads: 8 rows of 16 vectors at a time
     const int c = i / 16, u = i % 16;
-    char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(P.y[A.p]) + at) + (int64_t(c) * P.in + (left > 0 ? f0 : 0)) * 2 + u * 16;
+    char* to = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(P.y[A.p]) + at) +
+               (int64_t(c) * P.in + (left > 0 ? f0 : 0)) * 2 + u * 16;
 #pragma unroll
     for (int h = 0; h < kWgColumns / 8; ++h) {
       const unsigned char* from = o + (i + 128 * h) * 16;
@@ -1529,8 +1534,8 @@ int choose_rows_ragged(const MmParams& P) {
 
 // The launch but for its grid and stream, and the clusters that fit the device at
 // once (asked once for each kernel, cluster size and device).
-cudaError_t configure(const void* fn, int mode, bool ragged, int log_shares, cudaLaunchAttribute (&attr)[2], cudaLaunchConfig_t& cfg,
-                      int& clusters) {
+cudaError_t configure(const void* fn, int mode, bool ragged, int log_shares, cudaLaunchAttribute (&attr)[2],
+                      cudaLaunchConfig_t& cfg, int& clusters) {
   static std::atomic<int> known[3][kTcMostShares + 2][64];  // ragged ones last
   const int kind = ragged ? kTcMostShares + 1 : log_shares;
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -25,8 +25,8 @@ class ExpertLayer:
     """Buffers of k ranks x `tokens` tokens of `hidden`, top-`topk` of `experts` experts of width `ffn`.
 
     capacity: rows of each rank's receive buffer.  The default, k * tokens * topk, has room for every pair at any
-    rank; k * tokens * min(topk, experts / k) is enough where a token's experts are distinct.  A pair whose row does not fit is
-    dropped, and status bit 0 says so."""
+    rank; k * tokens * min(topk, experts / k) is enough where a token's experts are distinct.  A pair whose row does
+    not fit is dropped, and status bit 0 says so."""
 
     def __init__(self, k: int, tokens: int, topk: int, hidden: int, ffn: int, experts: int, capacity: int | None = None,
                  device: int = 0):

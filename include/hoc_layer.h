@@ -2,8 +2,8 @@
  * hoc_layer.h -- the matrix products that run between the collectives: the
  * products of an expert layer on the rows an expert-parallel dispatch
  * delivered (HOCCL section 2.1: EP token dispatch and combine surround them),
- * grouped by expert with ragged row counts that only the device knows, and the
- * dense linear layer of a pipeline stage.  Both have their epilogue fused
+ * grouped by expert with ragged row counts that only the device knows, and a
+ * dense linear layer on the same kernels.  Both have their epilogue fused
  * (bias, activation, residual) and both have their gradients.
  *
  * Conventions, beside those of hoc.h:
@@ -13,7 +13,8 @@
  *     HOC_ACT_SWIGLU its `out` rows of gates come first and the `out` rows of
  *     linear values after them: [experts, 2 * out, in].
  *   - `status` is a device int32; bit 2 (value 4) is set, never cleared, if a
- *     bounded wait inside a kernel gave up (the results are then undefined).
+ *     wait inside a kernel gave up after 2 s in which nothing moved (the results are
+ *     then undefined).
  *   - Everything is stream-ordered, never waits on the host and may be captured
  *     into a CUDA graph after one call of the same kind.
  *   - Rows of x, dy and the weights that start on 16-byte boundaries (widths and
