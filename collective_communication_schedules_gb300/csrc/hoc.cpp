@@ -562,6 +562,7 @@ hocResult_t read_cfg(const hocConfig_t* in, int k, Cfg* out) {
     else if (!strcmp(v, "proxy_block")) c.fault = kFaultProxyBlock;
     else if (!strcmp(v, "proxy_memop")) c.fault = kFaultProxyMemop;
     else if (!strcmp(v, "proxy_memop_reset")) c.fault = kFaultProxyMemopReset;
+    else if (!strcmp(v, "proxy_memop_late")) c.fault = kFaultProxyMemopLate;
   }
   if (c.order.empty())
     for (int i = 0; i < k; ++i) c.order.push_back(i);

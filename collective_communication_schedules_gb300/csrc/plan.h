@@ -117,7 +117,8 @@ enum Fault {
   kFaultTmaStall = 5,   // the TMA kernel's mbarriers expect bytes that never arrive
   kFaultProxyBlock = 6,  // the proxy thread is held up past a task's deadline (host sleep)
   kFaultProxyMemop = 7,  // the first device-count call: its wait for FINISH fails to queue
-  kFaultProxyMemopReset = 8  // the first device-count call: its reset of end_flag fails to queue
+  kFaultProxyMemopReset = 8,  // the first device-count call: its reset of end_flag fails to queue
+  kFaultProxyMemopLate = 9    // the same, 20 ms after the operations before it were queued
 };
 
 enum StepKind { kStepReduce = 0, kStepFused = 1, kStepCopy = 2, kStepTma = 3 };

@@ -19,10 +19,12 @@
 // reused once the stream has reset end_flag.
 //
 // Slot states: Free -> Queued (handed to the proxy; the stream has not reached
-// the start flag) -> Starting (start flag seen; planning and issuing) ->
-// Running (moves issued) -> Releasing (FINISH written) -> Free (the stream
-// reset end_flag).  Every transition happens under Proxy::mu; the release
-// writes happen under it too, so exactly one thread releases a task.
+// the start flag) -> Starting (start flag seen) -> Acked (acknowledged; nothing
+// is moved before the call has queued all its stream operations, which the
+// stream may be ahead of) -> Moving (planning and issuing) -> Running (moves
+// issued) -> Releasing (FINISH written) -> Free (the stream reset end_flag).
+// Every transition happens under Proxy::mu; the release writes happen under it
+// too, so exactly one thread releases a task.
 // If queueing the four stream operations fails part way, the call returns
 // HOC_ERR_CUDA and the slot is abandoned: once the stream writes the start
 // flag the proxy acknowledges it and, without moving anything, frees the
@@ -59,6 +61,7 @@ constexpr size_t kFlagBytes = 64;
 constexpr auto kTaskDeadline = std::chrono::seconds(10);
 constexpr auto kInjectedDeadline = std::chrono::milliseconds(200);
 constexpr auto kInjectedBlock = std::chrono::milliseconds(1500);
+constexpr auto kInjectedLate = std::chrono::milliseconds(20);
 constexpr auto kShutdownWait = std::chrono::seconds(60);
 // The proxy issues a task's copies only once the stream is at the start flag,
 // so the exchange is bound by whichever is longer: issuing the copies (about
@@ -69,7 +72,7 @@ constexpr auto kShutdownWait = std::chrono::seconds(60);
 constexpr size_t kProxyTaskCopies = 48;
 constexpr size_t kChunkGrain = size_t(1) << 20;
 
-enum SlotState { kFree = 0, kQueued = 1, kStarting = 2, kRunning = 3, kReleasing = 4, kRetired = 5 };
+enum SlotState { kFree, kQueued, kStarting, kAcked, kMoving, kRunning, kReleasing, kRetired };
 constexpr int kStreamOps = 4;  // write start, wait ack, wait finish, reset end
 
 const char* const kWhyDeadline =
@@ -89,7 +92,10 @@ struct Slot {
   int dtype = 0;
   std::vector<size_t> cap;   // receive capacities, elements
   std::vector<size_t> scap;  // send capacities, elements
+  bool queueing = false;     // the call has not queued all its stream operations yet
   int abandoned_ops = 0;     // > 0: queueing failed after this many stream operations
+  // A task that the proxy holds and the watchdog may have to release.
+  bool held() const { return state == kStarting || state == kAcked || state == kMoving || state == kRunning; }
   int transpose = 0;
   cudaEvent_t done = nullptr;
   bool stalled = false;  // host-injected: the moves are never reported complete
@@ -137,7 +143,7 @@ void trace(Proxy* P, const Slot& s, const char* what) {
 // Write the release (ack and FINISH) of a task the proxy still holds.  The
 // caller holds P->mu.  Returns false if the task was already released.
 bool release_locked(Proxy* P, Slot& s, int err, const char* why) {
-  if (s.state != kStarting && s.state != kRunning) return false;
+  if (!s.held()) return false;
   std::atomic_thread_fence(std::memory_order_seq_cst);
   *s.start = 0;  // no-op once acknowledged; frees a stream still at the start flag
   *s.end = kFinishValue;
@@ -160,7 +166,7 @@ void release(Proxy* P, Slot& s, int err, const char* why) {
   release_locked(P, s, err, why);
 }
 
-// The stream reached the start flag: acknowledge, plan and issue the moves.
+// The stream reached the start flag: acknowledge.
 void start_task(Proxy* P, Slot& s) {
   bool block = false;
   {
@@ -173,20 +179,49 @@ void start_task(Proxy* P, Slot& s) {
     s.deadline = Clock::now() + (injected ? Clock::duration(kInjectedDeadline) : Clock::duration(kTaskDeadline));
   }
   trace(P, s, "start flag seen");
+  // Injected on the host: the proxy thread is held up past the deadline, as in
+  // a driver call that waits for the held stream; the watchdog must release.
+  if (block) std::this_thread::sleep_for(kInjectedBlock);
+  std::lock_guard<std::mutex> lock(P->mu);
+  if (s.state != kStarting) return;  // the watchdog released it meanwhile
+  *s.start = 0;                      // acknowledge: the stream moves on to wait for the end flag
+  std::atomic_thread_fence(std::memory_order_seq_cst);
+  s.state = kAcked;
+}
+
+// The stream of an abandoned slot reached its start flag: let it pass without
+// moving anything.  The caller holds P->mu.
+void abandon_locked(Proxy* P, Slot& s) {
+  std::atomic_thread_fence(std::memory_order_seq_cst);
+  *s.start = 0;                   // the ack, if the stream waits for it
+  if (s.abandoned_ops >= 3) {     // the stream waits for FINISH, but nothing will reset end_flag
+    *s.end = kFinishValue;
+    s.state = kRetired;
+  } else {                        // nothing waits on end_flag
+    s.state = kFree;
+  }
+  std::atomic_thread_fence(std::memory_order_seq_cst);
+  s.abandoned_ops = 0;
+  P->cv.notify_all();
+}
+
+// The task was acknowledged and its stream operations are all queued, or could
+// not be: plan and issue the moves, or let the stream pass.
+void move_task(Proxy* P, Slot& s) {
   std::atomic_thread_fence(std::memory_order_acquire);
   const int k = P->k;
   std::vector<size_t> cnt(size_t(k) * k);
   for (int a = 0; a < k; ++a)
     for (int b = 0; b < k; ++b)
       cnt[size_t(a) * k + b] = size_t(s.transpose ? s.counts[size_t(b) * k + a] : s.counts[size_t(a) * k + b]);
-  // Injected on the host: the proxy thread is held up past the deadline, as in
-  // a driver call that waits for the held stream; the watchdog must release.
-  if (block) std::this_thread::sleep_for(kInjectedBlock);
   {
     std::lock_guard<std::mutex> lock(P->mu);
-    if (s.state != kStarting) return;  // the watchdog released it meanwhile
-    *s.start = 0;                      // acknowledge: the stream moves on to wait for the end flag
-    std::atomic_thread_fence(std::memory_order_seq_cst);
+    if (s.state != kAcked) return;  // the watchdog released it meanwhile
+    if (s.abandoned_ops > 0) {
+      abandon_locked(P, s);
+      return;
+    }
+    s.state = kMoving;
     if (P->orphaned) {
       release_locked(P, s, HOC_ERR_NOT_INITIALIZED, "the communicator was destroyed before the task started");
       return;
@@ -225,7 +260,7 @@ void start_task(Proxy* P, Slot& s) {
   }
   if (P->fault == kFaultProxyStall) {  // injected on the host: a completion that never arrives
     std::lock_guard<std::mutex> lock(P->mu);
-    if (s.state == kStarting) {
+    if (s.state == kMoving) {
       s.stalled = true;
       s.state = kRunning;
     }
@@ -256,26 +291,10 @@ void start_task(Proxy* P, Slot& s) {
   }
   trace(P, s, "moves issued");
   std::lock_guard<std::mutex> lock(P->mu);
-  if (s.state == kStarting) {
+  if (s.state == kMoving) {
     s.stalled = false;
     s.state = kRunning;
   }
-}
-
-// The stream of an abandoned slot reached its start flag: let it pass without
-// moving anything.  The caller holds P->mu.
-void abandon_locked(Proxy* P, Slot& s) {
-  std::atomic_thread_fence(std::memory_order_seq_cst);
-  *s.start = 0;                   // the ack, if the stream waits for it
-  if (s.abandoned_ops >= 3) {     // the stream waits for FINISH, but nothing will reset end_flag
-    *s.end = kFinishValue;
-    s.state = kRetired;
-  } else {                        // nothing waits on end_flag
-    s.state = kFree;
-  }
-  std::atomic_thread_fence(std::memory_order_seq_cst);
-  s.abandoned_ops = 0;
-  P->cv.notify_all();
 }
 
 void free_resources(Proxy* P) {
@@ -292,7 +311,7 @@ void watchdog_loop(Proxy* P) {
   while (!P->stop_watchdog) {
     const auto now = Clock::now();
     for (Slot& s : P->slots) {
-      if ((s.state != kStarting && s.state != kRunning) || now <= s.deadline) continue;
+      if (!s.held() || now <= s.deadline) continue;
       const bool issued = s.state == kRunning;
       release_locked(P, s, HOC_ERR_TIMEOUT, issued ? kWhyDeadline : "the proxy did not issue the moves before the deadline");
       if (P->trace)
@@ -309,9 +328,11 @@ void proxy_loop(Proxy* P) {
     bool busy = false, all_free = true;
     for (Slot& s : P->slots) {
       int st;
+      bool queueing;
       {
         std::lock_guard<std::mutex> lock(P->mu);
         st = s.state;
+        queueing = s.queueing;
       }
       if (st == kFree || st == kRetired) continue;
       all_free = false;
@@ -324,6 +345,12 @@ void proxy_loop(Proxy* P) {
             if (abandoned) abandon_locked(P, s);
           }
           if (!abandoned) start_task(P, s);
+          if (!abandoned && !queueing) move_task(P, s);
+          busy = true;
+        }
+      } else if (st == kAcked) {
+        if (!queueing) {
+          move_task(P, s);
           busy = true;
         }
       } else if (st == kRunning) {
@@ -564,7 +591,8 @@ extern "C" hocResult_t hoc_alltoall_device_counts(hocComm_t comm, const void* co
       if (cand->state == kFree) slot = cand;
     }
     ++P->next;
-    if ((P->fault == kFaultProxyMemop || P->fault == kFaultProxyMemopReset) && !P->memop_fault_used) {
+    if ((P->fault == kFaultProxyMemop || P->fault == kFaultProxyMemopReset || P->fault == kFaultProxyMemopLate) &&
+        !P->memop_fault_used) {
       P->memop_fault_used = true;
       inject_fail_at = P->fault == kFaultProxyMemop ? 3 : 4;
     }
@@ -577,12 +605,14 @@ extern "C" hocResult_t hoc_alltoall_device_counts(hocComm_t comm, const void* co
     slot->cap.assign(recv_capacity, recv_capacity + k);
     slot->scap.assign(send_capacity, send_capacity + k);
     slot->abandoned_ops = 0;
+    slot->queueing = true;
     slot->state = kQueued;
     P->cv.notify_all();  // wake an idle proxy thread
   }
   const size_t counts_bytes = size_t(k) * k * sizeof(uint64_t);
   if (cudaMemcpyAsync(slot->counts, d_sendcounts, counts_bytes, cudaMemcpyDeviceToHost, s) != cudaSuccess) {
     std::lock_guard<std::mutex> lock(P->mu);
+    slot->queueing = false;
     slot->state = kFree;  // nothing was queued on the stream
     set_error_detail("cudaMemcpyAsync of the device counts failed");
     return HOC_ERR_CUDA;
@@ -590,7 +620,10 @@ extern "C" hocResult_t hoc_alltoall_device_counts(hocComm_t comm, const void* co
   CUstream cu = reinterpret_cast<CUstream>(s);
   int queued = 0;  // stream operations queued so far, in order
   for (int op = 1; op <= kStreamOps; ++op) {
-    if (op == inject_fail_at) break;
+    if (op == inject_fail_at) {
+      if (P->fault == kFaultProxyMemopLate) std::this_thread::sleep_for(kInjectedLate);
+      break;
+    }
     CUresult e;
     switch (op) {
       case 1: e = P->write32(cu, slot->d_start, kStartValue, CU_STREAM_WRITE_VALUE_DEFAULT); break;
@@ -601,16 +634,18 @@ extern "C" hocResult_t hoc_alltoall_device_counts(hocComm_t comm, const void* co
     if (e != CUDA_SUCCESS) break;
     ++queued;
   }
+  std::lock_guard<std::mutex> lock(P->mu);
+  slot->queueing = false;
+  P->cv.notify_all();
   if (queued < kStreamOps) {
-    std::lock_guard<std::mutex> lock(P->mu);
-    if (queued == 0) {
+    if (queued == 0 || slot->state == kReleasing) {
       // The stream will never write the start flag, but the counts copy queued
-      // on it may still land in the slot: retire it rather than hand it out.
+      // on it may still land in the slot: retire it rather than hand it out.  Or the
+      // watchdog has released it meanwhile: FINISH stands, and nothing will reset it.
       slot->state = kRetired;
     } else {
       slot->abandoned_ops = queued;  // the proxy lets the stream pass its flags and moves nothing
     }
-    P->cv.notify_all();
     set_error_detail("queueing the stream memory operations failed; nothing will be moved");
     return HOC_ERR_CUDA;
   }

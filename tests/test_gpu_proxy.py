@@ -221,3 +221,9 @@ def test_failed_stream_operations_release_their_slot(monkeypatch, fault):
                 assert np.array_equal(to_host(rvv[d], "int32")[: len(want[d])], want[d]), (it, d)
         st = c.proxy_status()
         assert st["completed"] == 20 and st["released_on_error"] == 0
+
+
+def test_stream_operations_that_fail_late_move_nothing(monkeypatch):
+    """The same when the stream has reached its start flag, and the proxy has seen it, long before the call finds that its
+    last operation does not queue."""
+    test_failed_stream_operations_release_their_slot(monkeypatch, "proxy_memop_late")
