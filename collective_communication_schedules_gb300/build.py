@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libhoc.so")
 STAMP = LIB + ".stamp"  # the machine the library was built for: a copy from another machine is rebuilt
 
 SOURCES = ["reduce.cu", "reduce_tma.cu", "tma_copy.cu", "workload.cu", "plan.cpp", "hoc.cpp", "topo_sched.cpp", "proxy.cpp", "ep.cu", "host_ar.cpp",
-           "layer.cu", "mm_any.cu", "mm_few.cu", "mm_tc.cu", "grad.cu"]
+           "layer.cu", "mm_any.cu", "mm_few.cu", "mm_tc.cu", "grad.cu", "norm.cu", "route.cu", "dropout.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 # IEEE arithmetic in the reduce kernels: no flush to zero, no fast math.

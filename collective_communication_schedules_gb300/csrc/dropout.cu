@@ -1,0 +1,146 @@
+// Dropout from a counter-based generator, with the residual's addition (hoc_block.h).
+//
+// Element i's 16 random bits are a part of Philox4x32-10 of the counter i / 8, so that
+// nothing of the mask is stored and the gradient draws it again.  Bound by its bytes:
+// ten rounds for eight elements are about 6 integer operations an element.
+#include "block.h"
+
+namespace hoc {
+namespace {
+
+using namespace block;
+
+struct DropArgs {
+  const void *x, *r;
+  void* y;
+  const int64_t* seed;
+  int64_t ldx, ldr, ldy, total;  // total: rows * width
+  int64_t width;
+  unsigned t;                    // dropped where the element's bits are below this
+  float keep;                    // 65536 / (65536 - t)
+};
+
+// Philox4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw, 2011).
+__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = uint64_t(0xD2511F53u) * c.x, b = uint64_t(0xCD9E8D57u) * c.z;
+    c = make_uint4(uint32_t(b >> 32) ^ c.y ^ k0, uint32_t(b), uint32_t(a >> 32) ^ c.w ^ k1, uint32_t(a));
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return c;
+}
+
+constexpr int kDropThreads = 256, kDropAhead = 2;
+
+// A thread takes kDropAhead groups of eight elements.  VEC: rows are whole groups on
+// 16-byte boundaries.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropArgs A) {
+  after_the_last();
+  constexpr int N = 16 / sizeof(T), Q = 8 / N;
+  const T *x = static_cast<const T*>(A.x), *r = static_cast<const T*>(A.r);
+  T* y = static_cast<T*>(A.y);
+  const uint64_t key = A.t ? uint64_t(A.seed[0]) : 0, call = A.t ? uint64_t(A.seed[1]) : 0;
+  const int64_t first = int64_t(blockIdx.x) * kDropThreads * kDropAhead + threadIdx.x;
+  const int64_t groups = (A.total + 7) / 8;
+  Vec<T, N> v[kDropAhead][Q], w[kDropAhead][Q];
+  int64_t row[kDropAhead], col[kDropAhead];
+#pragma unroll
+  for (int u = 0; u < kDropAhead; ++u) {
+    const int64_t i = (first + u * kDropThreads) * 8;
+    row[u] = A.width >= A.total ? 0 : i < (int64_t(1) << 32) ? int64_t(unsigned(i) / unsigned(A.width)) : i / A.width;
+    col[u] = i - row[u] * A.width;
+    if (VEC && i < A.total) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        v[u][q] = *reinterpret_cast<const Vec<T, N>*>(x + row[u] * A.ldx + col[u] + q * N);
+        if (r) w[u][q] = *reinterpret_cast<const Vec<T, N>*>(r + row[u] * A.ldr + col[u] + q * N);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kDropAhead; ++u) {
+    const int64_t g = first + u * kDropThreads;
+    if (g >= groups) break;
+    uint32_t bits[4] = {};
+    if (A.t) {
+      const uint4 c = philox(make_uint4(uint32_t(g), uint32_t(uint64_t(g) >> 32), uint32_t(call), uint32_t(call >> 32)),
+                             uint32_t(key), uint32_t(key >> 32));
+      bits[0] = c.x, bits[1] = c.y, bits[2] = c.z, bits[3] = c.w;
+    }
+    auto result = [&](int e, T xv, T rv) {
+      const unsigned b = e & 1 ? bits[e >> 1] >> 16 : bits[e >> 1] & 0xFFFFu;
+      const float f = b >= A.t ? widen(xv) * A.keep : 0.f;
+      return narrow<T>(r ? widen(rv) + f : f);
+    };
+    if (VEC) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        Vec<T, N> o;
+#pragma unroll
+        for (int e = 0; e < N; ++e) o.v[e] = result(q * N + e, v[u][q].v[e], w[u][q].v[e]);
+        *reinterpret_cast<Vec<T, N>*>(y + row[u] * A.ldy + col[u] + q * N) = o;
+      }
+    } else {
+      int64_t at = row[u], c = col[u];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (g * 8 + e >= A.total) break;
+        y[at * A.ldy + c] = result(e, x[at * A.ldx + c], r ? r[at * A.ldr + c] : narrow<T>(0.f));
+        if (++c == A.width) {
+          c = 0;
+          ++at;
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t dropout_preload() {
+  const void* fns[] = {reinterpret_cast<const void*>(&dropout_kernel<float, true>),
+                       reinterpret_cast<const void*>(&dropout_kernel<float, false>),
+                       reinterpret_cast<const void*>(&dropout_kernel<__nv_bfloat16, true>),
+                       reinterpret_cast<const void*>(&dropout_kernel<__nv_bfloat16, false>)};
+  for (const void* f : fns) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, f);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace hoc
+
+using namespace hoc;
+using namespace hoc::block;
+
+extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, const void* x, size_t ldx,
+                                   const void* residual, size_t ldr, double p, const int64_t* seed, void* y, size_t ldy,
+                                   void* stream) {
+  const char* who = "hoc_dropout";
+  if (rows < 0 || width < 0) return refuse(who, "rows or width out of range");
+  if (!row_dtype(dtype)) return refuse(who, "dtype must be HOC_FLOAT32 or HOC_BFLOAT16");
+  if (!(p >= 0.0 && p < 1.0)) return refuse(who, "p must be at least 0 and below 1");
+  const bool none = rows == 0 || width == 0;
+  const size_t b = bytes_of(dtype);
+  const char* bad = bad_rows(x, ldx, rows, width, b, none);
+  if (!bad) bad = bad_rows(residual, ldr, rows, width, b, true);
+  if (!bad) bad = bad_rows(y, ldy, rows, width, b, none);
+  if (!bad && (!seed || !aligned(seed, 8))) bad = "seed must be given, aligned to its elements";
+  if (bad) return refuse(who, bad);
+  if (none) return HOC_SUCCESS;
+  const int64_t total = int64_t(rows) * width;
+  const int t = int(p * 65536 + 0.5) < 65535 ? int(p * 65536 + 0.5) : 65535;
+  const DropArgs A{x, residual, y, seed, int64_t(ldx), int64_t(ldr), int64_t(ldy), total, width, unsigned(t),
+                   65536.f / float(65536 - t)};
+  const int64_t ctas = ((total + 7) / 8 + kDropThreads * kDropAhead - 1) / (kDropThreads * kDropAhead);
+  if (ctas > 0x7FFFFFFF) return refuse(who, "more than 2^43 elements");
+  const bool vec = width % 8 == 0 && vector_rows(x, ldx, b) && (!residual || vector_rows(residual, ldr, b)) && vector_rows(y, ldy, b);
+  const auto kernel = dtype == HOC_FLOAT32 ? vec ? dropout_kernel<float, true> : dropout_kernel<float, false>
+                                           : vec ? dropout_kernel<__nv_bfloat16, true> : dropout_kernel<__nv_bfloat16, false>;
+  return launched(who, launch(kernel, dim3(unsigned(ctas)), dim3(kDropThreads), 0, static_cast<cudaStream_t>(stream), A));
+}

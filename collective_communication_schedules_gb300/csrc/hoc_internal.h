@@ -59,6 +59,9 @@ cudaError_t ep_preload();        // expert-parallel pack and combine kernels
 cudaError_t workload_preload();  // probe and stand-in compute kernels
 cudaError_t mm_preload();        // expert and linear products and the kernels beside them
 cudaError_t grad_preload();      // gradient norm and clipping
+cudaError_t norm_preload();      // RMS norm, its gradient, rows of 8 bits
+cudaError_t route_preload();     // routing to experts and its gradient
+cudaError_t dropout_preload();
 
 // TMA-fed variant (reduce_tma.cu): same fold, bulk copies through shared memory.
 uint64_t reduce_tma_seg_tiles(int dtype, const ReduceSeg& s, int k);

@@ -411,6 +411,9 @@ hocResult_t preload_kernels(int device) {
   if (e == cudaSuccess) e = workload_preload();
   if (e == cudaSuccess) e = mm_preload();
   if (e == cudaSuccess) e = grad_preload();
+  if (e == cudaSuccess) e = norm_preload();
+  if (e == cudaSuccess) e = route_preload();
+  if (e == cudaSuccess) e = dropout_preload();
   if (e != cudaSuccess) {
     set_error_detail("loading the library's kernels before starting the proxy failed");
     return HOC_ERR_CUDA;

@@ -156,6 +156,20 @@ _SIGS["hoc_grad_workspace"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)])
 _SIGS["hoc_grad_norm"] = (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p])
 _SIGS["hoc_grad_clip"] = (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_size_t,
                                     C.c_void_p])
+_ROWS = [C.c_void_p, C.c_size_t]  # rows and their stride
+_SIGS["hoc_wire8_row"] = (C.c_int, [C.c_int, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)])
+_SIGS["hoc_rms_norm"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 2 * _ROWS + [C.c_void_p, C.c_int, C.c_float] + 2 * _ROWS
+                         + [C.c_void_p, C.c_void_p])
+_SIGS["hoc_rms_norm_workspace"] = (C.c_int, [C.c_int, C.c_int, C.POINTER(C.c_size_t)])
+_SIGS["hoc_rms_norm_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 3 * _ROWS + [C.c_void_p, C.c_int, C.c_float]
+                              + 2 * _ROWS + [C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["hoc_expert_widen"] = (C.c_int, [C.POINTER(_RowGroups), C.POINTER(C.c_void_p), C.c_int, C.POINTER(C.c_void_p),
+                                       C.c_void_p])
+_SIGS["hoc_ep_route"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_size_t, C.c_int, C.c_void_p,
+                                   C.c_int, C.c_int, C.c_int, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p])
+_SIGS["hoc_ep_route_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_size_t, C.c_int, C.c_int,
+                                        C.c_float, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["hoc_dropout"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 2 * _ROWS + [C.c_double, C.c_void_p] + _ROWS + [C.c_void_p])
 _SIGS["hoc_allreduce_host"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.c_size_t,
                                          C.c_int, C.c_int, C.c_void_p])
 _SIGS["hoc_proxy_status"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64), C.POINTER(C.c_uint64),
@@ -872,6 +886,249 @@ def layer_trim(keep: int = 0):
     if keep < 0:
         raise ValueError("keep must not be negative")
     _check(lib().hoc_layer_trim(int(keep)), "hoc_layer_trim")
+
+
+# ------------------------------------- between the residual stream and the dispatch
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score is one of {', '.join(SCORES)}, not {score!r}")
+    return SCORES[score]
+
+
+def _row_dtype(x, what: str) -> int:
+    """The code of the dtype of `x`, rows of which the calls below take."""
+    dtype = getattr(x, "dtype", None)
+    if dtype is _dt("bfloat16"):
+        return BFLOAT16
+    if dtype is _dt("float32"):
+        return FLOAT32
+    raise TypeError(f"{what}: expected a bfloat16 or float32 tensor")
+
+
+def _here(x, what: str) -> int:
+    """The device of `x`, which has to be the current one: a launch would run there."""
+    import torch
+    if not x.is_cuda:
+        raise ValueError(f"{what}: must be a CUDA tensor")
+    device = x.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{what}: is on another device than the current one")
+    return device
+
+
+def _rows_of(x, shape, dtype, device: int, what: str):
+    """Address and row stride of the matrix `x`, whose rows' elements are contiguous; (None, 0) for None."""
+    if x is None:
+        return None, 0
+    if isinstance(x, int) or x.dtype is not dtype:
+        raise TypeError(f"{what}: expected a {str(dtype).split('.')[-1]} tensor")
+    if x.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
+    if not x.is_cuda or x.get_device() != device:
+        raise ValueError(f"{what}: must be a CUDA tensor on the device of the others")
+    rows, width = shape
+    if rows == 0 or width == 0:
+        return x.data_ptr(), width
+    ld, step = x.stride()
+    if width > 1 and step != 1:
+        raise ValueError(f"{what}: a row's elements must be contiguous")
+    if rows == 1:
+        return x.data_ptr(), width
+    if ld < width:
+        raise ValueError(f"{what}: rows must not overlap")
+    return x.data_ptr(), ld
+
+
+def _flat(x, n: int, dtype, device: int, what: str):
+    """Address of the contiguous tensor `x` of n elements; None for None."""
+    if x is None:
+        return None
+    if isinstance(x, int) or x.dtype is not dtype:
+        raise TypeError(f"{what}: expected a {str(dtype).split('.')[-1]} tensor")
+    if x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous elements, got shape {tuple(x.shape)}")
+    if not x.is_cuda or x.get_device() != device:
+        raise ValueError(f"{what}: must be a CUDA tensor on the device of the others")
+    return x.data_ptr()
+
+
+_WIRE8 = {}  # width -> (bytes of a row, where its scales start)
+
+
+def _wire8(width: int):
+    got = _WIRE8.get(width)
+    if got is None:
+        n, at = C.c_size_t(), C.c_size_t()
+        _check(lib().hoc_wire8_row(int(width), C.byref(n), C.byref(at)), "hoc_wire8_row")
+        got = _WIRE8[width] = (n.value, at.value)
+    return got
+
+
+def wire8_bytes(width: int) -> int:
+    """Bytes of a row of `width` values in 8 bits with their scales (see include/hoc_block.h): a dispatch moves such rows,
+    a uint8 tensor viewed as bfloat16, as rows of half as many elements."""
+    return _wire8(width)[0]
+
+
+def wire8_views(wire, width: int):
+    """The values (float8_e4m3fn, [rows, width]) and scales (float32, [rows, ceil(width / 128)]) in rows of 8 bits."""
+    import torch
+    n, at = _wire8(width)
+    if wire.dtype is not torch.uint8 or wire.dim() != 2 or wire.shape[1] != n:
+        raise ValueError(f"wire: expected a uint8 tensor of shape [rows, {n}]")
+    return (wire[:, :width].view(torch.float8_e4m3fn),
+            wire[:, at: at + (width + 127) // 128 * 4].view(torch.float32))
+
+
+def _wire_rows(wire, rows: int, width: int, device: int, what: str) -> Optional[int]:
+    import torch
+    if wire is None:
+        return None
+    if wire.dim() != 2 or wire.shape[0] != rows or wire.shape[1] != _wire8(width)[0]:
+        raise ValueError(f"{what}: expected shape {(rows, _wire8(width)[0])}, got {tuple(wire.shape)}")
+    return _flat(wire, wire.numel(), torch.uint8, device, what)
+
+
+def rms_norm(x, weight, y=None, *, eps: float, residual=None, h=None, wire=None, stream=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, stored as it is and / or as rows of 8 bits in wire, uint8
+    [rows, wire8_bytes(width)] (see include/hoc_block.h).  x, residual, h and y: [rows, width] in bf16 or float32, may be
+    rows of wider buffers; weight: [width] in either."""
+    dt = _row_dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    shape, dev = x.shape, _here(x, "x")
+    rows, width = shape
+    xp, ldx = _rows_of(x, shape, x.dtype, dev, "x")
+    rp, ldr = _rows_of(residual, shape, x.dtype, dev, "residual")
+    hp, ldh = _rows_of(h, shape, x.dtype, dev, "h")
+    yp, ldy = _rows_of(y, shape, x.dtype, dev, "y")
+    wdt = _row_dtype(weight, "weight")
+    _check(lib().hoc_rms_norm(rows, width, dt, xp, ldx, rp, ldr, _flat(weight, width, weight.dtype, dev, "weight"), wdt,
+                              eps, hp, ldh, yp, ldy, _wire_rows(wire, rows, width, dev, "wire"), _stream(stream)),
+           "hoc_rms_norm")
+
+
+def rms_norm_workspace(rows: int, width: int) -> int:
+    """int32 entries of scratch that rms_norm_grad needs for a weight gradient."""
+    n = C.c_size_t()
+    _check(lib().hoc_rms_norm_workspace(int(rows), int(width), C.byref(n)), "hoc_rms_norm_workspace")
+    return n.value
+
+
+def rms_norm_grad(dy, h, weight, dx, *, eps: float, dy2=None, dres=None, dw=None, accumulate: bool = False,
+                  workspace=None, stream=None):
+    """Gradients of rms_norm: dx for h (and so for x and the residual) from dy (+ dy2) for y and dres for h itself; dw (+)=
+    the weight's, in bf16 or float32, with an int32 workspace of rms_norm_workspace entries (see include/hoc_block.h)."""
+    dt = _row_dtype(dy, "dy")
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix")
+    shape, dev = dy.shape, _here(dy, "dy")
+    rows, width = shape
+    dyp, lddy = _rows_of(dy, shape, dy.dtype, dev, "dy")
+    dy2p, lddy2 = _rows_of(dy2, shape, dy.dtype, dev, "dy2")
+    hp, ldh = _rows_of(h, shape, dy.dtype, dev, "h")
+    drp, lddr = _rows_of(dres, shape, dy.dtype, dev, "dres")
+    dxp, lddx = _rows_of(dx, shape, dy.dtype, dev, "dx")
+    if hp is None or dxp is None:
+        raise ValueError("h and dx must be given")
+    wdt, dwdt = _row_dtype(weight, "weight"), FLOAT32 if dw is None else _row_dtype(dw, "dw")
+    wsp, ints = None, 0
+    if dw is not None:
+        if workspace is None:
+            raise ValueError("workspace: a weight gradient needs one")
+        ints = workspace.numel()
+        wsp = _flat(workspace, ints, _dt("int32"), dev, "workspace")
+    _check(lib().hoc_rms_norm_grad(rows, width, dt, dyp, lddy, dy2p, lddy2, hp, ldh,
+                                   _flat(weight, width, weight.dtype, dev, "weight"), wdt, eps, drp, lddr, dxp, lddx,
+                                   None if dw is None else _flat(dw, width, dw.dtype, dev, "dw"), dwdt,
+                                   int(bool(accumulate)), wsp, ints, _stream(stream)), "hoc_rms_norm_grad")
+
+
+def expert_widen(wire, seg, y, stream=None):
+    """y[d][r] = bf16 of the rows of 8 bits wire[d][r], for the rows that seg covers (see include/hoc_block.h): lists of k
+    device tensors, wire uint8 [capacity, wire8_bytes(width)], y bf16 [capacity, width]; seg as expert_mm's."""
+    k = len(y)
+    if not k or len(wire) != k or y[0].dim() != 2:
+        raise ValueError("wire and y: lists of as many matrices")
+    _typed(seg, "int64", "seg")
+    if seg.dim() != 2 or seg.shape[0] != k or seg.shape[1] < 2:
+        raise ValueError(f"seg: expected shape [{k}, sources * experts + 1], got {tuple(seg.shape)}")
+    dev, width = _here(y[0], "y[0]"), y[0].shape[1]
+    n, bf = wire8_bytes(width), _dt("bfloat16")
+    yp, wp, cap = (C.c_void_p * k)(), (C.c_void_p * k)(), (C.c_size_t * k)()
+    for d in range(k):
+        t, w = y[d], wire[d]
+        rows = t.shape[0]
+        if t.dim() != 2 or t.shape[1] != width:
+            raise ValueError(f"y[{d}]: expected shape [capacity, {width}], got {tuple(t.shape)}")
+        yp[d], cap[d] = _flat(t, rows * width, bf, dev, "y"), rows
+        wp[d] = _wire_rows(w, rows, width, dev, "wire")
+    g = _RowGroups(k, seg.shape[1] - 1, 1, _flat(seg, seg.numel(), seg.dtype, dev, "seg"), cap)
+    _check(lib().hoc_expert_widen(C.byref(g), wp, width, yp, _stream(stream)), "hoc_expert_widen")
+
+
+def _slots(logits, ids, gate, what: str):
+    """What both calls of the routing check: tokens, experts, topk, the logits' dtype and the addresses."""
+    dt = _row_dtype(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be a matrix [tokens, experts]")
+    shape, dev = logits.shape, _here(logits, "logits")
+    tokens, experts = shape
+    n = ids.numel()
+    if n % tokens if tokens else n:
+        raise ValueError("ids must hold topk ids per token")
+    lp, ldl = _rows_of(logits, shape, logits.dtype, dev, "logits")
+    return (tokens, experts, n // tokens if tokens else 1, lp, dt, ldl, dev, _flat(ids, n, _dt("int32"), dev, "ids"),
+            _flat(gate, n, _dt("float32"), dev, what))
+
+
+def ep_route(logits, ids, gate, *, score: str = "softmax", bias=None, groups: int = 1, top_groups: Optional[int] = None,
+             renormalise: bool = False, scale: float = 1.0, stream=None):
+    """Routing of tokens to their topk experts (see include/hoc_block.h): logits [tokens, experts] in bf16 or float32, may
+    be rows of a wider buffer; ids int32 and gate float32 of tokens * topk elements, as a dispatch and a combine take them;
+    bias float32 [experts], for the choice only; of `groups` groups of experts the best top_groups (default: all)."""
+    tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, gate, "gate")
+    _check(lib().hoc_ep_route(tokens, experts, topk, lp, dt, ldl, _score(score),
+                              _flat(bias, experts, _dt("float32"), dev, "bias"), groups,
+                              groups if top_groups is None else top_groups, int(bool(renormalise)), scale, ip, gp,
+                              _stream(stream)), "hoc_ep_route")
+
+
+def ep_route_grad(logits, ids, dgate, dlogits, *, score: str = "softmax", renormalise: bool = False, scale: float = 1.0,
+                  stream=None):
+    """Gradient of ep_route for the logits, from dgate for the gates; dlogits may be logits (see include/hoc_block.h)."""
+    tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, dgate, "dgate")
+    dp, ldd = _rows_of(dlogits, logits.shape, logits.dtype, dev, "dlogits")
+    _check(lib().hoc_ep_route_grad(tokens, experts, topk, lp, dt, ldl, _score(score), int(bool(renormalise)), scale, ip, gp,
+                                   dp, ldd, _stream(stream)), "hoc_ep_route_grad")
+
+
+def dropout(x, y, p: float, seed, *, residual=None, stream=None):
+    """y = residual + x / (1 - p) where an element is kept, residual (or 0) where it is dropped; which are is drawn from
+    seed, two int64 on the device, and not stored: the gradient is the same call on the gradient, without a residual (see
+    include/hoc_block.h).  x, y and residual: contiguous, of any shape, or [rows, width] that may be rows of wider buffers."""
+    dt, dev = _row_dtype(x, "x"), _here(x, "x")
+    shape = x.shape
+    if x.dim() != 2:
+        for t, what in ((x, "x"), (y, "y"), (residual, "residual")):
+            if t is not None and (t.shape != shape or not t.is_contiguous()):
+                raise ValueError(f"{what}: expected shape {tuple(shape)}, contiguous (or rows of a matrix)")
+        n = x.numel()
+        width = 1
+        for w in reversed(shape):  # rows of the last dimensions, within the limits of an int
+            if width * w >= 1 << 31:
+                break
+            width *= w
+        shape = (n // width if width else 0, width)
+        x, y, residual = x.view(shape), y.view(shape), None if residual is None else residual.view(shape)
+    xp, ldx = _rows_of(x, shape, x.dtype, dev, "x")
+    yp, ldy = _rows_of(y, shape, x.dtype, dev, "y")
+    rp, ldr = _rows_of(residual, shape, x.dtype, dev, "residual")
+    _check(lib().hoc_dropout(shape[0], shape[1], dt, xp, ldx, rp, ldr, p, _flat(seed, 2, _dt("int64"), dev, "seed"), yp,
+                             ldy, _stream(stream)), "hoc_dropout")
 
 
 # ------------------------------------------------------------- gradient clipping
