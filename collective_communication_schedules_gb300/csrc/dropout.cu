@@ -119,12 +119,12 @@ using namespace hoc;
 using namespace hoc::block;
 
 extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, const void* x, size_t ldx,
-                                   const void* residual, size_t ldr, double p, const int64_t* seed, void* y, size_t ldy,
+                                   const void* residual, size_t ldr, const double* p, const int64_t* seed, void* y, size_t ldy,
                                    void* stream) {
   const char* who = "hoc_dropout";
   if (rows < 0 || width < 0) return refuse(who, "rows or width out of range");
   if (!row_dtype(dtype)) return refuse(who, "dtype must be HOC_FLOAT32 or HOC_BFLOAT16");
-  if (!(p >= 0.0 && p < 1.0)) return refuse(who, "p must be at least 0 and below 1");
+  if (!p || !(*p >= 0.0 && *p < 1.0)) return refuse(who, "p must be given, at least 0 and below 1");
   const bool none = rows == 0 || width == 0;
   const size_t b = bytes_of(dtype);
   const char* bad = bad_rows(x, ldx, rows, width, b, none);
@@ -134,7 +134,7 @@ extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, con
   if (bad) return refuse(who, bad);
   if (none) return HOC_SUCCESS;
   const int64_t total = int64_t(rows) * width;
-  const int t = int(p * 65536 + 0.5) < 65535 ? int(p * 65536 + 0.5) : 65535;
+  const int t = int(*p * 65536 + 0.5) < 65535 ? int(*p * 65536 + 0.5) : 65535;
   const DropArgs A{x, residual, y, seed, int64_t(ldx), int64_t(ldr), int64_t(ldy), total, width, unsigned(t),
                    65536.f / float(65536 - t)};
   const int64_t ctas = ((total + 7) / 8 + kDropThreads * kDropAhead - 1) / (kDropThreads * kDropAhead);

@@ -563,11 +563,11 @@ extern "C" hocResult_t hoc_wire8_row(int width, size_t* bytes, size_t* at) {
 
 extern "C" hocResult_t hoc_rms_norm(int rows, int width, hocDataType_t dtype, const void* x, size_t ldx,
                                     const void* residual, size_t ldr, const void* weight, hocDataType_t weight_dtype,
-                                    float eps, void* h, size_t ldh, void* y, size_t ldy, void* wire, void* stream) {
+                                    const float* eps, void* h, size_t ldh, void* y, size_t ldy, void* wire, void* stream) {
   const char* who = "hoc_rms_norm";
   if (rows < 0 || width < 1 || width > kMaxWidth) return refuse(who, "rows or width out of range");
   if (!row_dtype(dtype) || !row_dtype(weight_dtype)) return refuse(who, "dtypes must be HOC_FLOAT32 or HOC_BFLOAT16");
-  if (!(eps >= 0.f)) return refuse(who, "eps must be at least 0");
+  if (!eps || !(*eps >= 0.f)) return refuse(who, "eps must be given, and at least 0");
   if (rows > 0 && !y && !wire) return refuse(who, "y or wire must be given");
   if (h && !residual) return refuse(who, "h is given where a residual is added");
   const size_t b = bytes_of(dtype);
@@ -580,7 +580,7 @@ extern "C" hocResult_t hoc_rms_norm(int rows, int width, hocDataType_t dtype, co
   if (bad) return refuse(who, bad);
   if (rows == 0) return HOC_SUCCESS;
   const NormArgs A{x,           residual,     weight,       h,    y,     static_cast<uint8_t*>(wire), int64_t(ldx), int64_t(ldr),
-                   int64_t(ldh), int64_t(ldy), rows, width, eps, weight_dtype == HOC_FLOAT32};
+                   int64_t(ldh), int64_t(ldy), rows, width, *eps, weight_dtype == HOC_FLOAT32};
   const bool vec = width * b % 16 == 0 && vector_rows(x, ldx, b) && (!residual || vector_rows(residual, ldr, b)) &&
                    (!h || vector_rows(h, ldh, b)) && (!y || vector_rows(y, ldy, b)) && aligned(weight, 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -596,14 +596,14 @@ extern "C" hocResult_t hoc_rms_norm_workspace(int rows, int width, size_t* ints)
 
 extern "C" hocResult_t hoc_rms_norm_grad(int rows, int width, hocDataType_t dtype, const void* dy, size_t lddy,
                                          const void* dy2, size_t lddy2, const void* h, size_t ldh, const void* weight,
-                                         hocDataType_t weight_dtype, float eps, const void* dres, size_t lddres,
+                                         hocDataType_t weight_dtype, const float* eps, const void* dres, size_t lddres,
                                          void* dx, size_t lddx, void* dw, hocDataType_t dw_dtype, int accumulate,
                                          int32_t* workspace, size_t workspace_ints, void* stream) {
   const char* who = "hoc_rms_norm_grad";
   if (rows < 0 || width < 1 || width > kMaxWidth) return refuse(who, "rows or width out of range");
   if (!row_dtype(dtype) || !row_dtype(weight_dtype) || (dw && !row_dtype(dw_dtype)))
     return refuse(who, "dtypes must be HOC_FLOAT32 or HOC_BFLOAT16");
-  if (!(eps >= 0.f)) return refuse(who, "eps must be at least 0");
+  if (!eps || !(*eps >= 0.f)) return refuse(who, "eps must be given, and at least 0");
   const size_t b = bytes_of(dtype);
   const char* bad = bad_rows(dy, lddy, rows, width, b, rows == 0);
   if (!bad) bad = bad_rows(dy2, lddy2, rows, width, b, true);
@@ -621,7 +621,7 @@ extern "C" hocResult_t hoc_rms_norm_grad(int rows, int width, hocDataType_t dtyp
   if (bad) return refuse(who, bad);
   if (rows == 0 && !dw) return HOC_SUCCESS;
   const NormGradArgs A{dy, dy2, h, weight, dres, dx, dw ? reinterpret_cast<float*>(workspace) : nullptr, int64_t(lddy),
-                       int64_t(lddy2), int64_t(ldh), int64_t(lddres), int64_t(lddx), rows, width, eps,
+                       int64_t(lddy2), int64_t(ldh), int64_t(lddres), int64_t(lddx), rows, width, *eps,
                        weight_dtype == HOC_FLOAT32};
   const bool vec = width * b % 16 == 0 && vector_rows(dy, lddy, b) && (!dy2 || vector_rows(dy2, lddy2, b)) &&
                    vector_rows(h, ldh, b) && (!dres || vector_rows(dres, lddres, b)) && vector_rows(dx, lddx, b) &&

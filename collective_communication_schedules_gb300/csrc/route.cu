@@ -477,12 +477,12 @@ int route_grid(int tokens) {
   ((E) <= 32 ? KERNEL<T, 1> : (E) <= 64 ? KERNEL<T, 2> : (E) <= 128 ? KERNEL<T, 4> : (E) <= 256 ? KERNEL<T, 8> \
                                                        : (E) <= 512 ? KERNEL<T, 16> : KERNEL<T, 32>)
 
-const char* bad_route(int tokens, int experts, int topk, const void* logits, int dtype, size_t ld, int score, float scale) {
+const char* bad_route(int tokens, int experts, int topk, const void* logits, int dtype, size_t ld, int score, const float* scale) {
   if (tokens < 0 || experts < 1 || experts > kMaxExperts) return "tokens or experts out of range";
   if (topk < 1 || topk > experts || topk > HOC_ROUTE_MAX_TOPK) return "topk out of range";
   if (!row_dtype(dtype)) return "dtype must be HOC_FLOAT32 or HOC_BFLOAT16";
   if (score != HOC_SCORE_SOFTMAX && score != HOC_SCORE_SIGMOID) return "score must be one of hocScore_t";
-  if (!(scale - scale == 0.f)) return "scale must be finite";
+  if (!scale || !(*scale - *scale == 0.f)) return "scale must be given, and finite";
   return bad_rows(logits, ld, tokens, experts, bytes_of(dtype), tokens == 0);
 }
 
@@ -511,7 +511,7 @@ using namespace hoc;
 using namespace hoc::block;
 
 extern "C" hocResult_t hoc_ep_route(int tokens, int experts, int topk, const void* logits, hocDataType_t dtype, size_t ldl,
-                                    int score, const float* bias, int groups, int top_groups, int renormalise, float scale,
+                                    int score, const float* bias, int groups, int top_groups, int renormalise, const float* scale,
                                     int32_t* ids, float* gate, void* stream) {
   const char* who = "hoc_ep_route";
   const char* bad = bad_route(tokens, experts, topk, logits, dtype, ldl, score, scale);
@@ -525,7 +525,7 @@ extern "C" hocResult_t hoc_ep_route(int tokens, int experts, int topk, const voi
   if (tokens == 0) return HOC_SUCCESS;
   const int epl = (experts + 31) / 32;
   const RouteArgs A{logits, bias, ids, gate, int64_t(ldl), tokens, experts, topk, epl, groups, top_groups,
-                    score == HOC_SCORE_SOFTMAX, renormalise != 0, access_of(logits, ldl, experts, epl, bytes_of(dtype)), scale};
+                    score == HOC_SCORE_SOFTMAX, renormalise != 0, access_of(logits, ldl, experts, epl, bytes_of(dtype)), *scale};
   const dim3 grid(route_grid(tokens)), cta(kRouteWarps * 32);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launched(who, dtype == HOC_FLOAT32 ? launch(HOC_ROUTE_PICK(route_kernel, float, experts), grid, cta, 0, s, A)
@@ -533,7 +533,7 @@ extern "C" hocResult_t hoc_ep_route(int tokens, int experts, int topk, const voi
 }
 
 extern "C" hocResult_t hoc_ep_route_grad(int tokens, int experts, int topk, const void* logits, hocDataType_t dtype,
-                                         size_t ldl, int score, int renormalise, float scale, const int32_t* ids,
+                                         size_t ldl, int score, int renormalise, const float* scale, const int32_t* ids,
                                          const float* dgate, void* dlogits, size_t ldd, void* stream) {
   const char* who = "hoc_ep_route_grad";
   const char* bad = bad_route(tokens, experts, topk, logits, dtype, ldl, score, scale);
@@ -546,7 +546,7 @@ extern "C" hocResult_t hoc_ep_route_grad(int tokens, int experts, int topk, cons
   const size_t b = bytes_of(dtype);
   const RouteGradArgs A{logits, ids, dgate, dlogits, int64_t(ldl), int64_t(ldd), tokens, experts, topk, epl,
                         score == HOC_SCORE_SOFTMAX, renormalise != 0, access_of(logits, ldl, experts, epl, b),
-                        access_of(dlogits, ldd, experts, epl, b), scale};
+                        access_of(dlogits, ldd, experts, epl, b), *scale};
   const dim3 grid(route_grid(tokens)), cta(kRouteWarps * 32);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launched(who, dtype == HOC_FLOAT32 ? launch(HOC_ROUTE_PICK(route_grad_kernel, float, experts), grid, cta, 0, s, A)

@@ -158,18 +158,18 @@ _SIGS["hoc_grad_clip"] = (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_float)
                                     C.c_void_p])
 _ROWS = [C.c_void_p, C.c_size_t]  # rows and their stride
 _SIGS["hoc_wire8_row"] = (C.c_int, [C.c_int, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)])
-_SIGS["hoc_rms_norm"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 2 * _ROWS + [C.c_void_p, C.c_int, C.c_float] + 2 * _ROWS
+_SIGS["hoc_rms_norm"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 2 * _ROWS + [C.c_void_p, C.c_int, C.POINTER(C.c_float)] + 2 * _ROWS
                          + [C.c_void_p, C.c_void_p])
 _SIGS["hoc_rms_norm_workspace"] = (C.c_int, [C.c_int, C.c_int, C.POINTER(C.c_size_t)])
-_SIGS["hoc_rms_norm_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 3 * _ROWS + [C.c_void_p, C.c_int, C.c_float]
+_SIGS["hoc_rms_norm_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 3 * _ROWS + [C.c_void_p, C.c_int, C.POINTER(C.c_float)]
                               + 2 * _ROWS + [C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p])
 _SIGS["hoc_expert_widen"] = (C.c_int, [C.POINTER(_RowGroups), C.POINTER(C.c_void_p), C.c_int, C.POINTER(C.c_void_p),
                                        C.c_void_p])
 _SIGS["hoc_ep_route"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_size_t, C.c_int, C.c_void_p,
-                                   C.c_int, C.c_int, C.c_int, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p])
+                                   C.c_int, C.c_int, C.c_int, C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_void_p])
 _SIGS["hoc_ep_route_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_size_t, C.c_int, C.c_int,
-                                        C.c_float, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p])
-_SIGS["hoc_dropout"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 2 * _ROWS + [C.c_double, C.c_void_p] + _ROWS + [C.c_void_p])
+                                        C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["hoc_dropout"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 2 * _ROWS + [C.POINTER(C.c_double), C.c_void_p] + _ROWS + [C.c_void_p])
 _SIGS["hoc_allreduce_host"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.c_size_t,
                                          C.c_int, C.c_int, C.c_void_p])
 _SIGS["hoc_proxy_status"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64), C.POINTER(C.c_uint64),
@@ -1007,7 +1007,7 @@ def rms_norm(x, weight, y=None, *, eps: float, residual=None, h=None, wire=None,
     yp, ldy = _rows_of(y, shape, x.dtype, dev, "y")
     wdt = _row_dtype(weight, "weight")
     _check(lib().hoc_rms_norm(rows, width, dt, xp, ldx, rp, ldr, _flat(weight, width, weight.dtype, dev, "weight"), wdt,
-                              eps, hp, ldh, yp, ldy, _wire_rows(wire, rows, width, dev, "wire"), _stream(stream)),
+                              C.byref(C.c_float(eps)), hp, ldh, yp, ldy, _wire_rows(wire, rows, width, dev, "wire"), _stream(stream)),
            "hoc_rms_norm")
 
 
@@ -1042,7 +1042,7 @@ def rms_norm_grad(dy, h, weight, dx, *, eps: float, dy2=None, dres=None, dw=None
         ints = workspace.numel()
         wsp = _flat(workspace, ints, _dt("int32"), dev, "workspace")
     _check(lib().hoc_rms_norm_grad(rows, width, dt, dyp, lddy, dy2p, lddy2, hp, ldh,
-                                   _flat(weight, width, weight.dtype, dev, "weight"), wdt, eps, drp, lddr, dxp, lddx,
+                                   _flat(weight, width, weight.dtype, dev, "weight"), wdt, C.byref(C.c_float(eps)), drp, lddr, dxp, lddx,
                                    None if dw is None else _flat(dw, width, dw.dtype, dev, "dw"), dwdt,
                                    int(bool(accumulate)), wsp, ints, _stream(stream)), "hoc_rms_norm_grad")
 
@@ -1093,7 +1093,7 @@ def ep_route(logits, ids, gate, *, score: str = "softmax", bias=None, groups: in
     tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, gate, "gate")
     _check(lib().hoc_ep_route(tokens, experts, topk, lp, dt, ldl, _score(score),
                               _flat(bias, experts, _dt("float32"), dev, "bias"), groups,
-                              groups if top_groups is None else top_groups, int(bool(renormalise)), scale, ip, gp,
+                              groups if top_groups is None else top_groups, int(bool(renormalise)), C.byref(C.c_float(scale)), ip, gp,
                               _stream(stream)), "hoc_ep_route")
 
 
@@ -1102,7 +1102,7 @@ def ep_route_grad(logits, ids, dgate, dlogits, *, score: str = "softmax", renorm
     """Gradient of ep_route for the logits, from dgate for the gates; dlogits may be logits (see include/hoc_block.h)."""
     tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, dgate, "dgate")
     dp, ldd = _rows_of(dlogits, logits.shape, logits.dtype, dev, "dlogits")
-    _check(lib().hoc_ep_route_grad(tokens, experts, topk, lp, dt, ldl, _score(score), int(bool(renormalise)), scale, ip, gp,
+    _check(lib().hoc_ep_route_grad(tokens, experts, topk, lp, dt, ldl, _score(score), int(bool(renormalise)), C.byref(C.c_float(scale)), ip, gp,
                                    dp, ldd, _stream(stream)), "hoc_ep_route_grad")
 
 
@@ -1127,7 +1127,7 @@ def dropout(x, y, p: float, seed, *, residual=None, stream=None):
     xp, ldx = _rows_of(x, shape, x.dtype, dev, "x")
     yp, ldy = _rows_of(y, shape, x.dtype, dev, "y")
     rp, ldr = _rows_of(residual, shape, x.dtype, dev, "residual")
-    _check(lib().hoc_dropout(shape[0], shape[1], dt, xp, ldx, rp, ldr, p, _flat(seed, 2, _dt("int64"), dev, "seed"), yp,
+    _check(lib().hoc_dropout(shape[0], shape[1], dt, xp, ldx, rp, ldr, C.byref(C.c_double(p)), _flat(seed, 2, _dt("int64"), dev, "seed"), yp,
                              ldy, _stream(stream)), "hoc_dropout")
 
 

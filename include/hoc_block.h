@@ -12,6 +12,7 @@
  *   - Everything is stream-ordered, never waits on the host, allocates nothing
  *     and may be captured into a CUDA graph.  Results are the same bits every
  *     time.  Pointers belong to the current device.
+ *   - eps, scale and p point to one host number each, read during the call.
  *   - Any alignment to the element is taken; rows that start on 16-byte boundaries
  *     (and are whole 16-byte vectors) run faster.
  *   - Inputs must not overlap outputs, except as stated.  rows == 0 or
@@ -56,7 +57,7 @@ hocResult_t hoc_wire8_row(int width, size_t* bytes, size_t* scales_at);
  * mean square overflows gives zeros.  h may be x or residual, and y may be x or,
  * where h is not stored there, residual, each with the same row stride. */
 hocResult_t hoc_rms_norm(int rows, int width, hocDataType_t dtype, const void* x, size_t ldx, const void* residual,
-                         size_t ldr, const void* weight, hocDataType_t weight_dtype, float eps, void* h, size_t ldh,
+                         size_t ldr, const void* weight, hocDataType_t weight_dtype, const float* eps, void* h, size_t ldh,
                          void* y, size_t ldy, void* wire, void* stream);
 
 /* int32 entries of the workspace hoc_rms_norm_grad needs where dw is wanted.  It
@@ -75,7 +76,7 @@ hocResult_t hoc_rms_norm_workspace(int rows, int width, size_t* ints);
  * row stride. */
 hocResult_t hoc_rms_norm_grad(int rows, int width, hocDataType_t dtype, const void* dy, size_t lddy, const void* dy2,
                               size_t lddy2, const void* h, size_t ldh, const void* weight, hocDataType_t weight_dtype,
-                              float eps, const void* dres, size_t lddres, void* dx, size_t lddx, void* dw,
+                              const float* eps, const void* dres, size_t lddres, void* dx, size_t lddx, void* dw,
                               hocDataType_t dw_dtype, int accumulate, int32_t* workspace, size_t workspace_ints,
                               void* stream);
 
@@ -108,7 +109,7 @@ typedef enum { HOC_SCORE_SOFTMAX = 0, HOC_SCORE_SIGMOID = 1 } hocScore_t;
  * than topk are left, the last slots get id -1, which a dispatch drops, and gate 0.  A
  * logit of +inf takes a softmax's whole, several of them equal parts. */
 hocResult_t hoc_ep_route(int tokens, int experts, int topk, const void* logits, hocDataType_t dtype, size_t ldl,
-                         int score, const float* bias, int groups, int top_groups, int renormalise, float scale,
+                         int score, const float* bias, int groups, int top_groups, int renormalise, const float* scale,
                          int32_t* ids, float* gate, void* stream);
 
 /* Gradient for the logits, [tokens, experts] of dtype with row stride ldd, where
@@ -117,7 +118,7 @@ hocResult_t hoc_ep_route(int tokens, int experts, int topk, const void* logits, 
  * whose id is outside [0, experts), or that of a masked expert, add nothing; masked
  * logits get 0.  dlogits may be logits, with the same row stride. */
 hocResult_t hoc_ep_route_grad(int tokens, int experts, int topk, const void* logits, hocDataType_t dtype, size_t ldl,
-                              int score, int renormalise, float scale, const int32_t* ids, const float* dgate,
+                              int score, int renormalise, const float* scale, const int32_t* ids, const float* dgate,
                               void* dlogits, size_t ldd, void* stream);
 
 /* y = residual + x * 65536 / (65536 - t) where the element is kept, residual (NULL:
@@ -132,7 +133,7 @@ hocResult_t hoc_ep_route_grad(int tokens, int experts, int topk, const void* log
  * seed[1] is changed).  The gradient is the same call on the gradient, without a
  * residual.  y may be x or residual, with the same row stride.  p == 0 draws nothing. */
 hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, const void* x, size_t ldx, const void* residual,
-                        size_t ldr, double p, const int64_t* seed, void* y, size_t ldy, void* stream);
+                        size_t ldr, const double* p, const int64_t* seed, void* y, size_t ldy, void* stream);
 
 #ifdef __cplusplus
 }

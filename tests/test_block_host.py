@@ -11,17 +11,27 @@ from tests import block_ref
 
 P = 4096  # a non-NULL, aligned address that no refused call may follow
 BAD = hoc.ERR_INVALID_ARG
+
+
+def f32(v):
+    return None if v is None else C.byref(C.c_float(v))
+
+
+def f64(v):
+    return None if v is None else C.byref(C.c_double(v))
+
+
 F32, BF = hoc.FLOAT32, hoc.BFLOAT16
 
 
 def norm(rows=4, width=64, dt=BF, x=P, ldx=64, r=None, ldr=64, w=P, wdt=BF, eps=1e-6, h=None, ldh=64, y=P, ldy=64, wire=None):
-    return hoc.lib().hoc_rms_norm(rows, width, dt, x, ldx, r, ldr, w, wdt, eps, h, ldh, y, ldy, wire, None)
+    return hoc.lib().hoc_rms_norm(rows, width, dt, x, ldx, r, ldr, w, wdt, f32(eps), h, ldh, y, ldy, wire, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(rows=-1), dict(width=0), dict(width=32769, ldx=40000, ldy=40000), dict(dt=hoc.INT32), dict(wdt=hoc.UINT8),
     dict(x=None), dict(x=P + 1), dict(dt=F32, x=P + 2), dict(ldx=63), dict(r=P, ldr=8), dict(r=P + 1), dict(w=None),
-    dict(w=P + 1), dict(wdt=F32, w=P + 2), dict(eps=-1.0), dict(eps=float("nan")), dict(h=P), dict(r=P, h=P, ldh=3),
+    dict(w=P + 1), dict(wdt=F32, w=P + 2), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=None), dict(h=P), dict(r=P, h=P, ldh=3),
     dict(y=None), dict(ldy=1), dict(wire=P + 8), dict(ldx=2 ** 60),
 ])
 def test_norm_refuses(bad):
@@ -31,7 +41,7 @@ def test_norm_refuses(bad):
 
 def grad(rows=4, width=64, dt=BF, dy=P, lddy=64, dy2=None, lddy2=64, h=P, ldh=64, w=P, wdt=BF, eps=1e-6, dres=None, lddres=64,
          dx=P, lddx=64, dw=P, dwdt=F32, ws=P, ints=4 * 64):
-    return hoc.lib().hoc_rms_norm_grad(rows, width, dt, dy, lddy, dy2, lddy2, h, ldh, w, wdt, eps, dres, lddres, dx, lddx, dw,
+    return hoc.lib().hoc_rms_norm_grad(rows, width, dt, dy, lddy, dy2, lddy2, h, ldh, w, wdt, f32(eps), dres, lddres, dx, lddx, dw,
                                        dwdt, 0, ws, ints, None)
 
 
@@ -48,8 +58,8 @@ def test_norm_gradient_refuses(bad):
 def test_calls_on_no_rows_do_nothing():
     assert norm(rows=0, x=None, y=P) == hoc.SUCCESS
     assert grad(rows=0, dy=None, h=None, dx=None, dw=None, ws=None, ints=0) == hoc.SUCCESS
-    assert hoc.lib().hoc_dropout(0, 8, BF, None, 8, None, 0, 0.5, P, None, 8, None) == hoc.SUCCESS
-    assert hoc.lib().hoc_dropout(8, 0, BF, None, 0, None, 0, 0.5, P, None, 0, None) == hoc.SUCCESS
+    assert hoc.lib().hoc_dropout(0, 8, BF, None, 8, None, 0, f64(0.5), P, None, 8, None) == hoc.SUCCESS
+    assert hoc.lib().hoc_dropout(8, 0, BF, None, 0, None, 0, f64(0.5), P, None, 0, None) == hoc.SUCCESS
     assert route(tokens=0, logits=None, ids=None, gate=None) == hoc.SUCCESS
     assert widen(cap=(0,), wire=(None,), y=(None,)) == hoc.SUCCESS
 
@@ -69,14 +79,14 @@ def test_widen_refuses(bad):
 
 def route(tokens=4, experts=64, topk=6, logits=P, dt=BF, ld=64, score=0, bias=None, groups=1, top=1, renorm=0, scale=1.0, ids=P,
           gate=P):
-    return hoc.lib().hoc_ep_route(tokens, experts, topk, logits, dt, ld, score, bias, groups, top, renorm, scale, ids, gate, None)
+    return hoc.lib().hoc_ep_route(tokens, experts, topk, logits, dt, ld, score, bias, groups, top, renorm, f32(scale), ids, gate, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(tokens=-1), dict(experts=0), dict(experts=1025, ld=1025), dict(topk=0), dict(topk=65), dict(topk=32), dict(logits=None),
     dict(logits=P + 1), dict(dt=hoc.INT32), dict(ld=63), dict(score=2), dict(score=-1), dict(bias=P + 2), dict(groups=0),
     dict(groups=7), dict(groups=64, top=64), dict(groups=8, top=0), dict(groups=8, top=9), dict(groups=16, top=1),
-    dict(scale=float("nan")), dict(scale=float("inf")), dict(ids=None), dict(gate=None), dict(ids=P + 2),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=None), dict(ids=None), dict(gate=None), dict(ids=P + 2),
 ])
 def test_route_refuses(bad):
     assert route(**bad) == BAD
@@ -91,17 +101,17 @@ def test_route_gradient_refuses(bad):
     a = dict(tokens=4, experts=64, topk=6, logits=P, dt=BF, ld=64, score=0, renorm=0, scale=1.0, ids=P, dgate=P, out=P, ldd=64)
     a.update(bad)
     assert hoc.lib().hoc_ep_route_grad(a["tokens"], a["experts"], a["topk"], a["logits"], a["dt"], a["ld"], a["score"], a["renorm"],
-                                       a["scale"], a["ids"], a["dgate"], a["out"], a["ldd"], None) == BAD
+                                       f32(a["scale"]), a["ids"], a["dgate"], a["out"], a["ldd"], None) == BAD
 
 
 @pytest.mark.parametrize("bad", [
     dict(rows=-1), dict(width=-1), dict(dt=hoc.INT32), dict(x=None), dict(x=P + 1), dict(ldx=7), dict(r=P + 1), dict(r=P, ldr=1),
-    dict(p=-0.1), dict(p=1.0), dict(p=float("nan")), dict(seed=None), dict(seed=P + 4), dict(y=None), dict(ldy=7),
+    dict(p=-0.1), dict(p=1.0), dict(p=float("nan")), dict(p=None), dict(seed=None), dict(seed=P + 4), dict(y=None), dict(ldy=7),
 ])
 def test_dropout_refuses(bad):
     a = dict(rows=4, width=8, dt=BF, x=P, ldx=8, r=None, ldr=0, p=0.5, seed=P, y=P, ldy=8)
     a.update(bad)
-    assert hoc.lib().hoc_dropout(a["rows"], a["width"], a["dt"], a["x"], a["ldx"], a["r"], a["ldr"], a["p"], a["seed"], a["y"],
+    assert hoc.lib().hoc_dropout(a["rows"], a["width"], a["dt"], a["x"], a["ldx"], a["r"], a["ldr"], f64(a["p"]), a["seed"], a["y"],
                                  a["ldy"], None) == BAD
 
 
