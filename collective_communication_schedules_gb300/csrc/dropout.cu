@@ -34,9 +34,12 @@ __device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
 
 constexpr int kDropThreads = 256, kDropAhead = 2;
 
-// A thread takes kDropAhead groups of eight elements.  VEC: rows are whole groups on
-// 16-byte boundaries.
-template <class T, bool VEC>
+// How rows lie: one after the other, so that they are one run of whole groups; in rows of whole
+// groups; or anyhow.  The first two start on 16-byte boundaries.
+enum Lie { kRun, kRows, kAnyhow };
+
+// A thread takes kDropAhead groups of eight elements.
+template <class T, int LIE, bool RES>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropArgs A) {
   after_the_last();
   constexpr int N = 16 / sizeof(T), Q = 8 / N;
@@ -45,18 +48,19 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
   const uint64_t key = A.t ? uint64_t(A.seed[0]) : 0, call = A.t ? uint64_t(A.seed[1]) : 0;
   const int64_t first = int64_t(blockIdx.x) * kDropThreads * kDropAhead + threadIdx.x;
   const int64_t groups = (A.total + 7) / 8;
+  const uint32_t t = A.t << 16;
   Vec<T, N> v[kDropAhead][Q], w[kDropAhead][Q];
-  int64_t row[kDropAhead], col[kDropAhead];
+  int64_t row[kDropAhead] = {}, col[kDropAhead];
 #pragma unroll
   for (int u = 0; u < kDropAhead; ++u) {
     const int64_t i = (first + u * kDropThreads) * 8;
-    row[u] = A.width >= A.total ? 0 : i < (int64_t(1) << 32) ? int64_t(unsigned(i) / unsigned(A.width)) : i / A.width;
-    col[u] = i - row[u] * A.width;
-    if (VEC && i < A.total) {
+    if (LIE != kRun) row[u] = i < (int64_t(1) << 32) ? int64_t(unsigned(i) / unsigned(A.width)) : i / A.width;
+    col[u] = LIE == kRun ? i : i - row[u] * A.width;
+    if (LIE != kAnyhow && i < A.total) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        v[u][q] = *reinterpret_cast<const Vec<T, N>*>(x + row[u] * A.ldx + col[u] + q * N);
-        if (r) w[u][q] = *reinterpret_cast<const Vec<T, N>*>(r + row[u] * A.ldr + col[u] + q * N);
+        v[u][q] = *reinterpret_cast<const Vec<T, N>*>(x + (LIE == kRun ? 0 : row[u] * A.ldx) + col[u] + q * N);
+        if (RES) w[u][q] = *reinterpret_cast<const Vec<T, N>*>(r + (LIE == kRun ? 0 : row[u] * A.ldr) + col[u] + q * N);
       }
     }
   }
@@ -70,25 +74,24 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
                              uint32_t(key), uint32_t(key >> 32));
       bits[0] = c.x, bits[1] = c.y, bits[2] = c.z, bits[3] = c.w;
     }
-    auto result = [&](int e, T xv, T rv) {
-      const unsigned b = e & 1 ? bits[e >> 1] >> 16 : bits[e >> 1] & 0xFFFFu;
-      const float f = b >= A.t ? widen(xv) * A.keep : 0.f;
-      return narrow<T>(r ? widen(rv) + f : f);
+    auto result = [&](int e, T xv, T rv) {  // (the other half of the word does not change how its upper half compares)
+      const float f = (e & 1 ? bits[e >> 1] : bits[e >> 1] << 16) >= t ? widen(xv) : 0.f;
+      return narrow<T>(RES ? fmaf(f, A.keep, widen(rv)) : f * A.keep);
     };
-    if (VEC) {
+    if (LIE != kAnyhow) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         Vec<T, N> o;
 #pragma unroll
         for (int e = 0; e < N; ++e) o.v[e] = result(q * N + e, v[u][q].v[e], w[u][q].v[e]);
-        *reinterpret_cast<Vec<T, N>*>(y + row[u] * A.ldy + col[u] + q * N) = o;
+        *reinterpret_cast<Vec<T, N>*>(y + (LIE == kRun ? 0 : row[u] * A.ldy) + col[u] + q * N) = o;
       }
     } else {
       int64_t at = row[u], c = col[u];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (g * 8 + e >= A.total) break;
-        y[at * A.ldy + c] = result(e, x[at * A.ldx + c], r ? r[at * A.ldr + c] : narrow<T>(0.f));
+        y[at * A.ldy + c] = result(e, x[at * A.ldx + c], RES ? r[at * A.ldr + c] : narrow<T>(0.f));
         if (++c == A.width) {
           c = 0;
           ++at;
@@ -98,18 +101,23 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
   }
 }
 
+template <class T>
+void (*drop_pick(int lie, bool res))(DropArgs) {
+  if (lie == kRun) return res ? dropout_kernel<T, kRun, true> : dropout_kernel<T, kRun, false>;
+  if (lie == kRows) return res ? dropout_kernel<T, kRows, true> : dropout_kernel<T, kRows, false>;
+  return res ? dropout_kernel<T, kAnyhow, true> : dropout_kernel<T, kAnyhow, false>;
+}
+
 }  // namespace
 
 cudaError_t dropout_preload() {
-  const void* fns[] = {reinterpret_cast<const void*>(&dropout_kernel<float, true>),
-                       reinterpret_cast<const void*>(&dropout_kernel<float, false>),
-                       reinterpret_cast<const void*>(&dropout_kernel<__nv_bfloat16, true>),
-                       reinterpret_cast<const void*>(&dropout_kernel<__nv_bfloat16, false>)};
-  for (const void* f : fns) {
-    cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, f);
-    if (e != cudaSuccess) return e;
-  }
+  for (int lie : {kRun, kRows, kAnyhow})
+    for (bool res : {false, true})
+      for (auto kernel : {drop_pick<float>(lie, res), drop_pick<__nv_bfloat16>(lie, res)}) {
+        cudaFuncAttributes a;
+        const cudaError_t e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kernel));
+        if (e != cudaSuccess) return e;
+      }
   return cudaSuccess;
 }
 
@@ -139,8 +147,10 @@ extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, con
                    65536.f / float(65536 - t)};
   const int64_t ctas = ((total + 7) / 8 + kDropThreads * kDropAhead - 1) / (kDropThreads * kDropAhead);
   if (ctas > 0x7FFFFFFF) return refuse(who, "more than 2^43 elements");
-  const bool vec = width % 8 == 0 && vector_rows(x, ldx, b) && (!residual || vector_rows(residual, ldr, b)) && vector_rows(y, ldy, b);
-  const auto kernel = dtype == HOC_FLOAT32 ? vec ? dropout_kernel<float, true> : dropout_kernel<float, false>
-                                           : vec ? dropout_kernel<__nv_bfloat16, true> : dropout_kernel<__nv_bfloat16, false>;
+  const bool vec = vector_rows(x, ldx, b) && (!residual || vector_rows(residual, ldr, b)) && vector_rows(y, ldy, b);
+  const bool together = rows == 1 || (ldx == size_t(width) && ldy == size_t(width) && (!residual || ldr == size_t(width)));
+  const bool starts = aligned(x, 16) && aligned(residual, 16) && aligned(y, 16);
+  const int lie = starts && together && total % 8 == 0 ? kRun : vec && width % 8 == 0 ? kRows : kAnyhow;
+  const auto kernel = dtype == HOC_FLOAT32 ? drop_pick<float>(lie, residual) : drop_pick<__nv_bfloat16>(lie, residual);
   return launched(who, launch(kernel, dim3(unsigned(ctas)), dim3(kDropThreads), 0, static_cast<cudaStream_t>(stream), A));
 }

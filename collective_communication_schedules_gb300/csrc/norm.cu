@@ -6,6 +6,8 @@
 // row takes width / (V * values of a vector) threads, a warp or a CTA of its own.
 // Rows that are not whole vectors are held element by element, four of a group of 128
 // columns to a lane.
+#include <atomic>
+
 #include <cuda_fp8.h>
 
 #include "block.h"
@@ -218,108 +220,156 @@ struct NormGradArgs {
   int w32;
 };
 
-// The sums of two values over the row's threads (sh: an entry per warp for each).
-__device__ __forceinline__ float2 row_sum2(float a, float b, float2* sh) {
+// The sums of two values over the row's threads.  Both go through one tree: the lower half
+// of a warp adds up the first, the upper the second.  sh: [2][16], an entry per warp for each,
+// 0 for the warps there are none of.
+__device__ __forceinline__ float2 row_sum2(float a, float b, float* sh) {
+  const int lane = threadIdx.x & 31;
+  const bool low = lane < 16;
+  float v = (low ? a : b) + __shfl_xor_sync(kAll, low ? b : a, 16);
 #pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    a += __shfl_xor_sync(kAll, a, off);
-    b += __shfl_xor_sync(kAll, b, off);
-  }
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
+  for (int off = 8; off; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  if ((lane & 15) == 0) sh[lane + (threadIdx.x >> 5)] = v;
   __syncthreads();
-  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  float2 v = lane < warps ? sh[lane] : make_float2(0.f, 0.f);
+  v = sh[lane];
 #pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    v.x += __shfl_xor_sync(kAll, v.x, off);
-    v.y += __shfl_xor_sync(kAll, v.y, off);
-  }
-  return v;
+  for (int off = 8; off; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  const float w = __shfl_xor_sync(kAll, v, 16);
+  return low ? make_float2(v, w) : make_float2(w, v);
 }
 
+// A thread's part of a row: dy + dy2 and h widened, dres as it came.
 template <class T, int V>
 struct GradRow {
-  Vec<T, 16 / sizeof(T)> dy[V], dy2[V], h[V], dres[V];
+  static constexpr int N = 16 / sizeof(T);
+  float d[V][N], h[V][N];
+  Vec<T, N> dres[V];
 };
 
-template <class T, int V>
-__device__ __forceinline__ void load_row(const NormGradArgs& A, int64_t row, GradRow<T, V>& R) {
-  constexpr int N = 16 / sizeof(T);
-  using Q = Vec<T, N>;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = (j * int(blockDim.x) + int(threadIdx.x)) * N;
-    if (c >= A.width) continue;
-    R.dy[j] = *reinterpret_cast<const Q*>(static_cast<const T*>(A.dy) + row * A.lddy + c);
-    R.h[j] = *reinterpret_cast<const Q*>(static_cast<const T*>(A.h) + row * A.ldh + c);
-    if (A.dy2) R.dy2[j] = *reinterpret_cast<const Q*>(static_cast<const T*>(A.dy2) + row * A.lddy2 + c);
-    if (A.dres) R.dres[j] = *reinterpret_cast<const Q*>(static_cast<const T*>(A.dres) + row * A.lddres + c);
-  }
+__device__ __forceinline__ void copy_ahead(void* to, const void* from) {  // 16 bytes, past L1
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(to))), "l"(from) : "memory");
 }
 
 // A CTA takes the rows blockIdx.x, + gridDim.x, ..; a thread has the same columns of
-// each, so that it sums the weight gradient over them in registers.  The next row is
-// on its way while this one is worked on.
-template <class T, int V>
+// each, so that it sums the weight gradient over them in registers.  With S > 0 the next S - 1
+// rows are on their way into shared memory while one is worked on: a thread fetches
+// what it reads itself, so that nothing but its own copies has to be waited for.
+template <class T, int V, int S>
 __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const __grid_constant__ NormGradArgs A) {
   constexpr int N = 16 / sizeof(T);
-  __shared__ float2 sh[2][kGradThreads / 32];
+  using Q = Vec<T, N>;
+  extern __shared__ uint4 ring[];  // [S][arrays][V][threads]
+  __shared__ float sh[2][32];
+  if (threadIdx.x < 64) sh[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+  if (blockDim.x < 64) sh[1][threadIdx.x] = 0.f;
+  __syncthreads();
   after_the_last();
+  const int threads = blockDim.x, two = A.dy2 != nullptr, arrays = 2 + two + (A.dres != nullptr);
+  auto column = [&](int j) { return (j * threads + int(threadIdx.x)) * N; };
   float w[V][N], acc[V][N];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int c = (j * int(blockDim.x) + int(threadIdx.x)) * N;
 #pragma unroll
     for (int e = 0; e < N; ++e) w[j][e] = acc[j][e] = 0.f;
-    if (c < A.width) load_weights<N>(A.w, A.w32, c, w[j]);
+    if (column(j) < A.width) load_weights<N>(A.w, A.w32, column(j), w[j]);
   }
-  constexpr bool kAhead = V <= 2;  // (more would not fit the registers)
-  GradRow<T, V> next = {};
-  if (kAhead && blockIdx.x < unsigned(A.rows)) load_row(A, blockIdx.x, next);
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
-    if (!kAhead) load_row(A, row, next);
-    const GradRow<T, V> R = next;
-    if (kAhead && row + gridDim.x < A.rows) load_row(A, row + gridDim.x, next);
+  auto at = [&](const void* base, int64_t ld, int64_t row, int j) { return static_cast<const T*>(base) + row * ld + column(j); };
+  auto fetch = [&](int64_t row, int stage) {
+    uint4* to = ring + size_t(stage) * arrays * V * threads + threadIdx.x;
+    if (row < A.rows) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (column(j) >= A.width) continue;
+        copy_ahead(to + j * threads, at(A.dy, A.lddy, row, j));
+        copy_ahead(to + (V + j) * threads, at(A.h, A.ldh, row, j));
+        if (A.dy2) copy_ahead(to + (2 * V + j) * threads, at(A.dy2, A.lddy2, row, j));
+        if (A.dres) copy_ahead(to + ((2 + two) * V + j) * threads, at(A.dres, A.lddres, row, j));
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int64_t row = blockIdx.x;
+  if constexpr (S > 0) {
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) fetch(row + int64_t(i) * gridDim.x, i);
+  }
+  const float inv = 1.f / float(A.width);
+  int turn = 0, stage = 0;
+  for (; row < A.rows; row += gridDim.x, turn ^= 1) {
+    GradRow<T, V> R;
+    Q x[V], y[V], x2[V];
+    if constexpr (S > 0) {
+      fetch(row + int64_t(S - 1) * gridDim.x, stage == 0 ? S - 1 : stage - 1);  // (read a turn ago, by this thread)
+      asm volatile("cp.async.wait_group %0;" ::"n"(S > 0 ? S - 1 : 0) : "memory");
+      const uint4* from = ring + size_t(stage) * arrays * V * threads + threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool in = column(j) < A.width;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const uint4 a = in ? from[j * threads] : zero, b = in ? from[(V + j) * threads] : zero;
+        const uint4 c = in && A.dy2 ? from[(2 * V + j) * threads] : zero;
+        const uint4 d = in && A.dres ? from[((2 + two) * V + j) * threads] : zero;
+        x[j] = *reinterpret_cast<const Q*>(&a);
+        y[j] = *reinterpret_cast<const Q*>(&b);
+        x2[j] = *reinterpret_cast<const Q*>(&c);
+        R.dres[j] = *reinterpret_cast<const Q*>(&d);
+      }
+      stage = stage == S - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        x[j] = y[j] = x2[j] = R.dres[j] = *reinterpret_cast<const Q*>(&zero);
+        if (column(j) >= A.width) continue;
+        x[j] = *reinterpret_cast<const Q*>(at(A.dy, A.lddy, row, j));
+        y[j] = *reinterpret_cast<const Q*>(at(A.h, A.ldh, row, j));
+        if (A.dy2) x2[j] = *reinterpret_cast<const Q*>(at(A.dy2, A.lddy2, row, j));
+        if (A.dres) R.dres[j] = *reinterpret_cast<const Q*>(at(A.dres, A.lddres, row, j));
+      }
+    }
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float h = widen(R.h[j].v[e]);
-        float d = widen(R.dy[j].v[e]);
-        if (A.dy2) d += widen(R.dy2[j].v[e]);
-        a = fmaf(h, h, a);
-        b = fmaf(d * w[j][e], h, b);
+        R.h[j][e] = widen(y[j].v[e]);
+        R.d[j][e] = widen(x[j].v[e]);
       }
-    const float2 t = row_sum2(a, b, sh[turn]);  // (two sets of entries: one barrier a row)
-    const float s = rsqrtf(t.x / float(A.width) + A.eps), k = s * s * (t.y / float(A.width));
+    if (A.dy2) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * int(blockDim.x) + int(threadIdx.x)) * N;
-      if (c >= A.width) continue;
-      Vec<T, N> o;
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int e = 0; e < N; ++e) R.d[j][e] += widen(x2[j].v[e]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float h = widen(R.h[j].v[e]);
-        float d = widen(R.dy[j].v[e]);
-        if (A.dy2) d += widen(R.dy2[j].v[e]);
-        acc[j][e] = fmaf(d, h * s, acc[j][e]);
-        float g = s * (d * w[j][e] - h * k);
-        if (A.dres) g += widen(R.dres[j].v[e]);
-        o.v[e] = narrow<T>(g);
+        a = fmaf(R.h[j][e], R.h[j][e], a);
+        b = fmaf(R.d[j][e] * w[j][e], R.h[j][e], b);
       }
-      *reinterpret_cast<Vec<T, N>*>(static_cast<T*>(A.dx) + row * A.lddx + c) = o;
+    const float2 t = row_sum2(a, b, sh[turn]);  // (two sets of entries: one barrier a row)
+    const float s = rsqrtf(t.x * inv + A.eps), k = -s * s * (t.y * inv);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (column(j) >= A.width) continue;
+      Q o;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float hs = R.h[j][e] * s;
+        acc[j][e] = fmaf(R.d[j][e], hs, acc[j][e]);
+        o.v[e] = narrow<T>(fmaf(s, R.d[j][e] * w[j][e], fmaf(hs, k, widen(R.dres[j].v[e]))));
+      }
+      *reinterpret_cast<Q*>(static_cast<T*>(A.dx) + row * A.lddx + column(j)) = o;
     }
   }
   if (!A.part) return;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int c = (j * int(blockDim.x) + int(threadIdx.x)) * N;
-    if (c >= A.width) continue;
+    if (column(j) >= A.width) continue;
 #pragma unroll
     for (int e = 0; e < N; e += 4)
-      *reinterpret_cast<float4*>(A.part + int64_t(blockIdx.x) * A.width + c + e) =
+      *reinterpret_cast<float4*>(A.part + int64_t(blockIdx.x) * A.width + column(j) + e) =
           make_float4(acc[j][e], acc[j][e + 1], acc[j][e + 2], acc[j][e + 3]);
   }
 }
@@ -329,7 +379,10 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const __grid_co
 template <class T>
 __global__ void __launch_bounds__(kGradThreads) norm_grad_any_kernel(const __grid_constant__ NormGradArgs A) {
   extern __shared__ float acc[];  // [width]; none where the weight gradient is not wanted
-  __shared__ float2 sh[2][kGradThreads / 32];
+  __shared__ float sh[2][32];
+  if (threadIdx.x < 64) sh[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+  if (blockDim.x < 64) sh[1][threadIdx.x] = 0.f;
+  __syncthreads();
   after_the_last();
   const int step = blockDim.x;
   if (A.part)
@@ -400,18 +453,19 @@ struct WidenArgs {
   int64_t cap[kMaxRanks];
   const int64_t* seg;
   int64_t segs;  // entries of one rank
-  int ranks, width;
+  int ranks, width, log;
 };
 
-constexpr int kWidenThreads = 256, kWidenCtas = kSms * 8, kWidenAhead = 4;
+constexpr int kWidenThreads = 256, kWidenCtas = kSms * 8;
+constexpr int kWidenAhead = 2;  // steps a thread has in flight
 
-// E values a step: 16 where rows of y are whole 32 bytes, else 8, else 1.  The rows of
-// all ranks are one run of steps, handed to the threads in turn.
+// A step is E values: 16 where rows of y are whole 32 bytes, else 8, else 1.  2^log neighbouring
+// lanes take a row, as many as it has steps, a warp at most; the rows of all ranks are one run,
+// handed out in turn.
 template <int E>
 __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_constant__ WidenArgs A) {
   __shared__ int64_t ends[kMaxRanks];
   after_the_last();
-  const unsigned per = unsigned(A.width) / E;  // steps of a row
   if (threadIdx.x < 32) {
     int64_t n = 0;
     if (int(threadIdx.x) < A.ranks) {
@@ -422,46 +476,54 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
       const int64_t v = __shfl_up_sync(kAll, n, off);
       if (int(threadIdx.x) >= off) n += v;
     }
-    if (int(threadIdx.x) < kMaxRanks) ends[threadIdx.x] = n * per;
+    if (int(threadIdx.x) < kMaxRanks) ends[threadIdx.x] = n;
   }
   __syncthreads();
   struct alignas(E) In {
     uint8_t v[E];
   };
-  const int64_t total = ends[A.ranks - 1], stride = int64_t(gridDim.x) * kWidenThreads;
-  const int row_bytes = wire_bytes(A.width), at = scales_at(A.width);
+  const int64_t total = ends[A.ranks - 1];
+  const int row_bytes = wire_bytes(A.width), at = scales_at(A.width), span = E << A.log;
+  const int first = (int(threadIdx.x) & ((1 << A.log) - 1)) * E;
   int d = 0;
-  for (int64_t base = int64_t(blockIdx.x) * kWidenThreads + threadIdx.x; base < total; base += stride * kWidenAhead) {
-    In q[kWidenAhead];
-    float scale[kWidenAhead];
-    __nv_bfloat16* to[kWidenAhead];
+  for (int64_t row = (int64_t(blockIdx.x) * kWidenThreads + threadIdx.x) >> A.log; row < total;
+       row += int64_t(gridDim.x) * kWidenThreads >> A.log) {
+    while (row >= ends[d]) ++d;
+    const int64_t k = row - (d ? ends[d - 1] : 0);
+    const uint8_t* from = A.wire[d] + k * row_bytes;
+    __nv_bfloat16* to = A.y[d] + k * A.width;
+    for (int c0 = first; c0 < A.width; c0 += span * kWidenAhead) {
+      In q[kWidenAhead];
+      float scale[kWidenAhead];
 #pragma unroll
-    for (int u = 0; u < kWidenAhead; ++u) {
-      const int64_t i = base + u * stride;
-      to[u] = nullptr;
-      if (i >= total) continue;
-      while (i >= ends[d]) ++d;
-      const int64_t k = i - (d ? ends[d - 1] : 0);
-      const int64_t row = k < (int64_t(1) << 32) ? int64_t(unsigned(k) / per) : k / per;
-      const int c = int(k - row * per) * E;
-      const uint8_t* from = A.wire[d] + row * row_bytes;
-      q[u] = *reinterpret_cast<const In*>(from + c);
-      scale[u] = *reinterpret_cast<const float*>(from + at + c / kGroup * 4);
-      to[u] = A.y[d] + row * A.width + c;
-    }
+      for (int u = 0; u < kWidenAhead; ++u) {
+        const int c = c0 + u * span;
+        if (c >= A.width) continue;
+        q[u] = *reinterpret_cast<const In*>(from + c);
+        scale[u] = *reinterpret_cast<const float*>(from + at + c / kGroup * 4);
+      }
 #pragma unroll
-    for (int u = 0; u < kWidenAhead; ++u) {
-      if (!to[u]) continue;
-      constexpr int M = E < 8 ? E : 8;
+      for (int u = 0; u < kWidenAhead; ++u) {
+        const int c = c0 + u * span;
+        if (c >= A.width) continue;
+        if constexpr (E == 1) {
+          to[c] = __float2bfloat16_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(q[u].v[0], __NV_E4M3))) * scale[u]);
+        } else {
+          uint32_t o[E / 2];
 #pragma unroll
-      for (int b = 0; b < E; b += M) {
-        Vec<__nv_bfloat16, M> o;
-#pragma unroll
-        for (int e = 0; e < M; ++e) {
-          const __half_raw f = __nv_cvt_fp8_to_halfraw(q[u].v[b + e], __NV_E4M3);
-          o.v[e] = __float2bfloat16_rn(__half2float(__half(f)) * scale[u]);
+          for (int e = 0; e < E; e += 2) {
+            const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(q[u].v[e] | q[u].v[e + 1] << 8), __NV_E4M3);
+            const float2 v = __half22float2(__half2(f));
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * scale[u], v.y * scale[u]);
+            o[e / 2] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          if constexpr (E == 16)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c), "r"(o[0]), "r"(o[1]),
+                         "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                         : "memory");
+          else
+            *reinterpret_cast<uint4*>(to + c) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<Vec<__nv_bfloat16, M>*>(to[u] + b) = o;
       }
     }
   }
@@ -496,27 +558,56 @@ cudaError_t start_norm(const NormArgs& A, bool vec, cudaStream_t s) {
 
 constexpr int kMostParts = kSms * 8;
 
-// CTAs of the gradient's kernel.
-int grad_parts(int rows, int threads) {
-  const int most = kSms * (1024 / threads > 8 ? 8 : 1024 / threads < 1 ? 1 : 1024 / threads);
+// CTAs of the gradient's kernel: what is resident at once.
+int grad_parts(int rows, int threads, size_t smem) {
+  int each = int(size_t(220) * 1024 / (smem + 2048)), regs = 640 / threads;  // (up to 100 registers a thread)
+  each = each < regs ? each : regs;
+  const int most = kSms * (each > 8 ? 8 : each < 1 ? 1 : each);
   return rows < most ? rows < 1 ? 1 : rows : most;
+}
+
+// More shared memory than a kernel has without asking (48 KiB, its own variables among them), once
+// per device.
+constexpr size_t kSmemAsIs = 47 * 1024;
+template <class Kernel>
+cudaError_t opt_in(Kernel kernel, size_t smem, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done.load() >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev);
+  return e;
+}
+
+constexpr size_t kMostRing = 200 * 1024;
+
+template <class T, int V, int S>
+cudaError_t launch_grad(const NormGradArgs& A, cudaStream_t s, int* parts) {
+  static std::atomic<uint64_t> done{0};
+  const int threads = row_threads(A.width / int(16 / sizeof(T)), V);
+  const size_t smem = size_t(S) * (2 + (A.dy2 != nullptr) + (A.dres != nullptr)) * V * threads * 16;
+  *parts = grad_parts(A.rows, threads, smem);
+  if (smem > kSmemAsIs) {
+    const cudaError_t e = opt_in(norm_grad_kernel<T, V, S>, kMostRing, done);
+    if (e != cudaSuccess) return e;
+  }
+  return launch(norm_grad_kernel<T, V, S>, dim3(*parts), dim3(threads), smem, s, A);
 }
 
 template <class T>
 cudaError_t start_grad(const NormGradArgs& A, bool vec, cudaStream_t s, int* parts) {
   const int nvec = A.width / int(16 / sizeof(T));
   if (vec && nvec <= 4 * kGradThreads) {
-    const int v = nvec <= kGradThreads ? 1 : nvec <= 2 * kGradThreads ? 2 : 4;
-    const int threads = row_threads(nvec, v);
-    *parts = grad_parts(A.rows, threads);
-    return launch(v == 1 ? norm_grad_kernel<T, 1> : v == 2 ? norm_grad_kernel<T, 2> : norm_grad_kernel<T, 4>,
-                  dim3(*parts), dim3(threads), 0, s, A);
+    if (nvec <= 256) return launch_grad<T, 2, 4>(A, s, parts);
+    if (nvec <= 2 * kGradThreads) return launch_grad<T, 2, 3>(A, s, parts);
+    return launch_grad<T, 4, 0>(A, s, parts);
   }
   const int threads = A.width >= kGradThreads ? kGradThreads : (A.width + 31) / 32 * 32;
-  *parts = grad_parts(A.rows, threads);
   const size_t smem = A.part ? size_t(A.width) * sizeof(float) : 0;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_grad_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  *parts = grad_parts(A.rows, threads, smem);
+  if (smem > kSmemAsIs) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = opt_in(norm_grad_any_kernel<T>, size_t(kMaxWidth) * sizeof(float), done);
     if (e != cudaSuccess) return e;
   }
   return launch(norm_grad_any_kernel<T>, dim3(*parts), dim3(threads), smem, s, A);
@@ -531,8 +622,8 @@ cudaError_t norm_preload() {
       reinterpret_cast<const void*>(&norm_weight_kernel<__nv_bfloat16>),
 #define HOC_NORM_OF(T)                                                                                               \
   reinterpret_cast<const void*>(&norm_any_kernel<T, 1>), reinterpret_cast<const void*>(&norm_any_kernel<T, 8>),      \
-      reinterpret_cast<const void*>(&norm_grad_kernel<T, 1>), reinterpret_cast<const void*>(&norm_grad_kernel<T, 2>), \
-      reinterpret_cast<const void*>(&norm_grad_kernel<T, 4>), reinterpret_cast<const void*>(&norm_grad_any_kernel<T>)
+      reinterpret_cast<const void*>(&norm_grad_kernel<T, 2, 4>), reinterpret_cast<const void*>(&norm_grad_kernel<T, 2, 3>), \
+      reinterpret_cast<const void*>(&norm_grad_kernel<T, 4, 0>), reinterpret_cast<const void*>(&norm_grad_any_kernel<T>)
 #define HOC_NORM_V(T, V)                                                                                           \
   reinterpret_cast<const void*>(&norm_kernel<T, V, false, false>),                                                 \
       reinterpret_cast<const void*>(&norm_kernel<T, V, false, true>),                                              \
@@ -654,7 +745,7 @@ extern "C" hocResult_t hoc_expert_widen(const hocRowGroups_t* G, const void* con
   A.ranks = G->nranks;
   A.width = width;
   size_t most = 0;
-  bool vec = true;
+  bool vec = true, wide = true;
   for (int d = 0; d < G->nranks; ++d) {
     const size_t cap = G->capacity[d];
     if (cap > (size_t(1) << 30)) return refuse(who, "a buffer of more than 2^30 rows");
@@ -664,11 +755,13 @@ extern "C" hocResult_t hoc_expert_widen(const hocRowGroups_t* G, const void* con
     A.y[d] = static_cast<__nv_bfloat16*>(y[d]);
     A.cap[d] = int64_t(cap);
     vec = vec && aligned(y[d], 16);
+    wide = wide && aligned(y[d], 32);
     most += cap;
   }
   if (most == 0) return HOC_SUCCESS;
-  const int e = vec && width % 16 == 0 ? 16 : vec && width % 8 == 0 ? 8 : 1;
-  const size_t want = (most * (width / e) + kWidenThreads - 1) / kWidenThreads;
+  const int e = wide && width % 16 == 0 ? 16 : vec && width % 8 == 0 ? 8 : 1;
+  while (A.log < 5 && (e << A.log) < width) ++A.log;
+  const size_t want = ((most << A.log) + kWidenThreads - 1) / kWidenThreads;
   return launched(who, launch(e == 16 ? widen_kernel<16> : e == 8 ? widen_kernel<8> : widen_kernel<1>,
                               dim3(unsigned(want < size_t(kWidenCtas) ? want : size_t(kWidenCtas))), dim3(kWidenThreads), 0,
                               static_cast<cudaStream_t>(stream), A));

@@ -1,18 +1,23 @@
 // Routing of tokens to experts, and its gradient (hoc_block.h).
 //
-// A warp takes a token.  Lane l holds the logits of the experts l * epl .. (l + 1) *
-// epl - 1, so that the lowest of several lanes with the same key has the lowest expert,
-// and a group of neighbouring experts is a run of lanes.  The topk largest keys are found
-// one after the other: a maximum over each lane's registers, one over the warp
-// (redux.sync), and the lane that had it looks for its next.
+// L neighbouring lanes take a token, so that a warp works on 32 / L of them at a time: what
+// is done once a token and round is bound by instructions, not by bytes.  Lane q of a
+// token holds the logits of the experts q * epl .. (q + 1) * epl - 1, so that the lowest of
+// several lanes with the same key has the lowest expert, and a group of neighbouring
+// experts is a run of lanes.  A lane sorts its keys once, as unsigned numbers whose last bits
+// are the expert's place in the lane; the topk largest are then found one after the other:
+// a maximum over the lanes' first keys, and the lane that had it moves its others up.
 //
-// Which of two near keys is larger is decided as 64-bit arithmetic decides it.  Without a
-// bias and groups the keys are the logits themselves, and there is nothing to round.  Else
-// keys are binary32 with a bound on their error, and a token for which two keys that are
-// compared lie within it (0.1 to 0.5 % of them, for normal logits) is done again in
-// binary64.  Keys with the same logit and the same bias are equal in any arithmetic, so
-// that logits of few bits do not send their tokens there.
+// Which of two near keys is larger is decided as 64-bit arithmetic decides it.  Keys are
+// binary32 without their last bits, with a bound on their error.  Where two neighbours in the
+// order lie within it (0.2 % of the tokens, for normal logits and 256 experts), the keys that may
+// be chosen are worked out again in binary64, a lane each, and ranked; where a group's
+// place is in doubt (0.03 %), or more keys than lanes, the whole token is done again.
+// Keys with the same logit and the same bias are equal in any arithmetic, so that logits
+// of few bits do not send their tokens there.  bf16 logits that are keys themselves have the bits
+// to spare and are exact.
 #include <type_traits>
+#include <utility>
 
 #include "block.h"
 
@@ -31,24 +36,15 @@ struct RouteArgs {
   int32_t* ids;
   float* gate;
   int64_t ld;
-  int tokens, experts, topk, epl, groups, top_groups, softmax, renorm;
-  int vec;  // elements of an access to the logits
+  int tokens, experts, topk, groups, top_groups, softmax, renorm;
+  int epl, vec;            // experts of a lane where L lanes take a token, and elements of an access to the logits
+  int epl_warp, vec_warp;  // the same where a warp does
+  int vec_bias, vec_bias_warp;
   float scale;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
-  return v;
-}
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int off = 16; off; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
+__device__ __forceinline__ float warp_max(float v) {  // (a NaN takes no part)
+  asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
   return v;
 }
 
@@ -56,7 +52,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // Both zeros are one.
 __device__ __forceinline__ uint32_t ordered(float k) {
   const uint32_t b = __float_as_uint(k + 0.f);
-  return k > -INFINITY ? (b >> 31 ? ~b : b | 0x80000000u) : 0u;
+  return k > -INFINITY ? b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u) : 0u;
 }
 __device__ __forceinline__ uint64_t ordered(double k) {
   const uint64_t b = uint64_t(__double_as_longlong(k + 0.0));
@@ -75,16 +71,48 @@ __device__ __forceinline__ uint64_t warp_most(uint64_t v) {
   return uint64_t(hi) << 32 | __reduce_max_sync(kAll, uint32_t(v >> 32) == hi ? uint32_t(v) : 0u);
 }
 
-template <class K>
-struct Bits;
-template <>
-struct Bits<float> {
-  using type = uint32_t;
-};
-template <>
-struct Bits<double> {
-  using type = uint64_t;
-};
+// The L lanes of a token.
+template <int L>
+__device__ __forceinline__ uint32_t most_of(uint32_t v) {
+  if constexpr (L == 32) {
+    return warp_most(v);
+  } else {
+#pragma unroll
+    for (int off = L / 2; off; off >>= 1) v = max(v, __shfl_xor_sync(kAll, v, off));
+    return v;
+  }
+}
+template <int L>
+__device__ __forceinline__ uint64_t most_of(uint64_t v) {
+#pragma unroll
+  for (int off = L / 2; off; off >>= 1) {
+    const uint64_t w = __shfl_xor_sync(kAll, v, off);
+    v = w > v ? w : v;
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float max_of(float v) {  // (a NaN takes no part)
+  if constexpr (L == 32) {
+    return warp_max(v);
+  } else {
+#pragma unroll
+    for (int off = L / 2; off; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
+    return v;
+  }
+}
+template <int L, class K>
+__device__ __forceinline__ K sum_of(K v) {
+#pragma unroll
+  for (int off = L / 2; off; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  return v;
+}
+// The lanes of the token for which `yes` holds, a bit each.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_of(bool yes) {
+  const uint32_t all = __ballot_sync(kAll, yes);
+  return L == 32 ? all : all >> (threadIdx.x & 31 & ~(L - 1)) & ((1u << (L & 31)) - 1);
+}
 
 // Calls by(elements of an access), known when compiling; vec divides a lane's share.
 template <class T, int EPL, class By>
@@ -95,10 +123,10 @@ __device__ __forceinline__ void with_access(int vec, By by) {
   else by(std::integral_constant<int, 1>{});
 }
 
-// A lane's logits; -inf for experts there are none of, and for NaN.
+// The logits of a token's lane q; -inf for experts there are none of, and for NaN.
 template <class T, int EPL>
-__device__ __forceinline__ void load_logits(const T* row, int experts, int epl, int vec, int lane, float (&z)[EPL]) {
-  const int e0 = lane * epl;
+__device__ __forceinline__ void load_logits(const T* row, int experts, int epl, int vec, int q, float (&z)[EPL]) {
+  const int e0 = q * epl;
   auto by = [&](auto step) {
     constexpr int S = decltype(step)::value;
 #pragma unroll
@@ -108,8 +136,7 @@ __device__ __forceinline__ void load_logits(const T* row, int experts, int epl, 
       if (in) v = *reinterpret_cast<const Vec<T, S>*>(row + e0 + i);
 #pragma unroll
       for (int e = 0; e < S; ++e) {
-        const float f = in ? widen(v.v[e]) : -INFINITY;
-        z[i + e] = f == f ? f : -INFINITY;
+        z[i + e] = in ? fmaxf(widen(v.v[e]), -INFINITY) : -INFINITY;  // (of a number and NaN the number)
       }
     }
   };
@@ -124,95 +151,81 @@ __device__ __forceinline__ double share(double z, double most) {
   return z == -double(INFINITY) ? 0.0 : z == most ? 1.0 : exp(z - most);
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
+// For keys: 1 / (1 + 2^(-z log2 e)) by the approximate instructions.
+__device__ __forceinline__ float sigmoid(float z) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504088896341f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(1.f + e));
+  return e;
+}
 __device__ __forceinline__ double sigmoid(double z) { return 1.0 / (1.0 + exp(-z)); }
 
-// Bounds on the error of a binary32 score relative to the largest score of the token.
-// Sigmoid: expf is off by 2 units in the last place at most, 1 + e and the quotient by one
-// each; in all below 4 * 2^-23.  Softmax: z - most is rounded, which changes exp by |z - most| 2^-24
+// Bounds on the error of a binary32 score, relative to the largest score there can be.
+// Sigmoid: its exponent is rounded, which changes s by |z| s (1 - s) 2^-24 < 0.23 * 2^-24, the
+// exponential by 2 units of 2^-23 of itself, s by a quarter of that; 1 + e and the reciprocal by
+// 2^-24 and 2^-23: below 2^-21.  Softmax: z - most is rounded, which changes exp by |z - most| 2^-24
 // of itself, and x exp(-x) < 0.4; expf 2 units; up to 36 additions of the sum, the quotient:
 // below 64 * 2^-23.
 constexpr float kSigmoidError = 0x1p-21f, kSoftmaxError = 0x1p-17f;
 
-// The largest and second largest key of a set (-inf: none).
-template <class K>
+// The largest and second largest key of a set (0: none).
+template <class U>
 struct Two {
-  K a, b;
-  __device__ __forceinline__ void add(K v) {
-    b = v > a ? a : v > b ? v : b;
-    a = v > a ? v : a;
+  U a, b;
+  __device__ __forceinline__ void add(U v) {
+    b = max(b, min(a, v));
+    a = max(a, v);
   }
-  __device__ __forceinline__ void join(K a2, K b2) {
-    b = a2 > a ? (a > b2 ? a : b2) : (a2 > b ? a2 : b);
-    a = a2 > a ? a2 : a;
+  __device__ __forceinline__ void join(U a2, U b2) {
+    b = max(min(a, a2), max(b, b2));
+    a = max(a, a2);
   }
 };
 
-// Which groups are kept (a bit each).  near: whether the least kept and the best left out
-// lie within `tol` and what the sums' own rounding adds.
-template <class K, int EPL>
-__device__ __forceinline__ uint32_t keep_groups(const RouteArgs& A, const typename Bits<K>::type (&u)[EPL], int lane,
-                                                K tol, bool* near) {
-  const int per = A.experts / A.groups, run = per / A.epl;
-  K score = -K(INFINITY), size = 0;
-  if (per % A.epl == 0 && (run & (run - 1)) == 0) {  // a group is `run` lanes, a power of two
-    Two<K> t{-K(INFINITY), -K(INFINITY)};
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (i < A.epl) t.add(value_of(u[i]));
-    for (int off = 1; off < run; off <<= 1) {
-      const K a = __shfl_xor_sync(kAll, t.a, off), b = __shfl_xor_sync(kAll, t.b, off);
-      t.join(a, b);
-    }
-    const int from = lane * run & 31;
-    t.a = __shfl_sync(kAll, t.a, from);
-    t.b = __shfl_sync(kAll, t.b, from);
-    if (lane < A.groups) {
-      score = t.b == -K(INFINITY) ? t.a : t.a + t.b;
-      size = t.b == -K(INFINITY) ? K(0) : fabs(t.a) + fabs(t.b);
-    }
-  } else {
-    for (int g = 0; g < A.groups; ++g) {
-      Two<K> t{-K(INFINITY), -K(INFINITY)};
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = lane * A.epl + i;
-        if (i < A.epl && e >= g * per && e < (g + 1) * per) t.add(value_of(u[i]));
-      }
-      for (int off = 1; off < 32; off <<= 1) {
-        const K a = __shfl_xor_sync(kAll, t.a, off), b = __shfl_xor_sync(kAll, t.b, off);
-        t.join(a, b);
-      }
-      if (lane == g) {
-        score = t.b == -K(INFINITY) ? t.a : t.a + t.b;
-        size = t.b == -K(INFINITY) ? K(0) : fabs(t.a) + fabs(t.b);
-      }
-    }
-  }
-  typename Bits<K>::type mine = ordered(score), last = 0;
+// Which groups are kept, a bit each: the top_groups largest scores, lane g having group g's.
+// *last and *next: the least that is kept and the largest that is not (0: there is none).
+template <int L, class U>
+__device__ __forceinline__ uint32_t keep_groups(int top_groups, U mine, int q, U* last, U* next) {
   uint32_t kept = 0;
-  for (int r = 0; r < A.top_groups; ++r) {
-    const auto most = warp_most(mine);
-    if (most == 0) return kept;
-    last = most;
-    const int winner = __ffs(__ballot_sync(kAll, mine == most)) - 1;
-    kept |= 1u << winner;
-    if (lane == winner) mine = 0;
+  *last = 0;
+  for (int r = 0; r < top_groups; ++r) {
+    const U most = most_of<L>(mine);
+    const int winner = __ffs(lanes_of<L>(mine == most)) - 1;
+    if (most) {
+      *last = most;
+      kept |= 1u << winner;
+    }
+    if (q == winner) mine = 0;
   }
-  const auto next = warp_most(mine);
-  if (near && next) {
-    const float most = warp_max(float(size));  // (finite: a sum of infinite keys has no near neighbour)
-    *near = !(value_of(last) - value_of(next) > K(4) * tol + K(most) * K(0x1p-21f));
-  }
+  *next = most_of<L>(mine);
   return kept;
 }
 
-// Takes the largest key of the warp out of u.  Returns its expert, and the key in *most; -1
-// where there is none left.
+// The two largest keys of every group, at lane g for group g.
+template <int EPL, int L = 32, class U>
+__device__ __forceinline__ Two<U> two_of_groups(int experts, int groups, int epl, int q, const U (&u)[EPL]) {
+  const int per = experts / groups;
+  Two<U> mine{0, 0};
+  for (int g = 0; g < groups; ++g) {
+    Two<U> t{0, 0};
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = q * epl + i;
+      if (i < epl && e >= g * per && e < (g + 1) * per) t.add(u[i]);
+    }
+    for (int off = 1; off < L; off <<= 1) {
+      const U a = __shfl_xor_sync(kAll, t.a, off), b = __shfl_xor_sync(kAll, t.b, off);
+      t.join(a, b);
+    }
+    if (q == g) mine = t;
+  }
+  return mine;
+}
+
+// Takes the largest key of the warp out of u.  Returns its expert; -1 where there is none left.
 template <class U, int EPL>
-__device__ __forceinline__ int pop(U (&u)[EPL], U& best, int epl, int lane, U* most) {
+__device__ __forceinline__ int pop(U (&u)[EPL], U& best, int epl, int lane) {
   const U m = warp_most(best);
-  *most = m;
   if (m == 0) return -1;
   const int winner = __ffs(__ballot_sync(kAll, best == m)) - 1;
   int at = 0;
@@ -233,141 +246,327 @@ __device__ __forceinline__ int pop(U (&u)[EPL], U& best, int epl, int lane, U* m
   return winner * epl + __shfl_sync(kAll, at, winner);
 }
 
-// The token once more in binary64: lane j's slot j.
+// The token once more in binary64, by the whole warp: lane j's slot j.
 template <class T, int EPL>
 __device__ __noinline__ int route_exactly(const RouteArgs& A, const T* row, int lane) {
+  const bool grouped = A.top_groups < A.groups, scored = A.bias || grouped;
+  const int epl = A.epl_warp;
   float z[EPL];
-  load_logits<T, EPL>(row, A.experts, A.epl, A.vec, lane, z);
+  load_logits<T, EPL>(row, A.experts, epl, A.vec_warp, lane, z);
   double most = -INFINITY, sum = 0;
-  if (A.softmax) {
+  if (scored && A.softmax) {
+    float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) most = z[i] > most ? double(z[i]) : most;
-    most = warp_max(float(most));
+    for (int i = 0; i < EPL; ++i) top = fmaxf(top, z[i]);
+    most = warp_max(top);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sum += share(double(z[i]), most);
-    sum = warp_sum(sum);
+    sum = sum_of<32>(sum);
   }
   uint64_t u[EPL], best = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane * A.epl + i;
-    const bool in = i < A.epl && e < A.experts;
-    const double s = A.softmax ? share(double(z[i]), most) / sum : sigmoid(double(z[i]));
-    u[i] = in && z[i] > -INFINITY ? ordered(s + (A.bias ? double(A.bias[e]) : 0.0)) : 0;
+    const int e = lane * epl + i;
+    u[i] = 0;
+    if (i < epl && e < A.experts && z[i] > -INFINITY) {
+      const double k = !scored ? double(z[i]) : A.softmax ? share(double(z[i]), most) / sum : sigmoid(double(z[i]));
+      u[i] = ordered(k + (A.bias ? double(A.bias[e]) : 0.0));
+    }
   }
-  if (A.top_groups < A.groups) {
-    const uint32_t kept = keep_groups<double, EPL>(A, u, lane, 0.0, nullptr);
-    const int per = A.experts / A.groups;
+  if (grouped) {
+    const int per = A.experts / A.groups, run = per / epl;
+    Two<uint64_t> t{0, 0};
+    if (per % epl == 0 && (run & (run - 1)) == 0) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) t.add(u[i]);
+      for (int off = 1; off < run; off <<= 1) {
+        const uint64_t a = __shfl_xor_sync(kAll, t.a, off), b = __shfl_xor_sync(kAll, t.b, off);
+        t.join(a, b);
+      }
+      t.a = __shfl_sync(kAll, t.a, lane * run & 31);
+      t.b = __shfl_sync(kAll, t.b, lane * run & 31);
+    } else {
+      t = two_of_groups<EPL>(A.experts, A.groups, epl, lane, u);
+    }
+    const double score = t.b ? value_of(t.a) + value_of(t.b) : value_of(t.a);
+    uint64_t last, next;
+    const uint32_t kept = keep_groups<32>(A.top_groups, lane < A.groups ? ordered(score) : uint64_t(0), lane, &last, &next);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (i < A.epl && !(kept >> (lane * A.epl + i < A.experts ? (lane * A.epl + i) / per : 0) & 1)) u[i] = 0;
+      if (u[i] && !(kept >> ((lane * epl + i) / per) & 1)) u[i] = 0;
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) best = u[i] > best ? u[i] : best;
   int mine = -1;
   for (int r = 0; r < A.topk; ++r) {
-    uint64_t key;
-    const int id = pop(u, best, A.epl, lane, &key);
+    const int id = pop(u, best, epl, lane);
     if (id < 0) break;
     if (lane == r) mine = id;
   }
   return mine;
 }
 
-template <class T, int EPL>
+// The exchanges of Batcher's odd-even merge sort of N keys, worked out by the compiler (loops
+// that it does not unroll leave the keys in local memory: top-1 of 256 for 32,768 tokens 31.7 us,
+// so 14.2).
+template <int N>
+struct Exchanges {
+  int n = 0;
+  unsigned char a[N * 8] = {}, b[N * 8] = {};
+  constexpr Exchanges() {
+    for (int p = 1; p < N; p <<= 1)
+      for (int k = p; k >= 1; k >>= 1)
+        for (int j = k % p; j + k < N; j += 2 * k)
+          for (int i = 0; i < k && i + j + k < N; ++i)
+            if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+              a[n] = static_cast<unsigned char>(i + j);
+              b[n++] = static_cast<unsigned char>(i + j + k);
+            }
+  }
+};
+
+template <int A, int B, int N>
+__device__ __forceinline__ void exchange(uint32_t (&u)[N]) {
+  const uint32_t a = u[A], b = u[B];
+  u[A] = max(a, b);
+  u[B] = min(a, b);
+}
+
+template <int N, size_t... I>
+__device__ __forceinline__ void sort_keys(uint32_t (&u)[N], std::index_sequence<I...>) {
+  constexpr Exchanges<N> net{};
+  (exchange<net.a[I], net.b[I]>(u), ...);
+}
+
+// Largest first.
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&u)[N]) {
+  constexpr size_t n = Exchanges<N>{}.n;
+  sort_keys<N>(u, std::make_index_sequence<n>{});
+}
+
+// The next of the token's sorted keys: its lane, and the key in *key (0: none is left).  Of
+// keys that are equal but for their places the first lane's.
+template <int EPL, int L>
+__device__ __forceinline__ int pop_sorted(uint32_t (&u)[EPL], int q, uint32_t* key) {
+  const uint32_t head = u[0] ? u[0] | (EPL - 1) : 0u, m = most_of<L>(head);
+  const int winner = __ffs(lanes_of<L>(head == m)) - 1;
+  *key = EPL == 1 ? m : __shfl_sync(kAll, u[0], winner, L);
+  if (q == winner) {
+#pragma unroll
+    for (int i = 0; i + 1 < EPL; ++i) u[i] = u[i + 1];
+    u[EPL - 1] = 0;
+  }
+  return winner;
+}
+
+template <class T, int EPL, int L, bool SOFTMAX>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteArgs A) {
   after_the_last();
-  const int lane = threadIdx.x & 31;
-  const bool scored = A.bias || A.top_groups < A.groups;  // keys are scores, not logits
-  const bool whole = A.softmax && (scored || !A.renorm);  // the softmax's sum is needed
-  float bias[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * A.epl + i;
-    bias[i] = A.bias && i < A.epl && e < A.experts ? A.bias[e] : 0.f;
-  }
-  for (int64_t t = int64_t(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5); t < A.tokens; t += int64_t(gridDim.x) * kRouteWarps) {
-    const T* row = static_cast<const T*>(A.logits) + t * A.ld;
+  constexpr uint32_t kPlaces = EPL - 1;
+  constexpr float kCut = float(EPL) * 0x1p-23f;  // what cutting the places' bits off may change, relative to a key
+  constexpr int kTokens = 32 / L;                // of a warp
+  const int lane = threadIdx.x & 31, q = lane & (L - 1);
+  const bool grouped = A.top_groups < A.groups;
+  const bool scored = A.bias || grouped;                // keys are scores, not logits
+  const bool whole = SOFTMAX && (scored || !A.renorm);  // the softmax's sum is needed
+  const bool check = scored || sizeof(T) == 4;          // keys are not exact
+  const int64_t t0 = (int64_t(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5)) * kTokens;
+  if (t0 >= A.tokens) return;
+  const int64_t t = t0 + lane / L;
+  const bool there = t < A.tokens;
+  const T* row = static_cast<const T*>(A.logits) + (there ? t : t0) * A.ld;
+  uint32_t u[EPL];
+  float most = -INFINITY, sum = 1.f, tol = 0.f;
+  {
     float z[EPL];
-    load_logits<T, EPL>(row, A.experts, A.epl, A.vec, lane, z);
-    float most = -INFINITY, sum = 1.f;
+    load_logits<T, EPL>(row, A.experts, A.epl, A.vec, q, z);
     if (whole) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) most = fmaxf(most, z[i]);
-      most = warp_max(most);
+      most = max_of<L>(most);
       sum = 0.f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) sum += share(z[i], most);
-      sum = warp_sum(sum);  // 0 for a token without experts
+      sum = sum_of<L>(sum);  // 0 for a token without experts
     }
-    uint32_t u[EPL], best = 0;
-    float tol = 0.f;
-    bool near = false;
-    if (!scored) {
+    if (scored) {
+      const float inv = SOFTMAX ? 1.f / sum : 1.f;
+      tol = SOFTMAX ? kSoftmaxError * inv : kSigmoidError;  // (inv: the largest score)
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) u[i] = ordered(z[i]);
+      for (int i = 0; i < EPL; ++i)
+        z[i] = z[i] > -INFINITY ? (SOFTMAX ? share(z[i], most) * inv : sigmoid(z[i])) : -INFINITY;
+      if (A.bias) {
+        float b[EPL];
+        load_logits<float, EPL>(A.bias, A.experts, A.epl, A.vec_bias, q, b);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) z[i] += b[i];  // (-inf for a NaN)
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t b = __float_as_uint(z[i] + 0.f);  // as ordered(), with the place
+      u[i] = z[i] > -INFINITY ? ((b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u)) & ~kPlaces) | (kPlaces - i) : 0u;
+    }
+  }
+  auto is_near = [&](float a, float b) {
+    return !(a - b > 2.f * tol + fmaxf(fabsf(a), fabsf(b)) * (kCut + 0x1p-22f) + 0x1p-140f);
+  };
+  // Expert e's key in 64 bits; the softmax's sum has to be there, which all lanes work out.
+  double sum64 = 0;
+  auto sum_in_64 = [&]() {
+    if (!SOFTMAX || !scored) return;
+    float z[EPL];
+    load_logits<T, EPL>(row, A.experts, A.epl, A.vec, q, z);
+    sum64 = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum64 += share(double(z[i]), double(most));
+    sum64 = sum_of<L>(sum64);
+  };
+  auto key_in_64 = [&](int e) {
+    const double z = widen(row[e]), s = !scored ? z : SOFTMAX ? share(z, double(most)) / sum64 : sigmoid(z);
+    return ordered(s + (A.bias ? double(A.bias[e]) : 0.0));
+  };
+  bool exactly = false;  // the token is done again
+  if (grouped) {
+    const int per = A.experts / A.groups, run = per / A.epl;
+    const bool runs = per % A.epl == 0 && (run & (run - 1)) == 0;  // a group is `run` lanes, a power of two
+    Two<uint32_t> g;
+    if (runs) {
+      sort_keys(u);
+      g = {u[0], EPL > 1 ? u[EPL > 1 ? 1 : 0] : 0u};
+      for (int off = 1; off < run; off <<= 1) {
+        const uint32_t a = __shfl_xor_sync(kAll, g.a, off), b = __shfl_xor_sync(kAll, g.b, off);
+        g.join(a, b);
+      }
+      g.a = __shfl_sync(kAll, g.a, q * run & (L - 1), L);  // to lane g
+      g.b = __shfl_sync(kAll, g.b, q * run & (L - 1), L);
     } else {
-      const float inv = A.softmax ? 1.f / sum : 1.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const float s = A.softmax ? share(z[i], most) * inv : sigmoid(z[i]);
-        u[i] = z[i] > -INFINITY ? ordered(s + bias[i]) : 0u;
-      }
-      tol = A.softmax ? kSoftmaxError * inv : kSigmoidError;  // (inv: the largest score)
-      if (A.top_groups < A.groups) {
-        const uint32_t kept = keep_groups<float, EPL>(A, u, lane, tol, &near);
-        const int per = A.experts / A.groups;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (i < A.epl && !(kept >> (lane * A.epl + i < A.experts ? (lane * A.epl + i) / per : 0) & 1)) u[i] = 0;
-      }
+      g = two_of_groups<EPL, L>(A.experts, A.groups, A.epl, q, u);
     }
+    const float ga = value_of(g.a & ~kPlaces), gb = value_of(g.b & ~kPlaces);
+    const float score = q < A.groups ? g.b ? ga + gb : ga : -INFINITY;
+    const float size = max_of<L>(q < A.groups && g.b ? fabsf(ga) + fabsf(gb) : 0.f);
+    uint32_t last, next;
+    uint32_t kept = keep_groups<L>(A.top_groups, ordered(score), q, &last, &next);
+    const bool near = next && !(value_of(last) - value_of(next) > 4.f * tol + size * (2.f * kCut + 0x1p-21f));
+    if (!runs) {
+      exactly = near;
+    } else if (__any_sync(kAll, near)) {
+      // The group's scores by 64-bit keys: of a lane's three largest, unless a fourth may be among them.
+      sum_in_64();
+      Two<uint64_t> t{0, 0};
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) best = u[i] > best ? u[i] : best;
-    int mine = -1, last = -1;
-    float key = -INFINITY;
-    for (int r = 0; !near && r < A.topk; ++r) {
-      uint32_t m;
-      const int id = pop(u, best, A.epl, lane, &m);
-      if (id < 0) break;
-      const float k = value_of(m);
-      if (lane == r) mine = id;
-      if (scored && r > 0 && !(key - k > 2.f * tol + fmaxf(fabsf(key), fabsf(k)) * 0x1p-22f))
-        near = row[last] != row[id] || (A.bias && A.bias[last] != A.bias[id]);
-      last = id;
+      for (int i = 0; i < (EPL < 3 ? EPL : 3); ++i)
+        if (u[i]) t.add(key_in_64(q * A.epl + int(kPlaces - (u[i] & kPlaces))));
+      constexpr int kFourth = EPL > 3 ? 3 : 0;
+      const bool more = EPL > 3 && u[kFourth] && is_near(value_of(u[EPL > 1 ? 1 : 0] & ~kPlaces), value_of(u[kFourth] & ~kPlaces));
+      for (int off = 1; off < run; off <<= 1) {
+        const uint64_t a = __shfl_xor_sync(kAll, t.a, off), b = __shfl_xor_sync(kAll, t.b, off);
+        t.join(a, b);
+      }
+      t.a = __shfl_sync(kAll, t.a, q * run & (L - 1), L);
+      t.b = __shfl_sync(kAll, t.b, q * run & (L - 1), L);
+      const double sum = t.b ? value_of(t.a) + value_of(t.b) : value_of(t.a);
+      uint64_t last64, next64;
+      const uint32_t kept64 = keep_groups<L>(A.top_groups, q < A.groups ? ordered(sum) : uint64_t(0), q, &last64, &next64);
+      const uint32_t doubt = lanes_of<L>(more);
+      exactly = near && doubt;
+      if (near) kept = kept64;
+    }
+    if (runs) {
+      const bool out = !(kept >> (q / run) & 1);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) u[i] = out ? 0u : u[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (u[i] && !(kept >> ((q * A.epl + i) / per) & 1)) u[i] = 0;
+      sort_keys(u);
+    }
+  } else {
+    sort_keys(u);
+  }
+  uint32_t key = 0;  // lane j: slot j's; slot topk is the first that is left out
+  int mine = -1;
+  const int slots = A.topk + check;
+  for (int r = 0; r < slots; ++r) {
+    uint32_t k;
+    const int from = pop_sorted<EPL, L>(u, q, &k);
+    if (q == r && k) {
       key = k;
+      mine = from * A.epl + int(kPlaces - (k & kPlaces));
     }
-    // and the first that is left out, of those that are not the last one's equals
-    while (scored && !near && __shfl_sync(kAll, mine, A.topk - 1) >= 0) {
-      uint32_t m;
-      const int id = pop(u, best, A.epl, lane, &m);
-      if (id < 0) break;
-      const float k = value_of(m);
-      if (key - k > 2.f * tol + fmaxf(fabsf(key), fabsf(k)) * 0x1p-22f) break;
-      near = row[last] != row[id] || (A.bias && A.bias[last] != A.bias[id]);
-    }
-    if (near) mine = route_exactly<T, EPL>(A, row, lane);
-    const float zc = mine >= 0 ? widen(row[mine]) : -INFINITY;
-    float s = 0.f;
-    if (A.renorm) {
-      const float top = warp_max(zc);
-      if (mine >= 0) {
-        if (A.softmax) {
-          s = share(zc, top);
-        } else {  // sigmoids, all divided by exp of the largest logit where that is below 0
-          const float m = fminf(top, 0.f);
-          s = 1.f / (expf(m) + expf(m - zc));
+  }
+  if (check) {
+    // Keys that are near the one before them; where that holds for the first that is left out,
+    // what follows it is taken too (lanes topk + 1, ..), as far as it is near the last chosen.
+    const float k = value_of(key & ~kPlaces), before = __shfl_up_sync(kAll, k, 1, L);
+    bool by = q > 0 && key && is_near(before, k);
+    if (__any_sync(kAll, by)) {
+      const uint32_t close = lanes_of<L>(by);  // (by all lanes: the rest is a token's own)
+      bool more = !exactly && (close >> A.topk & 1);
+      const float least = __shfl_sync(kAll, k, A.topk - 1, L);
+      for (int r = A.topk + 1; __any_sync(kAll, more); ++r) {
+        uint32_t next;
+        const int from = pop_sorted<EPL, L>(u, q, &next);
+        more = more && next && is_near(least, value_of(next & ~kPlaces));
+        if (more && q == r) {
+          key = next;
+          mine = from * A.epl + int(kPlaces - (next & kPlaces));
+          by = true;
         }
+        exactly = exactly || (more && r >= L);  // more of them than lanes
+        more = more && r < L;
       }
-      const float total = warp_sum(s);
-      s = mine >= 0 ? s / total : 0.f;
-    } else if (mine >= 0) {
-      s = A.softmax ? share(zc, most) / sum : 1.f / (1.f + expf(-zc));
+      // near ones that are not equals: their order by 64-bit keys
+      const int prev = __shfl_up_sync(kAll, mine, 1, L);
+      if (__any_sync(kAll, by && (row[prev] != row[mine] || (A.bias && A.bias[prev] != A.bias[mine])))) {
+        sum_in_64();
+        const uint64_t key64 = mine >= 0 ? key_in_64(mine) : 0;
+        int place = 0;
+        for (int r = 0; r < L; ++r) {
+          const uint64_t other = __shfl_sync(kAll, key64, r, L);
+          const int id = __shfl_sync(kAll, mine, r, L);
+          place += other > key64 || (other == key64 && id < mine && id >= 0);
+        }
+        if (mine < 0) place = L;
+        int sorted = -1;
+        for (int r = 0; r < L; ++r) {
+          const int id = __shfl_sync(kAll, mine, r, L);
+          if (__shfl_sync(kAll, place, r, L) == q) sorted = id;
+        }
+        mine = sorted;
+      }
     }
-    if (lane < A.topk) {
-      A.ids[t * A.topk + lane] = mine;
-      A.gate[t * A.topk + lane] = s * A.scale;
+    for (uint32_t left = __ballot_sync(kAll, exactly && there && q == 0); left; left &= left - 1) {
+      const int first = __ffs(left) - 1;
+      const T* it = static_cast<const T*>(A.logits) + (t0 + first / L) * A.ld;
+      const int id = __shfl_sync(kAll, route_exactly<T, (EPL * L + 31) / 32>(A, it, lane), q);
+      if (lane / L == first / L) mine = id;
     }
+  }
+  if (q >= A.topk) mine = -1;
+  const float zc = mine >= 0 ? widen(row[mine]) : -INFINITY;
+  float s = 0.f;
+  if (A.renorm) {
+    const float top = max_of<L>(zc);
+    if (mine >= 0) {
+      if (SOFTMAX) {
+        s = share(zc, top);
+      } else {  // sigmoids, all divided by exp of the largest logit where that is below 0
+        const float m = fminf(top, 0.f);
+        s = 1.f / (expf(m) + expf(m - zc));
+      }
+    }
+    const float total = sum_of<L>(s);
+    s = mine >= 0 ? s / total : 0.f;
+  } else if (mine >= 0) {
+    s = SOFTMAX ? share(zc, most) / sum : 1.f / (1.f + expf(-zc));
+  }
+  if (there && q < A.topk) {
+    A.ids[t * A.topk + q] = mine;
+    A.gate[t * A.topk + q] = s * A.scale;
   }
 }
 
@@ -378,85 +577,142 @@ struct RouteGradArgs {
   const float* dgate;
   void* out;
   int64_t ld, ldd;
-  int tokens, experts, topk, epl, softmax, renorm;
-  int vec, vec_out;
+  int tokens, experts, topk, renorm;
   float scale;
 };
 
-// A warp a token.  Only a softmax whose gates are not renormalised moves every logit: else
-// the chosen ones are all that is read, and the row is zeros but for them.
-template <class T, int EPL>
+// A slot of a token: its expert, -1 for one that adds nothing; the gradient for its score times
+// scale, and its logit (-inf with -1).
+struct Slot {
+  int id;
+  float dg, z;
+};
+
+template <class T>
+__device__ __forceinline__ Slot slot_of(const RouteGradArgs& A, const T* row, int64_t t, int q, bool there) {
+  Slot s;
+  s.id = there && q < A.topk ? A.ids[t * A.topk + q] : -1;
+  if (s.id >= A.experts || s.id < 0) s.id = -1;
+  s.z = s.id >= 0 ? fmaxf(widen(row[s.id]), -INFINITY) : -INFINITY;
+  s.dg = s.z > -INFINITY ? A.dgate[t * A.topk + q] * A.scale : 0.f;
+  return s;
+}
+
+// An expert that several slots name gets their sum, at the first of them: *same has the
+// lanes of a lane's expert.
+template <int L>
+__device__ __forceinline__ float sum_same(int id, int topk, float v, uint32_t* same) {
+  const int lane = threadIdx.x & 31;
+  *same = __match_any_sync(kAll, id < 0 ? -1 : id + (lane / L) * kMaxExperts);
+  if (__any_sync(kAll, id >= 0 && (*same & (*same - 1)))) {
+    float sum = 0.f;
+    for (int j = 0; j < topk; ++j) {
+      const float w = __shfl_sync(kAll, v, j, L);
+      if (*same >> (lane / L * L + j) & 1) sum += w;
+    }
+    v = sum;
+  }
+  return v;
+}
+
+// Every gate but those of a softmax that is not renormalised depends on the chosen logits alone:
+// they are all that is read, and the row is zeros but for them.  L lanes take a token.
+// Bound by its stores.  S: elements of a store.
+template <class T, int S, int L, bool SOFTMAX>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(const __grid_constant__ RouteGradArgs A) {
   after_the_last();
-  const int lane = threadIdx.x & 31;
-  const bool all = A.softmax && !A.renorm;
-  for (int64_t t = int64_t(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5); t < A.tokens; t += int64_t(gridDim.x) * kRouteWarps) {
-    const T* row = static_cast<const T*>(A.logits) + t * A.ld;
-    T* out = static_cast<T*>(A.out) + t * A.ldd;
-    int id = lane < A.topk ? A.ids[t * A.topk + lane] : -1;
-    if (id >= A.experts) id = -1;
-    float dg = id >= 0 ? A.dgate[t * A.topk + lane] * A.scale : 0.f;
-    float zc = id >= 0 ? widen(row[id]) : -INFINITY;
-    if (zc != zc) zc = -INFINITY;
-    if (zc == -INFINITY) dg = 0.f;
-    float z[EPL], most = -INFINITY, inv = 0.f, dot = 0.f, v = 0.f;
-    if (all) {
-      load_logits<T, EPL>(row, A.experts, A.epl, A.vec, lane, z);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) most = fmaxf(most, z[i]);
-      most = warp_max(most);
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) sum += share(z[i], most);
-      inv = 1.f / warp_sum(sum);
-      const float s = share(zc, most) * inv;
-      dot = warp_sum(zc > -INFINITY ? s * dg : 0.f);
-      v = zc > -INFINITY ? s * dg : 0.f;  // and - s dot, once an expert
-    } else if (A.renorm) {
-      const float top = warp_max(zc), m = fminf(top, 0.f);
-      float s = 0.f, slope = 1.f;
-      if (zc > -INFINITY) {
-        s = A.softmax ? share(zc, top) : 1.f / (expf(m) + expf(m - zc));
-        if (!A.softmax) slope = 1.f / (1.f + expf(zc));  // 1 - sigmoid
-      }
-      const float total = warp_sum(s), p = zc > -INFINITY ? s / total : 0.f;
-      // p_j (dg_j - sum p_i dg_i) as differences, which cancel exactly where the dg are equal
-      float mean = 0.f;
-      const float first = __shfl_sync(kAll, dg, __ffs(__ballot_sync(kAll, zc > -INFINITY) | 0x80000000u) - 1);
-      mean = warp_sum(zc > -INFINITY ? p * (dg - first) : 0.f);
-      v = zc > -INFINITY ? p * slope * ((dg - first) - mean) : 0.f;
-    } else {
-      const float e = expf(-fabsf(zc));
-      v = zc > -INFINITY ? dg * e / ((1.f + e) * (1.f + e)) : 0.f;
+  const int lane = threadIdx.x & 31, q = lane & (L - 1);
+  const int64_t t = (int64_t(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5)) * (32 / L) + lane / L;
+  const bool there = t < A.tokens;
+  const T* row = static_cast<const T*>(A.logits) + (there ? t : 0) * A.ld;
+  T* out = static_cast<T*>(A.out) + (there ? t : 0) * A.ldd;
+  const Slot c = slot_of(A, row, t, q, there);
+  const bool on = c.z > -INFINITY;
+  float v = 0.f;
+  if (A.renorm) {
+    const float top = max_of<L>(c.z), m = fminf(top, 0.f);
+    float s = 0.f, slope = 1.f;
+    if (on) {
+      s = SOFTMAX ? share(c.z, top) : 1.f / (expf(m) + expf(m - c.z));
+      if (!SOFTMAX) slope = 1.f / (1.f + expf(c.z));  // 1 - sigmoid
     }
-    // an expert that several slots name gets their sum
-    const uint32_t same = __match_any_sync(kAll, id);
-    if (__any_sync(kAll, id >= 0 && (same & (same - 1)))) {
-      float sum = 0.f;
-      for (int j = 0; j < A.topk; ++j) {
-        const float w = __shfl_sync(kAll, v, j);
-        if (same >> j & 1) sum += w;
-      }
-      v = sum;
-    }
-    if (all && zc > -INFINITY) v -= share(zc, most) * inv * dot;
-    __syncwarp();  // the logits have been read: dlogits may be they
-    auto store = [&](auto step) {
-      constexpr int S = decltype(step)::value;
-#pragma unroll
-      for (int i = 0; i < EPL; i += S) {
-        if (i >= A.epl || lane * A.epl + i >= A.experts) continue;
-        Vec<T, S> o;
-#pragma unroll
-        for (int e = 0; e < S; ++e)
-          o.v[e] = narrow<T>(all && z[i + e] > -INFINITY ? -share(z[i + e], most) * inv * dot : 0.f);
-        *reinterpret_cast<Vec<T, S>*>(out + lane * A.epl + i) = o;
-      }
-    };
-    with_access<T, EPL>(A.vec_out, store);
-    __syncwarp();  // (orders the stores of the lanes)
-    if (id >= 0 && __ffs(same) - 1 == lane) out[id] = narrow<T>(v);
+    const float total = sum_of<L>(s), p = on ? s / total : 0.f;
+    // p_j (dg_j - sum p_i dg_i) by differences, which vanish where the dg are equal
+    const uint32_t any = lanes_of<L>(on);
+    const float first = __shfl_sync(kAll, c.dg, any ? __ffs(any) - 1 : 0, L);
+    const float mean = sum_of<L>(on ? p * (c.dg - first) : 0.f);
+    v = on ? p * slope * ((c.dg - first) - mean) : 0.f;
+  } else {  // sigmoid
+    const float e = expf(-fabsf(c.z));
+    v = on ? c.dg * e / ((1.f + e) * (1.f + e)) : 0.f;
   }
+  uint32_t same;
+  v = sum_same<L>(c.id, A.topk, v, &same);
+  __syncwarp();  // the logits have been read: dlogits may be they
+  if (there) {
+    Vec<T, S> zero;
+#pragma unroll
+    for (int e = 0; e < S; ++e) zero.v[e] = narrow<T>(0.f);
+#pragma unroll 4
+    for (int e = q * S; e < A.experts; e += L * S) *reinterpret_cast<Vec<T, S>*>(out + e) = zero;
+  }
+  __syncwarp();  // (orders the stores of the lanes)
+  if (c.id >= 0 && __ffs(same) - 1 == lane) out[c.id] = narrow<T>(v);
+}
+
+// Gates that are a whole softmax's: every logit has a part.  A warp a token; lane l has the
+// vectors l, l + 32, .. of 16 bytes, EPL elements in all, also where they are accessed one by
+// one: the sums' order does not depend on the alignment.
+template <class T, bool VEC, int EPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_softmax_grad_kernel(const __grid_constant__ RouteGradArgs A) {
+  after_the_last();
+  const int lane = threadIdx.x & 31;
+  constexpr int S = 16 / sizeof(T);
+  const int64_t t = int64_t(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= A.tokens) return;
+  const T* row = static_cast<const T*>(A.logits) + t * A.ld;
+  T* out = static_cast<T*>(A.out) + t * A.ldd;
+  const Slot c = slot_of(A, row, t, lane, true);
+  float z[EPL], most = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < EPL; i += S) {
+    const int e0 = (i * 32 + lane * S);
+    Vec<T, S> v;
+    if (VEC && e0 < A.experts) v = *reinterpret_cast<const Vec<T, S>*>(row + e0);
+#pragma unroll
+    for (int e = 0; e < S; ++e) {
+      if (!VEC && e0 + e < A.experts) v.v[e] = row[e0 + e];
+      z[i + e] = e0 + e < A.experts ? fmaxf(widen(v.v[e]), -INFINITY) : -INFINITY;
+      most = fmaxf(most, z[i + e]);
+    }
+  }
+  most = warp_max(most);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    z[i] = share(z[i], most);
+    sum += z[i];
+  }
+  const float inv = 1.f / sum_of<32>(sum);
+  const bool on = c.z > -INFINITY;
+  const float s = on ? share(c.z, most) * inv : 0.f;
+  const float dot = sum_of<32>(on ? s * c.dg : 0.f);
+  uint32_t same;
+  const float v = sum_same<32>(c.id, A.topk, on ? s * c.dg : 0.f, &same);
+  __syncwarp();  // the logits have been read: dlogits may be they
+#pragma unroll
+  for (int i = 0; i < EPL; i += S) {
+    const int e0 = (i * 32 + lane * S);
+    if (e0 >= A.experts) continue;
+    Vec<T, S> o;
+#pragma unroll
+    for (int e = 0; e < S; ++e) o.v[e] = narrow<T>(z[i + e] > 0.f ? -(z[i + e] * inv) * dot : 0.f);
+    if (VEC) *reinterpret_cast<Vec<T, S>*>(out + e0) = o;
+#pragma unroll
+    for (int e = 0; e < S; ++e)
+      if (!VEC && e0 + e < A.experts) out[e0 + e] = o.v[e];
+  }
+  __syncwarp();  // (orders the stores of the lanes)
+  if (c.id >= 0 && __ffs(same) - 1 == lane) out[c.id] = narrow<T>(on ? v - s * dot : 0.f);
 }
 
 // ------------------------------------------------------------------ host side
@@ -467,15 +723,75 @@ int access_of(const void* p, size_t ld, int experts, int epl, size_t elem) {
   return v;
 }
 
-constexpr int kRouteCtas = kSms * 8;
-int route_grid(int tokens) {
-  const int want = (tokens + kRouteWarps - 1) / kRouteWarps;
-  return want < kRouteCtas ? want : kRouteCtas;
+// The lanes that take a token: as few as hold its experts in registers, have one lane for each
+// slot and the first that is left out, and one for each group.  32,768 tokens, top-8 of 256 in
+// 4 of 8 groups: 30.6 us with 16 lanes, 34.4 with 32; top-6 of 64: 6.8 us with 8, 12.8 with 32.
+template <class T, bool SOFTMAX>
+void (*route_pick(int experts, int topk, int groups, bool scored, int* lanes))(RouteArgs) {
+  const int slots = topk + (scored && sizeof(T) == 2 ? 4 : 1), need = slots > groups ? slots : groups;
+  if (experts <= 32 && need <= 8) {
+    *lanes = 8;
+    return route_kernel<T, 4, 8, SOFTMAX>;
+  }
+  if (experts <= 64 && need <= 8) {
+    *lanes = 8;
+    return route_kernel<T, 8, 8, SOFTMAX>;
+  }
+  if (experts <= 64 && need <= 16) {
+    *lanes = 16;
+    return route_kernel<T, 4, 16, SOFTMAX>;
+  }
+  if (experts <= 128 && need <= 16) {
+    *lanes = 16;
+    return route_kernel<T, 8, 16, SOFTMAX>;
+  }
+  if (experts <= 256 && need <= 16) {
+    *lanes = 16;
+    return route_kernel<T, 16, 16, SOFTMAX>;
+  }
+  *lanes = 32;
+  return experts <= 32    ? route_kernel<T, 1, 32, SOFTMAX>
+         : experts <= 64  ? route_kernel<T, 2, 32, SOFTMAX>
+         : experts <= 128 ? route_kernel<T, 4, 32, SOFTMAX>
+         : experts <= 256 ? route_kernel<T, 8, 32, SOFTMAX>
+         : experts <= 512 ? route_kernel<T, 16, 32, SOFTMAX>
+                          : route_kernel<T, 32, 32, SOFTMAX>;
 }
 
-#define HOC_ROUTE_PICK(KERNEL, T, E)                                                                         \
-  ((E) <= 32 ? KERNEL<T, 1> : (E) <= 64 ? KERNEL<T, 2> : (E) <= 128 ? KERNEL<T, 4> : (E) <= 256 ? KERNEL<T, 8> \
-                                                       : (E) <= 512 ? KERNEL<T, 16> : KERNEL<T, 32>)
+template <class T, int S, bool SOFTMAX>
+void (*route_grad_lanes(int topk, int* lanes))(RouteGradArgs) {
+  if (topk <= 8) {
+    *lanes = 8;
+    return route_grad_kernel<T, S, 8, SOFTMAX>;
+  }
+  if (topk <= 16) {
+    *lanes = 16;
+    return route_grad_kernel<T, S, 16, SOFTMAX>;
+  }
+  {
+    *lanes = 32;
+    return route_grad_kernel<T, S, 32, SOFTMAX>;
+  }
+}
+
+template <class T, int S>
+void (*route_grad_pick(const RouteGradArgs& A, bool softmax, int* lanes))(RouteGradArgs) {
+  if (!softmax) return route_grad_lanes<T, S, false>(A.topk, lanes);
+  if (A.renorm) return route_grad_lanes<T, S, true>(A.topk, lanes);
+  *lanes = 32;
+  const int e = A.experts;
+  constexpr bool vec = S > 1;
+  if (sizeof(T) == 4 && e <= 128) return route_softmax_grad_kernel<T, vec, sizeof(T) == 4 ? 4 : 8>;
+  return e <= 256 ? route_softmax_grad_kernel<T, vec, 8> : e <= 512 ? route_softmax_grad_kernel<T, vec, 16> : route_softmax_grad_kernel<T, vec, 32>;
+}
+
+template <class T>
+void (*route_grad_pick(const RouteGradArgs& A, bool softmax, bool vec, int* lanes))(RouteGradArgs) {
+  return vec ? route_grad_pick<T, 16 / sizeof(T)>(A, softmax, lanes) : route_grad_pick<T, 1>(A, softmax, lanes);
+}
+
+// CTAs for `tokens` tokens of `lanes` lanes each.
+dim3 route_grid(int tokens, int lanes) { return dim3(unsigned((int64_t(tokens) * lanes + kRouteWarps * 32 - 1) / (kRouteWarps * 32))); }
 
 const char* bad_route(int tokens, int experts, int topk, const void* logits, int dtype, size_t ld, int score, const float* scale) {
   if (tokens < 0 || experts < 1 || experts > kMaxExperts) return "tokens or experts out of range";
@@ -489,20 +805,32 @@ const char* bad_route(int tokens, int experts, int topk, const void* logits, int
 }  // namespace
 
 cudaError_t route_preload() {
-  const void* fns[] = {
-#define HOC_ROUTE_OF(T, N) \
-  reinterpret_cast<const void*>(&route_kernel<T, N>), reinterpret_cast<const void*>(&route_grad_kernel<T, N>)
-#define HOC_ROUTE_ALL(T) \
-  HOC_ROUTE_OF(T, 1), HOC_ROUTE_OF(T, 2), HOC_ROUTE_OF(T, 4), HOC_ROUTE_OF(T, 8), HOC_ROUTE_OF(T, 16), HOC_ROUTE_OF(T, 32)
-      HOC_ROUTE_ALL(float), HOC_ROUTE_ALL(__nv_bfloat16)};
-#undef HOC_ROUTE_ALL
-#undef HOC_ROUTE_OF
-  for (const void* f : fns) {
+  cudaError_t err = cudaSuccess;
+  auto load = [&](const void* f) {
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, f);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+    if (err == cudaSuccess) err = cudaFuncGetAttributes(&a, f);
+  };
+  int lanes;
+  for (int experts = 32; experts <= kMaxExperts; experts *= 2)
+    for (int topk : {1, 12, 31}) {
+      for (int groups : {1, 16}) {
+        load(reinterpret_cast<const void*>(route_pick<float, false>(experts, topk, groups, false, &lanes)));
+        load(reinterpret_cast<const void*>(route_pick<float, true>(experts, topk, groups, false, &lanes)));
+        load(reinterpret_cast<const void*>(route_pick<__nv_bfloat16, false>(experts, topk, groups, false, &lanes)));
+        load(reinterpret_cast<const void*>(route_pick<__nv_bfloat16, true>(experts, topk, groups, false, &lanes)));
+      }
+      RouteGradArgs A{};
+      A.experts = experts;
+      A.topk = topk;
+      for (int renorm = 0; renorm < 2; ++renorm)
+        for (int softmax = 0; softmax < 2; ++softmax)
+          for (int vec = 0; vec < 2; ++vec) {
+            A.renorm = renorm;
+            load(reinterpret_cast<const void*>(route_grad_pick<float>(A, softmax, vec, &lanes)));
+            load(reinterpret_cast<const void*>(route_grad_pick<__nv_bfloat16>(A, softmax, vec, &lanes)));
+          }
+    }
+  return err;
 }
 
 }  // namespace hoc
@@ -523,13 +851,18 @@ extern "C" hocResult_t hoc_ep_route(int tokens, int experts, int topk, const voi
     bad = "ids and gate must be given, aligned to their elements";
   if (bad) return refuse(who, bad);
   if (tokens == 0) return HOC_SUCCESS;
-  const int epl = (experts + 31) / 32;
-  const RouteArgs A{logits, bias, ids, gate, int64_t(ldl), tokens, experts, topk, epl, groups, top_groups,
-                    score == HOC_SCORE_SOFTMAX, renormalise != 0, access_of(logits, ldl, experts, epl, bytes_of(dtype)), *scale};
-  const dim3 grid(route_grid(tokens)), cta(kRouteWarps * 32);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launched(who, dtype == HOC_FLOAT32 ? launch(HOC_ROUTE_PICK(route_kernel, float, experts), grid, cta, 0, s, A)
-                                            : launch(HOC_ROUTE_PICK(route_kernel, __nv_bfloat16, experts), grid, cta, 0, s, A));
+  const bool softmax = score == HOC_SCORE_SOFTMAX, scored = bias || top_groups < groups;
+  const size_t b = bytes_of(dtype);
+  int lanes;
+  const auto kernel = dtype == HOC_FLOAT32
+                          ? softmax ? route_pick<float, true>(experts, topk, groups, scored, &lanes) : route_pick<float, false>(experts, topk, groups, scored, &lanes)
+                          : softmax ? route_pick<__nv_bfloat16, true>(experts, topk, groups, scored, &lanes)
+                                    : route_pick<__nv_bfloat16, false>(experts, topk, groups, scored, &lanes);
+  const int epl = (experts + lanes - 1) / lanes, epl_warp = (experts + 31) / 32;
+  const RouteArgs A{logits, bias, ids, gate, int64_t(ldl), tokens, experts, topk, groups, top_groups, softmax, renormalise != 0,
+                    epl, access_of(logits, ldl, experts, epl, b), epl_warp, access_of(logits, ldl, experts, epl_warp, b),
+                    access_of(bias, 0, experts, epl, 4), access_of(bias, 0, experts, epl_warp, 4), *scale};
+  return launched(who, launch(kernel, route_grid(tokens, lanes), dim3(kRouteWarps * 32), 0, static_cast<cudaStream_t>(stream), A));
 }
 
 extern "C" hocResult_t hoc_ep_route_grad(int tokens, int experts, int topk, const void* logits, hocDataType_t dtype,
@@ -542,13 +875,12 @@ extern "C" hocResult_t hoc_ep_route_grad(int tokens, int experts, int topk, cons
     bad = "ids and dgate must be given, aligned to their elements";
   if (bad) return refuse(who, bad);
   if (tokens == 0) return HOC_SUCCESS;
-  const int epl = (experts + 31) / 32;
   const size_t b = bytes_of(dtype);
-  const RouteGradArgs A{logits, ids, dgate, dlogits, int64_t(ldl), int64_t(ldd), tokens, experts, topk, epl,
-                        score == HOC_SCORE_SOFTMAX, renormalise != 0, access_of(logits, ldl, experts, epl, b),
-                        access_of(dlogits, ldd, experts, epl, b), *scale};
-  const dim3 grid(route_grid(tokens)), cta(kRouteWarps * 32);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launched(who, dtype == HOC_FLOAT32 ? launch(HOC_ROUTE_PICK(route_grad_kernel, float, experts), grid, cta, 0, s, A)
-                                            : launch(HOC_ROUTE_PICK(route_grad_kernel, __nv_bfloat16, experts), grid, cta, 0, s, A));
+  const bool softmax = score == HOC_SCORE_SOFTMAX;
+  const bool vec = experts * b % 16 == 0 && vector_rows(dlogits, ldd, b) && vector_rows(logits, ldl, b);
+  const RouteGradArgs A{logits, ids, dgate, dlogits, int64_t(ldl), int64_t(ldd), tokens, experts, topk, renormalise != 0, *scale};
+  int lanes;
+  const auto kernel = dtype == HOC_FLOAT32 ? route_grad_pick<float>(A, softmax, vec, &lanes)
+                                           : route_grad_pick<__nv_bfloat16>(A, softmax, vec, &lanes);
+  return launched(who, launch(kernel, route_grid(tokens, lanes), dim3(kRouteWarps * 32), 0, static_cast<cudaStream_t>(stream), A));
 }
