@@ -452,6 +452,7 @@ struct WidenArgs {
   __nv_bfloat16* y[kMaxRanks];
   int64_t cap[kMaxRanks];
   const int64_t* seg;
+  uint64_t* counts;
   int64_t segs;  // entries of one rank
   int ranks, width, log;
 };
@@ -462,6 +463,7 @@ constexpr int kWidenAhead = 2;  // steps a thread has in flight
 // A step is E values: 16 where rows of y are whole 32 bytes, else 8, else 1.  2^log neighbouring
 // lanes take a row, as many as it has steps, a warp at most; the rows of all ranks are one run,
 // handed out in turn.
+static_assert(kMaxRanks * kMaxRanks <= kWidenThreads, "a thread for each count");
 template <int E>
 __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_constant__ WidenArgs A) {
   __shared__ int64_t ends[kMaxRanks];
@@ -478,6 +480,8 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
     }
     if (int(threadIdx.x) < kMaxRanks) ends[threadIdx.x] = n;
   }
+  if (A.counts && blockIdx.x == 0 && int(threadIdx.x) < A.ranks * A.ranks)
+    A.counts[threadIdx.x] = A.counts[threadIdx.x] / uint64_t(wire_bytes(A.width) / 2) * uint64_t(A.width);
   __syncthreads();
   struct alignas(E) In {
     uint8_t v[E];
@@ -732,15 +736,16 @@ extern "C" hocResult_t hoc_rms_norm_grad(int rows, int width, hocDataType_t dtyp
 }
 
 extern "C" hocResult_t hoc_expert_widen(const hocRowGroups_t* G, const void* const* wire, int width, void* const* y,
-                                        void* stream) {
+                                        uint64_t* counts, void* stream) {
   const char* who = "hoc_expert_widen";
   if (!G || !G->seg || !G->capacity || !wire || !y) return refuse(who, "groups, its seg and its capacity, wire and y must be given");
   if (G->nranks < 1 || G->nranks > kMaxRanks || G->experts < 1 || G->sources < 1)
     return refuse(who, "rank, expert or source count out of range");
   if (width < 1 || width > kMaxWidth) return refuse(who, "width out of range");
-  if (!aligned(G->seg, 8)) return refuse(who, "seg must be aligned to 8 bytes");
+  if (!aligned(G->seg, 8) || !aligned(counts, 8)) return refuse(who, "seg and counts must be aligned to 8 bytes");
   WidenArgs A{};
   A.seg = G->seg;
+  A.counts = counts;
   A.segs = int64_t(G->experts) * G->sources + 1;
   A.ranks = G->nranks;
   A.width = width;
@@ -758,10 +763,10 @@ extern "C" hocResult_t hoc_expert_widen(const hocRowGroups_t* G, const void* con
     wide = wide && aligned(y[d], 32);
     most += cap;
   }
-  if (most == 0) return HOC_SUCCESS;
+  if (most == 0 && !counts) return HOC_SUCCESS;
   const int e = wide && width % 16 == 0 ? 16 : vec && width % 8 == 0 ? 8 : 1;
   while (A.log < 5 && (e << A.log) < width) ++A.log;
-  const size_t want = ((most << A.log) + kWidenThreads - 1) / kWidenThreads;
+  const size_t want = ((most << A.log) + kWidenThreads) / kWidenThreads;  // one at least
   return launched(who, launch(e == 16 ? widen_kernel<16> : e == 8 ? widen_kernel<8> : widen_kernel<1>,
                               dim3(unsigned(want < size_t(kWidenCtas) ? want : size_t(kWidenCtas))), dim3(kWidenThreads), 0,
                               static_cast<cudaStream_t>(stream), A));

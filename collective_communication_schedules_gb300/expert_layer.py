@@ -10,6 +10,11 @@ and the products between them (include/hoc_layer.h):
     out  = h W_down^T                            w_down[d]: [experts, hidden, ffn]
     y    = combine(out, gate)                    gate-weighted sum of a token's rows
 
+With rows of 8 bits (include/hoc_block.h) the dispatch moves those, about half the
+bytes, and they are widened to bf16 where the experts are:
+
+    recv = widen(dispatch(rows of 8 bits, ids))
+
 and back: the gradients for x, the gate weights and both weights.  Everything is
 stream-ordered with counts that only the device knows; buffers are allocated
 once, and a call may be captured into a CUDA graph (after one call of its kind).
@@ -26,10 +31,10 @@ class ExpertLayer:
 
     capacity: rows of each rank's receive buffer.  The default, k * tokens * topk, has room for every pair at any
     rank; k * tokens * min(topk, experts / k) is enough where a token's experts are distinct.  A pair whose row does
-    not fit is dropped, and status bit 0 says so."""
+    not fit is dropped, and status bit 0 says so.  wire8: forward takes x in rows of 8 bits."""
 
     def __init__(self, k: int, tokens: int, topk: int, hidden: int, ffn: int, experts: int, capacity: int | None = None,
-                 device: int = 0):
+                 device: int = 0, wire8: bool = False):
         if experts % k:
             raise ValueError("experts must be a multiple of the rank count")
         self.k, self.tokens, self.topk, self.hidden, self.ffn, self.experts = k, tokens, topk, hidden, ffn, experts
@@ -50,14 +55,27 @@ class ExpertLayer:
         self.ones = [torch.ones(tokens * topk, device=dev)] * k
         self.ws = torch.empty(max(1, k * hoc.ep_pack_workspace(tokens, topk, experts)), dtype=torch.int32, device=dev)
         self.caps = [self.rows * hidden] * k
+        self.recv8 = None
+        if wire8:
+            n = hoc.wire8_bytes(hidden)
+            self.recv8 = ranks(self.rows, n, dtype=torch.uint8)
+            self.caps8 = [self.rows * (n // 2)] * k
         torch.cuda.current_stream(dev).synchronize()  # status and ones are there for calls on any stream
 
     def forward(self, x, ids, gate, w_up, w_down, y, stream=None):
-        """y[s] [tokens, hidden] of every source s; x[s] [tokens, hidden] bf16, ids[s] [tokens * topk] int32,
-        gate[s] [tokens * topk] float32."""
-        hoc.ep_dispatch_fused(ids, x, self.experts, self.recv, self.caps, self.pos, self.counts, self.ws, self.status,
-                              stream=stream)
-        hoc.ep_segments(ids, self.experts, self.topk, self.seg, stream=stream)
+        """y[s] [tokens, hidden] of every source s; x[s] [tokens, hidden] bf16, or uint8 [tokens, wire8_bytes(hidden)] rows
+        of 8 bits with wire8; ids[s] [tokens * topk] int32, gate[s] [tokens * topk] float32."""
+        if self.recv8 is None:
+            hoc.ep_dispatch_fused(ids, x, self.experts, self.recv, self.caps, self.pos, self.counts, self.ws, self.status,
+                                  stream=stream)
+            hoc.ep_segments(ids, self.experts, self.topk, self.seg, stream=stream)
+        else:
+            if any(v.dtype is not torch.uint8 or v.shape != (self.tokens, self.recv8[0].shape[1]) for v in x):
+                raise ValueError(f"x: expected rows of 8 bits, uint8 [{self.tokens}, {self.recv8[0].shape[1]}]")
+            hoc.ep_dispatch_fused(ids, [v.view(torch.bfloat16) for v in x], self.experts, self.recv8, self.caps8, self.pos,
+                                  self.counts, self.ws, self.status, stream=stream)
+            hoc.ep_segments(ids, self.experts, self.topk, self.seg, stream=stream)
+            hoc.expert_widen(self.recv8, self.seg, self.recv, counts=self.counts, stream=stream)
         hoc.expert_mm(self.recv, w_up, self.seg, self.h, status=self.status, act="swiglu", pre=self.pre, stream=stream)
         hoc.expert_mm(self.h, w_down, self.seg, self.out, status=self.status, stream=stream)
         hoc.ep_combine_fused(self.out, self.caps, ids, self.pos, self.counts, gate, self.tokens, self.topk, self.hidden,

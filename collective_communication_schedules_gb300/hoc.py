@@ -164,7 +164,7 @@ _SIGS["hoc_rms_norm_workspace"] = (C.c_int, [C.c_int, C.c_int, C.POINTER(C.c_siz
 _SIGS["hoc_rms_norm_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 3 * _ROWS + [C.c_void_p, C.c_int, C.POINTER(C.c_float)]
                               + 2 * _ROWS + [C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p])
 _SIGS["hoc_expert_widen"] = (C.c_int, [C.POINTER(_RowGroups), C.POINTER(C.c_void_p), C.c_int, C.POINTER(C.c_void_p),
-                                       C.c_void_p])
+                                       C.c_void_p, C.c_void_p])
 _SIGS["hoc_ep_route"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_size_t, C.c_int, C.c_void_p,
                                    C.c_int, C.c_int, C.c_int, C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_void_p])
 _SIGS["hoc_ep_route_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_size_t, C.c_int, C.c_int,
@@ -696,7 +696,7 @@ _TORCH = {}  # torch dtypes by name, once torch is imported
 def _dt(name: str):
     if not _TORCH:
         import torch
-        _TORCH.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "int64")})
+        _TORCH.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "int64", "uint8")})
     return _TORCH[name]
 
 
@@ -908,15 +908,30 @@ def _row_dtype(x, what: str) -> int:
     raise TypeError(f"{what}: expected a bfloat16 or float32 tensor")
 
 
+_get_device = _raw_stream = None  # torch's own calls for the current device and its stream, once torch is imported
+
+
 def _here(x, what: str) -> int:
     """The device of `x`, which has to be the current one: a launch would run there."""
-    import torch
-    if not x.is_cuda:
-        raise ValueError(f"{what}: must be a CUDA tensor")
+    global _get_device, _raw_stream
+    if _get_device is None:
+        import torch
+        if not torch.cuda.is_available():
+            raise ValueError(f"{what}: must be a CUDA tensor, and there is no GPU")
+        torch.cuda.init()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     device = x.get_device()
-    if device != torch.cuda.current_device():
+    if device < 0 or not x.is_cuda:
+        raise ValueError(f"{what}: must be a CUDA tensor")
+    if device != _get_device():
         raise ValueError(f"{what}: is on another device than the current one")
     return device
+
+
+def _queue(stream, device: int) -> int:
+    """The handle of `stream`, of the current one of `device` for None; _here has been called."""
+    return _raw_stream(device) if stream is None and _raw_stream else _stream(stream)
 
 
 def _rows_of(x, shape, dtype, device: int, what: str):
@@ -927,19 +942,14 @@ def _rows_of(x, shape, dtype, device: int, what: str):
         raise TypeError(f"{what}: expected a {str(dtype).split('.')[-1]} tensor")
     if x.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
-    if not x.is_cuda or x.get_device() != device:
+    if x.get_device() != device:
         raise ValueError(f"{what}: must be a CUDA tensor on the device of the others")
     rows, width = shape
-    if rows == 0 or width == 0:
-        return x.data_ptr(), width
     ld, step = x.stride()
-    if width > 1 and step != 1:
-        raise ValueError(f"{what}: a row's elements must be contiguous")
-    if rows == 1:
-        return x.data_ptr(), width
-    if ld < width:
-        raise ValueError(f"{what}: rows must not overlap")
-    return x.data_ptr(), ld
+    if (step != 1 and width > 1) or (ld < width and rows > 1):
+        if rows and width:
+            raise ValueError(f"{what}: " + ("a row's elements must be contiguous" if step != 1 and width > 1 else "rows must not overlap"))
+    return x.data_ptr(), ld if rows > 1 and ld > width else width
 
 
 def _flat(x, n: int, dtype, device: int, what: str):
@@ -950,7 +960,7 @@ def _flat(x, n: int, dtype, device: int, what: str):
         raise TypeError(f"{what}: expected a {str(dtype).split('.')[-1]} tensor")
     if x.numel() != n or not x.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous elements, got shape {tuple(x.shape)}")
-    if not x.is_cuda or x.get_device() != device:
+    if x.get_device() != device:
         raise ValueError(f"{what}: must be a CUDA tensor on the device of the others")
     return x.data_ptr()
 
@@ -984,12 +994,11 @@ def wire8_views(wire, width: int):
 
 
 def _wire_rows(wire, rows: int, width: int, device: int, what: str) -> Optional[int]:
-    import torch
     if wire is None:
         return None
     if wire.dim() != 2 or wire.shape[0] != rows or wire.shape[1] != _wire8(width)[0]:
         raise ValueError(f"{what}: expected shape {(rows, _wire8(width)[0])}, got {tuple(wire.shape)}")
-    return _flat(wire, wire.numel(), torch.uint8, device, what)
+    return _flat(wire, wire.numel(), _dt("uint8"), device, what)
 
 
 def rms_norm(x, weight, y=None, *, eps: float, residual=None, h=None, wire=None, stream=None):
@@ -1007,7 +1016,7 @@ def rms_norm(x, weight, y=None, *, eps: float, residual=None, h=None, wire=None,
     yp, ldy = _rows_of(y, shape, x.dtype, dev, "y")
     wdt = _row_dtype(weight, "weight")
     _check(lib().hoc_rms_norm(rows, width, dt, xp, ldx, rp, ldr, _flat(weight, width, weight.dtype, dev, "weight"), wdt,
-                              C.byref(C.c_float(eps)), hp, ldh, yp, ldy, _wire_rows(wire, rows, width, dev, "wire"), _stream(stream)),
+                              C.byref(C.c_float(eps)), hp, ldh, yp, ldy, _wire_rows(wire, rows, width, dev, "wire"), _queue(stream, dev)),
            "hoc_rms_norm")
 
 
@@ -1044,12 +1053,13 @@ def rms_norm_grad(dy, h, weight, dx, *, eps: float, dy2=None, dres=None, dw=None
     _check(lib().hoc_rms_norm_grad(rows, width, dt, dyp, lddy, dy2p, lddy2, hp, ldh,
                                    _flat(weight, width, weight.dtype, dev, "weight"), wdt, C.byref(C.c_float(eps)), drp, lddr, dxp, lddx,
                                    None if dw is None else _flat(dw, width, dw.dtype, dev, "dw"), dwdt,
-                                   int(bool(accumulate)), wsp, ints, _stream(stream)), "hoc_rms_norm_grad")
+                                   int(bool(accumulate)), wsp, ints, _queue(stream, dev)), "hoc_rms_norm_grad")
 
 
-def expert_widen(wire, seg, y, stream=None):
+def expert_widen(wire, seg, y, *, counts=None, stream=None):
     """y[d][r] = bf16 of the rows of 8 bits wire[d][r], for the rows that seg covers (see include/hoc_block.h): lists of k
-    device tensors, wire uint8 [capacity, wire8_bytes(width)], y bf16 [capacity, width]; seg as expert_mm's."""
+    device tensors, wire uint8 [capacity, wire8_bytes(width)], y bf16 [capacity, width]; seg as expert_mm's.  counts: those
+    of the dispatch that moved the rows, int64 [k, k], turned into counts of y's elements for the combine."""
     k = len(y)
     if not k or len(wire) != k or y[0].dim() != 2:
         raise ValueError("wire and y: lists of as many matrices")
@@ -1057,17 +1067,28 @@ def expert_widen(wire, seg, y, stream=None):
     if seg.dim() != 2 or seg.shape[0] != k or seg.shape[1] < 2:
         raise ValueError(f"seg: expected shape [{k}, sources * experts + 1], got {tuple(seg.shape)}")
     dev, width = _here(y[0], "y[0]"), y[0].shape[1]
-    n, bf = wire8_bytes(width), _dt("bfloat16")
-    yp, wp, cap = (C.c_void_p * k)(), (C.c_void_p * k)(), (C.c_size_t * k)()
-    for d in range(k):
-        t, w = y[d], wire[d]
-        rows = t.shape[0]
-        if t.dim() != 2 or t.shape[1] != width:
-            raise ValueError(f"y[{d}]: expected shape [capacity, {width}], got {tuple(t.shape)}")
-        yp[d], cap[d] = _flat(t, rows * width, bf, dev, "y"), rows
-        wp[d] = _wire_rows(w, rows, width, dev, "wire")
+    n, bf, u8 = wire8_bytes(width), _dt("bfloat16"), _dt("uint8")
+    caps, yp, wp, rows, shape, fits = [], [], [], 0, None, False
+    for t, w in zip(y, wire):
+        if t.shape != shape:
+            shape, rows = t.shape, t.shape[0]
+            rows_n, fits = (rows, n), t.shape == (rows, width)
+        if (t.dtype is not bf or w.dtype is not u8 or not fits or w.shape != rows_n or not t.is_contiguous()
+                or not w.is_contiguous() or t.get_device() != dev or w.get_device() != dev):
+            d = len(caps)  # the checks once more, by those that name what is wrong
+            _flat(t, rows * width, bf, dev, f"y[{d}]")
+            _flat(w, rows * n, u8, dev, f"wire[{d}]")
+            raise ValueError(f"y[{d}] and wire[{d}]: expected shapes [capacity, {width}] and [capacity, {n}], got "
+                             f"{tuple(t.shape)} and {tuple(w.shape)}")
+        caps.append(rows)
+        yp.append(t.data_ptr())
+        wp.append(w.data_ptr())
+    arr = C.c_void_p * k
+    yp, wp, cap = arr(*yp), arr(*wp), (C.c_size_t * k)(*caps)
     g = _RowGroups(k, seg.shape[1] - 1, 1, _flat(seg, seg.numel(), seg.dtype, dev, "seg"), cap)
-    _check(lib().hoc_expert_widen(C.byref(g), wp, width, yp, _stream(stream)), "hoc_expert_widen")
+    _check(lib().hoc_expert_widen(C.byref(g), wp, width, yp,
+                                  None if counts is None else _flat(counts, k * k, _dt("int64"), dev, "counts"),
+                                  _queue(stream, dev)), "hoc_expert_widen")
 
 
 def _slots(logits, ids, gate, what: str):
@@ -1094,7 +1115,7 @@ def ep_route(logits, ids, gate, *, score: str = "softmax", bias=None, groups: in
     _check(lib().hoc_ep_route(tokens, experts, topk, lp, dt, ldl, _score(score),
                               _flat(bias, experts, _dt("float32"), dev, "bias"), groups,
                               groups if top_groups is None else top_groups, int(bool(renormalise)), C.byref(C.c_float(scale)), ip, gp,
-                              _stream(stream)), "hoc_ep_route")
+                              _queue(stream, dev)), "hoc_ep_route")
 
 
 def ep_route_grad(logits, ids, dgate, dlogits, *, score: str = "softmax", renormalise: bool = False, scale: float = 1.0,
@@ -1103,7 +1124,7 @@ def ep_route_grad(logits, ids, dgate, dlogits, *, score: str = "softmax", renorm
     tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, dgate, "dgate")
     dp, ldd = _rows_of(dlogits, logits.shape, logits.dtype, dev, "dlogits")
     _check(lib().hoc_ep_route_grad(tokens, experts, topk, lp, dt, ldl, _score(score), int(bool(renormalise)), C.byref(C.c_float(scale)), ip, gp,
-                                   dp, ldd, _stream(stream)), "hoc_ep_route_grad")
+                                   dp, ldd, _queue(stream, dev)), "hoc_ep_route_grad")
 
 
 def dropout(x, y, p: float, seed, *, residual=None, stream=None):
@@ -1128,7 +1149,7 @@ def dropout(x, y, p: float, seed, *, residual=None, stream=None):
     yp, ldy = _rows_of(y, shape, x.dtype, dev, "y")
     rp, ldr = _rows_of(residual, shape, x.dtype, dev, "residual")
     _check(lib().hoc_dropout(shape[0], shape[1], dt, xp, ldx, rp, ldr, C.byref(C.c_double(p)), _flat(seed, 2, _dt("int64"), dev, "seed"), yp,
-                             ldy, _stream(stream)), "hoc_dropout")
+                             ldy, _queue(stream, dev)), "hoc_dropout")
 
 
 # ------------------------------------------------------------- gradient clipping

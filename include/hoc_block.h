@@ -85,9 +85,12 @@ hocResult_t hoc_rms_norm_grad(int rows, int width, hocDataType_t dtype, const vo
  * covers, 0 .. seg[d][sources * experts] (cut to [0, capacity[d]]), wire[d]
  * being [capacity[d]][bytes of hoc_wire8_row], aligned to 16 bytes, and y[d]
  * [capacity[d], width] bf16.  Rows behind them are left as they were.  Buffers
- * of a rank with capacity 0 may be NULL. */
+ * of a rank with capacity 0 may be NULL.  counts (NULL: none): the device [nranks *
+ * nranks] element counts that the dispatch of these rows wrote, in elements of its
+ * rows (*bytes / 2 each), which become counts in elements of y, as a combine of
+ * rows of `width` takes them. */
 hocResult_t hoc_expert_widen(const hocRowGroups_t* groups, const void* const* wire, int width, void* const* y,
-                             void* stream);
+                             uint64_t* counts, void* stream);
 
 /* Scores of the experts. */
 typedef enum { HOC_SCORE_SOFTMAX = 0, HOC_SCORE_SIGMOID = 1 } hocScore_t;

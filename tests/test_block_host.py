@@ -64,14 +64,14 @@ def test_calls_on_no_rows_do_nothing():
     assert widen(cap=(0,), wire=(None,), y=(None,)) == hoc.SUCCESS
 
 
-def widen(k=1, experts=2, sources=1, seg=P, cap=(8,), wire=(P,), y=(P,), width=64):
+def widen(k=1, experts=2, sources=1, seg=P, cap=(8,), wire=(P,), y=(P,), width=64, counts=None):
     g = hoc._RowGroups(k, experts, sources, seg, (C.c_size_t * len(cap))(*cap))
-    return hoc.lib().hoc_expert_widen(C.byref(g), (C.c_void_p * len(wire))(*wire), width, (C.c_void_p * len(y))(*y), None)
+    return hoc.lib().hoc_expert_widen(C.byref(g), (C.c_void_p * len(wire))(*wire), width, (C.c_void_p * len(y))(*y), counts, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(k=0), dict(k=17, cap=(1,) * 17), dict(experts=0), dict(sources=0), dict(seg=None), dict(seg=P + 4), dict(cap=(2 ** 31,)),
-    dict(wire=(None,)), dict(wire=(P + 8,)), dict(y=(None,)), dict(y=(P + 1,)), dict(width=0), dict(width=32769),
+    dict(wire=(None,)), dict(wire=(P + 8,)), dict(y=(None,)), dict(y=(P + 1,)), dict(width=0), dict(width=32769), dict(counts=P + 4),
 ])
 def test_widen_refuses(bad):
     assert widen(**bad) == BAD

@@ -253,6 +253,19 @@ def test_widen(width, caps, counts):
         ys[d].check()
 
 
+@pytest.mark.parametrize("k,caps", [(1, [4]), (3, [5, 0, 9]), (16, [2] * 16), (2, [0, 0])])
+def test_widen_turns_the_counts_of_its_rows(k, caps):
+    """Counts in elements of the rows that were moved become counts in elements of y."""
+    width = 200
+    n = hoc.wire8_bytes(width)
+    wire = [torch.zeros(c, n, dtype=torch.uint8, device=DEV) for c in caps]
+    rows = torch.arange(k * k, device=DEV).view(k, k) * 1000003
+    counts = rows * (n // 2)
+    hoc.expert_widen(wire, torch.zeros(k, 2, dtype=torch.int64, device=DEV), [torch.empty(c, width, dtype=BF, device=DEV) for c in caps],
+                     counts=counts)
+    assert torch.equal(counts, rows * width)
+
+
 def test_widen_of_every_8_bit_value():
     wire = torch.zeros(1, hoc.wire8_bytes(256), dtype=torch.uint8, device=DEV)
     wire[0, :256] = torch.arange(256, device=DEV).to(torch.uint8)
