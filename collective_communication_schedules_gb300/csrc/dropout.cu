@@ -18,6 +18,8 @@ struct DropArgs {
   int64_t width;
   unsigned t;                    // dropped where the element's bits are below this
   float keep;                    // 65536 / (65536 - t)
+  // i / width of i below 2^31 as (umulhi(magic, i) + i) >> shift (Granlund and Montgomery, 1994)
+  unsigned magic, shift;
 };
 
 // Philox4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw, 2011).
@@ -54,7 +56,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
 #pragma unroll
   for (int u = 0; u < kDropAhead; ++u) {
     const int64_t i = (first + u * kDropThreads) * 8;
-    if (LIE != kRun) row[u] = i < (int64_t(1) << 32) ? int64_t(unsigned(i) / unsigned(A.width)) : i / A.width;
+    if (LIE != kRun) row[u] = A.total < (int64_t(1) << 31) ? int64_t((__umulhi(A.magic, unsigned(i)) + unsigned(i)) >> A.shift) : i / A.width;
     col[u] = LIE == kRun ? i : i - row[u] * A.width;
     if (LIE != kAnyhow && i < A.total) {
 #pragma unroll
@@ -143,8 +145,11 @@ extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, con
   if (none) return HOC_SUCCESS;
   const int64_t total = int64_t(rows) * width;
   const int t = int(*p * 65536 + 0.5) < 65535 ? int(*p * 65536 + 0.5) : 65535;
+  unsigned shift = 0;
+  while ((int64_t(1) << shift) < width) ++shift;
+  const unsigned magic = unsigned(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - uint64_t(width))) / uint64_t(width) + 1);
   const DropArgs A{x, residual, y, seed, int64_t(ldx), int64_t(ldr), int64_t(ldy), total, width, unsigned(t),
-                   65536.f / float(65536 - t)};
+                   65536.f / float(65536 - t), magic, shift};
   const int64_t ctas = ((total + 7) / 8 + kDropThreads * kDropAhead - 1) / (kDropThreads * kDropAhead);
   if (ctas > 0x7FFFFFFF) return refuse(who, "more than 2^43 elements");
   const bool vec = vector_rows(x, ldx, b) && (!residual || vector_rows(residual, ldr, b)) && vector_rows(y, ldy, b);

@@ -2,10 +2,9 @@
 // bits (hoc_block.h).
 //
 // All are bound by their bytes.  A row is read once and stays in registers between
-// its sum of squares and its result: a thread has V vectors of 16 bytes of it, so a
-// row takes width / (V * values of a vector) threads, a warp or a CTA of its own.
-// Rows that are not whole vectors are held element by element, four of a group of 128
-// columns to a lane.
+// its sum of squares and its result.  Narrow rows take a run of lanes of a warp, so that
+// nothing but the warp has to wait; wide ones take a CTA.  Rows that are not whole
+// 16-byte vectors are read element by element.
 #include <atomic>
 
 #include <cuda_fp8.h>
@@ -35,7 +34,19 @@ struct NormArgs {
   int rows, width;
   float eps;
   int w32;  // weights are binary32
+  int log;  // 2^log lanes take a row; -1: a CTA does
 };
+
+// The threads of a row: `count` of them, of which this is number `at`.
+struct RowThreads {
+  int64_t row;
+  int at, count;
+};
+__device__ __forceinline__ RowThreads row_threads_of(int log) {
+  const int t = threadIdx.x;
+  if (log < 0) return {int64_t(blockIdx.x), t, int(blockDim.x)};
+  return {(int64_t(blockIdx.x) * blockDim.x + t) >> log, t & ((1 << log) - 1), 1 << log};
+}
 
 // N weights from column c on.
 template <int N>
@@ -62,10 +73,13 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The sum over the row's threads: a warp, or the CTA (sh: one entry per warp).
-__device__ __forceinline__ float row_sum(float v, float* sh) {
+// The sum over the row's threads: 2^log lanes, or the CTA (sh: one entry per warp).
+__device__ __forceinline__ float row_sum(float v, int log, float* sh) {
+  if (log >= 0) {
+    for (int off = 1 << log >> 1; off; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+    return v;
+  }
   v = warp_sum(v);
-  if (blockDim.x == 32) return v;
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
   __syncthreads();
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -76,22 +90,21 @@ __device__ __forceinline__ unsigned e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// One row a warp (blockDim (32, rows)) or a CTA.
 template <class T, int V, bool RES, bool WIRE>
 __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs A) {
   constexpr int N = 16 / sizeof(T);
   __shared__ float sh[32];
   after_the_last();
-  const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (row >= A.rows) return;  // (a warp of its own: there is no barrier)
-  const int nvec = A.width / N, tpr = blockDim.x;
+  const RowThreads R = row_threads_of(A.log);
+  const bool there = R.row < A.rows;
+  auto column = [&](int j) { return (j * R.count + R.at) * N; };
   Vec<T, N> x[V], r[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int c = (j * tpr + int(threadIdx.x)) * N;
-    if (c < A.width) {
-      x[j] = *reinterpret_cast<const Vec<T, N>*>(static_cast<const T*>(A.x) + row * A.ldx + c);
-      if (RES) r[j] = *reinterpret_cast<const Vec<T, N>*>(static_cast<const T*>(A.r) + row * A.ldr + c);
+    const int c = column(j);
+    if (there && c < A.width) {
+      x[j] = *reinterpret_cast<const Vec<T, N>*>(static_cast<const T*>(A.x) + R.row * A.ldx + c);
+      if (RES) r[j] = *reinterpret_cast<const Vec<T, N>*>(static_cast<const T*>(A.r) + R.row * A.ldr + c);
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) x[j].v[e] = r[j].v[e] = narrow<T>(0.f);
@@ -108,17 +121,16 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
     }
   if (RES && A.h) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * tpr + int(threadIdx.x)) * N;
-      if (c < A.width) *reinterpret_cast<Vec<T, N>*>(static_cast<T*>(A.h) + row * A.ldh + c) = x[j];
-    }
+    for (int j = 0; j < V; ++j)
+      if (there && column(j) < A.width)
+        *reinterpret_cast<Vec<T, N>*>(static_cast<T*>(A.h) + R.row * A.ldh + column(j)) = x[j];
   }
-  sum = row_sum(sum, sh);
+  sum = row_sum(sum, A.log, sh);
   const float s = rsqrtf(sum / float(A.width) + A.eps);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int i = j * tpr + int(threadIdx.x), c = i * N;
-    const bool in = i < nvec;
+    const int c = column(j), i = c / N;
+    const bool in = there && c < A.width;
     float w[N], y[N];
     if (in) load_weights<N>(A.w, A.w32, c, w);
 #pragma unroll
@@ -127,17 +139,18 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
       Vec<T, N> o;
 #pragma unroll
       for (int e = 0; e < N; ++e) o.v[e] = narrow<T>(y[e]);
-      *reinterpret_cast<Vec<T, N>*>(static_cast<T*>(A.y) + row * A.ldy + c) = o;
+      *reinterpret_cast<Vec<T, N>*>(static_cast<T*>(A.y) + R.row * A.ldy + c) = o;
     }
-    if (WIRE) {  // a group is kGroup / N neighbouring lanes: rows of threads are whole warps
+    if (WIRE) {  // a group is kGroup / N neighbouring lanes, or the whole of a narrower row
       float most = 0.f;
 #pragma unroll
       for (int e = 0; e < N; ++e) most = fmaxf(most, fabsf(y[e]));
 #pragma unroll
-      for (int off = kGroup / N / 2; off; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
+      for (int off = kGroup / N / 2; off; off >>= 1)
+        if (off < R.count) most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
       const float scale = fmaxf(most / kE4m3Most, kLeastScale), inv = 1.f / scale;
       if (in) {
-        uint8_t* to = A.wire + row * wire_bytes(A.width);
+        uint8_t* to = A.wire + R.row * wire_bytes(A.width);
         if (i % (kGroup / N) == 0) *reinterpret_cast<float*>(to + scales_at(A.width) + i / (kGroup / N) * 4) = scale;
         uint32_t q[N / 4];
 #pragma unroll
@@ -150,32 +163,41 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
   }
 }
 
-// Any width and alignment, one row a CTA: warp w has the groups w, w + warps, .., U of
-// them at most, a lane the columns lane, lane + 32, .. of a group.
-template <class T, int U>
-__global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ NormArgs A) {
+// Any width and alignment.  A row's warp w has the groups w, w + warps, .., U of them at most, a
+// lane the columns lane, lane + 32, .. of a group.
+template <class T, int U, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_any_kernel(const __grid_constant__ NormArgs A) {
   __shared__ float sh[32];
   after_the_last();
-  const int64_t row = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const T* x = static_cast<const T*>(A.x) + row * A.ldx;
-  const T* r = static_cast<const T*>(A.r) + row * A.ldr;
-  T v[U][4];
+  const RowThreads R = row_threads_of(A.log);
+  const bool there = R.row < A.rows;
+  const int warp = R.at >> 5, lane = R.at & 31, warps = R.count >> 5;
+  const T* x = static_cast<const T*>(A.x) + R.row * A.ldx;
+  const T* r = static_cast<const T*>(A.r) + R.row * A.ldr;
+  T v[U][4], rv[U][4];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int c = (warp + u * warps) * kGroup + e * 32 + lane;
-      v[u][e] = c < A.width ? x[c] : narrow<T>(0.f);
-      if (A.r && c < A.width) v[u][e] = narrow<T>(widen(v[u][e]) + widen(r[c]));
+      const bool in = there && c < A.width;
+      v[u][e] = in ? x[c] : narrow<T>(0.f);
+      rv[u][e] = in && A.r ? r[c] : narrow<T>(0.f);
     }
+  if (A.r) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[u][e] = narrow<T>(widen(v[u][e]) + widen(rv[u][e]));
+  }
   float sum = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum = fmaf(widen(v[u][e]), widen(v[u][e]), sum);
-  sum = row_sum(sum, sh);
+  sum = row_sum(sum, A.log, sh);
   const float s = rsqrtf(sum / float(A.width) + A.eps);
+  if (!there) return;  // (a warp of its own)
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int g = warp + u * warps;
@@ -188,8 +210,8 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
       if (c < A.width) {
         const float w = A.w32 ? static_cast<const float*>(A.w)[c] : widen(static_cast<const __nv_bfloat16*>(A.w)[c]);
         y[e] = widen(v[u][e]) * s * w;
-        if (A.h) static_cast<T*>(A.h)[row * A.ldh + c] = v[u][e];
-        if (A.y) static_cast<T*>(A.y)[row * A.ldy + c] = narrow<T>(y[e]);
+        if (A.h) static_cast<T*>(A.h)[R.row * A.ldh + c] = v[u][e];
+        if (A.y) static_cast<T*>(A.y)[R.row * A.ldy + c] = narrow<T>(y[e]);
       }
       most = fmaxf(most, fabsf(y[e]));
     }
@@ -197,7 +219,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
 #pragma unroll
     for (int off = 16; off; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
     const float scale = fmaxf(most / kE4m3Most, kLeastScale), inv = 1.f / scale;
-    uint8_t* to = A.wire + row * wire_bytes(A.width);
+    uint8_t* to = A.wire + R.row * wire_bytes(A.width);
     if (lane == 0) *reinterpret_cast<float*>(to + scales_at(A.width) + g * 4) = scale;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -218,12 +240,20 @@ struct NormGradArgs {
   int rows, width;
   float eps;
   int w32;
+  int log;  // 2^log lanes take a row; -1: a CTA does
 };
 
-// The sums of two values over the row's threads.  Both go through one tree: the lower half
-// of a warp adds up the first, the upper the second.  sh: [2][16], an entry per warp for each,
-// 0 for the warps there are none of.
-__device__ __forceinline__ float2 row_sum2(float a, float b, float* sh) {
+// The sums of two values over the row's threads.  In a CTA both go through one tree: the
+// lower half of a warp adds up the first, the upper the second.  sh: [2][16], an entry per
+// warp for each, 0 for the warps there are none of.
+__device__ __forceinline__ float2 row_sum2(float a, float b, int log, float* sh) {
+  if (log >= 0) {
+    for (int off = 1 << log >> 1; off; off >>= 1) {
+      a += __shfl_xor_sync(kAll, a, off);
+      b += __shfl_xor_sync(kAll, b, off);
+    }
+    return make_float2(a, b);
+  }
   const int lane = threadIdx.x & 31;
   const bool low = lane < 16;
   float v = (low ? a : b) + __shfl_xor_sync(kAll, low ? b : a, 16);
@@ -238,42 +268,55 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float* sh) {
   return low ? make_float2(v, w) : make_float2(w, v);
 }
 
-// A thread's part of a row: dy + dy2 and h widened, dres as it came.
-template <class T, int V>
-struct GradRow {
-  static constexpr int N = 16 / sizeof(T);
-  float d[V][N], h[V][N];
-  Vec<T, N> dres[V];
-};
+// N sums, in vectors of 16 bytes where there are more than one.
+template <int N>
+__device__ __forceinline__ void store_sums(float* to, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    *to = v[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  }
+}
 
 __device__ __forceinline__ void copy_ahead(void* to, const void* from) {  // 16 bytes, past L1
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(to))), "l"(from) : "memory");
 }
 
-// A CTA takes the rows blockIdx.x, + gridDim.x, ..; a thread has the same columns of
-// each, so that it sums the weight gradient over them in registers.  With S > 0 the next S - 1
-// rows are on their way into shared memory while one is worked on: a thread fetches
-// what it reads itself, so that nothing but its own copies has to be waited for.
-template <class T, int V, int S>
-__global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const __grid_constant__ NormGradArgs A) {
-  constexpr int N = 16 / sizeof(T);
+// A row takes 2^log lanes or a CTA; rows are handed out in turn, and a thread has the same
+// columns of each, so that it sums the weight gradient over them in registers.  Rows of whole
+// vectors (N values): the next S - 1 rows are on their way into shared memory while one is
+// worked on; a thread fetches what it reads itself, so that nothing but its own copies
+// has to be waited for.  Other rows: N = 1, S = 0, everything of a row is loaded at once.
+template <class T, int N, int V, int S, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const __grid_constant__ NormGradArgs A) {
   using Q = Vec<T, N>;
   extern __shared__ uint4 ring[];  // [S][arrays][V][threads]
   __shared__ float sh[2][32];
-  if (threadIdx.x < 64) sh[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
-  if (blockDim.x < 64) sh[1][threadIdx.x] = 0.f;
+  for (int i = threadIdx.x; i < 64; i += blockDim.x) sh[i >> 5][i & 31] = 0.f;
   __syncthreads();
   after_the_last();
   const int threads = blockDim.x, two = A.dy2 != nullptr, arrays = 2 + two + (A.dres != nullptr);
-  auto column = [&](int j) { return (j * threads + int(threadIdx.x)) * N; };
+  const RowThreads R = row_threads_of(A.log);
+  const int64_t step = A.log < 0 ? int64_t(gridDim.x) : int64_t(gridDim.x) * threads >> A.log;
+  auto column = [&](int j) { return (j * R.count + R.at) * N; };
   float w[V][N], acc[V][N];
+  auto weights = [&]() {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < V; ++j) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) w[j][e] = acc[j][e] = 0.f;
-    if (column(j) < A.width) load_weights<N>(A.w, A.w32, column(j), w[j]);
-  }
-  auto at = [&](const void* base, int64_t ld, int64_t row, int j) { return static_cast<const T*>(base) + row * ld + column(j); };
+      for (int e = 0; e < N; ++e) w[j][e] = 0.f;
+      if (column(j) < A.width) load_weights<N>(A.w, A.w32, column(j), w[j]);
+    }
+  };
+  if (N > 1) weights();
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[j][e] = 0.f;
+  auto at = [&](const void* base, int64_t ld, int64_t row, int j) {
+    return reinterpret_cast<const Q*>(static_cast<const T*>(base) + row * ld + column(j));
+  };
   auto fetch = [&](int64_t row, int stage) {
     uint4* to = ring + size_t(stage) * arrays * V * threads + threadIdx.x;
     if (row < A.rows) {
@@ -288,43 +331,59 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const __grid_co
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  int64_t row = blockIdx.x;
   if constexpr (S > 0) {
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) fetch(row + int64_t(i) * gridDim.x, i);
+    for (int i = 0; i < S - 1; ++i) fetch(R.row + i * step, i);
   }
   const float inv = 1.f / float(A.width);
   int turn = 0, stage = 0;
-  for (; row < A.rows; row += gridDim.x, turn ^= 1) {
-    GradRow<T, V> R;
-    Q x[V], y[V], x2[V];
+  // (a warp's lanes go round together, also those whose rows have ended)
+  auto any_left = [&](int64_t row) { return A.log < 0 ? row < A.rows : bool(__any_sync(kAll, row < A.rows)); };
+  for (int64_t row = R.row; any_left(row); row += step, turn ^= 1) {
+    const bool there = row < A.rows;
+    float d[V][N], h[V][N];
+    Q dres[V];
     if constexpr (S > 0) {
-      fetch(row + int64_t(S - 1) * gridDim.x, stage == 0 ? S - 1 : stage - 1);  // (read a turn ago, by this thread)
+      fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);  // (read a turn ago, by this thread)
       asm volatile("cp.async.wait_group %0;" ::"n"(S > 0 ? S - 1 : 0) : "memory");
       const uint4* from = ring + size_t(stage) * arrays * V * threads + threadIdx.x;
+      Q x2[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const bool in = column(j) < A.width;
+        const bool in = there && column(j) < A.width;
         const uint4 zero = make_uint4(0, 0, 0, 0);
-        const uint4 a = in ? from[j * threads] : zero, b = in ? from[(V + j) * threads] : zero;
-        const uint4 c = in && A.dy2 ? from[(2 * V + j) * threads] : zero;
-        const uint4 d = in && A.dres ? from[((2 + two) * V + j) * threads] : zero;
-        x[j] = *reinterpret_cast<const Q*>(&a);
-        y[j] = *reinterpret_cast<const Q*>(&b);
-        x2[j] = *reinterpret_cast<const Q*>(&c);
-        R.dres[j] = *reinterpret_cast<const Q*>(&d);
+        const uint4 qx = in ? from[j * threads] : zero, qh = in ? from[(V + j) * threads] : zero;
+        const uint4 q2 = in && A.dy2 ? from[(2 * V + j) * threads] : zero;
+        const uint4 qr = in && A.dres ? from[((2 + two) * V + j) * threads] : zero;
+        x2[j] = *reinterpret_cast<const Q*>(&q2);
+        dres[j] = *reinterpret_cast<const Q*>(&qr);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          d[j][e] = widen(reinterpret_cast<const Q*>(&qx)->v[e]);
+          h[j][e] = widen(reinterpret_cast<const Q*>(&qh)->v[e]);
+        }
+      }
+      if (A.dy2) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+          for (int e = 0; e < N; ++e) d[j][e] += widen(x2[j].v[e]);
       }
       stage = stage == S - 1 ? 0 : stage + 1;
     } else {
+      T x[V], y[V], x2[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        x[j] = y[j] = x2[j] = R.dres[j] = *reinterpret_cast<const Q*>(&zero);
-        if (column(j) >= A.width) continue;
-        x[j] = *reinterpret_cast<const Q*>(at(A.dy, A.lddy, row, j));
-        y[j] = *reinterpret_cast<const Q*>(at(A.h, A.ldh, row, j));
-        if (A.dy2) x2[j] = *reinterpret_cast<const Q*>(at(A.dy2, A.lddy2, row, j));
-        if (A.dres) R.dres[j] = *reinterpret_cast<const Q*>(at(A.dres, A.lddres, row, j));
+        const bool in = there && column(j) < A.width;
+        x[j] = in ? at(A.dy, A.lddy, row, j)->v[0] : narrow<T>(0.f);
+        y[j] = in ? at(A.h, A.ldh, row, j)->v[0] : narrow<T>(0.f);
+        x2[j] = in && A.dy2 ? at(A.dy2, A.lddy2, row, j)->v[0] : narrow<T>(0.f);
+      }
+      weights();
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        d[j][0] = A.dy2 ? widen(x[j]) + widen(x2[j]) : widen(x[j]);
+        h[j][0] = widen(y[j]);
       }
     }
     float a = 0.f, b = 0.f;
@@ -332,91 +391,131 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel(const __grid_co
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        R.h[j][e] = widen(y[j].v[e]);
-        R.d[j][e] = widen(x[j].v[e]);
+        a = fmaf(h[j][e], h[j][e], a);
+        b = fmaf(d[j][e] * w[j][e], h[j][e], b);
       }
-    if (A.dy2) {
+    const float2 t = row_sum2(a, b, A.log, sh[turn]);  // (two sets of entries: one barrier a row)
+    const float s = rsqrtf(t.x * inv + A.eps), k = -s * s * (t.y * inv);
+    if constexpr (S == 0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int e = 0; e < N; ++e) R.d[j][e] += widen(x2[j].v[e]);
+      for (int j = 0; j < V; ++j) {
+        const bool in = there && column(j) < A.width && A.dres;
+        dres[j].v[0] = in ? at(A.dres, A.lddres, row, j)->v[0] : narrow<T>(0.f);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        a = fmaf(R.h[j][e], R.h[j][e], a);
-        b = fmaf(R.d[j][e] * w[j][e], R.h[j][e], b);
-      }
-    const float2 t = row_sum2(a, b, sh[turn]);  // (two sets of entries: one barrier a row)
-    const float s = rsqrtf(t.x * inv + A.eps), k = -s * s * (t.y * inv);
-#pragma unroll
     for (int j = 0; j < V; ++j) {
-      if (column(j) >= A.width) continue;
       Q o;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float hs = R.h[j][e] * s;
-        acc[j][e] = fmaf(R.d[j][e], hs, acc[j][e]);
-        o.v[e] = narrow<T>(fmaf(s, R.d[j][e] * w[j][e], fmaf(hs, k, widen(R.dres[j].v[e]))));
+        const float hs = h[j][e] * s;
+        acc[j][e] = fmaf(d[j][e], there ? hs : 0.f, acc[j][e]);
+        o.v[e] = narrow<T>(fmaf(s, d[j][e] * w[j][e], fmaf(hs, k, widen(dres[j].v[e]))));
       }
-      *reinterpret_cast<Q*>(static_cast<T*>(A.dx) + row * A.lddx + column(j)) = o;
+      if (there && column(j) < A.width) *reinterpret_cast<Q*>(static_cast<T*>(A.dx) + row * A.lddx + column(j)) = o;
     }
   }
   if (!A.part) return;
+  float* part = A.part + int64_t(blockIdx.x) * A.width;
+  if (A.log < 0) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if (column(j) >= A.width) continue;
-#pragma unroll
-    for (int e = 0; e < N; e += 4)
-      *reinterpret_cast<float4*>(A.part + int64_t(blockIdx.x) * A.width + column(j) + e) =
-          make_float4(acc[j][e], acc[j][e + 1], acc[j][e + 2], acc[j][e + 3]);
+    for (int j = 0; j < V; ++j) {
+      if (column(j) < A.width) store_sums<N>(part + column(j), acc[j]);
+    }
+    return;
   }
+  // the lanes that have the same columns, then the warps, one after the other
+  float* sums = reinterpret_cast<float*>(ring);  // [width]; nothing is on its way any more
+  asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      for (int off = R.count; off < 32; off <<= 1) acc[j][e] += __shfl_xor_sync(kAll, acc[j][e], off);
+  for (int warp = 0; warp < threads >> 5; ++warp) {
+    __syncthreads();
+    if (int(threadIdx.x) >> 5 != warp || (int(threadIdx.x) & 31) >= R.count) continue;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (column(j) < A.width) sums[column(j) + e] = warp ? sums[column(j) + e] + acc[j][e] : acc[j][e];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < A.width; c += threads) part[c] = sums[c];
 }
 
-// Any width and alignment: a thread has the columns threadIdx.x, + blockDim.x, .. and reads
-// them again for the second use; its sums for the weight gradient are in shared memory.
-template <class T>
-__global__ void __launch_bounds__(kGradThreads) norm_grad_any_kernel(const __grid_constant__ NormGradArgs A) {
-  extern __shared__ float acc[];  // [width]; none where the weight gradient is not wanted
-  __shared__ float sh[2][32];
-  if (threadIdx.x < 64) sh[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
-  if (blockDim.x < 64) sh[1][threadIdx.x] = 0.f;
-  __syncthreads();
+// Rows that do not fit the registers of a CTA's threads: read twice, the second time from L2.  V
+// vectors of N values to a thread.
+constexpr int kWideThreads = 1024;
+template <class T, int N, int V>
+__global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __grid_constant__ NormGradArgs A) {
+  using Q = Vec<T, N>;
+  __shared__ float sh[32];
   after_the_last();
-  const int step = blockDim.x;
-  if (A.part)
-    for (int c = threadIdx.x; c < A.width; c += step) acc[c] = 0.f;
-  auto weight = [&](int c) {
-    return A.w32 ? static_cast<const float*>(A.w)[c] : widen(static_cast<const __nv_bfloat16*>(A.w)[c]);
-  };
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
+  float acc[V][N] = {};
+  const float inv = 1.f / float(A.width);
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
     const T* dy = static_cast<const T*>(A.dy) + row * A.lddy;
     const T* dy2 = static_cast<const T*>(A.dy2) + row * A.lddy2;
     const T* hh = static_cast<const T*>(A.h) + row * A.ldh;
     const T* dres = static_cast<const T*>(A.dres) + row * A.lddres;
     T* dx = static_cast<T*>(A.dx) + row * A.lddx;
     float a = 0.f, b = 0.f;
-#pragma unroll 4
-    for (int c = threadIdx.x; c < A.width; c += step) {
-      const float h = widen(hh[c]), d = widen(dy[c]) + (A.dy2 ? widen(dy2[c]) : 0.f);
-      a = fmaf(h, h, a);
-      b = fmaf(d * weight(c), h, b);
+    auto load = [&](int c, float (&d)[N], float (&h)[N], float (&w)[N]) {
+      const Q x = *reinterpret_cast<const Q*>(dy + c), y = *reinterpret_cast<const Q*>(hh + c);
+      load_weights<N>(A.w, A.w32, c, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        d[e] = widen(x.v[e]);
+        h[e] = widen(y.v[e]);
+      }
+      if (A.dy2) {
+        const Q x2 = *reinterpret_cast<const Q*>(dy2 + c);
+#pragma unroll
+        for (int e = 0; e < N; ++e) d[e] += widen(x2.v[e]);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (j * kWideThreads + int(threadIdx.x)) * N;
+      if (c >= A.width) continue;
+      float d[N], h[N], w[N];
+      load(c, d, h, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        a = fmaf(h[e], h[e], a);
+        b = fmaf(d[e] * w[e], h[e], b);
+      }
     }
-    const float2 t = row_sum2(a, b, sh[turn]);
-    const float s = rsqrtf(t.x / float(A.width) + A.eps), k = s * s * (t.y / float(A.width));
-#pragma unroll 4
-    for (int c = threadIdx.x; c < A.width; c += step) {
-      const float h = widen(hh[c]), d = widen(dy[c]) + (A.dy2 ? widen(dy2[c]) : 0.f);
-      if (A.part) acc[c] = fmaf(d, h * s, acc[c]);
-      float g = s * (d * weight(c) - h * k);
-      if (A.dres) g += widen(dres[c]);
-      dx[c] = narrow<T>(g);
+    __syncthreads();  // sh is read no more
+    const float ta = row_sum(a, -1, sh);
+    __syncthreads();
+    const float tb = row_sum(b, -1, sh);
+    const float s = rsqrtf(ta * inv + A.eps), k = -s * s * (tb * inv);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (j * kWideThreads + int(threadIdx.x)) * N;
+      if (c >= A.width) continue;
+      float d[N], h[N], w[N];
+      load(c, d, h, w);
+      Q r = {}, o;
+      if (A.dres) r = *reinterpret_cast<const Q*>(dres + c);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float hs = h[e] * s;
+        acc[j][e] = fmaf(d[e], hs, acc[j][e]);
+        o.v[e] = narrow<T>(fmaf(s, d[e] * w[e], fmaf(hs, k, A.dres ? widen(r.v[e]) : 0.f)));
+      }
+      *reinterpret_cast<Q*>(dx + c) = o;
     }
   }
-  if (A.part)
-    for (int c = threadIdx.x; c < A.width; c += step) A.part[int64_t(blockIdx.x) * A.width + c] = acc[c];
+  if (!A.part) return;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = (j * kWideThreads + int(threadIdx.x)) * N;
+    if (c < A.width) store_sums<N>(A.part + int64_t(blockIdx.x) * A.width + c, acc[j]);
+  }
 }
 
 // dw (+)= sum over the parts, 32 columns a CTA, in an order that depends on the parts
@@ -428,15 +527,20 @@ __global__ void __launch_bounds__(32 * kSumRows) norm_weight_kernel(const float*
   __shared__ float sh[kSumRows][33];
   after_the_last();
   const int c = blockIdx.x * 32 + int(threadIdx.x);
-  float sum[4] = {};
+  constexpr int kAhead = 8;
+  float sum = 0.f;
   if (c < width) {
-    int p = threadIdx.y;
-    for (; p + 3 * kSumRows < parts; p += 4 * kSumRows)
+    for (int p0 = threadIdx.y; p0 < parts; p0 += kAhead * kSumRows) {
+      float v[kAhead];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sum[u] += part[int64_t(p + u * kSumRows) * width + c];
-    for (; p < parts; p += kSumRows) sum[0] += part[int64_t(p) * width + c];
+      for (int u = 0; u < kAhead; ++u) {
+        const int p = p0 + u * kSumRows;
+        v[u] = p < parts ? part[int64_t(p) * width + c] : 0.f;
+      }
+      sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
   }
-  sh[threadIdx.y][threadIdx.x] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  sh[threadIdx.y][threadIdx.x] = sum;
   __syncthreads();
   if (threadIdx.y == 0 && c < width) {
     float v = 0.f;
@@ -534,40 +638,67 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------ host side
-// Threads of a row that is `nvec` vectors, V to a thread: a warp, or whole warps.
-int row_threads(int nvec, int v) { return (nvec + 32 * v - 1) / (32 * v) * 32; }
+// Whole warps for a row that is `n` pieces, v to a thread.
+int row_threads(int n, int v) { return (n + 32 * v - 1) / (32 * v) * 32; }
+
+// The lanes that n pieces take, v to a lane, as a power of two; -1: more than a warp.
+int row_log(int n, int v) {
+  int log = 0;
+  while (log < 5 && (v << log) < n) ++log;
+  return (v << log) < n ? -1 : log;
+}
+
+constexpr int kNarrowThreads = 256;  // of a CTA whose rows take lanes
+
+// CTAs for `rows` rows.
+dim3 row_grid(int rows, int log, int threads) {
+  return dim3(unsigned(log < 0 ? rows : ((int64_t(rows) << log) + threads - 1) / threads));
+}
 
 template <class T, int V>
-cudaError_t launch_norm(const NormArgs& A, cudaStream_t s) {
-  const int tpr = row_threads(A.width / int(16 / sizeof(T)), V);
-  const dim3 cta = tpr > 32 ? dim3(tpr, 1) : dim3(32, 8);
-  const dim3 grid(unsigned((int64_t(A.rows) + cta.y - 1) / cta.y));
+cudaError_t launch_norm(NormArgs A, cudaStream_t s) {
+  const int nvec = A.width / int(16 / sizeof(T));
+  A.log = row_log(nvec, V);
+  const int threads = A.log < 0 ? row_threads(nvec, V) : kNarrowThreads;
   const auto kernel = A.r ? A.wire ? norm_kernel<T, V, true, true> : norm_kernel<T, V, true, false>
                           : A.wire ? norm_kernel<T, V, false, true> : norm_kernel<T, V, false, false>;
-  return launch(kernel, grid, cta, 0, s, A);
+  return launch(kernel, row_grid(A.rows, A.log, threads), dim3(threads), 0, s, A);
+}
+
+template <class T, int U, int THREADS>
+cudaError_t launch_norm_any(NormArgs A, cudaStream_t s) {
+  const int groups = (A.width + kGroup - 1) / kGroup, warps = (groups + U - 1) / U;
+  A.log = warps > 1 ? -1 : 5;
+  const int threads = warps > 1 ? warps * 32 : kNarrowThreads;
+  return launch(norm_any_kernel<T, U, THREADS>, row_grid(A.rows, A.log, threads), dim3(threads), 0, s, A);
 }
 
 template <class T>
 cudaError_t start_norm(const NormArgs& A, bool vec, cudaStream_t s) {
   const int nvec = A.width / int(16 / sizeof(T));
   if (vec && nvec <= 4096) {
-    if (nvec <= 1024) return launch_norm<T, 1>(A, s);
+    if (nvec <= 32) return launch_norm<T, 1>(A, s);
+    // two vectors of each operand keep enough of them on their way; NORM_V
+    if (nvec <= 64 || (nvec > 128 && nvec <= 2048)) return launch_norm<T, 2>(A, s);
     return launch_norm<T, 4>(A, s);
   }
   const int groups = (A.width + kGroup - 1) / kGroup;
-  const dim3 grid{unsigned(A.rows)};
-  if (groups <= 32) return launch(norm_any_kernel<T, 1>, grid, dim3(groups * 32), 0, s, A);
-  return launch(norm_any_kernel<T, 8>, grid, dim3(1024), 0, s, A);
+  if (groups <= 1) return launch_norm_any<T, 1, kNarrowThreads>(A, s);
+  if (groups <= 4) return launch_norm_any<T, 4, kNarrowThreads>(A, s);
+  if (groups <= 8) return launch_norm_any<T, 8, kNarrowThreads>(A, s);
+  if (groups <= 128) return launch_norm_any<T, 4, 1024>(A, s);
+  return launch_norm_any<T, 8, 1024>(A, s);
 }
 
 constexpr int kMostParts = kSms * 8;
 
-// CTAs of the gradient's kernel: what is resident at once.
-int grad_parts(int rows, int threads, size_t smem) {
-  int each = int(size_t(220) * 1024 / (smem + 2048)), regs = 640 / threads;  // (up to 100 registers a thread)
+// CTAs of the gradient's kernel: what is resident at once, of about 100 registers a thread.
+int grad_parts(int rows, int log, int threads, size_t smem) {
+  int each = int(size_t(220) * 1024 / (smem + 2048)), regs = 640 / threads;
   each = each < regs ? each : regs;
   const int most = kSms * (each > 8 ? 8 : each < 1 ? 1 : each);
-  return rows < most ? rows < 1 ? 1 : rows : most;
+  const int want = log < 0 ? rows : int(((int64_t(rows) << log) + threads - 1) / threads);
+  return want < most ? want < 1 ? 1 : want : most;
 }
 
 // More shared memory than a kernel has without asking (48 KiB, its own variables among them), once
@@ -584,37 +715,46 @@ cudaError_t opt_in(Kernel kernel, size_t smem, std::atomic<uint64_t>& done) {
 }
 
 constexpr size_t kMostRing = 200 * 1024;
+constexpr int kGradNarrow = 128;  // threads of a CTA whose rows take lanes
 
-template <class T, int V, int S>
-cudaError_t launch_grad(const NormGradArgs& A, cudaStream_t s, int* parts) {
+template <class T, int N, int V, int S, int THREADS = kGradThreads>
+cudaError_t launch_grad(NormGradArgs A, cudaStream_t s, int* parts) {
   static std::atomic<uint64_t> done{0};
-  const int threads = row_threads(A.width / int(16 / sizeof(T)), V);
-  const size_t smem = size_t(S) * (2 + (A.dy2 != nullptr) + (A.dres != nullptr)) * V * threads * 16;
-  *parts = grad_parts(A.rows, threads, smem);
+  const int pieces = (A.width + N - 1) / N;
+  A.log = row_log(pieces, V);
+  const int threads = A.log < 0 ? row_threads(pieces, V) : kGradNarrow;
+  size_t smem = size_t(S) * (2 + (A.dy2 != nullptr) + (A.dres != nullptr)) * V * threads * 16;
+  if (A.log >= 0 && smem < A.width * sizeof(float)) smem = A.width * sizeof(float);  // for the sums at the end
+  *parts = grad_parts(A.rows, A.log, threads, smem);
   if (smem > kSmemAsIs) {
-    const cudaError_t e = opt_in(norm_grad_kernel<T, V, S>, kMostRing, done);
+    const cudaError_t e = opt_in(norm_grad_kernel<T, N, V, S, THREADS>, kMostRing, done);
     if (e != cudaSuccess) return e;
   }
-  return launch(norm_grad_kernel<T, V, S>, dim3(*parts), dim3(threads), smem, s, A);
+  return launch(norm_grad_kernel<T, N, V, S, THREADS>, dim3(*parts), dim3(threads), smem, s, A);
+}
+
+template <class T, int N, int V>
+cudaError_t launch_grad_wide(const NormGradArgs& A, cudaStream_t s, int* parts) {
+  *parts = A.rows < kSms ? A.rows < 1 ? 1 : A.rows : kSms;
+  return launch(norm_grad_wide_kernel<T, N, V>, dim3(*parts), dim3(kWideThreads), 0, s, A);
 }
 
 template <class T>
 cudaError_t start_grad(const NormGradArgs& A, bool vec, cudaStream_t s, int* parts) {
-  const int nvec = A.width / int(16 / sizeof(T));
-  if (vec && nvec <= 4 * kGradThreads) {
-    if (nvec <= 256) return launch_grad<T, 2, 4>(A, s, parts);
-    if (nvec <= 2 * kGradThreads) return launch_grad<T, 2, 3>(A, s, parts);
-    return launch_grad<T, 4, 0>(A, s, parts);
+  constexpr int N = 16 / sizeof(T);
+  const int nvec = A.width / N;
+  if (vec) {
+    if (nvec <= 32) return launch_grad<T, N, 1, 4>(A, s, parts);
+    if (nvec <= 256) return launch_grad<T, N, 2, 4>(A, s, parts);
+    if (nvec <= 2 * kGradThreads) return launch_grad<T, N, 2, 3>(A, s, parts);
+    if (nvec <= 4 * kWideThreads) return launch_grad_wide<T, N, 4>(A, s, parts);
+    return launch_grad_wide<T, N, 8>(A, s, parts);
   }
-  const int threads = A.width >= kGradThreads ? kGradThreads : (A.width + 31) / 32 * 32;
-  const size_t smem = A.part ? size_t(A.width) * sizeof(float) : 0;
-  *parts = grad_parts(A.rows, threads, smem);
-  if (smem > kSmemAsIs) {
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = opt_in(norm_grad_any_kernel<T>, size_t(kMaxWidth) * sizeof(float), done);
-    if (e != cudaSuccess) return e;
-  }
-  return launch(norm_grad_any_kernel<T>, dim3(*parts), dim3(threads), smem, s, A);
+  if (A.width <= 128) return launch_grad<T, 1, 4, 0, kGradNarrow>(A, s, parts);
+  if (A.width <= 512) return launch_grad<T, 1, 16, 0, kGradNarrow>(A, s, parts);
+  if (A.width <= 1024) return launch_grad<T, 1, 32, 0, kGradNarrow>(A, s, parts);
+  if (A.width <= 16 * kGradThreads) return launch_grad<T, 1, 16, 0>(A, s, parts);
+  return launch_grad_wide<T, 1, 32>(A, s, parts);
 }
 
 }  // namespace
@@ -624,18 +764,24 @@ cudaError_t norm_preload() {
       reinterpret_cast<const void*>(&widen_kernel<16>), reinterpret_cast<const void*>(&widen_kernel<8>),
       reinterpret_cast<const void*>(&widen_kernel<1>), reinterpret_cast<const void*>(&norm_weight_kernel<float>),
       reinterpret_cast<const void*>(&norm_weight_kernel<__nv_bfloat16>),
-#define HOC_NORM_OF(T)                                                                                               \
-  reinterpret_cast<const void*>(&norm_any_kernel<T, 1>), reinterpret_cast<const void*>(&norm_any_kernel<T, 8>),      \
-      reinterpret_cast<const void*>(&norm_grad_kernel<T, 2, 4>), reinterpret_cast<const void*>(&norm_grad_kernel<T, 2, 3>), \
-      reinterpret_cast<const void*>(&norm_grad_kernel<T, 4, 0>), reinterpret_cast<const void*>(&norm_grad_any_kernel<T>)
-#define HOC_NORM_V(T, V)                                                                                           \
-  reinterpret_cast<const void*>(&norm_kernel<T, V, false, false>),                                                 \
-      reinterpret_cast<const void*>(&norm_kernel<T, V, false, true>),                                              \
-      reinterpret_cast<const void*>(&norm_kernel<T, V, true, false>), reinterpret_cast<const void*>(&norm_kernel<T, V, true, true>)
-      HOC_NORM_OF(float), HOC_NORM_OF(__nv_bfloat16), HOC_NORM_V(float, 1), HOC_NORM_V(float, 4),
-      HOC_NORM_V(__nv_bfloat16, 1), HOC_NORM_V(__nv_bfloat16, 4)};
+#define HOC_FN(...) reinterpret_cast<const void*>(&__VA_ARGS__)
+#define HOC_NORM_V(T, V)                                                                                    \
+  HOC_FN(norm_kernel<T, V, false, false>), HOC_FN(norm_kernel<T, V, false, true>),                          \
+      HOC_FN(norm_kernel<T, V, true, false>), HOC_FN(norm_kernel<T, V, true, true>)
+#define HOC_NORM_OF(T, N)                                                                                        \
+  HOC_NORM_V(T, 1), HOC_NORM_V(T, 2), HOC_NORM_V(T, 4), HOC_FN(norm_any_kernel<T, 1, kNarrowThreads>),               \
+      HOC_FN(norm_any_kernel<T, 4, kNarrowThreads>), HOC_FN(norm_any_kernel<T, 8, kNarrowThreads>),                     \
+      HOC_FN(norm_any_kernel<T, 4, 1024>), HOC_FN(norm_any_kernel<T, 8, 1024>),                                       \
+       HOC_FN(norm_grad_kernel<T, N, 1, 4, kGradThreads>),                                                           \
+      HOC_FN(norm_grad_kernel<T, N, 2, 4, kGradThreads>), HOC_FN(norm_grad_kernel<T, N, 2, 3, kGradThreads>),           \
+      HOC_FN(norm_grad_kernel<T, 1, 4, 0, kGradNarrow>), HOC_FN(norm_grad_kernel<T, 1, 16, 0, kGradNarrow>),            \
+      HOC_FN(norm_grad_kernel<T, 1, 32, 0, kGradNarrow>), HOC_FN(norm_grad_kernel<T, 1, 16, 0, kGradThreads>),          \
+      HOC_FN(norm_grad_wide_kernel<T, N, 4>), HOC_FN(norm_grad_wide_kernel<T, N, 8>), \
+      HOC_FN(norm_grad_wide_kernel<T, 1, 32>)
+      HOC_NORM_OF(float, 4), HOC_NORM_OF(__nv_bfloat16, 8)};
 #undef HOC_NORM_OF
 #undef HOC_NORM_V
+#undef HOC_FN
   for (const void* f : fns) {
     cudaFuncAttributes a;
     const cudaError_t e = cudaFuncGetAttributes(&a, f);
@@ -675,7 +821,7 @@ extern "C" hocResult_t hoc_rms_norm(int rows, int width, hocDataType_t dtype, co
   if (bad) return refuse(who, bad);
   if (rows == 0) return HOC_SUCCESS;
   const NormArgs A{x,           residual,     weight,       h,    y,     static_cast<uint8_t*>(wire), int64_t(ldx), int64_t(ldr),
-                   int64_t(ldh), int64_t(ldy), rows, width, *eps, weight_dtype == HOC_FLOAT32};
+                   int64_t(ldh), int64_t(ldy), rows, width, *eps, weight_dtype == HOC_FLOAT32, -1};
   const bool vec = width * b % 16 == 0 && vector_rows(x, ldx, b) && (!residual || vector_rows(residual, ldr, b)) &&
                    (!h || vector_rows(h, ldh, b)) && (!y || vector_rows(y, ldy, b)) && aligned(weight, 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -717,7 +863,7 @@ extern "C" hocResult_t hoc_rms_norm_grad(int rows, int width, hocDataType_t dtyp
   if (rows == 0 && !dw) return HOC_SUCCESS;
   const NormGradArgs A{dy, dy2, h, weight, dres, dx, dw ? reinterpret_cast<float*>(workspace) : nullptr, int64_t(lddy),
                        int64_t(lddy2), int64_t(ldh), int64_t(lddres), int64_t(lddx), rows, width, *eps,
-                       weight_dtype == HOC_FLOAT32};
+                       weight_dtype == HOC_FLOAT32, -1};
   const bool vec = width * b % 16 == 0 && vector_rows(dy, lddy, b) && (!dy2 || vector_rows(dy2, lddy2, b)) &&
                    vector_rows(h, ldh, b) && (!dres || vector_rows(dres, lddres, b)) && vector_rows(dx, lddx, b) &&
                    aligned(weight, 16);

@@ -76,6 +76,10 @@ template <int L>
 __device__ __forceinline__ uint32_t most_of(uint32_t v) {
   if constexpr (L == 32) {
     return warp_most(v);
+  } else if constexpr (L == 16) {  // two reductions of a warp are fewer instructions than four exchanges
+    const bool low = (threadIdx.x & 16) == 0;
+    const uint32_t a = warp_most(low ? v : 0u), b = warp_most(low ? 0u : v);
+    return low ? a : b;
   } else {
 #pragma unroll
     for (int off = L / 2; off; off >>= 1) v = max(v, __shfl_xor_sync(kAll, v, off));
@@ -345,13 +349,15 @@ __device__ __forceinline__ void sort_keys(uint32_t (&u)[N]) {
   sort_keys<N>(u, std::make_index_sequence<n>{});
 }
 
-// The next of the token's sorted keys: its lane, and the key in *key (0: none is left).  Of
-// keys that are equal but for their places the first lane's.
+// The next of the token's sorted keys: its lane, and the key in *key (0: none is left).  The
+// lanes' first keys are compared without their places, but with the lane in their stead: of
+// equal ones the first lane's is the largest.
 template <int EPL, int L>
 __device__ __forceinline__ int pop_sorted(uint32_t (&u)[EPL], int q, uint32_t* key) {
-  const uint32_t head = u[0] ? u[0] | (EPL - 1) : 0u, m = most_of<L>(head);
-  const int winner = __ffs(lanes_of<L>(head == m)) - 1;
-  *key = EPL == 1 ? m : __shfl_sync(kAll, u[0], winner, L);
+  constexpr uint32_t kLow = (EPL > L ? EPL : L) - 1;
+  const uint32_t m = most_of<L>((u[0] & ~kLow) | uint32_t(L - 1 - q));
+  const int winner = L - 1 - int(m & (L - 1));
+  *key = __shfl_sync(kAll, u[0], winner, L);
   if (q == winner) {
 #pragma unroll
     for (int i = 0; i + 1 < EPL; ++i) u[i] = u[i + 1];
@@ -364,7 +370,8 @@ template <class T, int EPL, int L, bool SOFTMAX>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteArgs A) {
   after_the_last();
   constexpr uint32_t kPlaces = EPL - 1;
-  constexpr float kCut = float(EPL) * 0x1p-23f;  // what cutting the places' bits off may change, relative to a key
+  // what comparing keys without their last bits may change, relative to a key
+  constexpr float kCut = float(EPL > L ? EPL : L) * 0x1p-23f;
   constexpr int kTokens = 32 / L;                // of a warp
   const int lane = threadIdx.x & 31, q = lane & (L - 1);
   const bool grouped = A.top_groups < A.groups;
@@ -447,9 +454,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     const float ga = value_of(g.a & ~kPlaces), gb = value_of(g.b & ~kPlaces);
     const float score = q < A.groups ? g.b ? ga + gb : ga : -INFINITY;
     const float size = max_of<L>(q < A.groups && g.b ? fabsf(ga) + fabsf(gb) : 0.f);
-    uint32_t last, next;
-    uint32_t kept = keep_groups<L>(A.top_groups, ordered(score), q, &last, &next);
-    const bool near = next && !(value_of(last) - value_of(next) > 4.f * tol + size * (2.f * kCut + 0x1p-21f));
+    // scores with their lanes as last bits: of equal ones the first group is the largest
+    constexpr uint32_t kLane = L - 1;
+    uint32_t mark = score > -INFINITY ? (ordered(score) & ~kLane) | (kLane - q) : 0u, last = 0, kept = 0;
+    for (int r = 0; r < A.top_groups; ++r) {
+      const uint32_t m = most_of<L>(mark);
+      last = m ? m : last;
+      kept |= m ? 1u << (kLane - (m & kLane)) : 0u;
+      mark = mark == m ? 0u : mark;
+    }
+    const uint32_t next = most_of<L>(mark);
+    const bool near = next && !(value_of(last & ~kLane) - value_of(next & ~kLane) >
+                                4.f * tol + size * (2.f * kCut + float(L) * 0x1p-23f + 0x1p-21f));
     if (!runs) {
       exactly = near;
     } else if (__any_sync(kAll, near)) {
@@ -488,16 +504,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     sort_keys(u);
   }
   uint32_t key = 0;  // lane j: slot j's; slot topk is the first that is left out
-  int mine = -1;
+  int owner = 0;
   const int slots = A.topk + check;
   for (int r = 0; r < slots; ++r) {
     uint32_t k;
     const int from = pop_sorted<EPL, L>(u, q, &k);
-    if (q == r && k) {
+    if (q == r) {
       key = k;
-      mine = from * A.epl + int(kPlaces - (k & kPlaces));
+      owner = from;
     }
   }
+  int mine = key ? owner * A.epl + int(kPlaces - (key & kPlaces)) : -1;
   if (check) {
     // Keys that are near the one before them; where that holds for the first that is left out,
     // what follows it is taken too (lanes topk + 1, ..), as far as it is near the last chosen.
@@ -556,13 +573,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
         s = share(zc, top);
       } else {  // sigmoids, all divided by exp of the largest logit where that is below 0
         const float m = fminf(top, 0.f);
-        s = 1.f / (expf(m) + expf(m - zc));
+        s = __fdividef(1.f, expf(m) + expf(m - zc));
       }
     }
     const float total = sum_of<L>(s);
-    s = mine >= 0 ? s / total : 0.f;
+    s = mine >= 0 ? __fdividef(s, total) : 0.f;
   } else if (mine >= 0) {
-    s = SOFTMAX ? share(zc, most) / sum : 1.f / (1.f + expf(-zc));
+    s = SOFTMAX ? __fdividef(share(zc, most), sum) : __fdividef(1.f, 1.f + expf(-zc));
   }
   if (there && q < A.topk) {
     A.ids[t * A.topk + q] = mine;
@@ -724,11 +741,16 @@ int access_of(const void* p, size_t ld, int experts, int epl, size_t elem) {
 }
 
 // The lanes that take a token: as few as hold its experts in registers, have one lane for each
-// slot and the first that is left out, and one for each group.  32,768 tokens, top-8 of 256 in
-// 4 of 8 groups: 30.6 us with 16 lanes, 34.4 with 32; top-6 of 64: 6.8 us with 8, 12.8 with 32.
+// slot and the first that is left out (for scores of bf16 logits, among which many are equal,
+// three more), and one for each group.  32,768 tokens, top-8 of 256 in 4 of 8 groups: 30.6 us with 16
+// lanes, 34.4 with 32; top-6 of 64: 6.8 us with 8, 12.8 with 32.  Where there are not enough
+// tokens to keep the SMs busy a warp each has less to do one after the other: 1024 tokens 6.8 us
+// with 32 lanes, 8.5 with 16; 2.5 and 2.9.  The sides meet near 3000 tokens at 64 experts and
+// between 8192 and 32,768 at 256.
 template <class T, bool SOFTMAX>
-void (*route_pick(int experts, int topk, int groups, bool scored, int* lanes))(RouteArgs) {
-  const int slots = topk + (scored && sizeof(T) == 2 ? 4 : 1), need = slots > groups ? slots : groups;
+void (*route_pick(int tokens, int experts, int topk, int groups, bool scored, int* lanes))(RouteArgs) {
+  const int slots = topk + (scored && sizeof(T) == 2 ? 4 : 1);
+  const int need = tokens <= kSms * (experts <= 128 ? 16 : 64) ? 32 : slots > groups ? slots : groups;
   if (experts <= 32 && need <= 8) {
     *lanes = 8;
     return route_kernel<T, 4, 8, SOFTMAX>;
@@ -813,12 +835,13 @@ cudaError_t route_preload() {
   int lanes;
   for (int experts = 32; experts <= kMaxExperts; experts *= 2)
     for (int topk : {1, 12, 31}) {
-      for (int groups : {1, 16}) {
-        load(reinterpret_cast<const void*>(route_pick<float, false>(experts, topk, groups, false, &lanes)));
-        load(reinterpret_cast<const void*>(route_pick<float, true>(experts, topk, groups, false, &lanes)));
-        load(reinterpret_cast<const void*>(route_pick<__nv_bfloat16, false>(experts, topk, groups, false, &lanes)));
-        load(reinterpret_cast<const void*>(route_pick<__nv_bfloat16, true>(experts, topk, groups, false, &lanes)));
-      }
+      for (int groups : {1, 16})
+        for (int tokens : {1, 1 << 30}) {
+          load(reinterpret_cast<const void*>(route_pick<float, false>(tokens, experts, topk, groups, false, &lanes)));
+          load(reinterpret_cast<const void*>(route_pick<float, true>(tokens, experts, topk, groups, false, &lanes)));
+          load(reinterpret_cast<const void*>(route_pick<__nv_bfloat16, false>(tokens, experts, topk, groups, false, &lanes)));
+          load(reinterpret_cast<const void*>(route_pick<__nv_bfloat16, true>(tokens, experts, topk, groups, false, &lanes)));
+        }
       RouteGradArgs A{};
       A.experts = experts;
       A.topk = topk;
@@ -855,9 +878,9 @@ extern "C" hocResult_t hoc_ep_route(int tokens, int experts, int topk, const voi
   const size_t b = bytes_of(dtype);
   int lanes;
   const auto kernel = dtype == HOC_FLOAT32
-                          ? softmax ? route_pick<float, true>(experts, topk, groups, scored, &lanes) : route_pick<float, false>(experts, topk, groups, scored, &lanes)
-                          : softmax ? route_pick<__nv_bfloat16, true>(experts, topk, groups, scored, &lanes)
-                                    : route_pick<__nv_bfloat16, false>(experts, topk, groups, scored, &lanes);
+                          ? softmax ? route_pick<float, true>(tokens, experts, topk, groups, scored, &lanes) : route_pick<float, false>(tokens, experts, topk, groups, scored, &lanes)
+                          : softmax ? route_pick<__nv_bfloat16, true>(tokens, experts, topk, groups, scored, &lanes)
+                                    : route_pick<__nv_bfloat16, false>(tokens, experts, topk, groups, scored, &lanes);
   const int epl = (experts + lanes - 1) / lanes, epl_warp = (experts + 31) / 32;
   const RouteArgs A{logits, bias, ids, gate, int64_t(ldl), tokens, experts, topk, groups, top_groups, softmax, renormalise != 0,
                     epl, access_of(logits, ldl, experts, epl, b), epl_warp, access_of(logits, ldl, experts, epl_warp, b),
