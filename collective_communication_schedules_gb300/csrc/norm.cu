@@ -678,23 +678,26 @@ cudaError_t start_norm(const NormArgs& A, bool vec, cudaStream_t s) {
   const int nvec = A.width / int(16 / sizeof(T));
   if (vec && nvec <= 4096) {
     if (nvec <= 32) return launch_norm<T, 1>(A, s);
-    // two vectors of each operand keep enough of them on their way; NORM_V
+    // Two vectors a thread keep enough bytes on their way: 16,384 x 4096 bf16 without a residual 50 us,
+    // with one 63; with a residual 81 and 84.  Up to 128 vectors a row stays in a warp.
     if (nvec <= 64 || (nvec > 128 && nvec <= 2048)) return launch_norm<T, 2>(A, s);
     return launch_norm<T, 4>(A, s);
   }
   const int groups = (A.width + kGroup - 1) / kGroup;
   if (groups <= 1) return launch_norm_any<T, 1, kNarrowThreads>(A, s);
   if (groups <= 4) return launch_norm_any<T, 4, kNarrowThreads>(A, s);
-  if (groups <= 8) return launch_norm_any<T, 8, kNarrowThreads>(A, s);
+  // 65,536 x 1001 bf16: 159 us with two groups a warp, 164 with one, 213 with eight (a warp a row)
+  if (groups <= 64) return launch_norm_any<T, 2, 1024>(A, s);
   if (groups <= 128) return launch_norm_any<T, 4, 1024>(A, s);
   return launch_norm_any<T, 8, 1024>(A, s);
 }
 
 constexpr int kMostParts = kSms * 8;
 
-// CTAs of the gradient's kernel: what is resident at once, of about 100 registers a thread.
-int grad_parts(int rows, int log, int threads, size_t smem) {
-  int each = int(size_t(220) * 1024 / (smem + 2048)), regs = 640 / threads;
+// CTAs of the gradient's kernel: what is resident at once, `resident` threads of an SM by their
+// registers.
+int grad_parts(int rows, int log, int threads, size_t smem, int resident) {
+  int each = int(size_t(220) * 1024 / (smem + 2048)), regs = resident / threads;
   each = each < regs ? each : regs;
   const int most = kSms * (each > 8 ? 8 : each < 1 ? 1 : each);
   const int want = log < 0 ? rows : int(((int64_t(rows) << log) + threads - 1) / threads);
@@ -725,7 +728,7 @@ cudaError_t launch_grad(NormGradArgs A, cudaStream_t s, int* parts) {
   const int threads = A.log < 0 ? row_threads(pieces, V) : kGradNarrow;
   size_t smem = size_t(S) * (2 + (A.dy2 != nullptr) + (A.dres != nullptr)) * V * threads * 16;
   if (A.log >= 0 && smem < A.width * sizeof(float)) smem = A.width * sizeof(float);  // for the sums at the end
-  *parts = grad_parts(A.rows, A.log, threads, smem);
+  *parts = grad_parts(A.rows, A.log, threads, smem, N == 1 ? V <= 4 ? 1536 : V <= 9 ? 768 : 512 : 640);
   if (smem > kSmemAsIs) {
     const cudaError_t e = opt_in(norm_grad_kernel<T, N, V, S, THREADS>, kMostRing, done);
     if (e != cudaSuccess) return e;
@@ -750,9 +753,12 @@ cudaError_t start_grad(const NormGradArgs& A, bool vec, cudaStream_t s, int* par
     if (nvec <= 4 * kWideThreads) return launch_grad_wide<T, N, 4>(A, s, parts);
     return launch_grad_wide<T, N, 8>(A, s, parts);
   }
+  // few columns to a thread and many rows at once: 65,536 x 1001 bf16 311 us with 2 columns, 321 with 4, 498
+  // with 8; 443 with two rows an SM instead of three
   if (A.width <= 128) return launch_grad<T, 1, 4, 0, kGradNarrow>(A, s, parts);
-  if (A.width <= 512) return launch_grad<T, 1, 16, 0, kGradNarrow>(A, s, parts);
-  if (A.width <= 1024) return launch_grad<T, 1, 32, 0, kGradNarrow>(A, s, parts);
+  if (A.width <= 2 * kGradThreads) return launch_grad<T, 1, 2, 0>(A, s, parts);
+  if (A.width <= 4 * kGradThreads) return launch_grad<T, 1, 4, 0>(A, s, parts);
+  if (A.width <= 9 * kGradThreads) return launch_grad<T, 1, 9, 0>(A, s, parts);
   if (A.width <= 16 * kGradThreads) return launch_grad<T, 1, 16, 0>(A, s, parts);
   return launch_grad_wide<T, 1, 32>(A, s, parts);
 }
@@ -770,12 +776,13 @@ cudaError_t norm_preload() {
       HOC_FN(norm_kernel<T, V, true, false>), HOC_FN(norm_kernel<T, V, true, true>)
 #define HOC_NORM_OF(T, N)                                                                                        \
   HOC_NORM_V(T, 1), HOC_NORM_V(T, 2), HOC_NORM_V(T, 4), HOC_FN(norm_any_kernel<T, 1, kNarrowThreads>),               \
-      HOC_FN(norm_any_kernel<T, 4, kNarrowThreads>), HOC_FN(norm_any_kernel<T, 8, kNarrowThreads>),                     \
+      HOC_FN(norm_any_kernel<T, 4, kNarrowThreads>), HOC_FN(norm_any_kernel<T, 2, 1024>),                               \
       HOC_FN(norm_any_kernel<T, 4, 1024>), HOC_FN(norm_any_kernel<T, 8, 1024>),                                       \
        HOC_FN(norm_grad_kernel<T, N, 1, 4, kGradThreads>),                                                           \
       HOC_FN(norm_grad_kernel<T, N, 2, 4, kGradThreads>), HOC_FN(norm_grad_kernel<T, N, 2, 3, kGradThreads>),           \
-      HOC_FN(norm_grad_kernel<T, 1, 4, 0, kGradNarrow>), HOC_FN(norm_grad_kernel<T, 1, 16, 0, kGradNarrow>),            \
-      HOC_FN(norm_grad_kernel<T, 1, 32, 0, kGradNarrow>), HOC_FN(norm_grad_kernel<T, 1, 16, 0, kGradThreads>),          \
+      HOC_FN(norm_grad_kernel<T, 1, 4, 0, kGradNarrow>), HOC_FN(norm_grad_kernel<T, 1, 2, 0, kGradThreads>),            \
+      HOC_FN(norm_grad_kernel<T, 1, 4, 0, kGradThreads>), HOC_FN(norm_grad_kernel<T, 1, 9, 0, kGradThreads>),           \
+      HOC_FN(norm_grad_kernel<T, 1, 16, 0, kGradThreads>),                                                              \
       HOC_FN(norm_grad_wide_kernel<T, N, 4>), HOC_FN(norm_grad_wide_kernel<T, N, 8>), \
       HOC_FN(norm_grad_wide_kernel<T, 1, 32>)
       HOC_NORM_OF(float, 4), HOC_NORM_OF(__nv_bfloat16, 8)};

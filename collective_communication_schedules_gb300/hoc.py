@@ -989,8 +989,8 @@ def wire8_views(wire, width: int):
     n, at = _wire8(width)
     if wire.dtype is not torch.uint8 or wire.dim() != 2 or wire.shape[1] != n:
         raise ValueError(f"wire: expected a uint8 tensor of shape [rows, {n}]")
-    return (wire[:, :width].view(torch.float8_e4m3fn),
-            wire[:, at: at + (width + 127) // 128 * 4].view(torch.float32))
+    return (wire.view(torch.float8_e4m3fn).narrow(1, 0, width),
+            wire.view(torch.float32).narrow(1, at // 4, (width + 127) // 128))
 
 
 def _wire_rows(wire, rows: int, width: int, device: int, what: str) -> Optional[int]:

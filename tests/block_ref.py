@@ -91,11 +91,11 @@ def gates(z, ids, score, renormalise, scale):
     return torch.where(there, g * scale, torch.zeros_like(g))
 
 
-def philox_bits(n, seed):
-    """16 random bits of each of n elements, in Python's own numbers (numpy uint64)."""
+def philox_bits(n, seed, first=0):
+    """16 random bits of each of n elements from element `first` on (a multiple of 8), in numpy's uint64."""
     mask = np.uint64(0xFFFFFFFF)
     w = lambda v, i: np.uint64((int(v) >> (32 * i)) & 0xFFFFFFFF)  # noqa: E731
-    g = np.arange((n + 7) // 8, dtype=np.uint64)
+    g = np.arange((n + 7) // 8, dtype=np.uint64) + np.uint64(first // 8)
     c = [g & mask, g >> np.uint64(32), np.full_like(g, w(seed[1], 0)), np.full_like(g, w(seed[1], 1))]
     k = [w(seed[0], 0), w(seed[0], 1)]
     for _ in range(10):

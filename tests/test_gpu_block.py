@@ -628,6 +628,76 @@ def test_same_bits_every_time():
     assert bool((dw == dw[0]).all())
 
 
+# ------------------------------------------------------------------------------------------------- offsets past 32 bits
+FAR = (70_001, 32_768)  # 2.3e9 elements
+
+
+def far(pad=0):
+    """Rows of zeros but for the last two, whose elements lie past 2^31."""
+    t = torch.zeros(FAR[0], FAR[1] + pad, dtype=BF, device=DEV)[:, :FAR[1]]
+    t[-2:] = torch.randn(2, FAR[1], generator=gen(40 + pad), device=DEV)
+    return t
+
+
+@pytest.mark.parametrize("pad", [0, 8, 1])
+def test_norm_past_2_to_the_31(pad):
+    x, w = far(pad), torch.rand(FAR[1], device=DEV) + 0.5
+    y = torch.full_like(x, 7.0)
+    hoc.rms_norm(x, w, y, eps=1e-6)
+    _, want = ref.norm(x[-2:].cpu(), None, w.cpu(), 1e-6)
+    within(y[-2:], want, (ref.half_step(BF) + NORM) * want.abs(), "y")
+    assert bool((y[:-2] == 0).all())
+    del y
+    dx, dw = torch.empty_like(x), torch.empty(FAR[1], device=DEV)
+    ws = torch.empty(hoc.rms_norm_workspace(*FAR), dtype=torch.int32, device=DEV)
+    hoc.rms_norm_grad(x, x, w, dx, eps=1e-6, dw=dw, workspace=ws)
+    wx, terms, ww, wterms = ref.norm_grad(x[-2:].cpu(), None, x[-2:].cpu(), w.cpu(), 1e-6, None)
+    within(dx[-2:], wx, ref.half_step(BF) * wx.abs() + 2.0 ** -18 * terms, "dx")
+    within(dw, ww, 200 * 2.0 ** -24 * wterms + 1e-30, "dw")  # two terms that are not zero
+    assert bool((dx[:-2] == 0).all())
+
+
+@pytest.mark.parametrize("pad", [0, 8, 1])
+def test_dropout_past_2_to_the_31(pad):
+    x = far(pad)
+    seed = (3, 4)
+    hoc.dropout(x, x, 0.25, seed_of(*seed), residual=None)
+    want = far(pad)[-2:].cpu().double()
+    keep = ref.philox_bits(2 * FAR[1], seed, (FAR[0] - 2) * FAR[1]).view(2, -1) >= 16384
+    want = torch.where(keep, want * 65536 / 49152, torch.zeros((), dtype=F64))
+    within(x[-2:], want, (ref.half_step(BF) + 2.0 ** -23) * want.abs(), "y")
+    assert bool((x[:-2] == 0).all())
+
+
+def test_routing_of_rows_that_lie_far_apart():
+    wide = torch.zeros(40_000, 65_536, device=DEV)
+    z = wide[:, :64]
+    z.copy_(torch.randn(40_000, 64, generator=gen(44), device=DEV))
+    together = z.clone()
+    ids, gate, ids2, gate2 = (torch.empty(240_000, dtype=t, device=DEV) for t in (torch.int32, F32) * 2)
+    hoc.ep_route(z, ids, gate, renormalise=True)
+    hoc.ep_route(together, ids2, gate2, renormalise=True)
+    assert torch.equal(ids, ids2) and torch.equal(gate, gate2)
+    dgate = torch.randn(240_000, generator=gen(45), device=DEV)
+    want = torch.empty_like(together)
+    for renormalise in (True, False):
+        hoc.ep_route_grad(together, ids, dgate, want, renormalise=renormalise)
+        z.copy_(together)
+        hoc.ep_route_grad(z, ids, dgate, z, renormalise=renormalise)
+        assert torch.equal(z, want)
+
+
+def test_widen_past_2_to_the_31():
+    rows, width = 1_100_000, 2048
+    wire = torch.zeros(rows, hoc.wire8_bytes(width), dtype=torch.uint8, device=DEV)
+    q, scale = hoc.wire8_views(wire, width)
+    q[-1] = torch.randn(width, generator=gen(46), device=DEV).to(q.dtype)
+    scale[-1] = 0.5
+    y = torch.full((rows, width), 7.0, dtype=BF, device=DEV)
+    hoc.expert_widen([wire], torch.tensor([[0, 5, rows]], device=DEV), [y])
+    assert torch.equal(y[-1], (q[-1].float() * 0.5).to(BF)) and bool((y[:-1] == 0).all())
+
+
 def test_the_binding_refuses_bad_shapes():
     x = torch.zeros(4, 64, device=DEV)
     w = torch.ones(64, device=DEV)
