@@ -366,6 +366,9 @@ __device__ __forceinline__ int pop_sorted(uint32_t (&u)[EPL], int q, uint32_t* k
   return winner;
 }
 
+// Bound by its instructions (comparisons and logic run at half the rate of additions): 32,768 tokens,
+// top-8 of 256 sigmoids with a bias in 4 of 8 groups 27 us, of which 13 are loading, packing and
+// sorting, 0.4 each round of the choice, 5 the groups; the bytes alone would take 5.
 template <class T, int EPL, int L, bool SOFTMAX>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteArgs A) {
   after_the_last();
@@ -634,7 +637,7 @@ __device__ __forceinline__ float sum_same(int id, int topk, float v, uint32_t* s
 
 // Every gate but those of a softmax that is not renormalised depends on the chosen logits alone:
 // they are all that is read, and the row is zeros but for them.  L lanes take a token.
-// Bound by its stores.  S: elements of a store.
+// Bound by its stores: 32,768 x 256 binary32 11.8 us.  S: elements of a store.
 template <class T, int S, int L, bool SOFTMAX>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(const __grid_constant__ RouteGradArgs A) {
   after_the_last();

@@ -58,14 +58,14 @@ class ExpertBlock:
         dropout, if there is one.  Keeps what the backward pass needs; x itself where there is no residual."""
         if self.drop and seed is None:
             raise ValueError("seed: the dropout needs one")
-        self.stream = self.h if residual is not None else x
+        self.held = self.h if residual is not None else x
         hoc.rms_norm(x, norm, self.n, eps=self.eps, residual=residual, h=self.h if residual is not None else None,
                      wire=self.wire, stream=stream)
         hoc.linear(self.n, router, self.logits, status=self.status, stream=stream)
         hoc.ep_route(self.logits, self.ids, self.gate, bias=bias, **self.routing, **self.choice, stream=stream)
         self.layer.forward(self._ranks(self.n if self.wire is None else self.wire), self._ranks(self.ids),
                            self._ranks(self.gate), w_up, w_down, self._ranks(self.out), stream=stream)
-        hoc.dropout(self.out, y, self.drop, self.no_seed if seed is None else seed, residual=self.stream, stream=stream)
+        hoc.dropout(self.out, y, self.drop, self.no_seed if seed is None else seed, residual=self.held, stream=stream)
 
     def backward(self, dy, norm, router, w_up, w_down, dx, dnorm, drouter, dw_up, dw_down, *, seed=None,
                  accumulate: bool = False, stream=None):
@@ -82,5 +82,5 @@ class ExpertBlock:
         hoc.ep_route_grad(self.logits, self.ids, self.dgate, self.dlogits, **self.routing, stream=stream)
         hoc.linear_wgrad(self.dlogits, self.n, drouter, status=self.status, accumulate=accumulate, stream=stream)
         hoc.linear_dgrad(self.dlogits, router, self.dn_router, status=self.status, stream=stream)
-        hoc.rms_norm_grad(self.dn, self.stream, norm, dx, eps=self.eps, dy2=self.dn_router, dres=dy, dw=dnorm,
+        hoc.rms_norm_grad(self.dn, self.held, norm, dx, eps=self.eps, dy2=self.dn_router, dres=dy, dw=dnorm,
                           accumulate=accumulate, workspace=self.ws, stream=stream)

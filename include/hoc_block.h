@@ -95,7 +95,9 @@ hocResult_t hoc_expert_widen(const hocRowGroups_t* groups, const void* const* wi
 /* Scores of the experts. */
 typedef enum { HOC_SCORE_SOFTMAX = 0, HOC_SCORE_SIGMOID = 1 } hocScore_t;
 
-/* Routing of `tokens` tokens to topk of `experts` experts each.  logits: [tokens,
+/* Routing of `tokens` tokens to topk of `experts` experts each; topk is at most
+ * HOC_ROUTE_MAX_TOPK and the experts of top_groups groups, groups divides experts and
+ * is at most 32.  logits: [tokens,
  * experts] of dtype, row stride ldl; with the score s of an expert (softmax over the
  * token's experts, or sigmoid)
  *   key  = s + bias            bias: [experts] binary32 (NULL: none), for the choice only
