@@ -167,10 +167,14 @@ __device__ __forceinline__ double sigmoid(double z) { return 1.0 / (1.0 + exp(-z
 // Bounds on the error of a binary32 score, relative to the largest score there can be.
 // Sigmoid: its exponent is rounded, which changes s by |z| s (1 - s) 2^-24 < 0.23 * 2^-24, the
 // exponential by 2 units of 2^-23 of itself, s by a quarter of that; 1 + e and the reciprocal by
-// 2^-24 and 2^-23: below 2^-21.  Softmax: z - most is rounded, which changes exp by |z - most| 2^-24
-// of itself, and x exp(-x) < 0.4; expf 2 units; up to 36 additions of the sum, the quotient:
-// below 64 * 2^-23.
-constexpr float kSigmoidError = 0x1p-21f, kSoftmaxError = 0x1p-17f;
+// 2^-24 and 2^-23: below 2^-21.
+constexpr float kSigmoidError = 0x1p-21f;
+// Softmax, in units of 2^-24: z - most is rounded, which changes exp by |z - most| of itself, 0.4 at
+// most beside the largest (x exp(-x)); expf 4; the reciprocal of the sum and the product with it
+// 1 each; in the sum EPL + 5 additions, and of its terms 4 for expf and their mean |z - most|, which
+// is below log(1024) = 7: EPL + 23 in all.
+template <int EPL>
+constexpr float kSoftmaxError = float(EPL + 32) * 0x1p-24f;
 
 // The largest and second largest key of a set (0: none).
 template <class U>
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     }
     if (scored) {
       const float inv = SOFTMAX ? 1.f / sum : 1.f;
-      tol = SOFTMAX ? kSoftmaxError * inv : kSigmoidError;  // (inv: the largest score)
+      tol = SOFTMAX ? kSoftmaxError<EPL> * inv : kSigmoidError;  // (inv: the largest score)
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
         z[i] = z[i] > -INFINITY ? (SOFTMAX ? share(z[i], most) * inv : sigmoid(z[i])) : -INFINITY;
@@ -422,16 +426,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
   auto is_near = [&](float a, float b) {
     return !(a - b > 2.f * tol + fmaxf(fabsf(a), fabsf(b)) * (kCut + 0x1p-22f) + 0x1p-140f);
   };
-  // Expert e's key in 64 bits; the softmax's sum has to be there, which all lanes work out.
-  double sum64 = 0;
-  auto sum_in_64 = [&]() {
+  // The softmax's sum in 64 bits for the tokens that ask for it, each by the whole warp; and expert e's key,
+  // which needs it.
+  double sum64 = 1;
+  auto sum_in_64 = [&](bool asked) {
     if (!SOFTMAX || !scored) return;
-    float z[EPL];
-    load_logits<T, EPL>(row, A.experts, A.epl, A.vec, q, z);
-    sum64 = 0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) sum64 += share(double(z[i]), double(most));
-    sum64 = sum_of<L>(sum64);
+    for (uint32_t left = __ballot_sync(kAll, asked && there && q == 0); left; left &= left - 1) {
+      const int first = __ffs(left) - 1;
+      const T* it = static_cast<const T*>(A.logits) + (t0 + first / L) * A.ld;
+      const double top = __shfl_sync(kAll, most, first);
+      double part = 0;
+      for (int e = lane; e < A.experts; e += 32) part += share(double(fmaxf(widen(it[e]), -INFINITY)), top);
+      part = sum_of<32>(part);
+      if (lane / L == first / L) sum64 = part;
+    }
   };
   auto key_in_64 = [&](int e) {
     const double z = widen(row[e]), s = !scored ? z : SOFTMAX ? share(z, double(most)) / sum64 : sigmoid(z);
@@ -473,7 +481,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
       exactly = near;
     } else if (__any_sync(kAll, near)) {
       // The group's scores by 64-bit keys: of a lane's three largest, unless a fourth may be among them.
-      sum_in_64();
+      sum_in_64(near);
       Two<uint64_t> t{0, 0};
 #pragma unroll
       for (int i = 0; i < (EPL < 3 ? EPL : 3); ++i)
@@ -541,8 +549,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
       }
       // near ones that are not equals: their order by 64-bit keys
       const int prev = __shfl_up_sync(kAll, mine, 1, L);
-      if (__any_sync(kAll, by && (row[prev] != row[mine] || (A.bias && A.bias[prev] != A.bias[mine])))) {
-        sum_in_64();
+      const uint32_t doubt = lanes_of<L>(by && (row[prev] != row[mine] || (A.bias && A.bias[prev] != A.bias[mine])));
+      if (__any_sync(kAll, doubt)) {
+        sum_in_64(doubt);
         const uint64_t key64 = mine >= 0 ? key_in_64(mine) : 0;
         int place = 0;
         for (int r = 0; r < L; ++r) {
@@ -556,7 +565,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
           const int id = __shfl_sync(kAll, mine, r, L);
           if (__shfl_sync(kAll, place, r, L) == q) sorted = id;
         }
-        mine = sorted;
+        if (doubt) mine = sorted;
       }
     }
     for (uint32_t left = __ballot_sync(kAll, exactly && there && q == 0); left; left &= left - 1) {
