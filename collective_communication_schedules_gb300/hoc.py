@@ -898,14 +898,29 @@ def _score(score) -> int:
     return SCORES[score]
 
 
+_ROW_DTYPES = {}  # torch dtypes of rows -> codes, once torch is imported
+
+
 def _row_dtype(x, what: str) -> int:
     """The code of the dtype of `x`, rows of which the calls below take."""
-    dtype = getattr(x, "dtype", None)
-    if dtype is _dt("bfloat16"):
-        return BFLOAT16
-    if dtype is _dt("float32"):
-        return FLOAT32
-    raise TypeError(f"{what}: expected a bfloat16 or float32 tensor")
+    if not _ROW_DTYPES:
+        _ROW_DTYPES.update({_dt("bfloat16"): BFLOAT16, _dt("float32"): FLOAT32})
+    code = _ROW_DTYPES.get(getattr(x, "dtype", None))
+    if code is None:
+        raise TypeError(f"{what}: expected a bfloat16 or float32 tensor")
+    return code
+
+
+_NUMBERS = {}  # host numbers by value, as the library reads them: an address each
+
+
+def _number(v, kind=C.c_float):
+    got = _NUMBERS.get((kind, v))
+    if got is None:
+        if len(_NUMBERS) >= 256:
+            _NUMBERS.clear()
+        got = _NUMBERS[kind, v] = C.byref(kind(v))
+    return got
 
 
 _get_device = _raw_stream = None  # torch's own calls for the current device and its stream, once torch is imported
@@ -944,12 +959,15 @@ def _rows_of(x, shape, dtype, device: int, what: str):
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
     if x.get_device() != device:
         raise ValueError(f"{what}: must be a CUDA tensor on the device of the others")
-    rows, width = shape
     ld, step = x.stride()
-    if (step != 1 and width > 1) or (ld < width and rows > 1):
-        if rows and width:
-            raise ValueError(f"{what}: " + ("a row's elements must be contiguous" if step != 1 and width > 1 else "rows must not overlap"))
-    return x.data_ptr(), ld if rows > 1 and ld > width else width
+    if step == 1 and ld >= shape[1]:
+        return x.data_ptr(), ld
+    rows, width = shape  # one row, one column or none may have any strides
+    if rows and width > 1 and step != 1:
+        raise ValueError(f"{what}: a row's elements must be contiguous")
+    if rows > 1 and width and ld < width:
+        raise ValueError(f"{what}: rows must not overlap")
+    return x.data_ptr(), max(ld, width)
 
 
 def _flat(x, n: int, dtype, device: int, what: str):
@@ -1015,9 +1033,10 @@ def rms_norm(x, weight, y=None, *, eps: float, residual=None, h=None, wire=None,
     hp, ldh = _rows_of(h, shape, x.dtype, dev, "h")
     yp, ldy = _rows_of(y, shape, x.dtype, dev, "y")
     wdt = _row_dtype(weight, "weight")
-    _check(lib().hoc_rms_norm(rows, width, dt, xp, ldx, rp, ldr, _flat(weight, width, weight.dtype, dev, "weight"), wdt,
-                              C.byref(C.c_float(eps)), hp, ldh, yp, ldy, _wire_rows(wire, rows, width, dev, "wire"), _queue(stream, dev)),
-           "hoc_rms_norm")
+    rc = (_lib or lib()).hoc_rms_norm(rows, width, dt, xp, ldx, rp, ldr, _flat(weight, width, weight.dtype, dev, "weight"), wdt,
+                              _number(eps), hp, ldh, yp, ldy, _wire_rows(wire, rows, width, dev, "wire"), _queue(stream, dev))
+    if rc:
+        _check(rc, "hoc_rms_norm")
 
 
 def rms_norm_workspace(rows: int, width: int) -> int:
@@ -1050,10 +1069,12 @@ def rms_norm_grad(dy, h, weight, dx, *, eps: float, dy2=None, dres=None, dw=None
             raise ValueError("workspace: a weight gradient needs one")
         ints = workspace.numel()
         wsp = _flat(workspace, ints, _dt("int32"), dev, "workspace")
-    _check(lib().hoc_rms_norm_grad(rows, width, dt, dyp, lddy, dy2p, lddy2, hp, ldh,
-                                   _flat(weight, width, weight.dtype, dev, "weight"), wdt, C.byref(C.c_float(eps)), drp, lddr, dxp, lddx,
+    rc = (_lib or lib()).hoc_rms_norm_grad(rows, width, dt, dyp, lddy, dy2p, lddy2, hp, ldh,
+                                   _flat(weight, width, weight.dtype, dev, "weight"), wdt, _number(eps), drp, lddr, dxp, lddx,
                                    None if dw is None else _flat(dw, width, dw.dtype, dev, "dw"), dwdt,
-                                   int(bool(accumulate)), wsp, ints, _queue(stream, dev)), "hoc_rms_norm_grad")
+                                   int(bool(accumulate)), wsp, ints, _queue(stream, dev))
+    if rc:
+        _check(rc, "hoc_rms_norm_grad")
 
 
 def expert_widen(wire, seg, y, *, counts=None, stream=None):
@@ -1086,9 +1107,11 @@ def expert_widen(wire, seg, y, *, counts=None, stream=None):
     arr = C.c_void_p * k
     yp, wp, cap = arr(*yp), arr(*wp), (C.c_size_t * k)(*caps)
     g = _RowGroups(k, seg.shape[1] - 1, 1, _flat(seg, seg.numel(), seg.dtype, dev, "seg"), cap)
-    _check(lib().hoc_expert_widen(C.byref(g), wp, width, yp,
+    rc = (_lib or lib()).hoc_expert_widen(C.byref(g), wp, width, yp,
                                   None if counts is None else _flat(counts, k * k, _dt("int64"), dev, "counts"),
-                                  _queue(stream, dev)), "hoc_expert_widen")
+                                  _queue(stream, dev))
+    if rc:
+        _check(rc, "hoc_expert_widen")
 
 
 def _slots(logits, ids, gate, what: str):
@@ -1112,10 +1135,12 @@ def ep_route(logits, ids, gate, *, score: str = "softmax", bias=None, groups: in
     be rows of a wider buffer; ids int32 and gate float32 of tokens * topk elements, as a dispatch and a combine take them;
     bias float32 [experts], for the choice only; of `groups` groups of experts the best top_groups (default: all)."""
     tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, gate, "gate")
-    _check(lib().hoc_ep_route(tokens, experts, topk, lp, dt, ldl, _score(score),
+    rc = (_lib or lib()).hoc_ep_route(tokens, experts, topk, lp, dt, ldl, _score(score),
                               _flat(bias, experts, _dt("float32"), dev, "bias"), groups,
-                              groups if top_groups is None else top_groups, int(bool(renormalise)), C.byref(C.c_float(scale)), ip, gp,
-                              _queue(stream, dev)), "hoc_ep_route")
+                              groups if top_groups is None else top_groups, int(bool(renormalise)), _number(scale), ip, gp,
+                              _queue(stream, dev))
+    if rc:
+        _check(rc, "hoc_ep_route")
 
 
 def ep_route_grad(logits, ids, dgate, dlogits, *, score: str = "softmax", renormalise: bool = False, scale: float = 1.0,
@@ -1123,8 +1148,10 @@ def ep_route_grad(logits, ids, dgate, dlogits, *, score: str = "softmax", renorm
     """Gradient of ep_route for the logits, from dgate for the gates; dlogits may be logits (see include/hoc_block.h)."""
     tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, dgate, "dgate")
     dp, ldd = _rows_of(dlogits, logits.shape, logits.dtype, dev, "dlogits")
-    _check(lib().hoc_ep_route_grad(tokens, experts, topk, lp, dt, ldl, _score(score), int(bool(renormalise)), C.byref(C.c_float(scale)), ip, gp,
-                                   dp, ldd, _queue(stream, dev)), "hoc_ep_route_grad")
+    rc = (_lib or lib()).hoc_ep_route_grad(tokens, experts, topk, lp, dt, ldl, _score(score), int(bool(renormalise)), _number(scale), ip, gp,
+                                   dp, ldd, _queue(stream, dev))
+    if rc:
+        _check(rc, "hoc_ep_route_grad")
 
 
 def dropout(x, y, p: float, seed, *, residual=None, stream=None):
@@ -1148,8 +1175,10 @@ def dropout(x, y, p: float, seed, *, residual=None, stream=None):
     xp, ldx = _rows_of(x, shape, x.dtype, dev, "x")
     yp, ldy = _rows_of(y, shape, x.dtype, dev, "y")
     rp, ldr = _rows_of(residual, shape, x.dtype, dev, "residual")
-    _check(lib().hoc_dropout(shape[0], shape[1], dt, xp, ldx, rp, ldr, C.byref(C.c_double(p)), _flat(seed, 2, _dt("int64"), dev, "seed"), yp,
-                             ldy, _queue(stream, dev)), "hoc_dropout")
+    rc = (_lib or lib()).hoc_dropout(shape[0], shape[1], dt, xp, ldx, rp, ldr, _number(p, C.c_double), _flat(seed, 2, _dt("int64"), dev, "seed"), yp,
+                             ldy, _queue(stream, dev))
+    if rc:
+        _check(rc, "hoc_dropout")
 
 
 # ------------------------------------------------------------- gradient clipping

@@ -10,8 +10,8 @@
  *     elements; sums, statistics and scores are binary32 or wider, each result is
  *     rounded once, when it is stored.
  *   - Everything is stream-ordered, never waits on the host, allocates nothing
- *     and may be captured into a CUDA graph.  Results are the same bits every
- *     time.  Pointers belong to the current device.
+ *     and may be captured into a CUDA graph after one call of the same kind.
+ *     Results are the same bits every time.  Pointers belong to the current device.
  *   - eps, scale and p point to one host number each, read during the call.
  *   - Any alignment to the element is taken; rows that start on 16-byte boundaries
  *     (and are whole 16-byte vectors) run faster.

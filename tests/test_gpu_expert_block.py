@@ -193,6 +193,17 @@ def test_tokens_without_an_expert_pass_by():
     assert torch.equal(o["y"], h) and torch.equal(o["dx"], p["dy"]) and bool((o["drouter"] == 0).all())
 
 
+def test_block_of_no_tokens():
+    p = problem(2, 0, 64, 32, 4, 1)
+    block = ExpertBlock(2, 0, 2, 64, 32, 4, drop=0.1, wire8=True)
+    o = outputs(p)
+    step(block, p, o)
+    torch.cuda.synchronize()
+    assert block.status.item() == 0
+    for t in [o["dnorm"], o["drouter"]] + o["dup"] + o["ddown"]:
+        assert bool((t == 0).all())
+
+
 def test_block_refuses():
     with pytest.raises(ValueError):
         ExpertBlock(2, 8, 1, 64, 32, 3)
