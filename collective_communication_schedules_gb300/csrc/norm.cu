@@ -768,7 +768,7 @@ cudaError_t start_grad(const NormGradArgs& A, bool vec, cudaStream_t s, int* par
     if (nvec <= 256) return launch_grad<T, N, 2, 4>(A, s, parts);
     if (nvec <= 2 * kGradThreads) return launch_grad<T, N, 2, 3>(A, s, parts);
     if (nvec <= 4 * kWideThreads) return launch_grad_wide<T, N, 4>(A, s, parts);
-    return launch_grad_wide<T, N, 8>(A, s, parts);
+    return launch_grad_wide<T, N, kMaxWidth / (N * kWideThreads)>(A, s, parts);
   }
   // few columns to a thread and many rows at once: 65,536 x 1001 bf16 311 us with 2 columns, 321 with 4, 498
   // with 8; 443 with two rows an SM instead of three
@@ -800,7 +800,7 @@ cudaError_t norm_preload() {
       HOC_FN(norm_grad_kernel<T, 1, 4, 0, kGradNarrow>), HOC_FN(norm_grad_kernel<T, 1, 2, 0, kGradThreads>),            \
       HOC_FN(norm_grad_kernel<T, 1, 4, 0, kGradThreads>), HOC_FN(norm_grad_kernel<T, 1, 9, 0, kGradThreads>),           \
       HOC_FN(norm_grad_kernel<T, 1, 16, 0, kGradThreads>),                                                              \
-      HOC_FN(norm_grad_wide_kernel<T, N, 4>), HOC_FN(norm_grad_wide_kernel<T, N, 8>), \
+      HOC_FN(norm_grad_wide_kernel<T, N, 4>), HOC_FN(norm_grad_wide_kernel<T, N, kMaxWidth / (N * kWideThreads)>), \
       HOC_FN(norm_grad_wide_kernel<T, 1, 32>)
       HOC_NORM_OF(float, 4), HOC_NORM_OF(__nv_bfloat16, 8)};
 #undef HOC_NORM_OF

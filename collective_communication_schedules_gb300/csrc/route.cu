@@ -39,7 +39,7 @@ struct RouteArgs {
   int tokens, experts, topk, groups, top_groups, softmax, renorm;
   int epl, vec;            // experts of a lane where L lanes take a token, and elements of an access to the logits
   int epl_warp, vec_warp;  // the same where a warp does
-  int vec_bias, vec_bias_warp;
+  int vec_bias;            // and of one to the bias
   float scale;
 };
 
@@ -912,7 +912,7 @@ extern "C" hocResult_t hoc_ep_route(int tokens, int experts, int topk, const voi
   const int epl = (experts + lanes - 1) / lanes, epl_warp = (experts + 31) / 32;
   const RouteArgs A{logits, bias, ids, gate, int64_t(ldl), tokens, experts, topk, groups, top_groups, softmax, renormalise != 0,
                     epl, access_of(logits, ldl, experts, epl, b), epl_warp, access_of(logits, ldl, experts, epl_warp, b),
-                    access_of(bias, 0, experts, epl, 4), access_of(bias, 0, experts, epl_warp, 4), *scale};
+                    access_of(bias, 0, experts, epl, 4), *scale};
   return launched(who, launch(kernel, route_grid(tokens, lanes), dim3(kRouteWarps * 32), 0, static_cast<cudaStream_t>(stream), A));
 }
 
