@@ -696,7 +696,8 @@ _TORCH = {}  # torch dtypes by name, once torch is imported
 def _dt(name: str):
     if not _TORCH:
         import torch
-        _TORCH.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "int64", "uint8")})
+        _TORCH.update({n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "int64", "uint8",
+                                                            "float8_e4m3fn")})
     return _TORCH[name]
 
 
@@ -1003,12 +1004,11 @@ def wire8_bytes(width: int) -> int:
 
 def wire8_views(wire, width: int):
     """The values (float8_e4m3fn, [rows, width]) and scales (float32, [rows, ceil(width / 128)]) in rows of 8 bits."""
-    import torch
     n, at = _wire8(width)
-    if wire.dtype is not torch.uint8 or wire.dim() != 2 or wire.shape[1] != n:
+    if wire.dtype is not _dt("uint8") or wire.dim() != 2 or wire.shape[1] != n:
         raise ValueError(f"wire: expected a uint8 tensor of shape [rows, {n}]")
-    return (wire.view(torch.float8_e4m3fn).narrow(1, 0, width),
-            wire.view(torch.float32).narrow(1, at // 4, (width + 127) // 128))
+    return (wire.view(_TORCH["float8_e4m3fn"]).narrow(1, 0, width),
+            wire.view(_TORCH["float32"]).narrow(1, at // 4, (width + 127) // 128))
 
 
 def _wire_rows(wire, rows: int, width: int, device: int, what: str) -> Optional[int]:
