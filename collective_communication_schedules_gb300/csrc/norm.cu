@@ -576,17 +576,18 @@ struct WidenArgs {
 };
 
 constexpr int kWidenThreads = 256, kWidenCtas = kSms * 8;
-constexpr int kWidenAhead = 2;  // steps a thread has in flight
+constexpr int kWidenAhead = 2;  // steps a thread has in flight; one where a step is one value (1001 wide: 159 us, 199 with two)
 
 // Bound by its stores: 8 x 18,432 rows of 2048 in 159 us are 3.8 TB/s of them beside 1.9 of loads,
-// and writing alone (a memset of as many bytes) takes this memory to 3.9.  16 values a step
-// stored as one 32-byte vector; in two of 16 bytes 260 us, with 8 values a step 230.
-// A step is E values: 16 where rows of y are whole 32 bytes, else 8, else 1.  2^log neighbouring
-// lanes take a row, as many as it has steps, a warp at most; the rows of all ranks are one run,
-// handed out in turn.
+// and writing alone (a memset of as many bytes) takes this memory to 3.9.  Steps of 8 values take
+// 230 us; rows of 1000, which are not whole vectors of 32 bytes, 90 us with steps of 16 and 106 with 8.
+// A step is E values: 16 where rows are whole vectors of 16 bytes (WIDE: of 32, and stored so; the
+// last step of a row may be half a one otherwise), else 1.  2^log neighbouring lanes take a
+// row, as many as it has steps, a warp at most; the rows of all ranks are one run, handed out in turn.
 static_assert(kMaxRanks * kMaxRanks <= kWidenThreads, "a thread for each count");
-template <int E>
+template <int E, bool WIDE>
 __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_constant__ WidenArgs A) {
+  constexpr int kAhead = E == 1 ? 1 : kWidenAhead;
   __shared__ int64_t ends[kMaxRanks];
   after_the_last();
   if (threadIdx.x < 32) {
@@ -617,18 +618,18 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
     const int64_t k = row - (d ? ends[d - 1] : 0);
     const uint8_t* from = A.wire[d] + k * row_bytes;
     __nv_bfloat16* to = A.y[d] + k * A.width;
-    for (int c0 = first; c0 < A.width; c0 += span * kWidenAhead) {
-      In q[kWidenAhead];
-      float scale[kWidenAhead];
+    for (int c0 = first; c0 < A.width; c0 += span * kAhead) {
+      In q[kAhead];
+      float scale[kAhead];
 #pragma unroll
-      for (int u = 0; u < kWidenAhead; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int c = c0 + u * span;
         if (c >= A.width) continue;
         q[u] = *reinterpret_cast<const In*>(from + c);
         scale[u] = *reinterpret_cast<const float*>(from + at + c / kGroup * 4);
       }
 #pragma unroll
-      for (int u = 0; u < kWidenAhead; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int c = c0 + u * span;
         if (c >= A.width) continue;
         if constexpr (E == 1) {
@@ -642,12 +643,14 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const __grid_const
             const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * scale[u], v.y * scale[u]);
             o[e / 2] = *reinterpret_cast<const uint32_t*>(&p);
           }
-          if constexpr (E == 16)
+          if constexpr (E == 16 && WIDE) {
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c), "r"(o[0]), "r"(o[1]),
                          "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
                          : "memory");
-          else
+          } else {  // (the last step of a row may be half a one)
             *reinterpret_cast<uint4*>(to + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (c + 8 < A.width) *reinterpret_cast<uint4*>(to + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
         }
       }
     }
@@ -784,8 +787,8 @@ cudaError_t start_grad(const NormGradArgs& A, bool vec, cudaStream_t s, int* par
 
 cudaError_t norm_preload() {
   const void* fns[] = {
-      reinterpret_cast<const void*>(&widen_kernel<16>), reinterpret_cast<const void*>(&widen_kernel<8>),
-      reinterpret_cast<const void*>(&widen_kernel<1>), reinterpret_cast<const void*>(&norm_weight_kernel<float>),
+      reinterpret_cast<const void*>(&widen_kernel<16, true>), reinterpret_cast<const void*>(&widen_kernel<16, false>),
+      reinterpret_cast<const void*>(&widen_kernel<1, false>), reinterpret_cast<const void*>(&norm_weight_kernel<float>),
       reinterpret_cast<const void*>(&norm_weight_kernel<__nv_bfloat16>),
 #define HOC_FN(...) reinterpret_cast<const void*>(&__VA_ARGS__)
 #define HOC_NORM_V(T, V)                                                                                    \
@@ -934,10 +937,11 @@ extern "C" hocResult_t hoc_expert_widen(const hocRowGroups_t* G, const void* con
     most += cap;
   }
   if (most == 0 && !counts) return HOC_SUCCESS;
-  const int e = wide && width % 16 == 0 ? 16 : vec && width % 8 == 0 ? 8 : 1;
+  const int e = vec && width % 8 == 0 ? 16 : 1;
+  wide = wide && width % 16 == 0;
   while (A.log < 5 && (e << A.log) < width) ++A.log;
   const size_t want = ((most << A.log) + kWidenThreads) / kWidenThreads;  // one at least
-  return launched(who, launch(e == 16 ? widen_kernel<16> : e == 8 ? widen_kernel<8> : widen_kernel<1>,
+  return launched(who, launch(e == 1 ? widen_kernel<1, false> : wide ? widen_kernel<16, true> : widen_kernel<16, false>,
                               dim3(unsigned(want < size_t(kWidenCtas) ? want : size_t(kWidenCtas))), dim3(kWidenThreads), 0,
                               static_cast<cudaStream_t>(stream), A));
 }
