@@ -83,7 +83,7 @@ inline bool vector_rows(const void* p, size_t ld, size_t elem) { return aligned(
 
 // A row operand: NULL only where it may be; its pointer on an element, its stride not
 // below the width, its extent below 2^60 bytes.
-inline const char* bad_rows(const void* p, size_t ld, int rows, int width, size_t elem, bool optional) {
+inline const char* bad_rows(const void* p, size_t ld, int64_t rows, int width, size_t elem, bool optional) {
   if (!p) return optional ? nullptr : "a NULL pointer";
   if (!aligned(p, elem)) return "a pointer that is not aligned to its elements";
   if (ld < size_t(width)) return "a row stride below the width";

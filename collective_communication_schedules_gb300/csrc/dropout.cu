@@ -131,7 +131,7 @@ cudaError_t dropout_preload() {
 using namespace hoc;
 using namespace hoc::block;
 
-extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, const void* x, size_t ldx,
+extern "C" hocResult_t hoc_dropout(int64_t rows, int width, hocDataType_t dtype, const void* x, size_t ldx,
                                    const void* residual, size_t ldr, const double* p, const int64_t* seed, void* y, size_t ldy,
                                    void* stream) {
   const char* who = "hoc_dropout";
@@ -139,6 +139,8 @@ extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, con
   if (!row_dtype(dtype)) return refuse(who, "dtype must be HOC_FLOAT32 or HOC_BFLOAT16");
   if (!p || !(*p >= 0.0 && *p < 1.0)) return refuse(who, "p must be given, at least 0 and below 1");
   const bool none = rows == 0 || width == 0;
+  constexpr int64_t kMost = int64_t(0x7FFFFFFF) * 8 * kDropThreads * kDropAhead;  // what a grid reaches
+  if (!none && rows > kMost / width) return refuse(who, "more than 2^43 elements");
   const size_t b = bytes_of(dtype);
   const char* bad = bad_rows(x, ldx, rows, width, b, none);
   if (!bad) bad = bad_rows(residual, ldr, rows, width, b, true);
@@ -146,7 +148,7 @@ extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, con
   if (!bad && (!seed || !aligned(seed, 8))) bad = "seed must be given, aligned to its elements";
   if (bad) return refuse(who, bad);
   if (none) return HOC_SUCCESS;
-  const int64_t total = int64_t(rows) * width;
+  const int64_t total = rows * width;
   const int t = int(*p * 65536 + 0.5) < 65535 ? int(*p * 65536 + 0.5) : 65535;
   unsigned shift = 0;
   while ((int64_t(1) << shift) < width) ++shift;
@@ -154,7 +156,6 @@ extern "C" hocResult_t hoc_dropout(int rows, int width, hocDataType_t dtype, con
   const DropArgs A{x, residual, y, seed, int64_t(ldx), int64_t(ldr), int64_t(ldy), total, width, unsigned(t),
                    65536.f / float(65536 - t), magic, shift};
   const int64_t ctas = ((total + 7) / 8 + kDropThreads * kDropAhead - 1) / (kDropThreads * kDropAhead);
-  if (ctas > 0x7FFFFFFF) return refuse(who, "more than 2^43 elements");
   const bool vec = vector_rows(x, ldx, b) && (!residual || vector_rows(residual, ldr, b)) && vector_rows(y, ldy, b);
   const bool together = rows == 1 || (ldx == size_t(width) && ldy == size_t(width) && (!residual || ldr == size_t(width)));
   const bool starts = aligned(x, 16) && aligned(residual, 16) && aligned(y, 16);

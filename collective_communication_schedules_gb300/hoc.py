@@ -169,7 +169,7 @@ _SIGS["hoc_ep_route"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_in
                                    C.c_int, C.c_int, C.c_int, C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_void_p])
 _SIGS["hoc_ep_route_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_size_t, C.c_int, C.c_int,
                                         C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p])
-_SIGS["hoc_dropout"] = (C.c_int, [C.c_int, C.c_int, C.c_int] + 2 * _ROWS + [C.POINTER(C.c_double), C.c_void_p] + _ROWS + [C.c_void_p])
+_SIGS["hoc_dropout"] = (C.c_int, [C.c_int64, C.c_int, C.c_int] + 2 * _ROWS + [C.POINTER(C.c_double), C.c_void_p] + _ROWS + [C.c_void_p])
 _SIGS["hoc_allreduce_host"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.c_size_t,
                                          C.c_int, C.c_int, C.c_void_p])
 _SIGS["hoc_proxy_status"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64), C.POINTER(C.c_uint64),
@@ -912,6 +912,16 @@ def _row_dtype(x, what: str) -> int:
     return code
 
 
+_MOST = (1 << 31) - 1  # what an int of the library holds; ctypes would keep the low 32 bits of more
+
+
+def _fits(**counts):
+    """Refuses counts that an int of the library does not hold."""
+    for what, n in counts.items():
+        if not -_MOST <= n <= _MOST:
+            raise ValueError(f"{what}: {n} is more than 2^31 - 1")
+
+
 _NUMBERS = {}  # host numbers by value, as the library reads them: an address each
 
 
@@ -990,6 +1000,7 @@ _WIRE8 = {}  # width -> (bytes of a row, where its scales start)
 def _wire8(width: int):
     got = _WIRE8.get(width)
     if got is None:
+        _fits(width=width)
         n, at = C.c_size_t(), C.c_size_t()
         _check(lib().hoc_wire8_row(int(width), C.byref(n), C.byref(at)), "hoc_wire8_row")
         got = _WIRE8[width] = (n.value, at.value)
@@ -1028,6 +1039,8 @@ def rms_norm(x, weight, y=None, *, eps: float, residual=None, h=None, wire=None,
         raise ValueError("x must be a matrix")
     shape, dev = x.shape, _here(x, "x")
     rows, width = shape
+    if rows > _MOST or width > _MOST:
+        _fits(rows=rows, width=width)
     xp, ldx = _rows_of(x, shape, x.dtype, dev, "x")
     rp, ldr = _rows_of(residual, shape, x.dtype, dev, "residual")
     hp, ldh = _rows_of(h, shape, x.dtype, dev, "h")
@@ -1041,6 +1054,7 @@ def rms_norm(x, weight, y=None, *, eps: float, residual=None, h=None, wire=None,
 
 def rms_norm_workspace(rows: int, width: int) -> int:
     """int32 entries of scratch that rms_norm_grad needs for a weight gradient."""
+    _fits(rows=rows, width=width)
     n = C.c_size_t()
     _check(lib().hoc_rms_norm_workspace(int(rows), int(width), C.byref(n)), "hoc_rms_norm_workspace")
     return n.value
@@ -1055,6 +1069,8 @@ def rms_norm_grad(dy, h, weight, dx, *, eps: float, dy2=None, dres=None, dw=None
         raise ValueError("dy must be a matrix")
     shape, dev = dy.shape, _here(dy, "dy")
     rows, width = shape
+    if rows > _MOST or width > _MOST:
+        _fits(rows=rows, width=width)
     dyp, lddy = _rows_of(dy, shape, dy.dtype, dev, "dy")
     dy2p, lddy2 = _rows_of(dy2, shape, dy.dtype, dev, "dy2")
     hp, ldh = _rows_of(h, shape, dy.dtype, dev, "h")
@@ -1088,6 +1104,8 @@ def expert_widen(wire, seg, y, *, counts=None, stream=None):
     if seg.dim() != 2 or seg.shape[0] != k or seg.shape[1] < 2:
         raise ValueError(f"seg: expected shape [{k}, sources * experts + 1], got {tuple(seg.shape)}")
     dev, width = _here(y[0], "y[0]"), y[0].shape[1]
+    if seg.shape[1] > _MOST:
+        _fits(seg=seg.shape[1])
     n, bf, u8 = wire8_bytes(width), _dt("bfloat16"), _dt("uint8")
     caps, yp, wp, rows, shape, fits = [], [], [], 0, None, False
     for t, w in zip(y, wire):
@@ -1124,6 +1142,8 @@ def _slots(logits, ids, gate, what: str):
     n = ids.numel()
     if n % tokens if tokens else n:
         raise ValueError("ids must hold topk ids per token")
+    if tokens > _MOST or experts > _MOST or n > _MOST * max(tokens, 1):
+        _fits(tokens=tokens, experts=experts, topk=n // max(tokens, 1))
     lp, ldl = _rows_of(logits, shape, logits.dtype, dev, "logits")
     return (tokens, experts, n // tokens if tokens else 1, lp, dt, ldl, dev, _flat(ids, n, _dt("int32"), dev, "ids"),
             _flat(gate, n, _dt("float32"), dev, what))
@@ -1135,10 +1155,12 @@ def ep_route(logits, ids, gate, *, score: str = "softmax", bias=None, groups: in
     be rows of a wider buffer; ids int32 and gate float32 of tokens * topk elements, as a dispatch and a combine take them;
     bias float32 [experts], for the choice only; of `groups` groups of experts the best top_groups (default: all)."""
     tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, gate, "gate")
+    top_groups = groups if top_groups is None else top_groups
+    if not -_MOST <= groups <= _MOST or not -_MOST <= top_groups <= _MOST:
+        _fits(groups=groups, top_groups=top_groups)
     rc = (_lib or lib()).hoc_ep_route(tokens, experts, topk, lp, dt, ldl, _score(score),
-                              _flat(bias, experts, _dt("float32"), dev, "bias"), groups,
-                              groups if top_groups is None else top_groups, int(bool(renormalise)), _number(scale), ip, gp,
-                              _queue(stream, dev))
+                              _flat(bias, experts, _dt("float32"), dev, "bias"), groups, top_groups,
+                              int(bool(renormalise)), _number(scale), ip, gp, _queue(stream, dev))
     if rc:
         _check(rc, "hoc_ep_route")
 
@@ -1160,14 +1182,14 @@ def dropout(x, y, p: float, seed, *, residual=None, stream=None):
     include/hoc_block.h).  x, y and residual: contiguous, of any shape, or [rows, width] that may be rows of wider buffers."""
     dt, dev = _row_dtype(x, "x"), _here(x, "x")
     shape = x.shape
-    if x.dim() != 2:
+    if x.dim() != 2 or shape[1] > _MOST:
         for t, what in ((x, "x"), (y, "y"), (residual, "residual")):
             if t is not None and (t.shape != shape or not t.is_contiguous()):
-                raise ValueError(f"{what}: expected shape {tuple(shape)}, contiguous (or rows of a matrix)")
+                raise ValueError(f"{what}: expected shape {tuple(shape)}, contiguous (or rows of a matrix, below 2^31 wide)")
         n = x.numel()
         width = 1
-        for w in reversed(shape):  # rows of the last dimensions, within the limits of an int
-            if width * w >= 1 << 31:
+        for w in reversed(shape):  # rows of the last dimensions, as wide as an int holds; there may be more rows than that
+            if width * w > _MOST:
                 break
             width *= w
         shape = (n // width if width else 0, width)
