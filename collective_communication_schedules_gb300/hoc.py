@@ -541,10 +541,28 @@ def topo_schedule(C_matrix, node_of, sym, bw_nvlink: int, bw_rdma: int):
     return Tm, stages, [ta[s] for s in range(n.value)], tot.value
 
 
+_MOST = (1 << 31) - 1  # what an int of the library holds; ctypes would keep the low 32 bits of more
+
+
+def _fits(**counts):
+    """Refuses counts that an int of the library does not hold."""
+    for what, n in counts.items():
+        if not -_MOST <= n <= _MOST:
+            raise ValueError(f"{what}: {n} is more than 2^31 - 1")
+
+
+def _int(n) -> int:
+    """n, which an int of the library has to hold."""
+    n = int(n)
+    if not -_MOST <= n <= _MOST:
+        raise ValueError(f"a count of {n} is more than 2^31 - 1")
+    return n
+
+
 def ep_pack_workspace(tokens: int, topk: int, experts: int) -> int:
     """int32 entries of scratch that ep_pack needs for this shape."""
     n = C.c_size_t()
-    _check(lib().hoc_ep_pack_workspace(int(tokens), int(topk), int(experts), C.byref(n)), "hoc_ep_pack_workspace")
+    _check(lib().hoc_ep_pack_workspace(_int(tokens), _int(topk), _int(experts), C.byref(n)), "hoc_ep_pack_workspace")
     return n.value
 
 
@@ -553,8 +571,8 @@ def ep_pack(expert_ids, x, experts: int, nranks: int, send, perm, pos_of, dst_co
     tokens, hidden = x.shape
     topk = expert_ids.numel() // tokens if tokens else 1
     n = tokens * topk
-    _check(lib().hoc_ep_pack(_ptr(expert_ids, 4 * n, "expert_ids"), _ptr(x, 2 * tokens * hidden, "x"), int(tokens),
-                             int(topk), int(hidden), int(experts), int(nranks), _ptr(send, 2 * n * hidden, "send"),
+    _check(lib().hoc_ep_pack(_ptr(expert_ids, 4 * n, "expert_ids"), _ptr(x, 2 * tokens * hidden, "x"), _int(tokens),
+                             _int(topk), _int(hidden), _int(experts), _int(nranks), _ptr(send, 2 * n * hidden, "send"),
                              _ptr(perm, 4 * n, "perm"), _ptr(pos_of, 4 * n, "pos_of"),
                              _ptr(dst_counts, 8 * int(nranks), "dst_counts"), _ptr(workspace, 0, "workspace"),
                              int(workspace.numel()), _stream(stream)), "hoc_ep_pack")
@@ -564,7 +582,7 @@ def ep_combine(rows, pos_of, weights, tokens: int, topk: int, hidden: int, y, st
     """Gate-weighted top-k combine of one source rank (see include/hoc_ep.h)."""
     n = int(tokens) * int(topk)
     _check(lib().hoc_ep_combine(_ptr(rows, 2 * n * int(hidden), "rows"), _ptr(pos_of, 4 * n, "pos_of"),
-                                _ptr(weights, 4 * n, "weights"), int(tokens), int(topk), int(hidden),
+                                _ptr(weights, 4 * n, "weights"), _int(tokens), _int(topk), _int(hidden),
                                 _ptr(y, 2 * int(tokens) * int(hidden), "y"), _stream(stream)), "hoc_ep_combine")
 
 
@@ -578,8 +596,8 @@ def _ep_scatter_call(fn_name, expert_ids, x, experts, out, out_capacity, pos_of,
         raise ValueError(f"expected {k} per-rank tensors and capacities")
     cap = (C.c_size_t * k)(*caps)
     _check(getattr(lib(), fn_name)(k, _ptr_array(expert_ids, 4 * n, "expert_ids"),
-                                   _ptr_array(x, 2 * tokens * hidden, "x"), int(tokens), int(topk), int(hidden),
-                                   int(experts), _ptr_array(out, [2 * c for c in caps], "out"), cap,
+                                   _ptr_array(x, 2 * tokens * hidden, "x"), _int(tokens), _int(topk), _int(hidden),
+                                   _int(experts), _ptr_array(out, [2 * c for c in caps], "out"), cap,
                                    _ptr_array(pos_of, 4 * n, "pos_of"), _ptr(counts, 8 * k * k, "counts"),
                                    _ptr(workspace, 0, "workspace"), int(workspace.numel()),
                                    _ptr(status, 4, "status"), _stream(stream)), fn_name)
@@ -602,7 +620,7 @@ def ep_combine_all(rows, rows_capacity, pos_of, weights, tokens: int, topk: int,
     cap = (C.c_size_t * k)(*caps)
     _check(lib().hoc_ep_combine_all(k, _ptr_array(rows, [2 * c for c in caps], "rows"), cap,
                                     _ptr_array(pos_of, 4 * n, "pos_of"), _ptr_array(weights, 4 * n, "weights"),
-                                    int(tokens), int(topk), int(hidden),
+                                    _int(tokens), _int(topk), _int(hidden),
                                     _ptr_array(y, 2 * int(tokens) * int(hidden), "y"), _ptr(status, 4, "status"),
                                     _stream(stream)), "hoc_ep_combine_all")
 
@@ -622,8 +640,8 @@ def ep_dispatch_fused(expert_ids, x, experts: int, recv, recv_capacity, pos_of, 
         raise ValueError(f"expected {k} per-rank tensors and capacities")
     cap = (C.c_size_t * k)(*caps)
     _check(lib().hoc_ep_dispatch_fused(k, _ptr_array(expert_ids, 4 * n, "expert_ids"),
-                                       _ptr_array(x, 2 * tokens * hidden, "x"), int(tokens), int(topk), int(hidden),
-                                       int(experts), _ptr_array(recv, [2 * c for c in caps], "recv"), cap,
+                                       _ptr_array(x, 2 * tokens * hidden, "x"), _int(tokens), _int(topk), _int(hidden),
+                                       _int(experts), _ptr_array(recv, [2 * c for c in caps], "recv"), cap,
                                        _ptr_array(pos_of, 4 * n, "pos_of"), _ptr(counts, 8 * k * k, "counts"),
                                        _ptr(workspace, 0, "workspace"), int(workspace.numel()),
                                        _ptr(status, 4, "status"), _stream(stream)), "hoc_ep_dispatch_fused")
@@ -641,7 +659,7 @@ def ep_combine_fused(rows, rows_capacity, expert_ids, pos_of, counts, weights, t
     _check(lib().hoc_ep_combine_fused(k, _ptr_array(rows, [2 * c for c in caps], "rows"), cap,
                                       _ptr_array(expert_ids, 4 * n, "expert_ids"), _ptr_array(pos_of, 4 * n, "pos_of"),
                                       _ptr(counts, 8 * k * k, "counts"), _ptr_array(weights, 4 * n, "weights"),
-                                      int(tokens), int(topk), int(hidden), int(experts),
+                                      _int(tokens), _int(topk), _int(hidden), _int(experts),
                                       _ptr_array(y, 2 * int(tokens) * int(hidden), "y"), _ptr(status, 4, "status"),
                                       _stream(stream)), "hoc_ep_combine_fused")
 
@@ -666,8 +684,8 @@ def ep_combine_grad(dy, rows, rows_capacity, expert_ids, pos_of, counts, weights
     if len(expert_ids) != k:
         raise ValueError(f"expected {k} per-rank tensors and capacities")
     _check(lib().hoc_ep_combine_grad(k, dyp, rp, cap, _ptr_array(expert_ids, 4 * n, "expert_ids"), pp,
-                                     _ptr(counts, 8 * k * k, "counts"), wp, int(tokens), int(topk), int(hidden),
-                                     int(experts), dp, dwp, _ptr(status, 4, "status"), _stream(stream)),
+                                     _ptr(counts, 8 * k * k, "counts"), wp, _int(tokens), _int(topk), _int(hidden),
+                                     _int(experts), dp, dwp, _ptr(status, 4, "status"), _stream(stream)),
            "hoc_ep_combine_grad")
 
 
@@ -676,7 +694,7 @@ def ep_combine_grad_all(dy, rows, rows_capacity, pos_of, weights, tokens: int, t
     """Gradient of ep_combine_all: rows and their gradients in each source's packed order."""
     k, _, cap, dyp, rp, pp, wp, dp, dwp = _combine_grad_args(dy, rows, rows_capacity, pos_of, weights, tokens, topk,
                                                              hidden, drows, dweights)
-    _check(lib().hoc_ep_combine_grad_all(k, dyp, rp, cap, pp, wp, int(tokens), int(topk), int(hidden), dp, dwp,
+    _check(lib().hoc_ep_combine_grad_all(k, dyp, rp, cap, pp, wp, _int(tokens), _int(topk), _int(hidden), dp, dwp,
                                          _ptr(status, 4, "status"), _stream(stream)), "hoc_ep_combine_grad_all")
 
 
@@ -749,7 +767,7 @@ def _groups(rows, experts: int, seg):
     if seg.dim() != 2 or seg.shape[0] != k or seg.shape[1] < experts + 1 or (seg.shape[1] - 1) % experts:
         raise ValueError(f"seg: expected shape [{k}, sources * {experts} + 1], got {tuple(seg.shape)}")
     cap = (C.c_size_t * max(1, k))(*rows)
-    return _RowGroups(k, experts, (seg.shape[1] - 1) // experts, _ptr(seg, 0, "seg"), cap), cap
+    return _RowGroups(k, _int(experts), _int((seg.shape[1] - 1) // experts), _ptr(seg, 0, "seg"), cap), cap
 
 
 def ep_segments(expert_ids, experts: int, topk: int, seg, stream=None):
@@ -761,7 +779,7 @@ def ep_segments(expert_ids, experts: int, topk: int, seg, stream=None):
         raise ValueError("expert_ids must hold topk ids per token")
     for r, v in enumerate(expert_ids):
         _typed(v, "int32", f"expert_ids[{r}]")
-    _check(lib().hoc_ep_segments(k, _ptr_array(expert_ids, 4 * n, "expert_ids"), n // topk, int(topk), int(experts),
+    _check(lib().hoc_ep_segments(k, _ptr_array(expert_ids, 4 * n, "expert_ids"), _int(n // topk), _int(topk), _int(experts),
                                  _shaped(seg, (k, int(experts) + 1), "seg", "int64"), _stream(stream)),
            "hoc_ep_segments")
 
@@ -781,7 +799,8 @@ def expert_mm(x, weight, seg, y, *, status, bias=None, act: str = "none", pre=No
     g, _keep = _groups(rows, experts, seg)
     _check(lib().hoc_expert_mm(C.byref(g), _per_rank(x, [(n, inp) for n in rows], "x"),
                                _per_rank(weight, [(experts, wide, inp)] * k, "weight"),
-                               None if bias is None else _per_rank(bias, [(experts, wide)] * k, "bias"), inp, out, a,
+                               None if bias is None else _per_rank(bias, [(experts, wide)] * k, "bias"), _int(inp),
+                               _int(out), a,
                                _per_rank(y, [(n, out) for n in rows], "y"),
                                None if pre is None else _per_rank(pre, [(n, wide) for n in rows], "pre"),
                                _ptr(status, 4, "status"), _stream(stream)), "hoc_expert_mm")
@@ -799,7 +818,7 @@ def expert_mm_dgrad(dy, weight, seg, dx, *, status, act: str = "none", pre=None,
     wide, rows = inp * (2 if act == "swiglu" else 1), [t.shape[0] for t in dy]
     g, _keep = _groups(rows, experts, seg)
     _check(lib().hoc_expert_mm_dgrad(C.byref(g), _per_rank(dy, [(n, out) for n in rows], "dy"),
-                                     _per_rank(weight, [(experts, out, inp)] * k, "weight"), inp, out, a,
+                                     _per_rank(weight, [(experts, out, inp)] * k, "weight"), _int(inp), _int(out), a,
                                      None if pre is None else _per_rank(pre, [(n, wide) for n in rows], "pre"),
                                      _per_rank(dx, [(n, wide) for n in rows], "dx"), _ptr(status, 4, "status"),
                                      _stream(stream)), "hoc_expert_mm_dgrad")
@@ -815,7 +834,7 @@ def expert_mm_wgrad(dy, x, seg, dw, *, status, db=None, accumulate: bool = False
     rows, dt = [t.shape[0] for t in x], "float32" if dw[0].dtype is _dt("float32") else "bfloat16"
     g, _keep = _groups(rows, experts, seg)
     _check(lib().hoc_expert_mm_wgrad(C.byref(g), _per_rank(dy, [(n, out) for n in rows], "dy"),
-                                     _per_rank(x, [(n, inp) for n in rows], "x"), inp, out, _dtype_code(dw[0]),
+                                     _per_rank(x, [(n, inp) for n in rows], "x"), _int(inp), _int(out), _dtype_code(dw[0]),
                                      int(bool(accumulate)), _per_rank(dw, [(experts, out, inp)] * k, "dw", dt),
                                      None if db is None else _per_rank(db, [(experts, out)] * k, "db", dt),
                                      _ptr(status, 4, "status"), _stream(stream)), "hoc_expert_mm_wgrad")
@@ -834,8 +853,9 @@ def linear(x, weight, y, *, status, bias=None, act: str = "none", pre=None, resi
     xp, ldx = _strided(x, (rows, inp), "x")
     yp, ldy = _strided(y, (rows, out), "y")
     rp, ldr = _strided(residual, (rows, out), "residual") if residual is not None else (None, 0)
-    _check(lib().hoc_linear(rows, xp, ldx, _shaped(weight, (wide, inp), "weight"),
-                            None if bias is None else _shaped(bias, (wide,), "bias"), rp, ldr, inp, out, a, yp, ldy,
+    _check(lib().hoc_linear(_int(rows), xp, ldx, _shaped(weight, (wide, inp), "weight"),
+                            None if bias is None else _shaped(bias, (wide,), "bias"), rp, ldr, _int(inp), _int(out), a, yp,
+                            ldy,
                             None if pre is None else _shaped(pre, (rows, wide), "pre"), _ptr(status, 4, "status"),
                             _stream(stream)), "hoc_linear")
 
@@ -850,7 +870,7 @@ def linear_dgrad(dy, weight, dx, *, status, act: str = "none", pre=None, stream=
     out, inp = weight.shape
     rows, wide = dy.shape[0], inp * (2 if act == "swiglu" else 1)
     dp, ldd = _strided(dy, (rows, out), "dy")
-    _check(lib().hoc_linear_dgrad(rows, dp, ldd, _shaped(weight, (out, inp), "weight"), inp, out, a,
+    _check(lib().hoc_linear_dgrad(_int(rows), dp, ldd, _shaped(weight, (out, inp), "weight"), _int(inp), _int(out), a,
                                   None if pre is None else _shaped(pre, (rows, wide), "pre"),
                                   _shaped(dx, (rows, wide), "dx"), _ptr(status, 4, "status"), _stream(stream)),
            "hoc_linear_dgrad")
@@ -864,7 +884,7 @@ def linear_wgrad(dy, x, dw, *, status, db=None, accumulate: bool = False, stream
     dt = "float32" if dw.dtype is _dt("float32") else "bfloat16"
     dp, ldd = _strided(dy, (rows, out), "dy")
     xp, ldx = _strided(x, (rows, inp), "x")
-    _check(lib().hoc_linear_wgrad(rows, dp, ldd, xp, ldx, inp, out, _dtype_code(dw), int(bool(accumulate)),
+    _check(lib().hoc_linear_wgrad(_int(rows), dp, ldd, xp, ldx, _int(inp), _int(out), _dtype_code(dw), int(bool(accumulate)),
                                   _shaped(dw, (out, inp), "dw", dt),
                                   None if db is None else _shaped(db, (out,), "db", dt), _ptr(status, 4, "status"),
                                   _stream(stream)), "hoc_linear_wgrad")
@@ -876,7 +896,7 @@ def act_grad(dy, pre, dz, act: str, stream=None):
         raise ValueError("dy must be a matrix")
     rows, width = dy.shape
     wide = width * (2 if act == "swiglu" else 1)
-    _check(lib().hoc_act_grad(rows, width, _act(act), _shaped(dy, (rows, width), "dy"),
+    _check(lib().hoc_act_grad(_int(rows), _int(width), _act(act), _shaped(dy, (rows, width), "dy"),
                               _shaped(pre, (rows, wide), "pre"), _shaped(dz, (rows, wide), "dz"), _stream(stream)),
            "hoc_act_grad")
 
@@ -910,16 +930,6 @@ def _row_dtype(x, what: str) -> int:
     if code is None:
         raise TypeError(f"{what}: expected a bfloat16 or float32 tensor")
     return code
-
-
-_MOST = (1 << 31) - 1  # what an int of the library holds; ctypes would keep the low 32 bits of more
-
-
-def _fits(**counts):
-    """Refuses counts that an int of the library does not hold."""
-    for what, n in counts.items():
-        if not -_MOST <= n <= _MOST:
-            raise ValueError(f"{what}: {n} is more than 2^31 - 1")
 
 
 _NUMBERS = {}  # host numbers by value, as the library reads them: an address each
