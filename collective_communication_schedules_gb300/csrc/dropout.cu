@@ -131,24 +131,24 @@ cudaError_t dropout_preload() {
 using namespace hoc;
 using namespace hoc::block;
 
-extern "C" hocResult_t hoc_dropout(int64_t rows, int width, hocDataType_t dtype, const void* x, size_t ldx,
+extern "C" hocResult_t hoc_dropout(size_t rows, int width, hocDataType_t dtype, const void* x, size_t ldx,
                                    const void* residual, size_t ldr, const double* p, const int64_t* seed, void* y, size_t ldy,
                                    void* stream) {
   const char* who = "hoc_dropout";
-  if (rows < 0 || width < 0) return refuse(who, "rows or width out of range");
+  constexpr size_t kMost = size_t(0x7FFFFFFF) * 8 * kDropThreads * kDropAhead;  // what a grid reaches
+  if (width < 0 || rows > kMost / size_t(width > 1 ? width : 1)) return refuse(who, "rows or width out of range");
   if (!row_dtype(dtype)) return refuse(who, "dtype must be HOC_FLOAT32 or HOC_BFLOAT16");
   if (!p || !(*p >= 0.0 && *p < 1.0)) return refuse(who, "p must be given, at least 0 and below 1");
   const bool none = rows == 0 || width == 0;
-  constexpr int64_t kMost = int64_t(0x7FFFFFFF) * 8 * kDropThreads * kDropAhead;  // what a grid reaches
-  if (!none && rows > kMost / width) return refuse(who, "more than 2^43 elements");
+  const int64_t n = int64_t(rows);
   const size_t b = bytes_of(dtype);
-  const char* bad = bad_rows(x, ldx, rows, width, b, none);
-  if (!bad) bad = bad_rows(residual, ldr, rows, width, b, true);
-  if (!bad) bad = bad_rows(y, ldy, rows, width, b, none);
+  const char* bad = bad_rows(x, ldx, n, width, b, none);
+  if (!bad) bad = bad_rows(residual, ldr, n, width, b, true);
+  if (!bad) bad = bad_rows(y, ldy, n, width, b, none);
   if (!bad && (!seed || !aligned(seed, 8))) bad = "seed must be given, aligned to its elements";
   if (bad) return refuse(who, bad);
   if (none) return HOC_SUCCESS;
-  const int64_t total = rows * width;
+  const int64_t total = n * width;
   const int t = int(*p * 65536 + 0.5) < 65535 ? int(*p * 65536 + 0.5) : 65535;
   unsigned shift = 0;
   while ((int64_t(1) << shift) < width) ++shift;

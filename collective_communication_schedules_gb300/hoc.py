@@ -169,7 +169,7 @@ _SIGS["hoc_ep_route"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_in
                                    C.c_int, C.c_int, C.c_int, C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_void_p])
 _SIGS["hoc_ep_route_grad"] = (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_size_t, C.c_int, C.c_int,
                                         C.POINTER(C.c_float), C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p])
-_SIGS["hoc_dropout"] = (C.c_int, [C.c_int64, C.c_int, C.c_int] + 2 * _ROWS + [C.POINTER(C.c_double), C.c_void_p] + _ROWS + [C.c_void_p])
+_SIGS["hoc_dropout"] = (C.c_int, [C.c_size_t, C.c_int, C.c_int] + 2 * _ROWS + [C.POINTER(C.c_double), C.c_void_p] + _ROWS + [C.c_void_p])
 _SIGS["hoc_allreduce_host"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.c_size_t,
                                          C.c_int, C.c_int, C.c_void_p])
 _SIGS["hoc_proxy_status"] = (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64), C.POINTER(C.c_uint64),

@@ -138,7 +138,7 @@ hocResult_t hoc_ep_route_grad(int tokens, int experts, int topk, const void* log
  * seed[1] is changed).  The gradient is the same call on the gradient, without a
  * residual.  y may be x or residual, with the same row stride.  p == 0 draws nothing.  There may be
  * 2^31 rows and more (almost 2^43 elements): a run of n elements is n rows of width 1. */
-hocResult_t hoc_dropout(int64_t rows, int width, hocDataType_t dtype, const void* x, size_t ldx, const void* residual,
+hocResult_t hoc_dropout(size_t rows, int width, hocDataType_t dtype, const void* x, size_t ldx, const void* residual,
                         size_t ldr, const double* p, const int64_t* seed, void* y, size_t ldy, void* stream);
 
 #ifdef __cplusplus
