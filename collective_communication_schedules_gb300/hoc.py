@@ -936,6 +936,8 @@ _NUMBERS = {}  # host numbers by value, as the library reads them: an address ea
 
 
 def _number(v, kind=C.c_float):
+    if type(v) is not float:  # a tensor or an array of one element would be found by its identity, whatever it holds by now
+        v = kind(v).value
     got = _NUMBERS.get((kind, v))
     if got is None:
         if len(_NUMBERS) >= 256:

@@ -109,3 +109,33 @@ def test_rows_of_8_bits_refuse_counts_that_an_int_does_not_hold(calls):
     with pytest.raises(ValueError):
         hoc.expert_widen([empty(4, 80, dtype=torch.uint8)], empty(1, TOP + 1, dtype=torch.int64), [empty(4, 64)])
     assert all(name == "hoc_wire8_row" for name, _ in calls)
+
+
+def test_a_number_that_lies_in_a_tensor_is_read_at_every_call():
+    for kind in (C.c_float, C.c_double):
+        t = torch.tensor(2.0)
+        first = hoc._number(t, kind)._obj
+        t.fill_(5.0)
+        assert hoc._number(t, kind)._obj.value == 5.0 and first.value == 2.0
+        p = torch.nn.Parameter(torch.tensor([0.5]), requires_grad=False)
+        assert hoc._number(p, kind)._obj.value == 0.5
+        p.mul_(0.5)
+        assert hoc._number(p, kind)._obj.value == 0.25
+    assert all(type(v) is float for _, v in hoc._NUMBERS), "what it holds would live as long as the table"
+
+
+def test_numbers_reach_the_calls_as_they_are(calls):
+    x, w, eps = empty(4, 8), empty(8, dtype=F32), torch.tensor(0.5)
+    for want in (0.5, 0.25, 1, 0.125):
+        eps.fill_(want)
+        hoc.rms_norm(x, w, x, eps=eps)
+        hoc.ep_route(x, empty(8, dtype=I32), empty(8, dtype=F32), scale=eps)
+        hoc.dropout(x, x, eps, SEED)
+        (_, norm), (_, route), (_, drop) = calls[-3:]
+        assert norm[9]._obj.value == route[11]._obj.value == drop[7]._obj.value == want
+
+
+def test_what_is_no_number_is_refused():
+    for v in ("0.5", None, torch.zeros(2)):
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            hoc._number(v)
