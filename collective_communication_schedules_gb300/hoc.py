@@ -1010,6 +1010,8 @@ _WIRE8 = {}  # width -> (bytes of a row, where its scales start)
 
 
 def _wire8(width: int):
+    if type(width) is not int:  # (as _number)
+        width = int(width)
     got = _WIRE8.get(width)
     if got is None:
         _fits(width=width)

@@ -139,3 +139,10 @@ def test_what_is_no_number_is_refused():
     for v in ("0.5", None, torch.zeros(2)):
         with pytest.raises((TypeError, ValueError, RuntimeError)):
             hoc._number(v)
+
+
+def test_a_width_that_lies_in_a_tensor_is_read_at_every_call():
+    w = torch.tensor(64)
+    assert hoc.wire8_bytes(w) == hoc.wire8_bytes(64)
+    w.fill_(2048)
+    assert hoc.wire8_bytes(w) == hoc.wire8_bytes(2048) and all(type(v) is int for v in hoc._WIRE8)
