@@ -376,7 +376,7 @@ __device__ __forceinline__ int pop_sorted(uint32_t (&u)[EPL], int q, uint32_t* k
 template <class T, int EPL, int L, bool SOFTMAX>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteArgs A) {
   after_the_last();
-  constexpr uint32_t kPlaces = EPL - 1;
+  constexpr uint32_t kPlaces = EPL - 1, kLow = (EPL > L ? EPL : L) - 1;  // (kLow: as in pop_sorted)
   // what comparing keys without their last bits may change, relative to a key
   constexpr float kCut = float(EPL > L ? EPL : L) * 0x1p-23f;
   constexpr int kTokens = 32 / L;                // of a warp
@@ -528,8 +528,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
   int mine = key ? owner * A.epl + int(kPlaces - (key & kPlaces)) : -1;
   if (check) {
     // Keys that are near the one before them; where that holds for the first that is left out,
-    // what follows it is taken too (lanes topk + 1, ..), as far as it is near the last chosen.
-    const float k = value_of(key & ~kPlaces), before = __shfl_up_sync(kAll, k, 1, L);
+    // what follows it is taken too (lanes topk + 1, ..), as far as it is near the last chosen.  They are compared by what
+    // orders them, without the bits that a lane may stand for (kLow): a key is at most that much above it, also those
+    // that are still in their lanes, which may be larger than the one that was found before them.
+    const float k = value_of(key & ~kLow), before = __shfl_up_sync(kAll, k, 1, L);
     bool by = q > 0 && key && is_near(before, k);
     if (__any_sync(kAll, by)) {
       const uint32_t close = lanes_of<L>(by);  // (by all lanes: the rest is a token's own)
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
       for (int r = A.topk + 1; __any_sync(kAll, more); ++r) {
         uint32_t next;
         const int from = pop_sorted<EPL, L>(u, q, &next);
-        more = more && next && is_near(least, value_of(next & ~kPlaces));
+        more = more && next && is_near(least, value_of(next & ~kLow));
         if (more && q == r) {
           key = next;
           mine = from * A.epl + int(kPlaces - (next & kPlaces));

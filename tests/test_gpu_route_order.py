@@ -1,0 +1,36 @@
+"""Which experts a routing chooses where its binary32 keys alone would choose others."""
+import pytest
+import torch
+
+from tests.test_gpu_block import DEV, check_route
+
+pytestmark = pytest.mark.gpu
+F64 = torch.float64
+
+
+def border_keys(tokens, experts, step, sure, g):
+    """Sigmoid keys above 1, in units of 2^-23: expert b a little below or above a multiple of `step` and c too, a at the end of
+    the range behind it, d at the start of the one before it, in the order b, a, d, c.  Keys are put in order without their last
+    bits, in ranges of `step`, and a range's by their experts: with b rounded up and c down, a is the last that is chosen and d
+    the first that is not, which lie far apart, and c behind them may still be larger than b.  `sure` more are chosen anyway."""
+    spots = torch.arange(4) * (experts // 8) + (experts > 32)
+    base = 1.6 + torch.rand(4, generator=g, dtype=F64)
+    bias = torch.zeros(experts)
+    bias[spots] = (1 - torch.sigmoid(base)).float()
+    bias[experts - sure:] = 1.5 + 0.25 * torch.arange(sure)
+    low = torch.tensor([3 * step - 1.0, 4 * step - 4.5, 2 * step + 0.5, 3 * step - 1.0], dtype=F64)
+    wide = torch.tensor([1.0, 3.8, 3.0, 1.0], dtype=F64)
+    key = 1 + (low + wide * torch.rand(tokens, 4, generator=g, dtype=F64)) * 2.0 ** -23
+    z = torch.full((tokens, experts), -3.0)
+    z[:, spots] = torch.special.logit(key - bias[spots].double()).float()
+    return z.to(DEV), bias.to(DEV)
+
+
+@pytest.mark.parametrize("tokens,experts,step,sure,calls", [
+    (60, 32, 32, 0, 40), (60, 64, 32, 0, 40), (60, 128, 32, 0, 40), (60, 256, 32, 0, 40), (2500, 64, 16, 8, 10),
+])
+def test_what_follows_the_first_that_is_left_out_may_still_be_chosen(tokens, experts, step, sure, calls):
+    g = torch.Generator().manual_seed(experts + step)
+    for _ in range(calls):
+        z, bias = border_keys(tokens, experts, step, sure, g)
+        check_route(z, 2 + sure, bias, "sigmoid")
