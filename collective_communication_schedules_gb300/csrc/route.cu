@@ -16,6 +16,7 @@
 // Keys with the same logit and the same bias are equal in any arithmetic, so that logits
 // of few bits do not send their tokens there.  bf16 logits that are keys themselves have the bits
 // to spare and are exact.
+#include <cfloat>
 #include <type_traits>
 #include <utility>
 
@@ -463,11 +464,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
       g = two_of_groups<EPL, L>(A.experts, A.groups, A.epl, q, u);
     }
     const float ga = value_of(g.a & ~kPlaces), gb = value_of(g.b & ~kPlaces);
-    const float score = q < A.groups ? g.b ? ga + gb : ga : -INFINITY;
-    const float size = max_of<L>(q < A.groups && g.b ? fabsf(ga) + fabsf(gb) : 0.f);
+    // (the sum of two of the lowest keys is -inf: the score is below all binary32 numbers then, and its group there all the same)
+    const float score = g.b ? ga + gb : ga;
+    const bool some = q < A.groups && g.a;
+    const float size = max_of<L>(some && g.b && score > -INFINITY ? fabsf(ga) + fabsf(gb) : 0.f);
     // scores with their lanes as last bits: of equal ones the first group is the largest
     constexpr uint32_t kLane = L - 1;
-    uint32_t mark = score > -INFINITY ? (ordered(score) & ~kLane) | (kLane - q) : 0u, last = 0, kept = 0;
+    uint32_t mark = some ? (ordered(fmaxf(score, -FLT_MAX)) & ~kLane) | (kLane - q) : 0u, last = 0, kept = 0;
     for (int r = 0; r < A.top_groups; ++r) {
       const uint32_t m = most_of<L>(mark);
       last = m ? m : last;

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests.test_gpu_block import DEV, check_route
+from tests.test_gpu_block import BF, DEV, F32, check_route, gen, route
 
 pytestmark = pytest.mark.gpu
 F64 = torch.float64
@@ -34,3 +34,24 @@ def test_what_follows_the_first_that_is_left_out_may_still_be_chosen(tokens, exp
     for _ in range(calls):
         z, bias = border_keys(tokens, experts, step, sure, g)
         check_route(z, 2 + sure, bias, "sigmoid")
+
+
+@pytest.mark.parametrize("experts,groups,top_groups,topk", [(32, 4, 2, 12), (32, 4, 3, 20), (64, 8, 4, 16), (256, 8, 4, 31), (40, 8, 5, 12)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("tokens", [9, 10_000])
+def test_groups_closed_by_the_lowest_finite_bias_come_last_and_are_there(experts, groups, top_groups, topk, score, dtype, tokens):
+    """The sum of two such keys is no binary32 number.  One group is open, of the others one has an open expert, or none has."""
+    g = gen(experts)
+    z = torch.randn(tokens, experts, generator=g, device=DEV).to(dtype)
+    per = experts // groups
+    bias = torch.full((experts,), torch.finfo(F32).min, device=DEV)
+    bias[2 * per: 3 * per] = 0.25
+    check = z[:500] if tokens > 500 else z  # (the 64-bit form goes token by token)
+    for _ in range(2):
+        ids, gate = check_route(check, topk, bias, score, groups, top_groups)
+        assert bool((ids >= 0).all())
+        if tokens > 500:
+            all_ids, all_gate = route(z, topk, bias=bias, score=score, groups=groups, top_groups=top_groups)
+            assert torch.equal(all_ids[:500], ids) and bool((all_ids >= 0).all())
+        bias[0] = 0.5
