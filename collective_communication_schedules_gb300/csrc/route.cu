@@ -463,23 +463,25 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
     } else {
       g = two_of_groups<EPL, L>(A.experts, A.groups, A.epl, q, u);
     }
-    const float ga = value_of(g.a & ~kPlaces), gb = value_of(g.b & ~kPlaces);
-    // (the sum of two of the lowest keys is -inf: the score is below all binary32 numbers then, and its group there all the same)
-    const float score = g.b ? ga + gb : ga;
+    // A group's score is within err of this sum, whose keys are cut to their places, rounded, and off by tol each.  The
+    // sum of two of the lowest keys is -inf: the score is below all binary32 numbers then, and its group there all the same.
+    const float ga = value_of(g.a & ~kPlaces), gb = g.b ? value_of(g.b & ~kPlaces) : 0.f, score = ga + gb;
+    const float err = 2.f * tol + (fabsf(ga) + fabsf(gb)) * (float(EPL) * 0x1p-23f + 0x1p-22f);
     const bool some = q < A.groups && g.a;
-    const float size = max_of<L>(some && g.b && score > -INFINITY ? fabsf(ga) + fabsf(gb) : 0.f);
     // scores with their lanes as last bits: of equal ones the first group is the largest
     constexpr uint32_t kLane = L - 1;
-    uint32_t mark = some ? (ordered(fmaxf(score, -FLT_MAX)) & ~kLane) | (kLane - q) : 0u, last = 0, kept = 0;
+    uint32_t mark = some ? (ordered(fmaxf(score, -FLT_MAX)) & ~kLane) | (kLane - q) : 0u, kept = 0;
     for (int r = 0; r < A.top_groups; ++r) {
       const uint32_t m = most_of<L>(mark);
-      last = m ? m : last;
       kept |= m ? 1u << (kLane - (m & kLane)) : 0u;
       mark = mark == m ? 0u : mark;
     }
-    const uint32_t next = most_of<L>(mark);
-    const bool near = next && !(value_of(last & ~kLane) - value_of(next & ~kLane) >
-                                4.f * tol + size * (2.f * kCut + float(L) * 0x1p-23f + 0x1p-21f));
+    // in doubt unless the least that a kept score may be is above the most that another may be (ordered() of -inf and of
+    // inf - inf is 0: as low as can be)
+    const bool in = kept >> q & 1;
+    const uint32_t low = ~most_of<L>(some && in ? ~ordered(score - err) : 0u);
+    const uint32_t high = most_of<L>(some && !in ? ordered(fmaxf(score + err, -FLT_MAX)) : 0u);
+    const bool near = high && low <= high;
     if (!runs) {
       exactly = near;
     } else if (__any_sync(kAll, near)) {

@@ -1,4 +1,6 @@
 """Which experts a routing chooses where its binary32 keys alone would choose others."""
+import math
+
 import pytest
 import torch
 
@@ -55,3 +57,17 @@ def test_groups_closed_by_the_lowest_finite_bias_come_last_and_are_there(experts
             all_ids, all_gate = route(z, topk, bias=bias, score=score, groups=groups, top_groups=top_groups)
             assert torch.equal(all_ids[:500], ids) and bool((all_ids >= 0).all())
         bias[0] = 0.5
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_groups_of_one_key_are_in_doubt_as_their_keys_are(masked):
+    """The same keys, each the only one of its group: alone in it, or beside a masked one."""
+    g = torch.Generator().manual_seed(7)
+    for _ in range(60):
+        z, bias = border_keys(60, 32, 32, 0, g)
+        groups = 32
+        if masked:
+            groups = 16
+            z = torch.stack([z[:, :16], torch.full_like(z[:, :16], -math.inf)], 2).reshape(60, 32)
+            bias = torch.stack([bias[:16], torch.zeros_like(bias[:16])], 1).reshape(32)
+        check_route(z, 2, bias, "sigmoid", groups, 2)
