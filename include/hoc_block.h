@@ -51,11 +51,12 @@ hocResult_t hoc_wire8_row(int width, size_t* bytes, size_t* scales_at);
  * dtype (NULL: not wanted) and in rows of 8 bits to wire ([rows][bytes of
  * hoc_wire8_row], aligned to 16 bytes; NULL: not wanted); one of the two is
  * given.  Those are of y before it is rounded: a group's scale is
- * max(max|y| / 448, 2^-100), its values y / scale rounded to the nearest even (a
- * NaN stays one and takes no part in the scale; an infinite y becomes NaN); bytes
- * of a row that hold neither are not written.  Squares are binary32: a row whose
- * mean square overflows gives zeros.  h may be x or residual, and y may be x or,
- * where h is not stored there, residual, each with the same row stride. */
+ * max(max|y| / 448, 2^-100), its values the binary32 quotients y / scale rounded to
+ * the nearest even (a NaN stays one and takes no part in the scale; an infinite y
+ * makes its whole group NaN); bytes of a row that hold neither are not written.
+ * Squares are binary32: a row whose mean square overflows gives zeros.  h may be x
+ * or residual, and y may be x or, where h is not stored there, residual, each with
+ * the same row stride. */
 hocResult_t hoc_rms_norm(int rows, int width, hocDataType_t dtype, const void* x, size_t ldx, const void* residual,
                          size_t ldr, const void* weight, hocDataType_t weight_dtype, const float* eps, void* h, size_t ldh,
                          void* y, size_t ldy, void* wire, void* stream);
