@@ -47,6 +47,7 @@ class ExpertBlock:
         self.ws = torch.empty(hoc.rms_norm_workspace(n, hidden), dtype=torch.int32, device=dev)
         self.no_seed = torch.zeros(2, dtype=torch.int64, device=dev)
         self.status = self.layer.status
+        self.held = None
         torch.cuda.current_stream(dev).synchronize()  # no_seed is there for calls on any stream
 
     def _ranks(self, t):
@@ -55,22 +56,27 @@ class ExpertBlock:
     def forward(self, x, norm, router, w_up, w_down, y, *, residual=None, bias=None, seed=None, stream=None):
         """y [k * tokens, hidden] = the residual stream behind the block; x and residual as y; norm [hidden]; router [experts,
         hidden]; w_up[d], w_down[d] as ExpertLayer's; bias float32 [experts] for the choice; seed: two int64 for the
-        dropout, if there is one.  Keeps what the backward pass needs; x itself where there is no residual."""
+        dropout, if there is one.  Keeps what the backward pass needs; x itself where there is no residual, which has to stay
+        as it is until then: y may be x, or the residual, but without a residual a y that is x leaves no backward pass."""
         if self.drop and seed is None:
             raise ValueError("seed: the dropout needs one")
-        self.held = self.h if residual is not None else x
+        held, self.held = self.h if residual is not None else x, None  # (until the whole pass is queued)
         hoc.rms_norm(x, norm, self.n, eps=self.eps, residual=residual, h=self.h if residual is not None else None,
                      wire=self.wire, stream=stream)
         hoc.linear(self.n, router, self.logits, status=self.status, stream=stream)
         hoc.ep_route(self.logits, self.ids, self.gate, bias=bias, **self.routing, **self.choice, stream=stream)
         self.layer.forward(self._ranks(self.n if self.wire is None else self.wire), self._ranks(self.ids),
                            self._ranks(self.gate), w_up, w_down, self._ranks(self.out), stream=stream)
-        hoc.dropout(self.out, y, self.drop, self.no_seed if seed is None else seed, residual=self.held, stream=stream)
+        hoc.dropout(self.out, y, self.drop, self.no_seed if seed is None else seed, residual=held, stream=stream)
+        if residual is not None or y.data_ptr() != x.data_ptr() or not x.numel():  # else what backward would read is gone
+            self.held = held
 
     def backward(self, dy, norm, router, w_up, w_down, dx, dnorm, drouter, dw_up, dw_down, *, seed=None,
                  accumulate: bool = False, stream=None):
         """Gradients of the last forward, which had these weights and this seed: dx [k * tokens, hidden] for x and for the
         residual alike; dnorm, drouter, dw_up[d] and dw_down[d] in bf16 or float32 (added to with accumulate)."""
+        if self.held is None:
+            raise ValueError("no forward pass to go back through: there was none, or it wrote y over the x that is needed here")
         dout = dy
         if self.drop:
             if seed is None:
