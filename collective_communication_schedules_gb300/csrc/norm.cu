@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel(const __grid_constan
         b = fmaf(d[j][e] * w[j][e], h[j][e], b);
       }
     const float2 t = row_sum2(a, b, A.log, sh[turn]);  // (two sets of entries: one barrier a row)
-    const float s = rsqrtf(t.x * inv + A.eps), k = -s * s * (t.y * inv);
+    const float s = rsqrtf(t.x * inv + A.eps), k = -s * (s * (t.y * inv));  // (s * s of a tiny row may be no binary32 number)
     if constexpr (S == 0) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
     const float ta = row_sum(a, -1, sh);
     __syncthreads();
     const float tb = row_sum(b, -1, sh);
-    const float s = rsqrtf(ta * inv + A.eps), k = -s * s * (tb * inv);
+    const float s = rsqrtf(ta * inv + A.eps), k = -s * (s * (tb * inv));
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * kWideThreads + int(threadIdx.x)) * N;
