@@ -1156,7 +1156,7 @@ def _slots(logits, ids, gate, what: str):
     n = ids.numel()
     if n % tokens if tokens else n:
         raise ValueError("ids must hold topk ids per token")
-    if tokens > _MOST or experts > _MOST or n > _MOST * max(tokens, 1):
+    if n > _MOST or experts > _MOST:  # (n is tokens * topk)
         _fits(tokens=tokens, experts=experts, topk=n // max(tokens, 1))
     lp, ldl = _rows_of(logits, shape, logits.dtype, dev, "logits")
     return (tokens, experts, n // tokens if tokens else 1, lp, dt, ldl, dev, _flat(ids, n, _dt("int32"), dev, "ids"),
@@ -1169,8 +1169,9 @@ def ep_route(logits, ids, gate, *, score: str = "softmax", bias=None, groups: in
     be rows of a wider buffer; ids int32 and gate float32 of tokens * topk elements, as a dispatch and a combine take them;
     bias float32 [experts], for the choice only; of `groups` groups of experts the best top_groups (default: all)."""
     tokens, experts, topk, lp, dt, ldl, dev, ip, gp = _slots(logits, ids, gate, "gate")
-    top_groups = groups if top_groups is None else top_groups
-    if not -_MOST <= groups <= _MOST or not -_MOST <= top_groups <= _MOST:
+    if top_groups is None:
+        top_groups = groups
+    if (groups != 1 or top_groups != 1) and not (-_MOST <= groups <= _MOST and -_MOST <= top_groups <= _MOST):
         _fits(groups=groups, top_groups=top_groups)
     rc = (_lib or lib()).hoc_ep_route(tokens, experts, topk, lp, dt, ldl, _score(score),
                               _flat(bias, experts, _dt("float32"), dev, "bias"), groups, top_groups,

@@ -92,7 +92,8 @@ def test_routing_refuses_counts_that_an_int_does_not_hold(calls, shape, topk):
     assert not calls
 
 
-@pytest.mark.parametrize("groups", [dict(groups=2 * TOP + 1), dict(groups=2, top_groups=2 * TOP + 1), dict(groups=1 - 2 * TOP)])
+@pytest.mark.parametrize("groups", [dict(groups=2 * TOP + 1), dict(groups=2, top_groups=2 * TOP + 1), dict(top_groups=2 * TOP + 1),
+                                    dict(groups=1 - 2 * TOP)])
 def test_routing_refuses_groups_that_an_int_does_not_hold(calls, groups):
     z, ids, gate = empty(4, 8), empty(8, dtype=I32), empty(8, dtype=F32)
     with pytest.raises(ValueError):
