@@ -554,12 +554,13 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const __gr
 }
 
 // dw (+)= sum over the parts, kSumCols columns a CTA, in an order that depends on the parts
-// alone.  Bound by its latency: a thread's parts are all on their way at once, and there are
+// alone.  They are still being written when this kernel starts, and so not what __restrict__ would call them: read-only
+// while it runs.  Bound by its latency: a thread's parts are all on their way at once, and there are
 // twice as many CTAs as with 32 columns each (509 x 1408 binary32, both kernels: 6.6 us, 7.1 with 32).
 constexpr int kSumCols = 16, kSumRows = 64;
 template <class T>
-__global__ void __launch_bounds__(kSumCols * kSumRows) norm_weight_kernel(const float* __restrict__ part, int parts, int width,
-                                                                          T* dw, int accumulate) {
+__global__ void __launch_bounds__(kSumCols * kSumRows) norm_weight_kernel(const float* part, int parts, int width, T* dw,
+                                                                          int accumulate) {
   __shared__ float sh[kSumRows][kSumCols + 1];
   after_the_last();
   const int c = blockIdx.x * kSumCols + int(threadIdx.x);
