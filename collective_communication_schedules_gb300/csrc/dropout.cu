@@ -2,7 +2,7 @@
 //
 // Element i's 16 random bits are a part of Philox4x32-10 of the counter i / 8, so that
 // nothing of the mask is stored and the gradient draws it again.  Bound by its bytes:
-// 32,768 x 4096 bf16 with the residual take 119 us, the copy rate.  Ten rounds for eight elements
+// 32,768 x 4096 bf16 with the residual take 121 us, 0.98 of the copy rate.  Ten rounds for eight elements
 // are about 8 integer operations an element, so the rest is kept short: a word's upper half
 // is compared as it stands, elements are dropped by a choice before the multiply-add, and rows that
 // lie together are one run, without a division (188 us before that).

@@ -10,9 +10,12 @@
 //
 // Which of two near keys is larger is decided as 64-bit arithmetic decides it.  Keys are
 // binary32 without their last bits, with a bound on their error.  Where two neighbours in the
-// order lie within it (0.2 % of the tokens, for normal logits and 256 experts), the keys that may
-// be chosen are worked out again in binary64, a lane each, and ranked; where a group's
-// place is in doubt (0.03 %), or more keys than lanes, the whole token is done again.
+// order lie within it, the keys that may be chosen are worked out again in binary64, a lane each, and ranked; where a
+// group's place is in doubt, or more keys than lanes, the whole token is done again.  For normal logits of standard
+// deviation 1 and 256 experts these are 0.2 % and 0.03 % of the tokens.  It depends on the scores: the softmax's
+// bound is that of its largest score, so that peaked ones leave many keys in doubt that a bias alone tells apart.  32,768
+// tokens, binary32 logits, a bias in steps of 0.001: top-6 of 64 by softmax 12.9, 32.6 and 105 us at standard deviations 1, 4
+// and 8, by sigmoid 8.0, 8.0 and 9.8; top-8 of 256 in 4 of 8 groups 43, 187 and 385 us, and 26.6, 28.3 and 32.1.
 // Keys with the same logit and the same bias are equal in any arithmetic, so that logits
 // of few bits do not send their tokens there.  bf16 logits that are keys themselves have the bits
 // to spare and are exact.
@@ -762,8 +765,8 @@ int access_of(const void* p, size_t ld, int experts, int epl, size_t elem) {
 
 // The lanes that take a token: as few as hold its experts in registers, have one lane for each
 // slot and the first that is left out (for scores of bf16 logits, among which many are equal,
-// three more), and one for each group.  32,768 tokens, top-8 of 256 in 4 of 8 groups: 30.6 us with 16
-// lanes, 34.4 with 32; top-6 of 64: 6.8 us with 8, 12.8 with 32.  Where there are not enough
+// three more), and one for each group.  32,768 tokens, top-8 of 256 in 4 of 8 groups: 27.0 us with 16
+// lanes, 30.8 with 32; top-6 of 64 in bf16: 5.9 us with 8, 10.1 with 32.  Where there are not enough
 // tokens to keep the SMs busy a warp each has less to do one after the other: 1024 tokens 6.8 us
 // with 32 lanes, 8.5 with 16; 2.5 and 2.9.  The sides meet near 3000 tokens at 64 experts and
 // between 8192 and 32,768 at 256.

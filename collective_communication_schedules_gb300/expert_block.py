@@ -23,8 +23,9 @@ from .expert_layer import ExpertLayer
 class ExpertBlock:
     """Buffers of k ranks x `tokens` tokens of `hidden`, top-`topk` of `experts` experts of width `ffn`.
 
-    score, groups, top_groups, renormalise and scale are the routing's (hoc.ep_route); drop the probability of the
-    dropout; wire8: tokens go to their experts in rows of 8 bits; capacity: as ExpertLayer's."""
+    score, groups, top_groups, renormalise and scale are the routing's (hoc.ep_route), whose logits and their gradients are
+    stored in bf16, as hoc.linear writes them; drop the probability of the dropout; wire8: tokens go to their experts in rows
+    of 8 bits; capacity: as ExpertLayer's."""
 
     def __init__(self, k: int, tokens: int, topk: int, hidden: int, ffn: int, experts: int, *, score: str = "softmax",
                  groups: int = 1, top_groups: int | None = None, renormalise: bool = True, scale: float = 1.0,

@@ -54,9 +54,9 @@ hocResult_t hoc_wire8_row(int width, size_t* bytes, size_t* scales_at);
  * max(max|y| / 448, 2^-100), its values the binary32 quotients y / scale rounded to
  * the nearest even (a NaN stays one and takes no part in the scale; an infinite y
  * makes its whole group NaN); bytes of a row that hold neither are not written.
- * Squares are binary32: a row whose mean square overflows gives zeros.  h may be x
- * or residual, and y may be x or, where h is not stored there, residual, each with
- * the same row stride. */
+ * Squares are binary32: a row whose squares add up to more than that holds gives
+ * zeros.  h may be x or residual, and y may be x or, where h is not stored there,
+ * residual, each with the same row stride. */
 hocResult_t hoc_rms_norm(int rows, int width, hocDataType_t dtype, const void* x, size_t ldx, const void* residual,
                          size_t ldr, const void* weight, hocDataType_t weight_dtype, const float* eps, void* h, size_t ldh,
                          void* y, size_t ldy, void* wire, void* stream);
